@@ -20,6 +20,7 @@ __all__ = ["build", "load", "select", "select_twopass", "replay", "select_worksp
            "select_fallback_chunks",
            "select_sharded", "select_varlen", "replay_varlen", "replay_backward",
            "replay_backward_varlen",
+           "rope", "rope_frequencies", "cache_write", "cache_read", "attend", "attend_backward",
            "twopass_workspace_size", "sample_plan", "HytopkError", "STATUS", "PHASES", "Stats",
            "symbols"]
 
@@ -30,8 +31,12 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape or dtype",
 DEV_REPLAY_BAD_INDEX = 0x1
 DEV_BAD_SCALE = 0x2
 DEV_BAD_POSITION = 0x4
+DEV_BAD_INDEX = DEV_REPLAY_BAD_INDEX
+DEV_NONFINITE = 0x8
 DEV_WAIT_TIMEOUT = 0x80000000  # a bounded wait gave up: the call's outputs are undefined
 BF16, E4M3, E4M3_BF16 = 0, 1, 2  # E4M3_BF16: e4m3 q (with q_scale), bf16 k
+
+ELEM_BF16, ELEM_E4M3, ELEM_F32 = 0, 1, 2
 
 # the C-ABI symbols declared in include/hytopk.h
 symbols = ("hytopk_select_workspace_size", "hytopk_select_fallback_chunks", "hytopk_select",
@@ -41,6 +46,8 @@ symbols = ("hytopk_select_workspace_size", "hytopk_select_fallback_chunks", "hyt
            "hytopk_replay_backward", "hytopk_select_varlen_workspace_size",
            "hytopk_select_varlen", "hytopk_replay_varlen", "hytopk_replay_grouped",
            "hytopk_replay_backward_varlen", "hytopk_sample_plan",
+           "hytopk_rope", "hytopk_cache_write", "hytopk_cache_read", "hytopk_attend",
+           "hytopk_attend_backward",
            "hytopk_status_string", "hytopk_version")
 
 
@@ -60,6 +67,12 @@ class Stats(ctypes.Structure):
 class SelectOptions(ctypes.Structure):
     _fields_ = [("threshold_override", ctypes.c_void_p), ("phase_events", ctypes.c_void_p),
                 ("reverse_schedule", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("rot", ctypes.c_int), ("first", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("inverse", ctypes.c_int), ("mscale", ctypes.c_float)]
 
 
 _lib = None
@@ -115,6 +128,18 @@ def load(path: str | None = None):
     lib.hytopk_replay_backward_varlen.restype = I
     lib.hytopk_replay_backward_varlen.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P,
                                                   P, P]
+    S, F = ctypes.c_int64, ctypes.c_float
+    lib.hytopk_rope.restype = I
+    lib.hytopk_rope.argtypes = [P, S, S, I, I, I, I, P, P, S, S, P, P]
+    lib.hytopk_cache_write.restype = I
+    lib.hytopk_cache_write.argtypes = [P, S, S, I, I, I, I, P, P, P, I, P, I, P, P]
+    lib.hytopk_cache_read.restype = I
+    lib.hytopk_cache_read.argtypes = [P, I, P, I, P, I, I, I, P, I, P, P]
+    lib.hytopk_attend.restype = I
+    lib.hytopk_attend.argtypes = [P, S, P, S, P, P, S, P, P, I, I, I, I, I, I, I, F, P, I, P, P, P]
+    lib.hytopk_attend_backward.restype = I
+    lib.hytopk_attend_backward.argtypes = [P, S, P, S, P, S, P, P, I, P, P, I, I, I, I, I, I, F, P,
+                                           P, P, P, P]
     lib.hytopk_sample_plan.restype = ctypes.c_int32
     lib.hytopk_sample_plan.argtypes = [ctypes.c_int64, ctypes.c_int32, P, P]
     lib.hytopk_status_string.restype = ctypes.c_char_p
@@ -488,3 +513,315 @@ def select_twopass(q, k, w, positions, k_top, *, q_scale=None, k_scale=None, row
     if st != 0:
         raise HytopkError(st, "hytopk_select_twopass")
     return idx, sc
+
+
+# ---- around the selection: rotary positions, cache rows, attention ------------------
+
+def _elem(name, t, allowed):
+    import torch
+
+    code = {torch.bfloat16: ELEM_BF16, torch.float32: ELEM_F32, torch.float8_e4m3fn: ELEM_E4M3,
+            torch.uint8: ELEM_E4M3}.get(t if isinstance(t, torch.dtype) else t.dtype)
+    if code not in allowed:
+        names = {ELEM_BF16: "bfloat16", ELEM_F32: "float32", ELEM_E4M3: "float8_e4m3fn"}
+        raise TypeError(f"{name} must be " + " or ".join(names[a] for a in allowed))
+    return code
+
+
+def _need(name, t, device, dtype, shape):
+    """A contiguous tensor of this type and shape on this device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check_tensor(name, t, device, dtype, shape)
+        raise ValueError(f"{name}: wrong tensor")
+
+
+def _rows3(name, t):
+    """t as [rows, heads, d] (a 2-D tensor has one head) with its last axis contiguous."""
+    if t.dim() == 2:
+        t = t.unsqueeze(1)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, d] or [rows, d]")
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t
+
+
+def _row_strides(t):
+    """(row, head) strides in elements; those of axes of length 1 are never used
+    and any value torch gives them is replaced by a packed one."""
+    n, H, d = t.shape
+    head = t.stride(1) if H > 1 else d
+    return (t.stride(0) if n > 1 else H * head), head
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    if status.element_size() != 4 or status.numel() < 1 or status.device != device:
+        raise ValueError("status must be a 32-bit integer tensor on the inputs' device")
+    return status.data_ptr()
+
+
+def _raw_stream(device, stream):
+    import torch
+
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_context=None,
+                     fast=32.0, slow=1.0, device="cuda"):
+    """(inv_freq [rot/2] fp32 tensor, mscale): the frequency table of ``rot``
+    rotated columns, base ** (-2 i / rot), and the factor that goes with it.
+
+    ``scaling`` stretches it for contexts ``factor`` times the original one:
+    ``None``; ``"linear"`` (all frequencies divided by the factor); ``"base"``
+    (the base raised to base * factor ** (rot / (rot - 2)), which keeps the
+    highest frequency and divides the lowest by the factor); ``"parts"``
+    (frequencies that turn more than ``fast`` times within
+    ``original_context`` are kept, those below ``slow`` turns divided by the
+    factor, a linear ramp over the turns between; mscale = 0.1 ln(factor) + 1).
+    """
+    import math
+
+    import torch
+
+    if rot < 2 or rot % 2 or not base > 0 or not factor >= 1.0:
+        raise ValueError("rot must be even and positive, base positive, factor at least 1")
+    mscale = 1.0
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError("base scaling needs at least two pairs")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if not original_context or original_context < 1 or not fast > slow:
+            raise ValueError("parts scaling needs original_context and fast > slow")
+        turns = original_context * f / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.float().to(device), mscale
+
+
+def _rope_params(positions, inv_freq, n, device, first, interleaved, inverse, mscale):
+    import torch
+
+    _need("positions", positions, device, torch.int32, (n,))
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    _need("inv_freq", inv_freq, device, torch.float32, (inv_freq.shape[0],))
+    return ctypes.byref(RopeParams(positions.data_ptr(), inv_freq.data_ptr(),
+                                   2 * inv_freq.shape[0], first, bool(interleaved), bool(inverse),
+                                   mscale))
+
+
+def rope(x, positions, inv_freq, *, first=0, interleaved=False, mscale=1.0, inverse=False,
+         out=None, status=None, stream=None):
+    """Rotary positions on columns [first, first + 2 len(inv_freq)) of x
+    ([n, H, d] or [n, d], bf16 or fp32, row and head strides allowed); the
+    other columns are copied. Pairs are (i, i + rot/2), or (2i, 2i + 1) if
+    ``interleaved``. ``out=x`` works in place. ``inverse`` rotates back, which
+    is also the gradient. See :func:`rope_frequencies`."""
+    import torch
+
+    lib = load()
+    x3 = _rows3("x", x)
+    n, H, d = x3.shape
+    dev = x.device
+    code = _elem("x", x, (ELEM_BF16, ELEM_F32))
+    params = _rope_params(positions, inv_freq, n, dev, first, interleaved, inverse, mscale)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+        raise ValueError("out must match x in shape, type and device")
+    o3 = _rows3("out", out)
+    xr, xh = _row_strides(x3)
+    orow, oh = _row_strides(o3)
+    st = lib.hytopk_rope(x3.data_ptr(), xr, xh, code, n, H, d, params, o3.data_ptr(), orow, oh,
+                         _status_ptr(status, dev), _raw_stream(dev, stream))
+    if st != 0:
+        raise HytopkError(st, "hytopk_rope")
+    return out
+
+
+def _cache3(cache, cache_scale):
+    import torch
+
+    c3 = _rows3("cache", cache)
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    code = _elem("cache", cache, (ELEM_E4M3, ELEM_BF16))
+    if (code == ELEM_E4M3) != (cache_scale is not None):
+        raise ValueError("an e4m3 cache needs cache_scale, a bf16 cache takes none")
+    if cache_scale is not None:
+        _need("cache_scale", cache_scale, cache.device, torch.float32, cache.shape[:-1])
+    return c3, code
+
+
+def cache_write(x, cache, cache_scale=None, *, slots=None, positions=None, inv_freq=None, first=0,
+                interleaved=False, mscale=1.0, status=None, stream=None):
+    """Write rows x ([n, H, d] or [n, d], bf16 or fp32) into cache rows
+    ``slots`` (int32 [n], -1 skips; None: rows 0..n-1), rotated first when
+    ``positions`` and ``inv_freq`` are given, and quantised when the cache
+    ([L, H, d] or [L, d]) is float8_e4m3fn: one scale per (row, head) in
+    ``cache_scale``, as :func:`select` and :func:`attend` take them."""
+    import torch
+
+    lib = load()
+    x3 = _rows3("x", x)
+    n, H, d = x3.shape
+    dev = x.device
+    code = _elem("x", x, (ELEM_BF16, ELEM_F32))
+    c3, ccode = _cache3(cache, cache_scale)
+    if cache.device != dev or c3.shape[1:] != (H, d):
+        raise ValueError(f"cache rows are {tuple(c3.shape[1:])} on {cache.device}, expected "
+                         f"{(H, d)} on {dev}")
+    params = None
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    if positions is not None:
+        params = _rope_params(positions, inv_freq, n, dev, first, interleaved, False, mscale)
+    if slots is not None:
+        _need("slots", slots, dev, torch.int32, (n,))
+    xr, xh = _row_strides(x3)
+    st = lib.hytopk_cache_write(x3.data_ptr(), xr, xh, code, n, H, d, params,
+                                None if slots is None else slots.data_ptr(), c3.data_ptr(), ccode,
+                                None if cache_scale is None else cache_scale.data_ptr(),
+                                c3.shape[0], _status_ptr(status, dev), _raw_stream(dev, stream))
+    if st != 0:
+        raise HytopkError(st, "hytopk_cache_write")
+    return cache
+
+
+def cache_read(cache, cache_scale=None, *, slots=None, dtype=None, out=None, status=None,
+               stream=None):
+    """Cache rows ``slots`` (int32 [m]; None: all) as bf16 (default) or fp32."""
+    import torch
+
+    lib = load()
+    c3, ccode = _cache3(cache, cache_scale)
+    dev = cache.device
+    L, H, d = c3.shape
+    n = L
+    if slots is not None:
+        n = slots.shape[0]
+        _need("slots", slots, dev, torch.int32, (n,))
+    shape = (n,) + tuple(cache.shape[1:])
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+    else:
+        _need("out", out, dev, dtype or out.dtype, shape)
+    code = _elem("dtype", out, (ELEM_BF16, ELEM_F32))
+    st = lib.hytopk_cache_read(c3.data_ptr(), ccode,
+                               None if cache_scale is None else cache_scale.data_ptr(), L,
+                               None if slots is None else slots.data_ptr(), n, H, d,
+                               out.data_ptr(), code, _status_ptr(status, dev),
+                               _raw_stream(dev, stream))
+    if st != 0:
+        raise HytopkError(st, "hytopk_cache_read")
+    return out
+
+
+def _packed_heads(name, t):
+    t = _rows3(name, t)
+    n, H, d = t.shape
+    row, head = _row_strides(t)
+    if H > 1 and head != d:
+        raise ValueError(f"{name}: heads must be contiguous within a row")
+    return t, row
+
+
+def _attention(q, k, v, idx):
+    import torch
+
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have one shape and type")
+    dev = q.device
+    q, q_row = _packed_heads("q", q)
+    k, k_row = _packed_heads("k", k)
+    v, v_row = _packed_heads("v", v)
+    n, Hq, d = q.shape
+    L, Hkv, dk = k.shape
+    if dk != d or k.device != dev or v.device != dev:
+        raise ValueError(f"k and v rows must be [{d}] per head on {dev}")
+    if idx.dim() != 2:
+        raise ValueError("idx must be [n, k]")
+    _need("idx", idx, dev, torch.int32, (n, idx.shape[1]))
+    return q, q_row, k, k_row, v, v_row, n, L, Hq, Hkv, d, idx.shape[1], dev
+
+
+def attend(q, k, v, idx, *, k_scale=None, v_scale=None, scale=None, out_dtype=None, out=None,
+           status=None, stream=None):
+    """Attention of each query over its own selected rows: q [n, Hq, d] bf16,
+    k and v [L, Hkv, d] (or [L, d]) bf16 or float8_e4m3fn with k_scale /
+    v_scale [L, Hkv] (or [L]) fp32, idx [n, k] int32 as :func:`select` returns
+    it (-1: none). ``scale`` defaults to d ** -0.5. Returns ``(out [n, Hq, d],
+    lse [n, Hq])``; ``out_dtype`` bf16 (default) or fp32 (for training:
+    :func:`attend_backward` then keeps fp32 accuracy)."""
+    import torch
+
+    lib = load()
+    code = _elem("k", k, (ELEM_BF16, ELEM_E4M3))
+    if (code == ELEM_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("an e4m3 cache needs k_scale and v_scale, a bf16 cache takes none")
+    if k_scale is not None:
+        _need("k_scale", k_scale, q.device, torch.float32, k.shape[:-1])
+        _need("v_scale", v_scale, q.device, torch.float32, v.shape[:-1])
+    q3, qr, k3, kr, v3, vr, n, L, Hq, Hkv, d, k_top, dev = _attention(q, k, v, idx)
+    if out is None:
+        out = torch.empty((n, Hq, d), dtype=out_dtype or torch.bfloat16, device=dev)
+    else:
+        _need("out", out, dev, out_dtype or out.dtype, (n, Hq, d))
+    ocode = _elem("out_dtype", out, (ELEM_BF16, ELEM_F32))
+    lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
+    st = lib.hytopk_attend(q3.data_ptr(), qr, k3.data_ptr(), kr,
+                           None if k_scale is None else k_scale.data_ptr(), v3.data_ptr(), vr,
+                           None if v_scale is None else v_scale.data_ptr(), idx.data_ptr(), n, L,
+                           Hq, Hkv, d, k_top, code, d ** -0.5 if scale is None else scale,
+                           out.data_ptr(), ocode, lse.data_ptr(), _status_ptr(status, dev),
+                           _raw_stream(dev, stream))
+    if st != 0:
+        raise HytopkError(st, "hytopk_attend")
+    return out, lse
+
+
+def attend_backward(q, k, v, idx, out, lse, grad, *, scale=None, dk=None, dv=None, status=None,
+                    stream=None):
+    """Gradients of :func:`attend` (bf16 k and v): ``(dq [n, Hq, d], dk, dv)``
+    in fp32, dk and dv shaped like k. ``grad`` [n, Hq, d] bf16 is the gradient
+    of out. ``dk`` / ``dv`` are added to when given (else zeroed tensors)."""
+    import torch
+
+    lib = load()
+    q3, qr, k3, kr, v3, vr, n, L, Hq, Hkv, d, k_top, dev = _attention(q, k, v, idx)
+    _elem("k", k, (ELEM_BF16,))
+    _need("grad", grad, dev, torch.bfloat16, (n, Hq, d))
+    _need("out", out, dev, out.dtype, (n, Hq, d))
+    _need("lse", lse, dev, torch.float32, (n, Hq))
+    ocode = _elem("out", out, (ELEM_BF16, ELEM_F32))
+    dq = torch.empty((n, Hq, d), dtype=torch.float32, device=dev)
+    if dk is None:
+        dk = torch.zeros(k.shape, dtype=torch.float32, device=dev)
+    else:
+        _need("dk", dk, dev, torch.float32, k.shape)
+    if dv is None:
+        dv = torch.zeros(v.shape, dtype=torch.float32, device=dev)
+    else:
+        _need("dv", dv, dev, torch.float32, v.shape)
+    st = lib.hytopk_attend_backward(q3.data_ptr(), qr, k3.data_ptr(), kr, v3.data_ptr(), vr,
+                                    idx.data_ptr(), out.data_ptr(), ocode, lse.data_ptr(),
+                                    grad.data_ptr(), n, L, Hq, Hkv, d, k_top,
+                                    d ** -0.5 if scale is None else scale, dq.data_ptr(),
+                                    dk.data_ptr(), dv.data_ptr(), _status_ptr(status, dev),
+                                    _raw_stream(dev, stream))
+    if st != 0:
+        raise HytopkError(st, "hytopk_attend_backward")
+    return dq, dk, dv

@@ -101,6 +101,8 @@ typedef enum { HYTOPK_BF16 = 0, HYTOPK_E4M3 = 1, HYTOPK_E4M3_BF16 = 2 } hytopk_d
 #define HYTOPK_DEV_REPLAY_BAD_INDEX 0x1u /* replay index not -1 and outside [0, L): entry is NaN */
 #define HYTOPK_DEV_BAD_SCALE 0x2u        /* a q_scale or k_scale <= 0 (results undefined) */
 #define HYTOPK_DEV_BAD_POSITION 0x4u     /* a position outside [0, L): that query is all -1 */
+#define HYTOPK_DEV_BAD_INDEX HYTOPK_DEV_REPLAY_BAD_INDEX /* a slot or index outside [0, L), not -1 */
+#define HYTOPK_DEV_NONFINITE 0x8u        /* a NaN or infinite value was quantised */
 /* A bounded wait inside a tensor-core kernel gave up (after 2 s): the kernel
  * stopped its loops, freed its tensor memory and returned, so every output of
  * that call is undefined. It signals a stalled GPU or a library bug. */
@@ -408,6 +410,132 @@ HYTOPK_API hytopk_status hytopk_replay_backward_varlen(
     const int32_t* idx, const float* grad, const int32_t* cu_q, const int32_t* cu_k, int B, int H,
     int d, int k_top, hytopk_dtype dt, float* dq, float* dk, float* dw, uint32_t* dev_status,
     cudaStream_t stream);
+
+/* ---- around the selection ------------------------------------------------------
+ * The operators a program runs next to hytopk_select: rotary positions on
+ * queries and keys, e4m3 cache rows written and read back (the codes and row
+ * scales that hytopk_select takes), and the attention over the selected rows
+ * with its gradients. They follow the conventions above (device pointers owned
+ * by the caller, asynchronous on `stream`, no allocation, no workspace, status
+ * codes) except that the arrays named below may have row strides. Strides
+ * count elements; the last axis is always contiguous. */
+
+/* Element types of these operators' arrays. */
+typedef enum {
+  HYTOPK_ELEM_BF16 = 0,
+  HYTOPK_ELEM_E4M3 = 1, /* OCP FP8 E4M3 codes with one fp32 scale per (row, head) */
+  HYTOPK_ELEM_F32 = 2
+} hytopk_elem;
+
+/* Rotary positions (host struct; the two pointers are device memory).
+ *   positions [n] int32, 0 <= pos < 2^24 (any other sets
+ *             HYTOPK_DEV_BAD_POSITION and makes the row's rotated part NaN)
+ *   inv_freq  [rot / 2] fp32: angle of pair i = positions[t] * inv_freq[i]
+ *   rot       rotated columns, a multiple of 16; first: the first of them, a
+ *             multiple of 8; first + rot <= d
+ *   interleaved  0: pair i is columns first + i, first + rot/2 + i;
+ *                1: columns first + 2i, first + 2i + 1
+ *   inverse   nonzero: rotate by the negative angle. The rotation's transpose
+ *             is its inverse, so this (with the same mscale) is the gradient.
+ *   mscale    factor on the rotated columns (1 for plain rotary positions) */
+typedef struct {
+  const int32_t* positions;
+  const float* inv_freq;
+  int rot, first, interleaved, inverse;
+  float mscale;
+} hytopk_rope_params;
+
+/* Rotary positions: for every row t, head h and pair i with angle
+ * a = positions[t] * inv_freq[i],
+ *   (y1, y2) = mscale * (x1 cos a - x2 sin a, x1 sin a + x2 cos a);
+ * columns outside [first, first + rot) are copied. Angles are reduced with the
+ * exact product (about 1 ulp of fp32 at every position); arithmetic is fp32,
+ * rounded once.
+ *   x    [n, H, d] bf16 or fp32 with strides x_row, x_head; out likewise, the
+ *        same type. out may be x itself (same strides); otherwise they must
+ *        not overlap.
+ *   d a multiple of 8, 8 <= d <= 1024, H >= 1, n >= 0. Base pointers must be
+ *   16-byte aligned and strides multiples of 16 bytes (HYTOPK_MISALIGNED). */
+HYTOPK_API hytopk_status hytopk_rope(const void* x, int64_t x_row, int64_t x_head,
+                                     hytopk_elem type, int n, int H, int d,
+                                     const hytopk_rope_params* rope, void* out, int64_t out_row,
+                                     int64_t out_head, uint32_t* dev_status, cudaStream_t stream);
+
+/* Rows into a cache: row t of x, rotated if `rope` is not NULL, goes to cache
+ * row slots[t] (row t if slots is NULL).
+ *   x      [n, H, d] bf16 or fp32, strides as in hytopk_rope
+ *   cache  [L, H, d] contiguous, e4m3 (with cache_scale [L, H] fp32) or bf16
+ *          (cache_scale NULL)
+ * e4m3: per (row, head) scale = max(amax / 448, 2^-126) over the finite
+ * elements (1 for a row of zeros), code = x / scale rounded to nearest even,
+ * so |code| <= 448 and the scale is finite and > 0 as hytopk_select requires.
+ * A NaN or infinite element becomes the NaN code and sets
+ * HYTOPK_DEV_NONFINITE. The rotated values are not rounded before they are
+ * quantised.
+ *   slots[t] = -1 skips the row; any other slot outside [0, L) skips it and
+ *   sets HYTOPK_DEV_BAD_INDEX. Slots of one call must be distinct: of rows
+ *   with one slot, parts of either may be left there. */
+HYTOPK_API hytopk_status hytopk_cache_write(const void* x, int64_t x_row, int64_t x_head,
+                                            hytopk_elem x_type, int n, int H, int d,
+                                            const hytopk_rope_params* rope, const int32_t* slots,
+                                            void* cache, hytopk_elem cache_type,
+                                            float* cache_scale, int L, uint32_t* dev_status,
+                                            cudaStream_t stream);
+
+/* Cache rows back: out [n, H, d] (bf16 or fp32, contiguous) row t = cache row
+ * slots[t] (row t if slots is NULL), code * scale for e4m3, rounded once.
+ * slots[t] = -1 gives a row of zeros; any other slot outside [0, L) gives NaN
+ * and sets HYTOPK_DEV_BAD_INDEX. */
+HYTOPK_API hytopk_status hytopk_cache_read(const void* cache, hytopk_elem cache_type,
+                                           const float* cache_scale, int L, const int32_t* slots,
+                                           int n, int H, int d, void* out, hytopk_elem out_type,
+                                           uint32_t* dev_status, cudaStream_t stream);
+
+/* Attention of each query over its own selected rows:
+ *   s[j] = scale * q[t,h] . k[idx[t,j], h / G],  G = Hq / Hkv
+ *   out[t,h] = sum_j softmax(s)[j] * v[idx[t,j], h / G],  lse[t,h] = log sum_j exp(s[j])
+ *   q    [n, Hq, d] bf16, row stride q_row (heads contiguous)
+ *   k, v [L, Hkv, d] bf16, or e4m3 with k_scale, v_scale [L, Hkv] fp32;
+ *        row strides k_row, v_row (heads contiguous)
+ *   idx  [n, k_top] int32 in any order; -1 is no row. Any other index outside
+ *        [0, L) counts as no row and sets HYTOPK_DEV_BAD_INDEX. A repeated
+ *        index counts as often as it is there. Causality is not checked.
+ *   out  [n, Hq, d] bf16 or fp32; lse [n, Hq] fp32 or NULL. A query with no
+ *        row gets out = 0 and lse = -inf.
+ * Sums and softmax statistics are fp32. The tensor cores take bf16 operands:
+ * a bf16 result uses the weights exp(s - max) rounded to bf16 (an error of the
+ * size of the result's own rounding); an fp32 result uses them as the sum of
+ * three bf16 parts (24 bits).
+ *   1 <= Hkv, Hq a multiple of Hkv, G <= 128, d in {64, 128, 256} (fp32
+ *   results: {64, 128}), 1 <= k_top <= 16384, n * Hkv < 2^31. Base pointers
+ *   16-byte aligned, strides multiples of 16 bytes. */
+HYTOPK_API hytopk_status hytopk_attend(const void* q, int64_t q_row, const void* k, int64_t k_row,
+                                       const float* k_scale, const void* v, int64_t v_row,
+                                       const float* v_scale, const int32_t* idx, int n, int L,
+                                       int Hq, int Hkv, int d, int k_top, hytopk_elem cache_type,
+                                       float scale, void* out, hytopk_elem out_type, float* lse,
+                                       uint32_t* dev_status, cudaStream_t stream);
+
+/* Gradients of hytopk_attend for bf16 k and v. With p[j] = exp(s[j] - lse),
+ * dp[j] = grad[t,h] . v[idx[t,j]] and ds[j] = p[j] (dp[j] - grad[t,h] . out[t,h]):
+ *   dq [n, Hq, d]  fp32, written:  scale * sum_j ds[j] k[idx[t,j]]
+ *   dk [L, Hkv, d] fp32, ADDED TO: scale * ds[j] q[t,h], summed over the group's heads
+ *   dv [L, Hkv, d] fp32, ADDED TO: p[j] grad[t,h], summed over the group's heads
+ *   out (bf16 or fp32; the fp32 result keeps the gradients at fp32 accuracy)
+ *   and lse are hytopk_attend's; grad [n, Hq, d] bf16 contiguous.
+ * p and ds enter the tensor cores as the sum of three bf16 parts (24 bits);
+ * sums are fp32. dk and dv take floating-point atomic additions, so their low
+ * bits depend on the order of arrival. Rows outside [0, L) as in
+ * hytopk_attend; a query with no row has dq = 0.
+ *   d in {64, 128}; otherwise shapes, strides and alignment of hytopk_attend. */
+HYTOPK_API hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, const void* k,
+                                                int64_t k_row, const void* v, int64_t v_row,
+                                                const int32_t* idx, const void* out,
+                                                hytopk_elem out_type, const float* lse,
+                                                const void* grad, int n, int L, int Hq, int Hkv,
+                                                int d, int k_top, float scale, float* dq,
+                                                float* dk, float* dv, uint32_t* dev_status,
+                                                cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 HYTOPK_API const char* hytopk_status_string(hytopk_status status);
