@@ -8,6 +8,15 @@
 #include "launch.h"
 
 namespace hytopk {
+
+// attend_d*.cu
+cudaError_t launch_attend_d64_bf16(const att::Args& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_d64_e4m3(const att::Args& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_d128_bf16(const att::Args& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_d128_e4m3(const att::Args& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_d256_bf16(const att::Args& a, bool f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_d256_e4m3(const att::Args& a, bool f32, int sms, cudaStream_t st);
+
 namespace att {
 namespace {
 
@@ -42,55 +51,6 @@ __device__ __forceinline__ int checked_row(const Args& a, int t, int j) {
   if (s >= 0 && s < a.L) return s;
   if (s != -1 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
   return -1;
-}
-
-// One query head per CTA: scores in shared memory, softmax, weighted sum.
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) k_attend_simple(const Args a, int out_f32) {
-  extern __shared__ float sh[];
-  float* p = sh;               // [k_top]
-  float* qs = sh + a.k_top;    // [d]
-  __shared__ float red[4];
-  const int Hq = a.Hkv * a.G;
-  const int t = blockIdx.x / Hq, h = blockIdx.x % Hq, hk = h / a.G;
-  for (int j = threadIdx.x; j < a.d; j += kThreads)
-    qs[j] = __bfloat162float(
-        static_cast<const __nv_bfloat16*>(a.q)[(size_t)t * a.q_row + (size_t)h * a.d + j]);
-  __syncthreads();
-  float top = -INFINITY;
-  for (int j = threadIdx.x; j < a.k_top; j += kThreads) {
-    const int s = checked_row(a, t, j);
-    float x = -INFINITY;
-    if (s >= 0) {
-      x = 0.0f;
-      for (int i = 0; i < a.d; ++i) x += qs[i] * row_elem<E4M3>(a.k, a.k_row, s, hk, a.d, i);
-      x *= a.scale * (E4M3 ? a.k_scale[(size_t)s * a.Hkv + hk] : 1.0f);
-    }
-    p[j] = x;
-    top = fmaxf(top, x);
-  }
-  top = block_reduce(top, true, red);
-  float z = 0.0f;
-  for (int j = threadIdx.x; j < a.k_top; j += kThreads) {
-    const float e = p[j] == -INFINITY ? 0.0f : __expf(p[j] - top);
-    z += e;
-    p[j] = e;
-  }
-  z = block_reduce(z, false, red);
-  const size_t at = ((size_t)t * Hq + h) * a.d;
-  for (int i = threadIdx.x; i < a.d; i += kThreads) {
-    float o = 0.0f;
-    for (int j = 0; j < a.k_top; ++j) {
-      if (p[j] == 0.0f) continue;
-      const int s = a.idx[(size_t)t * a.k_top + j];
-      o += p[j] * (E4M3 ? a.v_scale[(size_t)s * a.Hkv + hk] : 1.0f) *
-           row_elem<E4M3>(a.v, a.v_row, s, hk, a.d, i);
-    }
-    o = z > 0.0f ? o / z : 0.0f;
-    if (out_f32) static_cast<float*>(a.out)[at + i] = o;
-    else static_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16_rn(o);
-  }
-  if (threadIdx.x == 0 && a.lse) a.lse[(size_t)t * Hq + h] = z > 0.0f ? top + logf(z) : -INFINITY;
 }
 
 // One query head per CTA: a warp per selected row.
@@ -200,14 +160,11 @@ extern "C" hytopk_status hytopk_attend(const void* q, int64_t q_row, const void*
   a.out = out;
   a.lse = lse;
   a.status = dev_status;
-  const size_t smem = sizeof(float) * ((size_t)k_top + d);
-  const int f32 = out_type == HYTOPK_ELEM_F32;
-  auto kernel = e4 ? att::k_attend_simple<true> : att::k_attend_simple<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return HYTOPK_CUDA_ERROR;
-  kernel<<<(unsigned)n * Hq, att::kThreads, smem, stream>>>(a, f32);
-  return cudaGetLastError() == cudaSuccess ? HYTOPK_OK : HYTOPK_CUDA_ERROR;
+  const bool f32 = out_type == HYTOPK_ELEM_F32;
+  auto launch = d == 64    ? (e4 ? launch_attend_d64_e4m3 : launch_attend_d64_bf16)
+                : d == 128 ? (e4 ? launch_attend_d128_e4m3 : launch_attend_d128_bf16)
+                           : (e4 ? launch_attend_d256_e4m3 : launch_attend_d256_bf16);
+  return launch(a, f32, num_sms(), stream) == cudaSuccess ? HYTOPK_OK : HYTOPK_CUDA_ERROR;
 }
 
 extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, const void* k,
