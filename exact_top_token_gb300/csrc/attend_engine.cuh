@@ -25,9 +25,9 @@
 // three times; bf16 results use one part, whose rounding is of the size of the
 // result's own.
 //
-//   warps 0..7   softmax (warpgroup g: heads g N/2 ..), O read-out
-//   warps 8..    producers: 4 (bf16: cp.async) or 8 (e4m3: converted to bf16)
-//   last warp    MMA issuer, TMEM
+//   warps 0..7    softmax (warpgroup g: heads g N/2 ..), O read-out
+//   warps 8..11   producers (bf16: cp.async; e4m3: converted to bf16 on the way)
+//   warp 12       MMA issuer, TMEM
 //
 // Few items: a cluster of S CTAs shares an item, each taking a share of its
 // tiles; the partial O, m and sums are joined through distributed shared memory.
@@ -62,20 +62,19 @@ struct Cfg {
   static constexpr int OBLK = D <= 128 ? 1 : D / 128;  // blocks of 128 result columns
   static constexpr int QBYTES = N * RB;
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
-  static constexpr int PWARPS = E4 ? 8 : 4;
+  // P buffers: two, unless their three parts or 128 heads leave no room for the ring
+  static constexpr int PB = F32 || N > 64 ? 1 : 2;
+  static constexpr int PWARPS = 4;
   static constexpr int THREADS = (kSoftmaxWarps + PWARPS + 1) * 32;
   static constexpr int MMA_WARP = kSoftmaxWarps + PWARPS;
   // m, scale factors, 1 / sum [N] each; per-quadrant sums or maxima [4][N]
   static constexpr int MISC = (3 + 4) * N * 4 + 512;
-  static constexpr int FIXED = PARTS * PBYTES + QB * QBYTES + MISC + 1024;
+  static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + MISC + 1024;
   static constexpr int NS_MAX = (227 * 1024 - FIXED) / SLOT;
   static constexpr int NS = NS_MAX < 8 ? NS_MAX : 8;
-  // tiles whose copies may be unpublished while a producer waits: with more,
-  // the item whose queries it waits to replace might not have been published
-  static constexpr int LAG = NS - 2 < 3 ? NS - 2 : 3;
   static constexpr int RING_OFF = 0;
   static constexpr int P_OFF = NS * SLOT;
-  static constexpr int Q_OFF = P_OFF + PARTS * PBYTES;
+  static constexpr int Q_OFF = P_OFF + PB * PARTS * PBYTES;
   static constexpr int MISC_OFF = Q_OFF + QB * QBYTES;
   static constexpr int SMEM = MISC_OFF + MISC + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
@@ -162,6 +161,24 @@ __device__ __forceinline__ uint32_t p_offset(int r, int h) {
                     ((((h & 63) >> 3) ^ (r & 7)) << 4));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
+               : "memory");
+}
+
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -205,8 +222,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   uint64_t* s_full = q_empty + 2;
   uint64_t* s_empty = s_full + 2;
   uint64_t* p_full = s_empty + 2;
-  uint64_t* p_empty = p_full + 1;
-  uint64_t* o_full = p_empty + 1;
+  uint64_t* p_empty = p_full + 2;
+  uint64_t* o_full = p_empty + 2;
   uint64_t* o_empty = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -216,19 +233,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   if (pl.splits > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(full + i, C::PWARPS * 32);
+      tc::mbar_init(full + i, C::E4 ? C::PWARPS : C::PWARPS * 32);
       tc::mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(q_full + i, C::PWARPS * 32);
+      tc::mbar_init(q_full + i, C::PWARPS);
       tc::mbar_init(q_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(s_empty + i, kSoftmaxWarps);
       tc::mbar_init(o_full + i, 1);
       tc::mbar_init(o_empty + i, kSoftmaxWarps);
+      tc::mbar_init(p_full + i, kSoftmaxWarps);
+      tc::mbar_init(p_empty + i, 1);
     }
-    tc::mbar_init(p_full, kSoftmaxWarps * 32);
-    tc::mbar_init(p_empty, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -262,6 +279,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     x.nh = min(pl.heads, a.G - b * pl.heads);
     return x;
   };
+  // A role's walk over its tiles in order: the item and tile of tile g, kept by
+  // steps (an item costs divisions; a tile must not).
+  struct Walk {
+    int qi, i, t, hk;  // item, tile within it, its query and cache head
+  };
+  auto walk_start = [&]() -> Walk {
+    const Item x = item_of(0);
+    return Walk{0, 0, x.t, x.hk};
+  };
+  auto walk_next = [&](Walk& w) {
+    if (++w.i == ntile) {
+      w.i = 0;
+      const Item x = item_of(++w.qi);
+      w.t = x.t;
+      w.hk = x.hk;
+    }
+  };
   // selected row of entry j of query t, -1 if there is none
   auto row_of = [&](int t, int j) -> int {
     const int s = j < a.k_top ? __ldg(a.idx + (size_t)t * a.k_top + j) : -1;
@@ -272,6 +306,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // ---------------- producers ----------------
     const int tid = threadIdx.x - kSoftmaxWarps * 32;
     const int pw = warp - kSoftmaxWarps;
+    // this warp's writes to a buffer are done: one arrival per warp
+    auto publish = [&](uint64_t* bar) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar);
+    };
     // the item's query rows, zero beyond its heads
     auto load_query = [&](int qi) -> bool {
       const int qb = qi % C::QB;
@@ -288,8 +328,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         if (r < x.nh) v = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * C::RB) + c);
         *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v;
       }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(q_full + qb);
+      publish(q_full + qb);
       return true;
     };
     if constexpr (!C::E4) {
@@ -297,189 +336,222 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       constexpr int CPR = C::RB / 16;
       constexpr int RPP = CPR >= 32 ? 1 : 32 / CPR;
       constexpr int PASSES = 32 / RPP;              // row groups per warp and tile
-      constexpr int CPL = CPR > 32 ? CPR / 32 : 1;  // chunks a lane copies per row
-      int npend = 0, seq = 0;
-      auto publish_oldest = [&]() {
-        tc::mbar_arrive(full + (seq - npend) % NS);
-        --npend;
-      };
+      constexpr int SHIFT = CPR >= 32 ? 5 : (CPR == 16 ? 4 : 3);  // lanes per row
+      int slot = 0;
+      uint32_t phase = 1;
       bool ok = true;
-      int s_next = total > 0 ? row_of(item_of(0).t, tile0 * 128 + tid) : -1;
-      for (int g = 0; g < total && ok; ++g) {
-        const int qi = g / ntile, i = g - qi * ntile;
-        const Item x = item_of(qi);
-        if (i == 0) {
-          if (C::QB == 1 && npend) {
-            // the previous item must be able to finish before its queries are replaced
-            tc::cp_async_wait<0>();
-            tc::fence_proxy_async_smem();
-            while (npend) publish_oldest();
-          }
-          if (!load_query(qi)) break;
-        }
-        const int s_own = s_next;
+      Walk w = walk_start(), wn = w;  // this tile; the next one
+      int s_next = total > 0 ? row_of(w.t, tile0 * 128 + tid) : -1;
+      for (int g = 0; g < total && ok; ++g, w = wn) {
+        if (w.i == 0 && !load_query(w.qi)) break;
+        // every pass's row first, so that the copies go out back to back
+        int rows[PASSES];
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+          rows[p] = __shfl_sync(0xffffffffu, s_next, p * RPP + (lane >> SHIFT));
         if (g + 1 < total) {
-          const int q2 = (g + 1) / ntile;
-          s_next = row_of(item_of(q2).t, (tile0 + (g + 1) - q2 * ntile) * 128 + tid);
+          walk_next(wn);
+          s_next = row_of(wn.t, (tile0 + wn.i) * 128 + tid);
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const int slot = seq % NS;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(empty + slot, ((seq / NS) & 1) ^ 1,
-                                                     abort_flag, a.status));
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(empty + slot, phase, abort_flag, a.status));
           if (!ok) break;
-          uint8_t* dst = ring + slot * C::SLOT;
-          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) + (size_t)x.hk * C::RB;
+          const uint32_t dst = tc::smem_u32(ring + slot * C::SLOT);
+          const int c = lane & ((1 << SHIFT) - 1);
+          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) +
+                                (size_t)w.hk * C::RB + c * 16;
           const int64_t row_bytes = (kv ? a.v_row : a.k_row) * 2;
 #pragma unroll
           for (int p = 0; p < PASSES; ++p) {
-            const int sl = p * RPP + (CPR >= 32 ? 0 : lane / CPR);
-            const int s = __shfl_sync(0xffffffffu, s_own, sl);
-            const uint8_t* src = base + (s >= 0 ? (size_t)s * row_bytes : 0);
-#pragma unroll
-            for (int u = 0; u < CPL; ++u) {
-              const int c = (CPR >= 32 ? lane : lane % CPR) + u * 32;
-              tc::cp_async16(dst + Geo::chunk_offset(pw * 32 + sl, c, 128), src + c * 16, s >= 0);
-            }
+            const int s = rows[p];
+            const uint8_t* src = base + (s >= 0 ? s * row_bytes : 0);
+            cp_async16(dst + Geo::chunk_offset(pw * 32 + p * RPP + (lane >> SHIFT), c, 128), src,
+                       s >= 0);
           }
-          tc::cp_async_commit();
-          ++npend;
-          ++seq;
-          if (npend > C::LAG) {
-            tc::cp_async_wait<C::LAG>();
-            tc::fence_proxy_async_smem();
-            publish_oldest();
+          // arrives for this thread when its copies so far have landed; the MMA
+          // issuer's proxy fence makes them visible to the tensor core
+          cp_async_arrive(full + slot);
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
-      tc::cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      while (npend) publish_oldest();
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-      // warp w converts rows 16w .. 16w + 15 of every tile: CPR lanes of 16 codes per row
+      // Warp w converts rows 32w .. 32w + 31 of every tile, CPR lanes of 16 codes
+      // per row. A tile is two or four chunks of up to 8 loads a lane (K's, then
+      // V's); two chunks are in registers, so that one is always in flight.
       constexpr int CPR = D / 16;          // 4, 8 or 16
       constexpr int RPP = 32 / CPR;
-      constexpr int PASSES = 16 / RPP;
+      constexpr int PASSES = 32 / RPP;
+      constexpr int CP = PASSES < 8 ? PASSES : 8;  // passes of a chunk
+      constexpr int NCH = 2 * PASSES / CP;         // chunks of a tile (K and V)
       const int c = lane % CPR;
-      auto issue = [&](int g, int s_own, uint4 (&v)[2][PASSES]) {
-        const Item x = item_of(g / ntile);
+      uint4 buf[2][CP];
+      auto issue = [&](int hk, int s_own, int ch, uint4 (&v)[CP]) {
+        const bool isv = ch >= NCH / 2;
+        const uint8_t* base =
+            static_cast<const uint8_t*>(isv ? a.v : a.k) + (size_t)hk * D + c * 16;
+        const int64_t row_bytes = isv ? a.v_row : a.k_row;
+        const int p0 = (ch % (NCH / 2)) * CP;
+        int rows[CP];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) + (size_t)x.hk * D;
-          const int64_t row_bytes = kv ? a.v_row : a.k_row;
+        for (int p = 0; p < CP; ++p)
+          rows[p] = __shfl_sync(0xffffffffu, s_own, (p0 + p) * RPP + lane / CPR);
 #pragma unroll
-          for (int p = 0; p < PASSES; ++p) {
-            const int s = __shfl_sync(0xffffffffu, s_own, p * RPP + lane / CPR);
-            v[kv][p] = s >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + (size_t)s * row_bytes) + c)
+        for (int p = 0; p < CP; ++p)
+          v[p] = rows[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + rows[p] * row_bytes))
                               : make_uint4(0, 0, 0, 0);
-          }
+      };
+      int slot = 0;
+      uint32_t phase = 1;
+      auto store = [&](int ch, const uint4 (&v)[CP]) -> bool {
+        if (ch % (NCH / 2) == 0 &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(empty + slot, phase, abort_flag, a.status)))
+          return false;
+        uint8_t* dst = ring + slot * C::SLOT;
+        const int p0 = (ch % (NCH / 2)) * CP;
+#pragma unroll
+        for (int p = 0; p < CP; ++p) {
+          const int r = pw * 32 + (p0 + p) * RPP + lane / CPR;
+          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c, 128)) =
+              e4m3x8_to_bf16(make_uint2(v[p].x, v[p].y));
+          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c + 1, 128)) =
+              e4m3x8_to_bf16(make_uint2(v[p].z, v[p].w));
         }
-      };
-      auto own = [&](int g) -> int {
-        const int qi = g / ntile;
-        return row_of(item_of(qi).t, (tile0 + g - qi * ntile) * 128 + pw * 16 + (lane & 15));
-      };
-      auto store = [&](int g, const uint4 (&v)[2][PASSES]) -> bool {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int seq = 2 * g + kv, slot = seq % NS;
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(empty + slot, ((seq / NS) & 1) ^ 1,
-                                                     abort_flag, a.status)))
-            return false;
-          uint8_t* dst = ring + slot * C::SLOT;
-#pragma unroll
-          for (int p = 0; p < PASSES; ++p) {
-            const int r = pw * 16 + p * RPP + lane / CPR;
-            const uint4 w = v[kv][p];
-            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c, 128)) =
-                e4m3x8_to_bf16(make_uint2(w.x, w.y));
-            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c + 1, 128)) =
-                e4m3x8_to_bf16(make_uint2(w.z, w.w));
+        if (ch % (NCH / 2) == NCH / 2 - 1) {
+          publish(full + slot);
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
           }
-          tc::fence_proxy_async_smem();
-          tc::mbar_arrive(full + slot);
         }
         return true;
       };
-      uint4 v[2][PASSES], w[2][PASSES];
-      if (total > 0) issue(0, own(0), v);
-      int s_next = total > 1 ? own(1) : -1;
-      for (int g = 0; g < total; g += 2) {
-        if (g % ntile == 0 && !load_query(g / ntile)) break;
-        if (g + 1 < total) issue(g + 1, s_next, w);
-        if (g + 2 < total) s_next = own(g + 2);
-        if (!store(g, v)) break;
-        if (g + 1 >= total) break;
-        if ((g + 1) % ntile == 0 && !load_query((g + 1) / ntile)) break;
-        if (g + 2 < total) issue(g + 2, s_next, v);
-        if (g + 3 < total) s_next = own(g + 3);
-        if (!store(g + 1, w)) break;
+      Walk w = walk_start(), wn = w;  // this tile; the next one
+      auto own = [&](const Walk& x) { return row_of(x.t, (tile0 + x.i) * 128 + tid); };
+      int s_own = total > 0 ? own(w) : -1, s_next = -1;
+      if (total > 0) {
+        issue(w.hk, s_own, 0, buf[0]);
+        issue(w.hk, s_own, 1, buf[1]);
+      }
+      if (total > 1) {
+        walk_next(wn);
+        s_next = own(wn);
+      }
+      bool ok = true;
+      for (int g = 0; g < total && ok; ++g) {
+        if (w.i == 0 && !load_query(w.qi)) break;
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+          if (!store(ch, buf[ch & 1])) {
+            ok = false;
+            break;
+          }
+          if (ch + 2 < NCH) issue(w.hk, s_own, ch + 2, buf[ch & 1]);
+          else if (g + 1 < total) issue(wn.hk, s_next, ch + 2 - NCH, buf[ch & 1]);
+        }
+        w = wn;
+        s_own = s_next;
+        if (g + 2 < total) {
+          walk_next(wn);
+          s_next = own(wn);
+        }
       }
     }
   } else if (warp == C::MMA_WARP) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
-      constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
-      const uint32_t ring_a = tc::smem_u32(ring), p_a = tc::smem_u32(pbuf);
-      const uint32_t q_a = tc::smem_u32(smem + C::Q_OFF);
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return tc::mbar_wait(bar, parity, abort_flag, a.status);
-      };
-      auto scores = [&](int g) -> bool {
-        const int qi = g / ntile, i = g - qi * ntile;
-        const int seq = 2 * g, slot = seq % NS, qb = qi % C::QB;
-        if (i == 0 && !wait(q_full + qb, (qi / C::QB) & 1)) return false;
-        if (!wait(full + slot, (seq / NS) & 1)) return false;
-        if (!wait(s_empty + (g & 1), ((g >> 1) & 1) ^ 1)) return false;
-        tc::fence_after_sync();
+    // ---------------- MMA issuer ----------------
+    // The whole warp keeps the (uniform) state and waits; one elected lane
+    // issues. A single-lane branch would move every descriptor word through the
+    // vector registers, which took 100 cycles per product.
+    constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
+    constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
+    const uint64_t ring_k = desc2(tc::smem_u32(ring), 16, 1024);
+    const uint64_t ring_v = desc2(tc::smem_u32(ring), 16384, 1024);
+    const uint64_t p_d = desc2(tc::smem_u32(pbuf), 16384, 1024);
+    const uint64_t q_d = desc2(tc::smem_u32(smem + C::Q_OFF), 16, 1024);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, a.status)) != 0;
+    };
+    struct At {
+      int i, qi, slot;  // tile of its item, item, ring slot
+      uint32_t phase;
+    };
+    auto step = [&](At& w) {
+      if (++w.i == ntile) {
+        w.i = 0;
+        ++w.qi;
+      }
+      w.slot += 2;
+      if (w.slot >= NS) {
+        w.slot -= NS;
+        w.phase ^= 1u;
+      }
+    };
+    At ws{0, 0, 0, 0}, wo{0, 0, 1 % NS, 0};
+    auto scores = [&](int g) -> bool {
+      const int qb = ws.qi % C::QB;
+      if (ws.i == 0 && !wait(q_full + qb, (ws.qi / C::QB) & 1)) return false;
+      if (!wait(full + ws.slot, ws.phase)) return false;
+      if (!wait(s_empty + (g & 1), ((g >> 1) & 1) ^ 1)) return false;
+      if (!C::E4) tc::fence_proxy_async_smem();
+      tc::fence_after_sync();
+      const uint64_t ad = ring_k + (uint64_t)((ws.slot * C::SLOT) >> 4);
+      const uint64_t bd = q_d + (uint64_t)((qb * C::QBYTES) >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint64_t ad = desc2(ring_a + slot * C::SLOT + Geo::step_offset(j, 128), 16, 1024);
-          const uint64_t bd = desc2(q_a + qb * C::QBYTES + Geo::step_offset(j, N), 16, 1024);
-          tc::mma<0>(tmem + C::S_COL + (g & 1) * N, ad, bd, ID_S, j > 0 ? 1u : 0u);
-        }
+        for (int j = 0; j < D / 16; ++j)
+          tc::mma<0>(tmem + C::S_COL + (g & 1) * N, ad + (Geo::step_offset(j, 128) >> 4),
+                     bd + (Geo::step_offset(j, N) >> 4), ID_S, j > 0 ? 1u : 0u);
         tc::mma_commit(s_full + (g & 1));
-        tc::mma_commit(empty + slot);
-        if (i == ntile - 1) tc::mma_commit(q_empty + qb);
-        return true;
-      };
-      auto weighted = [&](int g) -> bool {
-        const int qi = g / ntile, i = g - qi * ntile;
-        const int seq = 2 * g + 1, slot = seq % NS, ob = qi & 1;
-        if (i == 0 && !wait(o_empty + ob, ((qi >> 1) & 1) ^ 1)) return false;
-        if (!wait(full + slot, (seq / NS) & 1)) return false;
-        if (!wait(p_full, g & 1)) return false;
-        tc::fence_after_sync();
+        tc::mma_commit(empty + ws.slot);
+        if (ws.i == ntile - 1) tc::mma_commit(q_empty + qb);
+      }
+      __syncwarp();
+      step(ws);
+      return true;
+    };
+    auto weighted = [&](int g) -> bool {
+      const int ob = wo.qi & 1, pb = g % C::PB;
+      if (wo.i == 0 && !wait(o_empty + ob, ((wo.qi >> 1) & 1) ^ 1)) return false;
+      if (!wait(full + wo.slot, wo.phase)) return false;
+      if (!wait(p_full + pb, (g / C::PB) & 1)) return false;
+      if (!C::E4) tc::fence_proxy_async_smem();
+      tc::fence_after_sync();
+      const uint64_t ad = ring_v + (uint64_t)((wo.slot * C::SLOT) >> 4);
+      const uint64_t bd = p_d + (uint64_t)((pb * C::PARTS * C::PBYTES) >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int blk = 0; blk < C::OBLK; ++blk) {
 #pragma unroll
           for (int part = 0; part < C::PARTS; ++part) {
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {  // 16 rows each
+            for (int s = 0; s < 8; ++s)  // 16 rows each
               // d = 64 has one 64-column atom; the second one that M = 128 takes is
               // whatever follows the tile, and fills accumulator lanes never read
-              const uint64_t ad =
-                  desc2(ring_a + slot * C::SLOT + blk * 32768 + s * 2048, 16384, 1024);
-              const uint64_t bd = desc2(p_a + part * C::PBYTES + s * 2048, 16384, 1024);
-              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * NP, ad, bd, ID_O,
-                         (i > 0 || part > 0 || s > 0) ? 1u : 0u);
-            }
+              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * NP,
+                         ad + ((blk * 32768 + s * 2048) >> 4),
+                         bd + ((part * C::PBYTES + s * 2048) >> 4), ID_O,
+                         (wo.i > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
-        tc::mma_commit(p_empty);
-        tc::mma_commit(empty + slot);
-        if (i == ntile - 1) tc::mma_commit(o_full + ob);
-        return true;
-      };
-      if (total > 0 && scores(0)) {
-        for (int g = 0; g < total; ++g) {
-          if (g + 1 < total && !scores(g + 1)) break;
-          if (!weighted(g)) break;
-        }
+        tc::mma_commit(p_empty + pb);
+        tc::mma_commit(empty + wo.slot);
+        if (wo.i == ntile - 1) tc::mma_commit(o_full + ob);
+      }
+      __syncwarp();
+      step(wo);
+      return true;
+    };
+    if (total > 0 && scores(0)) {
+      for (int g = 0; g < total; ++g) {
+        if (g + 1 < total && !scores(g + 1)) break;
+        if (!weighted(g)) break;
       }
     }
-  } else {
+  } else if (warp < kSoftmaxWarps) {
     // ---------------- softmax: TMEM lane = selected row ----------------
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
@@ -490,19 +562,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     bool have = false;  // some row of the item so far is valid (the same for the warpgroup)
     int s_next = -1;
     float ks_next = 1.0f, vs_next = 1.0f;
-    auto load_entry = [&](int g) {
-      const int qi = g / ntile;
-      const Item x = item_of(qi);
-      const int j = (tile0 + g - qi * ntile) * 128 + row;
-      int s = j < a.k_top ? __ldg(a.idx + (size_t)x.t * a.k_top + j) : -1;
+    auto load_entry = [&](const Walk& w) {
+      const int j = (tile0 + w.i) * 128 + row;
+      int s = j < a.k_top ? __ldg(a.idx + (size_t)w.t * a.k_top + j) : -1;
       if (s != -1 && (s < 0 || s >= a.L)) {
         if (a.status && wg == 0) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
         s = -1;
       }
       s_next = s;
       if (C::E4) {
-        ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + x.hk) : 1.0f;
-        vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + x.hk) : 1.0f;
+        ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + w.hk) : 1.0f;
+        vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + w.hk) : 1.0f;
       }
     };
     // the item's result from O, once its last product is done
@@ -545,11 +615,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (lane == 0) tc::mbar_arrive(o_empty + ob);
       return true;
     };
-    if (total > 0) load_entry(0);
+    Walk wn = walk_start();  // the next tile
+    if (total > 0) load_entry(wn);
     bool pend_any = false;
-    bool done = total == 0;
-    for (int g = 0; g < total && !done; ++g) {
-      const int qi = g / ntile, i = g - qi * ntile;
+    for (int g = 0; g < total; ++g) {
+      const int qi = wn.qi, i = wn.i;
       if (i == 0) {
         have = false;
 #pragma unroll
@@ -558,9 +628,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       const bool valid = s_next >= 0;
       const float c = valid ? c_scale * ks_next : 0.0f;
       const float vs = vs_next;
-      if (g + 1 < total) load_entry(g + 1);
+      if (g + 1 < total) {
+        walk_next(wn);
+        load_entry(wn);
+      }
       bool ok = tc::mbar_wait(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
-      ok = ok && tc::mbar_wait(p_empty, (g & 1) ^ 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
       const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * N + c0;
@@ -579,7 +651,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         }
         over = valid && top > kSlack;
       }
+      bool reload = HG > CH;  // v holds this tile's s - m
       if (tc::bar_or(1 + wg, 128, over || !ok)) {
+        // every product so far must be done before O is scaled
+        if (have && g > 0)
+          ok = ok && tc::mbar_wait(p_empty + (g - 1) % C::PB, ((g - 1) / C::PB) & 1, abort_flag,
+                                   a.status);
         if (tc::bar_or(1 + wg, 128, !ok)) break;
         // raise (or set) the references to this tile's column maxima
 #pragma unroll
@@ -601,42 +678,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         }
         tc::bar_sync(1 + wg, 128);
         if (have) {
-          // every product so far is done (p_empty): scale this warpgroup's columns of O
 #pragma unroll
           for (int u = 0; u < HG; ++u) l[u] *= f_s[c0 + u];
+          if (i > 0) {
 #pragma unroll 1
-          for (int blk = 0; blk < C::OBLK; ++blk) {
+            for (int blk = 0; blk < C::OBLK; ++blk) {
 #pragma unroll 1
-            for (int cc = 0; cc < HG; cc += 8) {
-              const uint32_t addr =
-                  tmem + lane_off + C::O_COL + ((qi & 1) * C::OBLK + blk) * NP + c0 + cc;
-              float o[8];
-              tmem_load(addr, o);
+              for (int cc = 0; cc < HG; cc += 8) {
+                const uint32_t addr =
+                    tmem + lane_off + C::O_COL + ((qi & 1) * C::OBLK + blk) * NP + c0 + cc;
+                float o[8];
+                tmem_load(addr, o);
 #pragma unroll
-              for (int u = 0; u < 8; ++u) o[u] *= f_s[c0 + cc + u];
-              tmem_store8(addr, o);
+                for (int u = 0; u < 8; ++u) o[u] *= f_s[c0 + cc + u];
+                tmem_store8(addr, o);
+              }
             }
+            tc::tmem_wait_st();
           }
-          tc::tmem_wait_st();
         }
         have = true;
+        reload = true;
       }
       // the weights of this row, rounded (or split) to bf16
       const bool all_valid = __all_sync(0xffffffffu, valid);
+      uint8_t* p_dst = pbuf + (g % C::PB) * C::PARTS * C::PBYTES;
 #pragma unroll
       for (int cc = 0; cc < HG; cc += CH) {
         if (have) {
-          tmem_load(s_addr + cc, v);
+          if (reload) {
+            tmem_load(s_addr + cc, v);
+#pragma unroll
+            for (int u = 0; u < CH; ++u) v[u] = __fmaf_rn(v[u], c, -m_s[c0 + cc + u]);
+          }
 #pragma unroll
           for (int u = 0; u < CH; ++u) {
-            const float x = __fmaf_rn(v[u], c, -m_s[c0 + cc + u]);
-            v[u] = ex2(all_valid || valid ? x : -INFINITY);
+            v[u] = ex2(all_valid || valid ? v[u] : -INFINITY);
             l[cc + u] += v[u];
             if (C::E4) v[u] *= vs;
           }
         } else {
 #pragma unroll
           for (int u = 0; u < CH; ++u) v[u] = 0.0f;
+        }
+        if (cc == 0) {
+          // the buffer's previous product
+          if (cc + CH >= HG) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
+          }
+          ok = tc::mbar_wait(p_empty + g % C::PB, ((g / C::PB) & 1) ^ 1, abort_flag, a.status);
+          // (a failed wait ends the warpgroup together at its next vote)
         }
 #pragma unroll
         for (int part = 0; part < C::PARTS; ++part) {
@@ -648,16 +741,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
               w[e] = pack_bf16(v[u + 2 * e], v[u + 2 * e + 1]);
               if (part + 1 < C::PARTS) take_bf16(w[e], v[u + 2 * e], v[u + 2 * e + 1]);
             }
-            *reinterpret_cast<uint4*>(pbuf + part * C::PBYTES + p_offset(row, c0 + cc + u)) =
+            *reinterpret_cast<uint4*>(p_dst + part * C::PBYTES + p_offset(row, c0 + cc + u)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
       tc::fence_before_sync();
       tc::fence_proxy_async_smem();
-      tc::mbar_arrive(p_full);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
+      if (lane == 0) {
+        if (HG > CH) tc::mbar_arrive(s_empty + (g & 1));
+        tc::mbar_arrive(p_full + g % C::PB);
+      }
       // the previous item's result, while this item's first product runs
       if (i == 0 && qi > 0 && ntile > 1 && !finish(qi - 1, pend_any)) break;
       if (i == ntile - 1) {
