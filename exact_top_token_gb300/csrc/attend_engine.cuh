@@ -83,20 +83,29 @@ struct Cfg {
   static_assert(NS * SLOT >= N * D * 4, "partial results of a split item");
 };
 
-// SW128 descriptor with both byte offsets.
-__device__ __forceinline__ uint64_t desc2(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 at a time: (a0, a1) * (b, b) + (c0, c1), and sums.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c0, float c1) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n"
+      " mov.b64 z, {%3, %4};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -210,8 +219,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   uint8_t* smem = tc::align1024(smem_dyn);
   uint8_t* ring = smem + C::RING_OFF;
   uint8_t* pbuf = smem + C::P_OFF;
-  float* m_s = reinterpret_cast<float*>(smem + C::MISC_OFF);  // [N] reference of each head (log2)
-  float* f_s = m_s + N;                                       // [N] factor of a raised reference
+  float* nm_s = reinterpret_cast<float*>(smem + C::MISC_OFF);  // [N] minus each head's reference
+  float* f_s = nm_s + N;                                       // [N] factor of a raised reference
   float* il_s = f_s + N;                                      // [N] 1 / sum (split: the sum)
   float* quad_s = il_s + N;                                   // [4][N]
   uint64_t* bars = reinterpret_cast<uint64_t*>(quad_s + 4 * N);
@@ -296,11 +305,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       w.hk = x.hk;
     }
   };
-  // selected row of entry j of query t, -1 if there is none
-  auto row_of = [&](int t, int j) -> int {
-    const int s = j < a.k_top ? __ldg(a.idx + (size_t)t * a.k_top + j) : -1;
-    return s >= a.L || s < 0 ? -1 : s;
+  // Index entry j of query t as stored (-1 past the list), and the row it selects
+  // (-1: none). Entries are loaded a tile or two ahead and only looked at when
+  // they are used: a test right after the load would wait for it.
+  auto entry_of = [&](int t, int j) -> int {
+    return j < a.k_top ? __ldg(a.idx + (size_t)t * a.k_top + j) : -1;
   };
+  auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
   if (warp >= kSoftmaxWarps && warp < C::MMA_WARP) {
     // ---------------- producers ----------------
@@ -341,17 +352,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       uint32_t phase = 1;
       bool ok = true;
       Walk w = walk_start(), wn = w;  // this tile; the next one
-      int s_next = total > 0 ? row_of(w.t, tile0 * 128 + tid) : -1;
+      int s_next = total > 0 ? entry_of(w.t, tile0 * 128 + tid) : -1;
       for (int g = 0; g < total && ok; ++g, w = wn) {
         if (w.i == 0 && !load_query(w.qi)) break;
         // every pass's row first, so that the copies go out back to back
+        const int s_own = row_of(s_next);
         int rows[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
-          rows[p] = __shfl_sync(0xffffffffu, s_next, p * RPP + (lane >> SHIFT));
+          rows[p] = __shfl_sync(0xffffffffu, s_own, p * RPP + (lane >> SHIFT));
         if (g + 1 < total) {
           walk_next(wn);
-          s_next = row_of(wn.t, (tile0 + wn.i) * 128 + tid);
+          s_next = entry_of(wn.t, (tile0 + wn.i) * 128 + tid);
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -431,15 +443,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         return true;
       };
       Walk w = walk_start(), wn = w;  // this tile; the next one
-      auto own = [&](const Walk& x) { return row_of(x.t, (tile0 + x.i) * 128 + tid); };
-      int s_own = total > 0 ? own(w) : -1, s_next = -1;
+      auto own = [&](const Walk& x) { return entry_of(x.t, (tile0 + x.i) * 128 + tid); };
+      int s_own = total > 0 ? row_of(own(w)) : -1, s_next = -1;
       if (total > 0) {
         issue(w.hk, s_own, 0, buf[0]);
         issue(w.hk, s_own, 1, buf[1]);
       }
       if (total > 1) {
         walk_next(wn);
-        s_next = own(wn);
+        s_next = row_of(own(wn));
+      }
+      // the entry of the tile after the next is in flight while a tile is stored
+      Walk wf = wn;
+      int e_far = -1;
+      if (total > 2) {
+        walk_next(wf);
+        e_far = own(wf);
       }
       bool ok = true;
       for (int g = 0; g < total && ok; ++g) {
@@ -454,10 +473,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           else if (g + 1 < total) issue(wn.hk, s_next, ch + 2 - NCH, buf[ch & 1]);
         }
         w = wn;
+        wn = wf;
         s_own = s_next;
-        if (g + 2 < total) {
-          walk_next(wn);
-          s_next = own(wn);
+        s_next = row_of(e_far);
+        if (g + 3 < total) {
+          walk_next(wf);
+          e_far = own(wf);
         }
       }
     }
@@ -468,10 +489,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // vector registers, which took 100 cycles per product.
     constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
     constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
-    const uint64_t ring_k = desc2(tc::smem_u32(ring), 16, 1024);
-    const uint64_t ring_v = desc2(tc::smem_u32(ring), 16384, 1024);
-    const uint64_t p_d = desc2(tc::smem_u32(pbuf), 16384, 1024);
-    const uint64_t q_d = desc2(tc::smem_u32(smem + C::Q_OFF), 16, 1024);
+    constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
+    // 14 address bits: in a cluster, shared addresses carry the CTA's rank above them
+    auto low = [](const void* p) { return (tc::smem_u32(p) >> 4) & 0x3FFFu; };
+    const uint32_t ring_lo = low(ring), p_lo = low(pbuf), q_lo = low(smem + C::Q_OFF);
+    constexpr uint32_t LBO_K = 1u << 16, LBO_MN = (16384u >> 4) << 16;
+    auto desc = [&](uint32_t lo) { return tc::desc_from_words(lo, D_HI); };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, a.status)) != 0;
     };
@@ -498,13 +521,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (!wait(s_empty + (g & 1), ((g >> 1) & 1) ^ 1)) return false;
       if (!C::E4) tc::fence_proxy_async_smem();
       tc::fence_after_sync();
-      const uint64_t ad = ring_k + (uint64_t)((ws.slot * C::SLOT) >> 4);
-      const uint64_t bd = q_d + (uint64_t)((qb * C::QBYTES) >> 4);
+      const uint32_t ad = (ring_lo + ws.slot * (C::SLOT >> 4)) | LBO_K;
+      const uint32_t bd = (q_lo + qb * (C::QBYTES >> 4)) | LBO_K;
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-          tc::mma<0>(tmem + C::S_COL + (g & 1) * N, ad + (Geo::step_offset(j, 128) >> 4),
-                     bd + (Geo::step_offset(j, N) >> 4), ID_S, j > 0 ? 1u : 0u);
+          tc::mma<0>(tmem + C::S_COL + (g & 1) * N, desc(ad + (Geo::step_offset(j, 128) >> 4)),
+                     desc(bd + (Geo::step_offset(j, N) >> 4)), ID_S, j > 0 ? 1u : 0u);
         tc::mma_commit(s_full + (g & 1));
         tc::mma_commit(empty + ws.slot);
         if (ws.i == ntile - 1) tc::mma_commit(q_empty + qb);
@@ -520,8 +543,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (!wait(p_full + pb, (g / C::PB) & 1)) return false;
       if (!C::E4) tc::fence_proxy_async_smem();
       tc::fence_after_sync();
-      const uint64_t ad = ring_v + (uint64_t)((wo.slot * C::SLOT) >> 4);
-      const uint64_t bd = p_d + (uint64_t)((pb * C::PARTS * C::PBYTES) >> 4);
+      const uint32_t ad = (ring_lo + wo.slot * (C::SLOT >> 4)) | LBO_MN;
+      const uint32_t bd = (p_lo + pb * (C::PARTS * C::PBYTES >> 4)) | LBO_MN;
       if (elect_one()) {
 #pragma unroll
         for (int blk = 0; blk < C::OBLK; ++blk) {
@@ -532,8 +555,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
               // d = 64 has one 64-column atom; the second one that M = 128 takes is
               // whatever follows the tile, and fills accumulator lanes never read
               tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * NP,
-                         ad + ((blk * 32768 + s * 2048) >> 4),
-                         bd + ((part * C::PBYTES + s * 2048) >> 4), ID_O,
+                         desc(ad + ((blk * 32768 + s * 2048) >> 4)),
+                         desc(bd + ((part * C::PBYTES + s * 2048) >> 4)), ID_O,
                          (wo.i > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
@@ -560,19 +583,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     const float c_scale = a.scale * kLog2e;
     float l[HG];
     bool have = false;  // some row of the item so far is valid (the same for the warpgroup)
-    int s_next = -1;
+    // this row's entry two tiles ahead as stored, its scales one tile ahead
+    int e_next = -1, e_far = -1;
     float ks_next = 1.0f, vs_next = 1.0f;
-    auto load_entry = [&](const Walk& w) {
-      const int j = (tile0 + w.i) * 128 + row;
-      int s = j < a.k_top ? __ldg(a.idx + (size_t)w.t * a.k_top + j) : -1;
-      if (s != -1 && (s < 0 || s >= a.L)) {
-        if (a.status && wg == 0) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-        s = -1;
-      }
-      s_next = s;
+    auto load_scales = [&](int e, int hk) {
       if (C::E4) {
-        ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + w.hk) : 1.0f;
-        vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + w.hk) : 1.0f;
+        const int s = row_of(e);
+        ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + hk) : 1.0f;
+        vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + hk) : 1.0f;
       }
     };
     // the item's result from O, once its last product is done
@@ -615,22 +633,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (lane == 0) tc::mbar_arrive(o_empty + ob);
       return true;
     };
-    Walk wn = walk_start();  // the next tile
-    if (total > 0) load_entry(wn);
+    Walk wf = walk_start();  // the tile whose entry is loaded: one ahead (e4m3: two)
+    int qi = 0, i = -1;
+    if (total > 0) {
+      e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+      load_scales(e_next, wf.hk);
+    }
+    int hk_far = 0;
+    if (C::E4 && total > 1) {
+      walk_next(wf);
+      e_far = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+      hk_far = wf.hk;
+    }
     bool pend_any = false;
     for (int g = 0; g < total; ++g) {
-      const int qi = wn.qi, i = wn.i;
+      if (++i == ntile) {
+        i = 0;
+        ++qi;
+      }
       if (i == 0) {
         have = false;
 #pragma unroll
         for (int u = 0; u < HG; ++u) l[u] = 0.0f;
       }
-      const bool valid = s_next >= 0;
+      const bool valid = row_of(e_next) >= 0;
+      if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
       const float c = valid ? c_scale * ks_next : 0.0f;
       const float vs = vs_next;
-      if (g + 1 < total) {
-        walk_next(wn);
-        load_entry(wn);
+      if (C::E4) {
+        e_next = e_far;
+        load_scales(e_next, hk_far);
+        if (g + 2 < total) {
+          walk_next(wf);
+          e_far = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+          hk_far = wf.hk;
+        }
+      } else if (g + 1 < total) {
+        walk_next(wf);
+        e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
       }
       bool ok = tc::mbar_wait(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -644,9 +684,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         for (int cc = 0; cc < HG; cc += CH) {
           tmem_load(s_addr + cc, v);
 #pragma unroll
-          for (int u = 0; u < CH; ++u) {
-            v[u] = __fmaf_rn(v[u], c, -m_s[c0 + cc + u]);
-            top = fmaxf(top, v[u]);
+          for (int u = 0; u < CH; u += 2) {
+            fma2(v[u], v[u + 1], c, nm_s[c0 + cc + u], nm_s[c0 + cc + u + 1]);
+            top = max3(top, v[u], v[u + 1]);
           }
         }
         over = valid && top > kSlack;
@@ -672,9 +712,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           const int col = c0 + h;
           const float top = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
                                   fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
-          const float m = have ? fmaxf(m_s[col], top) : top;
-          f_s[col] = have ? ex2(m_s[col] - m) : 1.0f;
-          m_s[col] = m;
+          const float m = have ? fmaxf(-nm_s[col], top) : top;
+          f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
+          nm_s[col] = -m;
         }
         tc::bar_sync(1 + wg, 128);
         if (have) {
@@ -709,13 +749,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           if (reload) {
             tmem_load(s_addr + cc, v);
 #pragma unroll
-            for (int u = 0; u < CH; ++u) v[u] = __fmaf_rn(v[u], c, -m_s[c0 + cc + u]);
+            for (int u = 0; u < CH; u += 2)
+              fma2(v[u], v[u + 1], c, nm_s[c0 + cc + u], nm_s[c0 + cc + u + 1]);
+          }
+          if (!all_valid) {
+#pragma unroll
+            for (int u = 0; u < CH; ++u) v[u] = valid ? v[u] : -INFINITY;
           }
 #pragma unroll
-          for (int u = 0; u < CH; ++u) {
-            v[u] = ex2(all_valid || valid ? v[u] : -INFINITY);
-            l[cc + u] += v[u];
-            if (C::E4) v[u] *= vs;
+          for (int u = 0; u < CH; u += 2) {
+            v[u] = ex2(v[u]);
+            v[u + 1] = ex2(v[u + 1]);
+            add2(l[cc + u], l[cc + u + 1], v[u], v[u + 1]);
+            if (C::E4) fma2(v[u], v[u + 1], vs, 0.0f, 0.0f);
           }
         } else {
 #pragma unroll
@@ -774,12 +820,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                                  : 0.0f;
           if (pl.splits > 1) {
             il_s[col] = sum;
-            if (!have) m_s[col] = -INFINITY;
+            if (!have) nm_s[col] = INFINITY;
           } else {
             il_s[col] = 1.0f / sum;
             if (a.lse && col < x.nh)
               a.lse[(size_t)x.t * Hq + x.h0 + col] =
-                  have ? (m_s[col] + log2f(sum)) * kLn2 : -INFINITY;
+                  have ? (log2f(sum) - nm_s[col]) * kLn2 : -INFINITY;
           }
         }
         tc::bar_sync(1 + wg, 128);
@@ -794,16 +840,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     cluster_sync();
     if (n_mine > 0 && !*abort_flag) {
       const Item x = item_of(0);
-      const uint32_t part_a = tc::smem_u32(ring), m_a = tc::smem_u32(m_s), l_a = tc::smem_u32(il_s);
+      const uint32_t part_a = tc::smem_u32(ring), m_a = tc::smem_u32(nm_s), l_a = tc::smem_u32(il_s);
       for (int f = threadIdx.x; f < x.nh * D; f += C::THREADS) {
         const int h = f / D, d = f - h * D;
         if (h % pl.splits != (int)rank) continue;
         float top = -INFINITY;
         for (int r = 0; r < pl.splits; ++r)
-          top = fmaxf(top, ld_cluster(map_cluster(m_a + h * 4, r)));
+          top = fmaxf(top, -ld_cluster(map_cluster(m_a + h * 4, r)));
         float sum = 0.0f, o = 0.0f;
         for (int r = 0; r < pl.splits; ++r) {
-          const float m = ld_cluster(map_cluster(m_a + h * 4, r));
+          const float m = -ld_cluster(map_cluster(m_a + h * 4, r));
           if (m == -INFINITY) continue;
           const float w = ex2(m - top);
           sum += w * ld_cluster(map_cluster(l_a + h * 4, r));
