@@ -25,9 +25,13 @@
 // three times; bf16 results use one part, whose rounding is of the size of the
 // result's own.
 //
-//   warps 0..7    softmax (warpgroup g: heads g N/2 ..), O read-out
-//   warps 8..11   producers (bf16: cp.async; e4m3: converted to bf16 on the way)
-//   warp 12       MMA issuer, TMEM
+//   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
+//                 columns), O read-out
+//   4 warps       producers (bf16: cp.async; e4m3: converted to bf16 on the way)
+//   last warp     MMA issuer, TMEM
+// A tile is a chain of short steps in different warps, so what counts is the
+// length of each step: no division, no wait for a load and little code per tile
+// (the roles share one instruction cache).
 //
 // Few items: a cluster of S CTAs shares an item, each taking a share of its
 // tiles; the partial O, m and sums are joined through distributed shared memory.
@@ -41,7 +45,6 @@
 namespace hytopk {
 namespace att {
 
-constexpr int kSoftmaxWarps = 8;
 constexpr float kSlack = 64.0f;  // largest s - m (log2) before m is raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -49,8 +52,9 @@ template <int D_, int N_, bool E4_, bool F32_>
 struct Cfg {
   static constexpr int D = D_, N = N_;
   static constexpr bool E4 = E4_, F32 = F32_;
-  static constexpr int HG = N / 2;             // heads of a softmax warpgroup
-  static constexpr int CH = HG < 32 ? HG : 32; // S columns held in registers at once
+  static constexpr int SWG = N >= 64 ? 4 : 2;     // softmax warpgroups
+  static constexpr int SWARPS = 4 * SWG;
+  static constexpr int HG = N / SWG;              // head columns of each: 8, 16 or 32
   static constexpr int PARTS = F32 ? 3 : 1;
   // columns of the second product: P rows are whole 128-byte atoms of 64 heads
   // (columns N.. of a narrower item are never read)
@@ -65,8 +69,8 @@ struct Cfg {
   // P buffers: two, unless their three parts or 128 heads leave no room for the ring
   static constexpr int PB = F32 || N > 64 ? 1 : 2;
   static constexpr int PWARPS = 4;
-  static constexpr int THREADS = (kSoftmaxWarps + PWARPS + 1) * 32;
-  static constexpr int MMA_WARP = kSoftmaxWarps + PWARPS;
+  static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
+  static constexpr int MMA_WARP = SWARPS + PWARPS;
   // m, scale factors, 1 / sum [N] each; per-quadrant sums or maxima [4][N]
   static constexpr int MISC = (3 + 4) * N * 4 + 512;
   static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + MISC + 1024;
@@ -118,6 +122,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ void take_bf16(uint32_t part, float& lo, float& hi) {
   lo -= __uint_as_float(part << 16);
   hi -= __uint_as_float(part & 0xFFFF0000u);
+}
+
+// Wait for a phase of `bar`; gives up (false, abort flag and status bit) when
+// another role has, or after kTries tests of at most 2 us each. The same as
+// tc::mbar_wait in a few instructions, since a tile passes a dozen of them.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         uint32_t* status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < kTries; ++i) {
+    if (tc::mbar_try_wait_suspend(bar, parity, tc::kSuspendHintNs)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  if (status) atomicOr(status, tc::kDevTimeout);
+  return false;
 }
 
 template <int W>
@@ -209,11 +230,13 @@ struct Plan {
   int heads;    // heads per block (the last may have fewer)
   int tiles;    // tiles of 128 rows per item
   int items;    // n * Hkv * blocks
+  int stride;   // items between a CTA's items, and the same as (t, hk, b) digits
+  int st, sh, sb;
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Plan pl) {
-  constexpr int D = C::D, N = C::N, HG = C::HG, CH = C::CH, NS = C::NS, NP = C::NP;
+  constexpr int D = C::D, N = C::N, HG = C::HG, NS = C::NS, NP = C::NP;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem = tc::align1024(smem_dyn);
@@ -237,7 +260,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // through a shuffle, so that the compiler knows the roles' branches are uniform
+  // and keeps the MMA issuer's state in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t rank = 0;
   if (pl.splits > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
@@ -249,10 +274,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       tc::mbar_init(q_full + i, C::PWARPS);
       tc::mbar_init(q_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
-      tc::mbar_init(s_empty + i, kSoftmaxWarps);
+      tc::mbar_init(s_empty + i, C::SWARPS);
       tc::mbar_init(o_full + i, 1);
-      tc::mbar_init(o_empty + i, kSoftmaxWarps);
-      tc::mbar_init(p_full + i, kSoftmaxWarps);
+      tc::mbar_init(o_empty + i, C::SWARPS);
+      tc::mbar_init(p_full + i, C::SWARPS);
       tc::mbar_init(p_empty + i, 1);
     }
     *abort_flag = 0;
@@ -265,46 +290,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   // items of this CTA: first, first + stride, ...; its tiles of each: [tile0, tile0 + ntile)
-  const int first = (int)(blockIdx.x / pl.splits), stride = (int)(gridDim.x / pl.splits);
-  const int n_mine = pl.items > first ? (pl.items - 1 - first) / stride + 1 : 0;
+  const int first = (int)blockIdx.x / pl.splits;
+  const int n_mine = pl.items > first ? (pl.items - 1 - first) / pl.stride + 1 : 0;
   const int tile0 = (int)((int64_t)pl.tiles * rank / pl.splits);
   const int ntile = (int)((int64_t)pl.tiles * (rank + 1) / pl.splits) - tile0;
   const int total = n_mine * ntile;
   const int Hq = a.Hkv * a.G;
 
-  struct Item {
-    int t, hk, h0, nh;  // query, cache head, first head, heads
-  };
-  auto item_of = [&](int i) -> Item {
-    const int it = first + i * stride;
-    const int b = it % pl.blocks, r = it / pl.blocks;
-    Item x;
-    x.hk = r % a.Hkv;
-    x.t = r / a.Hkv;
-    x.h0 = x.hk * a.G + b * pl.heads;
-    x.nh = min(pl.heads, a.G - b * pl.heads);
-    return x;
-  };
-  // A role's walk over its tiles in order: the item and tile of tile g, kept by
-  // steps (an item costs divisions; a tile must not).
+  // A role's walk over its tiles in order: item (query t, cache head hk, head
+  // block b) and tile i of it. Items advance by the stride's digits.
   struct Walk {
-    int qi, i, t, hk;  // item, tile within it, its query and cache head
+    int i, t, hk, b;
   };
-  auto walk_start = [&]() -> Walk {
-    const Item x = item_of(0);
-    return Walk{0, 0, x.t, x.hk};
-  };
+  Walk start;
+  start.i = 0;
+  start.b = first % pl.blocks;
+  start.hk = first / pl.blocks % a.Hkv;
+  start.t = first / pl.blocks / a.Hkv;
   auto walk_next = [&](Walk& w) {
     if (++w.i == ntile) {
       w.i = 0;
-      const Item x = item_of(++w.qi);
-      w.t = x.t;
-      w.hk = x.hk;
+      w.b += pl.sb;
+      w.hk += pl.sh;
+      w.t += pl.st;
+      if (w.b >= pl.blocks) {
+        w.b -= pl.blocks;
+        ++w.hk;
+      }
+      if (w.hk >= a.Hkv) {
+        w.hk -= a.Hkv;
+        ++w.t;
+      }
     }
   };
+  auto first_head = [&](const Walk& w) { return w.hk * a.G + w.b * pl.heads; };
+  auto head_count = [&](const Walk& w) { return min(pl.heads, a.G - w.b * pl.heads); };
   // Index entry j of query t as stored (-1 past the list), and the row it selects
   // (-1: none). Entries are loaded a tile or two ahead and only looked at when
   // they are used: a test right after the load would wait for it.
@@ -313,10 +336,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   };
   auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
-  if (warp >= kSoftmaxWarps && warp < C::MMA_WARP) {
+  if (warp >= C::SWARPS && warp < C::MMA_WARP) {
     // ---------------- producers ----------------
-    const int tid = threadIdx.x - kSoftmaxWarps * 32;
-    const int pw = warp - kSoftmaxWarps;
+    const int tid = threadIdx.x - C::SWARPS * 32;
+    const int pw = warp - C::SWARPS;
     // this warp's writes to a buffer are done: one arrival per warp
     auto publish = [&](uint64_t* bar) {
       tc::fence_proxy_async_smem();
@@ -324,20 +347,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (lane == 0) tc::mbar_arrive(bar);
     };
     // the item's query rows, zero beyond its heads
-    auto load_query = [&](int qi) -> bool {
+    auto load_query = [&](int qi, const Walk& w) -> bool {
       const int qb = qi % C::QB;
-      const bool ok = tc::mbar_wait(q_empty + qb, ((qi / C::QB) & 1) ^ 1, abort_flag, a.status);
+      const bool ok = wait_bar(q_empty + qb, ((qi / C::QB) & 1) ^ 1, abort_flag, a.status);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      const Item x = item_of(qi);
       const uint8_t* src = static_cast<const uint8_t*>(a.q) +
-                           ((size_t)x.t * a.q_row + (size_t)x.h0 * D) * 2;
+                           ((size_t)w.t * a.q_row + (size_t)first_head(w) * D) * 2;
+      const int nh = head_count(w);
       uint8_t* dst = smem + C::Q_OFF + qb * C::QBYTES;
       constexpr int CPR = C::RB / 16;
-      for (int f = tid; f < N * CPR; f += C::PWARPS * 32) {
-        const int r = f / CPR, c = f % CPR;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < x.nh) v = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * C::RB) + c);
-        *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v;
+      constexpr int PER = N * CPR / (C::PWARPS * 32);  // chunks a thread copies
+      constexpr int U = PER < 4 ? PER : 4;
+#pragma unroll 1
+      for (int p = 0; p < PER; p += U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int f = (p + u) * C::PWARPS * 32 + tid;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (f / CPR < nh) v[u] = __ldg(reinterpret_cast<const uint4*>(src) + f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int f = (p + u) * C::PWARPS * 32 + tid;
+          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(f / CPR, f % CPR, N)) = v[u];
+        }
       }
       publish(q_full + qb);
       return true;
@@ -351,10 +385,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       int slot = 0;
       uint32_t phase = 1;
       bool ok = true;
-      Walk w = walk_start(), wn = w;  // this tile; the next one
+      Walk w = start, wn = w;  // this tile; the next one
+      int qi = 0;
       int s_next = total > 0 ? entry_of(w.t, tile0 * 128 + tid) : -1;
       for (int g = 0; g < total && ok; ++g, w = wn) {
-        if (w.i == 0 && !load_query(w.qi)) break;
+        if (w.i == 0 && !load_query(qi++, w)) break;
         // every pass's row first, so that the copies go out back to back
         const int s_own = row_of(s_next);
         int rows[PASSES];
@@ -365,9 +400,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           walk_next(wn);
           s_next = entry_of(wn.t, (tile0 + wn.i) * 128 + tid);
         }
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(empty + slot, phase, abort_flag, a.status));
+          ok = __all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status));
           if (!ok) break;
           const uint32_t dst = tc::smem_u32(ring + slot * C::SLOT);
           const int c = lane & ((1 << SHIFT) - 1);
@@ -421,7 +456,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       uint32_t phase = 1;
       auto store = [&](int ch, const uint4 (&v)[CP]) -> bool {
         if (ch % (NCH / 2) == 0 &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(empty + slot, phase, abort_flag, a.status)))
+            !__all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status)))
           return false;
         uint8_t* dst = ring + slot * C::SLOT;
         const int p0 = (ch % (NCH / 2)) * CP;
@@ -442,7 +477,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         }
         return true;
       };
-      Walk w = walk_start(), wn = w;  // this tile; the next one
+      Walk w = start, wn = w;  // this tile; the next one
+      int qi = 0;
       auto own = [&](const Walk& x) { return entry_of(x.t, (tile0 + x.i) * 128 + tid); };
       int s_own = total > 0 ? row_of(own(w)) : -1, s_next = -1;
       if (total > 0) {
@@ -462,7 +498,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       }
       bool ok = true;
       for (int g = 0; g < total && ok; ++g) {
-        if (w.i == 0 && !load_query(w.qi)) break;
+        if (w.i == 0 && !load_query(qi++, w)) break;
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           if (!store(ch, buf[ch & 1])) {
@@ -496,7 +532,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     constexpr uint32_t LBO_K = 1u << 16, LBO_MN = (16384u >> 4) << 16;
     auto desc = [&](uint32_t lo) { return tc::desc_from_words(lo, D_HI); };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, a.status)) != 0;
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
     };
     struct At {
       int i, qi, slot;  // tile of its item, item, ring slot
@@ -574,294 +610,260 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         if (!weighted(g)) break;
       }
     }
-  } else if (warp < kSoftmaxWarps) {
+  } else if (warp < C::SWARPS) {
     // ---------------- softmax: TMEM lane = selected row ----------------
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const int c0 = wg * HG;  // first head column of this warpgroup
+    const int bar = 1 + wg;
     const float c_scale = a.scale * kLog2e;
-    float l[HG];
+    constexpr int LPC = 32 / HG;  // lanes that share a column after reduce_columns
+    float l[HG], v[HG];
     bool have = false;  // some row of the item so far is valid (the same for the warpgroup)
-    // this row's entry two tiles ahead as stored, its scales one tile ahead
-    int e_next = -1, e_far = -1;
+    // this row's entry as stored: of the next tile (e4m3: and of the one after,
+    // since the scales of the next tile's row are loaded a tile ahead too)
+    int e_next = -1, e_far = -1, hk_far = 0;
     float ks_next = 1.0f, vs_next = 1.0f;
     auto load_scales = [&](int e, int hk) {
-      if (C::E4) {
-        const int s = row_of(e);
-        ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + hk) : 1.0f;
-        vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + hk) : 1.0f;
-      }
+      const int s = row_of(e);
+      ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + hk) : 1.0f;
+      vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + hk) : 1.0f;
     };
-    // the item's result from O, once its last product is done
-    auto finish = [&](int qi, bool any) -> bool {
-      const Item x = item_of(qi);
-      const int ob = qi & 1;
-      const bool ok = tc::mbar_wait(o_full + ob, (qi >> 1) & 1, abort_flag, a.status);
-      if (tc::bar_or(1 + wg, 128, !ok)) return false;
-      tc::fence_after_sync();
-#pragma unroll
-      for (int blk = 0; blk < C::OBLK; ++blk) {
-        const int d = blk * 128 + row;
-        if (blk * 128 + quad * 32 >= D) continue;
-#pragma unroll
-        for (int cc = 0; cc < HG; cc += CH) {
-          if (c0 + cc >= x.nh) continue;
-          float v[CH];
-          tmem_load(tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * NP + c0 + cc, v);
-          if (pl.splits > 1) {
-            // partial results for the cluster: [head][d] in the ring, which is idle now
-            float* part = reinterpret_cast<float*>(ring);
-#pragma unroll
-            for (int u = 0; u < CH; ++u)
-              if (c0 + cc + u < x.nh) part[(c0 + cc + u) * D + d] = any ? v[u] : 0.0f;
-          } else {
-            const size_t at = ((size_t)x.t * Hq + x.h0 + c0 + cc) * D + d;
-#pragma unroll
-            for (int u = 0; u < CH; ++u) {
-              if (c0 + cc + u < x.nh) {
-                const float o = any ? v[u] * il_s[c0 + cc + u] : 0.0f;
-                if constexpr (C::F32) static_cast<float*>(a.out)[at + (size_t)u * D] = o;
-                else static_cast<__nv_bfloat16*>(a.out)[at + (size_t)u * D] = __float2bfloat16_rn(o);
-              }
-            }
-          }
-        }
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(o_empty + ob);
-      return true;
-    };
-    Walk wf = walk_start();  // the tile whose entry is loaded: one ahead (e4m3: two)
-    int qi = 0, i = -1;
+    Walk wf = start;  // the tile whose entry was loaded last
     if (total > 0) {
       e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
-      load_scales(e_next, wf.hk);
+      if (C::E4) load_scales(e_next, wf.hk);
     }
-    int hk_far = 0;
     if (C::E4 && total > 1) {
       walk_next(wf);
       e_far = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
       hk_far = wf.hk;
     }
-    bool pend_any = false;
-    for (int g = 0; g < total; ++g) {
-      if (++i == ntile) {
-        i = 0;
-        ++qi;
-      }
-      if (i == 0) {
-        have = false;
+    Walk w = start;
+    int qi = 0;
+    // the item before, whose result is still to be read from O
+    bool pend = false, pend_any = false;
+    int pend_nh = 0;
+    size_t pend_at = 0;
+#pragma unroll 1
+    for (int g = 0; g <= total; ++g) {
+      if (g < total) {
+        if (w.i == 0) {
+          have = false;
 #pragma unroll
-        for (int u = 0; u < HG; ++u) l[u] = 0.0f;
-      }
-      const bool valid = row_of(e_next) >= 0;
-      if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-      const float c = valid ? c_scale * ks_next : 0.0f;
-      const float vs = vs_next;
-      if (C::E4) {
-        e_next = e_far;
-        load_scales(e_next, hk_far);
-        if (g + 2 < total) {
+          for (int u = 0; u < HG; ++u) l[u] = 0.0f;
+        }
+        const bool valid = row_of(e_next) >= 0;
+        if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+        const float c = valid ? c_scale * ks_next : 0.0f;
+        const float vs = vs_next;
+        if (C::E4) {
+          e_next = e_far;
+          load_scales(e_next, hk_far);
+        }
+        if (g + (C::E4 ? 2 : 1) < total) {
           walk_next(wf);
-          e_far = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+          const int e = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+          (C::E4 ? e_far : e_next) = e;
           hk_far = wf.hk;
         }
-      } else if (g + 1 < total) {
-        walk_next(wf);
-        e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
-      }
-      bool ok = tc::mbar_wait(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
-      const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * N + c0;
-      float v[CH];
-      bool over = !have && valid;
-      if (have) {
-        float top = -INFINITY;
+        bool ok = wait_bar(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        tc::fence_after_sync();
+        const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * N + c0;
+        tmem_load(s_addr, v);
+        bool over = !have && valid;
+        if (have) {
+          float top = -INFINITY;
 #pragma unroll
-        for (int cc = 0; cc < HG; cc += CH) {
-          tmem_load(s_addr + cc, v);
-#pragma unroll
-          for (int u = 0; u < CH; u += 2) {
-            fma2(v[u], v[u + 1], c, nm_s[c0 + cc + u], nm_s[c0 + cc + u + 1]);
+          for (int u = 0; u < HG; u += 2) {
+            fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
             top = max3(top, v[u], v[u + 1]);
           }
+          over = valid && top > kSlack;
         }
-        over = valid && top > kSlack;
-      }
-      bool reload = HG > CH;  // v holds this tile's s - m
-      if (tc::bar_or(1 + wg, 128, over || !ok)) {
-        // every product so far must be done before O is scaled
-        if (have && g > 0)
-          ok = ok && tc::mbar_wait(p_empty + (g - 1) % C::PB, ((g - 1) / C::PB) & 1, abort_flag,
-                                   a.status);
-        if (tc::bar_or(1 + wg, 128, !ok)) break;
-        // raise (or set) the references to this tile's column maxima
+        if (tc::bar_or(bar, 128, over || !ok)) {
+          // every product so far must be done before O is scaled
+          if (have && g > 0)
+            ok = ok && wait_bar(p_empty + (g - 1) % C::PB, ((g - 1) / C::PB) & 1, abort_flag,
+                                a.status);
+          if (tc::bar_or(bar, 128, !ok)) break;
+          // raise (or set) the references to this tile's column maxima
+          tmem_load(s_addr, v);
 #pragma unroll
-        for (int cc = 0; cc < HG; cc += CH) {
-          tmem_load(s_addr + cc, v);
+          for (int u = 0; u < HG; ++u) v[u] = valid ? v[u] * c : -INFINITY;
+          const float top = reduce_columns<HG, true>(v, lane);
+          if (lane % LPC == 0) quad_s[quad * N + c0 + lane / LPC] = top;
+          tc::bar_sync(bar, 128);
+          if (row < HG) {
+            const int col = c0 + row;
+            const float high = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
+                                     fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
+            const float m = have ? fmaxf(-nm_s[col], high) : high;
+            f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
+            nm_s[col] = -m;
+          }
+          tc::bar_sync(bar, 128);
+          if (have) {
 #pragma unroll
-          for (int u = 0; u < CH; ++u) v[u] = valid ? v[u] * c : -INFINITY;
-          const float top = reduce_columns<CH, true>(v, lane);
-          if (lane % (32 / CH) == 0) quad_s[quad * N + c0 + cc + lane / (32 / CH)] = top;
-        }
-        tc::bar_sync(1 + wg, 128);
-        for (int h = row; h < HG; h += 128) {
-          const int col = c0 + h;
-          const float top = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
-                                  fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
-          const float m = have ? fmaxf(-nm_s[col], top) : top;
-          f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
-          nm_s[col] = -m;
-        }
-        tc::bar_sync(1 + wg, 128);
-        if (have) {
-#pragma unroll
-          for (int u = 0; u < HG; ++u) l[u] *= f_s[c0 + u];
-          if (i > 0) {
+            for (int u = 0; u < HG; ++u) l[u] *= f_s[c0 + u];
+            if (w.i > 0) {
 #pragma unroll 1
-            for (int blk = 0; blk < C::OBLK; ++blk) {
-#pragma unroll 1
-              for (int cc = 0; cc < HG; cc += 8) {
+              for (int cc = 0; cc < C::OBLK * HG; cc += 8) {
+                const int blk = cc / HG, h = c0 + cc % HG;
                 const uint32_t addr =
-                    tmem + lane_off + C::O_COL + ((qi & 1) * C::OBLK + blk) * NP + c0 + cc;
+                    tmem + lane_off + C::O_COL + ((qi & 1) * C::OBLK + blk) * NP + h;
                 float o[8];
                 tmem_load(addr, o);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) o[u] *= f_s[c0 + cc + u];
+                for (int u = 0; u < 8; ++u) o[u] *= f_s[h + u];
                 tmem_store8(addr, o);
               }
+              tc::tmem_wait_st();
             }
-            tc::tmem_wait_st();
           }
+          have = true;
+          tmem_load(s_addr, v);
+#pragma unroll
+          for (int u = 0; u < HG; u += 2)
+            fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
         }
-        have = true;
-        reload = true;
-      }
-      // the weights of this row, rounded (or split) to bf16
-      const bool all_valid = __all_sync(0xffffffffu, valid);
-      uint8_t* p_dst = pbuf + (g % C::PB) * C::PARTS * C::PBYTES;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
+        // the weights of this row, rounded (or split) to bf16
+        const bool off = !valid || !have;
+        if (__any_sync(0xffffffffu, off)) {
 #pragma unroll
-      for (int cc = 0; cc < HG; cc += CH) {
-        if (have) {
-          if (reload) {
-            tmem_load(s_addr + cc, v);
-#pragma unroll
-            for (int u = 0; u < CH; u += 2)
-              fma2(v[u], v[u + 1], c, nm_s[c0 + cc + u], nm_s[c0 + cc + u + 1]);
-          }
-          if (!all_valid) {
-#pragma unroll
-            for (int u = 0; u < CH; ++u) v[u] = valid ? v[u] : -INFINITY;
-          }
-#pragma unroll
-          for (int u = 0; u < CH; u += 2) {
-            v[u] = ex2(v[u]);
-            v[u + 1] = ex2(v[u + 1]);
-            add2(l[cc + u], l[cc + u + 1], v[u], v[u + 1]);
-            if (C::E4) fma2(v[u], v[u + 1], vs, 0.0f, 0.0f);
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < CH; ++u) v[u] = 0.0f;
+          for (int u = 0; u < HG; ++u) v[u] = off ? -INFINITY : v[u];
         }
-        if (cc == 0) {
-          // the buffer's previous product
-          if (cc + CH >= HG) {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
-          }
-          ok = tc::mbar_wait(p_empty + g % C::PB, ((g / C::PB) & 1) ^ 1, abort_flag, a.status);
-          // (a failed wait ends the warpgroup together at its next vote)
+#pragma unroll
+        for (int u = 0; u < HG; u += 2) {
+          v[u] = ex2(v[u]);
+          v[u + 1] = ex2(v[u + 1]);
+          add2(l[u], l[u + 1], v[u], v[u + 1]);
+          if (C::E4) fma2(v[u], v[u + 1], vs, 0.0f, 0.0f);
         }
+        // the buffer's previous product (a failed wait ends the warpgroup together
+        // at its next vote)
+        wait_bar(p_empty + g % C::PB, ((g / C::PB) & 1) ^ 1, abort_flag, a.status);
+        uint8_t* p_dst = pbuf + (g % C::PB) * C::PARTS * C::PBYTES;
 #pragma unroll
         for (int part = 0; part < C::PARTS; ++part) {
 #pragma unroll
-          for (int u = 0; u < CH; u += 8) {
-            uint32_t w[4];
+          for (int u = 0; u < HG; u += 8) {
+            uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              w[e] = pack_bf16(v[u + 2 * e], v[u + 2 * e + 1]);
-              if (part + 1 < C::PARTS) take_bf16(w[e], v[u + 2 * e], v[u + 2 * e + 1]);
+              x[e] = pack_bf16(v[u + 2 * e], v[u + 2 * e + 1]);
+              if (part + 1 < C::PARTS) take_bf16(x[e], v[u + 2 * e], v[u + 2 * e + 1]);
             }
-            *reinterpret_cast<uint4*>(p_dst + part * C::PBYTES + p_offset(row, c0 + cc + u)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p_dst + part * C::PBYTES + p_offset(row, c0 + u)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
-      }
-      tc::fence_before_sync();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (HG > CH) tc::mbar_arrive(s_empty + (g & 1));
-        tc::mbar_arrive(p_full + g % C::PB);
+        tc::fence_before_sync();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + g % C::PB);
       }
       // the previous item's result, while this item's first product runs
-      if (i == 0 && qi > 0 && ntile > 1 && !finish(qi - 1, pend_any)) break;
-      if (i == ntile - 1) {
-        // sums over the rows: lanes, then quadrants
-        if (ntile == 1 && qi > 0 && !finish(qi - 1, pend_any)) break;
-        const Item x = item_of(qi);
+      if (pend) {
+        const int ob = (qi & 1) ^ 1;
+        const bool ok = wait_bar(o_full + ob, ((qi - 1) >> 1) & 1, abort_flag, a.status);
+        if (tc::bar_or(bar, 128, !ok)) break;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int blk = 0; blk < C::OBLK; ++blk) {
+          const int d = blk * 128 + row;
+          if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
+          tmem_load(tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * NP + c0, v);
+          // a split item's part stays unnormalised: [head][d] in the ring, idle by now
+          float* part = reinterpret_cast<float*>(ring) + c0 * D + d;
 #pragma unroll
-        for (int cc = 0; cc < HG; cc += CH) {
-#pragma unroll
-          for (int u = 0; u < CH; ++u) v[u] = l[cc + u];
-          const float sum = reduce_columns<CH, false>(v, lane);
-          if (lane % (32 / CH) == 0) quad_s[quad * N + c0 + cc + lane / (32 / CH)] = sum;
-        }
-        tc::bar_sync(1 + wg, 128);
-        for (int h = row; h < HG; h += 128) {
-          const int col = c0 + h;
-          const float sum = have ? (quad_s[col] + quad_s[N + col]) +
-                                       (quad_s[2 * N + col] + quad_s[3 * N + col])
-                                 : 0.0f;
-          if (pl.splits > 1) {
-            il_s[col] = sum;
-            if (!have) nm_s[col] = INFINITY;
-          } else {
-            il_s[col] = 1.0f / sum;
-            if (a.lse && col < x.nh)
-              a.lse[(size_t)x.t * Hq + x.h0 + col] =
-                  have ? (log2f(sum) - nm_s[col]) * kLn2 : -INFINITY;
+          for (int u = 0; u < HG; ++u) {
+            if (c0 + u < pend_nh) {
+              const size_t at = pend_at + (size_t)(c0 + u) * D + d;
+              if (pl.splits > 1) {
+                part[u * D] = pend_any ? v[u] : 0.0f;
+              } else {
+                const float o = pend_any ? v[u] * il_s[c0 + u] : 0.0f;
+                if constexpr (C::F32) static_cast<float*>(a.out)[at] = o;
+                else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
+              }
+            }
           }
         }
-        tc::bar_sync(1 + wg, 128);
-        pend_any = have;
-        if (qi == n_mine - 1 && !finish(qi, have)) break;
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(o_empty + ob);
+        pend = false;
       }
+      if (g < total && w.i == ntile - 1) {
+        // the item's sums over its rows: lanes, then quadrants
+#pragma unroll
+        for (int u = 0; u < HG; ++u) v[u] = l[u];
+        const float sum = reduce_columns<HG, false>(v, lane);
+        if (lane % LPC == 0) quad_s[quad * N + c0 + lane / LPC] = sum;
+        tc::bar_sync(bar, 128);
+        const int h0 = first_head(w), nh = head_count(w);
+        if (row < HG) {
+          const int col = c0 + row;
+          const float z = have ? (quad_s[col] + quad_s[N + col]) +
+                                     (quad_s[2 * N + col] + quad_s[3 * N + col])
+                               : 0.0f;
+          if (pl.splits > 1) {
+            il_s[col] = z;
+            if (!have) nm_s[col] = INFINITY;
+          } else {
+            il_s[col] = 1.0f / z;
+            if (a.lse && col < nh)
+              a.lse[(size_t)w.t * Hq + h0 + col] =
+                  have ? (log2f(z) - nm_s[col]) * kLn2 : -INFINITY;
+          }
+        }
+        tc::bar_sync(bar, 128);
+        pend = true;
+        pend_any = have;
+        pend_nh = nh;
+        pend_at = ((size_t)w.t * Hq + h0) * D;
+        ++qi;
+      }
+      walk_next(w);
     }
   }
   if (pl.splits > 1) {
     // join the cluster's parts: rank r takes heads r, r + splits, ... of the one item
     __syncwarp();
     cluster_sync();
-    if (n_mine > 0 && !*abort_flag) {
-      const Item x = item_of(0);
+    if (!*abort_flag) {
+      const int h0 = first_head(start), nh = head_count(start);
       const uint32_t part_a = tc::smem_u32(ring), m_a = tc::smem_u32(nm_s), l_a = tc::smem_u32(il_s);
-      for (int f = threadIdx.x; f < x.nh * D; f += C::THREADS) {
-        const int h = f / D, d = f - h * D;
+#pragma unroll 1
+      for (int f = threadIdx.x; f < nh * D; f += C::THREADS) {
+        const int h = f / D, d = f % D;
         if (h % pl.splits != (int)rank) continue;
         float top = -INFINITY;
+#pragma unroll 1
         for (int r = 0; r < pl.splits; ++r)
           top = fmaxf(top, -ld_cluster(map_cluster(m_a + h * 4, r)));
         float sum = 0.0f, o = 0.0f;
+#pragma unroll 1
         for (int r = 0; r < pl.splits; ++r) {
           const float m = -ld_cluster(map_cluster(m_a + h * 4, r));
           if (m == -INFINITY) continue;
-          const float w = ex2(m - top);
-          sum += w * ld_cluster(map_cluster(l_a + h * 4, r));
-          o += w * ld_cluster(map_cluster(part_a + (h * D + d) * 4, r));
+          const float x = ex2(m - top);
+          sum += x * ld_cluster(map_cluster(l_a + h * 4, r));
+          o += x * ld_cluster(map_cluster(part_a + f * 4, r));
         }
         const bool any = top != -INFINITY;
         o = any ? o / sum : 0.0f;
-        const size_t at = ((size_t)x.t * Hq + x.h0 + h) * D + d;
+        const size_t at = ((size_t)start.t * Hq + h0) * D + f;
         if constexpr (C::F32) static_cast<float*>(a.out)[at] = o;
         else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
         if (d == 0 && a.lse)
-          a.lse[(size_t)x.t * Hq + x.h0 + h] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+          a.lse[(size_t)start.t * Hq + h0 + h] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
       }
     }
     cluster_sync();
@@ -890,8 +892,13 @@ cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   while (pl.splits < 8 && 2 * pl.splits <= pl.tiles &&
          (int64_t)pl.items * 2 * pl.splits <= sms)
     pl.splits *= 2;
+  const int ctas = pl.items < sms ? pl.items : sms;
+  pl.stride = pl.splits > 1 ? pl.items : ctas;
+  pl.sb = pl.stride % pl.blocks;
+  pl.sh = pl.stride / pl.blocks % a.Hkv;
+  pl.st = pl.stride / pl.blocks / a.Hkv;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(pl.splits > 1 ? pl.items * pl.splits : (pl.items < sms ? pl.items : sms)));
+  cfg.gridDim = dim3((unsigned)(pl.splits > 1 ? pl.items * pl.splits : ctas));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
