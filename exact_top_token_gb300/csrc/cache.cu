@@ -28,7 +28,9 @@ struct RowArgs {
 __device__ __forceinline__ float load_elem(const float* p) { return *p; }
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// One (row, head) per warp: values in shared memory, then rotated, then stored.
+// ---- any d: one (row, head) per warp, its values in shared memory -----------------
+// Kept for head widths other than 64, 128 and 256 (the kernels below need a
+// power of two of 16-byte chunks in a row).
 constexpr int kWarps = 4;
 
 template <typename T>
@@ -107,6 +109,226 @@ __global__ void __launch_bounds__(32 * kWarps) k_cache_write(const RowArgs a) {
   }
 }
 
+// ---- d = 64, 128, 256: a row in d / 8 lanes ---------------------------------------
+// Lane j of a row's group holds columns 8j .. 8j + 7. Bound by memory: a row is
+// read once and written once. What is computed per token, cos and sin of its
+// rot / 2 angles, is shared by all the rows of a block through shared memory,
+// and computed while the rows' loads are in flight; the other half of a pair of
+// the half layout comes from its lane by shuffles.
+constexpr int kFastThreads = 256;
+constexpr int kIter = 4;  // rows per group: 4 x 16 bytes (bf16) in flight per thread
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, uint32_t (&raw)[sizeof(T) * 2]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w;
+  if constexpr (sizeof(T) == 4) {
+    const uint4 b = *(reinterpret_cast<const uint4*>(p) + 1);
+    raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
+  }
+}
+template <int W>
+__device__ __forceinline__ void unpack8(const uint32_t (&raw)[W], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if constexpr (W == 8) {
+      v[i] = __uint_as_float(raw[i]);
+    } else {
+      v[2 * i] = __uint_as_float(raw[i] << 16);
+      v[2 * i + 1] = __uint_as_float(raw[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]),
+                                              bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+  }
+}
+// two values as e4m3 codes, round to nearest even, saturating
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// MODE 0: rotated rows; 1: into bf16 cache rows; 2: into e4m3 cache rows
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
+  constexpr int GL = D / 8, GROUPS = kFastThreads / GL, W = sizeof(T) * 2;
+  extern __shared__ float4 table4[];
+  float* table = reinterpret_cast<float*>(table4);  // [tokens][cos rot/2 | sin rot/2]
+  const int j = threadIdx.x % GL, group = threadIdx.x / GL;
+  const int64_t rows = (int64_t)a.n * a.H;
+  const int64_t row0 = (int64_t)blockIdx.x * (GROUPS * kIter);
+  // Rows are (t, h) in order; a group's are GROUPS apart.
+  int64_t row = row0 + group;
+  const int dt = GROUPS / a.H, dh = GROUPS - dt * a.H;
+  int t = (int)(row / a.H), h = (int)(row - (int64_t)t * a.H);
+  const int t0 = (int)(row0 / a.H);
+  uint32_t raw[kIter][W];
+  int ts[kIter], hs[kIter], slot[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    ts[i] = t;
+    hs[i] = h;
+    slot[i] = -1;
+    if (row < rows) {
+      slot[i] = t;
+      if (MODE != 0 && a.slots) slot[i] = __ldg(a.slots + t);
+      load8(static_cast<const T*>(a.x) + (size_t)t * a.x_row + (size_t)h * a.x_head + j * 8,
+            raw[i]);
+    }
+    row += GROUPS;
+    t += dt;
+    h += dh;
+    if (h >= a.H) {
+      h -= a.H;
+      ++t;
+    }
+  }
+  const int half = a.rot / 2;
+  if (a.positions) {
+    const int64_t last = min(row0 + GROUPS * kIter, rows) - 1;
+    const int tokens = (int)(last / a.H) - t0 + 1;
+    for (int f = threadIdx.x; f < tokens * half; f += kFastThreads) {
+      const int k = f / half, i = f - k * half;
+      const int pos = __ldg(a.positions + t0 + k);
+      const bool bad = pos < 0 || pos >= kMaxPosition;
+      float c, s;
+      rope_turn((float)pos, __ldg(a.inv_freq + i), c, s);
+      if (bad) {
+        c = s = __int_as_float(0x7fc00000);
+        if (a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+      }
+      table[k * a.rot + i] = c * a.mscale;
+      table[k * a.rot + half + i] = a.inverse ? -(s * a.mscale) : s * a.mscale;
+    }
+    __syncthreads();
+  }
+  const int col = j * 8 - a.first;  // within the rotated part if 0 <= col < rot
+  const bool turned = a.positions && col >= 0 && col < a.rot;
+  const bool upper = col >= half;   // half layout: the second of each pair
+  const int peer = (threadIdx.x & 31) + (upper ? -half / 8 : half / 8);
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    float v[8];
+    unpack8<W>(raw[i], v);
+    if (a.positions) {
+      // rows past the end (a group of the last block) take any token's angles
+      const float* tab = table + (size_t)(min(ts[i], a.n - 1) - t0) * a.rot;
+      if (a.interleaved) {
+        if (turned) {
+          const float4 c = *reinterpret_cast<const float4*>(tab + col / 2);
+          const float4 s = *reinterpret_cast<const float4*>(tab + half + col / 2);
+          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x1 = v[2 * e], x2 = v[2 * e + 1];
+            v[2 * e] = x1 * cs[e] - x2 * sn[e];
+            v[2 * e + 1] = x1 * sn[e] + x2 * cs[e];
+          }
+        }
+      } else {
+        uint32_t other[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) other[e] = __shfl_sync(0xffffffffu, raw[i][e], peer & 31);
+        if (turned) {
+          float o[8];
+          unpack8<W>(other, o);
+          const int at = upper ? col - half : col;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 c = *reinterpret_cast<const float4*>(tab + at + 4 * q);
+            const float4 s = *reinterpret_cast<const float4*>(tab + half + at + 4 * q);
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = v[4 * q + e], y = o[4 * q + e];
+              v[4 * q + e] = upper ? y * sn[e] + x * cs[e] : x * cs[e] - y * sn[e];
+            }
+          }
+        }
+      }
+    }
+    const int64_t r = row0 + group + (int64_t)i * GROUPS;
+    if constexpr (MODE == 0) {
+      if (r < rows)
+        store8(static_cast<T*>(a.out) + (size_t)ts[i] * a.out_row + (size_t)hs[i] * a.out_head +
+                   j * 8, v);
+    } else {
+      const bool in = r < rows && slot[i] >= 0 && slot[i] < a.L;
+      if (r < rows && !in && slot[i] != -1 && j == 0 && a.status)
+        atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+      const size_t at = in ? ((size_t)slot[i] * a.H + hs[i]) * D + j * 8 : 0;
+      if constexpr (MODE == 1) {
+        if (in) store8(static_cast<__nv_bfloat16*>(a.out) + at, v);
+      } else {
+        constexpr float kMost = 3.402823466e38f;
+        float amax = 0.0f;
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float m = fabsf(v[e]);
+          odd |= !(m <= kMost);
+          amax = fmaxf(amax, m <= kMost ? m : 0.0f);
+        }
+#pragma unroll
+        for (int o = GL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float scale = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f) : 1.0f;
+        // x / scale correctly rounded from the rounded reciprocal: one product, its
+        // exact remainder, one correction (Markstein, "Computation of elementary
+        // functions on the IBM RISC System/6000", 1990); a remainder that could
+        // underflow takes the divide
+        const float inv = __frcp_rn(scale);
+        if (scale > 1e-20f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float q = v[e] * inv;
+            // (the correction loses the sign of a negative zero)
+            const float c = copysignf(__fmaf_rn(__fmaf_rn(-q, scale, v[e]), inv, q), v[e]);
+            v[e] = odd ? (fabsf(v[e]) <= kMost ? c : __int_as_float(0x7fc00000)) : c;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = fabsf(v[e]) <= kMost ? __fdiv_rn(v[e], scale) : __int_as_float(0x7fc00000);
+        }
+        if (in) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) =
+              make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
+                         e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+          if (j == 0) a.scale[(size_t)slot[i] * a.H + hs[i]] = scale;
+          if (odd && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int MODE>
+bool launch_rows(const RowArgs& a, cudaStream_t st) {
+  if (a.d != 64 && a.d != 128 && a.d != 256) return false;
+  const int per = kFastThreads / (a.d / 8) * kIter;  // rows of a block
+  // a block of `per` rows touches at most this many tokens (32 KB of angles at most)
+  const int tokens = a.H >= per ? 2 : (per + a.H - 2) / a.H + 1;
+  const size_t smem = a.positions ? (size_t)tokens * a.rot * sizeof(float) : 0;
+  const unsigned grid = (unsigned)(((int64_t)a.n * a.H + per - 1) / per);
+  if (a.d == 64) k_rows<T, 64, MODE><<<grid, kFastThreads, smem, st>>>(a);
+  else if (a.d == 128) k_rows<T, 128, MODE><<<grid, kFastThreads, smem, st>>>(a);
+  else k_rows<T, 256, MODE><<<grid, kFastThreads, smem, st>>>(a);
+  return true;
+}
+
 struct ReadArgs {
   const void* cache;
   const float* scale;
@@ -116,30 +338,70 @@ struct ReadArgs {
   uint32_t* status;
 };
 
+// A thread converts 16-byte chunks of the cache (16 codes or 8 bf16 values),
+// kIter of them kFastThreads apart, all loaded before the first is stored. Bound
+// by memory: every row is read once and written once.
 template <bool E4M3, typename T>
-__global__ void __launch_bounds__(32 * kWarps) k_cache_read(const ReadArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (item >= (int64_t)a.n * a.H) return;
-  const int t = (int)(item / a.H), h = (int)(item % a.H);
-  const int slot = a.slots ? a.slots[t] : t;
-  const bool in = slot >= 0 && slot < a.L;
-  if (!in && slot != -1 && lane == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-  const size_t at = in ? ((size_t)slot * a.H + h) * a.d : 0;
-  const float scale = (E4M3 && in) ? a.scale[(size_t)slot * a.H + h] : 1.0f;
-  T* y = static_cast<T*>(a.out) + (size_t)item * a.d;
-  for (int j = lane; j < a.d; j += 32) {
-    float v = slot == -1 ? 0.0f : __int_as_float(0x7fc00000);
-    if (in) {
-      if constexpr (E4M3) {
-        const __half_raw r =
-            __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(a.cache)[at + j], __NV_E4M3);
-        v = __half2float(__half(r)) * scale;
-      } else {
-        v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache)[at + j]);
+__global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
+  constexpr int CE = E4M3 ? 16 : 8;  // elements of a chunk
+  const unsigned per_row = a.d / CE;
+  const int64_t total = (int64_t)a.n * a.H * per_row;
+  const int64_t f0 = (int64_t)blockIdx.x * (kFastThreads * kIter) + threadIdx.x;
+  uint4 raw[kIter];
+  float scale[kIter];
+  bool in[kIter];
+  int slot[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int64_t f = f0 + i * kFastThreads;
+    slot[i] = -1;
+    in[i] = false;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    scale[i] = 1.0f;
+    if (f < total) {
+      const unsigned item = (unsigned)(f / per_row), c = (unsigned)(f - (int64_t)item * per_row);
+      const unsigned t = item / a.H, h = item - t * a.H;
+      slot[i] = a.slots ? __ldg(a.slots + t) : (int)t;
+      in[i] = slot[i] >= 0 && slot[i] < a.L;
+      if (in[i]) {
+        const size_t row = (size_t)slot[i] * a.H + h;
+        raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.cache) +
+                                                      row * a.d * (E4M3 ? 1 : 2)) + c);
+        if (E4M3) scale[i] = __ldg(a.scale + row);
+      } else if (slot[i] != -1 && a.status) {
+        atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
       }
     }
-    y[j] = (T)v;
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int64_t f = f0 + i * kFastThreads;
+    if (f >= total) break;
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    T* y = static_cast<T*>(a.out) + f * CE;
+    const float none = slot[i] == -1 ? 0.0f : __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int p = 0; p < CE / 8; ++p) {
+      float v[8];
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint16_t two = (uint16_t)(w[2 * p + e / 2] >> (16 * (e % 2)));
+          uint32_t h2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          v[2 * e] = x.x * scale[i];
+          v[2 * e + 1] = x.y * scale[i];
+        }
+      } else {
+        unpack8<4>(w, v);
+      }
+      if (!in[i]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = none;
+      }
+      store8(y + 8 * p, v);
+    }
   }
 }
 
@@ -215,6 +477,9 @@ extern "C" hytopk_status hytopk_rope(const void* x, int64_t x_row, int64_t x_hea
   a.out_head = out_head;
   const unsigned grid = (unsigned)(((int64_t)n * H + kWarps - 1) / kWarps);
   const size_t smem = sizeof(float) * kWarps * d;
+  const bool f32 = type == HYTOPK_ELEM_F32;
+  if (f32 ? launch_rows<float, 0>(a, stream) : launch_rows<__nv_bfloat16, 0>(a, stream))
+    return launched();
   if (type == HYTOPK_ELEM_F32) k_rope<float><<<grid, 32 * kWarps, smem, stream>>>(a);
   else k_rope<__nv_bfloat16><<<grid, 32 * kWarps, smem, stream>>>(a);
   return launched();
@@ -242,6 +507,10 @@ extern "C" hytopk_status hytopk_cache_write(const void* x, int64_t x_row, int64_
   a.L = L;
   const unsigned grid = (unsigned)(((int64_t)n * H + kWarps - 1) / kWarps);
   const size_t smem = sizeof(float) * kWarps * d;
+  const bool f32 = x_type == HYTOPK_ELEM_F32;
+  if (f32 ? (e4 ? launch_rows<float, 2>(a, stream) : launch_rows<float, 1>(a, stream))
+          : (e4 ? launch_rows<__nv_bfloat16, 2>(a, stream) : launch_rows<__nv_bfloat16, 1>(a, stream)))
+    return launched();
   if (x_type == HYTOPK_ELEM_F32) {
     if (e4) k_cache_write<float, true><<<grid, 32 * kWarps, smem, stream>>>(a);
     else k_cache_write<float, false><<<grid, 32 * kWarps, smem, stream>>>(a);
@@ -267,13 +536,15 @@ extern "C" hytopk_status hytopk_cache_read(const void* cache, hytopk_elem cache_
   if (!aligned16(cache) || !aligned16(out) || !aligned4(cache_scale) || !aligned4(slots))
     return HYTOPK_MISALIGNED;
   const ReadArgs a{cache, cache_scale, slots, out, n, H, d, L, dev_status};
-  const unsigned grid = (unsigned)(((int64_t)n * H + kWarps - 1) / kWarps);
+  const int64_t per = kFastThreads * kIter;
+  const int64_t blocks = ((int64_t)n * H * (d / (e4 ? 16 : 8)) + per - 1) / per;
+  const unsigned grid = (unsigned)blocks;  // n H < 2^31 and at most 64 or 128 chunks a row: < 2^31
   if (out_type == HYTOPK_ELEM_F32) {
-    if (e4) k_cache_read<true, float><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else k_cache_read<false, float><<<grid, 32 * kWarps, 0, stream>>>(a);
+    if (e4) k_cache_read<true, float><<<grid, kFastThreads, 0, stream>>>(a);
+    else k_cache_read<false, float><<<grid, kFastThreads, 0, stream>>>(a);
   } else {
-    if (e4) k_cache_read<true, __nv_bfloat16><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else k_cache_read<false, __nv_bfloat16><<<grid, 32 * kWarps, 0, stream>>>(a);
+    if (e4) k_cache_read<true, __nv_bfloat16><<<grid, kFastThreads, 0, stream>>>(a);
+    else k_cache_read<false, __nv_bfloat16><<<grid, kFastThreads, 0, stream>>>(a);
   }
   return launched();
 }

@@ -1,13 +1,15 @@
-// rope.cuh -- rotary angles: cos and sin of position * frequency, accurate at
-// every position below 2^24.
+// rope.cuh -- rotary angles: cos and sin of position * frequency, accurate to
+// about an ulp of 1 at every position below 2^24.
 //
 // The product of a 24-bit position and a 24-bit frequency needs 48 bits; at a
 // million tokens its fp32 rounding alone is 0.03 rad. So the product is kept as
 // hi + lo (lo is the exact remainder, from a fused multiply-add) and reduced by
-// the nearest multiple of 2 pi with 2 pi = C1 + C2 + C3 in fp32 parts (the
-// reduction by constants in parts of Cody and Waite, "Software Manual for the
-// Elementary Functions", 1980), which leaves an angle in [-pi, pi] that is
-// good to about 2^-23.
+// the nearest multiple of pi / 2 = C1 + C2 + C3 in fp32 parts (the reduction by
+// constants in parts of Cody and Waite, "Software Manual for the Elementary
+// Functions", 1980). On the rest, in [-pi/4, pi/4], the Taylor series of sin and
+// cos to x^9 and x^10 are off by less than 2e-9. (25 instructions; sincosf, which
+// reduces once more, took the rotation of single-head keys from the memory bound
+// to 2.5 times it.)
 #pragma once
 
 #include "common.cuh"
@@ -17,18 +19,40 @@ namespace hytopk {
 constexpr int kMaxPosition = 1 << 24;  // positions below this are exact in fp32
 
 __device__ __forceinline__ void rope_turn(float pos, float freq, float& c, float& s) {
+  constexpr double kHalfPi = 1.5707963267948966192313216916398;
+  constexpr float C1 = (float)kHalfPi;
+  constexpr float C2 = (float)(kHalfPi - (double)C1);
+  constexpr float C3 = (float)(kHalfPi - (double)C1 - (double)C2);
   const float hi = __fmul_rn(pos, freq);
-  const float lo = __fmaf_rn(pos, freq, -hi);
-  // 2 pi = 6.28318548202514648 - 1.74845553146951715e-7 - ... (fp32 parts)
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
-  constexpr float C1 = (float)kTwoPi;
-  constexpr float C2 = (float)(kTwoPi - (double)C1);
-  constexpr float C3 = (float)(kTwoPi - (double)C1 - (double)C2);
-  const float turns = rintf(hi * (float)(1.0 / kTwoPi));
-  float r = __fmaf_rn(-turns, C1, hi);
-  r = __fmaf_rn(-turns, C2, r);
-  r = __fmaf_rn(-turns, C3, r);
-  sincosf(r + lo, &s, &c);
+  float r;
+  int q;
+  if (fabsf(hi) < 4194304.0f) {
+    const float lo = __fmaf_rn(pos, freq, -hi);
+    const float n = rintf(hi * (float)(1.0 / kHalfPi));
+    r = __fmaf_rn(-n, C1, hi);
+    r = __fmaf_rn(-n, C2, r);
+    r = __fmaf_rn(-n, C3, r) + lo;
+    q = (int)n;
+  } else {  // past 2^22 the multiple is no longer exact in fp32
+    const double x = (double)pos * (double)freq;
+    const double n = rint(x * (1.0 / kHalfPi));
+    r = (float)(x - n * kHalfPi);
+    q = (int)(long long)n;
+  }
+  const float z = r * r;
+  float sn = __fmaf_rn(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  sn = __fmaf_rn(sn, z, 1.0f / 120.0f);
+  sn = __fmaf_rn(sn, z, -1.0f / 6.0f);
+  sn = __fmaf_rn(sn * z, r, r);
+  float cs = __fmaf_rn(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  cs = __fmaf_rn(cs, z, -1.0f / 720.0f);
+  cs = __fmaf_rn(cs, z, 1.0f / 24.0f);
+  cs = __fmaf_rn(cs, z, -0.5f);
+  cs = __fmaf_rn(cs, z, 1.0f);
+  // quadrant: (c, s) -> (-s, c) for each quarter turn
+  const float a = (q & 1) ? sn : cs, b = (q & 1) ? cs : sn;
+  c = ((q + 1) & 2) ? -a : a;
+  s = (q & 2) ? -b : b;
 }
 
 }  // namespace hytopk
