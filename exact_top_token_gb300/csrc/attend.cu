@@ -2,9 +2,6 @@
 // query over its own selected cache rows, and its gradients.
 #include "attend.h"
 
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
 #include "launch.h"
 
 namespace hytopk {
@@ -16,90 +13,12 @@ cudaError_t launch_attend_d128_bf16(const att::Args& a, bool f32, int sms, cudaS
 cudaError_t launch_attend_d128_e4m3(const att::Args& a, bool f32, int sms, cudaStream_t st);
 cudaError_t launch_attend_d256_bf16(const att::Args& a, bool f32, int sms, cudaStream_t st);
 cudaError_t launch_attend_d256_e4m3(const att::Args& a, bool f32, int sms, cudaStream_t st);
+// attend_backward_d*.cu
+cudaError_t launch_attend_backward_d64(const att::Args& a, bool out_f32, int sms, cudaStream_t st);
+cudaError_t launch_attend_backward_d128(const att::Args& a, bool out_f32, int sms, cudaStream_t st);
 
 namespace att {
 namespace {
-
-constexpr int kThreads = 128;
-
-__device__ __forceinline__ float block_reduce(float v, bool maximum, float* red) {
-  for (int o = 16; o; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = maximum ? fmaxf(v, w) : v + w;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int i = 1; i < kThreads / 32; ++i) v = maximum ? fmaxf(v, red[i]) : v + red[i];
-  return v;
-}
-
-template <bool E4M3>
-__device__ __forceinline__ float row_elem(const void* base, int64_t row, int s, int hk, int d, int j) {
-  const size_t at = (size_t)s * row + (size_t)hk * d + j;
-  if constexpr (E4M3) {
-    const __half_raw r = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(base)[at], __NV_E4M3);
-    return __half2float(__half(r));
-  } else {
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
-  }
-}
-
-__device__ __forceinline__ int checked_row(const Args& a, int t, int j) {
-  const int s = a.idx[(size_t)t * a.k_top + j];
-  if (s >= 0 && s < a.L) return s;
-  if (s != -1 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-  return -1;
-}
-
-// One query head per CTA: a warp per selected row.
-__global__ void __launch_bounds__(kThreads) k_attend_backward_simple(const Args a, int out_f32) {
-  extern __shared__ float sh[];
-  float* qs = sh;
-  float* dos = qs + a.d;
-  float* dqs = dos + a.d;
-  __shared__ float red[4];
-  const int Hq = a.Hkv * a.G;
-  const int t = blockIdx.x / Hq, h = blockIdx.x % Hq, hk = h / a.G;
-  const size_t at = ((size_t)t * Hq + h) * a.d;
-  float delta = 0.0f;
-  for (int i = threadIdx.x; i < a.d; i += kThreads) {
-    qs[i] = __bfloat162float(
-        static_cast<const __nv_bfloat16*>(a.q)[(size_t)t * a.q_row + (size_t)h * a.d + i]);
-    dos[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[at + i]);
-    const float o = out_f32 ? static_cast<const float*>(a.out)[at + i]
-                            : __bfloat162float(static_cast<const __nv_bfloat16*>(a.out)[at + i]);
-    delta += dos[i] * o;
-    dqs[i] = 0.0f;
-  }
-  delta = block_reduce(delta, false, red);
-  const float lse = a.lse[(size_t)t * Hq + h];
-  const int lane = threadIdx.x & 31;
-  for (int j = threadIdx.x >> 5; j < a.k_top; j += kThreads / 32) {
-    const int s = checked_row(a, t, j);
-    if (s < 0 || lse == -INFINITY) continue;
-    float x = 0.0f, dp = 0.0f;
-    for (int i = lane; i < a.d; i += 32) {
-      x += qs[i] * row_elem<false>(a.k, a.k_row, s, hk, a.d, i);
-      dp += dos[i] * row_elem<false>(a.v, a.v_row, s, hk, a.d, i);
-    }
-    for (int o = 16; o; o >>= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      dp += __shfl_xor_sync(0xffffffffu, dp, o);
-    }
-    const float p = __expf(x * a.scale - lse);
-    const float ds = p * (dp - delta) * a.scale;
-    const size_t row = ((size_t)s * a.Hkv + hk) * a.d;
-    for (int i = lane; i < a.d; i += 32) {
-      atomicAdd(a.dv + row + i, p * dos[i]);
-      atomicAdd(a.dk + row + i, ds * qs[i]);
-      atomicAdd(dqs + i, ds * row_elem<false>(a.k, a.k_row, s, hk, a.d, i));
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.d; i += kThreads) a.dq[at + i] = dqs[i];
-}
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -207,7 +126,8 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  att::k_attend_backward_simple<<<(unsigned)n * Hq, att::kThreads, sizeof(float) * 3 * d, stream>>>(
-      a, out_type == HYTOPK_ELEM_F32);
-  return cudaGetLastError() == cudaSuccess ? HYTOPK_OK : HYTOPK_CUDA_ERROR;
+  auto launch = d == 64 ? launch_attend_backward_d64 : launch_attend_backward_d128;
+  return launch(a, out_type == HYTOPK_ELEM_F32, num_sms(), stream) == cudaSuccess
+             ? HYTOPK_OK
+             : HYTOPK_CUDA_ERROR;
 }

@@ -1,0 +1,546 @@
+// attend_backward_engine.cuh -- gradients of the attention over selected rows
+// (hytopk_attend_backward), on the tensor cores.
+//
+// One work item is a query and up to N = 64 of the heads that share a cache
+// head; its selected rows are gathered 128 at a time. As in the forward engine
+// the rows fill the 128 lanes and the heads are the narrow side. Per tile, with
+// P = exp(S - lse) and dS = P (dP - grad . out):
+//
+//   S^T  [128 rows x N]   = K . Q^T           dP^T [128 rows x N] = V . dO^T
+//   dV   [128 rows x d]   = P^T . dO          (A: P as [row][head], K-major)
+//   dK   [128 rows x d]   = dS^T . Q
+//   dQ^T [d x N]         += K^T . dS^T        (A: K as gathered, M = d contiguous;
+//                                              B: dS as [row][head], N contiguous)
+//
+// The results are fp32, so P and dS are written as three bf16 parts (24 bits)
+// and their products take three terms; the other operands are bf16 as given.
+// dQ^T takes the first two parts side by side (N = 128) and adds the third to
+// the second's columns.
+//
+// A tile's products keep the tensor core busy if a tile's softmax overlaps the
+// products of the tile before. The order is
+//   dV(g), dK(g), S(g+1) + dP(g+1), dQ(g)
+// so that the rows of tile g+1 have the time of dV(g) and dK(g) to arrive (K has
+// two buffers and V one: shared memory is full), dV(g) and dK(g) are added to
+// global memory while later products run, and P(g+1) is computed under dQ(g).
+//
+//   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
+//                 columns), additions of dV and dK (its share of the d columns),
+//                 dQ read-out
+//   4 warps       producers (cp.async); also the row sums grad . out
+//   last warp     MMA issuer, TMEM
+#pragma once
+
+#include "attend_engine.cuh"
+
+namespace hytopk {
+namespace att {
+
+template <int D_, int N_>
+struct BCfg {
+  static constexpr int D = D_, N = N_;
+  static constexpr int SWG = N >= 64 ? 4 : 2;
+  static constexpr int SWARPS = 4 * SWG;
+  static constexpr int HG = N / SWG;     // head columns of a warpgroup
+  static constexpr int DG = D / SWG;     // d columns it adds
+  static constexpr int RB = 2 * D;
+  using Geo = tc::Geo<RB>;
+  static constexpr int SLOT = 128 * RB;  // K or V tile
+  static constexpr int PBYTES = 16384;   // one part of P or dS: 128 rows x 64 heads
+  static constexpr int QBYTES = N * RB;
+  static constexpr int PWARPS = 4;
+  static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
+  static constexpr int MMA_WARP = SWARPS + PWARPS;
+  static constexpr int K_OFF = 0;                 // two buffers
+  static constexpr int V_OFF = 2 * SLOT;
+  static constexpr int P_OFF = 3 * SLOT;          // three parts
+  static constexpr int S_OFF = P_OFF + 3 * PBYTES;
+  static constexpr int Q_OFF = S_OFF + 3 * PBYTES;
+  static constexpr int G_OFF = Q_OFF + QBYTES;    // gradient rows
+  static constexpr int MISC_OFF = G_OFF + QBYTES;
+  static constexpr int MISC = 4 * N * 4 + 256;    // -lse, -grad . out [2][N]; barriers
+  static constexpr int SMEM = MISC_OFF + MISC + 1024;
+  // TMEM columns
+  static constexpr int S_COL = 0, DP_COL = N, DV_COL = 128, DK_COL = 128 + D, DQ_COL = 384;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(2 * N <= 128 && DK_COL + D <= DQ_COL, "TMEM columns");
+};
+
+__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a),
+               "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
+      " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+// The three bf16 parts of W weights of a row, to the three part buffers.
+template <int W>
+__device__ __forceinline__ void store_parts(uint8_t* dst, int row, int c0, float (&v)[W]) {
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+#pragma unroll
+    for (int u = 0; u < W; u += 8) {
+      uint32_t x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = pack_bf16(v[u + 2 * e], v[u + 2 * e + 1]);
+        if (part < 2) take_bf16(x[e], v[u + 2 * e], v[u + 2 * e + 1]);
+      }
+      *reinterpret_cast<uint4*>(dst + part * 16384 + p_offset(row, c0 + u)) =
+          make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+
+template <class C, bool OUT_F32>
+__global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a, const Plan pl) {
+  constexpr int D = C::D, N = C::N, HG = C::HG, DG = C::DG;
+  using Geo = typename C::Geo;
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  uint8_t* smem = tc::align1024(smem_dyn);
+  float* nl_s = reinterpret_cast<float*>(smem + C::MISC_OFF);  // [2][N] -lse (log2)
+  float* nd_s = nl_s + 2 * N;                                  // [2][N] -grad . out
+  uint64_t* bars = reinterpret_cast<uint64_t*>(nd_s + 2 * N);
+  uint64_t* k_full = bars;
+  uint64_t* k_empty = bars + 2;
+  uint64_t* v_full = bars + 4;
+  uint64_t* v_empty = bars + 5;
+  uint64_t* q_full = bars + 6;
+  uint64_t* q_empty = bars + 7;
+  uint64_t* s_full = bars + 8;
+  uint64_t* s_empty = bars + 9;
+  uint64_t* p_full = bars + 10;
+  uint64_t* ds_full = bars + 11;
+  uint64_t* ds_empty = bars + 12;
+  uint64_t* dv_full = bars + 13;
+  uint64_t* dv_empty = bars + 14;
+  uint64_t* dk_full = bars + 15;
+  uint64_t* dk_empty = bars + 16;
+  uint64_t* dq_full = bars + 17;
+  uint64_t* dq_empty = bars + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(k_full + i, C::PWARPS * 32);
+      tc::mbar_init(k_empty + i, 1);
+    }
+    tc::mbar_init(v_full, C::PWARPS * 32);
+    tc::mbar_init(q_full, C::PWARPS);
+    uint64_t* by_mma[] = {v_empty, q_empty, s_full, ds_empty, dv_full, dk_full, dq_full};
+    for (uint64_t* b : by_mma) tc::mbar_init(b, 1);
+    uint64_t* by_softmax[] = {s_empty, p_full, ds_full, dv_empty, dk_empty, dq_empty};
+    for (uint64_t* b : by_softmax) tc::mbar_init(b, C::SWARPS);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == C::MMA_WARP) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+  const int first = (int)blockIdx.x;
+  const int n_mine = pl.items > first ? (pl.items - 1 - first) / pl.stride + 1 : 0;
+  const int ntile = pl.tiles, total = n_mine * ntile;
+  const int Hq = a.Hkv * a.G;
+  struct Walk {
+    int i, t, hk, b;
+  };
+  Walk start;
+  start.i = 0;
+  start.b = first % pl.blocks;
+  start.hk = first / pl.blocks % a.Hkv;
+  start.t = first / pl.blocks / a.Hkv;
+  auto walk_next = [&](Walk& w) {
+    if (++w.i == ntile) {
+      w.i = 0;
+      w.b += pl.sb;
+      w.hk += pl.sh;
+      w.t += pl.st;
+      if (w.b >= pl.blocks) {
+        w.b -= pl.blocks;
+        ++w.hk;
+      }
+      if (w.hk >= a.Hkv) {
+        w.hk -= a.Hkv;
+        ++w.t;
+      }
+    }
+  };
+  auto first_head = [&](const Walk& w) { return w.hk * a.G + w.b * pl.heads; };
+  auto head_count = [&](const Walk& w) { return min(pl.heads, a.G - w.b * pl.heads); };
+  auto entry_of = [&](int t, int j) -> int {
+    return j < a.k_top ? __ldg(a.idx + (size_t)t * a.k_top + j) : -1;
+  };
+  auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
+
+  if (warp >= C::SWARPS && warp < C::MMA_WARP) {
+    // ---------------- producers ----------------
+    const int tid = threadIdx.x - C::SWARPS * 32;
+    const int pw = warp - C::SWARPS;
+    constexpr int CPR = C::RB / 16;              // 8 or 16
+    constexpr int RPP = 32 / CPR;
+    constexpr int PASSES = 32 / RPP;
+    constexpr int SHIFT = CPR == 16 ? 4 : 3;
+    // The item's query and gradient rows (zero beyond its heads), its -lse and
+    // its row sums grad . out (padded heads: weights of zero).
+    auto load_query = [&](int qi, const Walk& w) -> bool {
+      const int h0 = first_head(w), nh = head_count(w);
+      const size_t at = (size_t)w.t * Hq + h0;
+      const __nv_bfloat16* grad = static_cast<const __nv_bfloat16*>(a.grad) + at * D;
+      float* nl = nl_s + (qi & 1) * N;
+      float* nd = nd_s + (qi & 1) * N;
+      constexpr int EL = D / 32;  // elements of a row per lane
+#pragma unroll 4
+      for (int h = pw; h < N; h += C::PWARPS) {
+        float sum = 0.0f;
+        if (h < nh) {
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const size_t i = (size_t)h * D + e * 32 + lane;
+            const float o = OUT_F32 ? __ldg(static_cast<const float*>(a.out) + at * D + i)
+                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(a.out)[at * D + i]);
+            sum = __fmaf_rn(__bfloat162float(grad[i]), o, sum);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+          const float lse = h < nh ? __ldg(a.lse + at + h) : -INFINITY;
+          nd[h] = -sum;
+          nl[h] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+        }
+      }
+      const bool ok = wait_bar(q_empty, (qi & 1) ^ 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      const uint8_t* qsrc = static_cast<const uint8_t*>(a.q) +
+                            ((size_t)w.t * a.q_row + (size_t)h0 * D) * 2;
+      constexpr int PER = N * CPR / (C::PWARPS * 32);
+      constexpr int U = PER < 4 ? PER : 4;
+#pragma unroll 1
+      for (int p = 0; p < PER; p += U) {
+        uint4 v[U], x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int f = (p + u) * C::PWARPS * 32 + tid;
+          v[u] = x[u] = make_uint4(0, 0, 0, 0);
+          if (f / CPR < nh) {
+            v[u] = __ldg(reinterpret_cast<const uint4*>(qsrc) + f);
+            x[u] = __ldg(reinterpret_cast<const uint4*>(grad) + f);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int f = (p + u) * C::PWARPS * 32 + tid;
+          const uint32_t off = Geo::chunk_offset(f / CPR, f % CPR, N);
+          *reinterpret_cast<uint4*>(smem + C::Q_OFF + off) = v[u];
+          *reinterpret_cast<uint4*>(smem + C::G_OFF + off) = x[u];
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+      return true;
+    };
+    Walk w = start, wn = w;
+    int qi = 0;
+    bool ok = true;
+    int e_next = total > 0 ? entry_of(w.t, tid) : -1;
+#pragma unroll 1
+    for (int g = 0; g < total && ok; ++g, w = wn) {
+      const int s_own = row_of(e_next);
+      int rows[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        rows[p] = __shfl_sync(0xffffffffu, s_own, p * RPP + (lane >> SHIFT));
+      if (g + 1 < total) {
+        walk_next(wn);
+        e_next = entry_of(wn.t, wn.i * 128 + tid);
+      }
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t* empty = kv ? v_empty : k_empty + (g & 1);
+        uint64_t* full = kv ? v_full : k_full + (g & 1);
+        const uint32_t parity = kv ? (g & 1) ^ 1 : ((g >> 1) & 1) ^ 1;
+        ok = __all_sync(0xffffffffu, wait_bar(empty, parity, abort_flag, a.status));
+        if (!ok) break;
+        const uint32_t dst = tc::smem_u32(smem + (kv ? C::V_OFF : C::K_OFF + (g & 1) * C::SLOT));
+        const int c = lane & ((1 << SHIFT) - 1);
+        const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) + (size_t)w.hk * C::RB + c * 16;
+        const int64_t row_bytes = (kv ? a.v_row : a.k_row) * 2;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const int s = rows[p];
+          cp_async16(dst + Geo::chunk_offset(pw * 32 + p * RPP + (lane >> SHIFT), c, 128),
+                     base + (s >= 0 ? s * row_bytes : 0), s >= 0);
+        }
+        cp_async_arrive(full);
+      }
+      if (ok && w.i == 0 && !load_query(qi++, w)) break;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == C::MMA_WARP) {
+    // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
+    constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
+    constexpr uint32_t ID_DV = tc::instr_desc(0, 128, D) | (1u << 16);
+    constexpr uint32_t ID_DQ2 = tc::instr_desc(0, 128, 128) | (1u << 15) | (1u << 16);
+    constexpr uint32_t ID_DQ1 = tc::instr_desc(0, 128, 64) | (1u << 15) | (1u << 16);
+    constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+    constexpr uint32_t LBO_K = 1u << 16, LBO_MN = (16384u >> 4) << 16;
+    constexpr uint32_t LBO_Q = ((uint32_t)(N * 128) >> 4) << 16;
+    auto low = [](const void* p) { return (tc::smem_u32(p) >> 4) & 0x3FFFu; };
+    auto desc = [&](uint32_t lo) { return tc::desc_from_words(lo, D_HI); };
+    const uint32_t k_lo = low(smem + C::K_OFF), v_lo = low(smem + C::V_OFF);
+    const uint32_t p_lo = low(smem + C::P_OFF), s_lo = low(smem + C::S_OFF);
+    const uint32_t q_lo = low(smem + C::Q_OFF), g_lo = low(smem + C::G_OFF);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
+    };
+    int si = 0, sq = 0;  // tile of its item and item of the next scores
+    auto scores = [&](int g) -> bool {
+      if (si == 0 && !wait(q_full, sq & 1)) return false;
+      if (!wait(k_full + (g & 1), (g >> 1) & 1)) return false;
+      if (!wait(v_full, g & 1)) return false;
+      if (!wait(s_empty, (g & 1) ^ 1)) return false;
+      tc::fence_proxy_async_smem();
+      tc::fence_after_sync();
+      const uint32_t ka = (k_lo + (g & 1) * (C::SLOT >> 4)) | LBO_K;
+      if (elect_one()) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          tc::mma<0>(tmem + C::S_COL, desc(ka + (Geo::step_offset(j, 128) >> 4)),
+                     desc((q_lo | LBO_K) + (Geo::step_offset(j, N) >> 4)), ID_S, j > 0 ? 1u : 0u);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          tc::mma<0>(tmem + C::DP_COL, desc((v_lo | LBO_K) + (Geo::step_offset(j, 128) >> 4)),
+                     desc((g_lo | LBO_K) + (Geo::step_offset(j, N) >> 4)), ID_S, j > 0 ? 1u : 0u);
+        tc::mma_commit(s_full);
+        tc::mma_commit(v_empty);
+      }
+      __syncwarp();
+      if (++si == ntile) {
+        si = 0;
+        ++sq;
+      }
+      return true;
+    };
+    // D [128 rows x d] = sum over the parts of A (K-major, [row][head]) . B ([head][d])
+    auto rows_product = [&](uint32_t col, uint32_t a_lo, uint32_t b_lo) {
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int s = 0; s < N / 16; ++s)
+          tc::mma<0>(tmem + col, desc((a_lo | LBO_K) + ((part * C::PBYTES + s * 32) >> 4)),
+                     desc((b_lo | LBO_Q) + ((s * 2048) >> 4)), ID_DV, (part > 0 || s > 0) ? 1u : 0u);
+    };
+    int i = 0, qi = 0;
+    bool ok = total == 0 || scores(0);
+#pragma unroll 1
+    for (int g = 0; g < total && ok; ++g) {
+      const bool last = i == ntile - 1;
+      // dV
+      ok = wait(dv_empty, (g & 1) ^ 1) && wait(p_full, g & 1);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (elect_one()) {
+        rows_product(C::DV_COL, p_lo, g_lo);
+        tc::mma_commit(dv_full);
+      }
+      __syncwarp();
+      // dK
+      ok = wait(dk_empty, (g & 1) ^ 1) && wait(ds_full, g & 1);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (elect_one()) {
+        rows_product(C::DK_COL, s_lo, q_lo);
+        tc::mma_commit(dk_full);
+        if (last) tc::mma_commit(q_empty);
+      }
+      __syncwarp();
+      // the next item's scores wait for its queries: not before this item's dQ
+      if (!last && !(ok = scores(g + 1))) break;
+      if (i == 0 && !(ok = wait(dq_empty, (qi & 1) ^ 1))) break;
+      const uint32_t ka = (k_lo + (g & 1) * (C::SLOT >> 4)) | LBO_MN;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)  // 16 rows each
+          tc::mma<0>(tmem + C::DQ_COL, desc(ka + ((s * 2048) >> 4)),
+                     desc((s_lo | LBO_MN) + ((s * 2048) >> 4)), ID_DQ2, (i > 0 || s > 0) ? 1u : 0u);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc::mma<0>(tmem + C::DQ_COL + 64, desc(ka + ((s * 2048) >> 4)),
+                     desc((s_lo | LBO_MN) + ((2 * C::PBYTES + s * 2048) >> 4)), ID_DQ1, 1u);
+        tc::mma_commit(ds_empty);
+        tc::mma_commit(k_empty + (g & 1));
+        if (last) tc::mma_commit(dq_full);
+      }
+      __syncwarp();
+      if (last && g + 1 < total && !(ok = scores(g + 1))) break;
+      if (++i == ntile) {
+        i = 0;
+        ++qi;
+      }
+    }
+  } else {
+    // ---------------- softmax: TMEM lane = selected row ----------------
+    const int wg = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int c0 = wg * HG, d0 = wg * DG;
+    const float c_scale = a.scale * kLog2e;
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar);
+    };
+    // add this row's d columns of an accumulator to dst
+    auto add_rows = [&](uint32_t col, float* dst, float factor) {
+#pragma unroll 1
+      for (int cc = 0; cc < DG; cc += 32) {
+        constexpr int CW = DG < 32 ? DG : 32;
+        float x[CW];
+        tmem_load(tmem + lane_off + col + d0 + cc, x);
+        if (dst) {
+#pragma unroll
+          for (int u = 0; u < CW; u += 4)
+            red_add4(dst + d0 + cc + u, x[u] * factor, x[u + 1] * factor, x[u + 2] * factor,
+                     x[u + 3] * factor);
+        }
+      }
+      tc::fence_before_sync();
+    };
+    Walk w = start, wf = start;
+    int qi = 0;
+    int e_next = total > 0 ? entry_of(w.t, row) : -1;
+    int64_t prev = -1;       // element offset of the last tile's row in dk and dv, -1: none
+    bool pend = false;       // the item before has its dQ to be read
+    int pend_nh = 0;
+    size_t pend_at = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
+    };
+#pragma unroll 1
+    for (int g = 0; g <= total; ++g) {
+      const int s = row_of(e_next);
+      if (g < total) {
+        if (e_next != -1 && s < 0 && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+        if (g + 1 < total) {
+          walk_next(wf);
+          e_next = entry_of(wf.t, wf.i * 128 + row);
+        }
+      }
+      if (g > 0) {
+        // the last tile's dV and dK, under its later products
+        const uint32_t ph = (g - 1) & 1;
+        if (!wait(dv_full, ph)) break;
+        tc::fence_after_sync();
+        add_rows(C::DV_COL, prev >= 0 ? a.dv + prev : nullptr, 1.0f);
+        arrive(dv_empty);
+        if (!wait(dk_full, ph)) break;
+        tc::fence_after_sync();
+        add_rows(C::DK_COL, prev >= 0 ? a.dk + prev : nullptr, a.scale);
+        arrive(dk_empty);
+      }
+      if (g < total) {
+        if (w.i == 0 && !wait(q_full, qi & 1)) break;
+        if (!wait(s_full, g & 1)) break;
+        tc::fence_after_sync();
+        float p[HG], ds[HG];
+        tmem_load(tmem + lane_off + C::S_COL + c0, p);
+        tmem_load(tmem + lane_off + C::DP_COL + c0, ds);
+        const float* nl = nl_s + (qi & 1) * N + c0;
+        const float* nd = nd_s + (qi & 1) * N + c0;
+        const bool valid = s >= 0;
+#pragma unroll
+        for (int u = 0; u < HG; u += 2) {
+          fma2(p[u], p[u + 1], c_scale, nl[u], nl[u + 1]);
+          add2(ds[u], ds[u + 1], nd[u], nd[u + 1]);
+        }
+        // scores and the item's sums are read: both may be replaced
+        tc::fence_before_sync();
+        arrive(s_empty);
+#pragma unroll
+        for (int u = 0; u < HG; ++u) p[u] = valid ? ex2(p[u]) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < HG; u += 2) mul2(ds[u], ds[u + 1], p[u], p[u + 1]);
+        // (the last tile's dV, the last reader of P, is done)
+        store_parts<HG>(smem + C::P_OFF, row, c0, p);
+        tc::fence_proxy_async_smem();
+        arrive(p_full);
+        if (!valid) {
+#pragma unroll
+          for (int u = 0; u < HG; ++u) ds[u] = 0.0f;
+        }
+        if (!wait(ds_empty, (g & 1) ^ 1)) break;
+        store_parts<HG>(smem + C::S_OFF, row, c0, ds);
+        tc::fence_proxy_async_smem();
+        arrive(ds_full);
+        prev = valid ? ((int64_t)s * a.Hkv + w.hk) * D : -1;
+      }
+      // the item before: dQ^T, lane = d, the parts' two column blocks summed
+      if (pend) {
+        if (!wait(dq_full, (qi - 1) & 1)) break;
+        tc::fence_after_sync();
+        if (quad * 32 < D && c0 < pend_nh) {
+          float x[HG], y[HG];
+          tmem_load(tmem + lane_off + C::DQ_COL + c0, x);
+          tmem_load(tmem + lane_off + C::DQ_COL + 64 + c0, y);
+#pragma unroll
+          for (int u = 0; u < HG; ++u)
+            if (c0 + u < pend_nh)
+              a.dq[pend_at + (size_t)(c0 + u) * D + row] = (x[u] + y[u]) * a.scale;
+        }
+        tc::fence_before_sync();
+        arrive(dq_empty);
+        pend = false;
+      }
+      if (g < total && w.i == ntile - 1) {
+        pend = true;
+        pend_nh = head_count(w);
+        pend_at = ((size_t)w.t * Hq + first_head(w)) * D;
+        ++qi;
+      }
+      walk_next(w);
+    }
+    (void)ok;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <class C, bool OUT_F32>
+cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
+  auto kernel = k_attend_backward<C, OUT_F32>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  Plan pl{};
+  pl.splits = 1;
+  pl.blocks = (a.G + C::N - 1) / C::N;
+  pl.heads = (a.G + pl.blocks - 1) / pl.blocks;
+  pl.tiles = (a.k_top + 127) / 128;
+  pl.items = a.n * a.Hkv * pl.blocks;
+  pl.stride = pl.items < sms ? pl.items : sms;
+  pl.sb = pl.stride % pl.blocks;
+  pl.sh = pl.stride / pl.blocks % a.Hkv;
+  pl.st = pl.stride / pl.blocks / a.Hkv;
+  kernel<<<pl.stride, C::THREADS, C::SMEM, st>>>(a, pl);
+  return cudaGetLastError();
+}
+
+}  // namespace att
+}  // namespace hytopk
