@@ -24,9 +24,14 @@
 // two buffers and V one: shared memory is full), dV(g) and dK(g) are added to
 // global memory while later products run, and P(g+1) is computed under dQ(g).
 //
+// The tensor core's fp32 additions truncate, so a long chain of them drifts (128
+// steps: 2e-6 of the result). dQ^T is read out and added up in global memory
+// every kChunk tiles.
+//
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
-//                 columns), additions of dV and dK (its share of the d columns),
-//                 dQ read-out
+//                 columns)
+//   4 warps       read-out: additions of dV and dK, dQ (they wait on the L2's
+//                 additions, which the softmax must not)
 //   4 warps       producers (cp.async); also the row sums grad . out
 //   last warp     MMA issuer, TMEM
 #pragma once
@@ -36,21 +41,23 @@
 namespace hytopk {
 namespace att {
 
+constexpr int kChunk = 4;  // tiles whose dQ is summed on the tensor core
+
 template <int D_, int N_>
 struct BCfg {
   static constexpr int D = D_, N = N_;
   static constexpr int SWG = N >= 64 ? 4 : 2;
   static constexpr int SWARPS = 4 * SWG;
   static constexpr int HG = N / SWG;     // head columns of a warpgroup
-  static constexpr int DG = D / SWG;     // d columns it adds
   static constexpr int RB = 2 * D;
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;  // K or V tile
   static constexpr int PBYTES = 16384;   // one part of P or dS: 128 rows x 64 heads
   static constexpr int QBYTES = N * RB;
   static constexpr int PWARPS = 4;
-  static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
-  static constexpr int MMA_WARP = SWARPS + PWARPS;
+  static constexpr int READ_WARP = SWARPS, PROD_WARP = SWARPS + 4;
+  static constexpr int MMA_WARP = PROD_WARP + PWARPS;
+  static constexpr int THREADS = (MMA_WARP + 1) * 32;
   static constexpr int K_OFF = 0;                 // two buffers
   static constexpr int V_OFF = 2 * SLOT;
   static constexpr int P_OFF = 3 * SLOT;          // three parts
@@ -66,9 +73,8 @@ struct BCfg {
   static_assert(2 * N <= 128 && DK_COL + D <= DQ_COL, "TMEM columns");
 };
 
-__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d) {
-  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a),
-               "f"(b), "f"(c), "f"(d)
+__device__ __forceinline__ void red_add2(float* p, float a, float b) {
+  asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(a), "f"(b)
                : "memory");
 }
 __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
@@ -76,6 +82,16 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
       " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
+}
+
+// 16 TMEM lanes x 32 columns of 32 bit: lane l of the warp gets, per block b of 8
+// columns, columns 2 (l % 4), + 1 of TMEM lane l / 4 (v[4b], v[4b + 1]) and of
+// lane l / 4 + 8 (v[4b + 2], v[4b + 3]).
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t addr, float (&v)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+               : "r"(addr));
+  tc::tmem_wait_ld(v);
 }
 
 // The three bf16 parts of W weights of a row, to the three part buffers.
@@ -99,7 +115,7 @@ __device__ __forceinline__ void store_parts(uint8_t* dst, int row, int c0, float
 
 template <class C, bool OUT_F32>
 __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a, const Plan pl) {
-  constexpr int D = C::D, N = C::N, HG = C::HG, DG = C::DG;
+  constexpr int D = C::D, N = C::N, HG = C::HG;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem = tc::align1024(smem_dyn);
@@ -136,8 +152,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
     tc::mbar_init(q_full, C::PWARPS);
     uint64_t* by_mma[] = {v_empty, q_empty, s_full, ds_empty, dv_full, dk_full, dq_full};
     for (uint64_t* b : by_mma) tc::mbar_init(b, 1);
-    uint64_t* by_softmax[] = {s_empty, p_full, ds_full, dv_empty, dk_empty, dq_empty};
+    uint64_t* by_softmax[] = {s_empty, p_full, ds_full};
     for (uint64_t* b : by_softmax) tc::mbar_init(b, C::SWARPS);
+    uint64_t* by_read[] = {dv_empty, dk_empty, dq_empty};
+    for (uint64_t* b : by_read) tc::mbar_init(b, 4);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
@@ -185,10 +203,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
   };
   auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
-  if (warp >= C::SWARPS && warp < C::MMA_WARP) {
+  if (warp >= C::PROD_WARP && warp < C::MMA_WARP) {
     // ---------------- producers ----------------
-    const int tid = threadIdx.x - C::SWARPS * 32;
-    const int pw = warp - C::SWARPS;
+    const int tid = threadIdx.x - C::PROD_WARP * 32;
+    const int pw = warp - C::PROD_WARP;
     constexpr int CPR = C::RB / 16;              // 8 or 16
     constexpr int RPP = 32 / CPR;
     constexpr int PASSES = 32 / RPP;
@@ -344,7 +362,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
           tc::mma<0>(tmem + col, desc((a_lo | LBO_K) + ((part * C::PBYTES + s * 32) >> 4)),
                      desc((b_lo | LBO_Q) + ((s * 2048) >> 4)), ID_DV, (part > 0 || s > 0) ? 1u : 0u);
     };
-    int i = 0, qi = 0;
+    int i = 0, nq = 0;  // tile of its item; chunks of dQ begun
     bool ok = total == 0 || scores(0);
 #pragma unroll 1
     for (int g = 0; g < total && ok; ++g) {
@@ -370,150 +388,178 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
       __syncwarp();
       // the next item's scores wait for its queries: not before this item's dQ
       if (!last && !(ok = scores(g + 1))) break;
-      if (i == 0 && !(ok = wait(dq_empty, (qi & 1) ^ 1))) break;
+      const bool begin = i % kChunk == 0, end = i % kChunk == kChunk - 1 || last;
+      if (begin && !(ok = wait(dq_empty, (nq++ & 1) ^ 1))) break;
       const uint32_t ka = (k_lo + (g & 1) * (C::SLOT >> 4)) | LBO_MN;
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < 8; ++s)  // 16 rows each
           tc::mma<0>(tmem + C::DQ_COL, desc(ka + ((s * 2048) >> 4)),
-                     desc((s_lo | LBO_MN) + ((s * 2048) >> 4)), ID_DQ2, (i > 0 || s > 0) ? 1u : 0u);
+                     desc((s_lo | LBO_MN) + ((s * 2048) >> 4)), ID_DQ2, (!begin || s > 0) ? 1u : 0u);
 #pragma unroll
         for (int s = 0; s < 8; ++s)
           tc::mma<0>(tmem + C::DQ_COL + 64, desc(ka + ((s * 2048) >> 4)),
                      desc((s_lo | LBO_MN) + ((2 * C::PBYTES + s * 2048) >> 4)), ID_DQ1, 1u);
         tc::mma_commit(ds_empty);
         tc::mma_commit(k_empty + (g & 1));
-        if (last) tc::mma_commit(dq_full);
+        if (end) tc::mma_commit(dq_full);
       }
       __syncwarp();
       if (last && g + 1 < total && !(ok = scores(g + 1))) break;
-      if (++i == ntile) {
-        i = 0;
-        ++qi;
-      }
+      if (++i == ntile) i = 0;
     }
-  } else {
+  } else if (warp < C::SWARPS) {
     // ---------------- softmax: TMEM lane = selected row ----------------
     const int wg = warp >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const int c0 = wg * HG, d0 = wg * DG;
+    const int c0 = wg * HG;
     const float c_scale = a.scale * kLog2e;
     auto arrive = [&](uint64_t* bar) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar);
     };
-    // add this row's d columns of an accumulator to dst
-    auto add_rows = [&](uint32_t col, float* dst, float factor) {
-#pragma unroll 1
-      for (int cc = 0; cc < DG; cc += 32) {
-        constexpr int CW = DG < 32 ? DG : 32;
-        float x[CW];
-        tmem_load(tmem + lane_off + col + d0 + cc, x);
-        if (dst) {
-#pragma unroll
-          for (int u = 0; u < CW; u += 4)
-            red_add4(dst + d0 + cc + u, x[u] * factor, x[u + 1] * factor, x[u + 2] * factor,
-                     x[u + 3] * factor);
-        }
-      }
-      tc::fence_before_sync();
-    };
-    Walk w = start, wf = start;
-    int qi = 0;
-    int e_next = total > 0 ? entry_of(w.t, row) : -1;
-    int64_t prev = -1;       // element offset of the last tile's row in dk and dv, -1: none
-    bool pend = false;       // the item before has its dQ to be read
-    int pend_nh = 0;
-    size_t pend_at = 0;
-    bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
     };
+    Walk w = start;
+    int i = 0, qi = 0;
+    int e_next = total > 0 ? entry_of(w.t, row) : -1;
 #pragma unroll 1
-    for (int g = 0; g <= total; ++g) {
-      const int s = row_of(e_next);
-      if (g < total) {
-        if (e_next != -1 && s < 0 && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-        if (g + 1 < total) {
-          walk_next(wf);
-          e_next = entry_of(wf.t, wf.i * 128 + row);
-        }
+    for (int g = 0; g < total; ++g) {
+      const bool valid = row_of(e_next) >= 0;
+      if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+      if (g + 1 < total) {
+        walk_next(w);
+        e_next = entry_of(w.t, w.i * 128 + row);
       }
-      if (g > 0) {
-        // the last tile's dV and dK, under its later products
-        const uint32_t ph = (g - 1) & 1;
-        if (!wait(dv_full, ph)) break;
-        tc::fence_after_sync();
-        add_rows(C::DV_COL, prev >= 0 ? a.dv + prev : nullptr, 1.0f);
-        arrive(dv_empty);
-        if (!wait(dk_full, ph)) break;
-        tc::fence_after_sync();
-        add_rows(C::DK_COL, prev >= 0 ? a.dk + prev : nullptr, a.scale);
-        arrive(dk_empty);
+      if (i == 0 && !wait(q_full, qi & 1)) break;
+      if (!wait(s_full, g & 1)) break;
+      tc::fence_after_sync();
+      float p[HG], ds[HG];
+      tmem_load(tmem + lane_off + C::S_COL + c0, p);
+      tmem_load(tmem + lane_off + C::DP_COL + c0, ds);
+      const float* nl = nl_s + (qi & 1) * N + c0;
+      const float* nd = nd_s + (qi & 1) * N + c0;
+#pragma unroll
+      for (int u = 0; u < HG; u += 2) {
+        fma2(p[u], p[u + 1], c_scale, nl[u], nl[u + 1]);
+        add2(ds[u], ds[u + 1], nd[u], nd[u + 1]);
       }
-      if (g < total) {
-        if (w.i == 0 && !wait(q_full, qi & 1)) break;
-        if (!wait(s_full, g & 1)) break;
-        tc::fence_after_sync();
-        float p[HG], ds[HG];
-        tmem_load(tmem + lane_off + C::S_COL + c0, p);
-        tmem_load(tmem + lane_off + C::DP_COL + c0, ds);
-        const float* nl = nl_s + (qi & 1) * N + c0;
-        const float* nd = nd_s + (qi & 1) * N + c0;
-        const bool valid = s >= 0;
+      // scores and the item's sums are read: both may be replaced
+      tc::fence_before_sync();
+      arrive(s_empty);
 #pragma unroll
-        for (int u = 0; u < HG; u += 2) {
-          fma2(p[u], p[u + 1], c_scale, nl[u], nl[u + 1]);
-          add2(ds[u], ds[u + 1], nd[u], nd[u + 1]);
-        }
-        // scores and the item's sums are read: both may be replaced
-        tc::fence_before_sync();
-        arrive(s_empty);
+      for (int u = 0; u < HG; ++u) p[u] = valid ? ex2(p[u]) : 0.0f;
 #pragma unroll
-        for (int u = 0; u < HG; ++u) p[u] = valid ? ex2(p[u]) : 0.0f;
-#pragma unroll
-        for (int u = 0; u < HG; u += 2) mul2(ds[u], ds[u + 1], p[u], p[u + 1]);
-        // (the last tile's dV, the last reader of P, is done)
-        store_parts<HG>(smem + C::P_OFF, row, c0, p);
-        tc::fence_proxy_async_smem();
-        arrive(p_full);
-        if (!valid) {
-#pragma unroll
-          for (int u = 0; u < HG; ++u) ds[u] = 0.0f;
-        }
-        if (!wait(ds_empty, (g & 1) ^ 1)) break;
-        store_parts<HG>(smem + C::S_OFF, row, c0, ds);
-        tc::fence_proxy_async_smem();
-        arrive(ds_full);
-        prev = valid ? ((int64_t)s * a.Hkv + w.hk) * D : -1;
+      for (int u = 0; u < HG; u += 2) {
+        mul2(ds[u], ds[u + 1], a.scale, a.scale);  // here, so that dQ and dK come out scaled
+        mul2(ds[u], ds[u + 1], p[u], p[u + 1]);
       }
-      // the item before: dQ^T, lane = d, the parts' two column blocks summed
-      if (pend) {
-        if (!wait(dq_full, (qi - 1) & 1)) break;
-        tc::fence_after_sync();
-        if (quad * 32 < D && c0 < pend_nh) {
-          float x[HG], y[HG];
-          tmem_load(tmem + lane_off + C::DQ_COL + c0, x);
-          tmem_load(tmem + lane_off + C::DQ_COL + 64 + c0, y);
+      // P's last reader: the dV of the tile before
+      if (g > 0 && !wait(dv_full, (g - 1) & 1)) break;
+      store_parts<HG>(smem + C::P_OFF, row, c0, p);
+      tc::fence_proxy_async_smem();
+      arrive(p_full);
+      if (!valid) {
 #pragma unroll
-          for (int u = 0; u < HG; ++u)
-            if (c0 + u < pend_nh)
-              a.dq[pend_at + (size_t)(c0 + u) * D + row] = (x[u] + y[u]) * a.scale;
-        }
-        tc::fence_before_sync();
-        arrive(dq_empty);
-        pend = false;
+        for (int u = 0; u < HG; ++u) ds[u] = 0.0f;
       }
-      if (g < total && w.i == ntile - 1) {
-        pend = true;
-        pend_nh = head_count(w);
-        pend_at = ((size_t)w.t * Hq + first_head(w)) * D;
+      if (!wait(ds_empty, (g & 1) ^ 1)) break;
+      store_parts<HG>(smem + C::S_OFF, row, c0, ds);
+      tc::fence_proxy_async_smem();
+      arrive(ds_full);
+      if (++i == ntile) {
+        i = 0;
         ++qi;
       }
-      walk_next(w);
     }
-    (void)ok;
+  } else if (warp < C::PROD_WARP) {
+    // ---------------- read-out ----------------
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    auto arrive = [&](uint64_t* bar) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
+      tc::fence_after_sync();
+      return ok;
+    };
+    // Add this warp's 32 rows of an accumulator to dst. A row per lane would send
+    // every 16 bytes of a row as a line of its own (32 lines an instruction; a line
+    // a cycle); loaded as 16 x 256 bits, four lanes hold a row's 32-byte sector and
+    // an addition covers 8 rows of 32 bytes. at[q]: this lane's element in the row
+    // of lane 8 q + lane / 4, negative if that has none.
+    int64_t at[4];
+    auto add_rows = [&](uint32_t col, float* dst) {
+#pragma unroll 1
+      for (int cc = 0; cc < D; cc += 32) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[16];
+          tmem_ld_16x256(tmem + lane_off + ((uint32_t)(half * 16) << 16) + col + cc, x);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (at[2 * half + r] >= 0) {
+              float* to = dst + at[2 * half + r] + cc;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) red_add2(to + 8 * b, x[4 * b + 2 * r], x[4 * b + 2 * r + 1]);
+            }
+          }
+        }
+      }
+    };
+    Walk w = start, wf = start;
+    int nq = 0;
+    int e_next = total > 0 ? entry_of(w.t, row) : -1;
+#pragma unroll 1
+    for (int g = 0; g < total; ++g) {
+      const int s = row_of(e_next);
+      const int64_t own = s >= 0 ? ((int64_t)s * a.Hkv + w.hk) * D : -1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t o = __shfl_sync(0xffffffffu, own, 8 * q + lane / 4);
+        at[q] = o >= 0 ? o + 2 * (lane & 3) : -1;
+      }
+      if (g + 1 < total) {
+        walk_next(wf);
+        e_next = entry_of(wf.t, wf.i * 128 + row);
+      }
+      if (!wait(dv_full, g & 1)) break;
+      add_rows(C::DV_COL, a.dv);
+      arrive(dv_empty);
+      if (!wait(dk_full, g & 1)) break;
+      add_rows(C::DK_COL, a.dk);
+      arrive(dk_empty);
+      if (w.i % kChunk == kChunk - 1 || w.i == ntile - 1) {
+        // dQ^T of the chunk, lane = d, the parts' two column blocks summed
+        if (!wait(dq_full, nq++ & 1)) break;
+        const int nh = head_count(w);
+        float* dst = a.dq + ((size_t)w.t * Hq + first_head(w)) * D + row;
+        if (quad * 32 < D) {
+#pragma unroll 1
+          for (int cc = 0; cc < nh; cc += 16) {
+            float x[16], y[16];
+            tmem_load(tmem + lane_off + C::DQ_COL + cc, x);
+            tmem_load(tmem + lane_off + C::DQ_COL + 64 + cc, y);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              if (cc + u < nh) {
+                const float v = x[u] + y[u];
+                if (w.i < kChunk) dst[(size_t)(cc + u) * D] = v;
+                else atomicAdd(dst + (size_t)(cc + u) * D, v);  // after this thread's own store
+              }
+            }
+          }
+        }
+        arrive(dq_empty);
+      }
+      w = wf;
+    }
   }
   tc::fence_before_sync();
   __syncthreads();

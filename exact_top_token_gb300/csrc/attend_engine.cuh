@@ -21,9 +21,10 @@
 // test s - m <= 64 (one vote of the warpgroup per tile), and the rare tile that
 // fails raises m and scales O and the sums.
 //
-// fp32 results: P is written as three bf16 parts (24 bits) and multiplied
-// three times; bf16 results use one part, whose rounding is of the size of the
-// result's own.
+// fp32 results: P is written as three bf16 parts (24 bits); the first two are
+// multiplied side by side (twice the columns) and the third adds to the second's,
+// so that the largest sums take one addition per 16 rows. bf16 results use one
+// part, whose rounding is of the size of the result's own.
 //
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
 //                 columns), O read-out
@@ -64,6 +65,7 @@ struct Cfg {
   static constexpr int SLOT = 128 * RB;        // one K or V tile
   static constexpr int PBYTES = NP / 64 * 16384;
   static constexpr int OBLK = D <= 128 ? 1 : D / 128;  // blocks of 128 result columns
+  static constexpr int OCOLS = F32 ? 2 * NP : NP;      // accumulator columns of a block
   static constexpr int QBYTES = N * RB;
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
   // P buffers: two, unless their three parts or 128 heads leave no room for the ring
@@ -82,7 +84,7 @@ struct Cfg {
   static constexpr int MISC_OFF = Q_OFF + QB * QBYTES;
   static constexpr int SMEM = MISC_OFF + MISC + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
-  static_assert(2 * N <= 256 && 2 * OBLK * NP <= 256, "TMEM columns");
+  static_assert(2 * N <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
   static_assert(NS >= 2 && SMEM <= 227 * 1024, "shared memory");
   static_assert(NS * SLOT >= N * D * 4, "partial results of a split item");
 };
@@ -525,6 +527,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // vector registers, which took 100 cycles per product.
     constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
     constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
+    constexpr uint32_t ID_O2 = tc::instr_desc(0, 128, C::OCOLS) | (1u << 15) | (1u << 16);
     constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
     // 14 address bits: in a cluster, shared addresses carry the CTA's rank above them
     auto low = [](const void* p) { return (tc::smem_u32(p) >> 4) & 0x3FFFu; };
@@ -585,14 +588,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
 #pragma unroll
         for (int blk = 0; blk < C::OBLK; ++blk) {
 #pragma unroll
-          for (int part = 0; part < C::PARTS; ++part) {
+          for (int part = 0; part < C::PARTS; part += 2) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)  // 16 rows each
               // d = 64 has one 64-column atom; the second one that M = 128 takes is
               // whatever follows the tile, and fills accumulator lanes never read
-              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * NP,
+              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
                          desc(ad + ((blk * 32768 + s * 2048) >> 4)),
-                         desc(bd + ((part * C::PBYTES + s * 2048) >> 4)), ID_O,
+                         desc(bd + ((part * C::PBYTES + s * 2048) >> 4)), part ? ID_O : ID_O2,
                          (wo.i > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
@@ -710,10 +713,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
             for (int u = 0; u < HG; ++u) l[u] *= f_s[c0 + u];
             if (w.i > 0) {
 #pragma unroll 1
-              for (int cc = 0; cc < C::OBLK * HG; cc += 8) {
-                const int blk = cc / HG, h = c0 + cc % HG;
+              for (int cc = 0; cc < C::OBLK * (C::OCOLS / NP) * HG; cc += 8) {
+                const int blk = cc / HG, h = c0 + cc % HG;  // NP columns from block to block
                 const uint32_t addr =
-                    tmem + lane_off + C::O_COL + ((qi & 1) * C::OBLK + blk) * NP + h;
+                    tmem + lane_off + C::O_COL + (qi & 1) * C::OBLK * C::OCOLS + blk * NP + h;
                 float o[8];
                 tmem_load(addr, o);
 #pragma unroll
@@ -778,7 +781,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         for (int blk = 0; blk < C::OBLK; ++blk) {
           const int d = blk * 128 + row;
           if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
-          tmem_load(tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * NP + c0, v);
+          const uint32_t o_addr =
+              tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
+          tmem_load(o_addr, v);
+          if constexpr (C::F32) {
+            float y[HG];
+            tmem_load(o_addr + NP, y);
+#pragma unroll
+            for (int u = 0; u < HG; ++u) v[u] += y[u];
+          }
           // a split item's part stays unnormalised: [head][d] in the ring, idle by now
           float* part = reinterpret_cast<float*>(ring) + c0 * D + d;
 #pragma unroll
