@@ -7,8 +7,8 @@
 // P = exp(S - lse) and dS = P (dP - grad . out):
 //
 //   S^T  [128 rows x N]   = K . Q^T           dP^T [128 rows x N] = V . dO^T
-//   dV   [128 rows x d]   = P^T . dO          (A: P as [row][head], K-major)
-//   dK   [128 rows x d]   = dS^T . Q
+//   dV^T [d x 128 rows]   = dO^T . P^T        (A: M = d contiguous; B: P as
+//   dK^T [d x 128 rows]   = Q^T . dS^T         [row][head], K-major)
 //   dQ^T [d x N]         += K^T . dS^T        (A: K as gathered, M = d contiguous;
 //                                              B: dS as [row][head], N contiguous)
 //
@@ -16,6 +16,11 @@
 // and their products take three terms; the other operands are bf16 as given.
 // dQ^T takes the first two parts side by side (N = 128) and adds the third to
 // the second's columns.
+//
+// The roles share one instruction cache of about 32 KB: with their loops unrolled
+// (84 KB of code) each ran several times slower than its instructions take. So
+// every loop body is there once: P and dS come from the same code in two passes
+// (the exponentials twice), the MMA issuer's steps from one loop.
 //
 // A tile's products keep the tensor core busy if a tile's softmax overlaps the
 // products of the tile before. The order is
@@ -28,10 +33,14 @@
 // steps: 2e-6 of the result). dQ^T is read out and added up in global memory
 // every kChunk tiles.
 //
-//   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
-//                 columns)
-//   4 warps       read-out: additions of dV and dK, dQ (they wait on the L2's
-//                 additions, which the softmax must not)
+// dV and dK come out with d along the lanes, so that an addition instruction
+// covers 128 consecutive bytes of one row: random rows take 6.4 TB/s of such
+// additions, 3.8 TB/s in 32-byte pieces and 3.3 TB/s in 16-byte pieces (measured
+// alone, 67 MB of rows). They are the bound: 8 d bytes per selected row and head
+// group.
+//
+//   8 warps       softmax (two warpgroups, each with half of the N head columns)
+//   8 warps       read-out: four add dV (and write dQ), four add dK
 //   4 warps       producers (cp.async); also the row sums grad . out
 //   last warp     MMA issuer, TMEM
 #pragma once
@@ -46,16 +55,16 @@ constexpr int kChunk = 4;  // tiles whose dQ is summed on the tensor core
 template <int D_, int N_>
 struct BCfg {
   static constexpr int D = D_, N = N_;
-  static constexpr int SWG = N >= 64 ? 4 : 2;
-  static constexpr int SWARPS = 4 * SWG;
-  static constexpr int HG = N / SWG;     // head columns of a warpgroup
+  static constexpr int SWARPS = 8;
+  static constexpr int HG = N / 2;             // head columns of a warpgroup
+  static constexpr int CH = HG < 16 ? HG : 16; // columns at a time
   static constexpr int RB = 2 * D;
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;  // K or V tile
   static constexpr int PBYTES = 16384;   // one part of P or dS: 128 rows x 64 heads
   static constexpr int QBYTES = N * RB;
   static constexpr int PWARPS = 4;
-  static constexpr int READ_WARP = SWARPS, PROD_WARP = SWARPS + 4;
+  static constexpr int PROD_WARP = SWARPS + 8;
   static constexpr int MMA_WARP = PROD_WARP + PWARPS;
   static constexpr int THREADS = (MMA_WARP + 1) * 32;
   static constexpr int K_OFF = 0;                 // two buffers
@@ -66,32 +75,32 @@ struct BCfg {
   static constexpr int G_OFF = Q_OFF + QBYTES;    // gradient rows
   static constexpr int MISC_OFF = G_OFF + QBYTES;
   static constexpr int MISC = 4 * N * 4 + 256;    // -lse, -grad . out [2][N]; barriers
-  static constexpr int SMEM = MISC_OFF + MISC + 1024;
+  // d = 64 has one 64-column atom; the second one that M = 128 takes is what
+  // follows in shared memory (for the gradient rows: this pad), and fills
+  // accumulator lanes never read
+  static constexpr int PAD = D == 64 ? QBYTES : 0;
+  static constexpr int SMEM = MISC_OFF + MISC + PAD + 1024;
   // TMEM columns
-  static constexpr int S_COL = 0, DP_COL = N, DV_COL = 128, DK_COL = 128 + D, DQ_COL = 384;
+  static constexpr int S_COL = 0, DP_COL = N, DV_COL = 128, DK_COL = 256, DQ_COL = 384;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(2 * N <= 128 && DK_COL + D <= DQ_COL, "TMEM columns");
+  static_assert(2 * N <= 128, "TMEM columns");
 };
 
-__device__ __forceinline__ void red_add2(float* p, float a, float b) {
-  asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(a), "f"(b)
-               : "memory");
+__device__ __forceinline__ void red_add(float* p, float v) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+// the same if row >= 0, without a branch
+__device__ __forceinline__ void red_add_if(int row, float* p, float v) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ge.s32 p, %2, 0;\n @p red.relaxed.gpu.global.add.f32 [%0], %1;\n}\n" ::"l"(p),
+      "f"(v), "r"(row)
+      : "memory");
 }
 __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
   asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
       " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
-}
-
-// 16 TMEM lanes x 32 columns of 32 bit: lane l of the warp gets, per block b of 8
-// columns, columns 2 (l % 4), + 1 of TMEM lane l / 4 (v[4b], v[4b + 1]) and of
-// lane l / 4 + 8 (v[4b + 2], v[4b + 3]).
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t addr, float (&v)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-               : "r"(addr));
-  tc::tmem_wait_ld(v);
 }
 
 // The three bf16 parts of W weights of a row, to the three part buffers.
@@ -115,7 +124,7 @@ __device__ __forceinline__ void store_parts(uint8_t* dst, int row, int c0, float
 
 template <class C, bool OUT_F32>
 __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a, const Plan pl) {
-  constexpr int D = C::D, N = C::N, HG = C::HG;
+  constexpr int D = C::D, N = C::N, HG = C::HG, CH = C::CH;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem = tc::align1024(smem_dyn);
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
   } else if (warp == C::MMA_WARP) {
     // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
     constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
-    constexpr uint32_t ID_DV = tc::instr_desc(0, 128, D) | (1u << 16);
+    constexpr uint32_t ID_DV = tc::instr_desc(0, 128, 128) | (1u << 15);
     constexpr uint32_t ID_DQ2 = tc::instr_desc(0, 128, 128) | (1u << 15) | (1u << 16);
     constexpr uint32_t ID_DQ1 = tc::instr_desc(0, 128, 64) | (1u << 15) | (1u << 16);
     constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -353,59 +362,62 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
       }
       return true;
     };
-    // D [128 rows x d] = sum over the parts of A (K-major, [row][head]) . B ([head][d])
+    // D [d x 128 rows] = sum over the parts of A ([head][d]) . B (K-major, [row][head])
     auto rows_product = [&](uint32_t col, uint32_t a_lo, uint32_t b_lo) {
 #pragma unroll
       for (int part = 0; part < 3; ++part)
 #pragma unroll
         for (int s = 0; s < N / 16; ++s)
-          tc::mma<0>(tmem + col, desc((a_lo | LBO_K) + ((part * C::PBYTES + s * 32) >> 4)),
-                     desc((b_lo | LBO_Q) + ((s * 2048) >> 4)), ID_DV, (part > 0 || s > 0) ? 1u : 0u);
+          tc::mma<0>(tmem + col, desc((a_lo | LBO_Q) + ((s * 2048) >> 4)),
+                     desc((b_lo | LBO_K) + ((part * C::PBYTES + s * 32) >> 4)), ID_DV,
+                     (part > 0 || s > 0) ? 1u : 0u);
     };
-    int i = 0, nq = 0;  // tile of its item; chunks of dQ begun
-    bool ok = total == 0 || scores(0);
+    int i = -1, nq = 0;  // tile of its item; chunks of dQ begun
+    bool ok = true;
 #pragma unroll 1
-    for (int g = 0; g < total && ok; ++g) {
+    for (int g = -1; g < total && ok; ++g) {
       const bool last = i == ntile - 1;
-      // dV
-      ok = wait(dv_empty, (g & 1) ^ 1) && wait(p_full, g & 1);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (elect_one()) {
-        rows_product(C::DV_COL, p_lo, g_lo);
-        tc::mma_commit(dv_full);
+      if (g >= 0) {
+#pragma unroll 1
+        for (int k = 0; k < 2 && ok; ++k) {  // dV, dK
+          ok = wait(k ? dk_empty : dv_empty, (g & 1) ^ 1) && wait(k ? ds_full : p_full, g & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (elect_one()) {
+            rows_product(k ? C::DK_COL : C::DV_COL, k ? q_lo : g_lo, k ? s_lo : p_lo);
+            tc::mma_commit(k ? dk_full : dv_full);
+            if (k && last) tc::mma_commit(q_empty);
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
-      // dK
-      ok = wait(dk_empty, (g & 1) ^ 1) && wait(ds_full, g & 1);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (elect_one()) {
-        rows_product(C::DK_COL, s_lo, q_lo);
-        tc::mma_commit(dk_full);
-        if (last) tc::mma_commit(q_empty);
-      }
-      __syncwarp();
-      // the next item's scores wait for its queries: not before this item's dQ
-      if (!last && !(ok = scores(g + 1))) break;
-      const bool begin = i % kChunk == 0, end = i % kChunk == kChunk - 1 || last;
-      if (begin && !(ok = wait(dq_empty, (nq++ & 1) ^ 1))) break;
-      const uint32_t ka = (k_lo + (g & 1) * (C::SLOT >> 4)) | LBO_MN;
-      if (elect_one()) {
+      // the next tile's scores, then this one's dQ; the next item's scores wait for
+      // its queries, so they come after dQ
+#pragma unroll 1
+      for (int k = 0; k < 2 && ok; ++k) {
+        if ((k == 0) != (last && g >= 0)) {
+          if (g + 1 < total) ok = scores(g + 1);
+        } else if (g >= 0) {
+          const bool begin = i % kChunk == 0, end = i % kChunk == kChunk - 1 || last;
+          if (begin && !(ok = wait(dq_empty, (nq++ & 1) ^ 1))) break;
+          const uint32_t ka = (k_lo + (g & 1) * (C::SLOT >> 4)) | LBO_MN;
+          if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s)  // 16 rows each
-          tc::mma<0>(tmem + C::DQ_COL, desc(ka + ((s * 2048) >> 4)),
-                     desc((s_lo | LBO_MN) + ((s * 2048) >> 4)), ID_DQ2, (!begin || s > 0) ? 1u : 0u);
+            for (int s = 0; s < 8; ++s)  // 16 rows each
+              tc::mma<0>(tmem + C::DQ_COL, desc(ka + ((s * 2048) >> 4)),
+                         desc((s_lo | LBO_MN) + ((s * 2048) >> 4)), ID_DQ2,
+                         (!begin || s > 0) ? 1u : 0u);
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          tc::mma<0>(tmem + C::DQ_COL + 64, desc(ka + ((s * 2048) >> 4)),
-                     desc((s_lo | LBO_MN) + ((2 * C::PBYTES + s * 2048) >> 4)), ID_DQ1, 1u);
-        tc::mma_commit(ds_empty);
-        tc::mma_commit(k_empty + (g & 1));
-        if (end) tc::mma_commit(dq_full);
+            for (int s = 0; s < 8; ++s)
+              tc::mma<0>(tmem + C::DQ_COL + 64, desc(ka + ((s * 2048) >> 4)),
+                         desc((s_lo | LBO_MN) + ((2 * C::PBYTES + s * 2048) >> 4)), ID_DQ1, 1u);
+            tc::mma_commit(ds_empty);
+            tc::mma_commit(k_empty + (g & 1));
+            if (end) tc::mma_commit(dq_full);
+          }
+          __syncwarp();
+        }
       }
-      __syncwarp();
-      if (last && g + 1 < total && !(ok = scores(g + 1))) break;
       if (++i == ntile) i = 0;
     }
   } else if (warp < C::SWARPS) {
@@ -424,6 +436,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
     };
     Walk w = start;
     int i = 0, qi = 0;
+    bool ok = true;
     int e_next = total > 0 ? entry_of(w.t, row) : -1;
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
@@ -436,46 +449,54 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
       if (i == 0 && !wait(q_full, qi & 1)) break;
       if (!wait(s_full, g & 1)) break;
       tc::fence_after_sync();
-      float p[HG], ds[HG];
-      tmem_load(tmem + lane_off + C::S_COL + c0, p);
-      tmem_load(tmem + lane_off + C::DP_COL + c0, ds);
       const float* nl = nl_s + (qi & 1) * N + c0;
       const float* nd = nd_s + (qi & 1) * N + c0;
+      // pass 0: P, once its last reader, the dV of the tile before, is done;
+      // pass 1: dS, once the dQ of the tile before is
+#pragma unroll 1
+      for (int pass = 0; pass < 2 && ok; ++pass) {
+        if (g > 0) ok = wait(pass ? ds_empty : dv_full, (g - 1) & 1);
+        uint8_t* dst = smem + (pass ? C::S_OFF : C::P_OFF);
+#pragma unroll 1
+        for (int cc = 0; cc < HG; cc += CH) {
+          float p[CH];
+          tmem_load(tmem + lane_off + C::S_COL + c0 + cc, p);
 #pragma unroll
-      for (int u = 0; u < HG; u += 2) {
-        fma2(p[u], p[u + 1], c_scale, nl[u], nl[u + 1]);
-        add2(ds[u], ds[u + 1], nd[u], nd[u + 1]);
+          for (int u = 0; u < CH; u += 2) {
+            fma2(p[u], p[u + 1], c_scale, nl[cc + u], nl[cc + u + 1]);
+            p[u] = valid ? ex2(p[u]) : 0.0f;
+            p[u + 1] = valid ? ex2(p[u + 1]) : 0.0f;
+          }
+          if (pass) {
+            float dp[CH];
+            tmem_load(tmem + lane_off + C::DP_COL + c0 + cc, dp);
+#pragma unroll
+            for (int u = 0; u < CH; u += 2) {
+              add2(dp[u], dp[u + 1], nd[cc + u], nd[cc + u + 1]);
+              mul2(dp[u], dp[u + 1], a.scale, a.scale);  // here, so that dQ and dK come out scaled
+              mul2(dp[u], dp[u + 1], p[u], p[u + 1]);
+              p[u] = valid ? dp[u] : 0.0f;  // (0 x NaN of a gradient is none of this row's)
+              p[u + 1] = valid ? dp[u + 1] : 0.0f;
+            }
+          }
+          store_parts<CH>(dst, row, c0 + cc, p);
+        }
+        tc::fence_proxy_async_smem();
+        if (pass) {
+          // scores and the item's sums are read: both may be replaced
+          tc::fence_before_sync();
+          arrive(s_empty);
+        }
+        arrive(pass ? ds_full : p_full);
       }
-      // scores and the item's sums are read: both may be replaced
-      tc::fence_before_sync();
-      arrive(s_empty);
-#pragma unroll
-      for (int u = 0; u < HG; ++u) p[u] = valid ? ex2(p[u]) : 0.0f;
-#pragma unroll
-      for (int u = 0; u < HG; u += 2) {
-        mul2(ds[u], ds[u + 1], a.scale, a.scale);  // here, so that dQ and dK come out scaled
-        mul2(ds[u], ds[u + 1], p[u], p[u + 1]);
-      }
-      // P's last reader: the dV of the tile before
-      if (g > 0 && !wait(dv_full, (g - 1) & 1)) break;
-      store_parts<HG>(smem + C::P_OFF, row, c0, p);
-      tc::fence_proxy_async_smem();
-      arrive(p_full);
-      if (!valid) {
-#pragma unroll
-        for (int u = 0; u < HG; ++u) ds[u] = 0.0f;
-      }
-      if (!wait(ds_empty, (g & 1) ^ 1)) break;
-      store_parts<HG>(smem + C::S_OFF, row, c0, ds);
-      tc::fence_proxy_async_smem();
-      arrive(ds_full);
+      if (!ok) break;
       if (++i == ntile) {
         i = 0;
         ++qi;
       }
     }
   } else if (warp < C::PROD_WARP) {
-    // ---------------- read-out ----------------
+    // ---------------- read-out: TMEM lane = d ----------------
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -489,54 +510,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
       tc::fence_after_sync();
       return ok;
     };
-    // Add this warp's 32 rows of an accumulator to dst. A row per lane would send
-    // every 16 bytes of a row as a line of its own (32 lines an instruction; a line
-    // a cycle); loaded as 16 x 256 bits, four lanes hold a row's 32-byte sector and
-    // an addition covers 8 rows of 32 bytes. at[q]: this lane's element in the row
-    // of lane 8 q + lane / 4, negative if that has none.
-    int64_t at[4];
-    auto add_rows = [&](uint32_t col, float* dst) {
+    const bool is_dk = warp >= C::SWARPS + 4;
+    uint64_t* full = is_dk ? dk_full : dv_full;
+    uint64_t* empty = is_dk ? dk_empty : dv_empty;
+    const uint32_t addr = tmem + lane_off + (is_dk ? C::DK_COL : C::DV_COL);
+    const int64_t stride = (int64_t)a.Hkv * D;
+    Walk w = start, wf = start;
+    int nq = 0;
+    int e_next = total > 0 ? entry_of(w.t, lane) : -1;  // of the next 32 rows
 #pragma unroll 1
-      for (int cc = 0; cc < D; cc += 32) {
+    for (int g = 0; g < total; ++g) {
+      walk_next(wf);
+      if (!wait(full, g & 1)) break;
+      float* dst = (is_dk ? a.dk : a.dv) + (size_t)w.hk * D + row;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const int s = row_of(e_next);
+        if (q < 3) e_next = entry_of(w.t, w.i * 128 + 32 * (q + 1) + lane);
+        else if (g + 1 < total) e_next = entry_of(wf.t, wf.i * 128 + lane);
+        if (quad * 32 < D) {
+          float x[32];
+          tmem_load(addr + 32 * q, x);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[16];
-          tmem_ld_16x256(tmem + lane_off + ((uint32_t)(half * 16) << 16) + col + cc, x);
+          for (int b = 0; b < 32; b += 8) {
+            int r[8];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (at[2 * half + r] >= 0) {
-              float* to = dst + at[2 * half + r] + cc;
+            for (int u = 0; u < 8; ++u) r[u] = __shfl_sync(0xffffffffu, s, b + u);
 #pragma unroll
-              for (int b = 0; b < 4; ++b) red_add2(to + 8 * b, x[4 * b + 2 * r], x[4 * b + 2 * r + 1]);
-            }
+            for (int u = 0; u < 8; ++u) red_add_if(r[u], dst + r[u] * stride, x[b + u]);
           }
         }
       }
-    };
-    Walk w = start, wf = start;
-    int nq = 0;
-    int e_next = total > 0 ? entry_of(w.t, row) : -1;
-#pragma unroll 1
-    for (int g = 0; g < total; ++g) {
-      const int s = row_of(e_next);
-      const int64_t own = s >= 0 ? ((int64_t)s * a.Hkv + w.hk) * D : -1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t o = __shfl_sync(0xffffffffu, own, 8 * q + lane / 4);
-        at[q] = o >= 0 ? o + 2 * (lane & 3) : -1;
-      }
-      if (g + 1 < total) {
-        walk_next(wf);
-        e_next = entry_of(wf.t, wf.i * 128 + row);
-      }
-      if (!wait(dv_full, g & 1)) break;
-      add_rows(C::DV_COL, a.dv);
-      arrive(dv_empty);
-      if (!wait(dk_full, g & 1)) break;
-      add_rows(C::DK_COL, a.dk);
-      arrive(dk_empty);
-      if (w.i % kChunk == kChunk - 1 || w.i == ntile - 1) {
-        // dQ^T of the chunk, lane = d, the parts' two column blocks summed
+      arrive(empty);
+      if (!is_dk && (w.i % kChunk == kChunk - 1 || w.i == ntile - 1)) {
+        // dQ^T of the chunk, the parts' two column blocks summed
         if (!wait(dq_full, nq++ & 1)) break;
         const int nh = head_count(w);
         float* dst = a.dq + ((size_t)w.t * Hq + first_head(w)) * D + row;
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
               if (cc + u < nh) {
                 const float v = x[u] + y[u];
                 if (w.i < kChunk) dst[(size_t)(cc + u) * D] = v;
-                else atomicAdd(dst + (size_t)(cc + u) * D, v);  // after this thread's own store
+                else red_add(dst + (size_t)(cc + u) * D, v);  // after this thread's own store
               }
             }
           }
