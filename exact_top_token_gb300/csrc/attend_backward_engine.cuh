@@ -90,7 +90,7 @@ __device__ __forceinline__ void red_add(float* p, float v) {
   asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
 // the same if row >= 0, without a branch
-__device__ __forceinline__ void red_add_if(int row, float* p, float v) {
+__device__ __forceinline__ void red_add_if(int row, void* p, float v) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ge.s32 p, %2, 0;\n @p red.relaxed.gpu.global.add.f32 [%0], %1;\n}\n" ::"l"(p),
       "f"(v), "r"(row)
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
     uint64_t* full = is_dk ? dk_full : dv_full;
     uint64_t* empty = is_dk ? dk_empty : dv_empty;
     const uint32_t addr = tmem + lane_off + (is_dk ? C::DK_COL : C::DV_COL);
-    const int64_t stride = (int64_t)a.Hkv * D;
+    const uint32_t stride = (uint32_t)a.Hkv * D * 4;  // bytes of a row of dk and dv
     Walk w = start, wf = start;
     int nq = 0;
     int e_next = total > 0 ? entry_of(w.t, lane) : -1;  // of the next 32 rows
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
     for (int g = 0; g < total; ++g) {
       walk_next(wf);
       if (!wait(full, g & 1)) break;
-      float* dst = (is_dk ? a.dk : a.dv) + (size_t)w.hk * D + row;
+      uint8_t* dst = reinterpret_cast<uint8_t*>((is_dk ? a.dk : a.dv) + (size_t)w.hk * D + row);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         const int s = row_of(e_next);
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
 #pragma unroll
             for (int u = 0; u < 8; ++u) r[u] = __shfl_sync(0xffffffffu, s, b + u);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) red_add_if(r[u], dst + r[u] * stride, x[b + u]);
+            for (int u = 0; u < 8; ++u)  // 32 x 32 + 64 bits: one instruction an address
+              red_add_if(r[u], dst + (uint64_t)(uint32_t)r[u] * stride, x[b + u]);
           }
         }
       }
