@@ -139,7 +139,7 @@ def load(path: str | None = None):
     lib.hytopk_attend.argtypes = [P, S, P, S, P, P, S, P, P, I, I, I, I, I, I, I, F, P, I, P, P, P]
     lib.hytopk_attend_backward.restype = I
     lib.hytopk_attend_backward.argtypes = [P, S, P, S, P, S, P, P, I, P, P, I, I, I, I, I, I, F, P,
-                                           P, P, P, P]
+                                           P, P, I, P, P]
     lib.hytopk_sample_plan.restype = ctypes.c_int32
     lib.hytopk_sample_plan.argtypes = [ctypes.c_int64, ctypes.c_int32, P, P]
     lib.hytopk_status_string.restype = ctypes.c_char_p
@@ -516,12 +516,31 @@ def select_twopass(q, k, w, positions, k_top, *, q_scale=None, k_scale=None, row
 
 
 # ---- around the selection: rotary positions, cache rows, attention ------------------
+# These calls also serve single tokens, where the time is the host's: their checks
+# read each attribute once, and the current stream's handle comes without a stream
+# object (a call costs 8 to 12 us instead of 20 to 28).
 
-def _elem(name, t, allowed):
+_elems = {}  # torch dtype -> ELEM_*, filled on first use
+_raw_current = None
+
+
+def _fast_init():
+    global _raw_current
     import torch
 
-    code = {torch.bfloat16: ELEM_BF16, torch.float32: ELEM_F32, torch.float8_e4m3fn: ELEM_E4M3,
-            torch.uint8: ELEM_E4M3}.get(t if isinstance(t, torch.dtype) else t.dtype)
+    _elems.update({torch.bfloat16: ELEM_BF16, torch.float32: ELEM_F32,
+                   torch.float8_e4m3fn: ELEM_E4M3, torch.uint8: ELEM_E4M3})
+    _raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return load()
+
+
+def _stream_handle(device, stream):
+    return _raw_current(device.index) if stream is None else stream.cuda_stream
+
+
+def _elem(name, dtype, allowed):
+    code = _elems.get(dtype)
     if code not in allowed:
         names = {ELEM_BF16: "bfloat16", ELEM_F32: "float32", ELEM_E4M3: "float8_e4m3fn"}
         raise TypeError(f"{name} must be " + " or ".join(names[a] for a in allowed))
@@ -529,31 +548,44 @@ def _elem(name, t, allowed):
 
 
 def _need(name, t, device, dtype, shape):
-    """A contiguous tensor of this type and shape on this device."""
+    """A contiguous tensor of this type and shape on this device; its pointer."""
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         _check_tensor(name, t, device, dtype, shape)
         raise ValueError(f"{name}: wrong tensor")
+    return t.data_ptr()
 
 
-def _rows3(name, t):
-    """t as [rows, heads, d] (a 2-D tensor has one head) with its last axis contiguous."""
-    if t.dim() == 2:
-        t = t.unsqueeze(1)
-    if t.dim() != 3:
+def _rows(name, t):
+    """(rows, heads, d, row stride, head stride) of [rows, heads, d] or [rows, d],
+    in elements. A stride of an axis of length 1 is never used and is replaced by
+    a packed one."""
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        n, H, d = shape
+        row, head, last = st
+    elif len(shape) == 2:
+        n, d = shape
+        H, head = 1, d
+        row, last = st
+    else:
         raise ValueError(f"{name} must be [rows, heads, d] or [rows, d]")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if last != 1 and d > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    return t
+    if H == 1:
+        head = d
+    if n <= 1:
+        row = H * head
+    return n, H, d, row, head
 
 
-def _row_strides(t):
-    """(row, head) strides in elements; those of axes of length 1 are never used
-    and any value torch gives them is replaced by a packed one."""
-    n, H, d = t.shape
-    head = t.stride(1) if H > 1 else d
-    return (t.stride(0) if n > 1 else H * head), head
+def _packed_rows(name, t):
+    """_rows of a tensor whose heads are contiguous within a row."""
+    n, H, d, row, head = _rows(name, t)
+    if head != d:
+        raise ValueError(f"{name}: heads must be contiguous within a row")
+    return n, H, d, row
 
 
 def _status_ptr(status, device):
@@ -562,12 +594,6 @@ def _status_ptr(status, device):
     if status.element_size() != 4 or status.numel() < 1 or status.device != device:
         raise ValueError("status must be a 32-bit integer tensor on the inputs' device")
     return status.data_ptr()
-
-
-def _raw_stream(device, stream):
-    import torch
-
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
 def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_context=None,
@@ -612,13 +638,12 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_co
 def _rope_params(positions, inv_freq, n, device, first, interleaved, inverse, mscale):
     import torch
 
-    _need("positions", positions, device, torch.int32, (n,))
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot / 2]")
-    _need("inv_freq", inv_freq, device, torch.float32, (inv_freq.shape[0],))
-    return ctypes.byref(RopeParams(positions.data_ptr(), inv_freq.data_ptr(),
-                                   2 * inv_freq.shape[0], first, bool(interleaved), bool(inverse),
-                                   mscale))
+    pairs = inv_freq.shape[0]
+    return ctypes.byref(RopeParams(_need("positions", positions, device, torch.int32, (n,)),
+                                   _need("inv_freq", inv_freq, device, torch.float32, (pairs,)),
+                                   2 * pairs, first, bool(interleaved), bool(inverse), mscale))
 
 
 def rope(x, positions, inv_freq, *, first=0, interleaved=False, mscale=1.0, inverse=False,
@@ -630,38 +655,39 @@ def rope(x, positions, inv_freq, *, first=0, interleaved=False, mscale=1.0, inve
     is also the gradient. See :func:`rope_frequencies`."""
     import torch
 
-    lib = load()
-    x3 = _rows3("x", x)
-    n, H, d = x3.shape
-    dev = x.device
-    code = _elem("x", x, (ELEM_BF16, ELEM_F32))
+    lib = _lib if _elems else _fast_init()
+    n, H, d, row, head = _rows("x", x)
+    dev, dtype = x.device, x.dtype
+    code = _elem("x", dtype, (ELEM_BF16, ELEM_F32))
     params = _rope_params(positions, inv_freq, n, dev, first, interleaved, inverse, mscale)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
-        raise ValueError("out must match x in shape, type and device")
-    o3 = _rows3("out", out)
-    xr, xh = _row_strides(x3)
-    orow, oh = _row_strides(o3)
-    st = lib.hytopk_rope(x3.data_ptr(), xr, xh, code, n, H, d, params, o3.data_ptr(), orow, oh,
-                         _status_ptr(status, dev), _raw_stream(dev, stream))
+        out = torch.empty(x.shape, dtype=dtype, device=dev)
+        orow, ohead = H * d, d
+    else:
+        if out.shape != x.shape or out.dtype != dtype or out.device != dev:
+            raise ValueError("out must match x in shape, type and device")
+        _, _, _, orow, ohead = _rows("out", out)
+    st = lib.hytopk_rope(x.data_ptr(), row, head, code, n, H, d, params, out.data_ptr(), orow,
+                         ohead, _status_ptr(status, dev), _stream_handle(dev, stream))
     if st != 0:
         raise HytopkError(st, "hytopk_rope")
     return out
 
 
-def _cache3(cache, cache_scale):
+def _cache(cache, cache_scale):
+    """(rows, heads, d, ELEM_*, scale pointer) of a contiguous cache."""
     import torch
 
-    c3 = _rows3("cache", cache)
+    L, H, d, _, _ = _rows("cache", cache)
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
-    code = _elem("cache", cache, (ELEM_E4M3, ELEM_BF16))
+    code = _elem("cache", cache.dtype, (ELEM_E4M3, ELEM_BF16))
     if (code == ELEM_E4M3) != (cache_scale is not None):
         raise ValueError("an e4m3 cache needs cache_scale, a bf16 cache takes none")
+    scale = None
     if cache_scale is not None:
-        _need("cache_scale", cache_scale, cache.device, torch.float32, cache.shape[:-1])
-    return c3, code
+        scale = _need("cache_scale", cache_scale, cache.device, torch.float32, cache.shape[:-1])
+    return L, H, d, code, scale
 
 
 def cache_write(x, cache, cache_scale=None, *, slots=None, positions=None, inv_freq=None, first=0,
@@ -673,27 +699,22 @@ def cache_write(x, cache, cache_scale=None, *, slots=None, positions=None, inv_f
     ``cache_scale``, as :func:`select` and :func:`attend` take them."""
     import torch
 
-    lib = load()
-    x3 = _rows3("x", x)
-    n, H, d = x3.shape
+    lib = _lib if _elems else _fast_init()
+    n, H, d, row, head = _rows("x", x)
     dev = x.device
-    code = _elem("x", x, (ELEM_BF16, ELEM_F32))
-    c3, ccode = _cache3(cache, cache_scale)
-    if cache.device != dev or c3.shape[1:] != (H, d):
-        raise ValueError(f"cache rows are {tuple(c3.shape[1:])} on {cache.device}, expected "
-                         f"{(H, d)} on {dev}")
+    code = _elem("x", x.dtype, (ELEM_BF16, ELEM_F32))
+    L, cH, cd, ccode, scale = _cache(cache, cache_scale)
+    if cache.device != dev or cH != H or cd != d:
+        raise ValueError(f"cache rows are {(cH, cd)} on {cache.device}, expected {(H, d)} on {dev}")
     params = None
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
     if positions is not None:
         params = _rope_params(positions, inv_freq, n, dev, first, interleaved, False, mscale)
-    if slots is not None:
-        _need("slots", slots, dev, torch.int32, (n,))
-    xr, xh = _row_strides(x3)
-    st = lib.hytopk_cache_write(x3.data_ptr(), xr, xh, code, n, H, d, params,
-                                None if slots is None else slots.data_ptr(), c3.data_ptr(), ccode,
-                                None if cache_scale is None else cache_scale.data_ptr(),
-                                c3.shape[0], _status_ptr(status, dev), _raw_stream(dev, stream))
+    at = None if slots is None else _need("slots", slots, dev, torch.int32, (n,))
+    st = lib.hytopk_cache_write(x.data_ptr(), row, head, code, n, H, d, params, at,
+                                cache.data_ptr(), ccode, scale, L, _status_ptr(status, dev),
+                                _stream_handle(dev, stream))
     if st != 0:
         raise HytopkError(st, "hytopk_cache_write")
     return cache
@@ -704,40 +725,27 @@ def cache_read(cache, cache_scale=None, *, slots=None, dtype=None, out=None, sta
     """Cache rows ``slots`` (int32 [m]; None: all) as bf16 (default) or fp32."""
     import torch
 
-    lib = load()
-    c3, ccode = _cache3(cache, cache_scale)
-    dev = cache.device
-    L, H, d = c3.shape
-    n = L
+    lib = _lib if _elems else _fast_init()
+    n, H, d, ccode, scale = _cache(cache, cache_scale)
+    L, dev, at = n, cache.device, None
     if slots is not None:
         n = slots.shape[0]
-        _need("slots", slots, dev, torch.int32, (n,))
+        at = _need("slots", slots, dev, torch.int32, (n,))
     shape = (n,) + tuple(cache.shape[1:])
     if out is None:
         out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
     else:
         _need("out", out, dev, dtype or out.dtype, shape)
-    code = _elem("dtype", out, (ELEM_BF16, ELEM_F32))
-    st = lib.hytopk_cache_read(c3.data_ptr(), ccode,
-                               None if cache_scale is None else cache_scale.data_ptr(), L,
-                               None if slots is None else slots.data_ptr(), n, H, d,
-                               out.data_ptr(), code, _status_ptr(status, dev),
-                               _raw_stream(dev, stream))
+    code = _elem("dtype", out.dtype, (ELEM_BF16, ELEM_F32))
+    st = lib.hytopk_cache_read(cache.data_ptr(), ccode, scale, L, at, n, H, d, out.data_ptr(),
+                               code, _status_ptr(status, dev), _stream_handle(dev, stream))
     if st != 0:
         raise HytopkError(st, "hytopk_cache_read")
     return out
 
 
-def _packed_heads(name, t):
-    t = _rows3(name, t)
-    n, H, d = t.shape
-    row, head = _row_strides(t)
-    if H > 1 and head != d:
-        raise ValueError(f"{name}: heads must be contiguous within a row")
-    return t, row
-
-
 def _attention(q, k, v, idx):
+    """Shapes and row strides of the attention's inputs, checked."""
     import torch
 
     if q.dtype != torch.bfloat16:
@@ -745,17 +753,16 @@ def _attention(q, k, v, idx):
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have one shape and type")
     dev = q.device
-    q, q_row = _packed_heads("q", q)
-    k, k_row = _packed_heads("k", k)
-    v, v_row = _packed_heads("v", v)
-    n, Hq, d = q.shape
-    L, Hkv, dk = k.shape
+    n, Hq, d, q_row = _packed_rows("q", q)
+    L, Hkv, dk, k_row = _packed_rows("k", k)
+    v_row = _packed_rows("v", v)[3]
     if dk != d or k.device != dev or v.device != dev:
         raise ValueError(f"k and v rows must be [{d}] per head on {dev}")
     if idx.dim() != 2:
         raise ValueError("idx must be [n, k]")
-    _need("idx", idx, dev, torch.int32, (n, idx.shape[1]))
-    return q, q_row, k, k_row, v, v_row, n, L, Hq, Hkv, d, idx.shape[1], dev
+    k_top = idx.shape[1]
+    return dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, \
+        _need("idx", idx, dev, torch.int32, (n, k_top))
 
 
 def attend(q, k, v, idx, *, k_scale=None, v_scale=None, scale=None, out_dtype=None, out=None,
@@ -768,26 +775,26 @@ def attend(q, k, v, idx, *, k_scale=None, v_scale=None, scale=None, out_dtype=No
     :func:`attend_backward` then keeps fp32 accuracy)."""
     import torch
 
-    lib = load()
-    code = _elem("k", k, (ELEM_BF16, ELEM_E4M3))
+    lib = _lib if _elems else _fast_init()
+    code = _elem("k", k.dtype, (ELEM_BF16, ELEM_E4M3))
+    dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, at = _attention(q, k, v, idx)
     if (code == ELEM_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
         raise ValueError("an e4m3 cache needs k_scale and v_scale, a bf16 cache takes none")
+    ks = vs = None
     if k_scale is not None:
-        _need("k_scale", k_scale, q.device, torch.float32, k.shape[:-1])
-        _need("v_scale", v_scale, q.device, torch.float32, v.shape[:-1])
-    q3, qr, k3, kr, v3, vr, n, L, Hq, Hkv, d, k_top, dev = _attention(q, k, v, idx)
+        shape = k.shape[:-1]
+        ks = _need("k_scale", k_scale, dev, torch.float32, shape)
+        vs = _need("v_scale", v_scale, dev, torch.float32, shape)
     if out is None:
         out = torch.empty((n, Hq, d), dtype=out_dtype or torch.bfloat16, device=dev)
     else:
         _need("out", out, dev, out_dtype or out.dtype, (n, Hq, d))
-    ocode = _elem("out_dtype", out, (ELEM_BF16, ELEM_F32))
+    ocode = _elem("out_dtype", out.dtype, (ELEM_BF16, ELEM_F32))
     lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
-    st = lib.hytopk_attend(q3.data_ptr(), qr, k3.data_ptr(), kr,
-                           None if k_scale is None else k_scale.data_ptr(), v3.data_ptr(), vr,
-                           None if v_scale is None else v_scale.data_ptr(), idx.data_ptr(), n, L,
-                           Hq, Hkv, d, k_top, code, d ** -0.5 if scale is None else scale,
-                           out.data_ptr(), ocode, lse.data_ptr(), _status_ptr(status, dev),
-                           _raw_stream(dev, stream))
+    st = lib.hytopk_attend(q.data_ptr(), q_row, k.data_ptr(), k_row, ks, v.data_ptr(), v_row, vs,
+                           at, n, L, Hq, Hkv, d, k_top, code,
+                           d ** -0.5 if scale is None else scale, out.data_ptr(), ocode,
+                           lse.data_ptr(), _status_ptr(status, dev), _stream_handle(dev, stream))
     if st != 0:
         raise HytopkError(st, "hytopk_attend")
     return out, lse
@@ -797,31 +804,32 @@ def attend_backward(q, k, v, idx, out, lse, grad, *, scale=None, dk=None, dv=Non
                     stream=None):
     """Gradients of :func:`attend` (bf16 k and v): ``(dq [n, Hq, d], dk, dv)``
     in fp32, dk and dv shaped like k. ``grad`` [n, Hq, d] bf16 is the gradient
-    of out. ``dk`` / ``dv`` are added to when given (else zeroed tensors)."""
+    of out. ``dk`` and ``dv`` are added to when given (both or neither; else new
+    tensors are written)."""
     import torch
 
-    lib = load()
-    q3, qr, k3, kr, v3, vr, n, L, Hq, Hkv, d, k_top, dev = _attention(q, k, v, idx)
-    _elem("k", k, (ELEM_BF16,))
-    _need("grad", grad, dev, torch.bfloat16, (n, Hq, d))
-    _need("out", out, dev, out.dtype, (n, Hq, d))
-    _need("lse", lse, dev, torch.float32, (n, Hq))
-    ocode = _elem("out", out, (ELEM_BF16, ELEM_F32))
+    lib = _lib if _elems else _fast_init()
+    _elem("k", k.dtype, (ELEM_BF16,))
+    dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, at = _attention(q, k, v, idx)
+    go = _need("grad", grad, dev, torch.bfloat16, (n, Hq, d))
+    o = _need("out", out, dev, out.dtype, (n, Hq, d))
+    le = _need("lse", lse, dev, torch.float32, (n, Hq))
+    ocode = _elem("out", out.dtype, (ELEM_BF16, ELEM_F32))
     dq = torch.empty((n, Hq, d), dtype=torch.float32, device=dev)
-    if dk is None:
-        dk = torch.zeros(k.shape, dtype=torch.float32, device=dev)
-    else:
+    add = dk is not None
+    if add != (dv is not None):
+        raise ValueError("dk and dv go together")
+    if add:
         _need("dk", dk, dev, torch.float32, k.shape)
-    if dv is None:
-        dv = torch.zeros(v.shape, dtype=torch.float32, device=dev)
-    else:
         _need("dv", dv, dev, torch.float32, v.shape)
-    st = lib.hytopk_attend_backward(q3.data_ptr(), qr, k3.data_ptr(), kr, v3.data_ptr(), vr,
-                                    idx.data_ptr(), out.data_ptr(), ocode, lse.data_ptr(),
-                                    grad.data_ptr(), n, L, Hq, Hkv, d, k_top,
+    else:
+        dk = torch.empty(k.shape, dtype=torch.float32, device=dev)
+        dv = torch.empty(v.shape, dtype=torch.float32, device=dev)
+    st = lib.hytopk_attend_backward(q.data_ptr(), q_row, k.data_ptr(), k_row, v.data_ptr(), v_row,
+                                    at, o, ocode, le, go, n, L, Hq, Hkv, d, k_top,
                                     d ** -0.5 if scale is None else scale, dq.data_ptr(),
-                                    dk.data_ptr(), dv.data_ptr(), _status_ptr(status, dev),
-                                    _raw_stream(dev, stream))
+                                    dk.data_ptr(), dv.data_ptr(), add, _status_ptr(status, dev),
+                                    _stream_handle(dev, stream))
     if st != 0:
         raise HytopkError(st, "hytopk_attend_backward")
     return dq, dk, dv

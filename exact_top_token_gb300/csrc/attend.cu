@@ -92,18 +92,26 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
                                                 hytopk_elem out_type, const float* lse,
                                                 const void* grad, int n, int L, int Hq, int Hkv,
                                                 int d, int k_top, float scale, float* dq,
-                                                float* dk, float* dv, uint32_t* dev_status,
-                                                cudaStream_t stream) {
+                                                float* dk, float* dv, int accumulate,
+                                                uint32_t* dev_status, cudaStream_t stream) {
   hytopk_status s = att::check(n, L, Hq, Hkv, d, k_top, out_type, false);
   if (s != HYTOPK_OK) return s;
-  if (n == 0) return HYTOPK_OK;
-  if (!q || !k || !v || !idx || !out || !lse || !grad || !dq || !dk || !dv)
-    return HYTOPK_INVALID_ARG;
+  if (n == 0 && accumulate) return HYTOPK_OK;
+  if (!dk || !dv) return HYTOPK_INVALID_ARG;
+  if (n > 0 && (!q || !k || !v || !idx || !out || !lse || !grad || !dq)) return HYTOPK_INVALID_ARG;
   if (!att::aligned(q, 16) || !att::aligned(k, 16) || !att::aligned(v, 16) ||
       !att::aligned(out, 16) || !att::aligned(grad, 16) || !att::aligned(dq, 16) ||
       !att::aligned(dk, 16) || !att::aligned(dv, 16) || !att::aligned(idx, 4) ||
       !att::aligned(lse, 4) || q_row % 8 || k_row % 8 || v_row % 8)
     return HYTOPK_MISALIGNED;
+  if (!accumulate) {
+    const size_t bytes = (size_t)L * Hkv * d * sizeof(float);
+    const bool one = dv == dk + (size_t)L * Hkv * d;  // one block: one call
+    if (cudaMemsetAsync(dk, 0, one ? 2 * bytes : bytes, stream) != cudaSuccess ||
+        (!one && cudaMemsetAsync(dv, 0, bytes, stream) != cudaSuccess))
+      return HYTOPK_CUDA_ERROR;
+    if (n == 0) return HYTOPK_OK;
+  }
   att::Args a{};
   a.q = q;
   a.q_row = q_row;

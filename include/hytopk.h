@@ -519,8 +519,10 @@ HYTOPK_API hytopk_status hytopk_attend(const void* q, int64_t q_row, const void*
 /* Gradients of hytopk_attend for bf16 k and v. With p[j] = exp(s[j] - lse),
  * dp[j] = grad[t,h] . v[idx[t,j]] and ds[j] = p[j] (dp[j] - grad[t,h] . out[t,h]):
  *   dq [n, Hq, d]  fp32, written:  scale * sum_j ds[j] k[idx[t,j]]
- *   dk [L, Hkv, d] fp32, ADDED TO: scale * ds[j] q[t,h], summed over the group's heads
- *   dv [L, Hkv, d] fp32, ADDED TO: p[j] grad[t,h], summed over the group's heads
+ *   dk [L, Hkv, d] fp32: scale * ds[j] q[t,h], summed over the group's heads
+ *   dv [L, Hkv, d] fp32: p[j] grad[t,h], summed over the group's heads
+ *   accumulate  nonzero: dk and dv are ADDED TO; 0: they are written (set to
+ *       zero first, on the stream)
  *   out (bf16 or fp32; the fp32 result keeps the gradients at fp32 accuracy)
  *   and lse are hytopk_attend's; grad [n, Hq, d] bf16 contiguous.
  * p and ds enter the tensor cores as the sum of three bf16 parts (24 bits);
@@ -534,8 +536,8 @@ HYTOPK_API hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
                                                 hytopk_elem out_type, const float* lse,
                                                 const void* grad, int n, int L, int Hq, int Hkv,
                                                 int d, int k_top, float scale, float* dq,
-                                                float* dk, float* dv, uint32_t* dev_status,
-                                                cudaStream_t stream);
+                                                float* dk, float* dv, int accumulate,
+                                                uint32_t* dev_status, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 HYTOPK_API const char* hytopk_status_string(hytopk_status status);

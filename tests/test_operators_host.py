@@ -132,12 +132,12 @@ def test_attend_checks(lib):
 def test_attend_backward_checks(lib):
     def call(**kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, idx=FAKE, out=FAKE, ot=2, lse=FAKE, grad=FAKE, n=4, L=100,
-                 Hq=8, Hkv=2, d=64, k_top=10, dq=FAKE, dk=FAKE, dv=FAKE)
+                 Hq=8, Hkv=2, d=64, k_top=10, dq=FAKE, dk=FAKE, dv=FAKE, add=1)
         a.update(kw)
         return lib.hytopk_attend_backward(a["q"], 512, a["k"], 128, a["v"], 128, a["idx"], a["out"],
                                           a["ot"], a["lse"], a["grad"], a["n"], a["L"], a["Hq"],
                                           a["Hkv"], a["d"], a["k_top"], 0.125, a["dq"], a["dk"],
-                                          a["dv"], None, None)
+                                          a["dv"], a["add"], None, None)
 
     for name in ("q", "k", "v", "idx", "out", "lse", "grad", "dq", "dk", "dv"):
         assert call(**{name: None}) == 1, name
