@@ -106,9 +106,8 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
     return HYTOPK_MISALIGNED;
   if (!accumulate) {
     const size_t bytes = (size_t)L * Hkv * d * sizeof(float);
-    const bool one = dv == dk + (size_t)L * Hkv * d;  // one block: one call
-    if (cudaMemsetAsync(dk, 0, one ? 2 * bytes : bytes, stream) != cudaSuccess ||
-        (!one && cudaMemsetAsync(dv, 0, bytes, stream) != cudaSuccess))
+    if (cudaMemsetAsync(dk, 0, bytes, stream) != cudaSuccess ||
+        cudaMemsetAsync(dv, 0, bytes, stream) != cudaSuccess)
       return HYTOPK_CUDA_ERROR;
     if (n == 0) return HYTOPK_OK;
   }
