@@ -96,12 +96,6 @@ __device__ __forceinline__ void red_add_if(int row, void* p, float v) {
       "f"(v), "r"(row)
       : "memory");
 }
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
-      " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
-}
 
 // The three bf16 parts of W weights of a row, to the three part buffers.
 template <int W>

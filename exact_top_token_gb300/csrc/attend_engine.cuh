@@ -26,9 +26,20 @@
 // so that the largest sums take one addition per 16 rows. bf16 results use one
 // part, whose rounding is of the size of the result's own.
 //
+// e4m3 rows of 128 columns with a bf16 result stay as they are in memory
+// (Cfg::F8): q and P are each written as an e4m3 part and an e4m3 part of 16
+// times the rest, side by side, and the tensor core multiplies codes. A q row is
+// scaled by a power of two to 128 <= max < 256: 8 significant bits are exact down
+// to 2^-14 of the row's maximum and never off by more than 2^-22 of it. P takes the
+// row scale of V (one exponential serves both: 2^(s + log2 vs - m), and the sum
+// divides by vs again) and lies within 2^8.5, so weights down to 2^-10 of the
+// largest keep 8 bits and the others are off by at most 2^-19 of it; m is raised
+// when a weight would pass 2^8.5. Converting the rows to bf16 on the way, as the
+// other e4m3 instances do, took 2.5 times as long.
+//
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
 //                 columns), O read-out
-//   4 warps       producers (bf16: cp.async; e4m3: converted to bf16 on the way)
+//   4 or 8 warps  producers (cp.async, or e4m3 converted to bf16 on the way)
 //   last warp     MMA issuer, TMEM
 // A tile is a chain of short steps in different warps, so what counts is the
 // length of each step: no division, no wait for a load and little code per tile
@@ -46,7 +57,6 @@
 namespace hytopk {
 namespace att {
 
-constexpr float kSlack = 64.0f;  // largest s - m (log2) before m is raised
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D_, int N_, bool E4_, bool F32_>
@@ -56,25 +66,33 @@ struct Cfg {
   static constexpr int SWG = N >= 64 ? 4 : 2;     // softmax warpgroups
   static constexpr int SWARPS = 4 * SWG;
   static constexpr int HG = N / SWG;              // head columns of each: 8, 16 or 32
+  // e4m3 rows multiplied as codes; else converted to bf16 (or bf16 as given)
+  static constexpr bool F8 = E4 && !F32 && D == 128 && N <= 64;
+  static constexpr bool CONV = E4 && !F8;
   static constexpr int PARTS = F32 ? 3 : 1;
+  // m is the maximum less kOver, and is raised when s - m passes kSlack (log2)
+  static constexpr float kOver = F8 ? 4.0f : 0.0f, kSlack = F8 ? 8.5f : 64.0f;
   // columns of the second product: P rows are whole 128-byte atoms of 64 heads
   // (columns N.. of a narrower item are never read)
   static constexpr int NP = N < 64 ? 64 : N;
-  static constexpr int RB = 2 * D;             // bf16 row bytes
+  static constexpr int RB = F8 ? D : 2 * D;    // row bytes of the operands
+  static constexpr int SN = F8 ? 2 * N : N;    // score columns (F8: q's two parts)
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;        // one K or V tile
-  static constexpr int PBYTES = NP / 64 * 16384;
+  static constexpr int PBYTES = NP / 64 * 16384;  // (F8: both parts in 128-byte rows)
   static constexpr int OBLK = D <= 128 ? 1 : D / 128;  // blocks of 128 result columns
-  static constexpr int OCOLS = F32 ? 2 * NP : NP;      // accumulator columns of a block
-  static constexpr int QBYTES = N * RB;
+  static constexpr int OCOLS = F32 || F8 ? 2 * NP : NP;      // accumulator columns of a block
+  static constexpr int QBYTES = SN * RB;
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
   // P buffers: two, unless their three parts or 128 heads leave no room for the ring
   static constexpr int PB = F32 || N > 64 ? 1 : 2;
-  static constexpr int PWARPS = 4;
+  static constexpr int PWARPS = N > 64 ? 4 : 8;
+  static constexpr int RPW = 128 / PWARPS;        // rows of a tile per producer warp
   static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
   static constexpr int MMA_WARP = SWARPS + PWARPS;
   // m, scale factors, 1 / sum [N] each; per-quadrant sums or maxima [4][N]
-  static constexpr int MISC = (3 + 4) * N * 4 + 512;
+  // F8: q scales [2][N]
+  static constexpr int MISC = (3 + 4 + 2 * F8) * N * 4 + 64 + 448;
   static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + MISC + 1024;
   static constexpr int NS_MAX = (227 * 1024 - FIXED) / SLOT;
   static constexpr int NS = NS_MAX < 8 ? NS_MAX : 8;
@@ -84,7 +102,7 @@ struct Cfg {
   static constexpr int MISC_OFF = Q_OFF + QB * QBYTES;
   static constexpr int SMEM = MISC_OFF + MISC + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
-  static_assert(2 * N <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
+  static_assert(2 * SN <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
   static_assert(NS >= 2 && SMEM <= 227 * 1024, "shared memory");
   static_assert(NS * SLOT >= N * D * 4, "partial results of a split item");
 };
@@ -108,6 +126,12 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
 }
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
+      " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -118,6 +142,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// four values as e4m3 codes (nearest even, saturating; the first in the low byte)
+__device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4]) {
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(v[1]), "f"(v[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v[3]), "f"(v[2]));
+  return (uint32_t)a | ((uint32_t)b << 16);
+}
+// 16 times what is left of four values (below 2^9) after their codes: exact in fp32
+__device__ __forceinline__ void rest_e4m3x4(uint32_t codes, float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(codes >> (16 * e))));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    v[2 * e] = (v[2 * e] - x.x) * 16.0f;
+    v[2 * e + 1] = (v[2 * e + 1] - x.y) * 16.0f;
+  }
 }
 
 // the two values minus their bf16 parts (exact)
@@ -248,7 +291,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   float* f_s = nm_s + N;                                       // [N] factor of a raised reference
   float* il_s = f_s + N;                                      // [N] 1 / sum (split: the sum)
   float* quad_s = il_s + N;                                   // [4][N]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(quad_s + 4 * N);
+  float* qe_s = quad_s + 4 * N;                               // F8: [2][N] scales of q rows
+  float* vm_s = qe_s + 2 * C::F8 * N;                         // F8: [4][4] maxima of log2 vs
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vm_s + 16);
   uint64_t* full = bars;
   uint64_t* empty = full + NS;
   uint64_t* q_full = empty + NS;
@@ -269,12 +314,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   if (pl.splits > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(full + i, C::E4 ? C::PWARPS : C::PWARPS * 32);
+      tc::mbar_init(full + i, C::CONV ? C::PWARPS : C::PWARPS * 32);
       tc::mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full + i, C::PWARPS);
-      tc::mbar_init(q_empty + i, 1);
+      tc::mbar_init(q_empty + i, C::F8 ? 1 + C::SWARPS : 1);
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(s_empty + i, C::SWARPS);
       tc::mbar_init(o_full + i, 1);
@@ -357,8 +402,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                            ((size_t)w.t * a.q_row + (size_t)first_head(w) * D) * 2;
       const int nh = head_count(w);
       uint8_t* dst = smem + C::Q_OFF + qb * C::QBYTES;
-      constexpr int CPR = C::RB / 16;
-      constexpr int PER = N * CPR / (C::PWARPS * 32);  // chunks a thread copies
+      constexpr int CPR = 2 * D / 16;
+      constexpr int PER = (N * CPR + C::PWARPS * 32 - 1) / (C::PWARPS * 32);  // chunks a thread copies
       constexpr int U = PER < 4 ? PER : 4;
 #pragma unroll 1
       for (int p = 0; p < PER; p += U) {
@@ -371,53 +416,93 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int f = (p + u) * C::PWARPS * 32 + tid;
-          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(f / CPR, f % CPR, N)) = v[u];
+          const int f = (p + u) * C::PWARPS * 32 + tid, r = f / CPR, c = f % CPR;
+          if (N * CPR % (C::PWARPS * 32) && f >= N * CPR) continue;
+          if constexpr (!C::F8) {
+            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v[u];
+          } else {
+            // 16 lanes hold a row: its scale, then both parts of 8 values a lane
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            float x[8], amax = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(w[e] << 16);
+              x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+              amax = max3(amax, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
+            }
+#pragma unroll
+            for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // 2^e with 128 <= amax / 2^e < 256 (e >= -120: both factors are normal)
+            const int ex = max((int)(__float_as_uint(amax) >> 23) - 7, 7);
+            const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float y[4] = {x[4 * e] * down, x[4 * e + 1] * down, x[4 * e + 2] * down,
+                            x[4 * e + 3] * down};
+              hi[e] = to_e4m3x4(y);
+              rest_e4m3x4(hi[e], y);
+              lo[e] = to_e4m3x4(y);
+            }
+            const uint32_t half = (uint32_t)(c & 1) * 8;
+            *reinterpret_cast<uint2*>(dst + Geo::chunk_offset(r, c / 2, C::SN) + half) =
+                make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(dst + Geo::chunk_offset(N + r, c / 2, C::SN) + half) =
+                make_uint2(lo[0], lo[1]);
+            if (c == 0) qe_s[qb * N + r] = __uint_as_float((uint32_t)ex << 23);
+          }
         }
       }
       publish(q_full + qb);
       return true;
     };
-    if constexpr (!C::E4) {
-      // warp w gathers rows 32w .. 32w + 31 of every tile, CPR lanes per row
-      constexpr int CPR = C::RB / 16;
-      constexpr int RPP = CPR >= 32 ? 1 : 32 / CPR;
-      constexpr int PASSES = 32 / RPP;              // row groups per warp and tile
-      constexpr int SHIFT = CPR >= 32 ? 5 : (CPR == 16 ? 4 : 3);  // lanes per row
+    if constexpr (!C::CONV) {
+      // Warp w gathers rows RPW w .. of every tile, CPR lanes per row. The tile's
+      // period was these loops at one time: rows come from their lanes first, a
+      // source address is one multiply-add, and the swizzled destinations repeat
+      // every 8 rows.
+      constexpr int CPR = C::RB / 16;              // 8, 16 or 32 lanes a row
+      constexpr int SHIFT = CPR == 32 ? 5 : (CPR == 16 ? 4 : 3);
+      constexpr int RPP = 32 / CPR;
+      constexpr int PASSES = C::RPW / RPP;
+      constexpr int ES = C::F8 ? 1 : 2;
+      const int c = lane & (CPR - 1);
+      uint32_t pat[8 / RPP];
+#pragma unroll
+      for (int p = 0; p < 8 / RPP; ++p) {
+        const uint32_t r = p * RPP + (lane >> SHIFT);
+        pat[p] = (uint32_t)(c >> 3) * 16384 + pw * C::RPW * 128 + r * 128 + (((c & 7) ^ r) << 4);
+      }
       int slot = 0;
       uint32_t phase = 1;
       bool ok = true;
       Walk w = start, wn = w;  // this tile; the next one
       int qi = 0;
-      int s_next = total > 0 ? entry_of(w.t, tile0 * 128 + tid) : -1;
+      int e_next = total > 0 ? entry_of(w.t, tile0 * 128 + pw * C::RPW + lane % C::RPW) : -1;
+#pragma unroll 1
       for (int g = 0; g < total && ok; ++g, w = wn) {
         if (w.i == 0 && !load_query(qi++, w)) break;
-        // every pass's row first, so that the copies go out back to back
-        const int s_own = row_of(s_next);
+        const int s_own = row_of(e_next);
         int rows[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
           rows[p] = __shfl_sync(0xffffffffu, s_own, p * RPP + (lane >> SHIFT));
         if (g + 1 < total) {
           walk_next(wn);
-          s_next = entry_of(wn.t, (tile0 + wn.i) * 128 + tid);
+          e_next = entry_of(wn.t, (tile0 + wn.i) * 128 + pw * C::RPW + lane % C::RPW);
         }
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = __all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status));
           if (!ok) break;
           const uint32_t dst = tc::smem_u32(ring + slot * C::SLOT);
-          const int c = lane & ((1 << SHIFT) - 1);
           const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) +
                                 (size_t)w.hk * C::RB + c * 16;
-          const int64_t row_bytes = (kv ? a.v_row : a.k_row) * 2;
+          const uint32_t row_bytes = (uint32_t)((kv ? a.v_row : a.k_row) * ES);
 #pragma unroll
-          for (int p = 0; p < PASSES; ++p) {
-            const int s = rows[p];
-            const uint8_t* src = base + (s >= 0 ? s * row_bytes : 0);
-            cp_async16(dst + Geo::chunk_offset(pw * 32 + p * RPP + (lane >> SHIFT), c, 128), src,
-                       s >= 0);
-          }
+          for (int p = 0; p < PASSES; ++p)
+            cp_async16(dst + pat[p % (8 / RPP)] + p * RPP / 8 * 1024,
+                       base + (uint64_t)(uint32_t)max(rows[p], 0) * row_bytes, rows[p] >= 0);
           // arrives for this thread when its copies so far have landed; the MMA
           // issuer's proxy fence makes them visible to the tensor core
           cp_async_arrive(full + slot);
@@ -429,12 +514,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-      // Warp w converts rows 32w .. 32w + 31 of every tile, CPR lanes of 16 codes
+      // Warp w converts rows RPW w .. of every tile, CPR lanes of 16 codes
       // per row. A tile is two or four chunks of up to 8 loads a lane (K's, then
       // V's); two chunks are in registers, so that one is always in flight.
       constexpr int CPR = D / 16;          // 4, 8 or 16
       constexpr int RPP = 32 / CPR;
-      constexpr int PASSES = 32 / RPP;
+      constexpr int PASSES = C::RPW / RPP;
       constexpr int CP = PASSES < 8 ? PASSES : 8;  // passes of a chunk
       constexpr int NCH = 2 * PASSES / CP;         // chunks of a tile (K and V)
       const int c = lane % CPR;
@@ -464,7 +549,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         const int p0 = (ch % (NCH / 2)) * CP;
 #pragma unroll
         for (int p = 0; p < CP; ++p) {
-          const int r = pw * 32 + (p0 + p) * RPP + lane / CPR;
+          const int r = pw * C::RPW + (p0 + p) * RPP + lane / CPR;
           *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c, 128)) =
               e4m3x8_to_bf16(make_uint2(v[p].x, v[p].y));
           *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c + 1, 128)) =
@@ -481,7 +566,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       };
       Walk w = start, wn = w;  // this tile; the next one
       int qi = 0;
-      auto own = [&](const Walk& x) { return entry_of(x.t, (tile0 + x.i) * 128 + tid); };
+      auto own = [&](const Walk& x) {
+        return entry_of(x.t, (tile0 + x.i) * 128 + pw * C::RPW + lane % C::RPW);
+      };
       int s_own = total > 0 ? row_of(own(w)) : -1, s_next = -1;
       if (total > 0) {
         issue(w.hk, s_own, 0, buf[0]);
@@ -525,9 +612,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // The whole warp keeps the (uniform) state and waits; one elected lane
     // issues. A single-lane branch would move every descriptor word through the
     // vector registers, which took 100 cycles per product.
-    constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
-    constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
-    constexpr uint32_t ID_O2 = tc::instr_desc(0, 128, C::OCOLS) | (1u << 15) | (1u << 16);
+    constexpr int KIND = C::F8 ? 1 : 0;
+    constexpr int SB = C::F8 ? 4096 : 2048;  // bytes of the 32 or 16 rows of a step
+    constexpr uint32_t ID_S = tc::instr_desc(KIND, 128, C::SN);
+    constexpr uint32_t ID_O = tc::instr_desc(KIND, 128, NP) | (1u << 15) | (1u << 16);
+    constexpr uint32_t ID_O2 = tc::instr_desc(KIND, 128, C::OCOLS) | (1u << 15) | (1u << 16);
     constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
     // 14 address bits: in a cluster, shared addresses carry the CTA's rank above them
     auto low = [](const void* p) { return (tc::smem_u32(p) >> 4) & 0x3FFFu; };
@@ -558,15 +647,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (ws.i == 0 && !wait(q_full + qb, (ws.qi / C::QB) & 1)) return false;
       if (!wait(full + ws.slot, ws.phase)) return false;
       if (!wait(s_empty + (g & 1), ((g >> 1) & 1) ^ 1)) return false;
-      if (!C::E4) tc::fence_proxy_async_smem();
+      if (!C::CONV) tc::fence_proxy_async_smem();
       tc::fence_after_sync();
       const uint32_t ad = (ring_lo + ws.slot * (C::SLOT >> 4)) | LBO_K;
       const uint32_t bd = (q_lo + qb * (C::QBYTES >> 4)) | LBO_K;
       if (elect_one()) {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          tc::mma<0>(tmem + C::S_COL + (g & 1) * N, desc(ad + (Geo::step_offset(j, 128) >> 4)),
-                     desc(bd + (Geo::step_offset(j, N) >> 4)), ID_S, j > 0 ? 1u : 0u);
+        for (int j = 0; j < C::RB / 32; ++j)
+          tc::mma<KIND>(tmem + C::S_COL + (g & 1) * C::SN,
+                        desc(ad + (Geo::step_offset(j, 128) >> 4)),
+                        desc(bd + (Geo::step_offset(j, C::SN) >> 4)), ID_S, j > 0 ? 1u : 0u);
         tc::mma_commit(s_full + (g & 1));
         tc::mma_commit(empty + ws.slot);
         if (ws.i == ntile - 1) tc::mma_commit(q_empty + qb);
@@ -580,7 +670,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (wo.i == 0 && !wait(o_empty + ob, ((wo.qi >> 1) & 1) ^ 1)) return false;
       if (!wait(full + wo.slot, wo.phase)) return false;
       if (!wait(p_full + pb, (g / C::PB) & 1)) return false;
-      if (!C::E4) tc::fence_proxy_async_smem();
+      if (!C::CONV) tc::fence_proxy_async_smem();
       tc::fence_after_sync();
       const uint32_t ad = (ring_lo + wo.slot * (C::SLOT >> 4)) | LBO_MN;
       const uint32_t bd = (p_lo + pb * (C::PARTS * C::PBYTES >> 4)) | LBO_MN;
@@ -590,12 +680,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
 #pragma unroll
           for (int part = 0; part < C::PARTS; part += 2) {
 #pragma unroll
-            for (int s = 0; s < 8; ++s)  // 16 rows each
+            for (int s = 0; s < (C::F8 ? 4 : 8); ++s)  // 32 bytes of P's type: 16 or 32 rows
               // d = 64 has one 64-column atom; the second one that M = 128 takes is
               // whatever follows the tile, and fills accumulator lanes never read
-              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
-                         desc(ad + ((blk * 32768 + s * 2048) >> 4)),
-                         desc(bd + ((part * C::PBYTES + s * 2048) >> 4)), part ? ID_O : ID_O2,
+              tc::mma<KIND>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
+                         desc(ad + ((blk * 32768 + s * SB) >> 4)),
+                         desc(bd + ((part * C::PBYTES + s * SB) >> 4)), part ? ID_O : ID_O2,
                          (wo.i > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
@@ -633,6 +723,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + hk) : 1.0f;
       vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + hk) : 1.0f;
     };
+    float vmax = 0.0f;  // F8: largest log2 vs of the item's first rows; scales its sums
+    // Scores of a tile into v: raw, or (F8) joined, scaled and with log2 vs added;
+    // then minus the references.
+    auto load_scores = [&](uint32_t addr, float c, float lv, const float* qe) {
+      tmem_load(addr, v);
+      if constexpr (C::F8) {
+        float x[HG];
+        tmem_load(addr + N, x);
+#pragma unroll
+        for (int u = 0; u < HG; u += 2) {
+          fma2(x[u], x[u + 1], 0.0625f, v[u], v[u + 1]);
+          v[u] = x[u];
+          v[u + 1] = x[u + 1];
+          mul2(v[u], v[u + 1], qe[u], qe[u + 1]);
+          fma2(v[u], v[u + 1], c, lv, lv);
+        }
+      }
+    };
+    auto shift = [&](float c) {
+#pragma unroll
+      for (int u = 0; u < HG; u += 2) {
+        if constexpr (C::F8) add2(v[u], v[u + 1], nm_s[c0 + u], nm_s[c0 + u + 1]);
+        else fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
+      }
+    };
     Walk wf = start;  // the tile whose entry was loaded last
     if (total > 0) {
       e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
@@ -660,7 +775,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         const bool valid = row_of(e_next) >= 0;
         if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
         const float c = valid ? c_scale * ks_next : 0.0f;
-        const float vs = vs_next;
+        const float vs = vs_next;  // (F8: its log2)
         if (C::E4) {
           e_next = e_far;
           load_scales(e_next, hk_far);
@@ -674,17 +789,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         bool ok = wait_bar(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
-        const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * N + c0;
-        tmem_load(s_addr, v);
+        const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * C::SN + c0;
+        const float lv = C::F8 ? __log2f(vs) : 0.0f;
+        const float* qe = qe_s + (qi % C::QB) * N + c0;
+        load_scores(s_addr, c, lv, qe);
         bool over = !have && valid;
         if (have) {
+          shift(c);
           float top = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < HG; u += 2) {
-            fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
-            top = max3(top, v[u], v[u + 1]);
-          }
-          over = valid && top > kSlack;
+          for (int u = 0; u < HG; u += 2) top = max3(top, v[u], v[u + 1]);
+          over = valid && top > C::kSlack;
         }
         if (tc::bar_or(bar, 128, over || !ok)) {
           // every product so far must be done before O is scaled
@@ -693,16 +808,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                                 a.status);
           if (tc::bar_or(bar, 128, !ok)) break;
           // raise (or set) the references to this tile's column maxima
-          tmem_load(s_addr, v);
+          load_scores(s_addr, c, lv, qe);
 #pragma unroll
-          for (int u = 0; u < HG; ++u) v[u] = valid ? v[u] * c : -INFINITY;
+          for (int u = 0; u < HG; ++u) v[u] = valid ? (C::F8 ? v[u] : v[u] * c) : -INFINITY;
           const float top = reduce_columns<HG, true>(v, lane);
           if (lane % LPC == 0) quad_s[quad * N + c0 + lane / LPC] = top;
+          if (C::F8 && !have) {
+            float x = valid ? lv : -INFINITY;
+            for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) vm_s[wg * 4 + quad] = x;
+          }
           tc::bar_sync(bar, 128);
+          if (C::F8 && !have)
+            vmax = fmaxf(fmaxf(vm_s[wg * 4], vm_s[wg * 4 + 1]),
+                         fmaxf(vm_s[wg * 4 + 2], vm_s[wg * 4 + 3]));
           if (row < HG) {
             const int col = c0 + row;
             const float high = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
-                                     fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
+                                     fmaxf(quad_s[2 * N + col], quad_s[3 * N + col])) -
+                               C::kOver;
             const float m = have ? fmaxf(-nm_s[col], high) : high;
             f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
             nm_s[col] = -m;
@@ -727,16 +851,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
             }
           }
           have = true;
-          tmem_load(s_addr, v);
-#pragma unroll
-          for (int u = 0; u < HG; u += 2)
-            fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
+          load_scores(s_addr, c, lv, qe);
+          shift(c);
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
+        if (lane == 0) {
+          tc::mbar_arrive(s_empty + (g & 1));
+          if (C::F8 && w.i == ntile - 1) tc::mbar_arrive(q_empty + qi % C::QB);
+        }
         // the weights of this row, rounded (or split) to bf16
         const bool off = !valid || !have;
+        const float unscale = C::F8 ? ex2(fminf(vmax - lv, 100.0f)) : 1.0f;
         if (__any_sync(0xffffffffu, off)) {
 #pragma unroll
           for (int u = 0; u < HG; ++u) v[u] = off ? -INFINITY : v[u];
@@ -745,15 +871,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         for (int u = 0; u < HG; u += 2) {
           v[u] = ex2(v[u]);
           v[u + 1] = ex2(v[u + 1]);
-          add2(l[u], l[u + 1], v[u], v[u + 1]);
-          if (C::E4) fma2(v[u], v[u + 1], vs, 0.0f, 0.0f);
+          if constexpr (C::F8) {
+            // without the row scale again (relative to 2^vmax)
+            float x0 = v[u], x1 = v[u + 1];
+            fma2(x0, x1, unscale, l[u], l[u + 1]);
+            l[u] = x0;
+            l[u + 1] = x1;
+          } else {
+            add2(l[u], l[u + 1], v[u], v[u + 1]);
+            if (C::CONV) mul2(v[u], v[u + 1], vs, vs);
+          }
         }
         // the buffer's previous product (a failed wait ends the warpgroup together
         // at its next vote)
         wait_bar(p_empty + g % C::PB, ((g / C::PB) & 1) ^ 1, abort_flag, a.status);
         uint8_t* p_dst = pbuf + (g % C::PB) * C::PARTS * C::PBYTES;
+        if constexpr (C::F8) {
+          uint32_t hi[HG / 4], lo[HG / 4];
 #pragma unroll
-        for (int part = 0; part < C::PARTS; ++part) {
+          for (int u = 0; u < HG; u += 4) {
+            float y[4] = {v[u], v[u + 1], v[u + 2], v[u + 3]};
+            hi[u / 4] = to_e4m3x4(y);
+            rest_e4m3x4(hi[u / 4], y);
+            lo[u / 4] = to_e4m3x4(y);
+          }
+          // head c0 is byte c0 of the row, its second part byte 64 + c0
+          uint8_t* dst = p_dst + (row >> 3) * 1024 + (row & 7) * 128 + (c0 & 15);
+          uint8_t* at_hi = dst + (((c0 >> 4) ^ (row & 7)) << 4);
+          uint8_t* at_lo = dst + (((4 + (c0 >> 4)) ^ (row & 7)) << 4);
+          if constexpr (HG == 16) {
+            *reinterpret_cast<uint4*>(at_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(at_hi) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at_lo) = make_uint2(lo[0], lo[1]);
+          }
+        }
+#pragma unroll
+        for (int part = 0; part < (C::F8 ? 0 : C::PARTS); ++part) {
 #pragma unroll
           for (int u = 0; u < HG; u += 8) {
             uint32_t x[4];
@@ -784,11 +939,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           const uint32_t o_addr =
               tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
           tmem_load(o_addr, v);
-          if constexpr (C::F32) {
+          if constexpr (C::F32 || C::F8) {
             float y[HG];
             tmem_load(o_addr + NP, y);
 #pragma unroll
-            for (int u = 0; u < HG; ++u) v[u] += y[u];
+            for (int u = 0; u < HG; ++u) v[u] = C::F8 ? __fmaf_rn(y[u], 0.0625f, v[u]) : v[u] + y[u];
           }
           // a split item's part stays unnormalised: [head][d] in the ring, idle by now
           float* part = reinterpret_cast<float*>(ring) + c0 * D + d;
@@ -825,13 +980,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                                      (quad_s[2 * N + col] + quad_s[3 * N + col])
                                : 0.0f;
           if (pl.splits > 1) {
-            il_s[col] = z;
+            il_s[col] = C::F8 ? z * ex2(-vmax) : z;
             if (!have) nm_s[col] = INFINITY;
           } else {
-            il_s[col] = 1.0f / z;
+            il_s[col] = C::F8 ? ex2(vmax) / z : 1.0f / z;
             if (a.lse && col < nh)
               a.lse[(size_t)w.t * Hq + h0 + col] =
-                  have ? (log2f(z) - nm_s[col]) * kLn2 : -INFINITY;
+                  have ? (log2f(z) - vmax - nm_s[col]) * kLn2 : -INFINITY;
           }
         }
         tc::bar_sync(bar, 128);
