@@ -50,8 +50,6 @@
 namespace hytopk {
 namespace att {
 
-constexpr int kChunk = 4;  // tiles whose dQ is summed on the tensor core
-
 template <int D_, int N_>
 struct BCfg {
   static constexpr int D = D_, N = N_;

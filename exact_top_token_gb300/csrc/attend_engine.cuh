@@ -23,8 +23,10 @@
 //
 // fp32 results: P is written as three bf16 parts (24 bits); the first two are
 // multiplied side by side (twice the columns) and the third adds to the second's,
-// so that the largest sums take one addition per 16 rows. bf16 results use one
-// part, whose rounding is of the size of the result's own.
+// so that the largest sums take one addition per 16 rows. The tensor core's fp32
+// additions truncate, and a long chain of them drifts (128 of them: 2e-6 of the
+// result), so O is read out and added up in registers every kChunk tiles. bf16
+// results use one part, whose rounding is of the size of the result's own.
 //
 // e4m3 rows of 128 columns with a bf16 result stay as they are in memory
 // (Cfg::F8): q and P are each written as an e4m3 part and an e4m3 part of 16
@@ -57,6 +59,7 @@
 namespace hytopk {
 namespace att {
 
+constexpr int kChunk = 4;  // tiles summed on the tensor core where the result is fp32
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D_, int N_, bool E4_, bool F32_>
@@ -86,7 +89,7 @@ struct Cfg {
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
   // P buffers: two, unless their three parts or 128 heads leave no room for the ring
   static constexpr int PB = F32 || N > 64 ? 1 : 2;
-  static constexpr int PWARPS = N > 64 ? 4 : 8;
+  static constexpr int PWARPS = N > 64 || F32 ? 4 : 8;  // (fp32 sums need the registers)
   static constexpr int RPW = 128 / PWARPS;        // rows of a tile per producer warp
   static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
   static constexpr int MMA_WARP = SWARPS + PWARPS;
@@ -642,6 +645,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       }
     };
     At ws{0, 0, 0, 0}, wo{0, 0, 1 % NS, 0};
+    int nc = 0;  // accumulations of O begun: items, or chunks of them
     auto scores = [&](int g) -> bool {
       const int qb = ws.qi % C::QB;
       if (ws.i == 0 && !wait(q_full + qb, (ws.qi / C::QB) & 1)) return false;
@@ -666,8 +670,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       return true;
     };
     auto weighted = [&](int g) -> bool {
-      const int ob = wo.qi & 1, pb = g % C::PB;
-      if (wo.i == 0 && !wait(o_empty + ob, ((wo.qi >> 1) & 1) ^ 1)) return false;
+      const int ic = C::F32 ? wo.i % kChunk : wo.i, pb = g % C::PB;
+      const int ob = nc & 1;
+      if (ic == 0 && !wait(o_empty + ob, ((nc >> 1) & 1) ^ 1)) return false;
       if (!wait(full + wo.slot, wo.phase)) return false;
       if (!wait(p_full + pb, (g / C::PB) & 1)) return false;
       if (!C::CONV) tc::fence_proxy_async_smem();
@@ -686,13 +691,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
               tc::mma<KIND>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
                          desc(ad + ((blk * 32768 + s * SB) >> 4)),
                          desc(bd + ((part * C::PBYTES + s * SB) >> 4)), part ? ID_O : ID_O2,
-                         (wo.i > 0 || part > 0 || s > 0) ? 1u : 0u);
+                         (ic > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
         tc::mma_commit(p_empty + pb);
         tc::mma_commit(empty + wo.slot);
-        if (wo.i == ntile - 1) tc::mma_commit(o_full + ob);
+        if (wo.i == ntile - 1 || (C::F32 && ic == kChunk - 1)) tc::mma_commit(o_full + ob);
       }
+      if (wo.i == ntile - 1 || (C::F32 && ic == kChunk - 1)) ++nc;
       __syncwarp();
       step(wo);
       return true;
@@ -760,10 +766,66 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     }
     Walk w = start;
     int qi = 0;
-    // the item before, whose result is still to be read from O
-    bool pend = false, pend_any = false;
-    int pend_nh = 0;
+    // An accumulation of O that is still to be read: the item before, or (fp32) a
+    // chunk of an item. Its result goes out with the item's last.
+    bool pend = false, pend_last = false, pend_any = false;
+    int pend_nh = 0, nc = 0;  // accumulations read so far
     size_t pend_at = 0;
+    constexpr int SUMS = C::F32 ? C::OBLK * HG : 1;
+    float o_sum[SUMS];  // fp32: the item's chunks so far
+    if constexpr (C::F32) {
+#pragma unroll
+      for (int u = 0; u < SUMS; ++u) o_sum[u] = 0.0f;
+    }
+    auto read_out = [&]() -> bool {
+      const int ob = nc & 1;
+      const bool ok = wait_bar(o_full + ob, (nc >> 1) & 1, abort_flag, a.status);
+      if (tc::bar_or(bar, 128, !ok)) return false;
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int blk = 0; blk < C::OBLK; ++blk) {
+        const int d = blk * 128 + row;
+        if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
+        const uint32_t o_addr = tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
+        float o[HG];
+        tmem_load(o_addr, o);
+        if constexpr (C::F32 || C::F8) {
+          float y[HG];
+          tmem_load(o_addr + NP, y);
+#pragma unroll
+          for (int u = 0; u < HG; ++u) o[u] = C::F8 ? __fmaf_rn(y[u], 0.0625f, o[u]) : o[u] + y[u];
+        }
+        if constexpr (C::F32) {
+#pragma unroll
+          for (int u = 0; u < HG; ++u) {
+            o[u] += o_sum[u];
+            o_sum[u] = pend_last ? 0.0f : o[u];
+          }
+          if (!pend_last) continue;
+        }
+        // a split item's part stays unnormalised: [head][d] in the ring, idle by now
+        float* part = reinterpret_cast<float*>(ring) + c0 * D + d;
+#pragma unroll
+        for (int u = 0; u < HG; ++u) {
+          if (c0 + u < pend_nh) {
+            const size_t at = pend_at + (size_t)(c0 + u) * D + d;
+            if (pl.splits > 1) {
+              part[u * D] = pend_any ? o[u] : 0.0f;
+            } else {
+              const float y = pend_any ? o[u] * il_s[c0 + u] : 0.0f;
+              if constexpr (C::F32) static_cast<float*>(a.out)[at] = y;
+              else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(o_empty + ob);
+      pend = false;
+      ++nc;
+      return true;
+    };
 #pragma unroll 1
     for (int g = 0; g <= total; ++g) {
       if (g < total) {
@@ -833,14 +895,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           }
           tc::bar_sync(bar, 128);
           if (have) {
+            if (C::F32 && pend && !read_out()) break;  // the chunk before, before its sums scale
 #pragma unroll
-            for (int u = 0; u < HG; ++u) l[u] *= f_s[c0 + u];
-            if (w.i > 0) {
+            for (int u = 0; u < HG; ++u) {
+              l[u] *= f_s[c0 + u];
+              if (C::F32) o_sum[u] *= f_s[c0 + u];
+            }
+            if ((C::F32 ? w.i % kChunk : w.i) > 0) {
 #pragma unroll 1
               for (int cc = 0; cc < C::OBLK * (C::OCOLS / NP) * HG; cc += 8) {
                 const int blk = cc / HG, h = c0 + cc % HG;  // NP columns from block to block
                 const uint32_t addr =
-                    tmem + lane_off + C::O_COL + (qi & 1) * C::OBLK * C::OCOLS + blk * NP + h;
+                    tmem + lane_off + C::O_COL + (nc & 1) * C::OBLK * C::OCOLS + blk * NP + h;
                 float o[8];
                 tmem_load(addr, o);
 #pragma unroll
@@ -926,45 +992,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + g % C::PB);
       }
-      // the previous item's result, while this item's first product runs
-      if (pend) {
-        const int ob = (qi & 1) ^ 1;
-        const bool ok = wait_bar(o_full + ob, ((qi - 1) >> 1) & 1, abort_flag, a.status);
-        if (tc::bar_or(bar, 128, !ok)) break;
-        tc::fence_after_sync();
-#pragma unroll 1
-        for (int blk = 0; blk < C::OBLK; ++blk) {
-          const int d = blk * 128 + row;
-          if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
-          const uint32_t o_addr =
-              tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
-          tmem_load(o_addr, v);
-          if constexpr (C::F32 || C::F8) {
-            float y[HG];
-            tmem_load(o_addr + NP, y);
-#pragma unroll
-            for (int u = 0; u < HG; ++u) v[u] = C::F8 ? __fmaf_rn(y[u], 0.0625f, v[u]) : v[u] + y[u];
-          }
-          // a split item's part stays unnormalised: [head][d] in the ring, idle by now
-          float* part = reinterpret_cast<float*>(ring) + c0 * D + d;
-#pragma unroll
-          for (int u = 0; u < HG; ++u) {
-            if (c0 + u < pend_nh) {
-              const size_t at = pend_at + (size_t)(c0 + u) * D + d;
-              if (pl.splits > 1) {
-                part[u * D] = pend_any ? v[u] : 0.0f;
-              } else {
-                const float o = pend_any ? v[u] * il_s[c0 + u] : 0.0f;
-                if constexpr (C::F32) static_cast<float*>(a.out)[at] = o;
-                else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
-              }
-            }
-          }
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(o_empty + ob);
-        pend = false;
+      // the accumulation before, while this tile's product runs
+      if (pend && !read_out()) break;
+      if (C::F32 && g < total && w.i % kChunk == kChunk - 1 && w.i < ntile - 1) {
+        pend = true;
+        pend_last = false;
+        pend_nh = head_count(w);
       }
       if (g < total && w.i == ntile - 1) {
         // the item's sums over its rows: lanes, then quadrants
@@ -990,7 +1023,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           }
         }
         tc::bar_sync(bar, 128);
-        pend = true;
+        pend = pend_last = true;
         pend_any = have;
         pend_nh = nh;
         pend_at = ((size_t)w.t * Hq + h0) * D;
