@@ -161,6 +161,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Rows whose largest magnitude lies between these bits (1e-18 and 2^127) divide by a
+// reciprocal.
+constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
+
 // MODE 0: rotated rows; 1: into bf16 cache rows; 2: into e4m3 cache rows
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
@@ -168,64 +172,71 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
   extern __shared__ float4 table4[];
   float* table = reinterpret_cast<float*>(table4);  // [tokens][cos rot/2 | sin rot/2]
   const int j = threadIdx.x % GL, group = threadIdx.x / GL;
-  const int64_t rows = (int64_t)a.n * a.H;
-  const int64_t row0 = (int64_t)blockIdx.x * (GROUPS * kIter);
+  // (n H < 2^31: row numbers are 32 bits, and a division is 20 instructions, not 100)
+  const unsigned rows = (unsigned)a.n * a.H;
+  const unsigned row0 = blockIdx.x * (unsigned)(GROUPS * kIter);
   // Rows are (t, h) in order; a group's are GROUPS apart.
-  int64_t row = row0 + group;
+  unsigned row = row0 + group;
   const int dt = GROUPS / a.H, dh = GROUPS - dt * a.H;
-  int t = (int)(row / a.H), h = (int)(row - (int64_t)t * a.H);
-  const int t0 = (int)(row0 / a.H);
+  int t = (int)(row / (unsigned)a.H), h = (int)row - t * a.H;
+  const int t0 = (int)(row0 / (unsigned)a.H);
+  // steps of the source pointer: to the group's next row, and back by H heads and on
+  // by a token where the heads run over
+  const int64_t x_step = dt * a.x_row + dh * a.x_head, x_wrap = a.x_row - a.H * a.x_head;
+  const T* x = static_cast<const T*>(a.x) + t * a.x_row + h * a.x_head + j * 8;
   uint32_t raw[kIter][W];
   int ts[kIter], hs[kIter], slot[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    ts[i] = t;
+    ts[i] = min(t, a.n - 1);
     hs[i] = h;
     slot[i] = -1;
     if (row < rows) {
       slot[i] = t;
       if (MODE != 0 && a.slots) slot[i] = __ldg(a.slots + t);
-      load8(static_cast<const T*>(a.x) + (size_t)t * a.x_row + (size_t)h * a.x_head + j * 8,
-            raw[i]);
+      load8(x, raw[i]);
     }
     row += GROUPS;
     t += dt;
     h += dh;
+    x += x_step;
     if (h >= a.H) {
       h -= a.H;
       ++t;
+      x += x_wrap;
     }
   }
   const int half = a.rot / 2;
   if (a.positions) {
-    const int64_t last = min(row0 + GROUPS * kIter, rows) - 1;
-    const int tokens = (int)(last / a.H) - t0 + 1;
-    for (int f = threadIdx.x; f < tokens * half; f += kFastThreads) {
-      const int k = f / half, i = f - k * half;
+    const unsigned last = min(row0 + GROUPS * kIter, rows) - 1;
+    const int tokens = (int)(last / (unsigned)a.H) - t0 + 1;
+    const float m_sin = a.inverse ? -a.mscale : a.mscale;
+    for (int k = threadIdx.x >> 5; k < tokens; k += kFastThreads / 32) {
       const int pos = __ldg(a.positions + t0 + k);
       const bool bad = pos < 0 || pos >= kMaxPosition;
-      float c, s;
-      rope_turn((float)pos, __ldg(a.inv_freq + i), c, s);
-      if (bad) {
-        c = s = __int_as_float(0x7fc00000);
-        if (a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+      if (bad && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+      for (int i = threadIdx.x & 31; i < half; i += 32) {
+        float c, s;
+        rope_turn((float)pos, __ldg(a.inv_freq + i), c, s);
+        if (bad) c = s = __int_as_float(0x7fc00000);
+        table[k * a.rot + i] = c * a.mscale;
+        table[k * a.rot + half + i] = s * m_sin;
       }
-      table[k * a.rot + i] = c * a.mscale;
-      table[k * a.rot + half + i] = a.inverse ? -(s * a.mscale) : s * a.mscale;
     }
     __syncthreads();
   }
   const int col = j * 8 - a.first;  // within the rotated part if 0 <= col < rot
   const bool turned = a.positions && col >= 0 && col < a.rot;
   const bool upper = col >= half;   // half layout: the second of each pair
+  [[maybe_unused]] const uint32_t group_mask =  // the lanes of this row
+      GL == 32 ? 0xffffffffu : ((1u << (GL & 31)) - 1u) << ((threadIdx.x & 31) / GL * GL);
   const int peer = (threadIdx.x & 31) + (upper ? -half / 8 : half / 8);
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     float v[8];
     unpack8<W>(raw[i], v);
     if (a.positions) {
-      // rows past the end (a group of the last block) take any token's angles
-      const float* tab = table + (size_t)(min(ts[i], a.n - 1) - t0) * a.rot;
+      const float* tab = table + (ts[i] - t0) * a.rot;  // (rows past the end: the last token's)
       if (a.interleaved) {
         if (turned) {
           const float4 c = *reinterpret_cast<const float4*>(tab + col / 2);
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
         }
       }
     }
-    const int64_t r = row0 + group + (int64_t)i * GROUPS;
+    const unsigned r = row0 + group + i * GROUPS;
     if constexpr (MODE == 0) {
       if (r < rows)
         store8(static_cast<T*>(a.out) + (size_t)ts[i] * a.out_row + (size_t)hs[i] * a.out_head +
@@ -269,46 +280,59 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
       const bool in = r < rows && slot[i] >= 0 && slot[i] < a.L;
       if (r < rows && !in && slot[i] != -1 && j == 0 && a.status)
         atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-      const size_t at = in ? ((size_t)slot[i] * a.H + hs[i]) * D + j * 8 : 0;
+      // 32 x 32 bits: a cache row and its scales have fewer than 2^31 elements
+      const uint64_t at_row = (uint64_t)(uint32_t)max(slot[i], 0) * (uint32_t)a.H + hs[i];
+      const uint64_t at = at_row * D + j * 8;
       if constexpr (MODE == 1) {
         if (in) store8(static_cast<__nv_bfloat16*>(a.out) + at, v);
       } else {
-        constexpr float kMost = 3.402823466e38f;
-        float amax = 0.0f;
-        bool odd = false;
+        // The row's largest magnitude by its bits, which also order NaN and infinity
+        // above every finite value.
+        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float m = fabsf(v[e]);
-          odd |= !(m <= kMost);
-          amax = fmaxf(amax, m <= kMost ? m : 0.0f);
-        }
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = GL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float scale = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f) : 1.0f;
-        // x / scale correctly rounded from the rounded reciprocal: one product, its
-        // exact remainder, one correction (Markstein, "Computation of elementary
-        // functions on the IBM RISC System/6000", 1990); a remainder that could
-        // underflow takes the divide
-        const float inv = __frcp_rn(scale);
-        if (scale > 1e-20f) {
+        for (int o = GL / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float scale;
+        uint2 codes;
+        if (top - kTinyRow < kHugeRow - kTinyRow) {
+          // Divisions by the rounded reciprocal: one product, its exact remainder, one
+          // correction give the correctly rounded quotient (Markstein, "Computation of
+          // elementary functions on the IBM RISC System/6000", 1990) while nothing
+          // underflows. With the reciprocal negated the quotient comes out negated, a
+          // negative zero keeps its sign, and one XOR flips four codes.
+          const float amax = __uint_as_float(top);
+          scale = amax * (1.0f / 448.0f);
+          scale = __fmaf_rn(__fmaf_rn(-scale, 448.0f, amax), 1.0f / 448.0f, scale);
+          const float ninv = -__frcp_rn(scale);
+          float c[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float q = v[e] * inv;
-            // (the correction loses the sign of a negative zero)
-            const float c = copysignf(__fmaf_rn(__fmaf_rn(-q, scale, v[e]), inv, q), v[e]);
-            v[e] = odd ? (fabsf(v[e]) <= kMost ? c : __int_as_float(0x7fc00000)) : c;
+            const float q = v[e] * ninv;
+            c[e] = __fmaf_rn(__fmaf_rn(q, scale, v[e]), ninv, q);
           }
+          codes = make_uint2((e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16)) ^ 0x80808080u,
+                             (e4m3x2(c[4], c[5]) | (e4m3x2(c[6], c[7]) << 16)) ^ 0x80808080u);
         } else {
+          // a row of zeros, of values whose remainders could underflow, or with a
+          // value that is not finite
+          constexpr float kMost = 3.402823466e38f;
+          float amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]) <= kMost ? fabsf(v[e]) : 0.0f);
+#pragma unroll
+          for (int o = GL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group_mask, amax, o));
+          scale = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f) : 1.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             v[e] = fabsf(v[e]) <= kMost ? __fdiv_rn(v[e], scale) : __int_as_float(0x7fc00000);
+          codes = make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
+                             e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+          if (in && top >= 0x7F800000u && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
         }
         if (in) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) =
-              make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
-                         e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
-          if (j == 0) a.scale[(size_t)slot[i] * a.H + hs[i]] = scale;
-          if (odd && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = codes;
+          if (j == 0) a.scale[at_row] = scale;
         }
       }
     }
@@ -345,6 +369,7 @@ template <bool E4M3, typename T>
 __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
   constexpr int CE = E4M3 ? 16 : 8;  // elements of a chunk
   const unsigned per_row = a.d / CE;
+  const int shift = (per_row & (per_row - 1)) ? -1 : 31 - __clz(per_row);
   const int64_t total = (int64_t)a.n * a.H * per_row;
   const int64_t f0 = (int64_t)blockIdx.x * (kFastThreads * kIter) + threadIdx.x;
   uint4 raw[kIter];
@@ -359,7 +384,9 @@ __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
     raw[i] = make_uint4(0, 0, 0, 0);
     scale[i] = 1.0f;
     if (f < total) {
-      const unsigned item = (unsigned)(f / per_row), c = (unsigned)(f - (int64_t)item * per_row);
+      // rows of a power of two of chunks by a shift (the others: a 64-bit division)
+      const unsigned item = shift >= 0 ? (unsigned)(f >> shift) : (unsigned)(f / per_row);
+      const unsigned c = (unsigned)(f - (int64_t)item * per_row);
       const unsigned t = item / a.H, h = item - t * a.H;
       slot[i] = a.slots ? __ldg(a.slots + t) : (int)t;
       in[i] = slot[i] >= 0 && slot[i] < a.L;

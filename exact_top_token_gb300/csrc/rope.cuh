@@ -18,6 +18,15 @@ namespace hytopk {
 
 constexpr int kMaxPosition = 1 << 24;  // positions below this are exact in fp32
 
+// The same reduction in 64 bits, for angles past 2^22 (a call, so that its 64-bit
+// arithmetic is not run ahead of the branch).
+static __device__ __noinline__ float2 rope_reduce_far(float pos, float freq) {
+  constexpr double kHalfPi = 1.5707963267948966192313216916398;
+  const double x = (double)pos * (double)freq;
+  const double n = rint(x * (1.0 / kHalfPi));
+  return make_float2((float)(x - n * kHalfPi), __int_as_float((int)(long long)n));
+}
+
 __device__ __forceinline__ void rope_turn(float pos, float freq, float& c, float& s) {
   constexpr double kHalfPi = 1.5707963267948966192313216916398;
   constexpr float C1 = (float)kHalfPi;
@@ -34,10 +43,9 @@ __device__ __forceinline__ void rope_turn(float pos, float freq, float& c, float
     r = __fmaf_rn(-n, C3, r) + lo;
     q = (int)n;
   } else {  // past 2^22 the multiple is no longer exact in fp32
-    const double x = (double)pos * (double)freq;
-    const double n = rint(x * (1.0 / kHalfPi));
-    r = (float)(x - n * kHalfPi);
-    q = (int)(long long)n;
+    const float2 far = rope_reduce_far(pos, freq);
+    r = far.x;
+    q = __float_as_int(far.y);
   }
   const float z = r * r;
   float sn = __fmaf_rn(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
