@@ -161,14 +161,23 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Rows whose largest magnitude lies between these bits (1e-18 and 2^127) divide by a
 // reciprocal.
 constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
 
-// MODE 0: rotated rows; 1: into bf16 cache rows; 2: into e4m3 cache rows
-template <typename T, int D, int MODE>
+// MODE 0: rotated rows; 1: into bf16 cache rows; 2: into e4m3 cache rows.
+// V: neighbouring 8-column vectors a lane holds. Quantising is bound by its
+// instructions (30 a value octet beside the loads); with V = 2 half the lanes share
+// a row's scale, addresses and magnitude steps (8 heads x 65521 rows: 83 -> 68 us).
+template <typename T, int D, int MODE, int V>
 __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
-  constexpr int GL = D / 8, GROUPS = kFastThreads / GL, W = sizeof(T) * 2;
+  constexpr int GL = D / (8 * V), GROUPS = kFastThreads / GL, W = sizeof(T) * 2;
   extern __shared__ float4 table4[];
   float* table = reinterpret_cast<float*>(table4);  // [tokens][cos rot/2 | sin rot/2]
   const int j = threadIdx.x % GL, group = threadIdx.x / GL;
@@ -183,8 +192,8 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
   // steps of the source pointer: to the group's next row, and back by H heads and on
   // by a token where the heads run over
   const int64_t x_step = dt * a.x_row + dh * a.x_head, x_wrap = a.x_row - a.H * a.x_head;
-  const T* x = static_cast<const T*>(a.x) + t * a.x_row + h * a.x_head + j * 8;
-  uint32_t raw[kIter][W];
+  const T* x = static_cast<const T*>(a.x) + t * a.x_row + h * a.x_head + j * (8 * V);
+  uint32_t raw[kIter][V][W];
   int ts[kIter], hs[kIter], slot[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -194,7 +203,8 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
     if (row < rows) {
       slot[i] = t;
       if (MODE != 0 && a.slots) slot[i] = __ldg(a.slots + t);
-      load8(x, raw[i]);
+#pragma unroll
+      for (int u = 0; u < V; ++u) load8(x + 8 * u, raw[i][u]);
     }
     row += GROUPS;
     t += dt;
@@ -225,17 +235,17 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
     }
     __syncthreads();
   }
-  const int col = j * 8 - a.first;  // within the rotated part if 0 <= col < rot
-  const bool turned = a.positions && col >= 0 && col < a.rot;
-  const bool upper = col >= half;   // half layout: the second of each pair
   [[maybe_unused]] const uint32_t group_mask =  // the lanes of this row
       GL == 32 ? 0xffffffffu : ((1u << (GL & 31)) - 1u) << ((threadIdx.x & 31) / GL * GL);
-  const int peer = (threadIdx.x & 31) + (upper ? -half / 8 : half / 8);
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    float v[8];
-    unpack8<W>(raw[i], v);
-    if (a.positions) {
+    float v[V][8];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      unpack8<W>(raw[i][u], v[u]);
+      if (!a.positions) continue;
+      const int col = (j * V + u) * 8 - a.first;  // within the rotated part if 0 <= col < rot
+      const bool turned = col >= 0 && col < a.rot;
       const float* tab = table + (ts[i] - t0) * a.rot;  // (rows past the end: the last token's)
       if (a.interleaved) {
         if (turned) {
@@ -244,15 +254,19 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
           const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x1 = v[2 * e], x2 = v[2 * e + 1];
-            v[2 * e] = x1 * cs[e] - x2 * sn[e];
-            v[2 * e + 1] = x1 * sn[e] + x2 * cs[e];
+            const float x1 = v[u][2 * e], x2 = v[u][2 * e + 1];
+            v[u][2 * e] = x1 * cs[e] - x2 * sn[e];
+            v[u][2 * e + 1] = x1 * sn[e] + x2 * cs[e];
           }
         }
       } else {
+        // the other half of the pairs: the same vector of the lane half / (8 V) on or
+        // back (V = 2: half is a multiple of 16)
+        const bool upper = col >= half;
+        const int peer = (threadIdx.x & 31) + (upper ? -half / (8 * V) : half / (8 * V));
         uint32_t other[W];
 #pragma unroll
-        for (int e = 0; e < W; ++e) other[e] = __shfl_sync(0xffffffffu, raw[i][e], peer & 31);
+        for (int e = 0; e < W; ++e) other[e] = __shfl_sync(0xffffffffu, raw[i][u][e], peer & 31);
         if (turned) {
           float o[8];
           unpack8<W>(other, o);
@@ -264,8 +278,8 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
             const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = v[4 * q + e], y = o[4 * q + e];
-              v[4 * q + e] = upper ? y * sn[e] + x * cs[e] : x * cs[e] - y * sn[e];
+              const float x = v[u][4 * q + e], y = o[4 * q + e];
+              v[u][4 * q + e] = upper ? y * sn[e] + x * cs[e] : x * cs[e] - y * sn[e];
             }
           }
         }
@@ -273,28 +287,36 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
     }
     const unsigned r = row0 + group + i * GROUPS;
     if constexpr (MODE == 0) {
-      if (r < rows)
-        store8(static_cast<T*>(a.out) + (size_t)ts[i] * a.out_row + (size_t)hs[i] * a.out_head +
-                   j * 8, v);
+      if (r < rows) {
+        T* y = static_cast<T*>(a.out) + (size_t)ts[i] * a.out_row + (size_t)hs[i] * a.out_head;
+#pragma unroll
+        for (int u = 0; u < V; ++u) store8(y + (j * V + u) * 8, v[u]);
+      }
     } else {
       const bool in = r < rows && slot[i] >= 0 && slot[i] < a.L;
       if (r < rows && !in && slot[i] != -1 && j == 0 && a.status)
         atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-      // 32 x 32 bits: a cache row and its scales have fewer than 2^31 elements
       const uint64_t at_row = (uint64_t)(uint32_t)max(slot[i], 0) * (uint32_t)a.H + hs[i];
-      const uint64_t at = at_row * D + j * 8;
+      const uint64_t at = at_row * D + j * (8 * V);
       if constexpr (MODE == 1) {
-        if (in) store8(static_cast<__nv_bfloat16*>(a.out) + at, v);
+        if (in) {
+#pragma unroll
+          for (int u = 0; u < V; ++u)
+            store8(static_cast<__nv_bfloat16*>(a.out) + at + 8 * u, v[u]);
+        }
       } else {
-        // The row's largest magnitude by its bits, which also order NaN and infinity
-        // above every finite value.
-        uint32_t top = 0;
+        // The row's largest magnitude, two values an instruction; a NaN stays one, so
+        // that its bits, like infinity's, lie above every finite value's.
+        float most = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 8 * V; e += 2)
+          most = max3_nan(most, fabsf(v[e / 8][e % 8]), fabsf(v[e / 8][e % 8 + 1]));
 #pragma unroll
-        for (int o = GL / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = GL / 2; o; o >>= 1)
+          most = max3_nan(most, most, __shfl_xor_sync(0xffffffffu, most, o));
+        const uint32_t top = __float_as_uint(most);
         float scale;
-        uint2 codes;
+        uint32_t codes[2 * V];
         if (top - kTinyRow < kHugeRow - kTinyRow) {
           // Divisions by the rounded reciprocal: one product, its exact remainder, one
           // correction give the correctly rounded quotient (Markstein, "Computation of
@@ -305,33 +327,47 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
           scale = amax * (1.0f / 448.0f);
           scale = __fmaf_rn(__fmaf_rn(-scale, 448.0f, amax), 1.0f / 448.0f, scale);
           const float ninv = -__frcp_rn(scale);
-          float c[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float q = v[e] * ninv;
-            c[e] = __fmaf_rn(__fmaf_rn(q, scale, v[e]), ninv, q);
+          for (int w = 0; w < 2 * V; ++w) {
+            float c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = v[w / 2][w % 2 * 4 + e], q = y * ninv;
+              c[e] = __fmaf_rn(__fmaf_rn(q, scale, y), ninv, q);
+            }
+            codes[w] = (e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16)) ^ 0x80808080u;
           }
-          codes = make_uint2((e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16)) ^ 0x80808080u,
-                             (e4m3x2(c[4], c[5]) | (e4m3x2(c[6], c[7]) << 16)) ^ 0x80808080u);
         } else {
           // a row of zeros, of values whose remainders could underflow, or with a
           // value that is not finite
           constexpr float kMost = 3.402823466e38f;
           float amax = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]) <= kMost ? fabsf(v[e]) : 0.0f);
+          for (int e = 0; e < 8 * V; ++e) {
+            const float m = fabsf(v[e / 8][e % 8]);
+            amax = fmaxf(amax, m <= kMost ? m : 0.0f);
+          }
 #pragma unroll
           for (int o = GL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group_mask, amax, o));
           scale = amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 1.17549435e-38f) : 1.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = fabsf(v[e]) <= kMost ? __fdiv_rn(v[e], scale) : __int_as_float(0x7fc00000);
-          codes = make_uint2(e4m3x2(v[0], v[1]) | (e4m3x2(v[2], v[3]) << 16),
-                             e4m3x2(v[4], v[5]) | (e4m3x2(v[6], v[7]) << 16));
+          for (int w = 0; w < 2 * V; ++w) {
+            float c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = v[w / 2][w % 2 * 4 + e];
+              c[e] = fabsf(y) <= kMost ? __fdiv_rn(y, scale) : __int_as_float(0x7fc00000);
+            }
+            codes[w] = e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16);
+          }
           if (in && top >= 0x7F800000u && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
         }
         if (in) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + at) = codes;
+          uint8_t* y = static_cast<uint8_t*>(a.out) + at;
+          if constexpr (V == 2)
+            *reinterpret_cast<uint4*>(y) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+          else
+            *reinterpret_cast<uint2*>(y) = make_uint2(codes[0], codes[1]);
           if (j == 0) a.scale[at_row] = scale;
         }
       }
@@ -339,17 +375,36 @@ __global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
   }
 }
 
-template <typename T, int MODE>
-bool launch_rows(const RowArgs& a, cudaStream_t st) {
-  if (a.d != 64 && a.d != 128 && a.d != 256) return false;
-  const int per = kFastThreads / (a.d / 8) * kIter;  // rows of a block
-  // a block of `per` rows touches at most this many tokens (32 KB of angles at most)
+template <typename T, int D, int MODE, int V>
+void launch_rows_of(const RowArgs& a, cudaStream_t st) {
+  const int per = kFastThreads / (D / (8 * V)) * kIter;  // rows of a block
+  // a block of `per` rows touches at most this many tokens (64 KB of angles at most)
   const int tokens = a.H >= per ? 2 : (per + a.H - 2) / a.H + 1;
   const size_t smem = a.positions ? (size_t)tokens * a.rot * sizeof(float) : 0;
   const unsigned grid = (unsigned)(((int64_t)a.n * a.H + per - 1) / per);
-  if (a.d == 64) k_rows<T, 64, MODE><<<grid, kFastThreads, smem, st>>>(a);
-  else if (a.d == 128) k_rows<T, 128, MODE><<<grid, kFastThreads, smem, st>>>(a);
-  else k_rows<T, 256, MODE><<<grid, kFastThreads, smem, st>>>(a);
+  if (smem > 48 * 1024)
+    cudaFuncSetAttribute(k_rows<T, D, MODE, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         (int)smem);
+  k_rows<T, D, MODE, V><<<grid, kFastThreads, smem, st>>>(a);
+}
+
+template <typename T, int MODE>
+bool launch_rows(const RowArgs& a, cudaStream_t st) {
+  // two vectors a lane: when quantising bf16, and pairs lie whole lanes apart
+  constexpr bool kTwo = MODE == 2 && sizeof(T) == 2;
+  if constexpr (kTwo) {
+    if (!a.positions || a.interleaved || a.rot % 32 == 0) {
+      if (a.d == 64) launch_rows_of<T, 64, MODE, 2>(a, st);
+      else if (a.d == 128) launch_rows_of<T, 128, MODE, 2>(a, st);
+      else if (a.d == 256) launch_rows_of<T, 256, MODE, 2>(a, st);
+      else return false;
+      return true;
+    }
+  }
+  if (a.d == 64) launch_rows_of<T, 64, MODE, 1>(a, st);
+  else if (a.d == 128) launch_rows_of<T, 128, MODE, 1>(a, st);
+  else if (a.d == 256) launch_rows_of<T, 256, MODE, 1>(a, st);
+  else return false;
   return true;
 }
 
