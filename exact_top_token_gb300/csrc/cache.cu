@@ -176,7 +176,7 @@ constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
 // instructions (30 a value octet beside the loads); with V = 2 half the lanes share
 // a row's scale, addresses and magnitude steps (8 heads x 65521 rows: 83 -> 68 us).
 template <typename T, int D, int MODE, int V>
-__global__ void __launch_bounds__(kFastThreads) k_rows(const RowArgs a) {
+__global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
   constexpr int GL = D / (8 * V), GROUPS = kFastThreads / GL, W = sizeof(T) * 2;
   extern __shared__ float4 table4[];
   float* table = reinterpret_cast<float*>(table4);  // [tokens][cos rot/2 | sin rot/2]
