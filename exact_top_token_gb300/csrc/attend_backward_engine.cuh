@@ -572,8 +572,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
 template <class C, bool OUT_F32>
 cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
   auto kernel = k_attend_backward<C, OUT_F32>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
+  static unsigned long long opted_in = 0;
   Plan pl{};
   pl.splits = 1;
   pl.blocks = (a.G + C::N - 1) / C::N;
@@ -584,8 +583,10 @@ cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
   pl.sb = pl.stride % pl.blocks;
   pl.sh = pl.stride / pl.blocks % a.Hkv;
   pl.st = pl.stride / pl.blocks / a.Hkv;
-  kernel<<<pl.stride, C::THREADS, C::SMEM, st>>>(a, pl);
-  return cudaGetLastError();
+  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
+    kernel<<<pl.stride, C::THREADS, C::SMEM, st>>>(a, pl);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace att

@@ -1079,8 +1079,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
 template <class C>
 cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   auto kernel = k_attend<C>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
+  static unsigned long long opted_in = 0;
   Plan pl{};
   pl.blocks = (a.G + C::N - 1) / C::N;
   pl.heads = (a.G + pl.blocks - 1) / pl.blocks;
@@ -1108,7 +1107,8 @@ cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pl.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, pl);
+  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in,
+                         [&] { return cudaLaunchKernelEx(&cfg, kernel, a, pl); });
 }
 
 }  // namespace att

@@ -239,6 +239,8 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
       GL == 32 ? 0xffffffffu : ((1u << (GL & 31)) - 1u) << ((threadIdx.x & 31) / GL * GL);
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
+    const unsigned r = row0 + group + i * GROUPS;
+    if (__all_sync(0xffffffffu, r >= rows)) break;
     float v[V][8];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
@@ -285,7 +287,6 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
         }
       }
     }
-    const unsigned r = row0 + group + i * GROUPS;
     if constexpr (MODE == 0) {
       if (r < rows) {
         T* y = static_cast<T*>(a.out) + (size_t)ts[i] * a.out_row + (size_t)hs[i] * a.out_head;
@@ -317,7 +318,9 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
         const uint32_t top = __float_as_uint(most);
         float scale;
         uint32_t codes[2 * V];
-        if (top - kTinyRow < kHugeRow - kTinyRow) {
+        if (!in) {
+          // (a row past the end or skipped holds anything: no work for it)
+        } else if (top - kTinyRow < kHugeRow - kTinyRow) {
           // Divisions by the rounded reciprocal: one product, its exact remainder, one
           // correction give the correctly rounded quotient (Markstein, "Computation of
           // elementary functions on the IBM RISC System/6000", 1990) while nothing
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
             }
             codes[w] = e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16);
           }
-          if (in && top >= 0x7F800000u && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
+          if (top >= 0x7F800000u && a.status) atomicOr(a.status, HYTOPK_DEV_NONFINITE);
         }
         if (in) {
           uint8_t* y = static_cast<uint8_t*>(a.out) + at;
