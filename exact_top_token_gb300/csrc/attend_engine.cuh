@@ -59,6 +59,7 @@
 namespace hytopk {
 namespace att {
 
+constexpr int kSplits = 8;  // CTAs that share an item, at most (a portable cluster)
 constexpr int kChunk = 4;  // tiles summed on the tensor core where the result is fp32
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -397,30 +398,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (lane == 0) tc::mbar_arrive(bar);
     };
     // the item's query rows, zero beyond its heads
-    auto load_query = [&](int qi, const Walk& w) -> bool {
+    constexpr int QCPR = 2 * D / 16;
+    constexpr int QPER = (N * QCPR + C::PWARPS * 32 - 1) / (C::PWARPS * 32);  // chunks of a thread
+    constexpr int QU = QPER < 4 ? QPER : 4;                                   // at a time
+    auto fetch_query = [&](const Walk& w, int p, uint4 (&v)[QU]) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint8_t*>(a.q) + ((size_t)w.t * a.q_row + (size_t)first_head(w) * D) * 2);
+      const int nh = head_count(w);
+#pragma unroll
+      for (int u = 0; u < QU; ++u) {
+        const int f = (p + u) * C::PWARPS * 32 + tid;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (f / QCPR < nh) v[u] = __ldg(src + f);
+      }
+    };
+    // stores the chunks that are fetched already (v: the first) and the rest
+    auto store_query = [&](int qi, const Walk& w, uint4 (&v)[QU]) -> bool {
       const int qb = qi % C::QB;
       const bool ok = wait_bar(q_empty + qb, ((qi / C::QB) & 1) ^ 1, abort_flag, a.status);
       if (!__all_sync(0xffffffffu, ok)) return false;
-      const uint8_t* src = static_cast<const uint8_t*>(a.q) +
-                           ((size_t)w.t * a.q_row + (size_t)first_head(w) * D) * 2;
-      const int nh = head_count(w);
       uint8_t* dst = smem + C::Q_OFF + qb * C::QBYTES;
-      constexpr int CPR = 2 * D / 16;
-      constexpr int PER = (N * CPR + C::PWARPS * 32 - 1) / (C::PWARPS * 32);  // chunks a thread copies
-      constexpr int U = PER < 4 ? PER : 4;
 #pragma unroll 1
-      for (int p = 0; p < PER; p += U) {
-        uint4 v[U];
+      for (int p = 0; p < QPER; p += QU) {
+        if (p) fetch_query(w, p, v);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int f = (p + u) * C::PWARPS * 32 + tid;
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (f / CPR < nh) v[u] = __ldg(reinterpret_cast<const uint4*>(src) + f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int f = (p + u) * C::PWARPS * 32 + tid, r = f / CPR, c = f % CPR;
-          if (N * CPR % (C::PWARPS * 32) && f >= N * CPR) continue;
+        for (int u = 0; u < QU; ++u) {
+          const int f = (p + u) * C::PWARPS * 32 + tid, r = f / QCPR, c = f % QCPR;
+          if (N * QCPR % (C::PWARPS * 32) && f >= N * QCPR) continue;
           if constexpr (!C::F8) {
             *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v[u];
           } else {
@@ -484,7 +488,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       int e_next = total > 0 ? entry_of(w.t, tile0 * 128 + pw * C::RPW + lane % C::RPW) : -1;
 #pragma unroll 1
       for (int g = 0; g < total && ok; ++g, w = wn) {
-        if (w.i == 0 && !load_query(qi++, w)) break;
+        // an item's queries load while its first rows do
+        uint4 qv[QU];
+        if (w.i == 0) fetch_query(w, 0, qv);
         const int s_own = row_of(e_next);
         int rows[PASSES];
 #pragma unroll
@@ -513,6 +519,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
             slot = 0;
             phase ^= 1u;
           }
+          // Between K and V: with two slots V waits for the product of the tile before,
+          // which the MMA issuer starts only after this tile's scores.
+          if (kv == 0 && w.i == 0 && !(ok = store_query(qi++, w, qv))) break;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -590,7 +599,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       }
       bool ok = true;
       for (int g = 0; g < total && ok; ++g) {
-        if (w.i == 0 && !load_query(qi++, w)) break;
+        if (w.i == 0) {
+          uint4 qv[QU];
+          fetch_query(w, 0, qv);
+          if (!store_query(qi++, w, qv)) break;
+        }
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
           if (!store(ch, buf[ch & 1])) {
@@ -1033,35 +1046,42 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     }
   }
   if (pl.splits > 1) {
-    // join the cluster's parts: rank r takes heads r, r + splits, ... of the one item
+    // Join the cluster's parts: each rank takes a share of the item's nh x d values.
+    // Every CTA's reference, sum and part of a value are read at once; one after
+    // another they took 8 of a single token's 18 us.
     __syncwarp();
     cluster_sync();
     if (!*abort_flag) {
       const int h0 = first_head(start), nh = head_count(start);
       const uint32_t part_a = tc::smem_u32(ring), m_a = tc::smem_u32(nm_s), l_a = tc::smem_u32(il_s);
+      const int per = (nh * D + pl.splits - 1) / pl.splits;
+      const int end = min(nh * D, (int)(rank + 1) * per);
 #pragma unroll 1
-      for (int f = threadIdx.x; f < nh * D; f += C::THREADS) {
-        const int h = f / D, d = f % D;
-        if (h % pl.splits != (int)rank) continue;
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int r = 0; r < pl.splits; ++r)
-          top = fmaxf(top, -ld_cluster(map_cluster(m_a + h * 4, r)));
-        float sum = 0.0f, o = 0.0f;
-#pragma unroll 1
-        for (int r = 0; r < pl.splits; ++r) {
-          const float m = -ld_cluster(map_cluster(m_a + h * 4, r));
-          if (m == -INFINITY) continue;
-          const float x = ex2(m - top);
-          sum += x * ld_cluster(map_cluster(l_a + h * 4, r));
-          o += x * ld_cluster(map_cluster(part_a + f * 4, r));
+      for (int f = (int)rank * per + threadIdx.x; f < end; f += C::THREADS) {
+        const int h = f / D;
+        float m[kSplits], z[kSplits], o[kSplits];
+#pragma unroll
+        for (int r = 0; r < kSplits; ++r) {
+          const bool is = r < pl.splits;
+          m[r] = is ? -ld_cluster(map_cluster(m_a + h * 4, r)) : -INFINITY;
+          z[r] = is ? ld_cluster(map_cluster(l_a + h * 4, r)) : 0.0f;
+          o[r] = is ? ld_cluster(map_cluster(part_a + f * 4, r)) : 0.0f;
         }
+        float top = -INFINITY, sum = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kSplits; ++r) top = fmaxf(top, m[r]);
         const bool any = top != -INFINITY;
-        o = any ? o / sum : 0.0f;
+#pragma unroll
+        for (int r = 0; r < kSplits; ++r) {
+          const float x = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top);
+          sum += x * z[r];
+          y += x * o[r];
+        }
+        y = any ? y / sum : 0.0f;
         const size_t at = ((size_t)start.t * Hq + h0) * D + f;
-        if constexpr (C::F32) static_cast<float*>(a.out)[at] = o;
-        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
-        if (d == 0 && a.lse)
+        if constexpr (C::F32) static_cast<float*>(a.out)[at] = y;
+        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+        if (f % D == 0 && a.lse)
           a.lse[(size_t)start.t * Hq + h0 + h] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
       }
     }
@@ -1087,7 +1107,7 @@ cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   pl.items = a.n * a.Hkv * pl.blocks;
   pl.splits = 1;
   // split while every SM still gets at most one CTA and every CTA a tile
-  while (pl.splits < 8 && 2 * pl.splits <= pl.tiles &&
+  while (pl.splits < kSplits && 2 * pl.splits <= pl.tiles &&
          (int64_t)pl.items * 2 * pl.splits <= sms)
     pl.splits *= 2;
   const int ctas = pl.items < sms ? pl.items : sms;

@@ -107,6 +107,27 @@ def test_attend_f32_result(hk, dev, n, Hq, Hkv, d, k, L, cache):
     verify(hk, torch, q, kk, vv, idx, kw, torch.float32)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(12, 1, 64), (50, 1, 64), (12, 1, 128), (50, 1, 128), (100, 1, 128),
+                                      (12, 1, 256), (50, 1, 256), (100, 1, 256), (4, 2, 256)])
+def test_many_items_of_several_tiles(hk, dev, Hq, Hkv, d, cache):
+    """Several items per CTA, each of several tiles, in every instance of the engine: what is
+    kept from item to item (buffers, phases, references) and no bounded wait giving up."""
+    import torch
+
+    n, k, L = 500, 300, 400
+    q, kk, vv, idx, kw = make(torch, dev, n, Hq, Hkv, d, k, L, cache, seed=d + Hq)
+    types = [torch.bfloat16] if d == 256 else [torch.bfloat16, torch.float32]
+    sample = torch.arange(0, n, 29, device=dev)
+    for dt in types:
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        out, lse = hk.attend(q, kk, vv, idx, out_dtype=dt, status=status, **kw)
+        assert int(status.item()) == 0
+        r = reference(q[sample], kk, vv, idx[sample], kw, d ** -0.5, 8 if dt == torch.bfloat16 else 24)
+        check("out", out[sample].float().cpu().numpy(), r["out"], r["tol_out"])
+        check("lse", lse[sample].cpu().numpy(), r["lse"], r["tol_lse"])
+
+
 @pytest.mark.parametrize("out_dtype", ["bfloat16", "float32"])
 def test_large_scores_and_late_maxima(hk, dev, out_dtype):
     """Scores of several hundred, growing along the list: the running maximum moves at
@@ -295,6 +316,26 @@ def test_gradients(hk, dev, n, Hq, Hkv, d, k, L):
     r = reference(q, kk, vv, idx, kw, d ** -0.5, 24, grad)
     for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
         check(name, got.cpu().numpy(), r[name], r["tol_" + name])
+
+
+@pytest.mark.parametrize("Hq,d", [(12, 64), (50, 64), (12, 128), (100, 128)])
+def test_gradients_of_many_items_of_several_tiles(hk, dev, Hq, d):
+    import torch
+
+    n, k, L = 400, 650, 700
+    q, kk, vv, idx, kw = make(torch, dev, n, Hq, 1, d, k, L, seed=d + Hq)
+    keep = torch.arange(0, n, 57, device=dev)
+    grad = torch.zeros(n, Hq, d, device=dev, dtype=torch.bfloat16)  # the others' rows add nothing
+    g = torch.Generator(device=dev).manual_seed(3)
+    grad[keep] = torch.randn(len(keep), Hq, d, device=dev, generator=g).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    out, lse = hk.attend(q, kk, vv, idx, out_dtype=torch.float32)
+    dq, dk, dv = hk.attend_backward(q, kk, vv, idx, out, lse, grad, status=status)
+    assert int(status.item()) == 0
+    r = reference(q[keep], kk, vv, idx[keep], kw, d ** -0.5, 24, grad[keep])
+    check("dq", dq[keep].cpu().numpy(), r["dq"], r["tol_dq"])
+    check("dk", dk.cpu().numpy(), r["dk"], r["tol_dk"])
+    check("dv", dv.cpu().numpy(), r["dv"], r["tol_dv"])
 
 
 def test_gradients_against_differences(hk, dev):
