@@ -90,7 +90,7 @@ struct Cfg {
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
   // P buffers: two, unless their three parts or 128 heads leave no room for the ring
   static constexpr int PB = F32 || N > 64 ? 1 : 2;
-  static constexpr int PWARPS = N > 64 || F32 ? 4 : 8;  // (fp32 sums need the registers)
+  static constexpr int PWARPS = N > 64 ? 4 : 8;
   static constexpr int RPW = 128 / PWARPS;        // rows of a tile per producer warp
   static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
   static constexpr int MMA_WARP = SWARPS + PWARPS;
