@@ -155,6 +155,25 @@ __device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4]) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v[3]), "f"(v[2]));
   return (uint32_t)a | ((uint32_t)b << 16);
 }
+// Four weights (below 2^9) as e4m3 codes and as codes of 16 times the rest, through
+// f16 pairs: the weights' own rounding to 11 bits is an eighth of the second part's.
+__device__ __forceinline__ void split_e4m3x4(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
+  uint16_t h[2], l[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t p, b, r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h[e]) : "r"(p));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h[e]));
+    // 16 p - 16 b (0x4C00 is 16 in f16)
+    asm("{\n .reg .b32 t;\n mul.rn.f16x2 t, %1, %3;\n fma.rn.f16x2 %0, %2, %4, t;\n}\n"
+        : "=r"(r)
+        : "r"(p), "r"(b), "r"(0x4C004C00u), "r"(0xCC00CC00u));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l[e]) : "r"(r));
+  }
+  hi = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
+  lo = (uint32_t)l[0] | ((uint32_t)l[1] << 16);
+}
 // 16 times what is left of four values (below 2^9) after their codes: exact in fp32
 __device__ __forceinline__ void rest_e4m3x4(uint32_t codes, float (&v)[4]) {
 #pragma unroll
@@ -191,11 +210,23 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 }
 
 template <int W>
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[W]) {
+__device__ __forceinline__ void tmem_issue(uint32_t addr, float (&v)[W]) {
   if constexpr (W == 32) tc::tmem_ld32(addr, v);
   else if constexpr (W == 16) tc::tmem_ld16(addr, v);
   else tc::tmem_ld8(addr, v);
+}
+template <int W>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[W]) {
+  tmem_issue(addr, v);
   tc::tmem_wait_ld(v);
+}
+// two blocks of columns, one wait after the other's
+template <int W>
+__device__ __forceinline__ void tmem_load2(uint32_t a, uint32_t b, float (&v)[W], float (&x)[W]) {
+  tmem_issue(a, v);
+  tmem_issue(b, x);
+  tc::tmem_wait_ld(v);
+  tc::tmem_wait_ld(x);
 }
 
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const float (&v)[8]) {
@@ -746,10 +777,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // Scores of a tile into v: raw, or (F8) joined, scaled and with log2 vs added;
     // then minus the references.
     auto load_scores = [&](uint32_t addr, float c, float lv, const float* qe) {
-      tmem_load(addr, v);
-      if constexpr (C::F8) {
+      if constexpr (!C::F8) {
+        tmem_load(addr, v);
+      } else {
         float x[HG];
-        tmem_load(addr + N, x);
+        tmem_load2(addr, addr + N, v, x);
 #pragma unroll
         for (int u = 0; u < HG; u += 2) {
           fma2(x[u], x[u + 1], 0.0625f, v[u], v[u + 1]);
@@ -768,13 +800,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       }
     };
     Walk wf = start;  // the tile whose entry was loaded last
-    if (total > 0) {
-      e_next = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
-      if (C::E4) load_scales(e_next, wf.hk);
-    }
-    if (C::E4 && total > 1) {
-      walk_next(wf);
-      e_far = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+    int ahead = 0;    // tiles whose entries were loaded
+    auto next_entry = [&]() -> int {
+      if (ahead >= total) return -1;
+      if (ahead++) walk_next(wf);
+      return entry_of(wf.t, (tile0 + wf.i) * 128 + row);
+    };
+    e_next = next_entry();
+    if (C::E4) {
+      load_scales(e_next, wf.hk);
+      e_far = next_entry();
       hk_far = wf.hk;
     }
     Walk w = start;
@@ -801,10 +836,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
         const uint32_t o_addr = tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
         float o[HG];
-        tmem_load(o_addr, o);
-        if constexpr (C::F32 || C::F8) {
+        if constexpr (!C::F32 && !C::F8) {
+          tmem_load(o_addr, o);
+        } else {
           float y[HG];
-          tmem_load(o_addr + NP, y);
+          tmem_load2(o_addr, o_addr + NP, o, y);
 #pragma unroll
           for (int u = 0; u < HG; ++u) o[u] = C::F8 ? __fmaf_rn(y[u], 0.0625f, o[u]) : o[u] + y[u];
         }
@@ -851,15 +887,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
         const float c = valid ? c_scale * ks_next : 0.0f;
         const float vs = vs_next;  // (F8: its log2)
-        if (C::E4) {
+        if constexpr (C::E4) {
           e_next = e_far;
           load_scales(e_next, hk_far);
-        }
-        if (g + (C::E4 ? 2 : 1) < total) {
-          walk_next(wf);
-          const int e = entry_of(wf.t, (tile0 + wf.i) * 128 + row);
-          (C::E4 ? e_far : e_next) = e;
+          e_far = next_entry();
           hk_far = wf.hk;
+        } else {
+          e_next = next_entry();
         }
         bool ok = wait_bar(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -969,10 +1003,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           uint32_t hi[HG / 4], lo[HG / 4];
 #pragma unroll
           for (int u = 0; u < HG; u += 4) {
-            float y[4] = {v[u], v[u + 1], v[u + 2], v[u + 3]};
-            hi[u / 4] = to_e4m3x4(y);
-            rest_e4m3x4(hi[u / 4], y);
-            lo[u / 4] = to_e4m3x4(y);
+            const float y[4] = {v[u], v[u + 1], v[u + 2], v[u + 3]};
+            split_e4m3x4(y, hi[u / 4], lo[u / 4]);
           }
           // head c0 is byte c0 of the row, its second part byte 64 + c0
           uint8_t* dst = p_dst + (row >> 3) * 1024 + (row & 7) * 128 + (c0 & 15);
