@@ -20,6 +20,12 @@ cudaError_t launch_attend_backward_d128(const att::Args& a, bool out_f32, int sm
 namespace att {
 namespace {
 
+// Byte offsets of cache rows are 64-bit products of two 32-bit factors.
+hytopk_status check_row(int64_t row, int bytes) {
+  if (row < 0) return HYTOPK_INVALID_ARG;
+  return row >= ((int64_t)1 << 32) / bytes ? HYTOPK_UNSUPPORTED : HYTOPK_OK;
+}
+
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 hytopk_status check(int n, int L, int Hq, int Hkv, int d, int k_top, hytopk_elem out_type,
@@ -53,6 +59,9 @@ extern "C" hytopk_status hytopk_attend(const void* q, int64_t q_row, const void*
   if (n == 0) return HYTOPK_OK;
   if (!q || !k || !v || !idx || !out) return HYTOPK_INVALID_ARG;
   if (e4 != (k_scale != nullptr) || e4 != (v_scale != nullptr)) return HYTOPK_INVALID_ARG;
+  s = att::check_row(k_row, e4 ? 1 : 2);
+  if (s == HYTOPK_OK) s = att::check_row(v_row, e4 ? 1 : 2);
+  if (s != HYTOPK_OK) return s;
   const int per16 = e4 ? 16 : 8;
   if (!att::aligned(q, 16) || !att::aligned(k, 16) || !att::aligned(v, 16) ||
       !att::aligned(out, 16) || !att::aligned(idx, 4) || !att::aligned(lse, 4) ||
@@ -95,6 +104,10 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
                                                 float* dk, float* dv, int accumulate,
                                                 uint32_t* dev_status, cudaStream_t stream) {
   hytopk_status s = att::check(n, L, Hq, Hkv, d, k_top, out_type, false);
+  if (s != HYTOPK_OK) return s;
+  s = att::check_row(k_row, 2);
+  if (s == HYTOPK_OK) s = att::check_row(v_row, 2);
+  if (s == HYTOPK_OK) s = att::check_row((int64_t)Hkv * d, sizeof(float));
   if (s != HYTOPK_OK) return s;
   if (n == 0 && accumulate) return HYTOPK_OK;
   if (!dk || !dv) return HYTOPK_INVALID_ARG;

@@ -267,7 +267,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
           *reinterpret_cast<uint4*>(smem + C::G_OFF + off) = x[u];
         }
       }
-      tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_full);
       return true;
@@ -374,6 +373,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
         for (int k = 0; k < 2 && ok; ++k) {  // dV, dK
           ok = wait(k ? dk_empty : dv_empty, (g & 1) ^ 1) && wait(k ? ds_full : p_full, g & 1);
           if (!ok) break;
+          tc::fence_proxy_async_smem();
           tc::fence_after_sync();
           if (elect_one()) {
             rows_product(k ? C::DK_COL : C::DV_COL, k ? q_lo : g_lo, k ? s_lo : p_lo);
@@ -473,7 +473,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
           }
           store_parts<CH>(dst, row, c0 + cc, p);
         }
-        tc::fence_proxy_async_smem();
         if (pass) {
           // scores and the item's sums are read: both may be replaced
           tc::fence_before_sync();

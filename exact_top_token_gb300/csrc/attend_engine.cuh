@@ -16,10 +16,11 @@
 //
 // Softmax without a running maximum per tile. The weights p = 2^(s - m) are
 // stored in bf16 and summed in fp32, both with 8 exponent bits, so m need not
-// be the maximum: any m within 2^64 of it gives the same relative precision.
+// be the maximum: any m well within 2^126 of it gives the same relative precision.
 // m is the column maximum of the first tile with a valid row; later tiles only
-// test s - m <= 64 (one vote of the warpgroup per tile), and the rare tile that
-// fails raises m and scales O and the sums.
+// test s - m <= 24 in powers of two (one vote of the warpgroup per tile; a weight of
+// 2^24 times V below 2^88 still sums in fp32), and the rare tile that fails raises m
+// and scales O and the sums.
 //
 // fp32 results: P is written as three bf16 parts (24 bits); the first two are
 // multiplied side by side (twice the columns) and the third adds to the second's,
@@ -28,20 +29,19 @@
 // result), so O is read out and added up in registers every kChunk tiles. bf16
 // results use one part, whose rounding is of the size of the result's own.
 //
-// e4m3 rows of 128 columns with a bf16 result stay as they are in memory
-// (Cfg::F8): q and P are each written as an e4m3 part and an e4m3 part of 16
-// times the rest, side by side, and the tensor core multiplies codes. A q row is
-// scaled by a power of two to 128 <= max < 256: 8 significant bits are exact down
-// to 2^-14 of the row's maximum and never off by more than 2^-22 of it. P takes the
-// row scale of V (one exponential serves both: 2^(s + log2 vs - m), and the sum
-// divides by vs again) and lies within 2^8.5, so weights down to 2^-10 of the
-// largest keep 8 bits and the others are off by at most 2^-19 of it; m is raised
-// when a weight would pass 2^8.5. Converting the rows to bf16 on the way, as the
-// other e4m3 instances do, took 2.5 times as long.
+// e4m3 rows are widened to bf16, which holds every e4m3 value: the codes land in the
+// first half of their tile's place in shared memory and warps of their own widen them
+// there. K's row scale joins the factor of the row's scores, V's multiplies its weights.
+// 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 534 us (515 TFLOP/s, rows
+// gathered at 8.0 TB/s), e4m3 rows 712 us. Widening each row in a producer's registers
+// took 1667 us; multiplying the codes, with q and P in two e4m3 parts, 771 us; copies and
+// widening by the same warps, through a ring of its own, 742 us; widening to f16 with q
+// and P in f16 694 us, but 128 heads 1316 us instead of 1083, and small weights lost.
 //
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
 //                 columns), O read-out
-//   4 or 8 warps  producers (cp.async, or e4m3 converted to bf16 on the way)
+//   4 or 8 warps  producers: rows by cp.async, queries
+//   2 or 4 warps  e4m3 rows only: widening
 //   last warp     MMA issuer, TMEM
 // A tile is a chain of short steps in different warps, so what counts is the
 // length of each step: no division, no wait for a load and little code per tile
@@ -70,45 +70,51 @@ struct Cfg {
   static constexpr int SWG = N >= 64 ? 4 : 2;     // softmax warpgroups
   static constexpr int SWARPS = 4 * SWG;
   static constexpr int HG = N / SWG;              // head columns of each: 8, 16 or 32
-  // e4m3 rows multiplied as codes; else converted to bf16 (or bf16 as given)
-  static constexpr bool F8 = E4 && !F32 && D == 128 && N <= 64;
-  static constexpr bool CONV = E4 && !F8;
   static constexpr int PARTS = F32 ? 3 : 1;
-  // m is the maximum less kOver, and is raised when s - m passes kSlack (log2)
-  static constexpr float kOver = F8 ? 4.0f : 0.0f, kSlack = F8 ? 8.5f : 64.0f;
+  static constexpr float kSlack = 24.0f;  // m is raised when s - m passes this (log2)
   // columns of the second product: P rows are whole 128-byte atoms of 64 heads
   // (columns N.. of a narrower item are never read)
   static constexpr int NP = N < 64 ? 64 : N;
-  static constexpr int RB = F8 ? D : 2 * D;    // row bytes of the operands
-  static constexpr int SN = F8 ? 2 * N : N;    // score columns (F8: q's two parts)
+  static constexpr int RB = 2 * D;             // row bytes of the operands
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;        // one K or V tile
-  static constexpr int PBYTES = NP / 64 * 16384;  // (F8: both parts in 128-byte rows)
+  static constexpr int PBYTES = NP / 64 * 16384;
   static constexpr int OBLK = D <= 128 ? 1 : D / 128;  // blocks of 128 result columns
-  static constexpr int OCOLS = F32 || F8 ? 2 * NP : NP;      // accumulator columns of a block
-  static constexpr int QBYTES = SN * RB;
+  static constexpr int OCOLS = F32 ? 2 * NP : NP;      // accumulator columns of a block
+  static constexpr int QBYTES = N * RB;
   static constexpr int QB = N <= 64 && D <= 128 ? 2 : 1;
-  // P buffers: two, unless their three parts or 128 heads leave no room for the ring
-  static constexpr int PB = F32 || N > 64 ? 1 : 2;
-  static constexpr int PWARPS = N > 64 ? 4 : 8;
-  static constexpr int RPW = 128 / PWARPS;        // rows of a tile per producer warp
-  static constexpr int THREADS = (SWARPS + PWARPS + 1) * 32;
-  static constexpr int MMA_WARP = SWARPS + PWARPS;
+  // P buffers: two, unless their three parts, 128 heads or wide e4m3 rows leave no
+  // room for the ring
+  static constexpr int PB = F32 || N > 64 || (E4 && D == 256) ? 1 : 2;
+  // Warps that copy rows, and (e4m3) warps that widen them: as many as leave a thread 72
+  // (N = 128: 80) registers. (1024 queries of 32 heads on 8 cache heads: 1019 us with 8
+  // widening warps, 1102 with 4.)
+  static constexpr int PWARPS = E4 || N > 64 ? 4 : 8;
+  static constexpr int VWARPS = !E4 ? 0 : N > 64 ? 2 : N > 16 ? 4 : 8;
+  static constexpr int RPW = 128 / PWARPS;        // rows of a tile per copying warp
+  static constexpr int THREADS = (SWARPS + PWARPS + VWARPS + 1) * 32;
+  static constexpr int MMA_WARP = SWARPS + PWARPS + VWARPS;
   // m, scale factors, 1 / sum [N] each; per-quadrant sums or maxima [4][N]
-  // F8: q scales [2][N]
-  static constexpr int MISC = (3 + 4 + 2 * F8) * N * 4 + 64 + 448;
-  static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + MISC + 1024;
+  static constexpr int MISC = (3 + 4) * N * 4 + 512;
+  static constexpr int SR = E4 ? 8 : 0;           // tiles of k and v scales [2][128]
+  static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + SR * 1024 + MISC + 1024;
   static constexpr int NS_MAX = (227 * 1024 - FIXED) / SLOT;
   static constexpr int NS = NS_MAX < 8 ? NS_MAX : 8;
   static constexpr int RING_OFF = 0;
   static constexpr int P_OFF = NS * SLOT;
   static constexpr int Q_OFF = P_OFF + PB * PARTS * PBYTES;
-  static constexpr int MISC_OFF = Q_OFF + QB * QBYTES;
+  static constexpr int SCALE_OFF = Q_OFF + QB * QBYTES;
+  static constexpr int MISC_OFF = SCALE_OFF + SR * 1024;
   static constexpr int SMEM = MISC_OFF + MISC + 1024;
   static constexpr int S_COL = 0, O_COL = 256;
-  static_assert(2 * SN <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
+  static_assert(2 * N <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
   static_assert(NS >= 2 && SMEM <= 227 * 1024, "shared memory");
   static_assert(NS * SLOT >= N * D * 4, "partial results of a split item");
+  // Scales of tile j are copied once K's slot of the ring is free: V's before with NS
+  // odd, so the softmax is done with tile j - (NS + 1) / 2; K's with NS even, so the
+  // scores of tile j - NS / 2 are done, and for them the softmax has read tile
+  // j - NS / 2 - 2.
+  static_assert(!E4 || SR >= (NS % 2 ? (NS + 1) / 2 : NS / 2 + 2), "scales");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -146,44 +152,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// four values as e4m3 codes (nearest even, saturating; the first in the low byte)
-__device__ __forceinline__ uint32_t to_e4m3x4(const float (&v)[4]) {
-  uint16_t a, b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(v[1]), "f"(v[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(v[3]), "f"(v[2]));
-  return (uint32_t)a | ((uint32_t)b << 16);
-}
-// Four weights (below 2^9) as e4m3 codes and as codes of 16 times the rest, through
-// f16 pairs: the weights' own rounding to 11 bits is an eighth of the second part's.
-__device__ __forceinline__ void split_e4m3x4(const float (&v)[4], uint32_t& hi, uint32_t& lo) {
-  uint16_t h[2], l[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    uint32_t p, b, r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h[e]) : "r"(p));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(h[e]));
-    // 16 p - 16 b (0x4C00 is 16 in f16)
-    asm("{\n .reg .b32 t;\n mul.rn.f16x2 t, %1, %3;\n fma.rn.f16x2 %0, %2, %4, t;\n}\n"
-        : "=r"(r)
-        : "r"(p), "r"(b), "r"(0x4C004C00u), "r"(0xCC00CC00u));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l[e]) : "r"(r));
-  }
-  hi = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
-  lo = (uint32_t)l[0] | ((uint32_t)l[1] << 16);
-}
-// 16 times what is left of four values (below 2^9) after their codes: exact in fp32
-__device__ __forceinline__ void rest_e4m3x4(uint32_t codes, float (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(codes >> (16 * e))));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    v[2 * e] = (v[2 * e] - x.x) * 16.0f;
-    v[2 * e + 1] = (v[2 * e + 1] - x.y) * 16.0f;
-  }
 }
 
 // the two values minus their bf16 parts (exact)
@@ -276,6 +244,21 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                "r"(valid ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t src) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t dst, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -326,9 +309,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   float* f_s = nm_s + N;                                       // [N] factor of a raised reference
   float* il_s = f_s + N;                                      // [N] 1 / sum (split: the sum)
   float* quad_s = il_s + N;                                   // [4][N]
-  float* qe_s = quad_s + 4 * N;                               // F8: [2][N] scales of q rows
-  float* vm_s = qe_s + 2 * C::F8 * N;                         // F8: [4][4] maxima of log2 vs
-  uint64_t* bars = reinterpret_cast<uint64_t*>(vm_s + 16);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(quad_s + 4 * N);
   uint64_t* full = bars;
   uint64_t* empty = full + NS;
   uint64_t* q_full = empty + NS;
@@ -339,7 +320,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   uint64_t* p_empty = p_full + 2;
   uint64_t* o_full = p_empty + 2;
   uint64_t* o_empty = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 2);
+  uint64_t* landed = o_empty + 2;  // e4m3: [NS] codes are there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + NS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // through a shuffle, so that the compiler knows the roles' branches are uniform
@@ -349,12 +331,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   if (pl.splits > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(full + i, C::CONV ? C::PWARPS : C::PWARPS * 32);
+      tc::mbar_init(full + i, C::E4 ? C::VWARPS : C::PWARPS * 32);
+      tc::mbar_init(landed + i, C::PWARPS * 32);
       tc::mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full + i, C::PWARPS);
-      tc::mbar_init(q_empty + i, C::F8 ? 1 + C::SWARPS : 1);
+      tc::mbar_init(q_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(s_empty + i, C::SWARPS);
       tc::mbar_init(o_full + i, 1);
@@ -418,13 +401,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   };
   auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
-  if (warp >= C::SWARPS && warp < C::MMA_WARP) {
+  if (warp >= C::SWARPS && warp < C::SWARPS + C::PWARPS) {
     // ---------------- producers ----------------
     const int tid = threadIdx.x - C::SWARPS * 32;
     const int pw = warp - C::SWARPS;
     // this warp's writes to a buffer are done: one arrival per warp
     auto publish = [&](uint64_t* bar) {
-      tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar);
     };
@@ -456,202 +438,118 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         for (int u = 0; u < QU; ++u) {
           const int f = (p + u) * C::PWARPS * 32 + tid, r = f / QCPR, c = f % QCPR;
           if (N * QCPR % (C::PWARPS * 32) && f >= N * QCPR) continue;
-          if constexpr (!C::F8) {
-            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v[u];
-          } else {
-            // 16 lanes hold a row: its scale, then both parts of 8 values a lane
-            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            float x[8], amax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[2 * e] = __uint_as_float(w[e] << 16);
-              x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-              amax = max3(amax, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
-            }
-#pragma unroll
-            for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // 2^e with 128 <= amax / 2^e < 256 (e >= -120: both factors are normal)
-            const int ex = max((int)(__float_as_uint(amax) >> 23) - 7, 7);
-            const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float y[4] = {x[4 * e] * down, x[4 * e + 1] * down, x[4 * e + 2] * down,
-                            x[4 * e + 3] * down};
-              hi[e] = to_e4m3x4(y);
-              rest_e4m3x4(hi[e], y);
-              lo[e] = to_e4m3x4(y);
-            }
-            const uint32_t half = (uint32_t)(c & 1) * 8;
-            *reinterpret_cast<uint2*>(dst + Geo::chunk_offset(r, c / 2, C::SN) + half) =
-                make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + Geo::chunk_offset(N + r, c / 2, C::SN) + half) =
-                make_uint2(lo[0], lo[1]);
-            if (c == 0) qe_s[qb * N + r] = __uint_as_float((uint32_t)ex << 23);
-          }
+          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, c, N)) = v[u];
         }
       }
       publish(q_full + qb);
       return true;
     };
-    if constexpr (!C::CONV) {
-      // Warp w gathers rows RPW w .. of every tile, CPR lanes per row. The tile's
-      // period was these loops at one time: rows come from their lanes first, a
-      // source address is one multiply-add, and the swizzled destinations repeat
-      // every 8 rows.
-      constexpr int CPR = C::RB / 16;              // 8, 16 or 32 lanes a row
-      constexpr int SHIFT = CPR == 32 ? 5 : (CPR == 16 ? 4 : 3);
-      constexpr int RPP = 32 / CPR;
-      constexpr int PASSES = C::RPW / RPP;
-      constexpr int ES = C::F8 ? 1 : 2;
-      const int c = lane & (CPR - 1);
-      uint32_t pat[8 / RPP];
+    // Warp w gathers rows RPW w .. of every tile, CPR lanes per row. The tile's
+    // period was these loops at one time: rows come from their lanes first, a
+    // source address is one multiply-add, and the swizzled destinations repeat
+    // every 8 rows. The codes of an e4m3 row take the first 128-byte lines of its place
+    // (a row's pieces that went to several lines were fetched one by one).
+    constexpr int ES = C::E4 ? 1 : 2;
+    constexpr int CPR = D * ES / 16;  // 4, 8, 16 or 32 lanes a row
+    constexpr int SHIFT = CPR == 32 ? 5 : CPR == 16 ? 4 : CPR == 8 ? 3 : 2;
+    constexpr int RPP = 32 / CPR;
+    constexpr int PASSES = C::RPW / RPP;
+    const int c = lane & (CPR - 1);
+    uint32_t pat[8 / RPP];
 #pragma unroll
-      for (int p = 0; p < 8 / RPP; ++p) {
-        const uint32_t r = p * RPP + (lane >> SHIFT);
-        pat[p] = (uint32_t)(c >> 3) * 16384 + pw * C::RPW * 128 + r * 128 + (((c & 7) ^ r) << 4);
-      }
-      int slot = 0;
-      uint32_t phase = 1;
-      bool ok = true;
-      Walk w = start, wn = w;  // this tile; the next one
-      int qi = 0;
-      int e_next = total > 0 ? entry_of(w.t, tile0 * 128 + pw * C::RPW + lane % C::RPW) : -1;
+    for (int p = 0; p < 8 / RPP; ++p) {
+      const uint32_t r = p * RPP + (lane >> SHIFT);
+      pat[p] = (uint32_t)(c >> 3) * 16384 + pw * C::RPW * 128 + r * 128 + (((c & 7) ^ r) << 4);
+    }
+    const uint32_t scale0 = tc::smem_u32(smem + C::SCALE_OFF) + (pw * C::RPW + lane) * 4;
+    int slot = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    Walk w = start, wn = w;  // this tile; the next one
+    int qi = 0;
+    int e_next = total > 0 ? entry_of(w.t, tile0 * 128 + pw * C::RPW + lane % C::RPW) : -1;
 #pragma unroll 1
-      for (int g = 0; g < total && ok; ++g, w = wn) {
-        // an item's queries load while its first rows do
-        uint4 qv[QU];
-        if (w.i == 0) fetch_query(w, 0, qv);
-        const int s_own = row_of(e_next);
-        int rows[PASSES];
+    for (int g = 0; g < total && ok; ++g, w = wn) {
+      // an item's queries load while its first rows do
+      uint4 qv[QU];
+      if (w.i == 0) fetch_query(w, 0, qv);
+      const int s_own = row_of(e_next);
+      int rows[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        rows[p] = __shfl_sync(0xffffffffu, s_own, p * RPP + (lane >> SHIFT));
+      if (g + 1 < total) {
+        walk_next(wn);
+        e_next = entry_of(wn.t, (tile0 + wn.i) * 128 + pw * C::RPW + lane % C::RPW);
+      }
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = __all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status));
+        if (!ok) break;
+        const uint32_t dst = tc::smem_u32(ring + slot * C::SLOT);
+        const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) +
+                              (size_t)w.hk * D * ES + c * 16;
+        const uint32_t row_bytes = (uint32_t)((kv ? a.v_row : a.k_row) * ES);
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
-          rows[p] = __shfl_sync(0xffffffffu, s_own, p * RPP + (lane >> SHIFT));
-        if (g + 1 < total) {
-          walk_next(wn);
-          e_next = entry_of(wn.t, (tile0 + wn.i) * 128 + pw * C::RPW + lane % C::RPW);
+          cp_async16(dst + pat[p % (8 / RPP)] + p * RPP / 8 * 1024,
+                     base + (uint64_t)(uint32_t)max(rows[p], 0) * row_bytes, rows[p] >= 0);
+        // arrives for this thread when its copies so far have landed; the MMA
+        // issuer's proxy fence makes them visible to the tensor core
+        if (C::E4 && kv == 0) {
+          // with K's, the scales of this warp's rows (0 for no row)
+          const uint32_t sc = scale0 + (g & (C::SR - 1)) * 1024;
+          const size_t at = (size_t)max(s_own, 0) * a.Hkv + w.hk;
+          cp_async4(sc, a.k_scale + at, s_own >= 0);
+          cp_async4(sc + 512, a.v_scale + at, s_own >= 0);
         }
+        cp_async_arrive((C::E4 ? landed : full) + slot);
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        // Between K and V: with two slots V waits for the product of the tile before,
+        // which the MMA issuer starts only after this tile's scores.
+        if (kv == 0 && w.i == 0 && !(ok = store_query(qi++, w, qv))) break;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (C::E4 && warp >= C::SWARPS + C::PWARPS && warp < C::MMA_WARP) {
+    // ---------------- e4m3: codes to bf16, in place ----------------
+    // A lane takes 8 codes to one 16-byte chunk, LPR lanes a row; all codes of the rows
+    // at hand are read before the first chunk is written.
+    constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPP = 32 / LPR;
+    constexpr int ROWS = 128 / (C::VWARPS ? C::VWARPS : 1);
+    constexpr int U = 8 / RPP;  // passes at a time: the swizzle repeats every 8 rows
+    const int cl = lane % LPR, rl = lane / LPR;
+    uint32_t src[U], dst[U];
+#pragma unroll
+    for (int p = 0; p < U; ++p) {
+      const int r = (warp - C::SWARPS - C::PWARPS) * ROWS + p * RPP + rl;
+      src[p] = tc::smem_u32(ring) + Geo::chunk_offset(r, cl / 2, 128) + (cl & 1) * 8;
+      dst[p] = tc::smem_u32(ring) + Geo::chunk_offset(r, cl, 128);
+    }
+    int slot = 0;
+    uint32_t phase = 0;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status));
-          if (!ok) break;
-          const uint32_t dst = tc::smem_u32(ring + slot * C::SLOT);
-          const uint8_t* base = static_cast<const uint8_t*>(kv ? a.v : a.k) +
-                                (size_t)w.hk * C::RB + c * 16;
-          const uint32_t row_bytes = (uint32_t)((kv ? a.v_row : a.k_row) * ES);
+    for (int h = 0; h < 2 * total; ++h) {
+      if (!__all_sync(0xffffffffu, wait_bar(landed + slot, phase, abort_flag, a.status))) break;
+      const uint32_t at = slot * C::SLOT;
 #pragma unroll
-          for (int p = 0; p < PASSES; ++p)
-            cp_async16(dst + pat[p % (8 / RPP)] + p * RPP / 8 * 1024,
-                       base + (uint64_t)(uint32_t)max(rows[p], 0) * row_bytes, rows[p] >= 0);
-          // arrives for this thread when its copies so far have landed; the MMA
-          // issuer's proxy fence makes them visible to the tensor core
-          cp_async_arrive(full + slot);
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-          // Between K and V: with two slots V waits for the product of the tile before,
-          // which the MMA issuer starts only after this tile's scores.
-          if (kv == 0 && w.i == 0 && !(ok = store_query(qi++, w, qv))) break;
-        }
+      for (int r8 = 0; r8 < ROWS / 8; ++r8) {
+        uint2 x[U];
+#pragma unroll
+        for (int p = 0; p < U; ++p) x[p] = ld_shared8(src[p] + at + r8 * 1024);
+        __syncwarp();
+#pragma unroll
+        for (int p = 0; p < U; ++p)
+          st_shared16(dst[p] + at + r8 * 1024, e4m3x8_to_bf16(x[p]));
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-      // Warp w converts rows RPW w .. of every tile, CPR lanes of 16 codes
-      // per row. A tile is two or four chunks of up to 8 loads a lane (K's, then
-      // V's); two chunks are in registers, so that one is always in flight.
-      constexpr int CPR = D / 16;          // 4, 8 or 16
-      constexpr int RPP = 32 / CPR;
-      constexpr int PASSES = C::RPW / RPP;
-      constexpr int CP = PASSES < 8 ? PASSES : 8;  // passes of a chunk
-      constexpr int NCH = 2 * PASSES / CP;         // chunks of a tile (K and V)
-      const int c = lane % CPR;
-      uint4 buf[2][CP];
-      auto issue = [&](int hk, int s_own, int ch, uint4 (&v)[CP]) {
-        const bool isv = ch >= NCH / 2;
-        const uint8_t* base =
-            static_cast<const uint8_t*>(isv ? a.v : a.k) + (size_t)hk * D + c * 16;
-        const int64_t row_bytes = isv ? a.v_row : a.k_row;
-        const int p0 = (ch % (NCH / 2)) * CP;
-        int rows[CP];
-#pragma unroll
-        for (int p = 0; p < CP; ++p)
-          rows[p] = __shfl_sync(0xffffffffu, s_own, (p0 + p) * RPP + lane / CPR);
-#pragma unroll
-        for (int p = 0; p < CP; ++p)
-          v[p] = rows[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(base + rows[p] * row_bytes))
-                              : make_uint4(0, 0, 0, 0);
-      };
-      int slot = 0;
-      uint32_t phase = 1;
-      auto store = [&](int ch, const uint4 (&v)[CP]) -> bool {
-        if (ch % (NCH / 2) == 0 &&
-            !__all_sync(0xffffffffu, wait_bar(empty + slot, phase, abort_flag, a.status)))
-          return false;
-        uint8_t* dst = ring + slot * C::SLOT;
-        const int p0 = (ch % (NCH / 2)) * CP;
-#pragma unroll
-        for (int p = 0; p < CP; ++p) {
-          const int r = pw * C::RPW + (p0 + p) * RPP + lane / CPR;
-          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c, 128)) =
-              e4m3x8_to_bf16(make_uint2(v[p].x, v[p].y));
-          *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(r, 2 * c + 1, 128)) =
-              e4m3x8_to_bf16(make_uint2(v[p].z, v[p].w));
-        }
-        if (ch % (NCH / 2) == NCH / 2 - 1) {
-          publish(full + slot);
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        }
-        return true;
-      };
-      Walk w = start, wn = w;  // this tile; the next one
-      int qi = 0;
-      auto own = [&](const Walk& x) {
-        return entry_of(x.t, (tile0 + x.i) * 128 + pw * C::RPW + lane % C::RPW);
-      };
-      int s_own = total > 0 ? row_of(own(w)) : -1, s_next = -1;
-      if (total > 0) {
-        issue(w.hk, s_own, 0, buf[0]);
-        issue(w.hk, s_own, 1, buf[1]);
-      }
-      if (total > 1) {
-        walk_next(wn);
-        s_next = row_of(own(wn));
-      }
-      // the entry of the tile after the next is in flight while a tile is stored
-      Walk wf = wn;
-      int e_far = -1;
-      if (total > 2) {
-        walk_next(wf);
-        e_far = own(wf);
-      }
-      bool ok = true;
-      for (int g = 0; g < total && ok; ++g) {
-        if (w.i == 0) {
-          uint4 qv[QU];
-          fetch_query(w, 0, qv);
-          if (!store_query(qi++, w, qv)) break;
-        }
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          if (!store(ch, buf[ch & 1])) {
-            ok = false;
-            break;
-          }
-          if (ch + 2 < NCH) issue(w.hk, s_own, ch + 2, buf[ch & 1]);
-          else if (g + 1 < total) issue(wn.hk, s_next, ch + 2 - NCH, buf[ch & 1]);
-        }
-        w = wn;
-        wn = wf;
-        s_own = s_next;
-        s_next = row_of(e_far);
-        if (g + 3 < total) {
-          walk_next(wf);
-          e_far = own(wf);
-        }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full + slot);
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
   } else if (warp == C::MMA_WARP) {
@@ -659,11 +557,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     // The whole warp keeps the (uniform) state and waits; one elected lane
     // issues. A single-lane branch would move every descriptor word through the
     // vector registers, which took 100 cycles per product.
-    constexpr int KIND = C::F8 ? 1 : 0;
-    constexpr int SB = C::F8 ? 4096 : 2048;  // bytes of the 32 or 16 rows of a step
-    constexpr uint32_t ID_S = tc::instr_desc(KIND, 128, C::SN);
-    constexpr uint32_t ID_O = tc::instr_desc(KIND, 128, NP) | (1u << 15) | (1u << 16);
-    constexpr uint32_t ID_O2 = tc::instr_desc(KIND, 128, C::OCOLS) | (1u << 15) | (1u << 16);
+    constexpr uint32_t ID_S = tc::instr_desc(0, 128, N);
+    constexpr uint32_t ID_O = tc::instr_desc(0, 128, NP) | (1u << 15) | (1u << 16);
+    constexpr uint32_t ID_O2 = tc::instr_desc(0, 128, C::OCOLS) | (1u << 15) | (1u << 16);
     constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
     // 14 address bits: in a cluster, shared addresses carry the CTA's rank above them
     auto low = [](const void* p) { return (tc::smem_u32(p) >> 4) & 0x3FFFu; };
@@ -695,16 +591,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (ws.i == 0 && !wait(q_full + qb, (ws.qi / C::QB) & 1)) return false;
       if (!wait(full + ws.slot, ws.phase)) return false;
       if (!wait(s_empty + (g & 1), ((g >> 1) & 1) ^ 1)) return false;
-      if (!C::CONV) tc::fence_proxy_async_smem();
+      tc::fence_proxy_async_smem();
       tc::fence_after_sync();
       const uint32_t ad = (ring_lo + ws.slot * (C::SLOT >> 4)) | LBO_K;
       const uint32_t bd = (q_lo + qb * (C::QBYTES >> 4)) | LBO_K;
       if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < C::RB / 32; ++j)
-          tc::mma<KIND>(tmem + C::S_COL + (g & 1) * C::SN,
+          tc::mma<0>(tmem + C::S_COL + (g & 1) * N,
                         desc(ad + (Geo::step_offset(j, 128) >> 4)),
-                        desc(bd + (Geo::step_offset(j, C::SN) >> 4)), ID_S, j > 0 ? 1u : 0u);
+                        desc(bd + (Geo::step_offset(j, N) >> 4)), ID_S, j > 0 ? 1u : 0u);
         tc::mma_commit(s_full + (g & 1));
         tc::mma_commit(empty + ws.slot);
         if (ws.i == ntile - 1) tc::mma_commit(q_empty + qb);
@@ -719,7 +615,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       if (ic == 0 && !wait(o_empty + ob, ((nc >> 1) & 1) ^ 1)) return false;
       if (!wait(full + wo.slot, wo.phase)) return false;
       if (!wait(p_full + pb, (g / C::PB) & 1)) return false;
-      if (!C::CONV) tc::fence_proxy_async_smem();
+      tc::fence_proxy_async_smem();
       tc::fence_after_sync();
       const uint32_t ad = (ring_lo + wo.slot * (C::SLOT >> 4)) | LBO_MN;
       const uint32_t bd = (p_lo + pb * (C::PARTS * C::PBYTES >> 4)) | LBO_MN;
@@ -729,12 +625,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
 #pragma unroll
           for (int part = 0; part < C::PARTS; part += 2) {
 #pragma unroll
-            for (int s = 0; s < (C::F8 ? 4 : 8); ++s)  // 32 bytes of P's type: 16 or 32 rows
+            for (int s = 0; s < 8; ++s)  // 16 rows
               // d = 64 has one 64-column atom; the second one that M = 128 takes is
               // whatever follows the tile, and fills accumulator lanes never read
-              tc::mma<KIND>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
-                         desc(ad + ((blk * 32768 + s * SB) >> 4)),
-                         desc(bd + ((part * C::PBYTES + s * SB) >> 4)), part ? ID_O : ID_O2,
+              tc::mma<0>(tmem + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + (part ? NP : 0),
+                         desc(ad + ((blk * 32768 + s * 2048) >> 4)),
+                         desc(bd + ((part * C::PBYTES + s * 2048) >> 4)), part ? ID_O : ID_O2,
                          (ic > 0 || part > 0 || s > 0) ? 1u : 0u);
           }
         }
@@ -764,41 +660,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     constexpr int LPC = 32 / HG;  // lanes that share a column after reduce_columns
     float l[HG], v[HG];
     bool have = false;  // some row of the item so far is valid (the same for the warpgroup)
-    // this row's entry as stored: of the next tile (e4m3: and of the one after,
-    // since the scales of the next tile's row are loaded a tile ahead too)
-    int e_next = -1, e_far = -1, hk_far = 0;
-    float ks_next = 1.0f, vs_next = 1.0f;
-    auto load_scales = [&](int e, int hk) {
-      const int s = row_of(e);
-      ks_next = s >= 0 ? __ldg(a.k_scale + (size_t)s * a.Hkv + hk) : 1.0f;
-      vs_next = s >= 0 ? __ldg(a.v_scale + (size_t)s * a.Hkv + hk) : 1.0f;
-    };
-    float vmax = 0.0f;  // F8: largest log2 vs of the item's first rows; scales its sums
-    // Scores of a tile into v: raw, or (F8) joined, scaled and with log2 vs added;
-    // then minus the references.
-    auto load_scores = [&](uint32_t addr, float c, float lv, const float* qe) {
-      if constexpr (!C::F8) {
-        tmem_load(addr, v);
-      } else {
-        float x[HG];
-        tmem_load2(addr, addr + N, v, x);
-#pragma unroll
-        for (int u = 0; u < HG; u += 2) {
-          fma2(x[u], x[u + 1], 0.0625f, v[u], v[u + 1]);
-          v[u] = x[u];
-          v[u + 1] = x[u + 1];
-          mul2(v[u], v[u + 1], qe[u], qe[u + 1]);
-          fma2(v[u], v[u + 1], c, lv, lv);
-        }
-      }
-    };
-    auto shift = [&](float c) {
-#pragma unroll
-      for (int u = 0; u < HG; u += 2) {
-        if constexpr (C::F8) add2(v[u], v[u + 1], nm_s[c0 + u], nm_s[c0 + u + 1]);
-        else fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
-      }
-    };
+    int e_next = -1;  // this row's entry as stored, of the next tile
     Walk wf = start;  // the tile whose entry was loaded last
     int ahead = 0;    // tiles whose entries were loaded
     auto next_entry = [&]() -> int {
@@ -807,11 +669,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
       return entry_of(wf.t, (tile0 + wf.i) * 128 + row);
     };
     e_next = next_entry();
-    if (C::E4) {
-      load_scales(e_next, wf.hk);
-      e_far = next_entry();
-      hk_far = wf.hk;
-    }
     Walk w = start;
     int qi = 0;
     // An accumulation of O that is still to be read: the item before, or (fp32) a
@@ -836,13 +693,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         if (blk * 128 + quad * 32 >= D || c0 >= pend_nh) continue;
         const uint32_t o_addr = tmem + lane_off + C::O_COL + (ob * C::OBLK + blk) * C::OCOLS + c0;
         float o[HG];
-        if constexpr (!C::F32 && !C::F8) {
+        if constexpr (!C::F32) {
           tmem_load(o_addr, o);
         } else {
           float y[HG];
           tmem_load2(o_addr, o_addr + NP, o, y);
 #pragma unroll
-          for (int u = 0; u < HG; ++u) o[u] = C::F8 ? __fmaf_rn(y[u], 0.0625f, o[u]) : o[u] + y[u];
+          for (int u = 0; u < HG; ++u) o[u] += y[u];
         }
         if constexpr (C::F32) {
 #pragma unroll
@@ -885,26 +742,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         }
         const bool valid = row_of(e_next) >= 0;
         if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-        const float c = valid ? c_scale * ks_next : 0.0f;
-        const float vs = vs_next;  // (F8: its log2)
-        if constexpr (C::E4) {
-          e_next = e_far;
-          load_scales(e_next, hk_far);
-          e_far = next_entry();
-          hk_far = wf.hk;
-        } else {
-          e_next = next_entry();
-        }
+        e_next = next_entry();
         bool ok = wait_bar(s_full + (g & 1), (g >> 1) & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         tc::fence_after_sync();
-        const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * C::SN + c0;
-        const float lv = C::F8 ? __log2f(vs) : 0.0f;
-        const float* qe = qe_s + (qi % C::QB) * N + c0;
-        load_scores(s_addr, c, lv, qe);
+        const uint32_t s_addr = tmem + lane_off + C::S_COL + (g & 1) * N + c0;
+        const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) +
+                          (g & (C::SR - 1)) * 256 + row;
+        const float c = !valid ? 0.0f : C::E4 ? c_scale * sc[0] : c_scale;
+        const float vs = C::E4 ? sc[128] : 1.0f;
+        tmem_load(s_addr, v);
         bool over = !have && valid;
         if (have) {
-          shift(c);
+#pragma unroll
+          for (int u = 0; u < HG; u += 2)
+            fma2(v[u], v[u + 1], c, nm_s[c0 + u], nm_s[c0 + u + 1]);
           float top = -INFINITY;
 #pragma unroll
           for (int u = 0; u < HG; u += 2) top = max3(top, v[u], v[u + 1]);
@@ -917,25 +769,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                                 a.status);
           if (tc::bar_or(bar, 128, !ok)) break;
           // raise (or set) the references to this tile's column maxima
-          load_scores(s_addr, c, lv, qe);
+          tmem_load(s_addr, v);
 #pragma unroll
-          for (int u = 0; u < HG; ++u) v[u] = valid ? (C::F8 ? v[u] : v[u] * c) : -INFINITY;
+          for (int u = 0; u < HG; ++u) v[u] = valid ? __fmul_rn(v[u], c) : -INFINITY;
           const float top = reduce_columns<HG, true>(v, lane);
           if (lane % LPC == 0) quad_s[quad * N + c0 + lane / LPC] = top;
-          if (C::F8 && !have) {
-            float x = valid ? lv : -INFINITY;
-            for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane == 0) vm_s[wg * 4 + quad] = x;
-          }
           tc::bar_sync(bar, 128);
-          if (C::F8 && !have)
-            vmax = fmaxf(fmaxf(vm_s[wg * 4], vm_s[wg * 4 + 1]),
-                         fmaxf(vm_s[wg * 4 + 2], vm_s[wg * 4 + 3]));
           if (row < HG) {
             const int col = c0 + row;
             const float high = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
-                                     fmaxf(quad_s[2 * N + col], quad_s[3 * N + col])) -
-                               C::kOver;
+                                     fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
             const float m = have ? fmaxf(-nm_s[col], high) : high;
             f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
             nm_s[col] = -m;
@@ -964,18 +807,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
             }
           }
           have = true;
-          load_scores(s_addr, c, lv, qe);
-          shift(c);
+          tmem_load(s_addr, v);
+          // the products rounded as the references were (packed ones would be fused with
+          // the sum): of scores of 2^30 the largest would not be 0 otherwise
+#pragma unroll
+          for (int u = 0; u < HG; ++u)  // (volatile: loaded together they spill)
+            v[u] = __fadd_rn(__fmul_rn(v[u], c), static_cast<volatile float*>(nm_s)[c0 + u]);
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(s_empty + (g & 1));
-          if (C::F8 && w.i == ntile - 1) tc::mbar_arrive(q_empty + qi % C::QB);
-        }
+        if (lane == 0) tc::mbar_arrive(s_empty + (g & 1));
         // the weights of this row, rounded (or split) to bf16
         const bool off = !valid || !have;
-        const float unscale = C::F8 ? ex2(fminf(vmax - lv, 100.0f)) : 1.0f;
         if (__any_sync(0xffffffffu, off)) {
 #pragma unroll
           for (int u = 0; u < HG; ++u) v[u] = off ? -INFINITY : v[u];
@@ -984,42 +827,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
         for (int u = 0; u < HG; u += 2) {
           v[u] = ex2(v[u]);
           v[u + 1] = ex2(v[u + 1]);
-          if constexpr (C::F8) {
-            // without the row scale again (relative to 2^vmax)
-            float x0 = v[u], x1 = v[u + 1];
-            fma2(x0, x1, unscale, l[u], l[u + 1]);
-            l[u] = x0;
-            l[u + 1] = x1;
-          } else {
-            add2(l[u], l[u + 1], v[u], v[u + 1]);
-            if (C::CONV) mul2(v[u], v[u + 1], vs, vs);
-          }
+          add2(l[u], l[u + 1], v[u], v[u + 1]);
+          if (C::E4) mul2(v[u], v[u + 1], vs, vs);
         }
         // the buffer's previous product (a failed wait ends the warpgroup together
         // at its next vote)
         wait_bar(p_empty + g % C::PB, ((g / C::PB) & 1) ^ 1, abort_flag, a.status);
         uint8_t* p_dst = pbuf + (g % C::PB) * C::PARTS * C::PBYTES;
-        if constexpr (C::F8) {
-          uint32_t hi[HG / 4], lo[HG / 4];
 #pragma unroll
-          for (int u = 0; u < HG; u += 4) {
-            const float y[4] = {v[u], v[u + 1], v[u + 2], v[u + 3]};
-            split_e4m3x4(y, hi[u / 4], lo[u / 4]);
-          }
-          // head c0 is byte c0 of the row, its second part byte 64 + c0
-          uint8_t* dst = p_dst + (row >> 3) * 1024 + (row & 7) * 128 + (c0 & 15);
-          uint8_t* at_hi = dst + (((c0 >> 4) ^ (row & 7)) << 4);
-          uint8_t* at_lo = dst + (((4 + (c0 >> 4)) ^ (row & 7)) << 4);
-          if constexpr (HG == 16) {
-            *reinterpret_cast<uint4*>(at_hi) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            *reinterpret_cast<uint2*>(at_hi) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at_lo) = make_uint2(lo[0], lo[1]);
-          }
-        }
-#pragma unroll
-        for (int part = 0; part < (C::F8 ? 0 : C::PARTS); ++part) {
+        for (int part = 0; part < C::PARTS; ++part) {
 #pragma unroll
           for (int u = 0; u < HG; u += 8) {
             uint32_t x[4];
@@ -1033,7 +849,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
           }
         }
         tc::fence_before_sync();
-        tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + g % C::PB);
       }
@@ -1058,13 +873,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
                                      (quad_s[2 * N + col] + quad_s[3 * N + col])
                                : 0.0f;
           if (pl.splits > 1) {
-            il_s[col] = C::F8 ? z * ex2(-vmax) : z;
+            il_s[col] = z;
             if (!have) nm_s[col] = INFINITY;
           } else {
-            il_s[col] = C::F8 ? ex2(vmax) / z : 1.0f / z;
+            il_s[col] = 1.0f / z;
             if (a.lse && col < nh)
               a.lse[(size_t)w.t * Hq + h0 + col] =
-                  have ? (log2f(z) - vmax - nm_s[col]) * kLn2 : -INFINITY;
+                  have ? (log2f(z) - nm_s[col]) * kLn2 : -INFINITY;
           }
         }
         tc::bar_sync(bar, 128);

@@ -143,6 +143,66 @@ def test_large_scores_and_late_maxima(hk, dev, out_dtype):
     verify(hk, torch, q, kk, vv, idx, kw, getattr(torch, out_dtype))
 
 
+@pytest.mark.parametrize("n", [1, 200])  # items split over a cluster, and not
+@pytest.mark.parametrize("Hq,d,out_dtype", [(20, 64, "bfloat16"), (20, 128, "bfloat16"),
+                                            (100, 128, "bfloat16"), (20, 256, "bfloat16"),
+                                            (20, 128, "float32")])
+@pytest.mark.parametrize("what", ["scores", "wide", "rising", "falling", "zero first", "tiny"])
+def test_e4m3_scales_far_apart(hk, dev, Hq, d, out_dtype, n, what):
+    """Scores that grow by hundreds along the list, and row scales of V that differ by up to
+    2^120, rise or fall along the list, are zero (the row still counts in the sum) or are the
+    smallest that there are."""
+    import torch
+
+    k, L = 640, 640
+    q, kk, vv, idx, kw = make(torch, dev, n, Hq, 1, d, k, L, "e4m3", seed=d + Hq, qmul=3.0)
+    order = torch.arange(L, device=dev, dtype=torch.int32)
+    idx = order.expand(n, k).contiguous()
+    idx[:, 5::17] = -1
+    sv, sk = kw["v_scale"], kw["k_scale"]
+    up = torch.linspace(-60.0, 60.0, L, device=dev)[:, None]
+    if what == "scores":
+        sk *= torch.linspace(0.0, 60.0, L, device=dev)[:, None]
+        sk[0] = sk[1]
+    elif what == "wide":
+        sv.copy_(torch.exp2(up[torch.randperm(L, device=dev)]))
+    elif what == "rising":
+        sv.copy_(torch.exp2(up))
+    elif what == "falling":
+        sv.copy_(torch.exp2(-up))
+    elif what == "zero first":
+        sv[:200] = 0.0
+        sv[300:310] = 0.0
+    else:
+        sv.fill_(2.0 ** -126)
+    dt = getattr(torch, out_dtype)
+    sample = torch.arange(0, n, 67, device=dev)
+    out, lse = hk.attend(q, kk, vv, idx, out_dtype=dt, **kw)
+    r = reference(q[sample], kk, vv, idx[sample], kw, d ** -0.5, 8 if dt == torch.bfloat16 else 24)
+    check("out", out[sample].float().cpu().numpy(), r["out"], r["tol_out"])
+    check("lse", lse[sample].cpu().numpy(), r["lse"], r["tol_lse"])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,d", [(12, 64), (50, 128), (100, 128), (12, 256)])
+def test_heads_do_not_touch_each_other(hk, dev, Hq, d, cache):
+    """One head 2^40 times the others and one 2^-40 times; then infinities in one head."""
+    import torch
+
+    n, k, L = 3, 200, 300
+    q, kk, vv, idx, kw = make(torch, dev, n, Hq, 1, d, k, L, cache, seed=d)
+    q[:, 3] *= 2.0 ** 40
+    q[:, 5] *= 2.0 ** -40
+    q[:, 7] = 0.0
+    verify(hk, torch, q, kk, vv, idx, kw, torch.bfloat16)
+    r = reference(q, kk, vv, idx, kw, d ** -0.5, 8)
+    q[:, 7, ::9] = float("inf")
+    out, lse = hk.attend(q, kk, vv, idx, **kw)
+    keep = [h for h in range(Hq) if h != 7]
+    check("out", out[:, keep].float().cpu().numpy(), r["out"][:, keep], r["tol_out"][:, keep])
+    check("lse", lse[:, keep].cpu().numpy(), r["lse"][:, keep], r["tol_lse"][:, keep])
+
+
 def test_empty_rows_holes_and_bad_indices(hk, dev):
     import torch
 

@@ -125,6 +125,10 @@ def test_attend_checks(lib):
     assert call(q=P((1 << 20) + 8)) == 5
     assert call(qr=516) == 5
     assert call(kr=132) == 5
+    assert call(kr=-128) == 1
+    assert call(vr=-128) == 1
+    assert call(kr=1 << 31) == 2  # a row of 4 GiB
+    assert call(vr=1 << 31) == 2
     assert call(ct=1, ks=FAKE, vs=FAKE, vr=136) == 5
     assert call(n=0, q=None, out=None) == 0
 
@@ -132,9 +136,9 @@ def test_attend_checks(lib):
 def test_attend_backward_checks(lib):
     def call(**kw):
         a = dict(q=FAKE, k=FAKE, v=FAKE, idx=FAKE, out=FAKE, ot=2, lse=FAKE, grad=FAKE, n=4, L=100,
-                 Hq=8, Hkv=2, d=64, k_top=10, dq=FAKE, dk=FAKE, dv=FAKE, add=1)
+                 Hq=8, Hkv=2, d=64, k_top=10, dq=FAKE, dk=FAKE, dv=FAKE, add=1, kr=128, vr=128)
         a.update(kw)
-        return lib.hytopk_attend_backward(a["q"], 512, a["k"], 128, a["v"], 128, a["idx"], a["out"],
+        return lib.hytopk_attend_backward(a["q"], 512, a["k"], a["kr"], a["v"], a["vr"], a["idx"], a["out"],
                                           a["ot"], a["lse"], a["grad"], a["n"], a["L"], a["Hq"],
                                           a["Hkv"], a["d"], a["k_top"], 0.125, a["dq"], a["dk"],
                                           a["dv"], a["add"], None, None)
@@ -144,6 +148,9 @@ def test_attend_backward_checks(lib):
     assert call(d=256) == 2
     assert call(ot=1) == 1
     assert call(Hkv=5) == 1
+    assert call(kr=-128) == 1
+    assert call(vr=1 << 31) == 2
+    assert call(Hq=1 << 24, Hkv=1 << 24, n=1) == 2  # a gradient row of 4 GiB
     assert call(dk=P((1 << 20) + 4)) == 5
     assert call(grad=P((1 << 20) + 2)) == 5
     assert call(n=0, q=None) == 0
