@@ -516,84 +516,35 @@ def select_twopass(q, k, w, positions, k_top, *, q_scale=None, k_scale=None, row
 
 
 # ---- around the selection: rotary positions, cache rows, attention ------------------
-# These calls also serve single tokens, where the time is the host's: their checks
-# read each attribute once, and the current stream's handle comes without a stream
-# object (a call costs 8 to 12 us instead of 20 to 28).
+# These calls also serve single tokens, where the time is the host's, so their checks,
+# allocations and calls are in a C++ module (csrc/binding.cpp).
 
-_elems = {}  # torch dtype -> ELEM_*, filled on first use
-_raw_current = None
+_module = None
 
 
-def _fast_init():
-    global _raw_current
-    import torch
+def _operators():
+    """The operators' module, loaded once (raises if it has not been built)."""
+    global _module
+    if _module is None:
+        import importlib.machinery
+        import importlib.util
 
-    _elems.update({torch.bfloat16: ELEM_BF16, torch.float32: ELEM_F32,
-                   torch.float8_e4m3fn: ELEM_E4M3, torch.uint8: ELEM_E4M3})
-    _raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return load()
+        import torch
 
-
-def _stream_handle(device, stream):
-    return _raw_current(device.index) if stream is None else stream.cuda_stream
-
-
-def _elem(name, dtype, allowed):
-    code = _elems.get(dtype)
-    if code not in allowed:
-        names = {ELEM_BF16: "bfloat16", ELEM_F32: "float32", ELEM_E4M3: "float8_e4m3fn"}
-        raise TypeError(f"{name} must be " + " or ".join(names[a] for a in allowed))
-    return code
-
-
-def _need(name, t, device, dtype, shape):
-    """A contiguous tensor of this type and shape on this device; its pointer."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _check_tensor(name, t, device, dtype, shape)
-        raise ValueError(f"{name}: wrong tensor")
-    return t.data_ptr()
-
-
-def _rows(name, t):
-    """(rows, heads, d, row stride, head stride) of [rows, heads, d] or [rows, d],
-    in elements. A stride of an axis of length 1 is never used and is replaced by
-    a packed one."""
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        n, H, d = shape
-        row, head, last = st
-    elif len(shape) == 2:
-        n, d = shape
-        H, head = 1, d
-        row, last = st
-    else:
-        raise ValueError(f"{name} must be [rows, heads, d] or [rows, d]")
-    if not t.is_cuda:
-        raise ValueError("inputs must be CUDA tensors")
-    if last != 1 and d > 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    if H == 1:
-        head = d
-    if n <= 1:
-        row = H * head
-    return n, H, d, row, head
-
-
-def _packed_rows(name, t):
-    """_rows of a tensor whose heads are contiguous within a row."""
-    n, H, d, row, head = _rows(name, t)
-    if head != d:
-        raise ValueError(f"{name}: heads must be contiguous within a row")
-    return n, H, d, row
-
-
-def _status_ptr(status, device):
-    if status is None:
-        return None
-    if status.element_size() != 4 or status.numel() < 1 or status.device != device:
-        raise ValueError("status must be a 32-bit integer tensor on the inputs' device")
-    return status.data_ptr()
+        lib = load()
+        path = _build.binding()
+        if not os.path.exists(path):
+            raise RuntimeError(f"the operators' module is not built ({path}); "
+                               "call exact_top_token_gb300.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_operators", path)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_operators", path, loader=loader))
+        loader.exec_module(module)
+        module.init(HytopkError, torch.OutOfMemoryError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.hytopk_rope, lib.hytopk_cache_write, lib.hytopk_cache_read, lib.hytopk_attend,
+            lib.hytopk_attend_backward)))
+        _module = module
+    return _module
 
 
 def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_context=None,
@@ -635,17 +586,6 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_co
     return f.float().to(device), mscale
 
 
-def _rope_params(positions, inv_freq, n, device, first, interleaved, inverse, mscale):
-    import torch
-
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rot / 2]")
-    pairs = inv_freq.shape[0]
-    return ctypes.byref(RopeParams(_need("positions", positions, device, torch.int32, (n,)),
-                                   _need("inv_freq", inv_freq, device, torch.float32, (pairs,)),
-                                   2 * pairs, first, bool(interleaved), bool(inverse), mscale))
-
-
 def rope(x, positions, inv_freq, *, first=0, interleaved=False, mscale=1.0, inverse=False,
          out=None, status=None, stream=None):
     """Rotary positions on columns [first, first + 2 len(inv_freq)) of x
@@ -653,41 +593,8 @@ def rope(x, positions, inv_freq, *, first=0, interleaved=False, mscale=1.0, inve
     other columns are copied. Pairs are (i, i + rot/2), or (2i, 2i + 1) if
     ``interleaved``. ``out=x`` works in place. ``inverse`` rotates back, which
     is also the gradient. See :func:`rope_frequencies`."""
-    import torch
-
-    lib = _lib if _elems else _fast_init()
-    n, H, d, row, head = _rows("x", x)
-    dev, dtype = x.device, x.dtype
-    code = _elem("x", dtype, (ELEM_BF16, ELEM_F32))
-    params = _rope_params(positions, inv_freq, n, dev, first, interleaved, inverse, mscale)
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=dev)
-        orow, ohead = H * d, d
-    else:
-        if out.shape != x.shape or out.dtype != dtype or out.device != dev:
-            raise ValueError("out must match x in shape, type and device")
-        _, _, _, orow, ohead = _rows("out", out)
-    st = lib.hytopk_rope(x.data_ptr(), row, head, code, n, H, d, params, out.data_ptr(), orow,
-                         ohead, _status_ptr(status, dev), _stream_handle(dev, stream))
-    if st != 0:
-        raise HytopkError(st, "hytopk_rope")
-    return out
-
-
-def _cache(cache, cache_scale):
-    """(rows, heads, d, ELEM_*, scale pointer) of a contiguous cache."""
-    import torch
-
-    L, H, d, _, _ = _rows("cache", cache)
-    if not cache.is_contiguous():
-        raise ValueError("cache must be contiguous")
-    code = _elem("cache", cache.dtype, (ELEM_E4M3, ELEM_BF16))
-    if (code == ELEM_E4M3) != (cache_scale is not None):
-        raise ValueError("an e4m3 cache needs cache_scale, a bf16 cache takes none")
-    scale = None
-    if cache_scale is not None:
-        scale = _need("cache_scale", cache_scale, cache.device, torch.float32, cache.shape[:-1])
-    return L, H, d, code, scale
+    return (_module or _operators()).rope(x, positions, inv_freq, first, interleaved, mscale,
+                                          inverse, out, status, stream)
 
 
 def cache_write(x, cache, cache_scale=None, *, slots=None, positions=None, inv_freq=None, first=0,
@@ -697,72 +604,15 @@ def cache_write(x, cache, cache_scale=None, *, slots=None, positions=None, inv_f
     ``positions`` and ``inv_freq`` are given, and quantised when the cache
     ([L, H, d] or [L, d]) is float8_e4m3fn: one scale per (row, head) in
     ``cache_scale``, as :func:`select` and :func:`attend` take them."""
-    import torch
-
-    lib = _lib if _elems else _fast_init()
-    n, H, d, row, head = _rows("x", x)
-    dev = x.device
-    code = _elem("x", x.dtype, (ELEM_BF16, ELEM_F32))
-    L, cH, cd, ccode, scale = _cache(cache, cache_scale)
-    if cache.device != dev or cH != H or cd != d:
-        raise ValueError(f"cache rows are {(cH, cd)} on {cache.device}, expected {(H, d)} on {dev}")
-    params = None
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq go together")
-    if positions is not None:
-        params = _rope_params(positions, inv_freq, n, dev, first, interleaved, False, mscale)
-    at = None if slots is None else _need("slots", slots, dev, torch.int32, (n,))
-    st = lib.hytopk_cache_write(x.data_ptr(), row, head, code, n, H, d, params, at,
-                                cache.data_ptr(), ccode, scale, L, _status_ptr(status, dev),
-                                _stream_handle(dev, stream))
-    if st != 0:
-        raise HytopkError(st, "hytopk_cache_write")
-    return cache
+    return (_module or _operators()).cache_write(x, cache, cache_scale, slots, positions, inv_freq,
+                                                 first, interleaved, mscale, status, stream)
 
 
 def cache_read(cache, cache_scale=None, *, slots=None, dtype=None, out=None, status=None,
                stream=None):
     """Cache rows ``slots`` (int32 [m]; None: all) as bf16 (default) or fp32."""
-    import torch
-
-    lib = _lib if _elems else _fast_init()
-    n, H, d, ccode, scale = _cache(cache, cache_scale)
-    L, dev, at = n, cache.device, None
-    if slots is not None:
-        n = slots.shape[0]
-        at = _need("slots", slots, dev, torch.int32, (n,))
-    shape = (n,) + tuple(cache.shape[1:])
-    if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
-    else:
-        _need("out", out, dev, dtype or out.dtype, shape)
-    code = _elem("dtype", out.dtype, (ELEM_BF16, ELEM_F32))
-    st = lib.hytopk_cache_read(cache.data_ptr(), ccode, scale, L, at, n, H, d, out.data_ptr(),
-                               code, _status_ptr(status, dev), _stream_handle(dev, stream))
-    if st != 0:
-        raise HytopkError(st, "hytopk_cache_read")
-    return out
-
-
-def _attention(q, k, v, idx):
-    """Shapes and row strides of the attention's inputs, checked."""
-    import torch
-
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
-    if k.dtype != v.dtype or k.shape != v.shape:
-        raise ValueError("k and v must have one shape and type")
-    dev = q.device
-    n, Hq, d, q_row = _packed_rows("q", q)
-    L, Hkv, dk, k_row = _packed_rows("k", k)
-    v_row = _packed_rows("v", v)[3]
-    if dk != d or k.device != dev or v.device != dev:
-        raise ValueError(f"k and v rows must be [{d}] per head on {dev}")
-    if idx.dim() != 2:
-        raise ValueError("idx must be [n, k]")
-    k_top = idx.shape[1]
-    return dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, \
-        _need("idx", idx, dev, torch.int32, (n, k_top))
+    return (_module or _operators()).cache_read(cache, cache_scale, slots, dtype, out, status,
+                                                stream)
 
 
 def attend(q, k, v, idx, *, k_scale=None, v_scale=None, scale=None, out_dtype=None, out=None,
@@ -773,31 +623,8 @@ def attend(q, k, v, idx, *, k_scale=None, v_scale=None, scale=None, out_dtype=No
     it (-1: none). ``scale`` defaults to d ** -0.5. Returns ``(out [n, Hq, d],
     lse [n, Hq])``; ``out_dtype`` bf16 (default) or fp32 (for training:
     :func:`attend_backward` then keeps fp32 accuracy)."""
-    import torch
-
-    lib = _lib if _elems else _fast_init()
-    code = _elem("k", k.dtype, (ELEM_BF16, ELEM_E4M3))
-    dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, at = _attention(q, k, v, idx)
-    if (code == ELEM_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-        raise ValueError("an e4m3 cache needs k_scale and v_scale, a bf16 cache takes none")
-    ks = vs = None
-    if k_scale is not None:
-        shape = k.shape[:-1]
-        ks = _need("k_scale", k_scale, dev, torch.float32, shape)
-        vs = _need("v_scale", v_scale, dev, torch.float32, shape)
-    if out is None:
-        out = torch.empty((n, Hq, d), dtype=out_dtype or torch.bfloat16, device=dev)
-    else:
-        _need("out", out, dev, out_dtype or out.dtype, (n, Hq, d))
-    ocode = _elem("out_dtype", out.dtype, (ELEM_BF16, ELEM_F32))
-    lse = torch.empty((n, Hq), dtype=torch.float32, device=dev)
-    st = lib.hytopk_attend(q.data_ptr(), q_row, k.data_ptr(), k_row, ks, v.data_ptr(), v_row, vs,
-                           at, n, L, Hq, Hkv, d, k_top, code,
-                           d ** -0.5 if scale is None else scale, out.data_ptr(), ocode,
-                           lse.data_ptr(), _status_ptr(status, dev), _stream_handle(dev, stream))
-    if st != 0:
-        raise HytopkError(st, "hytopk_attend")
-    return out, lse
+    return (_module or _operators()).attend(q, k, v, idx, k_scale, v_scale, scale, out_dtype, out,
+                                            status, stream)
 
 
 def attend_backward(q, k, v, idx, out, lse, grad, *, scale=None, dk=None, dv=None, status=None,
@@ -806,30 +633,5 @@ def attend_backward(q, k, v, idx, out, lse, grad, *, scale=None, dk=None, dv=Non
     in fp32, dk and dv shaped like k. ``grad`` [n, Hq, d] bf16 is the gradient
     of out. ``dk`` and ``dv`` are added to when given (both or neither; else new
     tensors are written)."""
-    import torch
-
-    lib = _lib if _elems else _fast_init()
-    _elem("k", k.dtype, (ELEM_BF16,))
-    dev, n, L, Hq, Hkv, d, k_top, q_row, k_row, v_row, at = _attention(q, k, v, idx)
-    go = _need("grad", grad, dev, torch.bfloat16, (n, Hq, d))
-    o = _need("out", out, dev, out.dtype, (n, Hq, d))
-    le = _need("lse", lse, dev, torch.float32, (n, Hq))
-    ocode = _elem("out", out.dtype, (ELEM_BF16, ELEM_F32))
-    dq = torch.empty((n, Hq, d), dtype=torch.float32, device=dev)
-    add = dk is not None
-    if add != (dv is not None):
-        raise ValueError("dk and dv go together")
-    if add:
-        _need("dk", dk, dev, torch.float32, k.shape)
-        _need("dv", dv, dev, torch.float32, v.shape)
-    else:
-        dk = torch.empty(k.shape, dtype=torch.float32, device=dev)
-        dv = torch.empty(v.shape, dtype=torch.float32, device=dev)
-    st = lib.hytopk_attend_backward(q.data_ptr(), q_row, k.data_ptr(), k_row, v.data_ptr(), v_row,
-                                    at, o, ocode, le, go, n, L, Hq, Hkv, d, k_top,
-                                    d ** -0.5 if scale is None else scale, dq.data_ptr(),
-                                    dk.data_ptr(), dv.data_ptr(), add, _status_ptr(status, dev),
-                                    _stream_handle(dev, stream))
-    if st != 0:
-        raise HytopkError(st, "hytopk_attend_backward")
-    return dq, dk, dv
+    return (_module or _operators()).attend_backward(q, k, v, idx, out, lse, grad, scale, dk, dv,
+                                                     status, stream)

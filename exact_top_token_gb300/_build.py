@@ -1,5 +1,7 @@
 """Compile the CUDA library (sm_103a) in-tree with nvcc: one object per
-translation unit, compiled in parallel, linked into ``_build/libhytopk.so``."""
+translation unit, compiled in parallel, linked into ``_build/libhytopk.so``;
+and, with the host compiler, the operators' Python module against the torch
+that is installed (``csrc/binding.cpp``)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -13,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libhytopk.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -35,18 +38,55 @@ def _inputs():
         os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
+def _older(out, inputs) -> bool:
+    return not os.path.exists(out) or any(
+        os.path.getmtime(f) > os.path.getmtime(out) for f in inputs)
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _older(LIB, _inputs())
+
+
+def binding() -> str:
+    """Path of the operators' Python module, built for this torch."""
+    import torch
+
+    return os.path.join(BUILD, f"_operators-{torch.__version__}.so")
+
+
+def _build_binding(out):
+    """Compile csrc/binding.cpp; it uses the torch libraries of the process."""
+    import sysconfig
+
+    import torch
+
+    top = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    include = [INCLUDE, os.path.join(top, "include"),
+               os.path.join(top, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include"), os.path.join(cuda, "include")]
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{i}" for i in include), BINDING_SRC, f"-L{os.path.join(top, 'lib')}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Build the library if missing or out of date; returns its path."""
-    if not force and not stale():
-        return LIB
+    """Build the library and the operators' module if missing or out of date;
+    returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
+    module = binding()
+    module_stale = force or _older(
+        module, [BINDING_SRC, os.path.join(INCLUDE, "hytopk.h"), __file__])
+    if not force and not stale():
+        if module_stale:
+            _build_binding(module)
+        return LIB
     srcs = sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
@@ -58,8 +98,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        other = ex.submit(_build_binding, module) if module_stale else None
         logs = list(ex.map(compile_one, zip(srcs, objs)))
+        if other is not None:
+            other.result()
     if verbose:
         for s, log in zip(srcs, logs):
             if log.strip():

@@ -156,6 +156,26 @@ def test_attend_backward_checks(lib):
     assert call(n=0, q=None) == 0
 
 
+def test_entry_points_refuse_what_is_no_cuda_tensor(lib):
+    import torch
+
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    pos, f, idx = torch.zeros(2, dtype=torch.int32), torch.ones(32), torch.zeros(2, 4, dtype=torch.int32)
+    calls = [lambda a: hk.rope(a, pos, f), lambda a: hk.cache_write(a, x), lambda a: hk.cache_read(a),
+             lambda a: hk.attend(a, x, x, idx), lambda a: hk.attend_backward(a, x, x, idx, x, f, x)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(x)                     # not on a GPU
+        with pytest.raises(TypeError):
+            call([1, 2])                # no tensor
+        with pytest.raises(TypeError):
+            call(None)
+    with pytest.raises(TypeError):
+        hk.rope(x)
+    with pytest.raises(TypeError):
+        hk.attend(x, x, x, idx, no_such_argument=1)
+
+
 def test_frequency_tables():
     def table(*a, **kw):
         f, m = hk.rope_frequencies(*a, device="cpu", **kw)
