@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/record_stream.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -127,14 +128,21 @@ uint32_t* status_ptr(PyObject* o, at::Device device) {
   return static_cast<uint32_t*>(t.data_ptr());
 }
 
-cudaStream_t stream_of(PyObject* o, at::Device device) {
+// The stream to launch on. `made`: what was allocated for this call on the current
+// stream; a stream given explicitly is recorded with it, so that freed memory is not
+// used anew before that stream's work is done.
+cudaStream_t stream_of(PyObject* o, at::Device device, std::initializer_list<const at::Tensor*> made) {
   if (!given(o)) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
   PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
   if (!h) throw Raised{};
   void* p = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
   if (PyErr_Occurred()) throw Raised{};
-  return static_cast<cudaStream_t>(p);
+  const cudaStream_t stream = static_cast<cudaStream_t>(p);
+  for (const at::Tensor* t : made)
+    if (t->defined())
+      t->record_stream(c10::cuda::getStreamFromExternal(stream, device.index()).unwrap());
+  return stream;
 }
 
 double number(PyObject* o) {
@@ -231,7 +239,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
     }
     void* out = made.defined() ? made.data_ptr() : THPVariable_Unpack(a[7]).data_ptr();
     uint32_t* status = status_ptr(a[8], dev);
-    const cudaStream_t stream = stream_of(a[9], dev);
+    const cudaStream_t stream = stream_of(a[9], dev, {&made});
     call("hytopk_rope", [&] {
       return p_rope(x.data_ptr(), r.row, r.head, type, r.n, r.H, r.d, &params, out, o.row, o.head,
                     status, stream);
@@ -277,7 +285,7 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const int32_t* slots =
         given(a[3]) ? static_cast<int32_t*>(need("slots", a[3], dev, at::kInt, {r.n})) : nullptr;
     uint32_t* status = status_ptr(a[9], dev);
-    const cudaStream_t stream = stream_of(a[10], dev);
+    const cudaStream_t stream = stream_of(a[10], dev, {});
     call("hytopk_cache_write", [&] {
       return p_cache_write(x.data_ptr(), r.row, r.head, type, r.n, r.H, r.d,
                            given(a[4]) ? &params : nullptr, slots, cache.data_ptr(), c.type,
@@ -313,7 +321,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t na) {
         "dtype", given(a[4]) ? out.scalar_type() : dtype_or(a[3], at::kBFloat16), BF16 | F32);
     if (!given(a[4])) out = empty(shape, dtype_or(a[3], at::kBFloat16), dev);
     uint32_t* status = status_ptr(a[5], dev);
-    const cudaStream_t stream = stream_of(a[6], dev);
+    const cudaStream_t stream = stream_of(a[6], dev, {&out});
     call("hytopk_cache_read", [&] {
       return p_cache_read(cache.data_ptr(), c.type, c.scale, c.r.n, slots, n, c.r.H, c.r.d,
                           out.data_ptr(), type, status, stream);
@@ -376,7 +384,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t na) {
     if (!given(a[8])) out = empty(shape, type, t.dev);
     at::Tensor lse = empty({t.rq.n, t.rq.H}, at::kFloat, t.dev);
     uint32_t* status = status_ptr(a[9], t.dev);
-    const cudaStream_t stream = stream_of(a[10], t.dev);
+    const cudaStream_t stream = stream_of(a[10], t.dev, {&out, &lse});
     call("hytopk_attend", [&] {
       return p_attend(t.q.data_ptr(), t.rq.row, t.k.data_ptr(), t.rk.row, ks, t.v.data_ptr(),
                       t.rv.row, vs, t.idx, t.rq.n, t.rk.n, t.rq.H, t.rk.H, t.rq.d, t.k_top, t.type,
@@ -410,7 +418,7 @@ PyObject* attend_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     }
     at::Tensor dq = empty(shape, at::kFloat, t.dev);
     uint32_t* status = status_ptr(a[10], t.dev);
-    const cudaStream_t stream = stream_of(a[11], t.dev);
+    const cudaStream_t stream = stream_of(a[11], t.dev, {&dq, &dk, &dv});
     call("hytopk_attend_backward", [&] {
       return p_attend_backward(
           t.q.data_ptr(), t.rq.row, t.k.data_ptr(), t.rk.row, t.v.data_ptr(), t.rv.row, t.idx,

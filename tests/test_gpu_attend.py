@@ -332,6 +332,27 @@ def test_another_stream_and_repeat(hk, dev):
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+def test_a_stream_given_explicitly(hk, dev):
+    """stream=: the same bits, and memory of a dropped result is not used anew while the
+    call still writes it."""
+    import torch
+
+    q, kk, vv, idx, kw = make(torch, dev, 600, 32, 1, 128, 900, 900, seed=22)
+    want = hk.attend(q, kk, vv, idx)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = hk.attend(q, kk, vv, idx, stream=side)
+    side.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    del got
+    for _ in range(10):
+        side.wait_stream(torch.cuda.current_stream())
+        hk.attend(q, kk, vv, idx, stream=side)  # dropped at once
+        marks = torch.full_like(want[0], 7.0)
+        torch.cuda.synchronize()
+        assert bool((marks == 7.0).all())
+
+
 def test_captured_in_a_graph(hk, dev):
     import torch
 
