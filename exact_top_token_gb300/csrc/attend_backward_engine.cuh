@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  allow_next();
+  wait_for_earlier();
 
   const int first = (int)blockIdx.x;
   const int n_mine = pl.items > first ? (pl.items - 1 - first) / pl.stride + 1 : 0;
@@ -583,8 +585,7 @@ cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
   pl.sh = pl.stride / pl.blocks % a.Hkv;
   pl.st = pl.stride / pl.blocks / a.Hkv;
   return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
-    kernel<<<pl.stride, C::THREADS, C::SMEM, st>>>(a, pl);
-    return cudaGetLastError();
+    return launch_early(kernel, pl.stride, C::THREADS, C::SMEM, st, 1, a, pl);
   });
 }
 

@@ -54,6 +54,7 @@
 #include <cuda_bf16.h>
 
 #include "attend.h"
+#include "early.cuh"
 #include "tc.cuh"
 
 namespace hytopk {
@@ -356,6 +357,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  allow_next();
+  wait_for_earlier();
 
   // items of this CTA: first, first + stride, ...; its tiles of each: [tile0, tile0 + ntile)
   const int first = (int)blockIdx.x / pl.splits;
@@ -962,20 +965,11 @@ cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   pl.sb = pl.stride % pl.blocks;
   pl.sh = pl.stride / pl.blocks % a.Hkv;
   pl.st = pl.stride / pl.blocks / a.Hkv;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(pl.splits > 1 ? pl.items * pl.splits : ctas));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)pl.splits;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pl.splits > 1 ? 1 : 0;
   return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in,
-                         [&] { return cudaLaunchKernelEx(&cfg, kernel, a, pl); });
+                         [&] {
+                           return launch_early(kernel, pl.splits > 1 ? pl.items * pl.splits : ctas,
+                                               C::THREADS, C::SMEM, st, pl.splits, a, pl);
+                         });
 }
 
 }  // namespace att

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "launch.h"
+#include "early.cuh"
 #include "rope.cuh"
 
 namespace hytopk {
@@ -59,6 +60,8 @@ __device__ __forceinline__ void load_rotated(const RowArgs& a, int t, int h, flo
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) k_rope(const RowArgs a) {
+  allow_next();
+  wait_for_earlier();
   extern __shared__ float rows[];
   const int lane = threadIdx.x & 31;
   float* row = rows + (threadIdx.x >> 5) * a.d;
@@ -72,6 +75,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope(const RowArgs a) {
 
 template <typename T, bool E4M3>
 __global__ void __launch_bounds__(32 * kWarps) k_cache_write(const RowArgs a) {
+  allow_next();
+  wait_for_earlier();
   extern __shared__ float rows[];
   const int lane = threadIdx.x & 31;
   float* row = rows + (threadIdx.x >> 5) * a.d;
@@ -177,6 +182,8 @@ constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
 // a row's scale, addresses and magnitude steps (8 heads x 65521 rows: 83 -> 68 us).
 template <typename T, int D, int MODE, int V>
 __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
+  allow_next();
+  wait_for_earlier();
   constexpr int GL = D / (8 * V), GROUPS = kFastThreads / GL, W = sizeof(T) * 2;
   extern __shared__ float4 table4[];
   float* table = reinterpret_cast<float*>(table4);  // [tokens][cos rot/2 | sin rot/2]
@@ -388,7 +395,7 @@ void launch_rows_of(const RowArgs& a, cudaStream_t st) {
   if (smem > 48 * 1024)
     cudaFuncSetAttribute(k_rows<T, D, MODE, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          (int)smem);
-  k_rows<T, D, MODE, V><<<grid, kFastThreads, smem, st>>>(a);
+  launch_early(k_rows<T, D, MODE, V>, grid, kFastThreads, smem, st, 1, a);
 }
 
 template <typename T, int MODE>
@@ -425,6 +432,8 @@ struct ReadArgs {
 // by memory: every row is read once and written once.
 template <bool E4M3, typename T>
 __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
+  allow_next();
+  wait_for_earlier();
   constexpr int CE = E4M3 ? 16 : 8;  // elements of a chunk
   const unsigned per_row = a.d / CE;
   const int shift = (per_row & (per_row - 1)) ? -1 : 31 - __clz(per_row);
@@ -565,8 +574,8 @@ extern "C" hytopk_status hytopk_rope(const void* x, int64_t x_row, int64_t x_hea
   const bool f32 = type == HYTOPK_ELEM_F32;
   if (f32 ? launch_rows<float, 0>(a, stream) : launch_rows<__nv_bfloat16, 0>(a, stream))
     return launched();
-  if (type == HYTOPK_ELEM_F32) k_rope<float><<<grid, 32 * kWarps, smem, stream>>>(a);
-  else k_rope<__nv_bfloat16><<<grid, 32 * kWarps, smem, stream>>>(a);
+  if (type == HYTOPK_ELEM_F32) launch_early(k_rope<float>, grid, 32 * kWarps, smem, stream, 1, a);
+  else launch_early(k_rope<__nv_bfloat16>, grid, 32 * kWarps, smem, stream, 1, a);
   return launched();
 }
 
@@ -597,11 +606,11 @@ extern "C" hytopk_status hytopk_cache_write(const void* x, int64_t x_row, int64_
           : (e4 ? launch_rows<__nv_bfloat16, 2>(a, stream) : launch_rows<__nv_bfloat16, 1>(a, stream)))
     return launched();
   if (x_type == HYTOPK_ELEM_F32) {
-    if (e4) k_cache_write<float, true><<<grid, 32 * kWarps, smem, stream>>>(a);
-    else k_cache_write<float, false><<<grid, 32 * kWarps, smem, stream>>>(a);
+    if (e4) launch_early(k_cache_write<float, true>, grid, 32 * kWarps, smem, stream, 1, a);
+    else launch_early(k_cache_write<float, false>, grid, 32 * kWarps, smem, stream, 1, a);
   } else {
-    if (e4) k_cache_write<__nv_bfloat16, true><<<grid, 32 * kWarps, smem, stream>>>(a);
-    else k_cache_write<__nv_bfloat16, false><<<grid, 32 * kWarps, smem, stream>>>(a);
+    if (e4) launch_early(k_cache_write<__nv_bfloat16, true>, grid, 32 * kWarps, smem, stream, 1, a);
+    else launch_early(k_cache_write<__nv_bfloat16, false>, grid, 32 * kWarps, smem, stream, 1, a);
   }
   return launched();
 }
@@ -625,11 +634,11 @@ extern "C" hytopk_status hytopk_cache_read(const void* cache, hytopk_elem cache_
   const int64_t blocks = ((int64_t)n * H * (d / (e4 ? 16 : 8)) + per - 1) / per;
   const unsigned grid = (unsigned)blocks;  // n H < 2^31 and at most 64 or 128 chunks a row: < 2^31
   if (out_type == HYTOPK_ELEM_F32) {
-    if (e4) k_cache_read<true, float><<<grid, kFastThreads, 0, stream>>>(a);
-    else k_cache_read<false, float><<<grid, kFastThreads, 0, stream>>>(a);
+    if (e4) launch_early(k_cache_read<true, float>, grid, kFastThreads, 0, stream, 1, a);
+    else launch_early(k_cache_read<false, float>, grid, kFastThreads, 0, stream, 1, a);
   } else {
-    if (e4) k_cache_read<true, __nv_bfloat16><<<grid, kFastThreads, 0, stream>>>(a);
-    else k_cache_read<false, __nv_bfloat16><<<grid, kFastThreads, 0, stream>>>(a);
+    if (e4) launch_early(k_cache_read<true, __nv_bfloat16>, grid, kFastThreads, 0, stream, 1, a);
+    else launch_early(k_cache_read<false, __nv_bfloat16>, grid, kFastThreads, 0, stream, 1, a);
   }
   return launched();
 }
