@@ -32,11 +32,13 @@
 // e4m3 rows are widened to bf16, which holds every e4m3 value: the codes land in the
 // first half of their tile's place in shared memory and warps of their own widen them
 // there. K's row scale joins the factor of the row's scores, V's multiplies its weights.
-// 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 534 us (515 TFLOP/s, rows
-// gathered at 8.0 TB/s), e4m3 rows 712 us. Widening each row in a producer's registers
-// took 1667 us; multiplying the codes, with q and P in two e4m3 parts, 771 us; copies and
-// widening by the same warps, through a ring of its own, 742 us; widening to f16 with q
-// and P in f16 694 us, but 128 heads 1316 us instead of 1083, and small weights lost.
+// 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 533 us (515 TFLOP/s, rows
+// gathered at 8.0 TB/s), e4m3 rows 703 us; 128 heads 710 and 1030 us. Bound by the warp
+// instructions of a tile (6300 and 8100 on four schedulers), most of them the softmax's.
+// For e4m3 rows, widening each row in a producer's registers took 1667 us; multiplying the
+// codes, with q and P in two e4m3 parts, 771 us; copies and widening by the same warps,
+// through a ring of its own, 742 us; widening to f16 with q and P in f16 694 us, but 128
+// heads 1316 us, and weights 2^-31 of the largest were lost.
 //
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
 //                 columns), O read-out
@@ -64,6 +66,11 @@ constexpr int kSplits = 8;  // CTAs that share an item, at most (a portable clus
 constexpr int kChunk = 4;  // tiles summed on the tensor core where the result is fp32
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// N, the head columns of an item, is the smallest instance that holds a group's heads:
+// 16, 64 or, for bf16 results of d <= 128, 128; larger groups take several items, each
+// gathering the rows anew. 4096 queries, 2048 rows of 128 columns, bf16 and e4m3 rows: 16
+// heads 407 and 508 us with N = 16, 521 and 677 with 64; 128 heads 709 and 1028 us with
+// N = 128, 1055 and 1373 with two items of 64.
 template <int D_, int N_, bool E4_, bool F32_>
 struct Cfg {
   static constexpr int D = D_, N = N_;
@@ -287,6 +294,18 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
 
 struct Plan {
   int splits;   // CTAs per item (cluster size), 1: none
@@ -896,44 +915,65 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     }
   }
   if (pl.splits > 1) {
-    // Join the cluster's parts: each rank takes a share of the item's nh x d values.
-    // Every CTA's reference, sum and part of a value are read at once; one after
-    // another they took 8 of a single token's 18 us.
+    // Join the cluster's parts: each rank takes a share of the item's nh x d values, four
+    // at a time. First what each CTA's part of a head counts, its references and sums read
+    // once; reading them for every value took 3 of a single token's 14 us.
     __syncwarp();
     cluster_sync();
     if (!*abort_flag) {
       const int h0 = first_head(start), nh = head_count(start);
       const uint32_t part_a = tc::smem_u32(ring), m_a = tc::smem_u32(nm_s), l_a = tc::smem_u32(il_s);
-      const int per = (nh * D + pl.splits - 1) / pl.splits;
-      const int end = min(nh * D, (int)(rank + 1) * per);
+      float* fac = reinterpret_cast<float*>(pbuf);  // [splits][N], idle by now
+      const int all = nh * (D / 4), per = (all + pl.splits - 1) / pl.splits;
+      const int lo = min(all, (int)rank * per), hi = min(all, lo + per);
+      auto join = [&](auto parts) {
+        constexpr int S = decltype(parts)::value;
+        const int h = (lo * 4) / D + (int)threadIdx.x;  // of this share's heads
+        if (h * D < hi * 4) {
+          float m[S], z[S], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+          for (int r = 0; r < S; ++r) {
+            m[r] = -ld_cluster(map_cluster(m_a + h * 4, r));
+            z[r] = ld_cluster(map_cluster(l_a + h * 4, r));
+          }
+#pragma unroll
+          for (int r = 0; r < S; ++r) top = fmaxf(top, m[r]);
+          const bool any = top != -INFINITY;
+#pragma unroll
+          for (int r = 0; r < S; ++r) {
+            m[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top);
+            sum += m[r] * z[r];
+          }
+#pragma unroll
+          for (int r = 0; r < S; ++r) fac[r * N + h] = any ? m[r] / sum : 0.0f;
+          if (a.lse && h * D >= lo * 4)
+            a.lse[(size_t)start.t * Hq + h0 + h] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        }
+        __syncthreads();
 #pragma unroll 1
-      for (int f = (int)rank * per + threadIdx.x; f < end; f += C::THREADS) {
-        const int h = f / D;
-        float m[kSplits], z[kSplits], o[kSplits];
+        for (int f = lo + (int)threadIdx.x; f < hi; f += C::THREADS) {
+          float4 o[S], y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int r = 0; r < kSplits; ++r) {
-          const bool is = r < pl.splits;
-          m[r] = is ? -ld_cluster(map_cluster(m_a + h * 4, r)) : -INFINITY;
-          z[r] = is ? ld_cluster(map_cluster(l_a + h * 4, r)) : 0.0f;
-          o[r] = is ? ld_cluster(map_cluster(part_a + f * 4, r)) : 0.0f;
+          for (int r = 0; r < S; ++r) o[r] = ld_cluster4(map_cluster(part_a + f * 16, r));
+#pragma unroll
+          for (int r = 0; r < S; ++r) {
+            const float x = fac[r * N + f * 4 / D];
+            y.x += x * o[r].x;
+            y.y += x * o[r].y;
+            y.z += x * o[r].z;
+            y.w += x * o[r].w;
+          }
+          const size_t at = ((size_t)start.t * Hq + h0) * D + (size_t)f * 4;
+          if constexpr (C::F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
         }
-        float top = -INFINITY, sum = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int r = 0; r < kSplits; ++r) top = fmaxf(top, m[r]);
-        const bool any = top != -INFINITY;
-#pragma unroll
-        for (int r = 0; r < kSplits; ++r) {
-          const float x = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top);
-          sum += x * z[r];
-          y += x * o[r];
-        }
-        y = any ? y / sum : 0.0f;
-        const size_t at = ((size_t)start.t * Hq + h0) * D + f;
-        if constexpr (C::F32) static_cast<float*>(a.out)[at] = y;
-        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-        if (f % D == 0 && a.lse)
-          a.lse[(size_t)start.t * Hq + h0 + h] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
-      }
+      };
+      if (pl.splits == 2) join(Int<2>{});
+      else if (pl.splits == 4) join(Int<4>{});
+      else join(Int<8>{});
     }
     cluster_sync();
   }
@@ -950,15 +990,21 @@ template <class C>
 cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
   auto kernel = k_attend<C>;
   static unsigned long long opted_in = 0;
+  static int fits[64][4];  // of each device, clusters of 2, 4 and 8 that run at once, + 1
   Plan pl{};
   pl.blocks = (a.G + C::N - 1) / C::N;
   pl.heads = (a.G + pl.blocks - 1) / pl.blocks;
   pl.tiles = (a.k_top + 127) / 128;
   pl.items = a.n * a.Hkv * pl.blocks;
   pl.splits = 1;
-  // split while every SM still gets at most one CTA and every CTA a tile
+  // Split while every CTA has a tile and all clusters run at once: a second wave costs
+  // more than the longest split saves (64 heads, 2048 rows: 14 tokens 13 us in clusters
+  // of 8, 15 in clusters of 4; 16 tokens, of whose clusters of 8 not all fit, 23 and 15;
+  // one token 12, 14, 21 and 29 us in 8, 4, 2 and 1; 12 us with 16 CTAs).
   while (pl.splits < kSplits && 2 * pl.splits <= pl.tiles &&
-         (int64_t)pl.items * 2 * pl.splits <= sms)
+         (int64_t)pl.items * 2 * pl.splits <= sms &&
+         pl.items <= clusters_at_once(reinterpret_cast<const void*>(kernel), C::THREADS, C::SMEM,
+                                      2 * pl.splits, &opted_in, fits))
     pl.splits *= 2;
   const int ctas = pl.items < sms ? pl.items : sms;
   pl.stride = pl.splits > 1 ? pl.items : ctas;

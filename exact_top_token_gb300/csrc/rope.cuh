@@ -7,9 +7,7 @@
 // the nearest multiple of pi / 2 = C1 + C2 + C3 in fp32 parts (the reduction by
 // constants in parts of Cody and Waite, "Software Manual for the Elementary
 // Functions", 1980). On the rest, in [-pi/4, pi/4], the Taylor series of sin and
-// cos to x^9 and x^10 are off by less than 2e-9. (25 instructions; sincosf, which
-// reduces once more, took the rotation of single-head keys from the memory bound
-// to 2.5 times it.)
+// cos to x^9 and x^10 are off by less than 2e-9.
 #pragma once
 
 #include "common.cuh"

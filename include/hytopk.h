@@ -502,13 +502,16 @@ HYTOPK_API hytopk_status hytopk_cache_read(const void* cache, hytopk_elem cache_
  *        index counts as often as it is there. Causality is not checked.
  *   out  [n, Hq, d] bf16 or fp32; lse [n, Hq] fp32 or NULL. A query with no
  *        row gets out = 0 and lse = -inf.
- * Sums and softmax statistics are fp32. The tensor cores take bf16 operands:
- * a bf16 result uses the weights exp(s - max) rounded to bf16 (an error of the
- * size of the result's own rounding); an fp32 result uses them as the sum of
- * three bf16 parts (24 bits).
+ * Sums and softmax statistics are fp32. The tensor cores take bf16 operands
+ * (e4m3 values are bf16 values): a bf16 result uses the weights exp(s - max)
+ * rounded to bf16 (an error of the size of the result's own rounding); an fp32
+ * result uses them as the sum of three bf16 parts (24 bits). A weight is at
+ * most 2^24 times the first rows' largest before it is scaled again, so |v|
+ * (with its scale) must stay below 2^88 for sums within fp32.
  *   1 <= Hkv, Hq a multiple of Hkv, G <= 128, d in {64, 128, 256} (fp32
- *   results: {64, 128}), 1 <= k_top <= 16384, n * Hkv < 2^31. Base pointers
- *   16-byte aligned, strides multiples of 16 bytes. */
+ *   results: {64, 128}), 1 <= k_top <= 16384, n * Hq < 2^31. Base pointers
+ *   16-byte aligned, strides multiples of 16 bytes; k_row and v_row not
+ *   negative and below 4 GiB. */
 HYTOPK_API hytopk_status hytopk_attend(const void* q, int64_t q_row, const void* k, int64_t k_row,
                                        const float* k_scale, const void* v, int64_t v_row,
                                        const float* v_scale, const int32_t* idx, int n, int L,
@@ -529,7 +532,8 @@ HYTOPK_API hytopk_status hytopk_attend(const void* q, int64_t q_row, const void*
  * sums are fp32. dk and dv take floating-point atomic additions, so their low
  * bits depend on the order of arrival. Rows outside [0, L) as in
  * hytopk_attend; a query with no row has dq = 0.
- *   d in {64, 128}; otherwise shapes, strides and alignment of hytopk_attend. */
+ *   d in {64, 128}, rows of dk below 4 GiB; otherwise shapes, strides and
+ *   alignment of hytopk_attend. */
 HYTOPK_API hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, const void* k,
                                                 int64_t k_row, const void* v, int64_t v_row,
                                                 const int32_t* idx, const void* out,
