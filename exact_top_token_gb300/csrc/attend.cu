@@ -21,17 +21,21 @@ cudaError_t launch_attend_backward_d128(const att::Args& a, bool out_f32, int sm
 namespace att {
 namespace {
 
-// Zeros to dk and dv (16-byte aligned, whole float4s). Two clearing calls take 4 us of a
-// small step and the kernel after them cannot be launched early.
+// One kernel for all that is zeroed: two clearing calls took 4 us of a small step, and
+// the kernel after them cannot be launched early.
 constexpr int kZeroThreads = 512;
-__global__ void __launch_bounds__(kZeroThreads) k_zero(float4* x, float4* y, size_t n) {
+__global__ void __launch_bounds__(kZeroThreads) k_zero(float4* x, float4* y, size_t nx, float4* z,
+                                                       size_t nz) {
   allow_next();
   wait_for_earlier();
+  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const size_t step = (size_t)gridDim.x * kZeroThreads;
-  for (size_t i = (size_t)blockIdx.x * kZeroThreads + threadIdx.x; i < n; i += step) {
-    x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const size_t i0 = (size_t)blockIdx.x * kZeroThreads + threadIdx.x;
+  for (size_t i = i0; i < nx; i += step) {
+    x[i] = zero;
+    y[i] = zero;
   }
+  for (size_t i = i0; i < nz; i += step) z[i] = zero;
 }
 
 // Byte offsets of cache rows are 64-bit products of two 32-bit factors.
@@ -54,6 +58,16 @@ hytopk_status check(int n, int L, int Hq, int Hkv, int d, int k_top, hytopk_elem
 }
 
 }  // namespace
+
+cudaError_t launch_zero(float* x, float* y, size_t nx, float* z, size_t nz, int sms,
+                        cudaStream_t st) {
+  const size_t most = (nx > nz ? nx : nz) / 4, blocks = (most + kZeroThreads - 1) / kZeroThreads;
+  if (blocks == 0) return cudaSuccess;
+  return launch_early(k_zero, (unsigned)(blocks < 4 * (size_t)sms ? blocks : 4 * (size_t)sms),
+                      kZeroThreads, 0, st, 1, reinterpret_cast<float4*>(x),
+                      reinterpret_cast<float4*>(y), nx / 4, reinterpret_cast<float4*>(z), nz / 4);
+}
+
 }  // namespace att
 }  // namespace hytopk
 
@@ -131,15 +145,11 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
       !att::aligned(dk, 16) || !att::aligned(dv, 16) || !att::aligned(idx, 4) ||
       !att::aligned(lse, 4) || q_row % 8 || k_row % 8 || v_row % 8)
     return HYTOPK_MISALIGNED;
-  if (!accumulate) {
-    const size_t vectors = (size_t)L * Hkv * d / 4, most = (size_t)num_sms() * 4;
-    const size_t blocks = (vectors + att::kZeroThreads - 1) / att::kZeroThreads;
-    if (launch_early(att::k_zero, (unsigned)(blocks < most ? blocks : most), att::kZeroThreads, 0,
-                     stream, 1, reinterpret_cast<float4*>(dk), reinterpret_cast<float4*>(dv),
-                     vectors) != cudaSuccess)
-      return HYTOPK_CUDA_ERROR;
-    if (n == 0) return HYTOPK_OK;
-  }
+  if (n == 0)
+    return att::launch_zero(dk, dv, (size_t)L * Hkv * d, nullptr, 0, num_sms(), stream) ==
+                   cudaSuccess
+               ? HYTOPK_OK
+               : HYTOPK_CUDA_ERROR;
   att::Args a{};
   a.q = q;
   a.q_row = q_row;
@@ -162,6 +172,7 @@ extern "C" hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  a.zero = !accumulate;
   auto launch = d == 64 ? launch_attend_backward_d64 : launch_attend_backward_d128;
   return launch(a, out_type == HYTOPK_ELEM_F32, num_sms(), stream) == cudaSuccess
              ? HYTOPK_OK

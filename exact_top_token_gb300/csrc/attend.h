@@ -25,7 +25,12 @@ struct Args {
   float* dq;
   float* dk;
   float* dv;
+  int zero;            // dk and dv are set to zero first
 };
+
+// attend.cu: zeros to x and y (nx floats each) and z (nz), whole and aligned float4s
+cudaError_t launch_zero(float* x, float* y, size_t nx, float* z, size_t nz, int sms,
+                        cudaStream_t st);
 
 // Opt in to `bytes` of dynamic shared memory, once per kernel and device: the call
 // takes longer than a launch, and single-token calls are bound by the host. `done` is the

@@ -529,8 +529,9 @@ HYTOPK_API hytopk_status hytopk_attend(const void* q, int64_t q_row, const void*
  *   out (bf16 or fp32; the fp32 result keeps the gradients at fp32 accuracy)
  *   and lse are hytopk_attend's; grad [n, Hq, d] bf16 contiguous.
  * p and ds enter the tensor cores as the sum of three bf16 parts (24 bits);
- * sums are fp32. dk and dv take floating-point atomic additions, so their low
- * bits depend on the order of arrival. Rows outside [0, L) as in
+ * sums are fp32. dk and dv, and dq where several CTAs share a query (n * Hkv
+ * less than half the multiprocessors), take floating-point atomic additions,
+ * so their low bits depend on the order of arrival. Rows outside [0, L) as in
  * hytopk_attend; a query with no row has dq = 0.
  *   d in {64, 128}, rows of dk below 4 GiB; otherwise shapes, strides and
  *   alignment of hytopk_attend. */
