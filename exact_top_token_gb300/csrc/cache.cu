@@ -171,6 +171,16 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two quotients y / -scale from ninv = -1 / scale: q = y ninv, then q + (y + q scale) ninv.
+__device__ __forceinline__ void quotient2(float y0, float y1, float scale, float ninv, float& c0,
+                                          float& c1) {
+  asm("{\n .reg .b64 y, s, n, q, e;\n mov.b64 y, {%2, %3};\n mov.b64 s, {%4, %4};\n"
+      " mov.b64 n, {%5, %5};\n mul.rn.f32x2 q, y, n;\n fma.rn.f32x2 e, q, s, y;\n"
+      " fma.rn.f32x2 q, e, n, q;\n mov.b64 {%0, %1}, q;\n}\n"
+      : "=f"(c0), "=f"(c1)
+      : "f"(y0), "f"(y1), "f"(scale), "f"(ninv));
+}
+
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -236,13 +246,16 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
     const unsigned last = min(row0 + GROUPS * kIter, rows) - 1;
     const int tokens = (int)(last / (unsigned)a.H) - t0 + 1;
     const float m_sin = a.inverse ? -a.mscale : a.mscale;
-    for (int k = threadIdx.x >> 5; k < tokens; k += kFastThreads / 32) {
-      const int pos = __ldg(a.positions + t0 + k);
-      const bool bad = pos < 0 || pos >= kMaxPosition;
-      if (bad && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
-      for (int i = threadIdx.x & 31; i < half; i += 32) {
+    // a warp a token, a lane a pair: a pair's frequency stays in its lane
+    for (int i = threadIdx.x & 31; i < half; i += 32) {
+      const float f = __ldg(a.inv_freq + i);
+#pragma unroll 1
+      for (int k = threadIdx.x >> 5; k < tokens; k += kFastThreads / 32) {
+        const int pos = __ldg(a.positions + t0 + k);
+        const bool bad = pos < 0 || pos >= kMaxPosition;
+        if (bad && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
         float c, s;
-        rope_turn((float)pos, __ldg(a.inv_freq + i), c, s);
+        rope_turn((float)pos, f, c, s);
         if (bad) c = s = __int_as_float(0x7fc00000);
         table[k * a.rot + i] = c * a.mscale;
         table[k * a.rot + half + i] = s * m_sin;
@@ -349,10 +362,9 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
           for (int w = 0; w < 2 * V; ++w) {
             float c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = v[w / 2][w % 2 * 4 + e], q = y * ninv;
-              c[e] = __fmaf_rn(__fmaf_rn(q, scale, y), ninv, q);
-            }
+            for (int e = 0; e < 4; e += 2)
+              quotient2(v[w / 2][w % 2 * 4 + e], v[w / 2][w % 2 * 4 + e + 1], scale, ninv, c[e],
+                        c[e + 1]);
             codes[w] = (e4m3x2(c[0], c[1]) | (e4m3x2(c[2], c[3]) << 16)) ^ 0x80808080u;
           }
         } else {
