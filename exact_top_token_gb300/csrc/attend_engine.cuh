@@ -557,15 +557,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     for (int h = 0; h < 2 * total; ++h) {
       if (!__all_sync(0xffffffffu, wait_bar(landed + slot, phase, abort_flag, a.status))) break;
       const uint32_t at = slot * C::SLOT;
+      uint2 x[2][U];  // the rows at hand and the next ones
+#pragma unroll
+      for (int p = 0; p < U; ++p) x[0][p] = ld_shared8(src[p] + at);
 #pragma unroll
       for (int r8 = 0; r8 < ROWS / 8; ++r8) {
-        uint2 x[U];
+        if (r8 + 1 < ROWS / 8) {
 #pragma unroll
-        for (int p = 0; p < U; ++p) x[p] = ld_shared8(src[p] + at + r8 * 1024);
+          for (int p = 0; p < U; ++p)
+            x[(r8 + 1) & 1][p] = ld_shared8(src[p] + at + (r8 + 1) * 1024);
+        }
         __syncwarp();
 #pragma unroll
         for (int p = 0; p < U; ++p)
-          st_shared16(dst[p] + at + r8 * 1024, e4m3x8_to_bf16(x[p]));
+          st_shared16(dst[p] + at + r8 * 1024, e4m3x8_to_bf16(x[r8 & 1][p]));
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(full + slot);
