@@ -33,7 +33,7 @@
 // first half of their tile's place in shared memory and warps of their own widen them
 // there. K's row scale joins the factor of the row's scores, V's multiplies its weights.
 // 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 533 us (515 TFLOP/s, rows
-// gathered at 8.0 TB/s), e4m3 rows 703 us; 128 heads 710 and 1030 us. Bound by the warp
+// gathered at 8.0 TB/s), e4m3 rows 700 us; 128 heads 710 and 926 us. Bound by the warp
 // instructions of a tile (6300 and 8100 on four schedulers), most of them the softmax's.
 // For e4m3 rows, widening each row in a producer's registers took 1667 us; multiplying the
 // codes, with q and P in two e4m3 parts, 771 us; copies and widening by the same warps,
@@ -69,8 +69,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // N, the head columns of an item, is the smallest instance that holds a group's heads:
 // 16, 64 or, for bf16 results of d <= 128, 128; larger groups take several items, each
 // gathering the rows anew. 4096 queries, 2048 rows of 128 columns, bf16 and e4m3 rows: 16
-// heads 407 and 508 us with N = 16, 521 and 677 with 64; 128 heads 709 and 1028 us with
-// N = 128, 1055 and 1373 with two items of 64.
+// heads 407 and 508 us with N = 16, 521 and 677 with 64; 128 heads 709 and 1028 us (now
+// 926) with N = 128, 1055 and 1373 with two items of 64.
 template <int D_, int N_, bool E4_, bool F32_>
 struct Cfg {
   static constexpr int D = D_, N = N_;

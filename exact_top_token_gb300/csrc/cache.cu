@@ -1,9 +1,9 @@
 // cache.cu -- rotary positions (hytopk_rope) and cache rows: quantised as they
 // are written, with the rotation fused in (hytopk_cache_write), and read back
 // (hytopk_cache_read). All three move each row once. Measured, of 6.8 TB/s for a plain
-// copy: rotation of 8192 x 64 x 128 bf16 45.6 us (5.9 TB/s), of 30011 x 8 x 128 fp32
-// 43.9 us (5.6); read of 262144 x 8 x 128 e4m3 as bf16 138 us (5.9), all bound by memory;
-// write of 65521 x 8 x 128 bf16, rotated, as e4m3 65.6 us (3.1), bound by instructions.
+// copy: rotation of 8192 x 64 x 128 bf16 42.6 us (6.3 TB/s), of 30011 x 8 x 128 fp32
+// 41.8 us (5.9); read of 262144 x 8 x 128 e4m3 as bf16 136 us (6.0), all bound by memory;
+// write of 65521 x 8 x 128 bf16, rotated, as e4m3 62.5 us (3.3), bound by instructions.
 // Of a few rows each takes its launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -197,7 +197,7 @@ constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
 // quotients, codes); with V = 2 half the lanes share a row's scale, addresses and
 // magnitude steps (8 heads x 65521 rows: 83 -> 68 us). A block takes kIter rows a group,
 // so that the loads of several rows are in flight and their angles are computed once;
-// four blocks an SM (64 registers) 68 -> 65.6 us.
+// four blocks an SM (64 registers) 68 -> 65.6 us; quotients two at a time 62.5.
 template <typename T, int D, int MODE, int V>
 __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
   allow_next();
@@ -450,7 +450,7 @@ struct ReadArgs {
 // A thread converts 16-byte chunks of the cache (16 codes or 8 bf16 values),
 // kIter of them kFastThreads apart, all loaded before the first is stored. Bound
 // by memory: every row is read once and written once (262144 x 8 x 128 e4m3 rows as
-// bf16: 138 us, 5.9 TB/s of 6.8; a chunk at a time took 141).
+// bf16: 136 us, 6.0 TB/s of 6.8).
 template <bool E4M3, typename T>
 __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
   allow_next();
