@@ -8,7 +8,11 @@ cudaError_t launch_attend_d64_e4m3(const att::Args& a, bool f32, int sms, cudaSt
     if (a.G <= 16) return att::launch_attend<att::Cfg<64, 16, true, true>>(a, sms, st);
     return att::launch_attend<att::Cfg<64, 64, true, true>>(a, sms, st);
   }
-  if (a.G <= 16) return att::launch_attend<att::Cfg<64, 16, true, false>>(a, sms, st);
+  if (a.G <= 16) {
+    if ((int64_t)a.n * a.Hkv > sms)
+      return att::launch_attend<att::Cfg<64, 16, true, false, 2>>(a, sms, st);
+    return att::launch_attend<att::Cfg<64, 16, true, false>>(a, sms, st);
+  }
   if (a.G <= 64) return att::launch_attend<att::Cfg<64, 64, true, false>>(a, sms, st);
   return att::launch_attend<att::Cfg<64, 128, true, false>>(a, sms, st);
 }

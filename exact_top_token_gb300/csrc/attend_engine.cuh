@@ -71,10 +71,16 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // gathering the rows anew. 4096 queries, 2048 rows of 128 columns, bf16 and e4m3 rows: 16
 // heads 407 and 508 us with N = 16, 521 and 677 with 64; 128 heads 709 and 1028 us (now
 // 926) with N = 128, 1055 and 1373 with two items of 64.
-template <int D_, int N_, bool E4_, bool F32_>
+template <int D_, int N_, bool E4_, bool F32_, int CTAS_ = 1>
 struct Cfg {
   static constexpr int D = D_, N = N_;
   static constexpr bool E4 = E4_, F32 = F32_;
+  // CTAs of an SM. A tile of few heads is a chain that leaves the SM idle, so where shared
+  // memory and registers hold two CTAs (N = 16, d = 64) and there are more items than SMs,
+  // two run: 1024 queries of 32 heads on 8 cache heads, 2048 rows of 64 columns: bf16 519 us
+  // instead of 669, e4m3 711 instead of 753. With fewer items the shorter ring loses (16
+  // queries: 18 us instead of 16).
+  static constexpr int CTAS = CTAS_;
   static constexpr int SWG = N >= 64 ? 4 : 2;     // softmax warpgroups
   static constexpr int SWARPS = 4 * SWG;
   static constexpr int HG = N / SWG;              // head columns of each: 8, 16 or 32
@@ -98,7 +104,7 @@ struct Cfg {
   // (N = 128: 80) registers. (1024 queries of 32 heads on 8 cache heads: 1019 us with 8
   // widening warps, 1102 with 4.)
   static constexpr int PWARPS = E4 || N > 64 ? 4 : 8;
-  static constexpr int VWARPS = !E4 ? 0 : N > 64 ? 2 : N > 16 ? 4 : 8;
+  static constexpr int VWARPS = !E4 ? 0 : N > 64 ? 2 : N > 16 || CTAS > 1 ? 4 : 8;
   static constexpr int RPW = 128 / PWARPS;        // rows of a tile per copying warp
   static constexpr int THREADS = (SWARPS + PWARPS + VWARPS + 1) * 32;
   static constexpr int MMA_WARP = SWARPS + PWARPS + VWARPS;
@@ -106,7 +112,8 @@ struct Cfg {
   static constexpr int MISC = (3 + 4) * N * 4 + 512;
   static constexpr int SR = E4 ? 8 : 0;           // tiles of k and v scales [2][128]
   static constexpr int FIXED = PB * PARTS * PBYTES + QB * QBYTES + SR * 1024 + MISC + 1024;
-  static constexpr int NS_MAX = (227 * 1024 - FIXED) / SLOT;
+  static constexpr int ALL = CTAS > 1 ? 113 * 1024 : 227 * 1024;  // shared memory of a CTA
+  static constexpr int NS_MAX = (ALL - FIXED) / SLOT;
   static constexpr int NS = NS_MAX < 8 ? NS_MAX : 8;
   static constexpr int RING_OFF = 0;
   static constexpr int P_OFF = NS * SLOT;
@@ -114,9 +121,9 @@ struct Cfg {
   static constexpr int SCALE_OFF = Q_OFF + QB * QBYTES;
   static constexpr int MISC_OFF = SCALE_OFF + SR * 1024;
   static constexpr int SMEM = MISC_OFF + MISC + 1024;
-  static constexpr int S_COL = 0, O_COL = 256;
-  static_assert(2 * N <= 256 && 2 * OBLK * OCOLS <= 256, "TMEM columns");
-  static_assert(NS >= 2 && SMEM <= 227 * 1024, "shared memory");
+  static constexpr int S_COL = 0, O_COL = CTAS > 1 ? 64 : 256, COLS = CTAS > 1 ? 256 : 512;
+  static_assert(2 * N <= O_COL && O_COL + 2 * OBLK * OCOLS <= COLS, "TMEM columns");
+  static_assert(NS >= 2 && SMEM <= ALL, "shared memory");
   static_assert(NS * SLOT >= N * D * 4, "partial results of a split item");
   // Scales of tile j are copied once K's slot of the ring is free: V's before with NS
   // odd, so the softmax is done with tile j - (NS + 1) / 2; K's with NS even, so the
@@ -318,7 +325,7 @@ struct Plan {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Plan pl) {
+__global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, const Plan pl) {
   constexpr int D = C::D, N = C::N, HG = C::HG, NS = C::NS, NP = C::NP;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
     tc::fence_barrier_init();
   }
   if (warp == C::MMA_WARP) {
-    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_alloc(tmem_slot, C::COLS);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -986,7 +993,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend(const Args a, const Pl
   __syncthreads();
   if (warp == C::MMA_WARP) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(tmem, C::COLS);
   }
 }
 
@@ -1011,16 +1018,15 @@ cudaError_t launch_attend(const Args& a, int sms, cudaStream_t st) {
          pl.items <= clusters_at_once(reinterpret_cast<const void*>(kernel), C::THREADS, C::SMEM,
                                       2 * pl.splits, &opted_in, fits))
     pl.splits *= 2;
-  const int ctas = pl.items < sms ? pl.items : sms;
+  const int ctas = pl.items < C::CTAS * sms ? pl.items : C::CTAS * sms;
   pl.stride = pl.splits > 1 ? pl.items : ctas;
   pl.sb = pl.stride % pl.blocks;
   pl.sh = pl.stride / pl.blocks % a.Hkv;
   pl.st = pl.stride / pl.blocks / a.Hkv;
-  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in,
-                         [&] {
-                           return launch_early(kernel, pl.splits > 1 ? pl.items * pl.splits : ctas,
-                                               C::THREADS, C::SMEM, st, pl.splits, a, pl);
-                         });
+  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
+    return launch_early(kernel, pl.splits > 1 ? pl.items * pl.splits : ctas, C::THREADS, C::SMEM,
+                        st, pl.splits, a, pl);
+  });
 }
 
 }  // namespace att
