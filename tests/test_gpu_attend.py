@@ -399,6 +399,27 @@ def test_gradients(hk, dev, n, Hq, Hkv, d, k, L):
         check(name, got.cpu().numpy(), r[name], r["tol_" + name])
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,d", [(1, 8, 1, 64), (2, 20, 1, 128), (10, 16, 4, 64),
+                                        (20, 12, 2, 128), (70, 40, 1, 128)])
+def test_gradients_of_few_queries_with_many_rows(hk, dev, n, Hq, Hkv, d):
+    """Several CTAs share a query's rows and add up its dq; new tensors and given ones."""
+    import torch
+
+    k, L = 1700, 2500
+    q, kk, vv, idx, kw = make(torch, dev, n, Hq, Hkv, d, k, L, seed=41 + n)
+    if n > 2:
+        idx[1] = -1
+        idx[2, 100:1500] = -1  # shares with no row at all
+    grad = torch.randn(n, Hq, d, device=dev, generator=torch.Generator(device=dev).manual_seed(n)).bfloat16()
+    out, lse = hk.attend(q, kk, vv, idx, out_dtype=torch.float32)
+    r = reference(q, kk, vv, idx, kw, d ** -0.5, 24, grad)
+    dk0, dv0 = torch.zeros(L, Hkv, d, device=dev), torch.zeros(L, Hkv, d, device=dev)
+    for given in ({}, dict(dk=dk0, dv=dv0)):
+        got = hk.attend_backward(q, kk, vv, idx, out, lse, grad, **given)
+        for name, x in zip(("dq", "dk", "dv"), got):
+            check(name, x.cpu().numpy(), r[name], r["tol_" + name])
+
+
 @pytest.mark.parametrize("Hq,d", [(12, 64), (50, 64), (12, 128), (100, 128)])
 def test_gradients_of_many_items_of_several_tiles(hk, dev, Hq, d):
     import torch
