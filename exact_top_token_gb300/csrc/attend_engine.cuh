@@ -43,7 +43,7 @@
 //   first warps   softmax (2 or 4 warpgroups, each with its share of the N head
 //                 columns), O read-out
 //   4 or 8 warps  producers: rows by cp.async, queries
-//   2 or 4 warps  e4m3 rows only: widening
+//   2, 4 or 8     e4m3 rows only: widening
 //   last warp     MMA issuer, TMEM
 // A tile is a chain of short steps in different warps, so what counts is the
 // length of each step: no division, no wait for a load and little code per tile
