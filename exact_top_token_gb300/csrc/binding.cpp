@@ -165,12 +165,25 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device device) 
   return at::empty(shape, at::TensorOptions().dtype(type).device(device));
 }
 
+// Other Python threads run while this lives; taken back on every way out of its scope:
+// a pointer asked of a tensor that holds no memory (inside a vmap) throws.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 template <class F>
 void call(const char* what, F&& f) {
-  hytopk_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
+  const hytopk_status st = [&] {
+    Unlocked u;
+    return f();
+  }();
   if (st == HYTOPK_OK) return;
   PyObject* args = Py_BuildValue("(is)", static_cast<int>(st), what);
   if (args) PyErr_SetObject(status_error, args);
