@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/record_stream.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -128,22 +129,37 @@ uint32_t* status_ptr(PyObject* o, at::Device device) {
   return static_cast<uint32_t*>(t.data_ptr());
 }
 
-// The stream to launch on. `made`: what was allocated for this call on the current
-// stream; a stream given explicitly is recorded with it, so that freed memory is not
-// used anew before that stream's work is done.
-cudaStream_t stream_of(PyObject* o, at::Device device, std::initializer_list<const at::Tensor*> made) {
-  if (!given(o)) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (!h) throw Raised{};
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (PyErr_Occurred()) throw Raised{};
-  const cudaStream_t stream = static_cast<cudaStream_t>(p);
-  for (const at::Tensor* t : made)
-    if (t->defined())
-      t->record_stream(c10::cuda::getStreamFromExternal(stream, device.index()).unwrap());
-  return stream;
-}
+// The stream of a call: the current one of the device, or the one given. A stream given
+// is current while this lives, so that results are taken from its memory: the current
+// stream's may still be read there by work that was launched before it was freed.
+class Place {
+ public:
+  Place(PyObject* o, at::Device device) : caller_(c10::cuda::getCurrentCUDAStream(device.index())) {
+    stream_ = caller_.stream();
+    if (!given(o)) return;
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (!h) throw Raised{};
+    void* p = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (PyErr_Occurred()) throw Raised{};
+    stream_ = static_cast<cudaStream_t>(p);
+    if (stream_ != caller_.stream())
+      other_.reset_stream(c10::cuda::getStreamFromExternal(stream_, device.index()));
+  }
+  cudaStream_t stream() const { return stream_; }
+  // A result of a call on a stream given. Made here it is read on the caller's stream, so it
+  // is recorded there: once dropped, the given stream does not take it anew before that is
+  // done. One that the caller gave (`own`) is recorded with the stream that writes it.
+  void result(const at::Tensor& t, bool own = false) const {
+    if (stream_ == caller_.stream()) return;
+    t.record_stream(own ? other_.current_stream()->unwrap() : caller_.unwrap());
+  }
+
+ private:
+  c10::cuda::CUDAStream caller_;
+  cudaStream_t stream_;
+  c10::cuda::OptionalCUDAStreamGuard other_;
+};
 
 double number(PyObject* o) {
   const double x = PyFloat_AsDouble(o);
@@ -240,9 +256,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const at::Device dev = x.device();
     const hytopk_elem type = elem("x", x.scalar_type(), BF16 | F32);
     const auto params = rope_params(a[1], a[2], r.n, dev, a[3], a[4], truth(a[6]), a[5]);
+    const Place place(a[9], dev);
     at::Tensor made;
     Rows o{r.n, r.H, r.d, r.H * r.d, r.d};
-    if (given(a[7])) {
+    const bool own = given(a[7]);
+    if (own) {
       const at::Tensor& out = tensor("out", a[7]);
       if (out.sizes() != x.sizes() || out.scalar_type() != x.scalar_type() || out.device() != dev)
         raise(PyExc_ValueError, "out must match x in shape, type and device");
@@ -250,14 +268,14 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
     } else {
       made = empty(x.sizes(), x.scalar_type(), dev);
     }
-    void* out = made.defined() ? made.data_ptr() : THPVariable_Unpack(a[7]).data_ptr();
+    void* out = own ? THPVariable_Unpack(a[7]).data_ptr() : made.data_ptr();
     uint32_t* status = status_ptr(a[8], dev);
-    const cudaStream_t stream = stream_of(a[9], dev, {&made});
+    place.result(own ? THPVariable_Unpack(a[7]) : made, own);
     call("hytopk_rope", [&] {
       return p_rope(x.data_ptr(), r.row, r.head, type, r.n, r.H, r.d, &params, out, o.row, o.head,
-                    status, stream);
+                    status, place.stream());
     });
-    return made.defined() ? THPVariable_Wrap(std::move(made)) : ref(a[7]);
+    return own ? ref(a[7]) : THPVariable_Wrap(std::move(made));
   });
 }
 
@@ -298,11 +316,11 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const int32_t* slots =
         given(a[3]) ? static_cast<int32_t*>(need("slots", a[3], dev, at::kInt, {r.n})) : nullptr;
     uint32_t* status = status_ptr(a[9], dev);
-    const cudaStream_t stream = stream_of(a[10], dev, {});
+    const Place place(a[10], dev);
     call("hytopk_cache_write", [&] {
       return p_cache_write(x.data_ptr(), r.row, r.head, type, r.n, r.H, r.d,
                            given(a[4]) ? &params : nullptr, slots, cache.data_ptr(), c.type,
-                           c.scale, c.r.n, status, stream);
+                           c.scale, c.r.n, status, place.stream());
     });
     return ref(a[1]);
   });
@@ -332,12 +350,13 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t na) {
     }
     const hytopk_elem type = elem(
         "dtype", given(a[4]) ? out.scalar_type() : dtype_or(a[3], at::kBFloat16), BF16 | F32);
-    if (!given(a[4])) out = empty(shape, dtype_or(a[3], at::kBFloat16), dev);
     uint32_t* status = status_ptr(a[5], dev);
-    const cudaStream_t stream = stream_of(a[6], dev, {&out});
+    const Place place(a[6], dev);
+    if (!given(a[4])) out = empty(shape, dtype_or(a[3], at::kBFloat16), dev);
+    place.result(out, given(a[4]));
     call("hytopk_cache_read", [&] {
       return p_cache_read(cache.data_ptr(), c.type, c.scale, c.r.n, slots, n, c.r.H, c.r.d,
-                          out.data_ptr(), type, status, stream);
+                          out.data_ptr(), type, status, place.stream());
     });
     return given(a[4]) ? ref(a[4]) : THPVariable_Wrap(std::move(out));
   });
@@ -394,15 +413,17 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t na) {
     }
     const at::ScalarType type = given(a[8]) ? out.scalar_type() : dtype_or(a[7], at::kBFloat16);
     const hytopk_elem otype = elem("out_dtype", type, BF16 | F32);
+    uint32_t* status = status_ptr(a[9], t.dev);
+    const Place place(a[10], t.dev);
     if (!given(a[8])) out = empty(shape, type, t.dev);
     at::Tensor lse = empty({t.rq.n, t.rq.H}, at::kFloat, t.dev);
-    uint32_t* status = status_ptr(a[9], t.dev);
-    const cudaStream_t stream = stream_of(a[10], t.dev, {&out, &lse});
+    place.result(out, given(a[8]));
+    place.result(lse);
     call("hytopk_attend", [&] {
       return p_attend(t.q.data_ptr(), t.rq.row, t.k.data_ptr(), t.rk.row, ks, t.v.data_ptr(),
                       t.rv.row, vs, t.idx, t.rq.n, t.rk.n, t.rq.H, t.rk.H, t.rq.d, t.k_top, t.type,
                       t.scale, out.data_ptr(), otype, static_cast<float*>(lse.data_ptr()), status,
-                      stream);
+                      place.stream());
     });
     PyObject* o = given(a[8]) ? ref(a[8]) : THPVariable_Wrap(std::move(out));
     return Py_BuildValue("(NN)", o, THPVariable_Wrap(std::move(lse)));
@@ -421,6 +442,8 @@ PyObject* attend_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const hytopk_elem otype = elem("out", out.scalar_type(), BF16 | F32);
     const bool add = given(a[8]);
     if (add != given(a[9])) raise(PyExc_ValueError, "dk and dv go together");
+    uint32_t* status = status_ptr(a[10], t.dev);
+    const Place place(a[11], t.dev);
     at::Tensor dk, dv;
     if (add) {
       need("dk", dk = tensor("dk", a[8]), t.dev, at::kFloat, t.k.sizes());
@@ -429,16 +452,17 @@ PyObject* attend_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
       dk = empty(t.k.sizes(), at::kFloat, t.dev);
       dv = empty(t.v.sizes(), at::kFloat, t.dev);
     }
+    place.result(dk, add);
+    place.result(dv, add);
     at::Tensor dq = empty(shape, at::kFloat, t.dev);
-    uint32_t* status = status_ptr(a[10], t.dev);
-    const cudaStream_t stream = stream_of(a[11], t.dev, {&dq, &dk, &dv});
+    place.result(dq);
     call("hytopk_attend_backward", [&] {
       return p_attend_backward(
           t.q.data_ptr(), t.rq.row, t.k.data_ptr(), t.rk.row, t.v.data_ptr(), t.rv.row, t.idx,
           out.data_ptr(), otype, static_cast<const float*>(lse), grad, t.rq.n, t.rk.n, t.rq.H,
           t.rk.H, t.rq.d, t.k_top, t.scale, static_cast<float*>(dq.data_ptr()),
           static_cast<float*>(dk.data_ptr()), static_cast<float*>(dv.data_ptr()), add, status,
-          stream);
+          place.stream());
     });
     PyObject* pk = add ? ref(a[8]) : THPVariable_Wrap(std::move(dk));
     PyObject* pv = add ? ref(a[9]) : THPVariable_Wrap(std::move(dv));
