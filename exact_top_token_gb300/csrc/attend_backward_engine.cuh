@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
   const int left = a.k_top - tile0 * 128;
   const int32_t* idx = a.idx + tile0 * 128;
   auto entry_of = [&](int t, int j) -> int {  // of this CTA's share
-    return j < left ? __ldg(idx + (size_t)t * a.k_top + j) : -1;
+    return j < left ? ld_after(idx + (size_t)t * a.k_top + j) : -1;
   };
   auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
 #pragma unroll
           for (int e = 0; e < EL; ++e) {
             const size_t i = (size_t)h * D + e * 32 + lane;
-            const float o = OUT_F32 ? __ldg(static_cast<const float*>(a.out) + at * D + i)
+            const float o = OUT_F32 ? ld_after(static_cast<const float*>(a.out) + at * D + i)
                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.out)[at * D + i]);
             sum = __fmaf_rn(__bfloat162float(grad[i]), o, sum);
           }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
-          const float lse = h < nh ? __ldg(a.lse + at + h) : -INFINITY;
+          const float lse = h < nh ? ld_after(a.lse + at + h) : -INFINITY;
           nd[h] = -sum;
           nl[h] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
         }
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
           const int f = (p + u) * C::PWARPS * 32 + tid;
           v[u] = x[u] = make_uint4(0, 0, 0, 0);
           if (f / CPR < nh) {
-            v[u] = __ldg(reinterpret_cast<const uint4*>(qsrc) + f);
-            x[u] = __ldg(reinterpret_cast<const uint4*>(grad) + f);
+            v[u] = ld_after(reinterpret_cast<const uint4*>(qsrc) + f);
+            x[u] = ld_after(reinterpret_cast<const uint4*>(grad) + f);
           }
         }
 #pragma unroll

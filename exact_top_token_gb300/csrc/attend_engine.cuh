@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, co
   // (-1: none). Entries are loaded a tile or two ahead and only looked at when
   // they are used: a test right after the load would wait for it.
   auto entry_of = [&](int t, int j) -> int {
-    return j < a.k_top ? __ldg(a.idx + (size_t)t * a.k_top + j) : -1;
+    return j < a.k_top ? ld_after(a.idx + (size_t)t * a.k_top + j) : -1;
   };
   auto row_of = [&](int e) -> int { return e >= a.L || e < 0 ? -1 : e; };
 
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, co
       for (int u = 0; u < QU; ++u) {
         const int f = (p + u) * C::PWARPS * 32 + tid;
         v[u] = make_uint4(0, 0, 0, 0);
-        if (f / QCPR < nh) v[u] = __ldg(src + f);
+        if (f / QCPR < nh) v[u] = ld_after(src + f);
       }
     };
     // stores the chunks that are fetched already (v: the first) and the rest

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
     slot[i] = -1;
     if (row < rows) {
       slot[i] = t;
-      if (MODE != 0 && a.slots) slot[i] = __ldg(a.slots + t);
+      if (MODE != 0 && a.slots) slot[i] = ld_after(a.slots + t);
 #pragma unroll
       for (int u = 0; u < V; ++u) load8(x + 8 * u, raw[i][u]);
     }
@@ -248,10 +248,10 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
     const float m_sin = a.inverse ? -a.mscale : a.mscale;
     // a warp a token, a lane a pair: a pair's frequency stays in its lane
     for (int i = threadIdx.x & 31; i < half; i += 32) {
-      const float f = __ldg(a.inv_freq + i);
+      const float f = ld_after(a.inv_freq + i);
 #pragma unroll 1
       for (int k = threadIdx.x >> 5; k < tokens; k += kFastThreads / 32) {
-        const int pos = __ldg(a.positions + t0 + k);
+        const int pos = ld_after(a.positions + t0 + k);
         const bool bad = pos < 0 || pos >= kMaxPosition;
         if (bad && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
         float c, s;
@@ -476,13 +476,13 @@ __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
       const unsigned item = shift >= 0 ? (unsigned)(f >> shift) : (unsigned)(f / per_row);
       const unsigned c = (unsigned)(f - (int64_t)item * per_row);
       const unsigned t = item / a.H, h = item - t * a.H;
-      slot[i] = a.slots ? __ldg(a.slots + t) : (int)t;
+      slot[i] = a.slots ? ld_after(a.slots + t) : (int)t;
       in[i] = slot[i] >= 0 && slot[i] < a.L;
       if (in[i]) {
         const size_t row = (size_t)slot[i] * a.H + h;
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.cache) +
-                                                      row * a.d * (E4M3 ? 1 : 2)) + c);
-        if (E4M3) scale[i] = __ldg(a.scale + row);
+        raw[i] = ld_after(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.cache) +
+                                                         row * a.d * (E4M3 ? 1 : 2)) + c);
+        if (E4M3) scale[i] = ld_after(a.scale + row);
       } else if (slot[i] != -1 && a.status) {
         atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
       }

@@ -22,6 +22,15 @@ __device__ __forceinline__ void allow_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A load of what an earlier kernel may have written. The read-only path (__ldg, ld.global.nc)
+// is for data that nobody writes while the kernel lives, and a kernel launched early
+// lives while the one before it still writes: its lines are not kept coherent, and one that
+// a kernel two launches back read would do as well as the new one.
+template <typename T>
+__device__ __forceinline__ T ld_after(const T* p) {
+  return *p;
+}
+
 // cluster: CTAs of a cluster (1: none)
 template <class... P>
 cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem,

@@ -139,3 +139,54 @@ def test_given_tensors_written_on_a_given_stream_may_be_dropped(hk, dev):
     assert marks.data_ptr() != at
     torch.cuda.synchronize()
     assert bool((marks == 7.0).all())
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_calls_in_a_row_read_what_the_last_ones_wrote(hk, dev, n):
+    """Queries, cache rows, scales, results and log-sum-exps in the same places step after
+    step, each call launched while the ones before still run: the same bits as with a wait
+    after every call."""
+    import torch
+
+    g = torch.Generator(device=dev).manual_seed(n)
+    steps, d, L, k = 100, 128, 256, 6
+    x = torch.randn(steps, n, 1, d, device=dev, generator=g).bfloat16()
+    y = torch.randn(steps, n, 1, d, device=dev, generator=g).bfloat16()
+    grad = torch.randn(steps, n, 1, d, device=dev, generator=g).bfloat16()
+    # rows of its own for every query, so that a gradient's row takes one addition
+    idx = torch.arange(n * k, device=dev, dtype=torch.int32).view(n, k)
+    idx = idx if n * k <= L else (idx % L).contiguous()
+    slots = torch.randperm(L, device=dev, generator=g)[:n].int()
+    pos = torch.arange(n, device=dev, dtype=torch.int32)
+    freq, _ = hk.rope_frequencies(64, device=dev)
+
+    def run(wait):
+        def now():
+            if wait:
+                torch.cuda.synchronize()
+
+        codes = torch.zeros(L, 1, d, device=dev, dtype=torch.uint8).view(torch.float8_e4m3fn)
+        scale = torch.ones(L, 1, device=dev)
+        plain = torch.zeros(L, 1, d, device=dev, dtype=torch.bfloat16)
+        q, out = torch.zeros_like(x[0]), torch.zeros(n, 1, d, device=dev)
+        results = [torch.empty(steps, n, 1, d, device=dev) for _ in range(2)]
+        kept = []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            hk.rope(x[i], pos, freq, out=q), now()
+            hk.cache_write(y[i], codes, scale, slots=slots, positions=pos, inv_freq=freq), now()
+            hk.cache_read(codes, scale, slots=slots, out=results[0][i]), now()
+            hk.cache_write(x[i], plain, slots=slots), now()
+            hk.attend(q, codes, codes, idx, k_scale=scale, v_scale=scale, out=results[1][i]), now()
+            _, lse = hk.attend(q, plain, plain, idx, out=out)
+            now()
+            dq, dk, dv = hk.attend_backward(q, plain, plain, idx, out, lse, grad[i])
+            now()
+            kept.append((lse, dq, dk, dv) if n * k <= L else (lse, dq))
+        torch.cuda.synchronize()
+        return results + [t for one in kept for t in one]
+
+    want = run(True)
+    for _ in range(5):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
