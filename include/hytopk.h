@@ -37,6 +37,8 @@
  *     return code covers host-side argument checks and launch errors only;
  *     conditions found on the device are reported through the device status
  *     word (HYTOPK_DEV_* bits) of hytopk_stats or of the replay call.
+ *   - Calls run on the CUDA device that is current, which must be the one that
+ *     the pointers and the stream belong to.
  *   - Layouts are row-major and contiguous:
  *       q        [n, H, d] elements of `dt`
  *       q_scale  [n, H]    fp32, one scale per (query, head) row of d elements;

@@ -54,9 +54,9 @@ def built():
     hk.build()
 
 
-def child(code):
+def child(code, env=None):
     r = subprocess.run([sys.executable, "-W", "ignore", "-c", PRELUDE + code], cwd=ROOT, text=True,
-                       capture_output=True, timeout=300)
+                       capture_output=True, timeout=300, env=env)
     assert r.returncode == 0, f"exit code {r.returncode}\n{r.stdout}\n{r.stderr}"
     return r.stdout
 
@@ -78,3 +78,61 @@ refused(lambda b: hk.cache_write(x, b, positions=pos, inv_freq=freq, stream=Stre
 refused(lambda b: hk.cache_write(b, x, positions=pos, inv_freq=freq, stream=Stream()), many)
 assert not calls
 """)
+
+
+# Two devices that only remember which of them is current.
+FAKE_RUNTIME = """
+static int current = 0;
+int cudaGetDeviceCount(int* n) { *n = 2; return 0; }
+int cudaGetDevice(int* d) { *d = current; return 0; }
+int cudaSetDevice(int d) { current = d; return 0; }
+int cudaDeviceGetStreamPriorityRange(int* low, int* high) { *low = 0; *high = -5; return 0; }
+int cuDevicePrimaryCtxGetState(int d, unsigned* flags, int* active) {
+  *flags = 0;
+  *active = 1;
+  return 0;
+}
+int current_device(void) { return current; }
+"""
+
+
+def test_the_tensors_device_is_current_in_every_call(tmp_path):
+    """Tensors on device 1 while device 0 is current: the library is called with device 1
+    current, and device 0 is current afterwards, after refusals too."""
+    source, lib = tmp_path / "runtime.c", tmp_path / "libcuda.so.1"
+    source.write_text(FAKE_RUNTIME)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(source)], check=True)
+    env = dict(os.environ, LD_PRELOAD=str(lib), LD_LIBRARY_PATH=os.pathsep.join(
+        [str(tmp_path)] + [p for p in (os.environ.get("LD_LIBRARY_PATH"),) if p]))
+    got = child("""
+runtime, seen, status = ctypes.CDLL(None), [], 0
+
+
+@ctypes.CFUNCTYPE(ctypes.c_int, *([ctypes.c_void_p] * 13))
+def entry(*a):
+    seen.append(runtime.current_device())
+    return status
+
+
+address = ctypes.cast(entry, ctypes.c_void_p).value
+hk._operators().init(hk.HytopkError, torch.OutOfMemoryError, *[address] * 5)
+f32 = dict(dtype=torch.float32)
+cache, scale = Claims(9, 2, 64, dtype=torch.float8_e4m3fn), Claims(9, 2, **f32)
+idx, rows = Claims(4, 3, dtype=torch.int32), Claims(9, 2, 64)
+for st in (None, Stream()):
+    hk.cache_write(x, cache, scale, stream=st)
+    if st is None:  # (a result is recorded with a stream given: not these tensors)
+        hk.rope(x, pos, freq, out=x)
+        hk.cache_read(cache, scale, out=rows, dtype=torch.bfloat16)
+    assert runtime.current_device() == 0
+    status = 1
+    try:
+        hk.cache_write(x, cache, scale, stream=st)
+    except hk.HytopkError:
+        pass
+    status = 0
+    assert runtime.current_device() == 0
+assert set(seen) == {1}, seen
+print(len(seen))
+""", env)
+    assert int(got) == 6
