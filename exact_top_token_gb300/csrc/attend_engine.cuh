@@ -65,6 +65,7 @@ namespace att {
 constexpr int kSplits = 8;  // CTAs that share an item, at most (a portable cluster)
 constexpr int kChunk = 4;  // tiles summed on the tensor core where the result is fp32
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLargest = 3.402823466e38f;
 
 // N, the head columns of an item, is the smallest instance that holds a group's heads:
 // 16, 64 or, for bf16 results of d <= 128, 128; larger groups take several items, each
@@ -813,7 +814,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, co
             const int col = c0 + row;
             const float high = fmaxf(fmaxf(quad_s[col], quad_s[N + col]),
                                      fmaxf(quad_s[2 * N + col], quad_s[3 * N + col]));
-            const float m = have ? fmaxf(-nm_s[col], high) : high;
+            // (finite below: where all scores so far are -inf, so are their differences to it)
+            const float m = fmaxf(have ? fmaxf(-nm_s[col], high) : high, -kLargest);
             f_s[col] = have ? ex2(-nm_s[col] - m) : 1.0f;
             nm_s[col] = -m;
           }
@@ -910,7 +912,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, co
             il_s[col] = z;
             if (!have) nm_s[col] = INFINITY;
           } else {
-            il_s[col] = 1.0f / z;
+            il_s[col] = z == 0.0f ? 0.0f : 1.0f / z;  // 0: every score is -inf
             if (a.lse && col < nh)
               a.lse[(size_t)w.t * Hq + h0 + col] =
                   have ? (log2f(z) - nm_s[col]) * kLn2 : -INFINITY;
@@ -950,12 +952,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) k_attend(const Args a, co
           }
 #pragma unroll
           for (int r = 0; r < S; ++r) top = fmaxf(top, m[r]);
-          const bool any = top != -INFINITY;
 #pragma unroll
           for (int r = 0; r < S; ++r) {
             m[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top);
             sum += m[r] * z[r];
           }
+          const bool any = sum != 0.0f;
 #pragma unroll
           for (int r = 0; r < S; ++r) fac[r * N + h] = any ? m[r] / sum : 0.0f;
           if (a.lse && h * D >= lo * 4)

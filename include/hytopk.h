@@ -503,7 +503,7 @@ HYTOPK_API hytopk_status hytopk_cache_read(const void* cache, hytopk_elem cache_
  *        [0, L) counts as no row and sets HYTOPK_DEV_BAD_INDEX. A repeated
  *        index counts as often as it is there. Causality is not checked.
  *   out  [n, Hq, d] bf16 or fp32; lse [n, Hq] fp32 or NULL. A query with no
- *        row gets out = 0 and lse = -inf.
+ *        row, or none whose score is above -inf, gets out = 0 and lse = -inf.
  * Sums and softmax statistics are fp32. The tensor cores take bf16 operands
  * (e4m3 values are bf16 values): a bf16 result uses the weights exp(s - max)
  * rounded to bf16 (an error of the size of the result's own rounding); an fp32
