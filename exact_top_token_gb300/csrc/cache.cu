@@ -253,7 +253,12 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
       for (int k = threadIdx.x >> 5; k < tokens; k += kFastThreads / 32) {
         const int pos = ld_after(a.positions + t0 + k);
         const bool bad = pos < 0 || pos >= kMaxPosition;
-        if (bad && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+        if (bad && a.status) {
+          // of a row that is not written a position does not matter (asked only here: 65521 x 8
+          // rows 57.9 us, 61.3 with every token's slot looked at)
+          const int to = MODE != 0 && a.slots ? ld_after(a.slots + t0 + k) : 0;
+          if (to >= 0 && (MODE == 0 || to < a.L)) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+        }
         float c, s;
         rope_turn((float)pos, f, c, s);
         if (bad) c = s = __int_as_float(0x7fc00000);

@@ -474,9 +474,9 @@ HYTOPK_API hytopk_status hytopk_rope(const void* x, int64_t x_row, int64_t x_hea
  * A NaN or infinite element becomes the NaN code and sets
  * HYTOPK_DEV_NONFINITE. The rotated values are not rounded before they are
  * quantised.
- *   slots[t] = -1 skips the row; any other slot outside [0, L) skips it and
- *   sets HYTOPK_DEV_BAD_INDEX. Slots of one call must be distinct: of rows
- *   with one slot, parts of either may be left there. */
+ *   slots[t] = -1 skips the row, whatever its position is; any other slot
+ *   outside [0, L) skips it and sets HYTOPK_DEV_BAD_INDEX. Slots of one call
+ *   must be distinct: of rows with one slot, parts of either may be left there. */
 HYTOPK_API hytopk_status hytopk_cache_write(const void* x, int64_t x_row, int64_t x_head,
                                             hytopk_elem x_type, int n, int H, int d,
                                             const hytopk_rope_params* rope, const int32_t* slots,
