@@ -550,7 +550,8 @@ def _operators():
 def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_context=None,
                      fast=32.0, slow=1.0, device="cuda"):
     """(inv_freq [rot/2] fp32 tensor, mscale): the frequency table of ``rot``
-    rotated columns, base ** (-2 i / rot), and the factor that goes with it.
+    rotated columns, base ** (-2 i / rot), and the factor that goes with it, to be
+    given to :func:`rope` and :func:`cache_write` for queries and keys alike.
 
     ``scaling`` stretches it for contexts ``factor`` times the original one:
     ``None``; ``"linear"`` (all frequencies divided by the factor); ``"base"``

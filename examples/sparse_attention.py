@@ -27,8 +27,9 @@ class Cache:
             torch.float8_e4m3fn)
         self.scale = torch.ones(rows, heads, device=device)
 
-    def write(self, x, slots, positions=None, freq=None):
-        hk.cache_write(x, self.codes, self.scale, slots=slots, positions=positions, inv_freq=freq)
+    def write(self, x, slots, positions=None, freq=None, mscale=1.0):
+        hk.cache_write(x, self.codes, self.scale, slots=slots, positions=positions, inv_freq=freq,
+                       mscale=mscale)
 
 
 class Layer:
@@ -39,7 +40,9 @@ class Layer:
         self.k, self.heads, self.index_heads, self.d = k, heads, index_heads, d
         self.gen = torch.Generator(device=device).manual_seed(seed)
         self.device = device
-        # half of each row is rotated; frequencies scaled for a context past the original one
+        # half of each row is rotated; frequencies scaled for a context past the original one.
+        # The factor that goes with the table is on queries and keys, wherever they are rotated:
+        # the rotated part of a score carries its square.
         self.freq, self.mscale = hk.rope_frequencies(d // 2, scaling="parts", factor=16.0,
                                                      original_context=4096, device=device)
         self.index_keys = Cache(context, 1, d, device)
@@ -54,8 +57,8 @@ class Layer:
     def append(self, n):
         """n new tokens into the caches; returns their positions."""
         slots = torch.arange(self.length, self.length + n, dtype=torch.int32, device=self.device)
-        self.index_keys.write(self._rows(n, 1), slots, slots, self.freq)
-        self.keys.write(self._rows(n, self.cache_heads), slots, slots, self.freq)
+        self.index_keys.write(self._rows(n, 1), slots, slots, self.freq, self.mscale)
+        self.keys.write(self._rows(n, self.cache_heads), slots, slots, self.freq, self.mscale)
         self.values.write(self._rows(n, self.cache_heads), slots)
         self.length += n
         return slots
@@ -67,7 +70,7 @@ class Layer:
                          device=self.device).view(torch.float8_e4m3fn)
         iq_scale = torch.empty(n, self.index_heads, device=self.device)
         hk.cache_write(self._rows(n, self.index_heads), iq, iq_scale, positions=positions,
-                       inv_freq=self.freq)
+                       inv_freq=self.freq, mscale=self.mscale)
         w = torch.rand(n, self.index_heads, device=self.device, generator=self.gen)
         idx, _, _ = hk.select(iq, self.index_keys.codes[:self.length, 0], w, positions, self.k,
                               q_scale=iq_scale, k_scale=self.index_keys.scale[:self.length, 0])
@@ -83,13 +86,14 @@ class Layer:
         rows = torch.arange(self.length, dtype=torch.int32, device=self.device)
         x_q, x_k = self._rows(n, self.heads), self._rows(self.length, self.cache_heads)
         v = self._rows(self.length, self.cache_heads)
-        q = hk.rope(x_q, positions, self.freq)
-        k = hk.rope(x_k, rows, self.freq)
+        q = hk.rope(x_q, positions, self.freq, mscale=self.mscale)
+        k = hk.rope(x_k, rows, self.freq, mscale=self.mscale)
         out, lse = hk.attend(q, k, v, idx, out_dtype=torch.float32)
         grad = self._rows(n, self.heads)                       # of the loss with respect to out
         dq, dk, dv = hk.attend_backward(q, k, v, idx, out, lse, grad)
-        dx_q = hk.rope(dq, positions, self.freq, inverse=True)  # through the rotation
-        dx_k = hk.rope(dk, rows, self.freq, inverse=True)
+        # through the rotation
+        dx_q = hk.rope(dq, positions, self.freq, mscale=self.mscale, inverse=True)
+        dx_k = hk.rope(dk, rows, self.freq, mscale=self.mscale, inverse=True)
         return out, dx_q, dx_k, dv
 
 
