@@ -1,13 +1,14 @@
 """Compile the CUDA library (sm_103a) in-tree with nvcc: one object per
 translation unit, compiled in parallel, linked into ``_build/libhytopk.so``;
-and, with the host compiler, the operators' Python module against the torch
-that is installed (``csrc/binding.cpp``)."""
+and, where torch is installed, the operators' Python module against it with the
+host compiler (``csrc/binding.cpp``)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,11 +48,14 @@ def stale() -> bool:
     return _older(LIB, _inputs())
 
 
-def binding() -> str:
-    """Path of the operators' Python module, built for this torch."""
-    import torch
-
-    return os.path.join(BUILD, f"_operators-{torch.__version__}.so")
+def binding() -> str | None:
+    """Path of the operators' Python module, built for this Python and this torch; None
+    without torch (the library does not need it)."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return os.path.join(BUILD, f"_operators-{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 
 def _build_binding(out):
@@ -77,16 +81,24 @@ def _build_binding(out):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Build the library and the operators' module if missing or out of date;
-    returns the library's path."""
+    """Build the library and (with torch) the operators' module if missing or out of date;
+    returns the library's path. A module that does not build raises when the library is
+    there."""
     os.makedirs(BUILD, exist_ok=True)
     module = binding()
-    module_stale = force or _older(
-        module, [BINDING_SRC, os.path.join(INCLUDE, "hytopk.h"), __file__])
-    if not force and not stale():
-        if module_stale:
-            _build_binding(module)
-        return LIB
+    if module and not force and not _older(
+            module, [BINDING_SRC, os.path.join(INCLUDE, "hytopk.h"), __file__]):
+        module = None
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        other = ex.submit(_build_binding, module) if module else None
+        if force or stale():
+            _build_library(verbose, extra_flags)
+        if other is not None:
+            other.result()
+    return LIB
+
+
+def _build_library(verbose, extra_flags):
     srcs = sources()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
@@ -98,11 +110,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
-        other = ex.submit(_build_binding, module) if module_stale else None
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
         logs = list(ex.map(compile_one, zip(srcs, objs)))
-        if other is not None:
-            other.result()
     if verbose:
         for s, log in zip(srcs, logs):
             if log.strip():
@@ -112,4 +121,3 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
