@@ -517,7 +517,8 @@ def select_twopass(q, k, w, positions, k_top, *, q_scale=None, k_scale=None, row
 
 # ---- around the selection: rotary positions, cache rows, attention ------------------
 # These calls also serve single tokens, where the time is the host's, so their checks,
-# allocations and calls are in a C++ module (csrc/binding.cpp).
+# allocations and calls are in a C++ module (csrc/binding.cpp). They are not recorded by
+# autograd; with ``stream=`` their results come from that stream's memory.
 
 _module = None
 
@@ -560,6 +561,7 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_co
     (frequencies that turn more than ``fast`` times within
     ``original_context`` are kept, those below ``slow`` turns divided by the
     factor, a linear ramp over the turns between; mscale = 0.1 ln(factor) + 1).
+    A table made another way (a ramp over the column, say) goes to :func:`rope` as it is.
     """
     import math
 

@@ -17,10 +17,10 @@
 // dQ^T takes the first two parts side by side (N = 128) and adds the third to
 // the second's columns.
 //
-// Measured: 2048 queries of 64 heads, 2048 rows of 128 columns: 1235 us (279 TFLOP/s,
-// additions 3.5 TB/s); of 16 heads 836 us (5.1 TB/s); 64 columns 1065 us. Bound by the
-// chain of a tile at 64 heads (80 % of the time remains with no row selected; 17900 warp
-// instructions), by the additions at 16. What made it fast: read-out warps of their own
+// Measured: 2048 queries of 64 heads, 2048 rows of 128 columns: 1215 us (283 TFLOP/s,
+// additions 3.5 TB/s); of 16 heads 835 us (5.1 TB/s); 64 columns 1063 us. Bound by the
+// chain of a tile at 64 heads (80 % of the time remains with no row selected; 18000 warp
+// instructions), by the additions at 16 (12700). What made it fast: read-out warps of their own
 // 1640 -> 1500 us, d along the lanes (whole-line additions) -> 1350, additions predicated
 // instead of branched around and addresses of one instruction -> 1250. P and dS come from
 // the same code in two passes (the exponentials twice), which needs fewer registers.

@@ -32,9 +32,12 @@
 // e4m3 rows are widened to bf16, which holds every e4m3 value: the codes land in the
 // first half of their tile's place in shared memory and warps of their own widen them
 // there. K's row scale joins the factor of the row's scores, V's multiplies its weights.
-// 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 533 us (515 TFLOP/s, rows
-// gathered at 8.0 TB/s), e4m3 rows 700 us; 128 heads 710 and 926 us. Bound by the warp
-// instructions of a tile (6300 and 8100 on four schedulers), most of them the softmax's.
+// 4096 queries of 64 heads, 2048 rows of 128 columns: bf16 rows 531 us (518 TFLOP/s, rows
+// gathered at 8.1 TB/s), e4m3 rows 706 us; 128 heads 711 and 924 us. Bound by the warp
+// instructions of a tile, on four schedulers: 3400, 6340 and 7780 for 16, 64 and 128 heads
+// of bf16 rows, 5530 and 8150 for 16 and 64 of e4m3 ones. The last 64 heads add 5.6 for 32
+// scores, so of the 6340 under a quarter are the scores' own; the rest is paid per warp and
+// tile.
 // For e4m3 rows, widening each row in a producer's registers took 1667 us; multiplying the
 // codes, with q and P in two e4m3 parts, 771 us; copies and widening by the same warps,
 // through a ring of its own, 742 us; widening to f16 with q and P in f16 694 us, but 128
@@ -70,8 +73,8 @@ constexpr float kLargest = 3.402823466e38f;
 // N, the head columns of an item, is the smallest instance that holds a group's heads:
 // 16, 64 or, for bf16 results of d <= 128, 128; larger groups take several items, each
 // gathering the rows anew. 4096 queries, 2048 rows of 128 columns, bf16 and e4m3 rows: 16
-// heads 407 and 508 us with N = 16, 521 and 677 with 64; 128 heads 709 and 1028 us (now
-// 926) with N = 128, 1055 and 1373 with two items of 64.
+// heads 407 and 508 us with N = 16, 521 and 677 with 64; 32 heads, with 64, 522 and 680; 128
+// heads 709 and 1028 us (now 924) with N = 128, 1055 and 1373 with two items of 64.
 template <int D_, int N_, bool E4_, bool F32_, int CTAS_ = 1>
 struct Cfg {
   static constexpr int D = D_, N = N_;
@@ -102,8 +105,8 @@ struct Cfg {
   // room for the ring
   static constexpr int PB = F32 || N > 64 || (E4 && D == 256) ? 1 : 2;
   // Warps that copy rows, and (e4m3) warps that widen them: as many as leave a thread 72
-  // (N = 128: 80) registers. (1024 queries of 32 heads on 8 cache heads: 1019 us with 8
-  // widening warps, 1102 with 4.)
+  // registers for N = 64 and 80 for N = 128, where up to 32 bytes spill. (1024 queries of
+  // 32 heads on 8 cache heads: 1019 us with 8 widening warps, 1102 with 4.)
   static constexpr int PWARPS = E4 || N > 64 ? 4 : 8;
   static constexpr int VWARPS = !E4 ? 0 : N > 64 ? 2 : N > 16 || CTAS > 1 ? 4 : 8;
   static constexpr int RPW = 128 / PWARPS;        // rows of a tile per copying warp

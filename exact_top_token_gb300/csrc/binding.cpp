@@ -3,7 +3,7 @@
 // results' allocation and the call of the C ABI. They also serve single tokens, where
 // a call's time is the host's: written in Python around a foreign call of twenty
 // arguments, attend took the host 20.5 us a call, rope 14.4, cache_read 14.0 and
-// cache_write 9.1; here 6.8, 3.6, 4.1 and 5.4, of which the launch is the most.
+// cache_write 9.1; here 6.8, 3.6, 4.1 and 5.5, of which the launch is the most.
 //
 // The C entry points come as addresses (init), so that this module links to nothing
 // of the library; it is built against the torch that imports it.

@@ -1,10 +1,11 @@
 // cache.cu -- rotary positions (hytopk_rope) and cache rows: quantised as they
 // are written, with the rotation fused in (hytopk_cache_write), and read back
 // (hytopk_cache_read). All three move each row once. Measured, of 6.8 TB/s for a plain
-// copy: rotation of 8192 x 64 x 128 bf16 42.6 us (6.3 TB/s), of 30011 x 8 x 128 fp32
-// 41.8 us (5.9); read of 262144 x 8 x 128 e4m3 as bf16 136 us (6.0), all bound by memory;
-// write of 65521 x 8 x 128 bf16, rotated, as e4m3 62.5 us (3.3), bound by instructions.
-// Of a few rows each takes its launch.
+// copy: rotation of 8192 x 64 x 128 bf16 42.9 us (6.3 TB/s), of 30011 x 8 x 128 fp32
+// 41.7 us (5.9); read of 262144 x 8 x 128 e4m3 as bf16 130 us (6.3), all bound by memory;
+// write of 65521 x 8 x 128 bf16, rotated, as e4m3 58.3 us (3.5), bound by instructions, and
+// of 200000 x 1 x 128, half rotated, 37 us (2.1), most of it the angles that no head
+// shares. Of a few rows each takes its launch.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -35,7 +36,8 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bf
 
 // ---- any d: one (row, head) per warp, its values in shared memory -----------------
 // Kept for head widths other than 64, 128 and 256 (the kernels below need a
-// power of two of 16-byte chunks in a row).
+// power of two of 16-byte chunks in a row). Elements are taken one by one and angles anew
+// for every head: rotation of 43690 x 8 x 192 bf16, 64 columns rotated, 121 us (2.2 TB/s).
 constexpr int kWarps = 4;
 
 template <typename T>
@@ -193,11 +195,12 @@ constexpr uint32_t kTinyRow = 0x219392EFu, kHugeRow = 0x7F000000u;
 
 // MODE 0: rotated rows; 1: into bf16 cache rows; 2: into e4m3 cache rows.
 // V: neighbouring 8-column vectors a lane holds. Quantising is bound by its
-// instructions (400 a lane of 16 elements, 25 an element: rotation, magnitudes, exact
-// quotients, codes); with V = 2 half the lanes share a row's scale, addresses and
-// magnitude steps (8 heads x 65521 rows: 83 -> 68 us). A block takes kIter rows a group,
-// so that the loads of several rows are in flight and their angles are computed once;
-// four blocks an SM (64 registers) 68 -> 65.6 us; quotients two at a time 62.5.
+// instructions (360 a lane of 16 elements: 163 rotation and angles, the rest loads,
+// magnitudes, exact quotients (24) and codes); with V = 2 half the lanes share a row's
+// scale, addresses and magnitude steps (8 heads x 65521 rows: 83 -> 68 us). A block takes
+// kIter rows a group, so that the loads of several rows are in flight and their angles are
+// computed once; four blocks an SM 68 -> 65.6 us (64 registers, and 76 bytes a thread that
+// spill); quotients two at a time 62.5; coherent loads of slots and positions 57.9.
 template <typename T, int D, int MODE, int V>
 __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
   allow_next();
@@ -413,7 +416,8 @@ __global__ void __launch_bounds__(kFastThreads, 4) k_rows(const RowArgs a) {
 template <typename T, int D, int MODE, int V>
 void launch_rows_of(const RowArgs& a, cudaStream_t st) {
   const int per = kFastThreads / (D / (8 * V)) * kIter;  // rows of a block
-  // a block of `per` rows touches at most this many tokens (64 KB of angles at most)
+  // a block of `per` rows touches at most this many tokens (64 KB of angles at most, for rows
+  // of one head: three blocks an SM)
   const int tokens = a.H >= per ? 2 : (per + a.H - 2) / a.H + 1;
   const size_t smem = a.positions ? (size_t)tokens * a.rot * sizeof(float) : 0;
   const unsigned grid = (unsigned)(((int64_t)a.n * a.H + per - 1) / per);
@@ -455,7 +459,7 @@ struct ReadArgs {
 // A thread converts 16-byte chunks of the cache (16 codes or 8 bf16 values),
 // kIter of them kFastThreads apart, all loaded before the first is stored. Bound
 // by memory: every row is read once and written once (262144 x 8 x 128 e4m3 rows as
-// bf16: 136 us, 6.0 TB/s of 6.8).
+// bf16: 130 us, 6.3 TB/s of 6.8).
 template <bool E4M3, typename T>
 __global__ void __launch_bounds__(kFastThreads) k_cache_read(const ReadArgs a) {
   allow_next();
