@@ -120,8 +120,9 @@ __device__ __forceinline__ void store_parts(uint8_t* dst, int row, int c0, float
 }
 
 // SPLIT: CTAs share an item (an instance of its own: the others are 1 to 2 % faster
-// without it).
-template <class C, bool OUT_F32, bool SPLIT>
+// without it). PART: an item may have fewer than N heads (likewise: 64 heads 1215 us without
+// it, 1238 with).
+template <class C, bool OUT_F32, bool SPLIT, bool PART>
 __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a, const Plan pl) {
   constexpr int D = C::D, N = C::N, HG = C::HG, CH = C::CH;
   using Geo = typename C::Geo;
@@ -442,11 +443,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
       return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
     };
     Walk w = start;
-    int i = 0, qi = 0;
+    int i = 0, qi = 0, heads = 0;  // tile of its item, item, its heads from c0 on
     bool ok = true;
     int e_next = total > 0 ? entry_of(w.t, row) : -1;
 #pragma unroll 1
     for (int g = 0; g < total; ++g) {
+      if (PART && i == 0) heads = head_count(w) - c0;
       const bool valid = row_of(e_next) >= 0;
       if (e_next != -1 && !valid && wg == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
       if (g + 1 < total) {
@@ -485,6 +487,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
               p[u] = valid ? dp[u] : 0.0f;  // (0 x NaN of a gradient is none of this row's)
               p[u + 1] = valid ? dp[u + 1] : 0.0f;
             }
+          }
+          // of heads past the group's: their rows are zeros, but 0 times a key that is not
+          // finite is not
+          if (PART && cc + CH > heads) {
+#pragma unroll
+            for (int u = 0; u < CH; ++u) p[u] = cc + u < heads ? p[u] : 0.0f;
           }
           store_parts<CH>(dst, row, c0 + cc, p);
         }
@@ -585,7 +593,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_attend_backward(const Args a,
 
 template <class C, bool OUT_F32>
 cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
-  static unsigned long long opted_in[2] = {0, 0};
+  static unsigned long long opted_in[4] = {0, 0, 0, 0};
   Plan pl{};
   pl.blocks = (a.G + C::N - 1) / C::N;
   pl.heads = (a.G + pl.blocks - 1) / pl.blocks;
@@ -598,12 +606,16 @@ cudaError_t launch_backward(const Args& a, int sms, cudaStream_t st) {
   pl.sb = pl.stride % pl.blocks;
   pl.sh = pl.stride / pl.blocks % a.Hkv;
   pl.st = pl.stride / pl.blocks / a.Hkv;
-  auto kernel = pl.splits > 1 ? k_attend_backward<C, OUT_F32, true> : k_attend_backward<C, OUT_F32, false>;
+  const bool split = pl.splits > 1, part = C::N == 16 || pl.blocks * C::N != a.G;
+  auto kernel = split ? k_attend_backward<C, OUT_F32, true, true> : k_attend_backward<C, OUT_F32, false, true>;
+  if constexpr (C::N != 16)  // (of 16 heads 836 and 840 us: one instance)
+    if (!part)
+      kernel = split ? k_attend_backward<C, OUT_F32, true, false> : k_attend_backward<C, OUT_F32, false, false>;
   const size_t rows = a.zero ? (size_t)a.L * a.Hkv * C::D : 0;
-  const size_t own = pl.splits > 1 ? (size_t)a.n * a.Hkv * a.G * C::D : 0;
+  const size_t own = split ? (size_t)a.n * a.Hkv * a.G * C::D : 0;
   const cudaError_t e = launch_zero(a.dk, a.dv, rows, a.dq, own, sms, st);
   if (e != cudaSuccess) return e;
-  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, opted_in + (pl.splits > 1), [&] {
+  return launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, opted_in + 2 * part + split, [&] {
     return launch_early(kernel, pl.stride * pl.splits, C::THREADS, C::SMEM, st, 1, a, pl);
   });
 }
