@@ -18,7 +18,7 @@
 // the second's columns.
 //
 // Measured: 2048 queries of 64 heads, 2048 rows of 128 columns: 1215 us (283 TFLOP/s,
-// additions 3.5 TB/s); of 16 heads 835 us (5.1 TB/s); 64 columns 1063 us. Bound by the
+// additions 3.5 TB/s); of 16 heads 840 us (5.1 TB/s); 64 columns 1063 us. Bound by the
 // chain of a tile at 64 heads (80 % of the time remains with no row selected; 18000 warp
 // instructions), by the additions at 16 (12700). What made it fast: read-out warps of their own
 // 1640 -> 1500 us, d along the lanes (whole-line additions) -> 1350, additions predicated
@@ -54,7 +54,7 @@ namespace hytopk {
 namespace att {
 
 // N: 16 or 64 head columns; larger groups take several items. (2048 queries of 16 heads:
-// 836 us with N = 16, 1065 with N = 64; of 128 heads, two items of 64: 2364 us.)
+// 840 us with N = 16, 1065 with N = 64; of 128 heads, two items of 64: 2333 us.)
 template <int D_, int N_>
 struct BCfg {
   static constexpr int D = D_, N = N_;
