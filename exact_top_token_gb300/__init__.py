@@ -21,6 +21,8 @@ __all__ = ["build", "load", "select", "select_twopass", "replay", "select_worksp
            "select_sharded", "select_varlen", "replay_varlen", "replay_backward",
            "replay_backward_varlen",
            "rope", "rope_frequencies", "cache_write", "cache_read", "attend", "attend_backward",
+           "page_write", "attend_pages", "page_fork", "page_free", "page_grow", "page_compact",
+           "page_copy",
            "twopass_workspace_size", "sample_plan", "HytopkError", "STATUS", "PHASES", "Stats",
            "symbols"]
 
@@ -33,6 +35,7 @@ DEV_BAD_SCALE = 0x2
 DEV_BAD_POSITION = 0x4
 DEV_BAD_INDEX = DEV_REPLAY_BAD_INDEX
 DEV_NONFINITE = 0x8
+DEV_NO_PAGE = 0x10  # a context has no room to grow
 DEV_WAIT_TIMEOUT = 0x80000000  # a bounded wait gave up: the call's outputs are undefined
 BF16, E4M3, E4M3_BF16 = 0, 1, 2  # E4M3_BF16: e4m3 q (with q_scale), bf16 k
 
@@ -48,6 +51,9 @@ symbols = ("hytopk_select_workspace_size", "hytopk_select_fallback_chunks", "hyt
            "hytopk_replay_backward_varlen", "hytopk_sample_plan",
            "hytopk_rope", "hytopk_cache_write", "hytopk_cache_read", "hytopk_attend",
            "hytopk_attend_backward",
+           "hytopk_attend_pages_workspace_size", "hytopk_attend_pages", "hytopk_page_write",
+           "hytopk_page_workspace_size", "hytopk_page_fork", "hytopk_page_free",
+           "hytopk_page_grow", "hytopk_page_compact", "hytopk_page_copy",
            "hytopk_status_string", "hytopk_version")
 
 
@@ -73,6 +79,12 @@ class RopeParams(ctypes.Structure):
     _fields_ = [("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
                 ("rot", ctypes.c_int), ("first", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("inverse", ctypes.c_int), ("mscale", ctypes.c_float)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("B", ctypes.c_int), ("columns", ctypes.c_int),
+                ("N", ctypes.c_int), ("P", ctypes.c_int)]
 
 
 _lib = None
@@ -140,6 +152,25 @@ def load(path: str | None = None):
     lib.hytopk_attend_backward.restype = I
     lib.hytopk_attend_backward.argtypes = [P, S, P, S, P, S, P, P, I, P, P, I, I, I, I, I, I, F, P,
                                            P, P, I, P, P]
+    lib.hytopk_attend_pages_workspace_size.restype = Z
+    lib.hytopk_attend_pages_workspace_size.argtypes = [I, I, I]
+    lib.hytopk_attend_pages.restype = I
+    lib.hytopk_attend_pages.argtypes = [P, S, P, P, P, P, P, I, I, I, I, F, P, P, P, Z, P, P]
+    lib.hytopk_page_write.restype = I
+    lib.hytopk_page_write.argtypes = [P, S, S, I, I, I, I, P, P, P, P, P, P]
+    lib.hytopk_page_workspace_size.restype = Z
+    lib.hytopk_page_workspace_size.argtypes = [I]
+    pool = [P, P, P, I, I, I, I]  # table, lengths, refs, B, columns, N, P
+    lib.hytopk_page_fork.restype = I
+    lib.hytopk_page_fork.argtypes = pool + [P, P, I, P, P]
+    lib.hytopk_page_free.restype = I
+    lib.hytopk_page_free.argtypes = pool + [P, I, P, P]
+    lib.hytopk_page_grow.restype = I
+    lib.hytopk_page_grow.argtypes = pool + [P, P, P, P, Z, P, P]
+    lib.hytopk_page_compact.restype = I
+    lib.hytopk_page_compact.argtypes = pool + [P, P, P, Z, P, P]
+    lib.hytopk_page_copy.restype = I
+    lib.hytopk_page_copy.argtypes = [P, P, P, P, I, S, I, P, P, I, P, P]
     lib.hytopk_sample_plan.restype = ctypes.c_int32
     lib.hytopk_sample_plan.argtypes = [ctypes.c_int64, ctypes.c_int32, P, P]
     lib.hytopk_status_string.restype = ctypes.c_char_p
@@ -541,9 +572,17 @@ def _operators():
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_file_location("_operators", path, loader=loader))
         loader.exec_module(module)
-        module.init(HytopkError, torch.OutOfMemoryError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+
+        def addresses(*entries):
+            return (ctypes.cast(f, ctypes.c_void_p).value for f in entries)
+
+        module.init(HytopkError, torch.OutOfMemoryError, *addresses(
             lib.hytopk_rope, lib.hytopk_cache_write, lib.hytopk_cache_read, lib.hytopk_attend,
-            lib.hytopk_attend_backward)))
+            lib.hytopk_attend_backward))
+        module.init_pages(*addresses(
+            lib.hytopk_attend_pages_workspace_size, lib.hytopk_attend_pages, lib.hytopk_page_write,
+            lib.hytopk_page_workspace_size, lib.hytopk_page_fork, lib.hytopk_page_free,
+            lib.hytopk_page_grow, lib.hytopk_page_compact, lib.hytopk_page_copy))
         _module = module
     return _module
 
@@ -638,3 +677,71 @@ def attend_backward(q, k, v, idx, out, lse, grad, *, scale=None, dk=None, dv=Non
     tensors are written)."""
     return (_module or _operators()).attend_backward(q, k, v, idx, out, lse, grad, scale, dk, dv,
                                                      status, stream)
+
+
+# ---- a cache in pages -----------------------------------------------------------------
+# One pool of pages [N, P, H, d] (float8_e4m3fn, one fp32 scale per (page, head)) holds the
+# contexts of B sequences: table [B, columns] says which pages, lengths [B] how many rows,
+# refs [N] how many table entries hold a page (0: free); all int32 on the device. The rows of
+# a call belong to the sequences in turn, sequence b's being rows cu_q[b] .. cu_q[b + 1] - 1,
+# and stand at the end of its context, whose length counts them already. A step:
+#
+#     src, dst = page_grow(table, lengths, refs, add, page=P)
+#     page_copy(k_pages, v_pages, k_scale, v_scale, src, dst)          # each layer
+#     page_write(k, k_pages, k_scale, table, lengths, cu_q, inv_freq=freq)
+#     page_write(v, v_pages, v_scale, table, lengths, cu_q)
+#     out, lse = attend_pages(q, k_pages, v_pages, k_scale, v_scale, table, lengths, cu_q)
+
+def page_write(x, pages, page_scale, table, lengths, cu_q=None, *, positions=None, inv_freq=None,
+               first=0, interleaved=False, mscale=1.0, status=None, stream=None):
+    """Write rows x ([n, H, d], bf16 or fp32, row and head strides allowed) to the ends of
+    their contexts, rotated first when ``inv_freq`` is given (by ``positions`` [n], or by the
+    rows' places in their contexts). The scale of a page grows with what it holds: its
+    earlier rows are requantised then. ``cu_q`` [B + 1] (None: a row a sequence)."""
+    return (_module or _operators()).page_write(x, pages, page_scale, table, lengths, cu_q,
+                                                positions, inv_freq, first, interleaved, mscale,
+                                                status, stream)
+
+
+def attend_pages(q, k_pages, v_pages, k_scale, v_scale, table, lengths, cu_q=None, *, scale=None,
+                 out=None, lse=None, status=None, stream=None):
+    """Causal attention of rows q ([n, Hq, d] bf16) over their whole contexts, up to each
+    row's own position: ``(out [n, Hq, d] bf16, lse [n, Hq] fp32)``. ``scale`` defaults to
+    d ** -0.5. Rows past cu_q[B] (a padded batch) are left as they are in ``out`` and
+    ``lse``. For contexts that are attended whole; :func:`attend` takes selected rows."""
+    return (_module or _operators()).attend_pages(q, k_pages, v_pages, k_scale, v_scale, table,
+                                                  lengths, cu_q, scale, out, lse, status, stream)
+
+
+def page_fork(table, lengths, refs, src, dst, *, page, status=None, stream=None):
+    """Sequences ``dst`` [m] (empty, distinct) become holders of the pages of sequences
+    ``src`` [m] (-1: skipped). ``page``: rows of a page. Returns ``table``."""
+    return (_module or _operators()).page_fork(table, lengths, refs, src, dst, page, status, stream)
+
+
+def page_free(table, lengths, refs, sequences, *, page, status=None, stream=None):
+    """Empty ``sequences`` [m] (-1: skipped): their pages lose a holder. Returns ``table``."""
+    return (_module or _operators()).page_free(table, lengths, refs, sequences, page, status, stream)
+
+
+def page_grow(table, lengths, refs, add, *, page, status=None, stream=None):
+    """Every sequence grows by ``add`` [B] rows and gets the pages for them, and one of its
+    own in place of a partly filled last page that others hold. Returns ``(src, dst)`` [B]
+    (-1: none), the copies that :func:`page_copy` makes before anything is written. Where
+    the free pages end, the first sequence that lacks some and those after it stay as they
+    were (status ``DEV_NO_PAGE``)."""
+    return (_module or _operators()).page_grow(table, lengths, refs, add, page, status, stream)
+
+
+def page_compact(table, lengths, refs, *, page, status=None, stream=None):
+    """Renumber the pages in use to the front of the pool. Returns ``(src, dst)``
+    [max(1, N // 2)] (-1 past the last), for :func:`page_copy` on every pool that the table
+    is for, before anything else touches them."""
+    return (_module or _operators()).page_compact(table, lengths, refs, page, status, stream)
+
+
+def page_copy(k_pages, v_pages, k_scale, v_scale, src, dst, *, status=None, stream=None):
+    """Copy pages ``src`` [m] to ``dst`` [m] (-1: skipped) with their scales, in both pools
+    (``v_pages`` and ``v_scale`` may be None)."""
+    return (_module or _operators()).page_copy(k_pages, v_pages, k_scale, v_scale, src, dst, status,
+                                               stream)

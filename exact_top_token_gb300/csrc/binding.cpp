@@ -1,6 +1,7 @@
 // binding.cpp -- the Python entry points of the operators around the selection
-// (rope, cache_write, cache_read, attend, attend_backward): checks of tensors, the
-// results' allocation and the call of the C ABI. They also serve single tokens, where
+// (rope, cache_write, cache_read, attend, attend_backward) and of the cache in pages
+// (page_write, attend_pages, page_fork, page_free, page_grow, page_compact, page_copy):
+// checks of tensors, the results' allocation and the call of the C ABI. They also serve single tokens, where
 // a call's time is the host's: written in Python around a foreign call of twenty
 // arguments, attend took the host 20.5 us a call, rope 14.4, cache_read 14.0 and
 // cache_write 9.1; here 6.8, 3.6, 4.1 and 5.5, of which the launch is the most.
@@ -30,6 +31,15 @@ decltype(&hytopk_cache_write) p_cache_write;
 decltype(&hytopk_cache_read) p_cache_read;
 decltype(&hytopk_attend) p_attend;
 decltype(&hytopk_attend_backward) p_attend_backward;
+decltype(&hytopk_attend_pages_workspace_size) p_attend_pages_workspace_size;
+decltype(&hytopk_attend_pages) p_attend_pages;
+decltype(&hytopk_page_write) p_page_write;
+decltype(&hytopk_page_workspace_size) p_page_workspace_size;
+decltype(&hytopk_page_fork) p_page_fork;
+decltype(&hytopk_page_free) p_page_free;
+decltype(&hytopk_page_grow) p_page_grow;
+decltype(&hytopk_page_compact) p_page_compact;
+decltype(&hytopk_page_copy) p_page_copy;
 PyObject* status_error;  // the package's exception class
 PyObject* memory_error;  // torch's
 
@@ -474,6 +484,286 @@ PyObject* attend_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
   });
 }
 
+// ---- the cache in pages ---------------------------------------------------------------
+
+// [N, P, H, d] e4m3 pages with scales [N, H].
+struct Pages {
+  int N, P, H, d;
+  void* codes;
+  float* scale;
+};
+Pages pages_of(const char* name, const at::Tensor& t, const char* scale_name, PyObject* scale) {
+  if (t.dim() != 4) raise(PyExc_ValueError, name, " must be [pages, rows, heads, d]");
+  if (!t.is_cuda()) raise(PyExc_ValueError, "inputs must be CUDA tensors");
+  elem(name, t.scalar_type(), E4M3);
+  if (!t.is_contiguous()) raise(PyExc_ValueError, name, " must be contiguous");
+  for (const int64_t x : t.sizes())
+    if (x > INT32_MAX) raise(PyExc_ValueError, name, " has an axis of 2^31 or more");
+  Pages p{(int)t.size(0), (int)t.size(1), (int)t.size(2), (int)t.size(3), t.data_ptr(), nullptr};
+  p.scale = static_cast<float*>(need(scale_name, scale, t.device(), at::kFloat, {p.N, p.H}));
+  return p;
+}
+
+// table [B, columns] of a call
+const at::Tensor& table_of(PyObject* o) {
+  const at::Tensor& t = tensor("table", o);
+  if (t.dim() != 2) raise(PyExc_ValueError, "table must be [sequences, columns]");
+  if (!t.is_cuda()) raise(PyExc_ValueError, "inputs must be CUDA tensors");
+  if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX)
+    raise(PyExc_ValueError, "table has an axis of 2^31 or more");
+  return t;
+}
+
+hytopk_paged paged(PyObject* table, PyObject* lengths, PyObject* cu_q, const Pages& p,
+                   at::Device dev) {
+  const at::Tensor& t = table_of(table);
+  const int64_t B = t.size(0);
+  hytopk_paged s{};
+  s.table = static_cast<int32_t*>(need("table", t, dev, at::kInt, t.sizes()));
+  s.lengths = static_cast<int32_t*>(need("lengths", lengths, dev, at::kInt, {B}));
+  if (given(cu_q)) s.cu_q = static_cast<int32_t*>(need("cu_q", cu_q, dev, at::kInt, {B + 1}));
+  s.B = static_cast<int>(B);
+  s.columns = static_cast<int>(t.size(1));
+  s.N = p.N;
+  s.P = p.P;
+  return s;
+}
+
+// page_write(x, pages, page_scale, table, lengths, cu_q, positions, inv_freq, first, interleaved,
+//            mscale, status, stream)
+PyObject* page_write(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 13, [&]() -> PyObject* {
+    const at::Tensor& x = tensor("x", a[0]);
+    const Rows r = rows("x", x);
+    const at::Device dev = x.device();
+    const hytopk_elem type = elem("x", x.scalar_type(), BF16 | F32);
+    const at::Tensor& pages = tensor("pages", a[1]);
+    const Pages p = pages_of("pages", pages, "page_scale", a[2]);
+    if (pages.device() != dev || p.H != r.H || p.d != r.d)
+      raise(PyExc_ValueError, "page rows are ", p.H, " x ", p.d, " on ", pages.device(),
+            ", expected ", r.H, " x ", r.d, " on ", dev);
+    const hytopk_paged s = paged(a[3], a[4], a[5], p, dev);
+    hytopk_rope_params params{};
+    if (given(a[6]) && !given(a[7])) raise(PyExc_ValueError, "positions need inv_freq");
+    if (given(a[7])) {
+      const at::Tensor& f = tensor("inv_freq", a[7]);
+      if (f.dim() != 1) raise(PyExc_ValueError, "inv_freq must be [rot / 2]");
+      if (given(a[6]))
+        params.positions = static_cast<int32_t*>(need("positions", a[6], dev, at::kInt, {r.n}));
+      params.inv_freq = static_cast<float*>(need("inv_freq", f, dev, at::kFloat, f.sizes()));
+      params.rot = static_cast<int>(2 * f.size(0));
+      params.first = integer(a[8]);
+      params.interleaved = truth(a[9]);
+      params.mscale = static_cast<float>(number(a[10]));
+    }
+    uint32_t* status = status_ptr(a[11], dev);
+    const Place place(a[12], dev);
+    call("hytopk_page_write", [&] {
+      return p_page_write(x.data_ptr(), r.row, r.head, type, (int)r.n, (int)r.H, (int)r.d,
+                          given(a[7]) ? &params : nullptr, p.codes, p.scale, &s, status,
+                          place.stream());
+    });
+    return ref(a[1]);
+  });
+}
+
+// attend_pages(q, k_pages, v_pages, k_scale, v_scale, table, lengths, cu_q, scale, out, lse,
+//              status, stream)
+PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 13, [&]() -> PyObject* {
+    const at::Tensor& q = tensor("q", a[0]);
+    const Rows r = packed_rows("q", q);
+    const at::Device dev = q.device();
+    elem("q", q.scalar_type(), BF16);
+    const at::Tensor &kt = tensor("k_pages", a[1]), &vt = tensor("v_pages", a[2]);
+    const Pages k = pages_of("k_pages", kt, "k_scale", a[3]);
+    const Pages v = pages_of("v_pages", vt, "v_scale", a[4]);
+    if (kt.sizes() != vt.sizes()) raise(PyExc_ValueError, "k_pages and v_pages must have one shape");
+    if (k.d != r.d || kt.device() != dev || vt.device() != dev)
+      raise(PyExc_ValueError, "k_pages and v_pages rows must be [", r.d, "] per head on ", dev);
+    const hytopk_paged s = paged(a[5], a[6], a[7], k, dev);
+    const float scale = static_cast<float>(given(a[8]) ? number(a[8]) : std::pow((double)r.d, -0.5));
+    const int64_t shape[3] = {r.n, r.H, r.d};
+    at::Tensor out, lse;
+    if (given(a[9])) need("out", out = tensor("out", a[9]), dev, at::kBFloat16, shape);
+    if (given(a[10])) need("lse", lse = tensor("lse", a[10]), dev, at::kFloat, {r.n, r.H});
+    uint32_t* status = status_ptr(a[11], dev);
+    const Place place(a[12], dev);
+    if (!given(a[9])) out = empty(shape, at::kBFloat16, dev);
+    if (!given(a[10])) lse = empty({r.n, r.H}, at::kFloat, dev);
+    place.result(out, given(a[9]));
+    place.result(lse, given(a[10]));
+    const size_t bytes = p_attend_pages_workspace_size((int)r.H, k.H, (int)r.d);
+    const at::Tensor workspace = empty({(int64_t)bytes}, at::kByte, dev);
+    call("hytopk_attend_pages", [&] {
+      return p_attend_pages(q.data_ptr(), r.row, k.codes, k.scale, v.codes, v.scale, &s, (int)r.n,
+                            (int)r.H, k.H, (int)r.d, scale, out.data_ptr(),
+                            static_cast<float*>(lse.data_ptr()), workspace.data_ptr(), bytes,
+                            status, place.stream());
+    });
+    PyObject* o = given(a[9]) ? ref(a[9]) : THPVariable_Wrap(std::move(out));
+    PyObject* l = given(a[10]) ? ref(a[10]) : THPVariable_Wrap(std::move(lse));
+    return Py_BuildValue("(NN)", o, l);
+  });
+}
+
+// The pool's state: table [B, columns], lengths [B], refs [N].
+struct Pool {
+  at::Device dev;
+  int32_t *table, *lengths, *refs;
+  int B, columns, N, P;
+};
+Pool pool_of(PyObject* table, PyObject* lengths, PyObject* refs, PyObject* page) {
+  const at::Tensor& t = table_of(table);
+  const at::Tensor& r = tensor("refs", refs);
+  Pool p{t.device(), nullptr, nullptr, nullptr, (int)t.size(0), (int)t.size(1), 0, integer(page)};
+  p.table = static_cast<int32_t*>(need("table", t, p.dev, at::kInt, t.sizes()));
+  p.lengths = static_cast<int32_t*>(need("lengths", lengths, p.dev, at::kInt, {p.B}));
+  if (r.dim() != 1 || r.size(0) > INT32_MAX)
+    raise(PyExc_ValueError, "refs must be [pages], fewer than 2^31");
+  p.refs = static_cast<int32_t*>(need("refs", r, p.dev, at::kInt, r.sizes()));
+  p.N = (int)r.size(0);
+  return p;
+}
+int32_t* list_of(const char* name, PyObject* o, at::Device dev, int& count) {
+  const at::Tensor& t = tensor(name, o);
+  if (t.dim() != 1 || t.size(0) > INT32_MAX)
+    raise(PyExc_ValueError, name, " must be [count], fewer than 2^31");
+  count = (int)t.size(0);
+  return static_cast<int32_t*>(need(name, t, dev, at::kInt, t.sizes()));
+}
+
+// page_fork(table, lengths, refs, src, dst, page, status, stream)
+PyObject* page_fork(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 8, [&]() -> PyObject* {
+    const Pool p = pool_of(a[0], a[1], a[2], a[5]);
+    int count = 0, other = 0;
+    const int32_t* src = list_of("src", a[3], p.dev, count);
+    const int32_t* dst = list_of("dst", a[4], p.dev, other);
+    if (count != other) raise(PyExc_ValueError, "src and dst must have one length");
+    uint32_t* status = status_ptr(a[6], p.dev);
+    const Place place(a[7], p.dev);
+    call("hytopk_page_fork", [&] {
+      return p_page_fork(p.table, p.lengths, p.refs, p.B, p.columns, p.N, p.P, src, dst, count,
+                         status, place.stream());
+    });
+    return ref(a[0]);
+  });
+}
+
+// page_free(table, lengths, refs, rows, page, status, stream)
+PyObject* page_free(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 7, [&]() -> PyObject* {
+    const Pool p = pool_of(a[0], a[1], a[2], a[4]);
+    int count = 0;
+    const int32_t* rows = list_of("sequences", a[3], p.dev, count);
+    uint32_t* status = status_ptr(a[5], p.dev);
+    const Place place(a[6], p.dev);
+    call("hytopk_page_free", [&] {
+      return p_page_free(p.table, p.lengths, p.refs, p.B, p.columns, p.N, p.P, rows, count, status,
+                         place.stream());
+    });
+    return ref(a[0]);
+  });
+}
+
+// The lists of copies that page_grow and page_compact make: [2, count], as two tensors.
+PyObject* lists(const at::Tensor& both) {
+  PyObject* src = THPVariable_Wrap(both.select(0, 0));
+  PyObject* dst = THPVariable_Wrap(both.select(0, 1));
+  return Py_BuildValue("(NN)", src, dst);
+}
+
+// page_grow(table, lengths, refs, add, page, status, stream)
+PyObject* page_grow(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 7, [&]() -> PyObject* {
+    const Pool p = pool_of(a[0], a[1], a[2], a[4]);
+    const void* add = need("add", a[3], p.dev, at::kInt, {p.B});
+    uint32_t* status = status_ptr(a[5], p.dev);
+    const Place place(a[6], p.dev);
+    at::Tensor both = empty({2, p.B}, at::kInt, p.dev);
+    place.result(both);
+    const size_t bytes = p_page_workspace_size(p.N);
+    const at::Tensor workspace = empty({(int64_t)bytes}, at::kByte, p.dev);
+    int32_t* src = static_cast<int32_t*>(both.data_ptr());
+    call("hytopk_page_grow", [&] {
+      return p_page_grow(p.table, p.lengths, p.refs, p.B, p.columns, p.N, p.P,
+                         static_cast<const int32_t*>(add), src, src + p.B, workspace.data_ptr(),
+                         bytes, status, place.stream());
+    });
+    return lists(both);
+  });
+}
+
+// page_compact(table, lengths, refs, page, status, stream)
+PyObject* page_compact(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 6, [&]() -> PyObject* {
+    const Pool p = pool_of(a[0], a[1], a[2], a[3]);
+    uint32_t* status = status_ptr(a[4], p.dev);
+    const Place place(a[5], p.dev);
+    const int64_t most = p.N > 3 ? p.N / 2 : 1;
+    at::Tensor both = empty({2, most}, at::kInt, p.dev);
+    place.result(both);
+    const size_t bytes = p_page_workspace_size(p.N);
+    const at::Tensor workspace = empty({(int64_t)bytes}, at::kByte, p.dev);
+    int32_t* src = static_cast<int32_t*>(both.data_ptr());
+    call("hytopk_page_compact", [&] {
+      return p_page_compact(p.table, p.lengths, p.refs, p.B, p.columns, p.N, p.P, src, src + most,
+                            workspace.data_ptr(), bytes, status, place.stream());
+    });
+    return lists(both);
+  });
+}
+
+// page_copy(k_pages, v_pages, k_scale, v_scale, src, dst, status, stream)
+PyObject* page_copy(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 8, [&]() -> PyObject* {
+    const at::Tensor& kt = tensor("k_pages", a[0]);
+    const Pages k = pages_of("k_pages", kt, "k_scale", a[2]);
+    const at::Device dev = kt.device();
+    Pages v{};
+    if (given(a[1]) != given(a[3])) raise(PyExc_ValueError, "v_pages and v_scale go together");
+    if (given(a[1])) {
+      const at::Tensor& vt = tensor("v_pages", a[1]);
+      v = pages_of("v_pages", vt, "v_scale", a[3]);
+      if (vt.sizes() != kt.sizes() || vt.device() != dev)
+        raise(PyExc_ValueError, "k_pages and v_pages must have one shape and device");
+    }
+    int count = 0, other = 0;
+    const int32_t* src = list_of("src", a[4], dev, count);
+    const int32_t* dst = list_of("dst", a[5], dev, other);
+    if (count != other) raise(PyExc_ValueError, "src and dst must have one length");
+    uint32_t* status = status_ptr(a[6], dev);
+    const Place place(a[7], dev);
+    call("hytopk_page_copy", [&] {
+      return p_page_copy(k.codes, k.scale, v.codes, v.scale, k.N, (int64_t)k.P * k.H * k.d, k.H,
+                         src, dst, count, status, place.stream());
+    });
+    return ref(Py_None);
+  });
+}
+
+// init_pages(addresses of the C entry points of the cache in pages)
+PyObject* init_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
+  return guarded(na, 9, [&]() -> PyObject* {
+    void* p[9];
+    for (int i = 0; i < 9; ++i) {
+      p[i] = PyLong_AsVoidPtr(a[i]);
+      if (PyErr_Occurred()) throw Raised{};
+    }
+    p_attend_pages_workspace_size = reinterpret_cast<decltype(p_attend_pages_workspace_size)>(p[0]);
+    p_attend_pages = reinterpret_cast<decltype(p_attend_pages)>(p[1]);
+    p_page_write = reinterpret_cast<decltype(p_page_write)>(p[2]);
+    p_page_workspace_size = reinterpret_cast<decltype(p_page_workspace_size)>(p[3]);
+    p_page_fork = reinterpret_cast<decltype(p_page_fork)>(p[4]);
+    p_page_free = reinterpret_cast<decltype(p_page_free)>(p[5]);
+    p_page_grow = reinterpret_cast<decltype(p_page_grow)>(p[6]);
+    p_page_compact = reinterpret_cast<decltype(p_page_compact)>(p[7]);
+    p_page_copy = reinterpret_cast<decltype(p_page_copy)>(p[8]);
+    return ref(Py_None);
+  });
+}
+
 // init(error class, torch's out-of-memory class, addresses of the five C entry points)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t na) {
   return guarded(na, 7, [&]() -> PyObject* {
@@ -498,6 +788,9 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t na) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(init),   METHOD(rope),   METHOD(cache_write),
                          METHOD(cache_read), METHOD(attend), METHOD(attend_backward),
+                         METHOD(init_pages), METHOD(page_write), METHOD(attend_pages),
+                         METHOD(page_fork), METHOD(page_free), METHOD(page_grow),
+                         METHOD(page_compact), METHOD(page_copy),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -105,6 +105,7 @@ typedef enum { HYTOPK_BF16 = 0, HYTOPK_E4M3 = 1, HYTOPK_E4M3_BF16 = 2 } hytopk_d
 #define HYTOPK_DEV_BAD_POSITION 0x4u     /* a position outside [0, L): that query is all -1 */
 #define HYTOPK_DEV_BAD_INDEX HYTOPK_DEV_REPLAY_BAD_INDEX /* a slot or index outside [0, L), not -1 */
 #define HYTOPK_DEV_NONFINITE 0x8u        /* a NaN or infinite value was quantised */
+#define HYTOPK_DEV_NO_PAGE 0x10u         /* a context has no room to grow: pages or table columns */
 /* A bounded wait inside a tensor-core kernel gave up (after 2 s): the kernel
  * stopped its loops, freed its tensor memory and returned, so every output of
  * that call is undefined. It signals a stalled GPU or a library bug. */
@@ -545,6 +546,130 @@ HYTOPK_API hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
                                                 int d, int k_top, float scale, float* dq,
                                                 float* dk, float* dv, int accumulate,
                                                 uint32_t* dev_status, cudaStream_t stream);
+
+/* ---- a cache in pages ---------------------------------------------------------------
+ * Contexts of many sequences in one pool of pages: a page is P rows, held as e4m3 codes
+ * with one fp32 scale per (page, head), and belongs to one or several sequences. The
+ * conventions are those of the section above.
+ *
+ *   pages   [N, P, H, d] e4m3, contiguous; page_scale [N, H] fp32, finite and > 0.
+ *           P in {16, 32, 64, 128, 256}. Row j of a context is row j % P of its page j / P.
+ *   table   [B, columns] int32: page ids of each sequence's context, in order
+ *   lengths [B] int32: rows of each context
+ *   refs    [N] int32: how many table entries hold a page; 0: free
+ *
+ * Rows of a call (queries, keys) are those of all sequences one after another; sequence
+ * b's are rows cu_q[b] .. cu_q[b+1] - 1 and stand at the END of its context: row i of m at
+ * position lengths[b] - m + i. cu_q [B + 1] int32, non-decreasing, or NULL: one row for
+ * each sequence (then n = B). Rows past cu_q[B] belong to no sequence: what belongs to
+ * them in the outputs is left as it is. lengths below 0 or past columns * P, and cu_q that
+ * leave 0 .. n or decrease, are brought back into the range and set
+ * HYTOPK_DEV_BAD_POSITION; a row at a negative position sees nothing and is not written. */
+typedef struct {
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* cu_q; /* or NULL */
+  int B, columns, N, P;
+} hytopk_paged;
+
+/* Attention of each row over its whole context up to its own position p (causal):
+ *   s[j] = scale * k_scale[page, hk] * q[t,h] . k[page, row, hk],  j = 0 .. p, hk = h / G
+ *   out[t,h] = sum_j softmax(s)[j] * v_scale[page, hk] * v[page, row, hk]
+ *   lse[t,h] = log sum_j exp(s[j])
+ *   q [n, Hq, d] bf16, row stride q_row (heads contiguous); G = Hq / Hkv
+ *   out [n, Hq, d] bf16; lse [n, Hq] fp32 or NULL
+ * A row that sees nothing, or no score above -inf, gets out = 0 and lse = -inf. A table
+ * entry of -1 inside a context is rows that are not there; any other entry outside [0, N)
+ * counts as such and sets HYTOPK_DEV_BAD_INDEX. Rows past a row's position never reach
+ * it, whatever they hold. A scale that is not finite and above 0 makes the rows that see
+ * its page NaN and sets HYTOPK_DEV_BAD_SCALE.
+ * Scores, softmax statistics and sums are fp32. The tensor cores take codes and queries as
+ * f16, which holds every e4m3 value, and queries to 2^-39 of their row's largest (a power
+ * of two is taken out of each); weights are rounded to f16, 11 bits and at least 2^-28 of
+ * the largest, where the result has 8.
+ *   1 <= G <= 128, d in {64, 128}, n * Hq < 2^31. Base pointers 16-byte aligned, q_row a
+ *   multiple of 8.
+ *   workspace: hytopk_attend_pages_workspace_size bytes (parts of contexts that several
+ *   multiprocessors share), 256-byte aligned; it holds nothing between calls. */
+HYTOPK_API size_t hytopk_attend_pages_workspace_size(int Hq, int Hkv, int d);
+HYTOPK_API hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const void* k_pages,
+                                             const float* k_scale, const void* v_pages,
+                                             const float* v_scale, const hytopk_paged* paged,
+                                             int n, int Hq, int Hkv, int d, float scale, void* out,
+                                             float* lse, void* workspace, size_t workspace_bytes,
+                                             uint32_t* dev_status, cudaStream_t stream);
+
+/* The rows x [n, H, d] (bf16 or fp32, strides as in hytopk_rope), rotated if `rope` is not
+ * NULL, into their places at the end of each context. rope->positions may be NULL: the
+ * rows' positions in their contexts.
+ *   scale of (page, head) = max(amax / 448, 2^-126) over the finite new elements of the page
+ *     (1 if the page holds only zeros), and at least the old scale where the page holds
+ *     earlier rows of the context; code = x / scale rounded to nearest even
+ *   earlier rows of a page whose scale grows: code = code * (old / new), the quotient in
+ *     fp32, rounded to nearest even. Rows of a page past the context are left as they are.
+ * A NaN or infinite element becomes the NaN code and sets HYTOPK_DEV_NONFINITE; an old
+ * scale that is not finite and above 0 counts as none (its rows become the NaN code) and
+ * sets HYTOPK_DEV_BAD_SCALE. Rows whose entry is -1 are skipped, as are those of any other
+ * entry outside [0, N), which set HYTOPK_DEV_BAD_INDEX. A page that is written must be
+ * one sequence's alone (see hytopk_page_grow).
+ *   d in {64, 128, 256}, H >= 1, n * H < 2^31; alignment as hytopk_cache_write. */
+HYTOPK_API hytopk_status hytopk_page_write(const void* x, int64_t x_row, int64_t x_head,
+                                           hytopk_elem x_type, int n, int H, int d,
+                                           const hytopk_rope_params* rope, void* pages,
+                                           float* page_scale, const hytopk_paged* paged,
+                                           uint32_t* dev_status, cudaStream_t stream);
+
+/* The pool's bookkeeping, in place and on the device; no page is moved by these four.
+ * `count` sequence numbers are device int32 arrays; -1 is skipped, any other number outside
+ * [0, B) is skipped and sets HYTOPK_DEV_BAD_INDEX, as does a context whose length or pages
+ * are out of range (its bad pages are left out). Entries of a table row past the
+ * context's pages are taken to be -1 and left so.
+ *
+ * hytopk_page_fork: sequence dst[i] becomes another holder of all pages of sequence
+ *   src[i] (its length too). dst[i] must be empty (length 0), appear once in dst and not in
+ *   src; otherwise that entry (of a repeated dst all but the first) is skipped with
+ *   HYTOPK_DEV_BAD_INDEX.
+ * hytopk_page_free: the pages of each sequence lose a holder; its entries become -1, its
+ *   length 0. A sequence given twice is freed once.
+ * hytopk_page_grow: every sequence b grows by add[b] >= 0 rows: its table row gets the
+ *   pages it needs and lengths[b] the sum. Where its last page is partly filled and has
+ *   other holders, it gets a page of its own for it, and src_out[b], dst_out[b] (-1, -1
+ *   otherwise) say which page hytopk_page_copy must copy before anything is written; if
+ *   all holders of such a page grow in this call the last of them keeps it. Pages are
+ *   the lowest-numbered free ones, to sequences in order. The first sequence for which they
+ *   do not suffice and all after it stay as they are (HYTOPK_DEV_NO_PAGE), as does one
+ *   whose context would pass columns * P. workspace: hytopk_page_workspace_size(N) bytes.
+ * hytopk_page_compact: with K pages in use, those numbered K and up, in ascending order, are
+ *   to move to the free ones below K, in ascending order: src_out, dst_out [max(1, N / 2)]
+ *   (-1 past the last move) for hytopk_page_copy, with table and refs changed already.
+ *   B may be 0. workspace as above. */
+HYTOPK_API hytopk_status hytopk_page_fork(int32_t* table, int32_t* lengths, int32_t* refs, int B,
+                                          int columns, int N, int P, const int32_t* src,
+                                          const int32_t* dst, int count, uint32_t* dev_status,
+                                          cudaStream_t stream);
+HYTOPK_API hytopk_status hytopk_page_free(int32_t* table, int32_t* lengths, int32_t* refs, int B,
+                                          int columns, int N, int P, const int32_t* rows,
+                                          int count, uint32_t* dev_status, cudaStream_t stream);
+HYTOPK_API size_t hytopk_page_workspace_size(int N);
+HYTOPK_API hytopk_status hytopk_page_grow(int32_t* table, int32_t* lengths, int32_t* refs, int B,
+                                          int columns, int N, int P, const int32_t* add,
+                                          int32_t* src_out, int32_t* dst_out, void* workspace,
+                                          size_t workspace_bytes, uint32_t* dev_status,
+                                          cudaStream_t stream);
+HYTOPK_API hytopk_status hytopk_page_compact(int32_t* table, const int32_t* lengths, int32_t* refs,
+                                             int B, int columns, int N, int P, int32_t* src_out,
+                                             int32_t* dst_out, void* workspace,
+                                             size_t workspace_bytes, uint32_t* dev_status,
+                                             cudaStream_t stream);
+
+/* Pages src[i] to dst[i], i = 0 .. count - 1, with their scales, in one or two pools of N
+ * pages (v_pages and v_scale may be NULL). A pair with a -1 is skipped; any other number
+ * outside [0, N) skips it and sets HYTOPK_DEV_BAD_INDEX. A page must not be in dst twice, nor in
+ * both lists unless its pair is (p, p). page_bytes = P * H * d, a multiple of 16. */
+HYTOPK_API hytopk_status hytopk_page_copy(void* k_pages, float* k_scale, void* v_pages,
+                                          float* v_scale, int N, int64_t page_bytes, int H,
+                                          const int32_t* src, const int32_t* dst, int count,
+                                          uint32_t* dev_status, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 HYTOPK_API const char* hytopk_status_string(hytopk_status status);
