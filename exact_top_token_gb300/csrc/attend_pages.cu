@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(128) k_attend_pages(const AttendArgs a) {
   float q[E], o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[(size_t)t * a.q_row + (size_t)h * D + lane * E + e]);
+    q[e] = __bfloat162float(a.q[(size_t)t * a.q_row + (size_t)h * D + lane * E + e]) * 0x1p-40f;
     o[e] = 0.0f;
   }
   for (int j = 0; j <= last; ++j) {
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128) k_attend_pages(const AttendArgs a) {
       v[e + 1] = v2.y;
     }
     for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-    x *= a.scale * ks;
+    x *= a.scale * ks * 0x1p40f;
     if (x == -INFINITY) continue;
     const float top = fmaxf(m, x), f = m == -INFINITY ? 0.0f : expf(m - top), p = expf(x - top);
     m = top;
