@@ -153,7 +153,7 @@ def load(path: str | None = None):
     lib.hytopk_attend_backward.argtypes = [P, S, P, S, P, S, P, P, I, P, P, I, I, I, I, I, I, F, P,
                                            P, P, I, P, P]
     lib.hytopk_attend_pages_workspace_size.restype = Z
-    lib.hytopk_attend_pages_workspace_size.argtypes = [I, I, I]
+    lib.hytopk_attend_pages_workspace_size.argtypes = [I, I, I, I]
     lib.hytopk_attend_pages.restype = I
     lib.hytopk_attend_pages.argtypes = [P, S, P, P, P, P, P, I, I, I, I, F, P, P, P, Z, P, P]
     lib.hytopk_page_write.restype = I

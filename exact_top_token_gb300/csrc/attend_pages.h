@@ -1,0 +1,35 @@
+// attend_pages.h -- arguments of the attention over a cache in pages (internal).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "pages.h"
+
+namespace hytopk {
+namespace pages {
+
+constexpr int kMaxCtas = 160;  // shares of a call's work
+
+struct AttendArgs {
+  const __nv_bfloat16* q;
+  int64_t q_row;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  hytopk_paged s;
+  int n, Hkv, G;
+  int tokens;  // of a block of 128 rows: 128 / G
+  int shift;   // log2 of a page's rows
+  float scale;
+  __nv_bfloat16* out;
+  float* lse;
+  uint32_t* status;
+  float* part;   // [2 * ctas][rows][d] unnormalised results
+  float2* ml;    // [2 * ctas][rows] their sums and -m
+  int4* record;  // [2 * ctas][2]: what each is a part of
+  int rows;      // of a part
+};
+
+}  // namespace pages
+}  // namespace hytopk

@@ -1,0 +1,1195 @@
+// attend_pages_engine.cuh -- attention over a cache in pages on the tensor cores
+// (hytopk_attend_pages).
+//
+// An item is a cache head and up to 256 of the (token, head) rows that read it: tokens
+// neighbour in one sequence, so that they share keys. Keys are taken 128 at a time (a
+// tile); the rows are the 128 lanes of the tensor core, two blocks of them:
+//
+//   S [128 rows x 128 keys]  = Q . K^T    (both from shared memory, K-major)
+//   O [128 rows x d]        += P . V      (P from tensor memory, where it takes S's place)
+//
+// so a thread of the softmax owns a row: its maximum and sum need no other lane. Items of
+// more than a block of rows (A) give each of the two warpgroups a block, and both use every
+// tile; smaller ones, single tokens above all (B), give both warpgroups the same rows and
+// every other tile each, and the two results are joined in tensor memory.
+//
+// e4m3 codes are widened to f16, which holds every e4m3 value. The page scales never touch
+// them: sixteen neighbouring keys lie in one page (a group), so k's scale is a factor of a
+// group's scores, and v's, as b = log2(v_scale / reference), a summand of its exponents. The
+// weights 2^(s + b - m) are what is rounded to f16 and multiplied with the codes; their sum
+// over a group times 2^-b is the group's share of the softmax's denominator. m is at least
+// the largest s + b of the first tiles less 4, and is raised, with O scaled, when a weight
+// would pass 2^11: weights have 11 bits down to 2^-18 of the largest product with v's scale
+// and an error of 2^-29 of it below. m is a whole number, so that s + (b - m) is rounded
+// once. Queries are taken to f16 with a power of two out of each row.
+//
+// A masked weight is 0 whatever the score is, but 0 times a NaN code of v is not: in the
+// tiles that hold keys some row does not see, NaN codes of v are replaced by 0 and, by column,
+// the first key that has one is kept; the rows that see it become NaN there at the end.
+//
+// The work of a call is only known on the device (contexts and their new rows). Every CTA
+// adds it up, in units of a tile's time, and takes an equal share of it in order, tile by
+// tile: an item that lies in several shares leaves unnormalised parts in the workspace,
+// and a second kernel joins them. The result does not depend on timing.
+//
+//   warp 0        MMA issuer, TMEM
+//   warp 1        this CTA's segments: (item, tiles) in order, through a ring
+//   warp 2        page scales of a tile, through a ring
+//   warps 4-11    softmax, two warpgroups; queries; results
+//   warps 12-15   codes: loads of the next tile in registers, widened into the ring
+#pragma once
+
+#include "attend_engine.cuh"
+#include "attend_pages.h"
+
+namespace hytopk {
+namespace pages {
+
+using att::add2;
+using att::elect_one;
+using att::ex2;
+using att::fma2;
+using att::max3;
+using att::wait_bar;
+
+constexpr int kOverhead = 2;   // of an item, in the units below
+constexpr int kSegs = 8;       // ring of segments
+constexpr int kConsts = 8;     // ring of the tiles' scales
+constexpr int kThreads = 512;
+// Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 176 + 96) = 65536.
+constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 176, kRegsWide = 96;
+static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
+
+// A segment: tiles [t0, t1) of an item.
+struct Seg {
+  int b, hk, row0, tokens;  // sequence, cache head, first row of q, tokens
+  int p0, end;              // position of the first token; keys of the last one
+  int t0, t1;
+  int flags, part;          // part: its number, -1: the whole item
+};
+enum : int { kStop = 1, kSmall = 2, kStarts = 4, kEnds = 8 };
+
+struct TileConst {
+  float2 group[8];  // factor of the scores, b
+  float ref;        // reference of v's scales
+  uint32_t absent;  // groups that are not there
+  uint32_t pad[2];
+};
+
+template <int D_>
+struct PCfg {
+  static constexpr int D = D_;
+  static constexpr int RB = 2 * D;
+  using Geo = tc::Geo<RB>;
+  static constexpr int SLOT = 128 * RB;
+  static constexpr int NS = D == 128 ? 4 : 8;  // even: K in even slots, V in odd ones
+  static constexpr int NANS = D == 128 ? 4 : 8;  // items whose NaN columns are kept: see below
+  static constexpr int Q_OFF = NS * SLOT;
+  static constexpr int NAN_OFF = Q_OFF + 2 * SLOT;
+  static constexpr int CONST_OFF = NAN_OFF + NANS * 8 * D * 4;
+  static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
+  static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
+  static constexpr int BAR_OFF = (ML_OFF + 128 * 8 + 15) / 16 * 16;
+  static constexpr int SMEM = BAR_OFF + 768 + 1024;
+  static constexpr int S_COL = 0, O_COL = 256, COLS = 512;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(NS % 2 == 0 && NS / 2 + 2 <= kConsts, "rings");
+  // V of a later item is written while results of item i are awaited: with V of item
+  // i + 1 held back, up to V of item i + NS / 2.
+  static_assert(NANS > NS / 2, "NaN columns");
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// four codes to four f16
+__device__ __forceinline__ uint2 widen(uint32_t codes) {
+  uint2 r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(codes));
+  return r;
+}
+// bytes that are NaN codes, as 0x80 each
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// D[tmem] (+)= A . B, f16: A and B in shared memory, or A in tensor memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t add) {
+  tc::mma<0>(d, a, b, idesc, add);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// f16 operands, fp32 sums, M = 128
+__host__ __device__ constexpr uint32_t f16_desc(int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// ---- the work of a call ---------------------------------------------------------------
+
+// sum of floor((a j + b) / m) over j < n; a, b >= 0 (lattice points under a line, by the steps of
+// Euclid's algorithm)
+static __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// A sequence's items for one cache head: blocks of `per` = 2 * tokens tokens.
+struct Work {
+  int m, start, per, count;  // start: position of the first token (may be negative)
+
+  __device__ Work(const AttendArgs& a, const Seq& q)
+      : m(q.m), start(q.length - q.m), per(2 * a.tokens), count((q.m + per - 1) / per) {}
+  __device__ int tokens_of(int i) const { return min(per, m - i * per); }
+  __device__ int tiles_of(int i) const {
+    const int last = start + i * per + tokens_of(i) - 1;
+    return last < 0 ? 0 : (last >> 7) + 1;
+  }
+  // a tile of a large item takes twice a small one's time
+  __device__ int unit_of(int i) const { return 2 * tokens_of(i) > per ? 2 : 1; }
+  __device__ int64_t weight_of(int i) const {
+    return kOverhead + (int64_t)unit_of(i) * tiles_of(i);
+  }
+  // weight of the items before i
+  __device__ int64_t before(int i) const {
+    if (i <= 0) return 0;
+    if (i == count) return before(i - 1) + weight_of(i - 1);
+    // whole items: floor((start + (j + 1) per - 1) / 128) + 1 tiles from the first that has any
+    const int first = start >= 0 ? 0 : max((1 - start + per - 1) / per - 1, 0);
+    int64_t w = (int64_t)kOverhead * i;
+    if (i > first)
+      w += 2 * (floor_sum(i - first, 128, per, (int64_t)start + (int64_t)(first + 1) * per - 1) +
+                (i - first));
+    return w;
+  }
+};
+
+// Where a CTA's share begins: item `i` of head `hk` of sequence `b`, and its first unit.
+struct Share {
+  int64_t lo, hi, at;
+  int b, hk, i, any;
+};
+
+template <typename T>
+__device__ __forceinline__ T scan512(T x, T* warps, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warps[w];
+    total += warps[w];
+  }
+  return before + s - x;
+}
+
+// All threads; the result is in `share` (shared memory) after the next barrier.
+__device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, Share* share) {
+  int64_t mine = 0, kept = 0, total;
+  for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
+    const Seq q = seq_of(a.s, a.n, b);
+    if (q.bad && blockIdx.x == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
+    if (q.m > 0) {
+      const Work w(a, q);
+      kept = w.before(w.count) * a.Hkv;
+      mine += kept;
+    }
+  }
+  int64_t at = scan512(mine, warps, total);
+  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (threadIdx.x == 0) {
+    share->lo = lo;
+    share->hi = hi;
+    share->any = 0;
+  }
+  __syncthreads();
+  if (lo == hi) return;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t all = mine;  // one pass: as it was
+    if (a.s.B > kThreads) {
+      all = 0;
+      if (b < a.s.B) {
+        const Seq q = seq_of(a.s, a.n, b);
+        if (q.m > 0) {
+          const Work w(a, q);
+          all = w.before(w.count) * a.Hkv;
+        }
+      }
+      at = base + scan512(all, warps, total);
+    }
+    if (all > 0 && lo >= at && lo < at + all) {
+      const Work w(a, seq_of(a.s, a.n, b));
+      const int64_t head = all / a.Hkv;
+      const int hk = (int)((lo - at) / head);
+      const int64_t in = lo - at - hk * head;
+      int i = 0, j = w.count;  // before(i) <= in < before(j)
+      while (j - i > 1) {
+        const int mid = (i + j) / 2;
+        if (w.before(mid) <= in) i = mid;
+        else j = mid;
+      }
+      share->b = b;
+      share->hk = hk;
+      share->i = i;
+      share->at = at + hk * head + w.before(i);
+      share->any = 1;
+    }
+    base += total;
+  }
+}
+
+// ---- the kernel -------------------------------------------------------------------------
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a) {
+  constexpr int D = C::D, NS = C::NS;
+  using Geo = typename C::Geo;
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  uint8_t* smem = tc::align1024(smem_dyn);
+  int* nan_s = reinterpret_cast<int*>(smem + C::NAN_OFF);  // [NANS][8 warps][D] first key
+  TileConst* const_s = reinterpret_cast<TileConst*>(smem + C::CONST_OFF);
+  Seg* seg_s = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::ML_OFF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* full = bars;              // [NS] operands of a tile
+  uint64_t* empty = full + NS;
+  uint64_t* s_full = empty + NS;      // [2] scores of a warpgroup
+  uint64_t* p_full = s_full + 2;      // [2] its weights
+  uint64_t* pv_done = p_full + 2;     // [2] its products
+  uint64_t* q_full = pv_done + 2;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* o_empty = q_empty + 1;
+  uint64_t* ml_full = o_empty + 1;    // the second warpgroup's sums (small items)
+  uint64_t* ml_empty = ml_full + 1;
+  uint64_t* seg_full = ml_empty + 1;  // [kSegs]
+  uint64_t* seg_empty = seg_full + kSegs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegs);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* nan_any = tmem_slot + 2;  // [NANS][8 warps] some column of an item is NaN
+  Share* share = reinterpret_cast<Share*>(ml_s);           // (before anything else is there)
+  int64_t* scan_s = reinterpret_cast<int64_t*>(const_s);
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(full + i, i % 2 ? 4 : 5);
+      tc::mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(s_full + i, 1);
+      tc::mbar_init(p_full + i, 4);
+      tc::mbar_init(pv_done + i, 1);
+    }
+    tc::mbar_init(q_full, 8);
+    tc::mbar_init(q_empty, 1);
+    tc::mbar_init(o_empty, 8);
+    tc::mbar_init(ml_full, 4);
+    tc::mbar_init(ml_empty, 4);
+    for (int i = 0; i < kSegs; ++i) {
+      tc::mbar_init(seg_full + i, 1);
+      tc::mbar_init(seg_empty + i, 1 + 1 + 8 + 4);
+    }
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < C::NANS * 8 * D; i += kThreads) nan_s[i] = INT32_MAX;
+  if (threadIdx.x < C::NANS * 8) nan_any[threadIdx.x] = 0;
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, C::COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  allow_next();
+  wait_for_earlier();
+  find_share(a, scan_s, share);
+  __syncthreads();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
+  };
+  // The number-th segment, taken out of the ring (each role, in order); false after a failed
+  // wait.
+  auto take = [&](int number, Seg& s) -> bool {
+    if (!wait(seg_full + number % kSegs, (number / kSegs) & 1)) return false;
+    s = seg_s[number % kSegs];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(seg_empty + number % kSegs);
+    return true;
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    const Share sh = *share;
+    __syncwarp();
+    if (warp == 1) {
+      // ---------------- segments ----------------
+      int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;  // of an item begun before; begun here
+      int number = 0;
+      bool ok = true;
+      auto push = [&](const Seg& s) {
+        ok = wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1);
+        if (!ok) return;
+        if (lane == 0) {
+          seg_s[number % kSegs] = s;
+          tc::mbar_arrive(seg_full + number % kSegs);
+        }
+        ++number;
+      };
+      if (sh.any) {
+        int b = sh.b, hk = sh.hk, i = sh.i;
+        int64_t at = sh.at;
+        Seq q = seq_of(a.s, a.n, b);
+#pragma unroll 1
+        while (ok && at < sh.hi) {
+          const Work w(a, q);
+          const int T = w.tiles_of(i), unit = w.unit_of(i);
+          // tiles whose first unit lies in [lo, hi)
+          auto tile_at = [&](int64_t u) -> int {
+            const int64_t x = u - at - kOverhead;
+            return x <= 0 ? 0 : (int)min((int64_t)T, unit == 2 ? (x + 1) >> 1 : x);
+          };
+          const int t0 = tile_at(sh.lo), t1 = tile_at(sh.hi);
+          if (T == 0 ? at >= sh.lo : t0 < t1) {
+            Seg s;
+            s.b = b;
+            s.hk = hk;
+            s.row0 = q.row0 + i * w.per;
+            s.tokens = w.tokens_of(i);
+            s.p0 = w.start + i * w.per;
+            s.end = max(s.p0 + s.tokens, 0);
+            s.t0 = t0;
+            s.t1 = t1;
+            s.flags = (unit == 1 ? kSmall : 0) | (t0 == 0 ? kStarts : 0) | (t1 == T ? kEnds : 0);
+            s.part = -1;
+            if ((s.flags & (kStarts | kEnds)) != (kStarts | kEnds)) {
+              const int4 r = make_int4(s.flags | kStop, s.row0, s.tokens, s.hk);
+              s.part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+              if (t0 == 0) rec1 = r;
+              else rec0 = r;
+            }
+            push(s);
+          }
+          at += w.weight_of(i);
+          if (++i == w.count) {
+            i = 0;
+            if (++hk == a.Hkv) {
+              hk = 0;
+              do {
+                if (++b >= a.s.B) break;
+                q = seq_of(a.s, a.n, b);
+              } while (q.m == 0);
+              if (b >= a.s.B) break;
+            }
+          }
+        }
+      }
+      // (kStop: there is such a part)
+      if (lane == 0) {
+        a.record[2 * blockIdx.x] = rec0;
+        a.record[2 * blockIdx.x + 1] = rec1;
+      }
+      Seg s{};
+      s.flags = kStop;
+      if (ok) push(s);
+    } else if (warp == 2) {
+      // ---------------- scales of the tiles ----------------
+      // Lanes 0 .. 7 take a group each. The page of the tile after next and the scales of
+      // the next one are loaded while this one's are written.
+      struct At {
+        Seg s;
+        int number, t;
+        bool ok;
+      };
+      auto settle = [&](At& c) {  // to the next tile at or after c
+        while (c.ok && !(c.s.flags & kStop) && c.t >= c.s.t1) {
+          ++c.number;
+          c.ok = take(c.number, c.s);
+          c.t = c.s.t0;
+        }
+      };
+      auto live = [&](const At& c) { return c.ok && !(c.s.flags & kStop); };
+      auto next = [&](At c) {
+        if (live(c)) {
+          ++c.t;
+          settle(c);
+        }
+        return c;
+      };
+      auto page_of = [&](const At& c) -> int {
+        const int key = c.t * 128 + (lane & 7) * 16;
+        if (!live(c) || key >= c.s.end) return -1;
+        return ld_after(a.s.table + (size_t)c.s.b * a.s.columns + (key >> a.shift));
+      };
+      auto scales_of = [&](const At& c, int page) -> float2 {
+        if (page < 0 || page >= a.s.N) return make_float2(0.0f, 0.0f);
+        const size_t at = (size_t)page * a.Hkv + c.s.hk;
+        return make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
+      };
+      const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
+      At c0;
+      c0.number = 0;
+      c0.ok = take(0, c0.s);
+      c0.t = c0.s.t0;
+      settle(c0);
+      At c1 = next(c0);
+      int page0 = page_of(c0), page1 = page_of(c1);
+      float2 sc0 = scales_of(c0, page0);
+      int tile = 0;
+      float ref = 0.0f;
+      bool fresh = true;  // the segment's first tile, whose largest is the reference
+#pragma unroll 1
+      while (live(c0)) {
+        const At c2 = next(c1);
+        const int page2 = page_of(c2);
+        const float2 sc1 = scales_of(c1, page1);
+        const bool in = page0 >= 0 && page0 < a.s.N;
+        if (page0 != -1 && !in && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+        const bool k_ok = sc0.x > 0.0f && sc0.x <= att::kLargest;
+        const bool v_ok = sc0.y > 0.0f && sc0.y <= att::kLargest;
+        if (in && !(k_ok && v_ok) && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
+        if (fresh) {
+          float top = in && v_ok ? sc0.y : 0.0f;
+#pragma unroll
+          for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          ref = top > 0.0f ? top : 1.0f;
+          fresh = false;
+        }
+        const float nan = __int_as_float(0x7fc00000);
+        float2 group = make_float2(0.0f, 0.0f);
+        if (in) {
+          group.x = k_ok ? fmaxf(c_scale * sc0.x, 1.17549435e-38f) : nan;
+          group.y = v_ok ? fminf(fmaxf(log2f(sc0.y / ref), -100.0f), 100.0f) : nan;
+        }
+        const uint32_t absent = ~__ballot_sync(0xffffffffu, in) & 0xFFu;
+        const int seq = 2 * tile, slot = seq % NS;
+        if (!wait(empty + slot, ((seq / NS) & 1) ^ 1)) break;
+        TileConst* out = const_s + tile % kConsts;
+        if (lane < 8) out->group[lane] = group;
+        if (lane == 0) {
+          out->ref = ref;
+          out->absent = absent;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(full + slot);
+        ++tile;
+        if (c1.number != c0.number) fresh = true;
+        c0 = c1;
+        c1 = c2;
+        page0 = page1;
+        page1 = page2;
+        sc0 = sc1;
+      }
+      // (the last segments, which had no tile after them, need no release)
+    } else if (warp == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
+      constexpr uint32_t LBO_K = 1u << 16, LBO_MN = (16384u >> 4) << 16;
+      constexpr uint32_t ID_S = f16_desc(128), ID_O = f16_desc(D) | (1u << 16);
+      const uint32_t ring_lo = (tc::smem_u32(smem) >> 4) & 0x3FFFu;
+      const uint32_t q_lo = (tc::smem_u32(smem + C::Q_OFF) >> 4) & 0x3FFFu;
+      auto desc = [&](uint32_t lo) { return tc::desc_from_words(lo, D_HI); };
+      int base = 0;            // slots of the segments before
+      uint32_t done[2] = {0, 0};  // tiles of each warpgroup whose products were issued
+      int segs = 0;            // segments with tiles so far
+      auto wait_slot = [&](int seq) { return wait(full + seq % NS, (seq / NS) & 1); };
+      // b1, b2: other barriers that these products complete. What the softmax waits for is
+      // committed last: nothing arrives after a CTA's end.
+      auto scores = [&](int w, int seq, int qb, uint64_t* b1, uint64_t* b2) {
+        tc::fence_after_sync();
+        const uint32_t ad = (q_lo + qb * (C::SLOT >> 4)) | LBO_K;
+        const uint32_t bd = (ring_lo + (seq % NS) * (C::SLOT >> 4)) | LBO_K;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < C::RB / 32; ++j)
+            mma_ss(tmem + C::S_COL + w * 128, desc(ad + (Geo::step_offset(j, 128) >> 4)),
+                   desc(bd + (Geo::step_offset(j, 128) >> 4)), ID_S, j > 0 ? 1u : 0u);
+          if (b1) tc::mma_commit(b1);
+          if (b2) tc::mma_commit(b2);
+          tc::mma_commit(s_full + w);
+        }
+        __syncwarp();
+      };
+      auto products = [&](int w, int seq, bool add, uint64_t* b1) {
+        tc::fence_after_sync();
+        const uint32_t bd = (ring_lo + (seq % NS) * (C::SLOT >> 4)) | LBO_MN;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)  // 16 keys
+            mma_ts(tmem + C::O_COL + w * D, tmem + C::S_COL + w * 128 + j * 8,
+                   desc(bd + (j * 2048 >> 4)), ID_O, add || j > 0 ? 1u : 0u);
+          if (b1) tc::mma_commit(b1);
+          tc::mma_commit(pv_done + w);
+        }
+        __syncwarp();
+        ++done[w];
+      };
+      Seg s;
+#pragma unroll 1
+      for (int number = 0; take(number, s) && !(s.flags & kStop); ++number) {
+        const int T = s.t1 - s.t0;
+        if (T == 0) continue;
+        bool ok = wait(q_full, segs & 1);
+        if (s.flags & kSmall) {
+#pragma unroll 1
+          for (int t = 0; ok && t < 2 && t < T; ++t) {
+            const int seq = base + 2 * t;
+            if (!(ok = wait_slot(seq))) break;
+            scores(t, seq, 0, empty + seq % NS, t == T - 1 ? q_empty : nullptr);
+          }
+#pragma unroll 1
+          for (int t = 0; ok && t < T; ++t) {
+            const int w = t & 1, seq = base + 2 * t + 1;
+            ok = wait(p_full + w, done[w] & 1);
+            if (ok && t == 0) ok = wait(o_empty, (segs & 1) ^ 1);
+            ok = ok && wait_slot(seq);
+            if (!ok) break;
+            products(w, seq, t >= 2, empty + seq % NS);
+            if (t + 2 < T) {
+              const int k = base + 2 * t + 4;
+              if (!(ok = wait_slot(k))) break;
+              scores(w, k, 0, empty + k % NS, t + 3 == T ? q_empty : nullptr);
+            }
+          }
+        } else {
+          if (ok && (ok = wait_slot(base))) {
+            scores(0, base, 0, nullptr, nullptr);
+            scores(1, base, 1, empty + base % NS, T == 1 ? q_empty : nullptr);
+          }
+#pragma unroll 1
+          for (int t = 0; ok && t < T; ++t) {
+            const int seq = base + 2 * t + 1, k = seq + 1;
+#pragma unroll 1
+            for (int w = 0; w < 2; ++w) {
+              ok = wait(p_full + w, done[w] & 1);
+              if (ok && t == 0 && w == 0) ok = wait(o_empty, (segs & 1) ^ 1);
+              if (w == 0) ok = ok && wait_slot(seq);
+              if (!ok) break;
+              products(w, seq, t > 0, w ? empty + seq % NS : nullptr);
+              if (t + 1 < T) {
+                if (w == 0 && !(ok = wait_slot(k))) break;
+                scores(w, k, w, w ? empty + k % NS : nullptr,
+                       w && t + 2 == T ? q_empty : nullptr);
+              }
+            }
+          }
+        }
+        if (!ok) break;
+        base += 2 * T;
+        ++segs;
+      }
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWide));
+    // ---------------- codes to f16 ----------------
+    // A warp takes 32 rows of a tile, two groups, CPR lanes a row.
+    constexpr int CPR = D / 16, RPP = 32 / CPR, PASSES = 32 / RPP;
+    const int ww = warp - 12, c = lane % CPR, rl = lane / CPR;
+    const uint32_t row_bytes = (uint32_t)(a.Hkv * D);
+    struct Codes {
+      uint4 x[PASSES];
+    };
+    struct At {
+      Seg s;
+      int number, t;
+      bool ok;
+    };
+    auto settle = [&](At& p) {
+      while (p.ok && !(p.s.flags & kStop) && p.t >= p.s.t1) {
+        ++p.number;
+        p.ok = take(p.number, p.s);
+        p.t = p.s.t0;
+      }
+    };
+    auto live = [&](const At& p) { return p.ok && !(p.s.flags & kStop); };
+    // pages of the warp's two groups (-1: not there)
+    auto pages_at = [&](const At& p, int (&page)[2]) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int key = p.t * 128 + ww * 32 + g * 16;
+        page[g] = -1;
+        if (live(p) && key < p.s.end)
+          page[g] = ld_after(a.s.table + (size_t)p.s.b * a.s.columns + (key >> a.shift));
+      }
+    };
+    auto load = [&](const uint8_t* from, const At& p, const int (&page)[2], Codes& r) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int in = (p.t * 128 + ww * 32 + g * 16) & (a.s.P - 1);
+        const bool there = page[g] >= 0 && page[g] < a.s.N;
+        const uint8_t* src = from + ((size_t)(uint32_t)max(page[g], 0) << a.shift) * row_bytes +
+                             (size_t)(uint32_t)(in + rl) * row_bytes + (uint32_t)(p.s.hk * D + c * 16);
+#pragma unroll
+        for (int u = 0; u < PASSES / 2; ++u) {
+          r.x[g * (PASSES / 2) + u] = make_uint4(0, 0, 0, 0);
+          if (there)
+            r.x[g * (PASSES / 2) + u] =
+                ld_after(reinterpret_cast<const uint4*>(src + (size_t)(u * RPP) * row_bytes));
+        }
+      }
+    };
+    // Two 16-byte chunks of f16 for 16 codes. Lanes of the second 128-byte line of a row
+    // write theirs in the other order: eight lanes at a time then meet eight banks.
+    const int flip = (2 * c) >> 3 & 1;
+    uint32_t place[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      place[e] = tc::smem_u32(smem) + Geo::chunk_offset(ww * 32 + rl, 2 * c + (e ^ flip), 128);
+    // (rows RPP apart: the swizzle repeats every 8 rows)
+    auto spread = [&](int slot, const Codes& r) {
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u) {
+        const uint32_t w[4] = {r.x[u].x, r.x[u].y, r.x[u].z, r.x[u].w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // rows u * RPP on: 8-row groups are 1024 bytes apart, and a half of one flips the
+          // chunk's third bit
+          const uint32_t at = (RPP == 8 ? place[e] + u * 1024
+                                        : (place[e] + (u / 2) * 1024 + (u % 2) * 512) ^
+                                              ((u % 2) * 64u)) +
+                              slot * C::SLOT;
+          const int h = e ^ flip;
+          const uint2 lo = widen(h ? w[2] : w[0]), hi = widen(h ? w[3] : w[1]);
+          att::st_shared16(at, make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full + slot);
+    };
+    At cur;
+    cur.number = 0;
+    cur.ok = take(0, cur.s);
+    cur.t = cur.s.t0;
+    settle(cur);
+    int page[2], seq = 0, segs = 0;
+    Codes kc, vc;
+    pages_at(cur, page);
+    load(a.k, cur, page, kc);
+    load(a.v, cur, page, vc);
+#pragma unroll 1
+    while (live(cur)) {
+      At nxt = cur;
+      ++nxt.t;
+      settle(nxt);
+      int page1[2];
+      pages_at(nxt, page1);
+      if (!wait(empty + seq % NS, ((seq / NS) & 1) ^ 1)) break;
+      spread(seq % NS, kc);
+      load(a.k, nxt, page1, kc);
+      ++seq;
+      if (!wait(empty + seq % NS, ((seq / NS) & 1) ^ 1)) break;
+      if (cur.t * 128 + 127 > cur.s.p0) {
+        // keys that some row does not see
+#pragma unroll
+        for (int u = 0; u < PASSES; ++u) {
+          uint32_t w[4] = {vc.x[u].x, vc.x[u].y, vc.x[u].z, vc.x[u].w};
+          if (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3])) {
+            const int key = cur.t * 128 + ww * 32 + u * RPP + rl;
+            int* at = nan_s + (segs % C::NANS) * 8 * D + c * 16;
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t byte = 0xFFu << (e % 4 * 8);
+              uint32_t x = e < 4 ? w[0] : e < 8 ? w[1] : e < 12 ? w[2] : w[3];
+              if (!(nan_codes(x) & byte)) continue;
+              x &= ~byte;
+              if (e < 4) w[0] = x;
+              else if (e < 8) w[1] = x;
+              else if (e < 12) w[2] = x;
+              else w[3] = x;
+              if (key < cur.s.end) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {  // a softmax warp's own, which it clears
+                  atomicMin(at + i * D + e, key);
+                  nan_any[segs % C::NANS * 8 + i] = 1;
+                }
+              }
+            }
+            vc.x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      spread(seq % NS, vc);
+      load(a.v, nxt, page1, vc);
+      ++seq;
+      if (nxt.number != cur.number) ++segs;
+      cur = nxt;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ---------------- softmax: TMEM lane = row ----------------
+    const int w = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + C::S_COL + w * 128;
+    const uint32_t o_addr = tmem + lane_off + C::O_COL + w * D;
+    const int my_token = row / a.G, my_head = row % a.G, Hq = a.Hkv * a.G;
+    const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
+    uint32_t cnt = 0;   // tiles of this warpgroup so far
+    int tile0 = 0;      // tiles of the segments before
+    int segs = 0, smalls = 0;
+    Seg s;
+#pragma unroll 1
+    for (int number = 0; take(number, s) && !(s.flags & kStop); ++number) {
+      const bool small = s.flags & kSmall;
+      const int T = s.t1 - s.t0;
+      const int token = my_token + (small ? 0 : w * a.tokens);
+      const bool there = my_token < a.tokens && token < s.tokens;
+      const int p = there ? s.p0 + token : -1;  // the row's position
+      const size_t q_at = (size_t)(s.row0 + token);
+      const int head = s.hk * a.G + my_head;
+      if (T == 0) {
+        if (there && w == 0 || there && !small) {
+          uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
+        }
+        continue;
+      }
+      // the row's query: a power of two is taken out, so that the largest is 2^14 to 2^15
+      float qs;
+      {
+        uint4 x[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + q_at * a.q_row + (size_t)head * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = there ? ld_after(src + i) : make_uint4(0, 0, 0, 0);
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            most = max(most, max((y[e] << 16) & 0x7FFFFFFFu, y[e] & 0x7FFF0000u));
+        }
+        const int ex = max((int)(most >> 23) - 127 - 14, -110);
+        qs = __int_as_float((ex + 127) << 23);
+        const float inv = sign * __int_as_float((127 - ex) << 23);
+        if (!wait(q_empty, (segs & 1) ^ 1)) break;
+        if (!small || w == 0) {
+          uint8_t* dst = smem + C::Q_OFF + w * C::SLOT;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              h[e] = pack_f16(__uint_as_float(y[e] << 16) * inv,
+                              __uint_as_float(y[e] & 0xFFFF0000u) * inv);
+            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(row, i, 128)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(q_full);
+      }
+      const bool warp_there = __any_sync(0xffffffffu, there);
+      const int p_first = s.p0 + (small ? 0 : w * a.tokens);  // the least position
+      float nm = -INFINITY, l = 0.0f, ref = 1.0f;
+      const int step = small ? 2 : 1;
+      bool ok = true;
+      int mine = 0;  // tiles of this segment so far
+#pragma unroll 1
+      for (int t = s.t0 + (small ? w : 0); t < s.t1; t += step, ++mine, ++cnt) {
+        const TileConst* tile = const_s + (tile0 + t - s.t0) % kConsts;
+        if (!(ok = wait(s_full + w, cnt & 1))) break;
+        tc::fence_after_sync();
+        if (warp_there) {
+          float v[2][64];
+          tc::tmem_ld64(s_addr, v[0]);
+          tc::tmem_ld64(s_addr + 64, v[1]);
+          tc::tmem_wait_ld(v[0]);
+          tc::tmem_wait_ld(v[1]);
+          ref = tile->ref;
+          const uint32_t absent = tile->absent;
+          // (uniform in the warpgroup) some key is not seen by some row
+          const bool masked = absent != 0 || t * 128 + 127 > p_first;
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (t * 128 + j > p || (absent >> (j / 16) & 1)) v[j / 64][j % 64] = -INFINITY;
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float2 k = tile->group[g];
+            const float* x = v[g / 4] + g % 4 * 16;
+            float most = max3(x[0], x[1], x[2]);
+#pragma unroll
+            for (int j = 3; j < 15; j += 2) most = max3(most, x[j], x[j + 1]);
+            most = fmaxf(most, x[15]);
+            top = fmaxf(top, __fadd_rn(__fmul_rn(most, k.x * qs), k.y));
+          }
+          const bool raise = top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float to = raise ? 4.0f - ceilf(fmaxf(top, -att::kLargest)) : nm;
+            const float f = nm == -INFINITY ? 1.0f : ex2(to - nm);
+            l *= f;
+            if (mine > 0) {
+              if (!(ok = wait(pv_done + w, (cnt - 1) & 1))) break;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 8) {
+                float o[8];
+                att::tmem_load(o_addr + i, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= f;
+                att::tmem_store8(o_addr + i, o);
+              }
+              tc::tmem_wait_st();
+            }
+            nm = to;
+          }
+          // Weights. Far from 0 the products are rounded as the maximum was, a masked weight
+          // is 0 whatever its group's scale is, and a row without a score so far (nm = -inf)
+          // has none.
+          const bool slow = __any_sync(0xffffffffu, fabsf(nm) > 1048576.0f) || masked;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int g = 2 * i + h;
+              const float2 k = tile->group[g];
+              const float cc = k.x * qs, kb = k.y + nm;
+              float s0 = 0.0f, s1 = 0.0f;
+              if (!slow) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  float x0 = v[i / 2][i % 2 * 32 + 16 * h + j], x1 = v[i / 2][i % 2 * 32 + 16 * h + j + 1];
+                  fma2(x0, x1, cc, kb, kb);
+                  x0 = ex2(x0);
+                  x1 = ex2(x1);
+                  add2(s0, s1, x0, x1);
+                  y[8 * h + j / 2] = pack_f16(x0, x1);
+                }
+                l += (s0 + s1) * ex2(nm - kb);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  float x0 = v[i / 2][i % 2 * 32 + 16 * h + j], x1 = v[i / 2][i % 2 * 32 + 16 * h + j + 1];
+                  const bool off0 = t * 128 + 16 * g + j > p || (absent >> g & 1);
+                  const bool off1 = t * 128 + 16 * g + j + 1 > p || (absent >> g & 1);
+                  x0 = __fadd_rn(__fadd_rn(__fmul_rn(x0, cc), k.y), nm);
+                  x1 = __fadd_rn(__fadd_rn(__fmul_rn(x1, cc), k.y), nm);
+                  x0 = off0 ? 0.0f : ex2(x0);
+                  x1 = off1 ? 0.0f : ex2(x1);
+                  s0 += x0;
+                  s1 += x1;
+                  y[8 * h + j / 2] = pack_f16(x0, x1);
+                }
+                if (s0 + s1 != 0.0f) l += (s0 + s1) * ex2(-k.y);
+              }
+            }
+            tmem_store16(s_addr + 16 * i, y);
+          }
+          tc::tmem_wait_st();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + w);
+      }
+      if (!ok) break;
+      tile0 += T;
+      // ---- the result ----
+      if (mine > 0) {
+        if (!wait(pv_done + w, (cnt - 1) & 1)) break;
+        tc::fence_after_sync();
+      }
+      float l2 = 0.0f, nm2 = -INFINITY;  // the other warpgroup's
+      const bool other = small && T > 1;
+      if (small) {
+        if (w == 1) {
+          if (!wait(ml_empty, (smalls & 1) ^ 1)) break;
+          ml_s[row] = make_float2(l, nm);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(ml_full);
+        } else {
+          if (!wait(ml_full, smalls & 1)) break;
+          tc::fence_after_sync();
+          const float2 x = ml_s[row];
+          l2 = x.x;
+          nm2 = x.y;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(ml_empty);
+        }
+        ++smalls;
+      }
+      int* nans = nan_s + ((segs % C::NANS) * 8 + warp - 4) * D;
+      uint32_t* any = nan_any + segs % C::NANS * 8 + warp - 4;
+      const bool nan_here = *reinterpret_cast<volatile uint32_t*>(any) != 0;
+      if (warp_there && !(small && w == 1)) {
+        // one reference for both; -inf: no row so far
+        const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
+        float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
+        float f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
+        const float sum = l * f1 + l2 * f2;
+        const bool part = s.part >= 0;
+        const int r = w * 128 + row;
+        float norm = ref;
+        if (!part) norm = sum == 0.0f ? 0.0f : ref / sum;
+        f1 *= norm;
+        f2 *= norm;
+        const bool none = !part && sum == 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 16) {
+          float o[16];
+          att::tmem_load(o_addr + i, o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
+          if (other) {
+            float x[16];
+            att::tmem_load(o_addr + D + i, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
+          }
+          if (nan_here) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
+          }
+          if (there && part) {
+            float4* y = reinterpret_cast<float4*>(a.part + ((size_t)s.part * a.rows + r) * D + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (there) {
+            uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D + i);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              y[e] = make_uint4(att::pack_bf16(o[8 * e], o[8 * e + 1]),
+                                att::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                att::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                                att::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          }
+          __syncwarp();
+        }
+        if (there) {
+          const float m = both == INFINITY ? -INFINITY : both;
+          if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, m);
+          else if (a.lse) a.lse[q_at * Hq + head] = none ? -INFINITY : (log2f(sum) - m) * att::kLn2;
+        }
+      }
+      if (nan_here) {
+        __syncwarp();
+        for (int i = lane; i < D; i += 32) nans[i] = INT32_MAX;
+        if (lane == 0) *any = 0;
+      }
+      // Eight arrivals: of a small item all are the first warpgroup's, which reads both
+      // results (the second may have no tile and be an item ahead).
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && !(small && w == 1)) {
+        tc::mbar_arrive(o_empty);
+        if (small) tc::mbar_arrive(o_empty);
+      }
+      ++segs;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+// ---- joining the parts ------------------------------------------------------------------
+
+constexpr int kJoinThreads = 256;
+
+// Parts of an item: number 2c + 1 of the CTA c where it starts, then 2c' + 0 of the CTAs after
+// it, up to the one that ends it (CTAs between may hold none of it).
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a, int ctas) {
+  allow_next();
+  wait_for_earlier();
+  constexpr int WARPS = kJoinThreads / 32, V = D / 32;
+  __shared__ int4 rec[2 * kMaxCtas];
+  __shared__ float4 acc_s[WARPS][32];
+  __shared__ float2 ml_s[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool any = false;
+  for (int i = tid; i < 2 * ctas; i += kJoinThreads) {
+    rec[i] = ld_after(a.record + i);
+    any |= (i & 1) && (rec[i].x & kStop);
+  }
+  if (!__syncthreads_or(any)) return;
+  const int Hq = a.Hkv * a.G;
+  int64_t unit = 0;  // rows (or blocks of rows) of the items so far
+#pragma unroll 1
+  for (int c = 0; c < ctas; ++c) {
+    const int4 first = rec[2 * c + 1];
+    if (!(first.x & kStop)) continue;
+    // the CTAs after it that hold parts
+    int last = c + 1, parts = 1;
+    while (last < ctas) {
+      const int4 r = rec[2 * last];
+      if (r.x & kStop) {
+        ++parts;
+        if (r.x & kEnds) break;
+      }
+      ++last;
+    }
+    const bool wide = parts > 8;  // a block a row, its warps sharing the parts; else a warp a row
+    const bool small = first.x & kSmall;
+    const int rows = first.z * a.G;
+    const int64_t units = wide ? rows : (rows + WARPS - 1) / WARPS;
+    // this block's units of the item: unit + u = blockIdx.x modulo the grid
+    int64_t u = (int64_t)blockIdx.x - unit % gridDim.x;
+    if (u < 0) u += gridDim.x;
+    unit += units;
+#pragma unroll 1
+    for (; u < units; u += gridDim.x) {
+      const int x = wide ? (int)u : (int)u * WARPS + warp;  // row of the item
+      const bool on = x < rows;
+      const int token = x / a.G, head = x % a.G;
+      const int block = small || token < a.tokens ? 0 : 1;
+      const int r = block * 128 + (token - block * a.tokens) * a.G + head;
+      float top = INFINITY, sum = 0.0f, o[V];  // top: the least -m
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = 0.0f;
+      if (on) {
+        // the parts' references first, lanes taking parts
+        for (int i = c + lane; i <= last && i < ctas; i += 32) {
+          const int part = i == c ? 2 * c + 1 : 2 * i;
+          if (!(rec[part].x & kStop)) continue;
+          const float2 m = ld_after(a.ml + (size_t)part * a.rows + r);
+          if (m.y > -INFINITY) top = fminf(top, m.y);
+        }
+#pragma unroll
+        for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+#pragma unroll 4
+        for (int i = c + (wide ? warp : 0); i <= last && i < ctas; i += wide ? WARPS : 1) {
+          const int part = i == c ? 2 * c + 1 : 2 * i;
+          if (!(rec[part].x & kStop)) continue;
+          const float2 m = ld_after(a.ml + (size_t)part * a.rows + r);
+          const float* y = a.part + ((size_t)part * a.rows + r) * D + lane * V;
+          float z[V];
+          if constexpr (V == 4) {
+            const float4 t = ld_after(reinterpret_cast<const float4*>(y));
+            z[0] = t.x, z[1] = t.y, z[2] = t.z, z[3] = t.w;
+          } else {
+            const float2 t = ld_after(reinterpret_cast<const float2*>(y));
+            z[0] = t.x, z[1] = t.y;
+          }
+          // a part without rows counts nothing, but its NaN columns do
+          const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
+          sum += m.x * f;
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
+        }
+      }
+      if (wide) {
+        __syncthreads();
+        float4 t = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
+        acc_s[warp][lane] = t;
+        if (lane == 0) ml_s[warp] = make_float2(sum, 0.0f);
+        __syncthreads();
+        if (warp) continue;
+        sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) {
+          t = acc_s[i][lane];
+          o[0] += t.x;
+          o[1] += t.y;
+          if constexpr (V > 2) {
+            o[2] += t.z;
+            o[3] += t.w;
+          }
+          sum += ml_s[i].x;
+        }
+      }
+      if (!on) continue;
+      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= norm;
+      const size_t at = (size_t)(first.y + token) * Hq + first.w * a.G + head;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(a.out + at * D + lane * V) =
+            make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));
+      else
+        *reinterpret_cast<uint32_t*>(a.out + at * D + lane * V) = att::pack_bf16(o[0], o[1]);
+      if (a.lse && lane == 0)
+        a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
+    }
+  }
+}
+
+template <class C>
+cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) {
+  auto kernel = k_attend_pages<C>;
+  static unsigned long long opted_in = 0;
+  static int regs_ok = 0;
+  // setmaxnreg waits for registers that the launch must have brought
+  if (!__atomic_load_n(&regs_ok, __ATOMIC_RELAXED)) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+    __atomic_store_n(&regs_ok, 1, __ATOMIC_RELAXED);
+  }
+  const cudaError_t e =
+      att::launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
+        return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a);
+      });
+  if (e != cudaSuccess) return e;
+  return launch_early(k_join_parts<C::D>, 2u * (unsigned)ctas, kJoinThreads, 0, st, 1, a, ctas);
+}
+
+}  // namespace pages
+}  // namespace hytopk

@@ -593,7 +593,7 @@ PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
     if (!given(a[10])) lse = empty({r.n, r.H}, at::kFloat, dev);
     place.result(out, given(a[9]));
     place.result(lse, given(a[10]));
-    const size_t bytes = p_attend_pages_workspace_size((int)r.H, k.H, (int)r.d);
+    const size_t bytes = p_attend_pages_workspace_size((int)r.n, (int)r.H, k.H, (int)r.d);
     const at::Tensor workspace = empty({(int64_t)bytes}, at::kByte, dev);
     call("hytopk_attend_pages", [&] {
       return p_attend_pages(q.data_ptr(), r.row, k.codes, k.scale, v.codes, v.scale, &s, (int)r.n,

@@ -591,7 +591,7 @@ typedef struct {
  *   multiple of 8.
  *   workspace: hytopk_attend_pages_workspace_size bytes (parts of contexts that several
  *   multiprocessors share), 256-byte aligned; it holds nothing between calls. */
-HYTOPK_API size_t hytopk_attend_pages_workspace_size(int Hq, int Hkv, int d);
+HYTOPK_API size_t hytopk_attend_pages_workspace_size(int n, int Hq, int Hkv, int d);
 HYTOPK_API hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const void* k_pages,
                                              const float* k_scale, const void* v_pages,
                                              const float* v_scale, const hytopk_paged* paged,
