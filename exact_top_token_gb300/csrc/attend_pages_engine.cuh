@@ -56,8 +56,8 @@ constexpr int kOverhead = 2;   // of an item, in the units below
 constexpr int kSegs = 8;       // ring of segments
 constexpr int kConsts = 8;     // ring of the tiles' scales
 constexpr int kThreads = 512;
-// Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 176 + 96) = 65536.
-constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 176, kRegsWide = 96;
+// Registers: 128 a thread at launch, then by role: 128 (48 + 2 * 168 + 128) = 65536.
+constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsSoft = 168, kRegsWide = 128;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
 
 // A segment: tiles [t0, t1) of an item.
@@ -89,7 +89,8 @@ struct PCfg {
   static constexpr int CONST_OFF = NAN_OFF + NANS * 8 * D * 4;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
-  static constexpr int BAR_OFF = (ML_OFF + 128 * 8 + 15) / 16 * 16;
+  static constexpr int QS_OFF = ML_OFF + 128 * 8;
+  static constexpr int BAR_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;
   static constexpr int SMEM = BAR_OFF + 768 + 1024;
   static constexpr int S_COL = 0, O_COL = 256, COLS = 512;
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -127,11 +128,7 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[
       : "memory");
 }
 
-// D[tmem] (+)= A . B, f16: A and B in shared memory, or A in tensor memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t add) {
-  tc::mma<0>(d, a, b, idesc, add);
-}
+// D[tmem] (+)= A[tmem] * B[smem], f16
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t add) {
   asm volatile(
@@ -188,7 +185,7 @@ struct Work {
     return kOverhead + (int64_t)unit_of(i) * tiles_of(i);
   }
   // weight of the items before i
-  __device__ int64_t before(int i) const {
+  __device__ __noinline__ int64_t before(int i) const {
     if (i <= 0) return 0;
     if (i == count) return before(i - 1) + weight_of(i - 1);
     // whole items: floor((start + (j + 1) per - 1) / 128) + 1 tiles from the first that has any
@@ -298,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
   TileConst* const_s = reinterpret_cast<TileConst*>(smem + C::CONST_OFF);
   Seg* seg_s = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
   float2* ml_s = reinterpret_cast<float2*>(smem + C::ML_OFF);
+  float* qs_s = reinterpret_cast<float*>(smem + C::QS_OFF);  // [2][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* full = bars;              // [NS] operands of a tile
   uint64_t* empty = full + NS;
@@ -533,100 +531,137 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
       // (the last segments, which had no tile after them, need no release)
     } else if (warp == 0) {
       // ---------------- MMA issuer ----------------
+      // The whole warp waits and keeps the state, all of it in uniform registers (numbers
+      // of a segment come through a shuffle, so that the compiler knows): descriptors that
+      // pass through vector registers cost 100 cycles a product. One elected lane issues.
       constexpr uint32_t D_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, SW128
       constexpr uint32_t LBO_K = 1u << 16, LBO_MN = (16384u >> 4) << 16;
       constexpr uint32_t ID_S = f16_desc(128), ID_O = f16_desc(D) | (1u << 16);
       const uint32_t ring_lo = (tc::smem_u32(smem) >> 4) & 0x3FFFu;
       const uint32_t q_lo = (tc::smem_u32(smem + C::Q_OFF) >> 4) & 0x3FFFu;
       auto desc = [&](uint32_t lo) { return tc::desc_from_words(lo, D_HI); };
-      int base = 0;            // slots of the segments before
-      uint32_t done[2] = {0, 0};  // tiles of each warpgroup whose products were issued
-      int segs = 0;            // segments with tiles so far
-      auto wait_slot = [&](int seq) { return wait(full + seq % NS, (seq / NS) & 1); };
-      // b1, b2: other barriers that these products complete. What the softmax waits for is
-      // committed last: nothing arrives after a CTA's end.
-      auto scores = [&](int w, int seq, int qb, uint64_t* b1, uint64_t* b2) {
+      // Slots of the next K and V, whose tiles are taken in the order of the ring.
+      struct At {
+        int slot;
+        uint32_t phase;
+      };
+      At k{0, 0}, v{1, 0};
+      auto step = [&](At& x) {
+        x.slot += 2;
+        if (x.slot >= NS) {
+          x.slot -= NS;
+          x.phase ^= 1u;
+        }
+      };
+      auto landed = [&](const At& x) {
+        const bool ok = wait(full + x.slot, x.phase);
+        tc::fence_proxy_async_smem();  // of all that was stored into the ring
+        return ok;
+      };
+      // Scores of a warpgroup, of query block qb; `release`: the tile's slot is free after
+      // them, `last`: so are the queries. What the softmax waits for is committed last:
+      // nothing arrives after a CTA's end.
+      auto scores = [&](auto wg, auto qb, bool release, bool last) {
+        constexpr int W = decltype(wg)::value, Q = decltype(qb)::value;
         tc::fence_after_sync();
-        const uint32_t ad = (q_lo + qb * (C::SLOT >> 4)) | LBO_K;
-        const uint32_t bd = (ring_lo + (seq % NS) * (C::SLOT >> 4)) | LBO_K;
+        const uint32_t ad = (q_lo + Q * (C::SLOT >> 4)) | LBO_K;
+        const uint32_t bd = (ring_lo + k.slot * (C::SLOT >> 4)) | LBO_K;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < C::RB / 32; ++j)
-            mma_ss(tmem + C::S_COL + w * 128, desc(ad + (Geo::step_offset(j, 128) >> 4)),
-                   desc(bd + (Geo::step_offset(j, 128) >> 4)), ID_S, j > 0 ? 1u : 0u);
-          if (b1) tc::mma_commit(b1);
-          if (b2) tc::mma_commit(b2);
-          tc::mma_commit(s_full + w);
+            tc::mma<0>(tmem + C::S_COL + W * 128, desc(ad + (Geo::step_offset(j, 128) >> 4)),
+                       desc(bd + (Geo::step_offset(j, 128) >> 4)), ID_S, j > 0 ? 1u : 0u);
+          if (release) tc::mma_commit(empty + k.slot);
+          if (last) tc::mma_commit(q_empty);
+          tc::mma_commit(s_full + W);
         }
         __syncwarp();
       };
-      auto products = [&](int w, int seq, bool add, uint64_t* b1) {
+      uint32_t phase0 = 0, phase1 = 0;  // of the weights of each warpgroup
+      auto weights = [&](auto wg) {
+        constexpr int W = decltype(wg)::value;
+        uint32_t& phase = W ? phase1 : phase0;
+        const bool ok = wait(p_full + W, phase);
+        phase ^= 1u;
+        return ok;
+      };
+      auto products = [&](auto wg, bool add, bool release) {
+        constexpr int W = decltype(wg)::value;
         tc::fence_after_sync();
-        const uint32_t bd = (ring_lo + (seq % NS) * (C::SLOT >> 4)) | LBO_MN;
+        const uint32_t bd = (ring_lo + v.slot * (C::SLOT >> 4)) | LBO_MN;
+        const uint32_t first = add ? 1u : 0u;
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)  // 16 keys
-            mma_ts(tmem + C::O_COL + w * D, tmem + C::S_COL + w * 128 + j * 8,
-                   desc(bd + (j * 2048 >> 4)), ID_O, add || j > 0 ? 1u : 0u);
-          if (b1) tc::mma_commit(b1);
-          tc::mma_commit(pv_done + w);
+            mma_ts(tmem + C::O_COL + W * D, tmem + C::S_COL + W * 128 + j * 8,
+                   desc(bd + (j * 2048 >> 4)), ID_O, j > 0 ? 1u : first);
+          if (release) tc::mma_commit(empty + v.slot);
+          tc::mma_commit(pv_done + W);
         }
         __syncwarp();
-        ++done[w];
       };
+      constexpr att::Int<0> g0{};
+      constexpr att::Int<1> g1{};
+      uint32_t odd = 0;  // segments with tiles so far, modulo 2
       Seg s;
 #pragma unroll 1
       for (int number = 0; take(number, s) && !(s.flags & kStop); ++number) {
-        const int T = s.t1 - s.t0;
+        const int T = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0);
+        const bool small = __shfl_sync(0xffffffffu, s.flags & kSmall, 0) != 0;
         if (T == 0) continue;
-        bool ok = wait(q_full, segs & 1);
-        if (s.flags & kSmall) {
-#pragma unroll 1
-          for (int t = 0; ok && t < 2 && t < T; ++t) {
-            const int seq = base + 2 * t;
-            if (!(ok = wait_slot(seq))) break;
-            scores(t, seq, 0, empty + seq % NS, t == T - 1 ? q_empty : nullptr);
+        bool ok = wait(q_full, odd) && landed(k);
+        if (!ok) break;
+        if (small) {
+          // tile t is warpgroup t % 2's
+          scores(g0, g0, true, T == 1);
+          step(k);
+          if (T > 1) {
+            if (!landed(k)) break;
+            scores(g1, g0, true, T == 2);
+            step(k);
           }
-#pragma unroll 1
-          for (int t = 0; ok && t < T; ++t) {
-            const int w = t & 1, seq = base + 2 * t + 1;
-            ok = wait(p_full + w, done[w] & 1);
-            if (ok && t == 0) ok = wait(o_empty, (segs & 1) ^ 1);
-            ok = ok && wait_slot(seq);
-            if (!ok) break;
-            products(w, seq, t >= 2, empty + seq % NS);
+          auto tile = [&](auto wg, int t) -> bool {
+            if (!weights(wg) || (t == 0 && !wait(o_empty, odd ^ 1u)) || !landed(v)) return false;
+            products(wg, t >= 2, true);
+            step(v);
             if (t + 2 < T) {
-              const int k = base + 2 * t + 4;
-              if (!(ok = wait_slot(k))) break;
-              scores(w, k, 0, empty + k % NS, t + 3 == T ? q_empty : nullptr);
+              if (!landed(k)) return false;
+              scores(wg, g0, true, t + 3 == T);
+              step(k);
             }
+            return true;
+          };
+#pragma unroll 1
+          for (int t = 0; t < T; t += 2) {
+            if (!(ok = tile(g0, t))) break;
+            if (t + 1 < T && !(ok = tile(g1, t + 1))) break;
           }
         } else {
-          if (ok && (ok = wait_slot(base))) {
-            scores(0, base, 0, nullptr, nullptr);
-            scores(1, base, 1, empty + base % NS, T == 1 ? q_empty : nullptr);
-          }
+          scores(g0, g0, false, false);
+          scores(g1, g1, true, T == 1);
+          step(k);
 #pragma unroll 1
-          for (int t = 0; ok && t < T; ++t) {
-            const int seq = base + 2 * t + 1, k = seq + 1;
-#pragma unroll 1
-            for (int w = 0; w < 2; ++w) {
-              ok = wait(p_full + w, done[w] & 1);
-              if (ok && t == 0 && w == 0) ok = wait(o_empty, (segs & 1) ^ 1);
-              if (w == 0) ok = ok && wait_slot(seq);
-              if (!ok) break;
-              products(w, seq, t > 0, w ? empty + seq % NS : nullptr);
-              if (t + 1 < T) {
-                if (w == 0 && !(ok = wait_slot(k))) break;
-                scores(w, k, w, w ? empty + k % NS : nullptr,
-                       w && t + 2 == T ? q_empty : nullptr);
-              }
+          for (int t = 0; t < T; ++t) {
+            if (!(ok = weights(g0))) break;
+            if (t == 0 && !(ok = wait(o_empty, odd ^ 1u))) break;
+            if (!(ok = landed(v))) break;
+            products(g0, t > 0, false);
+            const bool more = t + 1 < T;
+            if (more) {
+              if (!(ok = landed(k))) break;
+              scores(g0, g0, false, false);
+            }
+            if (!(ok = weights(g1))) break;
+            products(g1, t > 0, true);
+            step(v);
+            if (more) {
+              scores(g1, g1, true, t + 2 == T);
+              step(k);
             }
           }
         }
         if (!ok) break;
-        base += 2 * T;
-        ++segs;
+        odd ^= 1u;
       }
     }
   } else if (warp >= 12) {
@@ -639,42 +674,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
     struct Codes {
       uint4 x[PASSES];
     };
+    // The next tile to load: t of segment `number`, whose numbers these are. Kept small: a
+    // spilled register's load would wait behind the loads of the codes.
     struct At {
+      const int32_t* pages;  // of the sequence
+      uint32_t column;       // of the lane's codes in a row
+      int p0, end, t, t1, number;
+    };
+    auto take_next = [&](At& p) -> bool {  // false: no more
       Seg s;
-      int number, t;
-      bool ok;
+      if (!take(p.number, s) || (s.flags & kStop)) return false;
+      ++p.number;
+      p.pages = a.s.table + (size_t)s.b * a.s.columns;
+      p.column = (uint32_t)(s.hk * D + c * 16);
+      p.p0 = s.p0;
+      p.end = s.end;
+      p.t = s.t0;
+      p.t1 = s.t1;
+      return true;
     };
-    auto settle = [&](At& p) {
-      while (p.ok && !(p.s.flags & kStop) && p.t >= p.s.t1) {
-        ++p.number;
-        p.ok = take(p.number, p.s);
-        p.t = p.s.t0;
-      }
-    };
-    auto live = [&](const At& p) { return p.ok && !(p.s.flags & kStop); };
     // pages of the warp's two groups (-1: not there)
     auto pages_at = [&](const At& p, int (&page)[2]) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int key = p.t * 128 + ww * 32 + g * 16;
         page[g] = -1;
-        if (live(p) && key < p.s.end)
-          page[g] = ld_after(a.s.table + (size_t)p.s.b * a.s.columns + (key >> a.shift));
+        if (key < p.end) page[g] = ld_after(p.pages + (key >> a.shift));
       }
     };
     auto load = [&](const uint8_t* from, const At& p, const int (&page)[2], Codes& r) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int in = (p.t * 128 + ww * 32 + g * 16) & (a.s.P - 1);
-        const bool there = page[g] >= 0 && page[g] < a.s.N;
-        const uint8_t* src = from + ((size_t)(uint32_t)max(page[g], 0) << a.shift) * row_bytes +
-                             (size_t)(uint32_t)(in + rl) * row_bytes + (uint32_t)(p.s.hk * D + c * 16);
+        const uint32_t in = (uint32_t)(p.t * 128 + ww * 32 + g * 16) & (uint32_t)(a.s.P - 1);
+        const bool there = (uint32_t)page[g] < (uint32_t)a.s.N;
+        const uint8_t* src = from + p.column +
+                             (((uint64_t)(uint32_t)max(page[g], 0) << a.shift) + in + rl) * row_bytes;
 #pragma unroll
         for (int u = 0; u < PASSES / 2; ++u) {
           r.x[g * (PASSES / 2) + u] = make_uint4(0, 0, 0, 0);
-          if (there)
-            r.x[g * (PASSES / 2) + u] =
-                ld_after(reinterpret_cast<const uint4*>(src + (size_t)(u * RPP) * row_bytes));
+          if (there) r.x[g * (PASSES / 2) + u] = ld_after(reinterpret_cast<const uint4*>(src));
+          src += RPP * row_bytes;
         }
       }
     };
@@ -703,141 +742,179 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
           att::st_shared16(at, make_uint4(lo.x, lo.y, hi.x, hi.y));
         }
       }
-      tc::fence_proxy_async_smem();
+    };
+    // (the MMA issuer makes it visible to the tensor core: a fence here would wait for the
+    // loads of the next tile)
+    auto publish = [&](int slot) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(full + slot);
     };
-    At cur;
-    cur.number = 0;
-    cur.ok = take(0, cur.s);
-    cur.t = cur.s.t0;
-    settle(cur);
-    int page[2], seq = 0, segs = 0;
+    At at;
+    at.number = 0;
+    auto next_segment = [&]() {
+      bool more = take_next(at);
+      while (more && at.t >= at.t1) more = take_next(at);
+      return more;
+    };
+    bool more = next_segment();
+    int slot = 0, item = 0;  // item: of the NaN columns
+    uint32_t phase = 1;
+    auto step = [&]() {
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
     Codes kc, vc;
-    pages_at(cur, page);
-    load(a.k, cur, page, kc);
-    load(a.v, cur, page, vc);
+    if (more) {
+      int page[2];
+      pages_at(at, page);
+      load(a.k, at, page, kc);
+      load(a.v, at, page, vc);
+    }
 #pragma unroll 1
-    while (live(cur)) {
-      At nxt = cur;
-      ++nxt.t;
-      settle(nxt);
-      int page1[2];
-      pages_at(nxt, page1);
-      if (!wait(empty + seq % NS, ((seq / NS) & 1) ^ 1)) break;
-      spread(seq % NS, kc);
-      load(a.k, nxt, page1, kc);
-      ++seq;
-      if (!wait(empty + seq % NS, ((seq / NS) & 1) ^ 1)) break;
-      if (cur.t * 128 + 127 > cur.s.p0) {
-        // keys that some row does not see
+    while (more) {
+      const int key0 = at.t * 128 + ww * 32 + rl, p0 = at.p0, end = at.end;
+      const bool partly = at.t * 128 + 127 > p0;  // keys that some row does not see
+      const int nans = item;
+      if (++at.t == at.t1) {
+        more = next_segment();
+        item = (item + 1) % C::NANS;
+      }
+      int page[2] = {-1, -1};
+      if (more) pages_at(at, page);
+      if (!wait(empty + slot, phase)) break;
+      spread(slot, kc);
+      publish(slot);
+      // (looked at only here: a test right after its load would wait for it)
+      asm volatile("" : "+r"(page[0]), "+r"(page[1]));
+      if (more) load(a.k, at, page, kc);
+      step();
+      if (!wait(empty + slot, phase)) break;
+      bool odd = false;  // NaN codes where some row does not see the key
+      if (partly) {
+        uint32_t found = 0;
 #pragma unroll
-        for (int u = 0; u < PASSES; ++u) {
-          uint32_t w[4] = {vc.x[u].x, vc.x[u].y, vc.x[u].z, vc.x[u].w};
-          if (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3])) {
-            const int key = cur.t * 128 + ww * 32 + u * RPP + rl;
-            int* at = nan_s + (segs % C::NANS) * 8 * D + c * 16;
+        for (int u = 0; u < PASSES; ++u)
+          found |= nan_codes(vc.x[u].x) | nan_codes(vc.x[u].y) | nan_codes(vc.x[u].z) |
+                   nan_codes(vc.x[u].w);
+        odd = __any_sync(0xffffffffu, found != 0);
+      }
+      spread(slot, vc);
+      if (odd) {
+        // replaced by 0 where they went, and their keys kept by column for the rows that see
+        // them (each softmax warp clears its own)
+        int* first = nan_s + nans * 8 * D + c * 16;
 #pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t byte = 0xFFu << (e % 4 * 8);
-              uint32_t x = e < 4 ? w[0] : e < 8 ? w[1] : e < 12 ? w[2] : w[3];
-              if (!(nan_codes(x) & byte)) continue;
-              x &= ~byte;
-              if (e < 4) w[0] = x;
-              else if (e < 8) w[1] = x;
-              else if (e < 12) w[2] = x;
-              else w[3] = x;
-              if (key < cur.s.end) {
+        for (int u = 0; u < PASSES * 16; ++u) {
+          const int e = u % 16, r = ww * 32 + u / 16 * RPP + rl, key = key0 + u / 16 * RPP;
+          uint16_t* h = reinterpret_cast<uint16_t*>(smem + slot * C::SLOT +
+                                                    Geo::chunk_offset(r, 2 * c + e / 8, 128)) + e % 8;
+          if ((*h & 0x7FFFu) <= 0x7C00u) continue;
+          *h = 0;
+          if (key >= end) continue;
 #pragma unroll 1
-                for (int i = 0; i < 8; ++i) {  // a softmax warp's own, which it clears
-                  atomicMin(at + i * D + e, key);
-                  nan_any[segs % C::NANS * 8 + i] = 1;
-                }
-              }
-            }
-            vc.x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 8; ++i) {
+            atomicMin(first + i * D + e, key);
+            nan_any[nans * 8 + i] = 1;
           }
         }
-        __syncwarp();
       }
-      spread(seq % NS, vc);
-      load(a.v, nxt, page1, vc);
-      ++seq;
-      if (nxt.number != cur.number) ++segs;
-      cur = nxt;
+      publish(slot);
+      if (more) load(a.v, at, page, vc);
+      step();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ---------------- softmax: TMEM lane = row ----------------
+    // The roles share one instruction cache, so only a tile that every row sees whole is
+    // straight code; the others are loops.
     const int w = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + C::S_COL + w * 128;
     const uint32_t o_addr = tmem + lane_off + C::O_COL + w * D;
     const int my_token = row / a.G, my_head = row % a.G, Hq = a.Hkv * a.G;
     const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
-    uint32_t cnt = 0;   // tiles of this warpgroup so far
-    int tile0 = 0;      // tiles of the segments before
-    int segs = 0, smalls = 0;
-    Seg s;
-#pragma unroll 1
-    for (int number = 0; take(number, s) && !(s.flags & kStop); ++number) {
+    // of a segment: this row's token
+    auto token_of = [&](const Seg& s) {
+      return my_token + (s.flags & kSmall ? 0 : w * a.tokens);
+    };
+    auto is_there = [&](const Seg& s) { return my_token < a.tokens && token_of(s) < s.tokens; };
+    uint32_t loaded = 0;  // segments whose queries were taken
+    // The queries of a segment into shared memory, and there to f16; `qs` is what was taken out
+    // of this row's, a power of two, so that the largest is 2^14 to 2^15. They are copied in
+    // whole lines, LPR lanes a row, all at once, and converted by the rows' threads. A small
+    // item has one block of rows, the first warpgroup's, and the second is told `qs`.
+    auto queries = [&](const Seg& s, float& qs) -> bool {
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows at a time
       const bool small = s.flags & kSmall;
-      const int T = s.t1 - s.t0;
-      const int token = my_token + (small ? 0 : w * a.tokens);
-      const bool there = my_token < a.tokens && token < s.tokens;
-      const int p = there ? s.p0 + token : -1;  // the row's position
-      const size_t q_at = (size_t)(s.row0 + token);
-      const int head = s.hk * a.G + my_head;
-      if (T == 0) {
-        if (there && w == 0 || there && !small) {
-          uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
+      if (!wait(q_empty, (loaded & 1) ^ 1)) return false;
+      float* told = qs_s + (loaded & 1) * 128 + row;
+      if (!small || w == 0) {
+        uint8_t* block = smem + C::Q_OFF + w * C::SLOT;
+        const int c = lane % LPR;
+        const int64_t at = (int64_t)(s.row0 + token_of(s)) * a.q_row + (int64_t)(s.hk * a.G + my_head) * D;
+        const bool there = is_there(s);
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int r = i * RPI + lane / LPR;
+          const int64_t from = __shfl_sync(0xffffffffu, at, r);
+          const bool on = __shfl_sync(0xffffffffu, (int)there, r) != 0;
+          att::cp_async16(tc::smem_u32(block) + Geo::chunk_offset(quad * 32 + r, c, 128),
+                          a.q + (on ? from : 0) + c * 8, on);
         }
-        continue;
-      }
-      // the row's query: a power of two is taken out, so that the largest is 2^14 to 2^15
-      float qs;
-      {
-        uint4 x[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + q_at * a.q_row + (size_t)head * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = there ? ld_after(src + i) : make_uint4(0, 0, 0, 0);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
         uint32_t most = 0;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 8
+        for (int i = 0; i < LPR; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(block + Geo::chunk_offset(row, i, 128));
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             most = max(most, max((y[e] << 16) & 0x7FFFFFFFu, y[e] & 0x7FFF0000u));
         }
         const int ex = max((int)(most >> 23) - 127 - 14, -110);
-        qs = __int_as_float((ex + 127) << 23);
         const float inv = sign * __int_as_float((127 - ex) << 23);
-        if (!wait(q_empty, (segs & 1) ^ 1)) break;
-        if (!small || w == 0) {
-          uint8_t* dst = smem + C::Q_OFF + w * C::SLOT;
+        qs = __int_as_float((ex + 127) << 23);
+#pragma unroll 4
+        for (int i = 0; i < LPR; ++i) {
+          uint4* place = reinterpret_cast<uint4*>(block + Geo::chunk_offset(row, i, 128));
+          const uint4 x = *place;
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[4];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = pack_f16(__uint_as_float(y[e] << 16) * inv,
-                              __uint_as_float(y[e] & 0xFFFF0000u) * inv);
-            *reinterpret_cast<uint4*>(dst + Geo::chunk_offset(row, i, 128)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          tc::fence_proxy_async_smem();
+          for (int e = 0; e < 4; ++e)
+            h[e] = pack_f16(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xFFFF0000u) * inv);
+          *place = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(q_full);
+        if (small) *told = qs;
       }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+      if (small && w == 1) {
+        if (!wait(q_full, loaded & 1)) return false;
+        qs = *reinterpret_cast<volatile float*>(told);
+      }
+      ++loaded;
+      return true;
+    };
+    uint32_t cnt = 0;  // tiles of this warpgroup so far
+    int tile0 = 0;     // tiles of the segments before
+    int segs = 0, smalls = 0;
+    Seg s;
+    float qs = 1.0f;
+    bool more = take(0, s) && !(s.flags & kStop);
+    if (more && s.t1 > s.t0) more = queries(s, qs);
+#pragma unroll 1
+    for (int number = 1; more; ++number) {
+      const bool small = s.flags & kSmall;
+      const int T = s.t1 - s.t0, step = small ? 2 : 1;
+      const bool there = is_there(s);
+      const int p = there ? s.p0 + token_of(s) : -1;  // the row's position
       const bool warp_there = __any_sync(0xffffffffu, there);
       const int p_first = s.p0 + (small ? 0 : w * a.tokens);  // the least position
       float nm = -INFINITY, l = 0.0f, ref = 1.0f;
-      const int step = small ? 2 : 1;
       bool ok = true;
       int mine = 0;  // tiles of this segment so far
 #pragma unroll 1
@@ -846,93 +923,133 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
         if (!(ok = wait(s_full + w, cnt & 1))) break;
         tc::fence_after_sync();
         if (warp_there) {
-          float v[2][64];
-          tc::tmem_ld64(s_addr, v[0]);
-          tc::tmem_ld64(s_addr + 64, v[1]);
-          tc::tmem_wait_ld(v[0]);
-          tc::tmem_wait_ld(v[1]);
           ref = tile->ref;
           const uint32_t absent = tile->absent;
           // (uniform in the warpgroup) some key is not seen by some row
           const bool masked = absent != 0 || t * 128 + 127 > p_first;
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (t * 128 + j > p || (absent >> (j / 16) & 1)) v[j / 64][j % 64] = -INFINITY;
-          }
-          float top = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float2 k = tile->group[g];
-            const float* x = v[g / 4] + g % 4 * 16;
-            float most = max3(x[0], x[1], x[2]);
-#pragma unroll
-            for (int j = 3; j < 15; j += 2) most = max3(most, x[j], x[j + 1]);
-            most = fmaxf(most, x[15]);
-            top = fmaxf(top, __fadd_rn(__fmul_rn(most, k.x * qs), k.y));
-          }
-          const bool raise = top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float to = raise ? 4.0f - ceilf(fmaxf(top, -att::kLargest)) : nm;
+          // Groups of 16 keys: their largest score with b added.
+          auto top_of = [&](const float2& k, const float* x) {
+            float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+            m0 = max3(m0, x[6], x[7]);
+            m1 = max3(m1, x[8], x[9]);
+            m0 = max3(m0, x[10], x[11]);
+            m1 = max3(m1, x[12], x[13]);
+            m0 = max3(m0, x[14], x[15]);
+            return __fadd_rn(__fmul_rn(fmaxf(m0, m1), k.x * qs), k.y);
+          };
+          // The row's reference to at least `top` - 4 where a weight would pass 2^11.
+          auto raise = [&](float top) -> bool {
+            const bool over = top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
+            if (!__any_sync(0xffffffffu, over)) return true;
+            const float to = over ? 4.0f - ceilf(fmaxf(top, -att::kLargest)) : nm;
             const float f = nm == -INFINITY ? 1.0f : ex2(to - nm);
             l *= f;
-            if (mine > 0) {
-              if (!(ok = wait(pv_done + w, (cnt - 1) & 1))) break;
-              tc::fence_after_sync();
-#pragma unroll 1
-              for (int i = 0; i < D; i += 8) {
-                float o[8];
-                att::tmem_load(o_addr + i, o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= f;
-                att::tmem_store8(o_addr + i, o);
-              }
-              tc::tmem_wait_st();
-            }
             nm = to;
-          }
-          // Weights. Far from 0 the products are rounded as the maximum was, a masked weight
-          // is 0 whatever its group's scale is, and a row without a score so far (nm = -inf)
-          // has none.
-          const bool slow = __any_sync(0xffffffffu, fabsf(nm) > 1048576.0f) || masked;
+            if (mine == 0) return true;
+            if (!wait(pv_done + w, (cnt - 1) & 1)) return false;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 8) {
+              float o[8];
+              att::tmem_load(o_addr + i, o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t y[16];
+              for (int e = 0; e < 8; ++e) o[e] *= f;
+              att::tmem_store8(o_addr + i, o);
+            }
+            tc::tmem_wait_st();
+            return true;
+          };
+          bool slow = masked;
+          if (!masked) {
+            float v[2][64];
+            tc::tmem_ld64(s_addr, v[0]);
+            tc::tmem_ld64(s_addr + 64, v[1]);
+            tc::tmem_wait_ld(v[0]);
+            tc::tmem_wait_ld(v[1]);
+            float top = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int g = 2 * i + h;
-              const float2 k = tile->group[g];
-              const float cc = k.x * qs, kb = k.y + nm;
-              float s0 = 0.0f, s1 = 0.0f;
-              if (!slow) {
+            for (int g = 0; g < 8; ++g)
+              top = fmaxf(top, top_of(tile->group[g], v[g / 4] + g % 4 * 16));
+            if (!(ok = raise(top))) break;
+            // Far from 0 the products must be rounded as the maximum was; a row without a
+            // score so far (nm = -inf) has no weights: both below.
+            slow = __any_sync(0xffffffffu, fabsf(nm) > 1048576.0f);
+            if (!slow) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float x0 = v[i / 2][i % 2 * 32 + 16 * h + j], x1 = v[i / 2][i % 2 * 32 + 16 * h + j + 1];
-                  fma2(x0, x1, cc, kb, kb);
-                  x0 = ex2(x0);
-                  x1 = ex2(x1);
-                  add2(s0, s1, x0, x1);
-                  y[8 * h + j / 2] = pack_f16(x0, x1);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t y[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float2 k = tile->group[2 * i + h];
+                  const float cc = k.x * qs, kb = k.y + nm;
+                  float* x = v[i / 2] + i % 2 * 32 + 16 * h;
+                  float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+                  for (int j = 0; j < 16; j += 4) {
+                    fma2(x[j], x[j + 1], cc, kb, kb);
+                    fma2(x[j + 2], x[j + 3], cc, kb, kb);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[j + e] = ex2(x[j + e]);
+                    add2(s0, s1, x[j], x[j + 1]);
+                    add2(s2, s3, x[j + 2], x[j + 3]);
+                    y[8 * h + j / 2] = pack_f16(x[j], x[j + 1]);
+                    y[8 * h + j / 2 + 1] = pack_f16(x[j + 2], x[j + 3]);
+                  }
+                  l += ((s0 + s1) + (s2 + s3)) * ex2(nm - kb);
                 }
-                l += (s0 + s1) * ex2(nm - kb);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float x0 = v[i / 2][i % 2 * 32 + 16 * h + j], x1 = v[i / 2][i % 2 * 32 + 16 * h + j + 1];
-                  const bool off0 = t * 128 + 16 * g + j > p || (absent >> g & 1);
-                  const bool off1 = t * 128 + 16 * g + j + 1 > p || (absent >> g & 1);
-                  x0 = __fadd_rn(__fadd_rn(__fmul_rn(x0, cc), k.y), nm);
-                  x1 = __fadd_rn(__fadd_rn(__fmul_rn(x1, cc), k.y), nm);
-                  x0 = off0 ? 0.0f : ex2(x0);
-                  x1 = off1 ? 0.0f : ex2(x1);
-                  s0 += x0;
-                  s1 += x1;
-                  y[8 * h + j / 2] = pack_f16(x0, x1);
-                }
-                if (s0 + s1 != 0.0f) l += (s0 + s1) * ex2(-k.y);
+                tmem_store16(s_addr + 16 * i, y);
               }
             }
-            tmem_store16(s_addr + 16 * i, y);
+          }
+          if (slow) {
+            // keys that the row sees, of 32 at a time, as bits
+            auto seen = [&](int i) -> uint32_t {
+              if (!masked) return ~0u;
+              const int upto = p - (t * 128 + i * 32) + 1;
+              uint32_t m = upto <= 0 ? 0u : upto >= 32 ? ~0u : (1u << upto) - 1u;
+              if (absent >> (2 * i) & 1) m &= 0xFFFF0000u;
+              if (absent >> (2 * i + 1) & 1) m &= 0x0000FFFFu;
+              return m;
+            };
+            if (masked) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                float v[32];
+                tc::tmem_ld32(s_addr + 32 * i, v);
+                tc::tmem_wait_ld(v);
+                const uint32_t see = seen(i);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = see >> j & 1 ? v[j] : -INFINITY;
+                top = fmaxf(top, top_of(tile->group[2 * i], v));
+                top = fmaxf(top, top_of(tile->group[2 * i + 1], v + 16));
+              }
+              if (!(ok = raise(top))) break;
+            }
+            // (a masked weight is 0 whatever its group's scale is)
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              float v[32];
+              uint32_t y[16];
+              tc::tmem_ld32(s_addr + 32 * i, v);
+              tc::tmem_wait_ld(v);
+              const uint32_t see = seen(i);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float2 k = tile->group[2 * i + h];
+                const float cc = k.x * qs;
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 16 * h; j < 16 * h + 16; ++j) {
+                  const float x = __fadd_rn(__fadd_rn(__fmul_rn(v[j], cc), k.y), nm);
+                  v[j] = see >> j & 1 ? ex2(x) : 0.0f;
+                  sum += v[j];
+                  if (j & 1) y[j / 2] = pack_f16(v[j - 1], v[j]);
+                }
+                if (sum != 0.0f) l += sum * ex2(-k.y);
+              }
+              tmem_store16(s_addr + 16 * i, y);
+            }
           }
           tc::tmem_wait_st();
         }
@@ -941,6 +1058,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
         if (lane == 0) tc::mbar_arrive(p_full + w);
       }
       if (!ok) break;
+      // The next segment's queries first: its scores are made while this one's result goes out.
+      Seg next;
+      float qs_next = 1.0f;
+      more = take(number, next) && !(next.flags & kStop);
+      if (more && next.t1 > next.t0) more = queries(next, qs_next);
+      const int token = token_of(s), head = s.hk * a.G + my_head;
+      const size_t q_at = (size_t)(s.row0 + token);
+      if (T == 0) {
+        if (there && !(small && w)) {
+          uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
+#pragma unroll 1
+          for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
+        }
+        s = next;
+        qs = qs_next;
+        continue;
+      }
       tile0 += T;
       // ---- the result ----
       if (mine > 0) {
@@ -978,22 +1113,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
         const float sum = l * f1 + l2 * f2;
         const bool part = s.part >= 0;
         const int r = w * 128 + row;
-        float norm = ref;
-        if (!part) norm = sum == 0.0f ? 0.0f : ref / sum;
+        const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
         f1 *= norm;
         f2 *= norm;
-        const bool none = !part && sum == 0.0f;
+        float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
+        __nv_bfloat16* to_out = a.out + (q_at * Hq + head) * D;
 #pragma unroll 1
         for (int i = 0; i < D; i += 16) {
-          float o[16];
-          att::tmem_load(o_addr + i, o);
+          float o[16], x[16];
+          tc::tmem_ld16(o_addr + i, o);
+          tc::tmem_ld16(o_addr + (other ? D : 0) + i, x);
+          tc::tmem_wait_ld(o);
+          tc::tmem_wait_ld(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
-          if (other) {
-            float x[16];
-            att::tmem_load(o_addr + D + i, x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
+          for (int e = 0; e < 16; ++e) {
+            o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
+            o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
           }
           if (nan_here) {
 #pragma unroll
@@ -1001,25 +1136,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
               if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
           }
           if (there && part) {
-            float4* y = reinterpret_cast<float4*>(a.part + ((size_t)s.part * a.rows + r) * D + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           } else if (there) {
-            uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D + i);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              y[e] = make_uint4(att::pack_bf16(o[8 * e], o[8 * e + 1]),
-                                att::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                att::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                                att::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(to_out + i + e) =
+                  make_uint4(att::pack_bf16(o[e], o[e + 1]), att::pack_bf16(o[e + 2], o[e + 3]),
+                             att::pack_bf16(o[e + 4], o[e + 5]), att::pack_bf16(o[e + 6], o[e + 7]));
           }
           __syncwarp();
         }
         if (there) {
           const float m = both == INFINITY ? -INFINITY : both;
           if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, m);
-          else if (a.lse) a.lse[q_at * Hq + head] = none ? -INFINITY : (log2f(sum) - m) * att::kLn2;
+          else if (a.lse) a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
         }
       }
       if (nan_here) {
@@ -1036,6 +1168,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
         if (small) tc::mbar_arrive(o_empty);
       }
       ++segs;
+      s = next;
+      qs = qs_next;
     }
   }
   tc::fence_before_sync();
