@@ -44,6 +44,8 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   if (Hkv < 1 || Hq < 1 || Hq % Hkv) return HYTOPK_INVALID_ARG;
   if (Hq / Hkv > 128 || (d != 64 && d != 128) || (int64_t)n * Hq >= (int64_t)1 << 31)
     return HYTOPK_UNSUPPORTED;
+  // rows of a pool are numbered in 32 bits, one past the last included
+  if ((int64_t)paged->N * paged->P >= ((int64_t)1 << 31) - 16) return HYTOPK_UNSUPPORTED;
   if (n == 0 || paged->B == 0) return HYTOPK_OK;
   if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !out || !workspace)
     return HYTOPK_INVALID_ARG;

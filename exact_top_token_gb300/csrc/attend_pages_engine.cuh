@@ -34,13 +34,14 @@
 //
 //   warp 0        MMA issuer, TMEM
 //   warp 1        this CTA's segments: (item, tiles) in order, through a ring
-//   warp 2        page scales of a tile, through a ring
+//   warp 2        pages: codes of the tiles by TMA, their scales through a ring
 //   warps 4-11    softmax, two warpgroups; queries; results
-//   warps 12-15   codes: loads of the next tile in registers, widened into the ring
+//   warps 12-15   codes to f16, as they land, into the ring of operands
 #pragma once
 
 #include "attend_engine.cuh"
 #include "attend_pages.h"
+#include "launch.h"
 
 namespace hytopk {
 namespace pages {
@@ -52,12 +53,12 @@ using att::fma2;
 using att::max3;
 using att::wait_bar;
 
-constexpr int kOverhead = 2;   // of an item, in the units below
+constexpr int kOverhead = 8;   // of an item, in the units below
 constexpr int kSegs = 8;       // ring of segments
-constexpr int kConsts = 8;     // ring of the tiles' scales
+constexpr int kConsts = 16;    // ring of the tiles' scales
 constexpr int kThreads = 512;
-// Registers: 128 a thread at launch, then by role: 128 (48 + 2 * 168 + 128) = 65536.
-constexpr int kRegsLaunch = 128, kRegsCtl = 48, kRegsSoft = 168, kRegsWide = 128;
+// Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 184 + 80) = 65536.
+constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 184, kRegsWide = 80;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
 
 // A segment: tiles [t0, t1) of an item.
@@ -70,7 +71,7 @@ struct Seg {
 enum : int { kStop = 1, kSmall = 2, kStarts = 4, kEnds = 8 };
 
 struct TileConst {
-  float2 group[8];  // factor of the scores, b
+  float4 group[4];  // of two groups: factor of the scores, b
   float ref;        // reference of v's scales
   uint32_t absent;  // groups that are not there
   uint32_t pad[2];
@@ -83,21 +84,31 @@ struct PCfg {
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;
   static constexpr int NS = D == 128 ? 4 : 8;  // even: K in even slots, V in odd ones
-  static constexpr int NANS = D == 128 ? 4 : 8;  // items whose NaN columns are kept: see below
+  // V of a later item is written while results of item i are awaited: with V of item
+  // i + 1 held back, up to V of item i + NS / 2.
+  static constexpr int NANS = NS / 2 + 2;  // items whose NaN columns are kept
+  // Codes on their way: 32 rows a unit, a widening warp's own, UNITS of each warp. For d = 128
+  // shared memory holds one beside large items; small ones, which wait for memory rather
+  // than for the tensor core, have two more in the place of the second block of queries.
+  static constexpr int UNIT = 32 * D;
+  static constexpr int UNITS = D == 128 ? 1 : 6;
+  static constexpr bool SHARED = D == 128;
+  static constexpr int SMALL_UNITS = SHARED ? UNITS + SLOT / (4 * UNIT) : UNITS;
   static constexpr int Q_OFF = NS * SLOT;
-  static constexpr int NAN_OFF = Q_OFF + 2 * SLOT;
-  static constexpr int CONST_OFF = NAN_OFF + NANS * 8 * D * 4;
+  static constexpr int STAGE_OFF = Q_OFF + 2 * SLOT;
+  static constexpr int NAN_OFF = STAGE_OFF + 4 * UNITS * UNIT;
+  static constexpr int CONST_OFF = NAN_OFF + NANS * 2 * D * 4;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
   static constexpr int QS_OFF = ML_OFF + 128 * 8;
   static constexpr int BAR_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;
-  static constexpr int SMEM = BAR_OFF + 768 + 1024;
+  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static constexpr int S_COL = 0, O_COL = 256, COLS = 512;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(NS % 2 == 0 && NS / 2 + 2 <= kConsts, "rings");
-  // V of a later item is written while results of item i are awaited: with V of item
-  // i + 1 held back, up to V of item i + NS / 2.
-  static_assert(NANS > NS / 2, "NaN columns");
+  static_assert(NS % 2 == 0, "K in even slots, V in odd ones");
+  // The scales of a tile are written once its K has a place: the tile SMALL_UNITS / 2 before
+  // it is widened then, so the one NS / 2 before that is done with.
+  static_assert((SMALL_UNITS + 1) / 2 + NS / 2 + 1 < kConsts, "scales");
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -286,12 +297,14 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
 // ---- the kernel -------------------------------------------------------------------------
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attend_pages(const AttendArgs a, const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map) {
   constexpr int D = C::D, NS = C::NS;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem = tc::align1024(smem_dyn);
-  int* nan_s = reinterpret_cast<int*>(smem + C::NAN_OFF);  // [NANS][8 warps][D] first key
+  int* nan_s = reinterpret_cast<int*>(smem + C::NAN_OFF);  // [NANS][2][D] first key
   TileConst* const_s = reinterpret_cast<TileConst*>(smem + C::CONST_OFF);
   Seg* seg_s = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
   float2* ml_s = reinterpret_cast<float2*>(smem + C::ML_OFF);
@@ -309,16 +322,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
   uint64_t* ml_empty = ml_full + 1;
   uint64_t* seg_full = ml_empty + 1;  // [kSegs]
   uint64_t* seg_empty = seg_full + kSegs;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegs);
+  uint64_t* c_full = seg_empty + kSegs;       // [kConsts] scales of a tile
+  uint64_t* unit_full = c_full + kConsts;     // [SMALL_UNITS][4] codes
+  uint64_t* unit_empty = unit_full + 4 * C::SMALL_UNITS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + 4 * C::SMALL_UNITS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* nan_any = tmem_slot + 2;  // [NANS][8 warps] some column of an item is NaN
+  // [NANS][2]: some column of an item is NaN; softmax warps that are done with them
+  uint32_t* nan_any = tmem_slot + 2;
+  uint32_t* nan_done = nan_any + 2 * C::NANS;
   Share* share = reinterpret_cast<Share*>(ml_s);           // (before anything else is there)
   int64_t* scan_s = reinterpret_cast<int64_t*>(const_s);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(full + i, i % 2 ? 4 : 5);
+      tc::mbar_init(full + i, 4);
       tc::mbar_init(empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -335,11 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
       tc::mbar_init(seg_full + i, 1);
       tc::mbar_init(seg_empty + i, 1 + 1 + 8 + 4);
     }
+    for (int i = 0; i < kConsts; ++i) tc::mbar_init(c_full + i, 1);
+    for (int i = 0; i < 4 * C::SMALL_UNITS; ++i) {
+      tc::mbar_init(unit_full + i, 1);
+      tc::mbar_init(unit_empty + i, 1);
+    }
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  for (int i = threadIdx.x; i < C::NANS * 8 * D; i += kThreads) nan_s[i] = INT32_MAX;
-  if (threadIdx.x < C::NANS * 8) nan_any[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < C::NANS * 2 * D; i += kThreads) nan_s[i] = INT32_MAX;
+  if (threadIdx.x < C::NANS * 4) nan_any[threadIdx.x] = 0;  // (and nan_done)
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, C::COLS);
     tc::tmem_relinquish();
@@ -364,6 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(seg_empty + number % kSegs);
     return true;
+  };
+  // place of unit i of a widening warp
+  auto unit_at = [&](int i, int ww) -> uint8_t* {
+    return smem + (i < C::UNITS ? C::STAGE_OFF + (i * 4 + ww) * C::UNIT
+                                : C::Q_OFF + C::SLOT + ((i - C::UNITS) * 4 + ww) * C::UNIT);
   };
 
   if (warp < 4) {
@@ -441,24 +469,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
       s.flags = kStop;
       if (ok) push(s);
     } else if (warp == 2) {
-      // ---------------- scales of the tiles ----------------
-      // Lanes 0 .. 7 take a group each. The page of the tile after next and the scales of
-      // the next one are loaded while this one's are written.
+      // ---------------- codes and scales of the tiles ----------------
+      // Lanes 0 .. 7 take a group each: its page, its scales, its 16 rows of K and V by TMA (a
+      // group that is not there lies past the pool's end, where rows of zeros are). The page
+      // of the tile after next and the scales of the next one are loaded while this one's go
+      // out.
       struct At {
-        Seg s;
-        int number, t;
+        int b, hk, end, t, t1, flags, number;
         bool ok;
       };
       auto settle = [&](At& c) {  // to the next tile at or after c
-        while (c.ok && !(c.s.flags & kStop) && c.t >= c.s.t1) {
+        while (c.ok && c.t >= c.t1) {
+          Seg s;
+          c.ok = take(c.number, s) && !(s.flags & kStop);
           ++c.number;
-          c.ok = take(c.number, c.s);
-          c.t = c.s.t0;
+          c.b = s.b;
+          c.hk = s.hk;
+          c.end = s.end;
+          c.t = s.t0;
+          c.t1 = s.t1;
+          c.flags = s.flags;
         }
       };
-      auto live = [&](const At& c) { return c.ok && !(c.s.flags & kStop); };
       auto next = [&](At c) {
-        if (live(c)) {
+        if (c.ok) {
           ++c.t;
           settle(c);
         }
@@ -466,31 +500,69 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
       };
       auto page_of = [&](const At& c) -> int {
         const int key = c.t * 128 + (lane & 7) * 16;
-        if (!live(c) || key >= c.s.end) return -1;
-        return ld_after(a.s.table + (size_t)c.s.b * a.s.columns + (key >> a.shift));
+        if (!c.ok || key >= c.end) return -1;
+        return ld_after(a.s.table + (size_t)c.b * a.s.columns + (key >> a.shift));
       };
       auto scales_of = [&](const At& c, int page) -> float2 {
         if (page < 0 || page >= a.s.N) return make_float2(0.0f, 0.0f);
-        const size_t at = (size_t)page * a.Hkv + c.s.hk;
+        const size_t at = (size_t)page * a.Hkv + c.hk;
         return make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
       };
       const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
-      At c0;
-      c0.number = 0;
-      c0.ok = take(0, c0.s);
-      c0.t = c0.s.t0;
+      At c0{0, 0, 0, 0, 0, 0, 0, true};
       settle(c0);
       At c1 = next(c0);
       int page0 = page_of(c0), page1 = page_of(c1);
       float2 sc0 = scales_of(c0, page0);
-      int tile = 0;
-      float ref = 0.0f;
+      int tile = 0, segs = 0;  // tiles and segments (with tiles) so far
+      float ref = 1.0f;
       bool fresh = true;  // the segment's first tile, whose largest is the reference
+      bool was_large = false;
+      int unit = 0;
+      uint32_t used = 0, phases = 0;  // bits of the units' places
+      auto copy = [&](const CUtensorMap* map, const At& c, int page) -> bool {
+        const int i = unit;
+        const uint32_t bit = 1u << i;
+        bool ok = true;
 #pragma unroll 1
-      while (live(c0)) {
+        for (int ww = 0; ww < 4 && ok; ++ww)
+          ok = wait(unit_empty + i * 4 + ww, (phases & bit) ? 0u : 1u);
+        if (!ok) return false;
+        phases ^= bit;
+        used |= bit;
+        if (lane < 4) tc::mbar_expect_tx(unit_full + i * 4 + lane, C::UNIT);
+        __syncwarp();
+        if (lane < 8) {
+          const bool in = page >= 0 && page < a.s.N;
+          const int row = in ? (page << a.shift) + ((c.t * 128 + lane * 16) & (a.s.P - 1))
+                             : a.s.N << a.shift;
+          tc::tma_load_2d(unit_at(i, lane >> 1) + (lane & 1) * 16 * D, map,
+                          unit_full + i * 4 + (lane >> 1), c.hk * D, row);
+        }
+        __syncwarp();
+        unit = unit + 1 < (c.flags & kSmall ? C::SMALL_UNITS : C::UNITS) ? unit + 1 : 0;
+        return true;
+      };
+      if (lane == 0) {
+        tc::tma_prefetch(&k_map);
+        tc::tma_prefetch(&v_map);
+      }
+      // (what earlier kernels stored is read by the copies' own path)
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      bool ok = true;
+#pragma unroll 1
+      while (c0.ok) {
         const At c2 = next(c1);
         const int page2 = page_of(c2);
         const float2 sc1 = scales_of(c1, page1);
+        if (fresh) {
+          const bool small = c0.flags & kSmall;
+          if (C::SHARED && small == was_large) unit = 0;
+          // (the last large item's queries lie in the place of a small one's codes)
+          if (C::SHARED && small && was_large && !(ok = wait(q_empty, (segs - 1) & 1))) break;
+          was_large = !small;
+        }
+        if (!(ok = copy(&k_map, c0, page0))) break;
         const bool in = page0 >= 0 && page0 < a.s.N;
         if (page0 != -1 && !in && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
         const bool k_ok = sc0.x > 0.0f && sc0.x <= att::kLargest;
@@ -510,25 +582,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
           group.y = v_ok ? fminf(fmaxf(log2f(sc0.y / ref), -100.0f), 100.0f) : nan;
         }
         const uint32_t absent = ~__ballot_sync(0xffffffffu, in) & 0xFFu;
-        const int seq = 2 * tile, slot = seq % NS;
-        if (!wait(empty + slot, ((seq / NS) & 1) ^ 1)) break;
         TileConst* out = const_s + tile % kConsts;
-        if (lane < 8) out->group[lane] = group;
+        if (lane < 8) reinterpret_cast<float2*>(out->group)[lane] = group;
         if (lane == 0) {
           out->ref = ref;
           out->absent = absent;
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full + slot);
+        if (lane == 0) tc::mbar_arrive(c_full + tile % kConsts);
+        if (!(ok = copy(&v_map, c0, page0))) break;
         ++tile;
-        if (c1.number != c0.number) fresh = true;
+        if (c1.number != c0.number) {
+          fresh = true;
+          ++segs;
+        }
         c0 = c1;
         c1 = c2;
         page0 = page1;
         page1 = page2;
         sc0 = sc1;
       }
-      // (the last segments, which had no tile after them, need no release)
+      if (!ok || *abort_flag) {
+        // given up: copies in flight land before the CTA ends (a bounded wait)
+#pragma unroll 1
+        for (int i = 0; i < 4 * C::SMALL_UNITS; ++i) {
+          if (!(used >> (i / 4) & 1)) continue;
+          const uint32_t parity = phases >> (i / 4) & 1 ? 0u : 1u;  // of the last copy there
+          for (int n = 0; n < 100000; ++n)
+            if (tc::mbar_try_wait(unit_full + i, parity)) break;
+        }
+      }
     } else if (warp == 0) {
       // ---------------- MMA issuer ----------------
       // The whole warp waits and keeps the state, all of it in uniform registers (numbers
@@ -667,56 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWide));
     // ---------------- codes to f16 ----------------
-    // A warp takes 32 rows of a tile, two groups, CPR lanes a row.
+    // A warp takes 32 rows of a tile as they land, CPR lanes a row.
     constexpr int CPR = D / 16, RPP = 32 / CPR, PASSES = 32 / RPP;
     const int ww = warp - 12, c = lane % CPR, rl = lane / CPR;
-    const uint32_t row_bytes = (uint32_t)(a.Hkv * D);
-    struct Codes {
-      uint4 x[PASSES];
-    };
-    // The next tile to load: t of segment `number`, whose numbers these are. Kept small: a
-    // spilled register's load would wait behind the loads of the codes.
-    struct At {
-      const int32_t* pages;  // of the sequence
-      uint32_t column;       // of the lane's codes in a row
-      int p0, end, t, t1, number;
-    };
-    auto take_next = [&](At& p) -> bool {  // false: no more
-      Seg s;
-      if (!take(p.number, s) || (s.flags & kStop)) return false;
-      ++p.number;
-      p.pages = a.s.table + (size_t)s.b * a.s.columns;
-      p.column = (uint32_t)(s.hk * D + c * 16);
-      p.p0 = s.p0;
-      p.end = s.end;
-      p.t = s.t0;
-      p.t1 = s.t1;
-      return true;
-    };
-    // pages of the warp's two groups (-1: not there)
-    auto pages_at = [&](const At& p, int (&page)[2]) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int key = p.t * 128 + ww * 32 + g * 16;
-        page[g] = -1;
-        if (key < p.end) page[g] = ld_after(p.pages + (key >> a.shift));
-      }
-    };
-    auto load = [&](const uint8_t* from, const At& p, const int (&page)[2], Codes& r) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t in = (uint32_t)(p.t * 128 + ww * 32 + g * 16) & (uint32_t)(a.s.P - 1);
-        const bool there = (uint32_t)page[g] < (uint32_t)a.s.N;
-        const uint8_t* src = from + p.column +
-                             (((uint64_t)(uint32_t)max(page[g], 0) << a.shift) + in + rl) * row_bytes;
-#pragma unroll
-        for (int u = 0; u < PASSES / 2; ++u) {
-          r.x[g * (PASSES / 2) + u] = make_uint4(0, 0, 0, 0);
-          if (there) r.x[g * (PASSES / 2) + u] = ld_after(reinterpret_cast<const uint4*>(src));
-          src += RPP * row_bytes;
-        }
-      }
-    };
     // Two 16-byte chunks of f16 for 16 codes. Lanes of the second 128-byte line of a row
     // write theirs in the other order: eight lanes at a time then meet eight banks.
     const int flip = (2 * c) >> 3 & 1;
@@ -724,15 +760,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       place[e] = tc::smem_u32(smem) + Geo::chunk_offset(ww * 32 + rl, 2 * c + (e ^ flip), 128);
-    // (rows RPP apart: the swizzle repeats every 8 rows)
-    auto spread = [&](int slot, const Codes& r) {
+    int unit = 0, slot = 0;
+    uint32_t phases = 0, phase = 1;
+    bool large = false;
+    // The next unit's codes into the next slot of the ring, whose row `key0` + ... some row of
+    // the item may not see (`partly`). (The MMA issuer makes them visible to the tensor core.)
+    auto spread = [&](bool partly, int key0, int end, int nans) -> bool {
+      const uint32_t bit = 1u << unit;
+      if (!wait(unit_full + unit * 4 + ww, (phases & bit) ? 1u : 0u)) return false;
+      phases ^= bit;
+      const uint4* from = reinterpret_cast<const uint4*>(unit_at(unit, ww)) + lane;
+      uint4 x[PASSES];
+#pragma unroll
+      for (int u = 0; u < PASSES; ++u) x[u] = from[u * 32];
+      uint32_t found = 0;
+      if (partly) {
+#pragma unroll
+        for (int u = 0; u < PASSES; ++u)
+          found |= nan_codes(x[u].x) | nan_codes(x[u].y) | nan_codes(x[u].z) | nan_codes(x[u].w);
+      }
+      const bool odd = __any_sync(0xffffffffu, found != 0);  // (and all have read the unit)
+      if (lane == 0) tc::mbar_arrive(unit_empty + unit * 4 + ww);
+      unit = unit + 1 < (large ? C::UNITS : C::SMALL_UNITS) ? unit + 1 : 0;
+      if (!wait(empty + slot, phase)) return false;
+      // (rows RPP apart: the swizzle repeats every 8 rows)
 #pragma unroll
       for (int u = 0; u < PASSES; ++u) {
-        const uint32_t w[4] = {r.x[u].x, r.x[u].y, r.x[u].z, r.x[u].w};
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // rows u * RPP on: 8-row groups are 1024 bytes apart, and a half of one flips the
-          // chunk's third bit
+          // 8-row groups are 1024 bytes apart, and a half of one flips the chunk's third bit
           const uint32_t at = (RPP == 8 ? place[e] + u * 1024
                                         : (place[e] + (u / 2) * 1024 + (u % 2) * 512) ^
                                               ((u % 2) * 64u)) +
@@ -742,69 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
           att::st_shared16(at, make_uint4(lo.x, lo.y, hi.x, hi.y));
         }
       }
-    };
-    // (the MMA issuer makes it visible to the tensor core: a fence here would wait for the
-    // loads of the next tile)
-    auto publish = [&](int slot) {
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(full + slot);
-    };
-    At at;
-    at.number = 0;
-    auto next_segment = [&]() {
-      bool more = take_next(at);
-      while (more && at.t >= at.t1) more = take_next(at);
-      return more;
-    };
-    bool more = next_segment();
-    int slot = 0, item = 0;  // item: of the NaN columns
-    uint32_t phase = 1;
-    auto step = [&]() {
-      if (++slot == NS) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    };
-    Codes kc, vc;
-    if (more) {
-      int page[2];
-      pages_at(at, page);
-      load(a.k, at, page, kc);
-      load(a.v, at, page, vc);
-    }
-#pragma unroll 1
-    while (more) {
-      const int key0 = at.t * 128 + ww * 32 + rl, p0 = at.p0, end = at.end;
-      const bool partly = at.t * 128 + 127 > p0;  // keys that some row does not see
-      const int nans = item;
-      if (++at.t == at.t1) {
-        more = next_segment();
-        item = (item + 1) % C::NANS;
-      }
-      int page[2] = {-1, -1};
-      if (more) pages_at(at, page);
-      if (!wait(empty + slot, phase)) break;
-      spread(slot, kc);
-      publish(slot);
-      // (looked at only here: a test right after its load would wait for it)
-      asm volatile("" : "+r"(page[0]), "+r"(page[1]));
-      if (more) load(a.k, at, page, kc);
-      step();
-      if (!wait(empty + slot, phase)) break;
-      bool odd = false;  // NaN codes where some row does not see the key
-      if (partly) {
-        uint32_t found = 0;
-#pragma unroll
-        for (int u = 0; u < PASSES; ++u)
-          found |= nan_codes(vc.x[u].x) | nan_codes(vc.x[u].y) | nan_codes(vc.x[u].z) |
-                   nan_codes(vc.x[u].w);
-        odd = __any_sync(0xffffffffu, found != 0);
-      }
-      spread(slot, vc);
       if (odd) {
-        // replaced by 0 where they went, and their keys kept by column for the rows that see
-        // them (each softmax warp clears its own)
-        int* first = nan_s + nans * 8 * D + c * 16;
+        // NaN codes are replaced by 0 where they went, and their keys kept by column for the
+        // rows that see them
+        int* first = nan_s + nans * 2 * D + c * 16;
 #pragma unroll 1
         for (int u = 0; u < PASSES * 16; ++u) {
           const int e = u % 16, r = ww * 32 + u / 16 * RPP + rl, key = key0 + u / 16 * RPP;
@@ -814,15 +812,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
           *h = 0;
           if (key >= end) continue;
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 2; ++i) {  // a softmax warpgroup's own, which it clears
             atomicMin(first + i * D + e, key);
-            nan_any[nans * 8 + i] = 1;
+            nan_any[nans * 2 + i] = 1;
           }
         }
       }
-      publish(slot);
-      if (more) load(a.v, at, page, vc);
-      step();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full + slot);
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      return true;
+    };
+    Seg s;
+    bool ok = true, first = true;
+    int item = 0;  // of the NaN columns
+#pragma unroll 1
+    for (int number = 0; ok && take(number, s) && !(s.flags & kStop); ++number) {
+      if (s.t0 >= s.t1) continue;
+      const bool now = !(s.flags & kSmall);
+      if (C::SHARED && (first || now != large)) unit = 0;
+      large = now;
+      first = false;
+#pragma unroll 1
+      for (int u = 2 * s.t0; ok && u < 2 * s.t1; ++u) {  // K, V, K, V, ...
+        const int key = (u >> 1) * 128;
+        ok = spread((u & 1) && key + 127 > s.p0, key + ww * 32 + rl, s.end, item);
+      }
+      item = (item + 1) % C::NANS;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
@@ -902,12 +921,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
     uint32_t cnt = 0;  // tiles of this warpgroup so far
     int tile0 = 0;     // tiles of the segments before
     int segs = 0, smalls = 0;
-    Seg s;
+    uint32_t cnt0 = 0;   // the first warpgroup's
+    bool dirty = false;  // codes of a small item may lie in the second block of queries
+    Seg s{};             // (nothing yet: no token, no tile)
     float qs = 1.0f;
-    bool more = take(0, s) && !(s.flags & kStop);
-    if (more && s.t1 > s.t0) more = queries(s, qs);
 #pragma unroll 1
-    for (int number = 1; more; ++number) {
+    for (int number = 0;; ++number) {
       const bool small = s.flags & kSmall;
       const int T = s.t1 - s.t0, step = small ? 2 : 1;
       const bool there = is_there(s);
@@ -919,12 +938,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
       int mine = 0;  // tiles of this segment so far
 #pragma unroll 1
       for (int t = s.t0 + (small ? w : 0); t < s.t1; t += step, ++mine, ++cnt) {
-        const TileConst* tile = const_s + (tile0 + t - s.t0) % kConsts;
+        // the tile's scales, before its scores are there
+        const int number_c = tile0 + t - s.t0;
+        const TileConst* tile = const_s + number_c % kConsts;
+        if (!(ok = wait(c_full + number_c % kConsts, (number_c / kConsts) & 1))) break;
+        const float4 g0 = tile->group[0], g1 = tile->group[1], g2 = tile->group[2], g3 = tile->group[3];
+        ref = tile->ref;
+        const uint32_t absent = tile->absent;
         if (!(ok = wait(s_full + w, cnt & 1))) break;
         tc::fence_after_sync();
         if (warp_there) {
-          ref = tile->ref;
-          const uint32_t absent = tile->absent;
+          const float2 groups[8] = {{g0.x, g0.y}, {g0.z, g0.w}, {g1.x, g1.y}, {g1.z, g1.w},
+                                    {g2.x, g2.y}, {g2.z, g2.w}, {g3.x, g3.y}, {g3.z, g3.w}};
+          auto group_of = [&](int g) {  // (of a loop: from shared memory)
+            return reinterpret_cast<const float2*>(tile->group)[g];
+          };
           // (uniform in the warpgroup) some key is not seen by some row
           const bool masked = absent != 0 || t * 128 + 127 > p_first;
           // Groups of 16 keys: their largest score with b added.
@@ -969,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
             float top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < 8; ++g)
-              top = fmaxf(top, top_of(tile->group[g], v[g / 4] + g % 4 * 16));
+              top = fmaxf(top, top_of(groups[g], v[g / 4] + g % 4 * 16));
             if (!(ok = raise(top))) break;
             // Far from 0 the products must be rounded as the maximum was; a row without a
             // score so far (nm = -inf) has no weights: both below.
@@ -980,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
                 uint32_t y[16];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float2 k = tile->group[2 * i + h];
+                  const float2 k = groups[2 * i + h];
                   const float cc = k.x * qs, kb = k.y + nm;
                   float* x = v[i / 2] + i % 2 * 32 + 16 * h;
                   float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
@@ -1021,8 +1049,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
                 const uint32_t see = seen(i);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = see >> j & 1 ? v[j] : -INFINITY;
-                top = fmaxf(top, top_of(tile->group[2 * i], v));
-                top = fmaxf(top, top_of(tile->group[2 * i + 1], v + 16));
+                top = fmaxf(top, top_of(group_of(2 * i), v));
+                top = fmaxf(top, top_of(group_of(2 * i + 1), v + 16));
               }
               if (!(ok = raise(top))) break;
             }
@@ -1036,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
               const uint32_t see = seen(i);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float2 k = tile->group[2 * i + h];
+                const float2 k = group_of(2 * i + h);
                 const float cc = k.x * qs;
                 float sum = 0.0f;
 #pragma unroll
@@ -1058,116 +1086,143 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_pages(const AttendArgs a
         if (lane == 0) tc::mbar_arrive(p_full + w);
       }
       if (!ok) break;
-      // The next segment's queries first: its scores are made while this one's result goes out.
+      if (T > 0) {
+        cnt0 += small ? (T + 1) / 2 : T;
+        dirty = C::SHARED && small;
+      }
+      // The next segment's queries, and this one's result: the queries first, so that the next
+      // scores are made while the result goes out; but where the queries take the place of
+      // codes, all products first.
       Seg next;
       float qs_next = 1.0f;
-      more = take(number, next) && !(next.flags & kStop);
-      if (more && next.t1 > next.t0) more = queries(next, qs_next);
-      const int token = token_of(s), head = s.hk * a.G + my_head;
-      const size_t q_at = (size_t)(s.row0 + token);
-      if (T == 0) {
-        if (there && !(small && w)) {
-          uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
+      const bool more = take(number, next) && !(next.flags & kStop);
+      const bool ask = more && next.t1 > next.t0;
+      const bool late = ask && dirty && !(next.flags & kSmall);
 #pragma unroll 1
-          for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
+      for (int pass = 0; ok && pass < 2; ++pass) {
+        if ((pass == 0) != late) {
+          if (!ask) continue;
+          if (late) {
+            // (own products are done; the first warpgroup's wait for these queries to go on)
+            if (w == 1 && !(ok = wait(pv_done, (cnt0 - 1) & 1))) break;
+            dirty = false;
+          }
+          ok = queries(next, qs_next);
+          continue;
         }
-        s = next;
-        qs = qs_next;
-        continue;
-      }
-      tile0 += T;
-      // ---- the result ----
-      if (mine > 0) {
-        if (!wait(pv_done + w, (cnt - 1) & 1)) break;
-        tc::fence_after_sync();
-      }
-      float l2 = 0.0f, nm2 = -INFINITY;  // the other warpgroup's
-      const bool other = small && T > 1;
-      if (small) {
-        if (w == 1) {
-          if (!wait(ml_empty, (smalls & 1) ^ 1)) break;
-          ml_s[row] = make_float2(l, nm);
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(ml_full);
-        } else {
-          if (!wait(ml_full, smalls & 1)) break;
+        const int token = token_of(s), head = s.hk * a.G + my_head;
+        const size_t q_at = (size_t)(s.row0 + token);
+        if (T == 0) {
+          if (there && !(small && w)) {
+            uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
+#pragma unroll 1
+            for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
+          }
+          continue;
+        }
+        tile0 += T;
+        // ---- the result ----
+        if (mine > 0) {
+          if (!(ok = wait(pv_done + w, (cnt - 1) & 1))) break;
           tc::fence_after_sync();
-          const float2 x = ml_s[row];
-          l2 = x.x;
-          nm2 = x.y;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(ml_empty);
         }
-        ++smalls;
-      }
-      int* nans = nan_s + ((segs % C::NANS) * 8 + warp - 4) * D;
-      uint32_t* any = nan_any + segs % C::NANS * 8 + warp - 4;
-      const bool nan_here = *reinterpret_cast<volatile uint32_t*>(any) != 0;
-      if (warp_there && !(small && w == 1)) {
-        // one reference for both; -inf: no row so far
-        const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
-        float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
-        float f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
-        const float sum = l * f1 + l2 * f2;
-        const bool part = s.part >= 0;
-        const int r = w * 128 + row;
-        const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
-        f1 *= norm;
-        f2 *= norm;
-        float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
-        __nv_bfloat16* to_out = a.out + (q_at * Hq + head) * D;
+        float l2 = 0.0f, nm2 = -INFINITY;  // the other warpgroup's
+        const bool other = small && T > 1;
+        if (small) {
+          if (w == 1) {
+            if (!(ok = wait(ml_empty, (smalls & 1) ^ 1))) break;
+            ml_s[row] = make_float2(l, nm);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(ml_full);
+          } else {
+            if (!(ok = wait(ml_full, smalls & 1))) break;
+            tc::fence_after_sync();
+            const float2 x = ml_s[row];
+            l2 = x.x;
+            nm2 = x.y;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(ml_empty);
+          }
+          ++smalls;
+        }
+        int* nans = nan_s + ((segs % C::NANS) * 2 + w) * D;
+        uint32_t* any = nan_any + segs % C::NANS * 2 + w;
+        const bool nan_here = *reinterpret_cast<volatile uint32_t*>(any) != 0;
+        if (warp_there && !(small && w == 1)) {
+          // one reference for both; -inf: no row so far
+          const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
+          float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
+          float f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
+          const float sum = l * f1 + l2 * f2;
+          const bool part = s.part >= 0;
+          const int r = w * 128 + row;
+          const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
+          f1 *= norm;
+          f2 *= norm;
+          float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
+          __nv_bfloat16* to_out = a.out + (q_at * Hq + head) * D;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 16) {
-          float o[16], x[16];
-          tc::tmem_ld16(o_addr + i, o);
-          tc::tmem_ld16(o_addr + (other ? D : 0) + i, x);
-          tc::tmem_wait_ld(o);
-          tc::tmem_wait_ld(x);
+          for (int i = 0; i < D; i += 16) {
+            float o[16], x[16];
+            tc::tmem_ld16(o_addr + i, o);
+            tc::tmem_ld16(o_addr + (other ? D : 0) + i, x);
+            tc::tmem_wait_ld(o);
+            tc::tmem_wait_ld(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
-            o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
+            for (int e = 0; e < 16; ++e) {
+              o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
+              o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
+            }
+            if (nan_here) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
+            }
+            if (there && part) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else if (there) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
+                *reinterpret_cast<uint4*>(to_out + i + e) =
+                    make_uint4(att::pack_bf16(o[e], o[e + 1]), att::pack_bf16(o[e + 2], o[e + 3]),
+                               att::pack_bf16(o[e + 4], o[e + 5]), att::pack_bf16(o[e + 6], o[e + 7]));
+            }
+            __syncwarp();
           }
-          if (nan_here) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
+          if (there) {
+            const float m = both == INFINITY ? -INFINITY : both;
+            if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, m);
+            else if (a.lse) a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
           }
-          if (there && part) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else if (there) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              *reinterpret_cast<uint4*>(to_out + i + e) =
-                  make_uint4(att::pack_bf16(o[e], o[e + 1]), att::pack_bf16(o[e + 2], o[e + 3]),
-                             att::pack_bf16(o[e + 4], o[e + 5]), att::pack_bf16(o[e + 6], o[e + 7]));
-          }
+        }
+        if (nan_here) {
+          // the last of the warpgroup's warps clears them
           __syncwarp();
+          uint32_t before = 0;
+          if (lane == 0) before = atomicAdd(nan_done + segs % C::NANS * 2 + w, 1u);
+          if (__shfl_sync(0xffffffffu, before, 0) == 3) {
+            for (int i = lane; i < D; i += 32) nans[i] = INT32_MAX;
+            if (lane == 0) {
+              *any = 0;
+              nan_done[segs % C::NANS * 2 + w] = 0;
+            }
+          }
         }
-        if (there) {
-          const float m = both == INFINITY ? -INFINITY : both;
-          if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, m);
-          else if (a.lse) a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
-        }
-      }
-      if (nan_here) {
+        // Eight arrivals: of a small item all are the first warpgroup's, which reads both
+        // results (the second may have no tile and be an item ahead).
+        tc::fence_before_sync();
         __syncwarp();
-        for (int i = lane; i < D; i += 32) nans[i] = INT32_MAX;
-        if (lane == 0) *any = 0;
+        if (lane == 0 && !(small && w == 1)) {
+          tc::mbar_arrive(o_empty);
+          if (small) tc::mbar_arrive(o_empty);
+        }
+        ++segs;
       }
-      // Eight arrivals: of a small item all are the first warpgroup's, which reads both
-      // results (the second may have no tile and be an item ahead).
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0 && !(small && w == 1)) {
-        tc::mbar_arrive(o_empty);
-        if (small) tc::mbar_arrive(o_empty);
-      }
-      ++segs;
+      if (!ok || !more) break;
       s = next;
       qs = qs_next;
     }
@@ -1307,6 +1362,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
 template <class C>
 cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) {
   auto kernel = k_attend_pages<C>;
+  // 16 rows of one head of a pool [N P rows, Hkv d]
+  CUtensorMap k_map, v_map;
+  const uint64_t rows = (uint64_t)a.s.N * a.s.P;
+  if (!make_tmap_2d(&k_map, a.k, 1, (uint64_t)a.Hkv * C::D, rows, C::D, 16, 0) ||
+      !make_tmap_2d(&v_map, a.v, 1, (uint64_t)a.Hkv * C::D, rows, C::D, 16, 0))
+    return cudaErrorInvalidValue;
   static unsigned long long opted_in = 0;
   static int regs_ok = 0;
   // setmaxnreg waits for registers that the launch must have brought
@@ -1319,7 +1380,7 @@ cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) 
   }
   const cudaError_t e =
       att::launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
-        return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a);
+        return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
   if (e != cudaSuccess) return e;
   return launch_early(k_join_parts<C::D>, 2u * (unsigned)ctas, kJoinThreads, 0, st, 1, a, ctas);
