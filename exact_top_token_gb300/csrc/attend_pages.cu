@@ -72,6 +72,7 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   a.status = dev_status;
   a.tokens = 128 / a.G;
   a.shift = __builtin_ctz((unsigned)paged->P);
+  a.box = paged->P < 128 ? paged->P : 128;
   a.rows = part_rows(n, a.G);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part = reinterpret_cast<float*>(ws);

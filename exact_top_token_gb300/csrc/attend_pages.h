@@ -21,6 +21,7 @@ struct AttendArgs {
   int n, Hkv, G;
   int tokens;  // of a block of 128 rows: 128 / G
   int shift;   // log2 of a page's rows
+  int box;     // rows that a page and a tile of 128 share
   float scale;
   __nv_bfloat16* out;
   float* lse;

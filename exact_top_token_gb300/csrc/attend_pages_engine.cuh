@@ -87,22 +87,23 @@ struct PCfg {
   // V of a later item is written while results of item i are awaited: with V of item
   // i + 1 held back, up to V of item i + NS / 2.
   static constexpr int NANS = NS / 2 + 2;  // items whose NaN columns are kept
-  // Codes on their way: 32 rows a unit, a widening warp's own, UNITS of each warp. For d = 128
-  // shared memory holds one beside large items; small ones, which wait for memory rather
-  // than for the tensor core, have two more in the place of the second block of queries.
-  static constexpr int UNIT = 32 * D;
+  // Codes on their way, a unit K or V of a tile. For d = 128 shared memory holds one beside
+  // large items; small ones, which wait for memory rather than for the tensor core, have
+  // two more in the place of the second block of queries.
+  static constexpr int UNIT = 128 * D;
   static constexpr int UNITS = D == 128 ? 1 : 6;
   static constexpr bool SHARED = D == 128;
-  static constexpr int SMALL_UNITS = SHARED ? UNITS + SLOT / (4 * UNIT) : UNITS;
+  static constexpr int SMALL_UNITS = SHARED ? UNITS + SLOT / UNIT : UNITS;
   static constexpr int Q_OFF = NS * SLOT;
   static constexpr int STAGE_OFF = Q_OFF + 2 * SLOT;
-  static constexpr int NAN_OFF = STAGE_OFF + 4 * UNITS * UNIT;
+  static constexpr int NAN_OFF = STAGE_OFF + UNITS * UNIT;
   static constexpr int CONST_OFF = NAN_OFF + NANS * 2 * D * 4;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
   static constexpr int QS_OFF = ML_OFF + 128 * 8;
-  static constexpr int BAR_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;
-  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+  static constexpr int EPI_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;  // [8 warps][1 KB]
+  static constexpr int BAR_OFF = EPI_OFF + 8 * 1024;
+  static constexpr int SMEM = BAR_OFF + 768 + 1024;
   static constexpr int S_COL = 0, O_COL = 256, COLS = 512;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NS % 2 == 0, "K in even slots, V in odd ones");
@@ -323,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_full = ml_empty + 1;  // [kSegs]
   uint64_t* seg_empty = seg_full + kSegs;
   uint64_t* c_full = seg_empty + kSegs;       // [kConsts] scales of a tile
-  uint64_t* unit_full = c_full + kConsts;     // [SMALL_UNITS][4] codes
-  uint64_t* unit_empty = unit_full + 4 * C::SMALL_UNITS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + 4 * C::SMALL_UNITS);
+  uint64_t* unit_full = c_full + kConsts;     // [SMALL_UNITS] codes
+  uint64_t* unit_empty = unit_full + C::SMALL_UNITS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + C::SMALL_UNITS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // [NANS][2]: some column of an item is NaN; softmax warps that are done with them
   uint32_t* nan_any = tmem_slot + 2;
@@ -354,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(seg_empty + i, 1 + 1 + 8 + 4);
     }
     for (int i = 0; i < kConsts; ++i) tc::mbar_init(c_full + i, 1);
-    for (int i = 0; i < 4 * C::SMALL_UNITS; ++i) {
+    for (int i = 0; i < C::SMALL_UNITS; ++i) {
       tc::mbar_init(unit_full + i, 1);
-      tc::mbar_init(unit_empty + i, 1);
+      tc::mbar_init(unit_empty + i, 4);
     }
     *abort_flag = 0;
     tc::fence_barrier_init();
@@ -388,10 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) tc::mbar_arrive(seg_empty + number % kSegs);
     return true;
   };
-  // place of unit i of a widening warp
-  auto unit_at = [&](int i, int ww) -> uint8_t* {
-    return smem + (i < C::UNITS ? C::STAGE_OFF + (i * 4 + ww) * C::UNIT
-                                : C::Q_OFF + C::SLOT + ((i - C::UNITS) * 4 + ww) * C::UNIT);
+  auto unit_at = [&](int i) -> uint8_t* {
+    return smem + (i < C::UNITS ? C::STAGE_OFF + i * C::UNIT
+                                : C::Q_OFF + C::SLOT + (i - C::UNITS) * C::UNIT);
   };
 
   if (warp < 4) {
@@ -470,10 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) push(s);
     } else if (warp == 2) {
       // ---------------- codes and scales of the tiles ----------------
-      // Lanes 0 .. 7 take a group each: its page, its scales, its 16 rows of K and V by TMA (a
-      // group that is not there lies past the pool's end, where rows of zeros are). The page
-      // of the tile after next and the scales of the next one are loaded while this one's go
-      // out.
+      // Lanes 0 .. 7 take a group each: its page and its scales. The codes come by TMA, as many
+      // rows at a time as a page and a tile share (a page that is not there lies past the
+      // pool's end, where rows of zeros are); eight copies for each tile, issued by a lane
+      // each, took 2500 cycles of it. The page of the tile after next and the scales of the
+      // next one are loaded while this one's go out.
       struct At {
         int b, hk, end, t, t1, flags, number;
         bool ok;
@@ -515,31 +516,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       int page0 = page_of(c0), page1 = page_of(c1);
       float2 sc0 = scales_of(c0, page0);
       int tile = 0, segs = 0;  // tiles and segments (with tiles) so far
-      float ref = 1.0f;
+      float ref = 1.0f, inv_ref = 1.0f;
       bool fresh = true;  // the segment's first tile, whose largest is the reference
       bool was_large = false;
       int unit = 0;
       uint32_t used = 0, phases = 0;  // bits of the units' places
       auto copy = [&](const CUtensorMap* map, const At& c, int page) -> bool {
-        const int i = unit;
-        const uint32_t bit = 1u << i;
-        bool ok = true;
-#pragma unroll 1
-        for (int ww = 0; ww < 4 && ok; ++ww)
-          ok = wait(unit_empty + i * 4 + ww, (phases & bit) ? 0u : 1u);
-        if (!ok) return false;
+        const uint32_t bit = 1u << unit;
+        if (!wait(unit_empty + unit, (phases & bit) ? 0u : 1u)) return false;
         phases ^= bit;
         used |= bit;
-        if (lane < 4) tc::mbar_expect_tx(unit_full + i * 4 + lane, C::UNIT);
+        uint8_t* to = unit_at(unit);
+        if (elect_one()) tc::mbar_expect_tx(unit_full + unit, C::UNIT);
         __syncwarp();
-        if (lane < 8) {
-          const bool in = page >= 0 && page < a.s.N;
-          const int row = in ? (page << a.shift) + ((c.t * 128 + lane * 16) & (a.s.P - 1))
-                             : a.s.N << a.shift;
-          tc::tma_load_2d(unit_at(i, lane >> 1) + (lane & 1) * 16 * D, map,
-                          unit_full + i * 4 + (lane >> 1), c.hk * D, row);
+#pragma unroll 1
+        for (int r = 0; r < 128; r += a.box) {
+          const int pg = __shfl_sync(0xffffffffu, page, r >> 4);
+          const int row = (uint32_t)pg < (uint32_t)a.s.N
+                              ? (pg << a.shift) + ((c.t * 128 + r) & (a.s.P - 1))
+                              : a.s.N << a.shift;
+          if (elect_one()) tc::tma_load_2d(to + r * D, map, unit_full + unit, c.hk * D, row);
+          __syncwarp();
         }
-        __syncwarp();
         unit = unit + 1 < (c.flags & kSmall ? C::SMALL_UNITS : C::UNITS) ? unit + 1 : 0;
         return true;
       };
@@ -572,14 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           float top = in && v_ok ? sc0.y : 0.0f;
 #pragma unroll
           for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          ref = top > 0.0f ? top : 1.0f;
+          ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
+          inv_ref = 1.0f / ref;
           fresh = false;
         }
         const float nan = __int_as_float(0x7fc00000);
         float2 group = make_float2(0.0f, 0.0f);
         if (in) {
           group.x = k_ok ? fmaxf(c_scale * sc0.x, 1.17549435e-38f) : nan;
-          group.y = v_ok ? fminf(fmaxf(log2f(sc0.y / ref), -100.0f), 100.0f) : nan;
+          group.y = v_ok ? fminf(fmaxf(log2f(sc0.y * inv_ref), -100.0f), 100.0f) : nan;
         }
         const uint32_t absent = ~__ballot_sync(0xffffffffu, in) & 0xFFu;
         TileConst* out = const_s + tile % kConsts;
@@ -605,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || *abort_flag) {
         // given up: copies in flight land before the CTA ends (a bounded wait)
 #pragma unroll 1
-        for (int i = 0; i < 4 * C::SMALL_UNITS; ++i) {
-          if (!(used >> (i / 4) & 1)) continue;
-          const uint32_t parity = phases >> (i / 4) & 1 ? 0u : 1u;  // of the last copy there
+        for (int i = 0; i < C::SMALL_UNITS; ++i) {
+          if (!(used >> i & 1)) continue;
+          const uint32_t parity = phases >> i & 1 ? 0u : 1u;  // of the last copy there
           for (int n = 0; n < 100000; ++n)
             if (tc::mbar_try_wait(unit_full + i, parity)) break;
         }
@@ -767,9 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the item may not see (`partly`). (The MMA issuer makes them visible to the tensor core.)
     auto spread = [&](bool partly, int key0, int end, int nans) -> bool {
       const uint32_t bit = 1u << unit;
-      if (!wait(unit_full + unit * 4 + ww, (phases & bit) ? 1u : 0u)) return false;
+      if (!wait(unit_full + unit, (phases & bit) ? 1u : 0u)) return false;
       phases ^= bit;
-      const uint4* from = reinterpret_cast<const uint4*>(unit_at(unit, ww)) + lane;
+      const uint4* from = reinterpret_cast<const uint4*>(unit_at(unit) + ww * 32 * D) + lane;
       uint4 x[PASSES];
 #pragma unroll
       for (int u = 0; u < PASSES; ++u) x[u] = from[u * 32];
@@ -780,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           found |= nan_codes(x[u].x) | nan_codes(x[u].y) | nan_codes(x[u].z) | nan_codes(x[u].w);
       }
       const bool odd = __any_sync(0xffffffffu, found != 0);  // (and all have read the unit)
-      if (lane == 0) tc::mbar_arrive(unit_empty + unit * 4 + ww);
+      if (lane == 0) tc::mbar_arrive(unit_empty + unit);
       unit = unit + 1 < (large ? C::UNITS : C::SMALL_UNITS) ? unit + 1 : 0;
       if (!wait(empty + slot, phase)) return false;
       // (rows RPP apart: the swizzle repeats every 8 rows)
@@ -874,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = lane % LPR;
         const int64_t at = (int64_t)(s.row0 + token_of(s)) * a.q_row + (int64_t)(s.hk * a.G + my_head) * D;
         const bool there = is_there(s);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < 32 / RPI; ++i) {
           const int r = i * RPI + lane / LPR;
           const int64_t from = __shfl_sync(0xffffffffu, at, r);
@@ -883,29 +882,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                           a.q + (on ? from : 0) + c * 8, on);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-        uint32_t most = 0;
+        qs = 1.0f;
+        if (__any_sync(0xffffffffu, there)) {  // (rows of zeros are the same in both types)
+          uint32_t most2 = 0;  // two magnitudes' bits, each its own maximum
 #pragma unroll 8
-        for (int i = 0; i < LPR; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(block + Geo::chunk_offset(row, i, 128));
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          for (int i = 0; i < LPR; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(block + Geo::chunk_offset(row, i, 128));
+            most2 = __vmaxu2(most2, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                             __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+          }
+          const uint32_t most = max(most2 << 16, most2 & 0xFFFF0000u);
+          const int ex = max((int)(most >> 23) - 127 - 14, -110);
+          const float inv = sign * __int_as_float((127 - ex) << 23);
+          qs = __int_as_float((ex + 127) << 23);
+#pragma unroll 8
+          for (int i = 0; i < LPR; ++i) {
+            uint4* place = reinterpret_cast<uint4*>(block + Geo::chunk_offset(row, i, 128));
+            const uint4 x = *place;
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+            uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            most = max(most, max((y[e] << 16) & 0x7FFFFFFFu, y[e] & 0x7FFF0000u));
-        }
-        const int ex = max((int)(most >> 23) - 127 - 14, -110);
-        const float inv = sign * __int_as_float((127 - ex) << 23);
-        qs = __int_as_float((ex + 127) << 23);
-#pragma unroll 4
-        for (int i = 0; i < LPR; ++i) {
-          uint4* place = reinterpret_cast<uint4*>(block + Geo::chunk_offset(row, i, 128));
-          const uint4 x = *place;
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = pack_f16(__uint_as_float(y[e] << 16) * inv, __uint_as_float(y[e] & 0xFFFF0000u) * inv);
-          *place = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int e = 0; e < 4; ++e) {
+              float lo = __uint_as_float(y[e] << 16), hi = __uint_as_float(y[e] & 0xFFFF0000u);
+              att::mul2(lo, hi, inv, inv);
+              h[e] = pack_f16(lo, hi);
+            }
+            *place = make_uint4(h[0], h[1], h[2], h[3]);
+          }
         }
         if (small) *told = qs;
       }
@@ -967,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           // The row's reference to at least `top` - 4 where a weight would pass 2^11.
           auto raise = [&](float top) -> bool {
-            const bool over = top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
+            const bool over = there && top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
             if (!__any_sync(0xffffffffu, over)) return true;
             const float to = over ? 4.0f - ceilf(fmaxf(top, -att::kLargest)) : nm;
             const float f = nm == -INFINITY ? 1.0f : ex2(to - nm);
@@ -1001,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = raise(top))) break;
             // Far from 0 the products must be rounded as the maximum was; a row without a
             // score so far (nm = -inf) has no weights: both below.
-            slow = __any_sync(0xffffffffu, fabsf(nm) > 1048576.0f);
+            slow = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f);
             if (!slow) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -1054,7 +1057,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (!(ok = raise(top))) break;
             }
-            // (a masked weight is 0 whatever its group's scale is)
+            // Far from 0 the products are rounded as the maximum was; a row without a score so
+            // far (nm = -inf) is such a row. (A masked weight is 0 whatever its group's scale.)
+            const bool exact = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               float v[32];
@@ -1066,15 +1071,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int h = 0; h < 2; ++h) {
                 const float2 k = group_of(2 * i + h);
                 const float cc = k.x * qs;
-                float sum = 0.0f;
+                float* x = v + 16 * h;
+                if (exact) {
 #pragma unroll
-                for (int j = 16 * h; j < 16 * h + 16; ++j) {
-                  const float x = __fadd_rn(__fadd_rn(__fmul_rn(v[j], cc), k.y), nm);
-                  v[j] = see >> j & 1 ? ex2(x) : 0.0f;
-                  sum += v[j];
-                  if (j & 1) y[j / 2] = pack_f16(v[j - 1], v[j]);
+                  for (int j = 0; j < 16; ++j)
+                    x[j] = __fadd_rn(__fadd_rn(__fmul_rn(x[j], cc), k.y), nm);
+                } else {
+                  const float kb = k.y + nm;
+#pragma unroll
+                  for (int j = 0; j < 16; j += 2) fma2(x[j], x[j + 1], cc, kb, kb);
                 }
-                if (sum != 0.0f) l += sum * ex2(-k.y);
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  x[j] = see >> (16 * h + j) & 1 ? ex2(x[j]) : 0.0f;
+                  x[j + 1] = see >> (16 * h + j + 1) & 1 ? ex2(x[j + 1]) : 0.0f;
+                  add2(s0, s1, x[j], x[j + 1]);
+                  y[8 * h + j / 2] = pack_f16(x[j], x[j + 1]);
+                }
+                if (s0 + s1 != 0.0f) l += (s0 + s1) * (exact ? ex2(-k.y) : ex2(nm - (k.y + nm)));
               }
               tmem_store16(s_addr + 16 * i, y);
             }
@@ -1162,36 +1177,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           f1 *= norm;
           f2 *= norm;
           float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
-          __nv_bfloat16* to_out = a.out + (q_at * Hq + head) * D;
+          const uint64_t to_out = there ? (q_at * Hq + head) * D : 0;
+          uint8_t* stage = smem + C::EPI_OFF + (warp - 4) * 1024;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 16) {
-            float o[16], x[16];
-            tc::tmem_ld16(o_addr + i, o);
-            tc::tmem_ld16(o_addr + (other ? D : 0) + i, x);
-            tc::tmem_wait_ld(o);
-            tc::tmem_wait_ld(x);
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tc::tmem_ld32(o_addr + i, o);
+            if (other) {
+              float x[32];
+              tc::tmem_ld32(o_addr + D + i, x);
+              tc::tmem_wait_ld(o);
+              tc::tmem_wait_ld(x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
-              o[e] += f2 == 0.0f ? 0.0f : x[e] * f2;
+              for (int e = 0; e < 32; ++e)
+                o[e] = (f1 == 0.0f ? 0.0f : o[e] * f1) + (f2 == 0.0f ? 0.0f : x[e] * f2);
+            } else {
+              tc::tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
             }
             if (nan_here) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
+              for (int e = 0; e < 32; ++e)
                 if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
             }
-            if (there && part) {
+            if (part) {
+              if (there) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            } else if (there) {
-#pragma unroll
-              for (int e = 0; e < 16; e += 8)
-                *reinterpret_cast<uint4*>(to_out + i + e) =
-                    make_uint4(att::pack_bf16(o[e], o[e + 1]), att::pack_bf16(o[e + 2], o[e + 3]),
-                               att::pack_bf16(o[e + 4], o[e + 5]), att::pack_bf16(o[e + 6], o[e + 7]));
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
+              __syncwarp();
+              continue;
             }
-            __syncwarp();
+            // 16 rows at a time through shared memory, so that four lanes write 64 bytes of a
+            // row (a lane a row, every store met 32 lines: 8100 cycles an item of 256 rows)
+            uint32_t y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = att::pack_bf16(o[2 * e], o[2 * e + 1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              __syncwarp();
+              if (lane >> 4 == h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4*>(stage + (lane & 15) * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
+                      make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int rr = e * 8 + lane / 4, cc = lane & 3;
+                const uint64_t to = __shfl_sync(0xffffffffu, to_out, h * 16 + rr);
+                const bool on = __shfl_sync(0xffffffffu, (int)there, h * 16 + rr) != 0;
+                const uint4 z = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((cc ^ (rr >> 1 & 3)) << 4));
+                if (on) *reinterpret_cast<uint4*>(a.out + to + i + cc * 8) = z;
+              }
+            }
           }
           if (there) {
             const float m = both == INFINITY ? -INFINITY : both;
@@ -1240,133 +1282,124 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 
 // Parts of an item: number 2c + 1 of the CTA c where it starts, then 2c' + 0 of the CTAs after
-// it, up to the one that ends it (CTAs between may hold none of it).
+// it, up to the one that ends it (CTAs between may hold none of it). kJoinBlocks blocks take
+// the rows of the item that starts in a CTA, if one does that does not end there. Many parts: a
+// block a row, its warps sharing the parts; few: a warp a row.
+constexpr int kJoinBlocks = 32;
+
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a, int ctas) {
   allow_next();
   wait_for_earlier();
   constexpr int WARPS = kJoinThreads / 32, V = D / 32;
-  __shared__ int4 rec[2 * kMaxCtas];
+  __shared__ int last_s;
+  __shared__ uint32_t held[(kMaxCtas + 31) / 32];  // CTAs after c that hold a part
   __shared__ float4 acc_s[WARPS][32];
-  __shared__ float2 ml_s[WARPS];
+  __shared__ float sum_s[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  bool any = false;
-  for (int i = tid; i < 2 * ctas; i += kJoinThreads) {
-    rec[i] = ld_after(a.record + i);
-    any |= (i & 1) && (rec[i].x & kStop);
-  }
-  if (!__syncthreads_or(any)) return;
-  const int Hq = a.Hkv * a.G;
-  int64_t unit = 0;  // rows (or blocks of rows) of the items so far
+  const int c = blockIdx.x / kJoinBlocks, block = blockIdx.x % kJoinBlocks;
+  const int4 first = ld_after(a.record + 2 * c + 1);
+  if (!(first.x & kStop)) return;
+  if (tid == 0) last_s = ctas - 1;
+  __syncthreads();
+  const int i0 = c + 1 + tid;  // (kMaxCtas <= kJoinThreads)
+  const int flags = i0 < ctas ? ld_after(&a.record[2 * i0].x) : 0;
+  if ((flags & kStop) && (flags & kEnds)) atomicMin(&last_s, i0);
+  const uint32_t some = __ballot_sync(0xffffffffu, (flags & kStop) != 0);
+  if (lane == 0 && warp < (int)(sizeof(held) / 4)) held[warp] = some;
+  __syncthreads();
+  const int count = last_s - c;  // CTAs after c, of which held tells
+  auto part_of = [&](int i) -> int {  // i-th CTA from c on; -1: no part
+    if (i == 0) return 2 * c + 1;
+    return held[(i - 1) / 32] >> ((i - 1) % 32) & 1 ? 2 * (c + i) : -1;
+  };
+  const int Hq = a.Hkv * a.G, rows = first.z * a.G;
+  const bool small = first.x & kSmall, wide = count > 8;
+  const int units = wide ? rows : (rows + WARPS - 1) / WARPS;
 #pragma unroll 1
-  for (int c = 0; c < ctas; ++c) {
-    const int4 first = rec[2 * c + 1];
-    if (!(first.x & kStop)) continue;
-    // the CTAs after it that hold parts
-    int last = c + 1, parts = 1;
-    while (last < ctas) {
-      const int4 r = rec[2 * last];
-      if (r.x & kStop) {
-        ++parts;
-        if (r.x & kEnds) break;
+  for (int u = block; u < units; u += kJoinBlocks) {
+    const int x = wide ? u : u * WARPS + warp;  // row of the item
+    const bool on = x < rows;
+    const int token = x / a.G, head = x % a.G;
+    const int half = small || token < a.tokens ? 0 : 1;
+    const size_t r = half * 128 + (token - half * a.tokens) * a.G + head;
+    float top = INFINITY, sum = 0.0f, o[V];  // top: the least -m
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+    if (on) {
+      for (int i = lane; i <= count; i += 32) {
+        const int part = part_of(i);
+        if (part < 0) continue;
+        const float m = ld_after(&a.ml[part * (size_t)a.rows + r].y);
+        if (m > -INFINITY) top = fminf(top, m);
       }
-      ++last;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+#pragma unroll 8
+      for (int i = wide ? warp : 0; i <= count; i += wide ? WARPS : 1) {
+        const int part = part_of(i);
+        if (part < 0) continue;
+        const float2 m = ld_after(a.ml + part * (size_t)a.rows + r);
+        const float* y = a.part + (part * (size_t)a.rows + r) * D + lane * V;
+        float z[V];
+        if constexpr (V == 4) {
+          const float4 t = ld_after(reinterpret_cast<const float4*>(y));
+          z[0] = t.x, z[1] = t.y, z[2] = t.z, z[3] = t.w;
+        } else {
+          const float2 t = ld_after(reinterpret_cast<const float2*>(y));
+          z[0] = t.x, z[1] = t.y;
+        }
+        // a part without rows counts nothing, but its NaN columns do
+        const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
+        sum += m.x * f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
+      }
     }
-    const bool wide = parts > 8;  // a block a row, its warps sharing the parts; else a warp a row
-    const bool small = first.x & kSmall;
-    const int rows = first.z * a.G;
-    const int64_t units = wide ? rows : (rows + WARPS - 1) / WARPS;
-    // this block's units of the item: unit + u = blockIdx.x modulo the grid
-    int64_t u = (int64_t)blockIdx.x - unit % gridDim.x;
-    if (u < 0) u += gridDim.x;
-    unit += units;
-#pragma unroll 1
-    for (; u < units; u += gridDim.x) {
-      const int x = wide ? (int)u : (int)u * WARPS + warp;  // row of the item
-      const bool on = x < rows;
-      const int token = x / a.G, head = x % a.G;
-      const int block = small || token < a.tokens ? 0 : 1;
-      const int r = block * 128 + (token - block * a.tokens) * a.G + head;
-      float top = INFINITY, sum = 0.0f, o[V];  // top: the least -m
+    if (wide) {
+      __syncthreads();
+      acc_s[warp][lane] = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
+      if (lane == 0) sum_s[warp] = sum;
+      __syncthreads();
+      if (warp) continue;
+      sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = 0.0f;
-      if (on) {
-        // the parts' references first, lanes taking parts
-        for (int i = c + lane; i <= last && i < ctas; i += 32) {
-          const int part = i == c ? 2 * c + 1 : 2 * i;
-          if (!(rec[part].x & kStop)) continue;
-          const float2 m = ld_after(a.ml + (size_t)part * a.rows + r);
-          if (m.y > -INFINITY) top = fminf(top, m.y);
-        }
 #pragma unroll
-        for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
-#pragma unroll 4
-        for (int i = c + (wide ? warp : 0); i <= last && i < ctas; i += wide ? WARPS : 1) {
-          const int part = i == c ? 2 * c + 1 : 2 * i;
-          if (!(rec[part].x & kStop)) continue;
-          const float2 m = ld_after(a.ml + (size_t)part * a.rows + r);
-          const float* y = a.part + ((size_t)part * a.rows + r) * D + lane * V;
-          float z[V];
-          if constexpr (V == 4) {
-            const float4 t = ld_after(reinterpret_cast<const float4*>(y));
-            z[0] = t.x, z[1] = t.y, z[2] = t.z, z[3] = t.w;
-          } else {
-            const float2 t = ld_after(reinterpret_cast<const float2*>(y));
-            z[0] = t.x, z[1] = t.y;
-          }
-          // a part without rows counts nothing, but its NaN columns do
-          const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
-          sum += m.x * f;
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
+      for (int i = 0; i < WARPS; ++i) {
+        const float4 t = acc_s[i][lane];
+        o[0] += t.x;
+        o[1] += t.y;
+        if constexpr (V > 2) {
+          o[2] += t.z;
+          o[3] += t.w;
         }
+        sum += sum_s[i];
       }
-      if (wide) {
-        __syncthreads();
-        float4 t = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
-        acc_s[warp][lane] = t;
-        if (lane == 0) ml_s[warp] = make_float2(sum, 0.0f);
-        __syncthreads();
-        if (warp) continue;
-        sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < WARPS; ++i) {
-          t = acc_s[i][lane];
-          o[0] += t.x;
-          o[1] += t.y;
-          if constexpr (V > 2) {
-            o[2] += t.z;
-            o[3] += t.w;
-          }
-          sum += ml_s[i].x;
-        }
-      }
-      if (!on) continue;
-      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] *= norm;
-      const size_t at = (size_t)(first.y + token) * Hq + first.w * a.G + head;
-      if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(a.out + at * D + lane * V) =
-            make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));
-      else
-        *reinterpret_cast<uint32_t*>(a.out + at * D + lane * V) = att::pack_bf16(o[0], o[1]);
-      if (a.lse && lane == 0)
-        a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
     }
+    if (!on) continue;
+    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= norm;
+    const size_t at = (size_t)(first.y + token) * Hq + first.w * a.G + head;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(a.out + at * D + lane * V) =
+          make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));
+    else
+      *reinterpret_cast<uint32_t*>(a.out + at * D + lane * V) = att::pack_bf16(o[0], o[1]);
+    if (a.lse && lane == 0)
+      a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
   }
 }
 
 template <class C>
 cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) {
   auto kernel = k_attend_pages<C>;
-  // 16 rows of one head of a pool [N P rows, Hkv d]
+  // rows of one head of a pool [N P rows, Hkv d]
   CUtensorMap k_map, v_map;
   const uint64_t rows = (uint64_t)a.s.N * a.s.P;
-  if (!make_tmap_2d(&k_map, a.k, 1, (uint64_t)a.Hkv * C::D, rows, C::D, 16, 0) ||
-      !make_tmap_2d(&v_map, a.v, 1, (uint64_t)a.Hkv * C::D, rows, C::D, 16, 0))
+  if (!make_tmap_2d(&k_map, a.k, 1, (uint64_t)a.Hkv * C::D, rows, C::D, a.box, 0) ||
+      !make_tmap_2d(&v_map, a.v, 1, (uint64_t)a.Hkv * C::D, rows, C::D, a.box, 0))
     return cudaErrorInvalidValue;
   static unsigned long long opted_in = 0;
   static int regs_ok = 0;
@@ -1383,7 +1416,8 @@ cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) 
         return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
   if (e != cudaSuccess) return e;
-  return launch_early(k_join_parts<C::D>, 2u * (unsigned)ctas, kJoinThreads, 0, st, 1, a, ctas);
+  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * kJoinBlocks), kJoinThreads, 0, st, 1, a,
+                      ctas);
 }
 
 }  // namespace pages
