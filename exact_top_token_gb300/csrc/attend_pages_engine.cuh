@@ -18,8 +18,8 @@
 // group's scores, and v's, as b = log2(v_scale / reference), a summand of its exponents. The
 // weights 2^(s + b - m) are what is rounded to f16 and multiplied with the codes; their sum
 // over a group times 2^-b is the group's share of the softmax's denominator. m is at least
-// the largest s + b of the first tiles less 4, and is raised, with O scaled, when a weight
-// would pass 2^11: weights have 11 bits down to 2^-18 of the largest product with v's scale
+// the largest s + b of an item's first tile less 4, and is raised, with O and the tile's
+// weights so far scaled, when a weight would pass 2^11: weights have 11 bits down to 2^-18 of the largest product with v's scale
 // and an error of 2^-29 of it below. m is a whole number, so that s + (b - m) is rounded
 // once. Queries are taken to f16 with a power of two out of each row.
 //
@@ -57,6 +57,7 @@ constexpr int kOverhead = 8;   // of an item, in the units below
 constexpr int kSegs = 8;       // ring of segments
 constexpr int kConsts = 16;    // ring of the tiles' scales
 constexpr int kThreads = 512;
+constexpr int kBlock = 4;      // groups of 16 keys that the softmax takes at a time
 // Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 184 + 80) = 65536.
 constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 184, kRegsWide = 80;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
@@ -73,7 +74,7 @@ enum : int { kStop = 1, kSmall = 2, kStarts = 4, kEnds = 8 };
 struct TileConst {
   float4 group[4];  // of two groups: factor of the scores, b
   float ref;        // reference of v's scales
-  uint32_t absent;  // groups that are not there
+  uint32_t absent;  // groups of the contexts' rows that are not there
   uint32_t pad[2];
 };
 
@@ -131,6 +132,26 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
+// two f16 products
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   addr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -575,12 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           fresh = false;
         }
         const float nan = __int_as_float(0x7fc00000);
-        float2 group = make_float2(0.0f, 0.0f);
+        // (masked keys: any factor will do)
+        const bool past = c0.t * 128 + (lane & 7) * 16 >= c0.end;
+        float2 group = make_float2(1.0f, 0.0f);
         if (in) {
           group.x = k_ok ? fmaxf(c_scale * sc0.x, 1.17549435e-38f) : nan;
           group.y = v_ok ? fminf(fmaxf(log2f(sc0.y * inv_ref), -100.0f), 100.0f) : nan;
         }
-        const uint32_t absent = ~__ballot_sync(0xffffffffu, in) & 0xFFu;
+        const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past) & 0xFFu;
         TileConst* out = const_s + tile % kConsts;
         if (lane < 8) reinterpret_cast<float2*>(out->group)[lane] = group;
         if (lane == 0) {
@@ -611,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tc::mbar_try_wait(unit_full + i, parity)) break;
         }
       }
-    } else if (warp == 0) {
+    } else if (warp == 3) {
       // ---------------- MMA issuer ----------------
       // The whole warp waits and keeps the state, all of it in uniform registers (numbers
       // of a segment come through a shuffle, so that the compiler knows): descriptors that
@@ -640,109 +663,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_async_smem();  // of all that was stored into the ring
         return ok;
       };
-      // Scores of a warpgroup, of query block qb; `release`: the tile's slot is free after
-      // them, `last`: so are the queries. What the softmax waits for is committed last:
-      // nothing arrives after a CTA's end.
-      auto scores = [&](auto wg, auto qb, bool release, bool last) {
-        constexpr int W = decltype(wg)::value, Q = decltype(qb)::value;
-        tc::fence_after_sync();
-        const uint32_t ad = (q_lo + Q * (C::SLOT >> 4)) | LBO_K;
-        const uint32_t bd = (ring_lo + k.slot * (C::SLOT >> 4)) | LBO_K;
-        if (elect_one()) {
-#pragma unroll
-          for (int j = 0; j < C::RB / 32; ++j)
-            tc::mma<0>(tmem + C::S_COL + W * 128, desc(ad + (Geo::step_offset(j, 128) >> 4)),
-                       desc(bd + (Geo::step_offset(j, 128) >> 4)), ID_S, j > 0 ? 1u : 0u);
-          if (release) tc::mma_commit(empty + k.slot);
-          if (last) tc::mma_commit(q_empty);
-          tc::mma_commit(s_full + W);
-        }
-        __syncwarp();
-      };
-      uint32_t phase0 = 0, phase1 = 0;  // of the weights of each warpgroup
-      auto weights = [&](auto wg) {
-        constexpr int W = decltype(wg)::value;
-        uint32_t& phase = W ? phase1 : phase0;
-        const bool ok = wait(p_full + W, phase);
-        phase ^= 1u;
-        return ok;
-      };
-      auto products = [&](auto wg, bool add, bool release) {
-        constexpr int W = decltype(wg)::value;
-        tc::fence_after_sync();
-        const uint32_t bd = (ring_lo + v.slot * (C::SLOT >> 4)) | LBO_MN;
-        const uint32_t first = add ? 1u : 0u;
-        if (elect_one()) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)  // 16 keys
-            mma_ts(tmem + C::O_COL + W * D, tmem + C::S_COL + W * 128 + j * 8,
-                   desc(bd + (j * 2048 >> 4)), ID_O, j > 0 ? 1u : first);
-          if (release) tc::mma_commit(empty + v.slot);
-          tc::mma_commit(pv_done + W);
-        }
-        __syncwarp();
-      };
-      constexpr att::Int<0> g0{};
-      constexpr att::Int<1> g1{};
-      uint32_t odd = 0;  // segments with tiles so far, modulo 2
+      uint32_t p_phase = 0;  // bits: of the weights of each warpgroup
+      uint32_t odd = 0;      // segments with tiles so far, modulo 2
       Seg s;
+      bool ok = true;
 #pragma unroll 1
-      for (int number = 0; take(number, s) && !(s.flags & kStop); ++number) {
+      for (int number = 0; ok && take(number, s) && !(s.flags & kStop); ++number) {
         const int T = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0);
         const bool small = __shfl_sync(0xffffffffu, s.flags & kSmall, 0) != 0;
         if (T == 0) continue;
-        bool ok = wait(q_full, odd) && landed(k);
-        if (!ok) break;
-        if (small) {
-          // tile t is warpgroup t % 2's
-          scores(g0, g0, true, T == 1);
-          step(k);
-          if (T > 1) {
-            if (!landed(k)) break;
-            scores(g1, g0, true, T == 2);
-            step(k);
-          }
-          auto tile = [&](auto wg, int t) -> bool {
-            if (!weights(wg) || (t == 0 && !wait(o_empty, odd ^ 1u)) || !landed(v)) return false;
-            products(wg, t >= 2, true);
-            step(v);
-            if (t + 2 < T) {
-              if (!landed(k)) return false;
-              scores(wg, g0, true, t + 3 == T);
-              step(k);
-            }
-            return true;
-          };
+        // Step i is warpgroup i % 2's: the products of its tile, then the scores of its next
+        // one (which take the place of the weights). Of a large item both have every tile,
+        // of a small one every other.
+        const int N = small ? T : 2 * T;
+        if (!(ok = wait(q_full, odd))) break;
 #pragma unroll 1
-          for (int t = 0; t < T; t += 2) {
-            if (!(ok = tile(g0, t))) break;
-            if (t + 1 < T && !(ok = tile(g1, t + 1))) break;
+        for (int i = -2; i < N; ++i) {
+          const int w = i & 1;
+          const bool first = small || w == 0, last = small || w == 1;  // with this K or V
+          if (i >= 0) {
+            if (!(ok = wait(p_full + w, p_phase >> w & 1u))) break;
+            p_phase ^= 1u << w;
+            if (i == 0 && !(ok = wait(o_empty, odd ^ 1u))) break;
+            if (first && !(ok = landed(v))) break;
+            tc::fence_after_sync();
+            const uint32_t bd = (ring_lo + v.slot * (C::SLOT >> 4)) | LBO_MN;
+            const uint32_t add = i >= 2 ? 1u : 0u;
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)  // 16 keys
+                mma_ts(tmem + C::O_COL + w * D, tmem + C::S_COL + w * 128 + j * 8,
+                       desc(bd + (j * 2048 >> 4)), ID_O, j > 0 ? 1u : add);
+              // (what the softmax waits for is committed last: nothing arrives after a CTA's end)
+              if (last) tc::mma_commit(empty + v.slot);
+              tc::mma_commit(pv_done + w);
+            }
+            __syncwarp();
+            if (last) step(v);
           }
-        } else {
-          scores(g0, g0, false, false);
-          scores(g1, g1, true, T == 1);
-          step(k);
-#pragma unroll 1
-          for (int t = 0; t < T; ++t) {
-            if (!(ok = weights(g0))) break;
-            if (t == 0 && !(ok = wait(o_empty, odd ^ 1u))) break;
-            if (!(ok = landed(v))) break;
-            products(g0, t > 0, false);
-            const bool more = t + 1 < T;
-            if (more) {
-              if (!(ok = landed(k))) break;
-              scores(g0, g0, false, false);
+          if (i + 2 < N) {
+            if (first && !(ok = landed(k))) break;
+            tc::fence_after_sync();
+            const uint32_t ad = (q_lo + (small ? 0 : w) * (C::SLOT >> 4)) | LBO_K;
+            const uint32_t bd = (ring_lo + k.slot * (C::SLOT >> 4)) | LBO_K;
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < C::RB / 32; ++j)
+                tc::mma<0>(tmem + C::S_COL + w * 128, desc(ad + (Geo::step_offset(j, 128) >> 4)),
+                           desc(bd + (Geo::step_offset(j, 128) >> 4)), ID_S, j > 0 ? 1u : 0u);
+              if (last) tc::mma_commit(empty + k.slot);
+              if (i + 3 == N) tc::mma_commit(q_empty);
+              tc::mma_commit(s_full + w);
             }
-            if (!(ok = weights(g1))) break;
-            products(g1, t > 0, true);
-            step(v);
-            if (more) {
-              scores(g1, g1, true, t + 2 == T);
-              step(k);
-            }
+            __syncwarp();
+            if (last) step(k);
           }
         }
-        if (!ok) break;
         odd ^= 1u;
       }
     }
@@ -845,8 +821,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ---------------- softmax: TMEM lane = row ----------------
-    // The roles share one instruction cache, so only a tile that every row sees whole is
-    // straight code; the others are loops.
+    // What bounds a tile is how fast instructions come: a tile as straight code took 2200
+    // cycles here for 560 instructions, and slowed the other roles, a second copy of the
+    // widening warps' loop alone 1.4 times. So all that runs per tile is a short loop.
     const int w = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + C::S_COL + w * 128;
@@ -873,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = lane % LPR;
         const int64_t at = (int64_t)(s.row0 + token_of(s)) * a.q_row + (int64_t)(s.hk * a.G + my_head) * D;
         const bool there = is_there(s);
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < 32 / RPI; ++i) {
           const int r = i * RPI + lane / LPR;
           const int64_t from = __shfl_sync(0xffffffffu, at, r);
@@ -895,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ex = max((int)(most >> 23) - 127 - 14, -110);
           const float inv = sign * __int_as_float((127 - ex) << 23);
           qs = __int_as_float((ex + 127) << 23);
-#pragma unroll 8
+#pragma unroll 4
           for (int i = 0; i < LPR; ++i) {
             uint4* place = reinterpret_cast<uint4*>(block + Geo::chunk_offset(row, i, 128));
             const uint4 x = *place;
@@ -945,153 +922,165 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int number_c = tile0 + t - s.t0;
         const TileConst* tile = const_s + number_c % kConsts;
         if (!(ok = wait(c_full + number_c % kConsts, (number_c / kConsts) & 1))) break;
-        const float4 g0 = tile->group[0], g1 = tile->group[1], g2 = tile->group[2], g3 = tile->group[3];
         ref = tile->ref;
         const uint32_t absent = tile->absent;
         if (!(ok = wait(s_full + w, cnt & 1))) break;
         tc::fence_after_sync();
         if (warp_there) {
-          const float2 groups[8] = {{g0.x, g0.y}, {g0.z, g0.w}, {g1.x, g1.y}, {g1.z, g1.w},
-                                    {g2.x, g2.y}, {g2.z, g2.w}, {g3.x, g3.y}, {g3.z, g3.w}};
-          auto group_of = [&](int g) {  // (of a loop: from shared memory)
-            return reinterpret_cast<const float2*>(tile->group)[g];
-          };
-          // (uniform in the warpgroup) some key is not seen by some row
-          const bool masked = absent != 0 || t * 128 + 127 > p_first;
-          // Groups of 16 keys: their largest score with b added.
-          auto top_of = [&](const float2& k, const float* x) {
-            float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
-            m0 = max3(m0, x[6], x[7]);
-            m1 = max3(m1, x[8], x[9]);
-            m0 = max3(m0, x[10], x[11]);
-            m1 = max3(m1, x[12], x[13]);
-            m0 = max3(m0, x[14], x[15]);
-            return __fadd_rn(__fmul_rn(fmaxf(m0, m1), k.x * qs), k.y);
-          };
-          // The row's reference to at least `top` - 4 where a weight would pass 2^11.
-          auto raise = [&](float top) -> bool {
-            const bool over = there && top > -INFINITY && (nm == -INFINITY || top + nm > 11.0f);
-            if (!__any_sync(0xffffffffu, over)) return true;
-            const float to = over ? 4.0f - ceilf(fmaxf(top, -att::kLargest)) : nm;
-            const float f = nm == -INFINITY ? 1.0f : ex2(to - nm);
+          const int seen = p - t * 128;  // the tile's keys up to this one
+          // (uniform in the warp) some key is not seen by some row, or not there
+          const bool masked = t * 128 + 127 > p_first || absent != 0;
+          auto upto = [&](int g) { return absent >> g & 1 ? -1 : seen - 16 * g; };
+          // m by `by` more (whole numbers), where that is not 0; the tile's weights so far are
+          // those of `done` blocks.
+          auto raise = [&](float by, int done) -> bool {
+            const float f = ex2(-by);
             l *= f;
-            nm = to;
-            if (mine == 0) return true;
-            if (!wait(pv_done + w, (cnt - 1) & 1)) return false;
-            tc::fence_after_sync();
+            nm -= by;
+            const uint32_t f2 = pack_f16(f, f);
+            tc::tmem_wait_st();
 #pragma unroll 1
-            for (int i = 0; i < D; i += 8) {
-              float o[8];
-              att::tmem_load(o_addr + i, o);
+            for (int i = 0; i < 16 * done; i += 8) {
+              uint32_t y[8];
+              tmem_load8(s_addr + i, y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= f;
-              att::tmem_store8(o_addr + i, o);
+              for (int e = 0; e < 8; ++e) y[e] = mul_f16(y[e], f2);
+              tmem_store8(s_addr + i, y);
+            }
+            if (mine > 0) {
+              if (!wait(pv_done + w, (cnt - 1) & 1)) return false;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 8) {
+                float o[8];
+                att::tmem_load(o_addr + i, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= f;
+                att::tmem_store8(o_addr + i, o);
+              }
             }
             tc::tmem_wait_st();
             return true;
           };
-          bool slow = masked;
-          if (!masked) {
-            float v[2][64];
-            tc::tmem_ld64(s_addr, v[0]);
-            tc::tmem_ld64(s_addr + 64, v[1]);
-            tc::tmem_wait_ld(v[0]);
-            tc::tmem_wait_ld(v[1]);
+          bool exact = __any_sync(0xffffffffu, there && !(fabsf(nm) <= 1048576.0f));
+          if (exact) {
+            // Rows without a reference (the item's first tile), or far from 0: the maximum of
+            // the whole tile first.
             float top = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < 8; ++g) {
+              float v[16];
+              tc::tmem_ld16(s_addr + 16 * g, v);
+              tc::tmem_wait_ld(v);
+              const float2 k = reinterpret_cast<const float2*>(tile->group)[g];
+              if (masked) {
+                const int last = upto(g);
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-              top = fmaxf(top, top_of(groups[g], v[g / 4] + g % 4 * 16));
-            if (!(ok = raise(top))) break;
-            // Far from 0 the products must be rounded as the maximum was; a row without a
-            // score so far (nm = -inf) has no weights: both below.
-            slow = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f);
-            if (!slow) {
+                for (int j = 0; j < 16; ++j) v[j] = j <= last ? v[j] : -INFINITY;
+              }
+              float m0 = max3(v[0], v[1], v[2]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int j = 3; j < 15; j += 2) m0 = max3(m0, v[j], v[j + 1]);
+              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(m0, v[15]), k.x * qs), k.y));
+            }
+            const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
+            const bool none = nm == -INFINITY, over = there && top > -INFINITY && (none || top + nm > 11.0f);
+            if (__any_sync(0xffffffffu, over && !none)) {
+              if (!(ok = raise(over && !none ? nm - to : 0.0f, 0))) break;
+            }
+            if (over) nm = to;
+            exact = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f && nm > -INFINITY);
+          }
+          if (!exact) {
+#pragma unroll 1
+            for (int i = 0; i < 8; i += kBlock) {  // groups
+              float v[kBlock / 2][32], c[kBlock], kb[kBlock];
+#pragma unroll
+              for (int h = 0; h < kBlock / 2; ++h) tc::tmem_ld32(s_addr + 16 * i + 32 * h, v[h]);
+#pragma unroll
+              for (int h = 0; h < kBlock / 2; ++h) {
+                const float4 k = tile->group[i / 2 + h];
+                c[2 * h] = k.x * qs;
+                kb[2 * h] = k.y + nm;
+                c[2 * h + 1] = k.z * qs;
+                kb[2 * h + 1] = k.w + nm;
+              }
+#pragma unroll
+              for (int h = 0; h < kBlock / 2; ++h) tc::tmem_wait_ld(v[h]);
+              float most[kBlock];
+#pragma unroll
+              for (int g = 0; g < kBlock; ++g) {
+                float* x = v[g / 2] + g % 2 * 16;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) fma2(x[j], x[j + 1], c[g], kb[g], kb[g]);
+                if (masked) {
+                  const int last = upto(i + g);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) x[j] = j <= last ? x[j] : -INFINITY;
+                }
+                float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+                m0 = max3(m0, x[6], x[7]);
+                m1 = max3(m1, x[8], x[9]);
+                m0 = max3(m0, x[10], x[11]);
+                m1 = max3(m1, x[12], x[13]);
+                most[g] = fmaxf(max3(m0, x[14], x[15]), m1);
+              }
+              float top = most[0];
+#pragma unroll
+              for (int g = 1; g + 1 < kBlock; g += 2) top = max3(top, most[g], most[g + 1]);
+              top = fmaxf(top, most[kBlock - 1]);
+              // (what was added to a group's scores is taken out of its sum)
+#pragma unroll
+              for (int g = 0; g < kBlock; ++g) kb[g] = nm - kb[g];
+              if (__any_sync(0xffffffffu, there && top > 11.0f)) {
+                const float by = there && top > 11.0f ? ceilf(top) - 4.0f : 0.0f;
+                if (!(ok = raise(by, i / 2))) break;
+#pragma unroll
+                for (int j = 0; j < 16 * kBlock; ++j) v[j / 32][j % 32] -= by;
+              }
+#pragma unroll
+              for (int h = 0; h < kBlock / 2; ++h) {
                 uint32_t y[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float2 k = groups[2 * i + h];
-                  const float cc = k.x * qs, kb = k.y + nm;
-                  float* x = v[i / 2] + i % 2 * 32 + 16 * h;
-                  float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                for (int g = 0; g < 2; ++g) {
+                  float* x = v[h] + 16 * g;
+                  float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-                  for (int j = 0; j < 16; j += 4) {
-                    fma2(x[j], x[j + 1], cc, kb, kb);
-                    fma2(x[j + 2], x[j + 3], cc, kb, kb);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[j + e] = ex2(x[j + e]);
+                  for (int j = 0; j < 16; j += 2) {
+                    x[j] = ex2(x[j]);
+                    x[j + 1] = ex2(x[j + 1]);
                     add2(s0, s1, x[j], x[j + 1]);
-                    add2(s2, s3, x[j + 2], x[j + 3]);
-                    y[8 * h + j / 2] = pack_f16(x[j], x[j + 1]);
-                    y[8 * h + j / 2 + 1] = pack_f16(x[j + 2], x[j + 3]);
+                    y[8 * g + j / 2] = pack_f16(x[j], x[j + 1]);
                   }
-                  l += ((s0 + s1) + (s2 + s3)) * ex2(nm - kb);
+                  // (a row without a score so far has nm = -inf and no weights)
+                  const float sum = s0 + s1, share = sum * ex2(kb[2 * h + g]);
+                  l += sum != 0.0f ? share : 0.0f;
                 }
-                tmem_store16(s_addr + 16 * i, y);
+                tmem_store16(s_addr + 8 * i + 16 * h, y);
               }
             }
-          }
-          if (slow) {
-            // keys that the row sees, of 32 at a time, as bits
-            auto seen = [&](int i) -> uint32_t {
-              if (!masked) return ~0u;
-              const int upto = p - (t * 128 + i * 32) + 1;
-              uint32_t m = upto <= 0 ? 0u : upto >= 32 ? ~0u : (1u << upto) - 1u;
-              if (absent >> (2 * i) & 1) m &= 0xFFFF0000u;
-              if (absent >> (2 * i + 1) & 1) m &= 0x0000FFFFu;
-              return m;
-            };
-            if (masked) {
-              float top = -INFINITY;
+            if (!ok) break;
+          } else {
+            // far from 0: products rounded as the maximum was
 #pragma unroll 1
-              for (int i = 0; i < 4; ++i) {
-                float v[32];
-                tc::tmem_ld32(s_addr + 32 * i, v);
-                tc::tmem_wait_ld(v);
-                const uint32_t see = seen(i);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = see >> j & 1 ? v[j] : -INFINITY;
-                top = fmaxf(top, top_of(group_of(2 * i), v));
-                top = fmaxf(top, top_of(group_of(2 * i + 1), v + 16));
-              }
-              if (!(ok = raise(top))) break;
-            }
-            // Far from 0 the products are rounded as the maximum was; a row without a score so
-            // far (nm = -inf) is such a row. (A masked weight is 0 whatever its group's scale.)
-            const bool exact = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f);
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              float v[32];
-              uint32_t y[16];
-              tc::tmem_ld32(s_addr + 32 * i, v);
+            for (int g = 0; g < 8; ++g) {
+              float v[16];
+              tc::tmem_ld16(s_addr + 16 * g, v);
               tc::tmem_wait_ld(v);
-              const uint32_t see = seen(i);
+              const float2 k = reinterpret_cast<const float2*>(tile->group)[g];
+              const int last = masked ? upto(g) : 15;
+              const float cc = k.x * qs;
+              float sum = 0.0f;
+              uint32_t y[8];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float2 k = group_of(2 * i + h);
-                const float cc = k.x * qs;
-                float* x = v + 16 * h;
-                if (exact) {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j)
-                    x[j] = __fadd_rn(__fadd_rn(__fmul_rn(x[j], cc), k.y), nm);
-                } else {
-                  const float kb = k.y + nm;
-#pragma unroll
-                  for (int j = 0; j < 16; j += 2) fma2(x[j], x[j + 1], cc, kb, kb);
-                }
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  x[j] = see >> (16 * h + j) & 1 ? ex2(x[j]) : 0.0f;
-                  x[j + 1] = see >> (16 * h + j + 1) & 1 ? ex2(x[j + 1]) : 0.0f;
-                  add2(s0, s1, x[j], x[j + 1]);
-                  y[8 * h + j / 2] = pack_f16(x[j], x[j + 1]);
-                }
-                if (s0 + s1 != 0.0f) l += (s0 + s1) * (exact ? ex2(-k.y) : ex2(nm - (k.y + nm)));
+              for (int j = 0; j < 16; ++j) {
+                v[j] = ex2(__fadd_rn(__fadd_rn(__fmul_rn(v[j], cc), k.y), nm));
+                v[j] = j <= last ? v[j] : 0.0f;
+                sum += v[j];
+                if (j & 1) y[j / 2] = pack_f16(v[j - 1], v[j]);
               }
-              tmem_store16(s_addr + 16 * i, y);
+              if (sum != 0.0f) l += sum * ex2(-k.y);
+              tmem_store8(s_addr + 8 * g, y);
             }
           }
           tc::tmem_wait_st();
@@ -1183,29 +1172,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < D; i += 32) {
             float o[32];
             tc::tmem_ld32(o_addr + i, o);
+            tc::tmem_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) att::mul2(o[e], o[e + 1], f1, f1);
             if (other) {
               float x[32];
               tc::tmem_ld32(o_addr + D + i, x);
-              tc::tmem_wait_ld(o);
               tc::tmem_wait_ld(x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = (f1 == 0.0f ? 0.0f : o[e] * f1) + (f2 == 0.0f ? 0.0f : x[e] * f2);
-            } else {
-              tc::tmem_wait_ld(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = f1 == 0.0f ? 0.0f : o[e] * f1;
-            }
-            if (nan_here) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (nans[i + e] <= p) o[e] = __int_as_float(0x7fc00000);
+              for (int e = 0; e < 32; e += 2) {
+                fma2(x[e], x[e + 1], f2, o[e], o[e + 1]);
+                o[e] = x[e];
+                o[e + 1] = x[e + 1];
+              }
             }
             if (part) {
               if (there) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                   *reinterpret_cast<float4*>(to_part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                if (nan_here) {
+#pragma unroll 1
+                  for (int e = i; e < i + 32; ++e)
+                    if (nans[e] <= p) to_part[e] = __int_as_float(0x7fc00000);
+                }
               }
               __syncwarp();
               continue;
@@ -1223,6 +1213,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e)
                   *reinterpret_cast<uint4*>(stage + (lane & 15) * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
                       make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                if (nan_here) {
+#pragma unroll 1
+                  for (int e = 0; e < 32; ++e)
+                    if (nans[i + e] <= p)
+                      *reinterpret_cast<uint16_t*>(stage + (lane & 15) * 64 +
+                                                   (((e >> 3) ^ (lane >> 1 & 3)) << 4) + (e & 7) * 2) = 0x7FC0;
+                }
               }
               __syncwarp();
 #pragma unroll
