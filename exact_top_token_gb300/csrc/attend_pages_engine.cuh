@@ -51,13 +51,12 @@ using att::elect_one;
 using att::ex2;
 using att::fma2;
 using att::max3;
-using att::wait_bar;
 
 constexpr int kOverhead = 8;   // of an item, in the units below
 constexpr int kSegs = 8;       // ring of segments
 constexpr int kConsts = 16;    // ring of the tiles' scales
 constexpr int kThreads = 512;
-constexpr int kBlock = 2;      // groups of 16 keys that the softmax takes at a time
+constexpr int kBlock = 4;      // groups of 16 keys that the softmax takes at a time
 // Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 184 + 80) = 65536.
 constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 184, kRegsWide = 80;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
@@ -101,7 +100,7 @@ struct PCfg {
   static constexpr int CONST_OFF = NAN_OFF + NANS * 2 * D * 4;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
-  static constexpr int QS_OFF = ML_OFF + 256 * 8;
+  static constexpr int QS_OFF = ML_OFF + 128 * 8;
   static constexpr int EPI_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;  // [8 warps][1 KB]
   static constexpr int BAR_OFF = EPI_OFF + 8 * 1024;
   static constexpr int SMEM = BAR_OFF + 768 + 1024;
@@ -318,6 +317,24 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
 
 // ---- the kernel -------------------------------------------------------------------------
 
+// Wait for a phase of `bar`; gives up (false, abort flag) when another role has, or after
+// kTries tests of at most 2 us each. As few instructions as that takes: the code of all
+// roles shares one instruction cache, and there are forty waits. (The status bit is set at
+// the kernel's end.)
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t abort_at) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 n, f;\n mov.b32 n, 0;\n"
+      "W_:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra D_;\n"
+      " ld.volatile.shared.b32 f, [%4];\n add.u32 n, n, 1;\n setp.ne.b32 q, f, 0;\n"
+      " setp.gt.or.u32 q, n, %5, q;\n @!q bra W_;\n st.volatile.shared.b32 [%4], 1;\n"
+      "D_:\n selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(tc::kSuspendHintNs), "r"(abort_at), "n"(att::kTries)
+      : "memory");
+  return ok != 0;
+}
+
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_pages(const AttendArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -342,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_empty = q_empty + 1;
   uint64_t* ml_full = o_empty + 1;    // the second warpgroup's sums (small items)
   uint64_t* ml_empty = ml_full + 1;
-  uint64_t* all_here = ml_empty + 1;  // the softmax warps, at the end of an item of few rows
-  uint64_t* seg_full = all_here + 1;  // [kSegs]
+  uint64_t* seg_full = ml_empty + 1;  // [kSegs]
   uint64_t* seg_empty = seg_full + kSegs;
   uint64_t* c_full = seg_empty + kSegs;       // [kConsts] scales of a tile
   uint64_t* unit_full = c_full + kConsts;     // [SMALL_UNITS] codes
@@ -372,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(o_empty, 8);
     tc::mbar_init(ml_full, 4);
     tc::mbar_init(ml_empty, 4);
-    tc::mbar_init(all_here, 8);
     for (int i = 0; i < kSegs; ++i) {
       tc::mbar_init(seg_full + i, 1);
       tc::mbar_init(seg_empty + i, 1 + 1 + 8 + 4);
@@ -400,8 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_share(a, scan_s, share);
   __syncthreads();
 
+  const uint32_t abort_at = tc::smem_u32(tmem_slot + 1);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, a.status)) != 0;
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_at)) != 0;
   };
   // The number-th segment, taken out of the ring (each role, in order); false after a failed
   // wait.
@@ -830,29 +846,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + C::S_COL + w * 128;
     const uint32_t o_addr = tmem + lane_off + C::O_COL + w * D;
-    const int Hq = a.Hkv * a.G;
+    const int my_token = row / a.G, my_head = row % a.G, Hq = a.Hkv * a.G;
     const float sign = a.scale < 0.0f ? -1.0f : a.scale == 0.0f ? 0.0f : 1.0f;
-    // A segment for this thread. An item of at most 32 or 64 rows has them four or two times
-    // over, 32 or 64 lanes apart, and each copy takes its own share of every tile's keys:
-    // its rows' weights of the others are 0, and the results are added at the end.
-    struct Place {
-      int rows, mask;   // of a small item; its copies are mask + 1 lanes apart
-      int token, head;  // of the item's tokens, of the cache head's
-      bool there;
+    // of a segment: this row's token
+    auto token_of = [&](const Seg& s) {
+      return my_token + (s.flags & kSmall ? 0 : w * a.tokens);
     };
-    auto place_of = [&](const Seg& s) {
-      Place x;
-      const bool small = s.flags & kSmall;
-      x.rows = s.tokens * a.G;
-      x.mask = !small || x.rows > 64 ? 127 : x.rows > 32 ? 63 : 31;
-      const int r = row & x.mask;
-      x.token = r / a.G;
-      x.head = r - x.token * a.G;
-      x.there = x.token < a.tokens;
-      if (!small) x.token += w * a.tokens;
-      x.there = x.there && x.token < s.tokens;
-      return x;
-    };
+    auto is_there = [&](const Seg& s) { return my_token < a.tokens && token_of(s) < s.tokens; };
     uint32_t loaded = 0;  // segments whose queries were taken
     // The queries of a segment into shared memory, and there to f16; `qs` is what was taken out
     // of this row's, a power of two, so that the largest is 2^14 to 2^15. They are copied in
@@ -866,9 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!small || w == 0) {
         uint8_t* block = smem + C::Q_OFF + w * C::SLOT;
         const int c = lane % LPR;
-        const Place me = place_of(s);
-        const int64_t at = (int64_t)(s.row0 + me.token) * a.q_row + (int64_t)(s.hk * a.G + me.head) * D;
-        const bool there = me.there;
+        const int64_t at = (int64_t)(s.row0 + token_of(s)) * a.q_row + (int64_t)(s.hk * a.G + my_head) * D;
+        const bool there = is_there(s);
 #pragma unroll 4
         for (int i = 0; i < 32 / RPI; ++i) {
           const int r = i * RPI + lane / LPR;
@@ -878,7 +877,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           a.q + (on ? from : 0) + c * 8, on);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
         qs = 1.0f;
         if (__any_sync(0xffffffffu, there)) {  // (rows of zeros are the same in both types)
           uint32_t most2 = 0;  // two magnitudes' bits, each its own maximum
@@ -922,7 +920,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile0 = 0;     // tiles of the segments before
     int segs = 0, smalls = 0;
     uint32_t cnt0 = 0;   // the first warpgroup's
-    uint32_t heres = 0;  // phases of all_here
     bool dirty = false;  // codes of a small item may lie in the second block of queries
     Seg s{};             // (nothing yet: no token, no tile)
     float qs = 1.0f;
@@ -930,14 +927,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int number = 0;; ++number) {
       const bool small = s.flags & kSmall;
       const int T = s.t1 - s.t0, step = small ? 2 : 1;
-      const Place me = place_of(s);
-      const bool there = me.there;
-      const int p = there ? s.p0 + me.token : -1;  // the row's position
-      // groups of a tile's keys that this copy of the rows takes
-      const int g_lo = (quad * 32 & ~me.mask) >> 4, g_hi = g_lo + ((me.mask + 1) >> 4);
+      const bool there = is_there(s);
+      const int p = there ? s.p0 + token_of(s) : -1;  // the row's position
       const bool warp_there = __any_sync(0xffffffffu, there);
       const int p_first = s.p0 + (small ? 0 : w * a.tokens);  // the least position
-      float nm = -INFINITY, l = 0.0f;
+      float nm = -INFINITY, l = 0.0f, ref = 1.0f;
       bool ok = true;
       int mine = 0;  // tiles of this segment so far
 #pragma unroll 1
@@ -946,6 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int number_c = tile0 + t - s.t0;
         const TileConst* tile = const_s + number_c % kConsts;
         if (!(ok = wait(c_full + number_c % kConsts, (number_c / kConsts) & 1))) break;
+        ref = tile->ref;
         const uint32_t absent = tile->absent;
         if (!(ok = wait(s_full + w, cnt & 1))) break;
         tc::fence_after_sync();
@@ -955,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool masked = t * 128 + 127 > p_first || absent != 0;
           auto upto = [&](int g) { return absent >> g & 1 ? -1 : seen - 16 * g; };
           // m by `by` more (whole numbers), where that is not 0; the tile's weights so far are
-          // those of the groups up to `done`.
+          // those of `done` blocks.
           auto raise = [&](float by, int done) -> bool {
             const float f = ex2(-by);
             l *= f;
@@ -963,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t f2 = pack_f16(f, f);
             tc::tmem_wait_st();
 #pragma unroll 1
-            for (int i = 8 * g_lo; i < 8 * done; i += 8) {
+            for (int i = 0; i < 16 * done; i += 8) {
               uint32_t y[8];
               tmem_load8(s_addr + i, y);
 #pragma unroll
@@ -991,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the whole tile first.
             float top = -INFINITY;
 #pragma unroll 1
-            for (int g = g_lo; g < g_hi; ++g) {
+            for (int g = 0; g < 8; ++g) {
               float v[16];
               tc::tmem_ld16(s_addr + 16 * g, v);
               tc::tmem_wait_ld(v);
@@ -1009,14 +1004,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
             const bool none = nm == -INFINITY, over = there && top > -INFINITY && (none || top + nm > 11.0f);
             if (__any_sync(0xffffffffu, over && !none)) {
-              if (!(ok = raise(over && !none ? nm - to : 0.0f, g_lo))) break;
+              if (!(ok = raise(over && !none ? nm - to : 0.0f, 0))) break;
             }
             if (over) nm = to;
             exact = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f && nm > -INFINITY);
           }
           if (!exact) {
 #pragma unroll 1
-            for (int i = g_lo; i < g_hi; i += kBlock) {
+            for (int i = 0; i < 8; i += kBlock) {  // groups
               float v[kBlock / 2][32], c[kBlock], kb[kBlock];
 #pragma unroll
               for (int h = 0; h < kBlock / 2; ++h) tc::tmem_ld32(s_addr + 16 * i + 32 * h, v[h]);
@@ -1057,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int g = 0; g < kBlock; ++g) kb[g] = nm - kb[g];
               if (__any_sync(0xffffffffu, there && top > 11.0f)) {
                 const float by = there && top > 11.0f ? ceilf(top) - 4.0f : 0.0f;
-                if (!(ok = raise(by, i))) break;
+                if (!(ok = raise(by, i / 2))) break;
 #pragma unroll
                 for (int j = 0; j < 16 * kBlock; ++j) v[j / 32][j % 32] -= by;
               }
@@ -1086,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // far from 0: products rounded as the maximum was
 #pragma unroll 1
-            for (int g = g_lo; g < g_hi; ++g) {
+            for (int g = 0; g < 8; ++g) {
               float v[16];
               tc::tmem_ld16(s_addr + 16 * g, v);
               tc::tmem_wait_ld(v);
@@ -1105,12 +1100,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (sum != 0.0f) l += sum * ex2(-k.y);
               tmem_store8(s_addr + 8 * g, y);
             }
-          }
-          if (me.mask < 127) {  // (after the scores that these take the place of were read)
-            const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-            for (int g = 0; g < 8; ++g)
-              if (g < g_lo || g >= g_hi) tmem_store8(s_addr + 8 * g, none);
           }
           tc::tmem_wait_st();
         }
@@ -1143,8 +1132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = queries(next, qs_next);
           continue;
         }
-        const int head = s.hk * a.G + me.head;
-        const size_t q_at = (size_t)(s.row0 + me.token);
+        const int token = token_of(s), head = s.hk * a.G + my_head;
+        const size_t q_at = (size_t)(s.row0 + token);
         if (T == 0) {
           if (there && !(small && w)) {
             uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
@@ -1160,12 +1149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(pv_done + w, (cnt - 1) & 1))) break;
           tc::fence_after_sync();
         }
-        const bool copies = me.mask < 127;
-        // (of v's scales, from the segment's last tile, which some warpgroup has had)
-        auto ref_of = [&]() { return *reinterpret_cast<volatile float*>(&const_s[(tile0 - 1) % kConsts].ref); };
         float l2 = 0.0f, nm2 = -INFINITY;  // the other warpgroup's
         const bool other = small && T > 1;
-        if (small && !copies) {
+        if (small) {
           if (w == 1) {
             if (!(ok = wait(ml_empty, (smalls & 1) ^ 1))) break;
             ml_s[row] = make_float2(l, nm);
@@ -1186,70 +1172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int* nans = nan_s + ((segs % C::NANS) * 2 + w) * D;
         uint32_t* any = nan_any + segs % C::NANS * 2 + w;
         const bool nan_here = *reinterpret_cast<volatile uint32_t*>(any) != 0;
-        if (copies) {
-          // Eight warps' (or four pairs') results of the same rows: their references and sums
-          // first, then the results, as many columns at a time as there is room for.
-          auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(all_here);
-            return wait(all_here, heres++ & 1);
-          };
-          const int per = me.mask + 1, many = 256 / per;   // rows of a copy, copies
-          const int mine_at = w * (many / 2) + (quad * 32) / per, vrow = row & me.mask;
-          float2* ml = reinterpret_cast<float2*>(ml_s);
-          ml[mine_at * per + vrow] = make_float2(l, nm);
-          if (!(ok = meet())) break;
-          float both = INFINITY, sum = 0.0f;
-#pragma unroll 1
-          for (int i = 0; i < many; ++i) {
-            const float m = ml[i * per + vrow].y;
-            if (m > -INFINITY) both = fminf(both, m);
-          }
-#pragma unroll 1
-          for (int i = 0; i < many; ++i) {
-            const float2 x = ml[i * per + vrow];
-            sum += x.x * (x.y == -INFINITY ? 0.0f : ex2(both - x.y));
-          }
-          const bool part = s.part >= 0;
-          const float f = (nm == -INFINITY ? 0.0f : ex2(both - nm)) *
-                          (part ? ref_of() : sum == 0.0f ? 0.0f : ref_of() / sum);
-          if (mine_at == 0 && there) {
-            if (part)
-              a.ml[(size_t)s.part * a.rows + vrow] = make_float2(sum, both == INFINITY ? -INFINITY : both);
-            else if (a.lse)
-              a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - both) * att::kLn2;
-          }
-          int nr = 4;  // rows, as a power of two
-          while (nr < me.rows) nr *= 2;
-          const int cols = 2048 / (many * nr);
-          float* buf = reinterpret_cast<float*>(smem + C::EPI_OFF);  // [copy][column][row]
-          for (int c0 = 0; c0 < D; c0 += cols) {
-#pragma unroll 1
-            for (int c = 0; c < cols && c0 + c < D; c += 8) {
-              float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-              if (mine > 0) att::tmem_load(o_addr + c0 + c, o);
-              if (vrow < nr) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) buf[(mine_at * cols + c + e) * nr + vrow] = o[e] * f;
-              }
-            }
-            if (!(ok = meet())) break;
-#pragma unroll 1
-            for (int i = w * 128 + row; i < nr * cols; i += 256) {
-              const int r = i % nr, col = c0 + i / nr, token = r / a.G;
-              if (r >= me.rows || col >= D) continue;
-              float x = 0.0f;
-              for (int k = 0; k < many; ++k) x += buf[k * cols * nr + i];
-              if (nan_here && nans[col] <= s.p0 + token) x = __int_as_float(0x7fc00000);
-              if (part) a.part[((size_t)s.part * a.rows + r) * D + col] = x;
-              else
-                a.out[((size_t)(s.row0 + token) * Hq + s.hk * a.G + (r - token * a.G)) * D + col] =
-                    __float2bfloat16_rn(x);
-            }
-            if (!(ok = meet())) break;
-          }
-          if (!ok) break;
-        } else if (warp_there && !(small && w == 1)) {
+        if (warp_there && !(small && w == 1)) {
           // one reference for both; -inf: no row so far
           const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
           float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
@@ -1257,7 +1180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sum = l * f1 + l2 * f2;
           const bool part = s.part >= 0;
           const int r = w * 128 + row;
-          const float ref = ref_of(), norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
+          const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
           f1 *= norm;
           f2 *= norm;
           float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
@@ -1346,13 +1269,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // Eight arrivals: of a small item without copies all are the first warpgroup's, which
-        // reads both results (the second may have no tile and be an item ahead).
+        // Eight arrivals: of a small item all are the first warpgroup's, which reads both
+        // results (the second may have no tile and be an item ahead).
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0 && !(small && !copies && w == 1)) {
+        if (lane == 0 && !(small && w == 1)) {
           tc::mbar_arrive(o_empty);
-          if (small && !copies) tc::mbar_arrive(o_empty);
+          if (small) tc::mbar_arrive(o_empty);
         }
         ++segs;
       }
@@ -1363,6 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag && a.status) atomicOr(a.status, tc::kDevTimeout);
   if (warp == 0) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::COLS);
