@@ -9,6 +9,9 @@ namespace pages {
 // attend_pages_d*.cu
 cudaError_t launch_attend_pages_d64(const AttendArgs& a, int ctas, cudaStream_t st);
 cudaError_t launch_attend_pages_d128(const AttendArgs& a, int ctas, cudaStream_t st);
+// attend_pages_t*.cu: one row of each sequence, at most 64 heads on a cache head
+cudaError_t launch_attend_tokens_d64(const AttendArgs& a, int ctas, cudaStream_t st);
+cudaError_t launch_attend_tokens_d128(const AttendArgs& a, int ctas, cudaStream_t st);
 
 namespace {
 
@@ -79,7 +82,10 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   a.ml = reinterpret_cast<float2*>(ws + part_bytes(a.rows, d));
   a.record = reinterpret_cast<int4*>(ws + part_bytes(a.rows, d) + ml_bytes(a.rows));
   const int sms = num_sms(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  const cudaError_t e =
-      d == 64 ? launch_attend_pages_d64(a, ctas, stream) : launch_attend_pages_d128(a, ctas, stream);
+  cudaError_t e;
+  if (!paged->cu_q && a.G <= 64)
+    e = d == 64 ? launch_attend_tokens_d64(a, ctas, stream) : launch_attend_tokens_d128(a, ctas, stream);
+  else
+    e = d == 64 ? launch_attend_pages_d64(a, ctas, stream) : launch_attend_pages_d128(a, ctas, stream);
   return e == cudaSuccess ? HYTOPK_OK : HYTOPK_CUDA_ERROR;
 }

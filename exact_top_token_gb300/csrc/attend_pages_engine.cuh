@@ -326,6 +326,82 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
   }
 }
 
+// A CTA's segments in order, to push(segment), which tells whether to go on, and a last one with
+// kStop; the records of its parts (kStop there: there is such a part). One warp. Items whose
+// rows see nothing get their results here: roles look ahead to a segment's successors, so
+// any number of segments without a tile between two others would fill the ring.
+template <int D, class Push>
+__device__ __forceinline__ void segments(const AttendArgs& a, const Share& share, int lane, Push push) {
+  const Share sh = share;
+  int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;  // of an item begun before; begun here
+  bool ok = true;
+  if (sh.any) {
+    int b = sh.b, hk = sh.hk, i = sh.i;
+    int64_t at = sh.at;
+    Seq q = seq_of(a.s, a.n, b);
+#pragma unroll 1
+    while (ok && at < sh.hi) {
+      const Work w(a, q);
+      const int T = w.tiles_of(i), unit = w.unit_of(i);
+      // tiles whose first unit lies in [lo, hi)
+      auto tile_at = [&](int64_t u) -> int {
+        const int64_t x = u - at - kOverhead;
+        return x <= 0 ? 0 : (int)min((int64_t)T, unit == 2 ? (x + 1) >> 1 : x);
+      };
+      const int t0 = tile_at(sh.lo), t1 = tile_at(sh.hi);
+      if (T == 0 && at >= sh.lo) {
+        const int tokens = w.tokens_of(i);
+#pragma unroll 1
+        for (int t = 0; t < tokens; ++t) {
+          const size_t head = (size_t)(q.row0 + i * w.per + t) * (a.Hkv * a.G) + hk * a.G;
+          for (int e = lane; e < a.G * (D / 8); e += 32)
+            reinterpret_cast<uint4*>(a.out + head * D)[e] = make_uint4(0, 0, 0, 0);
+          for (int h = lane; a.lse && h < a.G; h += 32) a.lse[head + h] = -INFINITY;
+        }
+      }
+      if (t0 < t1) {
+        Seg s;
+        s.b = b;
+        s.hk = hk;
+        s.row0 = q.row0 + i * w.per;
+        s.tokens = w.tokens_of(i);
+        s.p0 = w.start + i * w.per;
+        s.end = max(s.p0 + s.tokens, 0);
+        s.t0 = t0;
+        s.t1 = t1;
+        s.flags = (unit == 1 ? kSmall : 0) | (t0 == 0 ? kStarts : 0) | (t1 == T ? kEnds : 0);
+        s.part = -1;
+        if ((s.flags & (kStarts | kEnds)) != (kStarts | kEnds)) {
+          const int4 r = make_int4(s.flags | kStop, s.row0, s.tokens, s.hk);
+          s.part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+          if (t0 == 0) rec1 = r;
+          else rec0 = r;
+        }
+        ok = push(s);
+      }
+      at += w.weight_of(i);
+      if (++i == w.count) {
+        i = 0;
+        if (++hk == a.Hkv) {
+          hk = 0;
+          do {
+            if (++b >= a.s.B) break;
+            q = seq_of(a.s, a.n, b);
+          } while (q.m == 0);
+          if (b >= a.s.B) break;
+        }
+      }
+    }
+  }
+  if (lane == 0) {
+    a.record[2 * blockIdx.x] = rec0;
+    a.record[2 * blockIdx.x + 1] = rec1;
+  }
+  Seg s{};
+  s.flags = kStop;
+  if (ok) push(s);
+}
+
 // ---- the kernel -------------------------------------------------------------------------
 
 // Wait for a phase of `bar`; gives up (false, abort flag) when another role has, or after
@@ -446,78 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-    const Share sh = *share;
-    __syncwarp();
     if (warp == 1) {
       // ---------------- segments ----------------
-      int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;  // of an item begun before; begun here
       int number = 0;
-      bool ok = true;
-      auto push = [&](const Seg& s) {
-        ok = wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1);
-        if (!ok) return;
+      segments<D>(a, *share, lane, [&](const Seg& s) {
+        const bool ok = wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1);
+        if (!ok) return false;
         if (lane == 0) {
           seg_s[number % kSegs] = s;
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
-      };
-      if (sh.any) {
-        int b = sh.b, hk = sh.hk, i = sh.i;
-        int64_t at = sh.at;
-        Seq q = seq_of(a.s, a.n, b);
-#pragma unroll 1
-        while (ok && at < sh.hi) {
-          const Work w(a, q);
-          const int T = w.tiles_of(i), unit = w.unit_of(i);
-          // tiles whose first unit lies in [lo, hi)
-          auto tile_at = [&](int64_t u) -> int {
-            const int64_t x = u - at - kOverhead;
-            return x <= 0 ? 0 : (int)min((int64_t)T, unit == 2 ? (x + 1) >> 1 : x);
-          };
-          const int t0 = tile_at(sh.lo), t1 = tile_at(sh.hi);
-          if (T == 0 ? at >= sh.lo : t0 < t1) {
-            Seg s;
-            s.b = b;
-            s.hk = hk;
-            s.row0 = q.row0 + i * w.per;
-            s.tokens = w.tokens_of(i);
-            s.p0 = w.start + i * w.per;
-            s.end = max(s.p0 + s.tokens, 0);
-            s.t0 = t0;
-            s.t1 = t1;
-            s.flags = (unit == 1 ? kSmall : 0) | (t0 == 0 ? kStarts : 0) | (t1 == T ? kEnds : 0);
-            s.part = -1;
-            if ((s.flags & (kStarts | kEnds)) != (kStarts | kEnds)) {
-              const int4 r = make_int4(s.flags | kStop, s.row0, s.tokens, s.hk);
-              s.part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-              if (t0 == 0) rec1 = r;
-              else rec0 = r;
-            }
-            push(s);
-          }
-          at += w.weight_of(i);
-          if (++i == w.count) {
-            i = 0;
-            if (++hk == a.Hkv) {
-              hk = 0;
-              do {
-                if (++b >= a.s.B) break;
-                q = seq_of(a.s, a.n, b);
-              } while (q.m == 0);
-              if (b >= a.s.B) break;
-            }
-          }
-        }
-      }
-      // (kStop: there is such a part)
-      if (lane == 0) {
-        a.record[2 * blockIdx.x] = rec0;
-        a.record[2 * blockIdx.x + 1] = rec1;
-      }
-      Seg s{};
-      s.flags = kStop;
-      if (ok) push(s);
+        return true;
+      });
     } else if (warp == 2) {
       // ---------------- codes and scales of the tiles ----------------
       // Lanes 0 .. 7 take a group each: its page and its scales. The codes come by TMA, as many
@@ -700,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int number = 0; ok && take(number, s) && !(s.flags & kStop); ++number) {
         const int T = __shfl_sync(0xffffffffu, s.t1 - s.t0, 0);
         const bool small = __shfl_sync(0xffffffffu, s.flags & kSmall, 0) != 0;
-        if (T == 0) continue;
         // Step i is warpgroup i % 2's: the products of its tile, then the scores of its next
         // one (which take the place of the weights). Of a large item both have every tile,
         // of a small one every other.
@@ -835,7 +851,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int item = 0;  // of the NaN columns
 #pragma unroll 1
     for (int number = 0; ok && take(number, s) && !(s.flags & kStop); ++number) {
-      if (s.t0 >= s.t1) continue;
       const bool now = !(s.flags & kSmall);
       if (C::SHARED && (first || now != large)) unit = 0;
       large = now;
@@ -1129,12 +1144,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seg next;
       float qs_next = 1.0f;
       const bool more = take(number, next) && !(next.flags & kStop);
-      const bool ask = more && next.t1 > next.t0;
-      const bool late = ask && dirty && !(next.flags & kSmall);
+      const bool late = more && dirty && !(next.flags & kSmall);
 #pragma unroll 1
       for (int pass = 0; ok && pass < 2; ++pass) {
         if ((pass == 0) != late) {
-          if (!ask) continue;
+          if (!more) continue;
           if (late) {
             // (own products are done; the first warpgroup's wait for these queries to go on)
             if (w == 1 && !(ok = wait(pv_done, (cnt0 - 1) & 1))) break;
@@ -1145,15 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int token = token_of(s), head = s.hk * a.G + my_head;
         const size_t q_at = (size_t)(s.row0 + token);
-        if (T == 0) {
-          if (there && !(small && w)) {
-            uint4* y = reinterpret_cast<uint4*>(a.out + (q_at * Hq + head) * D);
-#pragma unroll 1
-            for (int i = 0; i < D / 8; ++i) y[i] = make_uint4(0, 0, 0, 0);
-            if (a.lse) a.lse[q_at * Hq + head] = -INFINITY;
-          }
-          continue;
-        }
+        if (T == 0) continue;  // (nothing yet)
         tile0 += T;
         // ---- the result ----
         if (mine > 0) {
