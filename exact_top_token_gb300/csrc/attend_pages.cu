@@ -1,5 +1,7 @@
 // attend_pages.cu -- hytopk_attend_pages: host checks and dispatch; instances in
 // attend_pages_d*.cu.
+#include <numeric>
+
 #include "attend_pages.h"
 #include "launch.h"
 
@@ -82,6 +84,7 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   a.ml = reinterpret_cast<float2*>(ws + part_bytes(a.rows, d));
   a.record = reinterpret_cast<int4*>(ws + part_bytes(a.rows, d) + ml_bytes(a.rows));
   const int sms = num_sms(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  a.groups = std::gcd(Hkv, ctas);
   cudaError_t e;
   if (!paged->cu_q && a.G <= 64)
     e = d == 64 ? launch_attend_tokens_d64(a, ctas, stream) : launch_attend_tokens_d128(a, ctas, stream);

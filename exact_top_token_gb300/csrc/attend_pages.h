@@ -30,6 +30,7 @@ struct AttendArgs {
   float2* ml;    // [2 * ctas][rows] their sums and -m
   int4* record;  // [2 * ctas][2]: what each is a part of
   int rows;      // of a part
+  int groups;    // of CTAs, by cache heads: divides Hkv and the number of CTAs
 };
 
 }  // namespace pages

@@ -31,7 +31,9 @@
 // The work of a call is only known on the device (contexts and their new rows). Every CTA
 // adds it up, in units of a tile's time, and takes an equal share of it in order, tile by
 // tile: an item that lies in several shares leaves unnormalised parts in the workspace,
-// and a second kernel joins them. The result does not depend on timing.
+// and a second kernel joins them. The result does not depend on timing. A row of a page holds
+// all cache heads, so neighbouring CTAs take the same places of different heads: read by
+// themselves, pieces of 128 bytes 1 KB apart come at 4.1 TB/s, whole rows at 5.4.
 //
 //   warp 0        tensor memory
 //   warp 1        this CTA's segments: (item, tiles) in order, through a ring
@@ -241,14 +243,19 @@ struct Work {
   }
 };
 
-// Where a CTA's share begins: item `i` of head `hk` of sequence `b`, and its first unit.
+// CTA c belongs to group c % groups, which has the heads h groups + c % groups; shares are numbered
+// group by group. Where a share begins: item `i` of the group's head `h` of sequence `b`, and
+// its first unit, all in units of the group's work.
 struct Share {
   int64_t lo, hi, at;
-  int b, hk, i, any;
+  int b, h, i, any;
 };
+__device__ __forceinline__ int share_number(const AttendArgs& a) {
+  return (int)(blockIdx.x % a.groups * (gridDim.x / a.groups) + blockIdx.x / a.groups);
+}
 
-template <typename T>
-__device__ __forceinline__ T scan512(T x, T* warps, T& total) {
+template <int THREADS, typename T>
+__device__ __forceinline__ T scan(T x, T* warps, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T s = x;
 #pragma unroll
@@ -262,27 +269,31 @@ __device__ __forceinline__ T scan512(T x, T* warps, T& total) {
   T before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warps[w];
     total += warps[w];
   }
   return before + s - x;
 }
 
-// All threads; the result is in `share` (shared memory) after the next barrier.
+// All threads; the result is in `share` (shared memory) after the next barrier. `warps`: a
+// number for each warp.
+template <int THREADS>
 __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, Share* share) {
+  const int heads = a.Hkv / a.groups;
   int64_t mine = 0, kept = 0, total;
-  for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
+  for (int b = threadIdx.x; b < a.s.B; b += THREADS) {
     const Seq q = seq_of(a.s, a.n, b);
     if (q.bad && blockIdx.x == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
     if (q.m > 0) {
       const Work w(a, q);
-      kept = w.before(w.count) * a.Hkv;
+      kept = w.before(w.count) * heads;
       mine += kept;
     }
   }
-  int64_t at = scan512(mine, warps, total);
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  int64_t at = scan<THREADS>(mine, warps, total);
+  const int64_t shares = gridDim.x / a.groups, number = blockIdx.x / a.groups;
+  const int64_t lo = total * number / shares, hi = total * (number + 1) / shares;
   if (threadIdx.x == 0) {
     share->lo = lo;
     share->hi = hi;
@@ -291,25 +302,25 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
   __syncthreads();
   if (lo == hi) return;
   int64_t base = 0;
-  for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.s.B; b0 += THREADS) {
     const int b = b0 + threadIdx.x;
     int64_t all = mine;  // one pass: as it was
-    if (a.s.B > kThreads) {
+    if (a.s.B > THREADS) {
       all = 0;
       if (b < a.s.B) {
         const Seq q = seq_of(a.s, a.n, b);
         if (q.m > 0) {
           const Work w(a, q);
-          all = w.before(w.count) * a.Hkv;
+          all = w.before(w.count) * heads;
         }
       }
-      at = base + scan512(all, warps, total);
+      at = base + scan<THREADS>(all, warps, total);
     }
     if (all > 0 && lo >= at && lo < at + all) {
       const Work w(a, seq_of(a.s, a.n, b));
-      const int64_t head = all / a.Hkv;
-      const int hk = (int)((lo - at) / head);
-      const int64_t in = lo - at - hk * head;
+      const int64_t head = all / heads;
+      const int h = (int)((lo - at) / head);
+      const int64_t in = lo - at - h * head;
       int i = 0, j = w.count;  // before(i) <= in < before(j)
       while (j - i > 1) {
         const int mid = (i + j) / 2;
@@ -317,9 +328,9 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
         else j = mid;
       }
       share->b = b;
-      share->hk = hk;
+      share->h = h;
       share->i = i;
-      share->at = at + hk * head + w.before(i);
+      share->at = at + h * head + w.before(i);
       share->any = 1;
     }
     base += total;
@@ -333,14 +344,16 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
 template <int D, class Push>
 __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share, int lane, Push push) {
   const Share sh = share;
+  const int place = 2 * share_number(a), heads = a.Hkv / a.groups;
   int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;  // of an item begun before; begun here
   bool ok = true;
   if (sh.any) {
-    int b = sh.b, hk = sh.hk, i = sh.i;
+    int b = sh.b, h = sh.h, i = sh.i;
     int64_t at = sh.at;
     Seq q = seq_of(a.s, a.n, b);
 #pragma unroll 1
     while (ok && at < sh.hi) {
+      const int hk = h * a.groups + (int)(blockIdx.x % a.groups);
       const Work w(a, q);
       const int T = w.tiles_of(i), unit = w.unit_of(i);
       // tiles whose first unit lies in [lo, hi)
@@ -356,7 +369,7 @@ __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share
           const size_t head = (size_t)(q.row0 + i * w.per + t) * (a.Hkv * a.G) + hk * a.G;
           for (int e = lane; e < a.G * (D / 8); e += 32)
             reinterpret_cast<uint4*>(a.out + head * D)[e] = make_uint4(0, 0, 0, 0);
-          for (int h = lane; a.lse && h < a.G; h += 32) a.lse[head + h] = -INFINITY;
+          for (int e = lane; a.lse && e < a.G; e += 32) a.lse[head + e] = -INFINITY;
         }
       }
       if (t0 < t1) {
@@ -373,7 +386,7 @@ __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share
         s.part = -1;
         if ((s.flags & (kStarts | kEnds)) != (kStarts | kEnds)) {
           const int4 r = make_int4(s.flags | kStop, s.row0, s.tokens, s.hk);
-          s.part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+          s.part = place + (t0 == 0 ? 1 : 0);
           if (t0 == 0) rec1 = r;
           else rec0 = r;
         }
@@ -382,8 +395,8 @@ __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share
       at += w.weight_of(i);
       if (++i == w.count) {
         i = 0;
-        if (++hk == a.Hkv) {
-          hk = 0;
+        if (++h == heads) {
+          h = 0;
           do {
             if (++b >= a.s.B) break;
             q = seq_of(a.s, a.n, b);
@@ -394,8 +407,8 @@ __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share
     }
   }
   if (lane == 0) {
-    a.record[2 * blockIdx.x] = rec0;
-    a.record[2 * blockIdx.x + 1] = rec1;
+    a.record[place] = rec0;
+    a.record[place + 1] = rec1;
   }
   Seg s{};
   s.flags = kStop;
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   allow_next();
   wait_for_earlier();
-  find_share(a, scan_s, share);
+  find_share<kThreads>(a, scan_s, share);
   __syncthreads();
 
   const uint32_t abort_at = tc::smem_u32(tmem_slot + 1);
@@ -1314,9 +1327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinThreads = 256;
 
-// Parts of an item: number 2c + 1 of the CTA c where it starts, then 2c' + 0 of the CTAs after
-// it, up to the one that ends it (CTAs between may hold none of it). kJoinBlocks blocks take
-// the rows of the item that starts in a CTA, if one does that does not end there. Many parts: a
+// Parts of an item: number 2c + 1 of the share c where it starts, then 2c' + 0 of the shares after
+// it, up to the one that ends it (shares between may hold none of it). kJoinBlocks blocks take
+// the rows of the item that starts in a share, if one does that does not end there. Many parts: a
 // block a row, its warps sharing the parts; few: a warp a row.
 constexpr int kJoinBlocks = 32;
 
@@ -1326,7 +1339,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   wait_for_earlier();
   constexpr int WARPS = kJoinThreads / 32, V = D / 32;
   __shared__ int last_s;
-  __shared__ uint32_t held[(kMaxCtas + 31) / 32];  // CTAs after c that hold a part
+  __shared__ uint32_t held[(kMaxCtas + 31) / 32];  // shares after c that hold a part
   __shared__ float4 acc_s[WARPS][32];
   __shared__ float sum_s[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1341,8 +1354,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   const uint32_t some = __ballot_sync(0xffffffffu, (flags & kStop) != 0);
   if (lane == 0 && warp < (int)(sizeof(held) / 4)) held[warp] = some;
   __syncthreads();
-  const int count = last_s - c;  // CTAs after c, of which held tells
-  auto part_of = [&](int i) -> int {  // i-th CTA from c on; -1: no part
+  const int count = last_s - c;  // shares after c, of which held tells
+  auto part_of = [&](int i) -> int {  // i-th share from c on; -1: no part
     if (i == 0) return 2 * c + 1;
     return held[(i - 1) / 32] >> ((i - 1) % 32) & 1 ? 2 * (c + i) : -1;
   };
