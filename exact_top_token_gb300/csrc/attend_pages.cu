@@ -11,9 +11,17 @@ namespace pages {
 // attend_pages_d*.cu
 cudaError_t launch_attend_pages_d64(const AttendArgs& a, int ctas, cudaStream_t st);
 cudaError_t launch_attend_pages_d128(const AttendArgs& a, int ctas, cudaStream_t st);
-// attend_pages_t*.cu: one row of each sequence, at most 64 heads on a cache head
-cudaError_t launch_attend_tokens_d64(const AttendArgs& a, int ctas, cudaStream_t st);
-cudaError_t launch_attend_tokens_d128(const AttendArgs& a, int ctas, cudaStream_t st);
+// attend_pages_t*.cu: one row of a sequence, at most kTokenHeads heads on a cache head
+cudaError_t launch_attend_tokens_d64(const AttendArgs& a, int ctas, bool join, cudaStream_t st);
+cudaError_t launch_attend_tokens_d128(const AttendArgs& a, int ctas, bool join, cudaStream_t st);
+
+constexpr int kTokenHeads = 16;
+// The kernel of single rows is taken where at most that many rows are given as there are
+// sequences, and contexts may be long enough: 64 rows over up to 16384 keys, 8 cache heads of 128
+// columns, take 208 us with it and 233 with the general one, but a cu_q may hold several rows
+// of a sequence all the same, so that both are launched and the second one mostly ends at once,
+// which takes 2 us: as much as 16 tiles of 128 keys a multiprocessor gain.
+constexpr int kTokenTiles = 16;
 
 namespace {
 
@@ -23,6 +31,7 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 int part_rows(int n, int G) { return n > 128 / G ? 256 : 128; }
 
 size_t part_bytes(int rows, int d) { return (size_t)2 * kMaxCtas * rows * d * sizeof(float); }
+constexpr size_t kRecordBytes = 2 * kMaxCtas * sizeof(int4);
 size_t ml_bytes(int rows) { return (size_t)2 * kMaxCtas * rows * sizeof(float2); }
 
 }  // namespace
@@ -35,7 +44,7 @@ using namespace hytopk::pages;
 extern "C" size_t hytopk_attend_pages_workspace_size(int n, int Hq, int Hkv, int d) {
   if (n < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 128 || (d != 64 && d != 128)) return 0;
   const int rows = part_rows(n, Hq / Hkv);
-  return part_bytes(rows, d) + ml_bytes(rows) + 2 * kMaxCtas * sizeof(int4);
+  return part_bytes(rows, d) + ml_bytes(rows) + kRecordBytes + 256;
 }
 
 extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const void* k_pages,
@@ -86,9 +95,15 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   const int sms = num_sms(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
   a.groups = std::gcd(Hkv, ctas);
   cudaError_t e;
-  if (!paged->cu_q && a.G <= 64)
-    e = d == 64 ? launch_attend_tokens_d64(a, ctas, stream) : launch_attend_tokens_d128(a, ctas, stream);
-  else
+  const int64_t tiles = ((int64_t)paged->columns * paged->P + 127) / 128 * paged->B * Hkv;
+  const bool tokens = n <= paged->B && a.G <= kTokenHeads && tiles >= (int64_t)kTokenTiles * ctas;
+  if (tokens && paged->cu_q)
+    a.several = reinterpret_cast<int*>(ws + part_bytes(a.rows, d) + ml_bytes(a.rows) + kRecordBytes);
+  e = cudaSuccess;
+  if (tokens)
+    e = d == 64 ? launch_attend_tokens_d64(a, ctas, !a.several, stream)
+                : launch_attend_tokens_d128(a, ctas, !a.several, stream);
+  if (e == cudaSuccess && (!tokens || a.several))
     e = d == 64 ? launch_attend_pages_d64(a, ctas, stream) : launch_attend_pages_d128(a, ctas, stream);
   return e == cudaSuccess ? HYTOPK_OK : HYTOPK_CUDA_ERROR;
 }

@@ -30,6 +30,9 @@ struct AttendArgs {
   float2* ml;    // [2 * ctas][rows] their sums and -m
   int4* record;  // [2 * ctas][2]: what each is a part of
   int rows;      // of a part
+  // both kernels are launched: the first tells here whether some sequence has several rows, which
+  // are the second's; NULL: one alone
+  int* several;
   int groups;    // of CTAs, by cache heads: divides Hkv and the number of CTAs
 };
 

@@ -277,13 +277,15 @@ __device__ __forceinline__ T scan(T x, T* warps, T& total) {
 }
 
 // All threads; the result is in `share` (shared memory) after the next barrier. `warps`: a
-// number for each warp.
+// number for each warp. Whether this thread saw a sequence with several rows.
 template <int THREADS>
-__device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, Share* share) {
+__device__ __forceinline__ bool find_share(const AttendArgs& a, int64_t* warps, Share* share) {
   const int heads = a.Hkv / a.groups;
   int64_t mine = 0, kept = 0, total;
+  bool several = false;
   for (int b = threadIdx.x; b < a.s.B; b += THREADS) {
     const Seq q = seq_of(a.s, a.n, b);
+    several |= q.m > 1;
     if (q.bad && blockIdx.x == 0 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_POSITION);
     if (q.m > 0) {
       const Work w(a, q);
@@ -300,7 +302,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
     share->any = 0;
   }
   __syncthreads();
-  if (lo == hi) return;
+  if (lo == hi) return several;
   int64_t base = 0;
   for (int b0 = 0; b0 < a.s.B; b0 += THREADS) {
     const int b = b0 + threadIdx.x;
@@ -335,6 +337,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t* warps, 
     }
     base += total;
   }
+  return several;
 }
 
 // A CTA's segments in order, to push(segment), which tells whether to go on, and a last one with
@@ -472,6 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Share* share = reinterpret_cast<Share*>(ml_s);           // (before anything else is there)
   int64_t* scan_s = reinterpret_cast<int64_t*>(const_s);
 
+  if (a.several) {
+    allow_next();
+    wait_for_earlier();
+    if (!ld_after(a.several)) return;
+  }
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {

@@ -1,8 +1,8 @@
-// attend_pages_tokens.cuh -- attention over a cache in pages for one new row of each sequence
-// (hytopk_attend_pages without cu_q), at most 64 heads on a cache head.
+// attend_pages_tokens.cuh -- attention over a cache in pages where each sequence has one new row
+// or none, and at most 16 heads share a cache head (hytopk_attend_pages).
 //
-// An item is a sequence's row and the N heads that share a cache head; N is few, and every key
-// is seen by all of them. So the keys are the 128 lanes of the tensor core, and nothing is
+// An item is a sequence's row and the heads that share a cache head, few, and every key is seen
+// by all of them. So the keys are the 128 lanes of the tensor core, and nothing is
 // computed for rows that no head uses:
 //
 //   S^T [128 keys x N]  = K . Q^T      (K from tensor memory, Q from shared memory)
@@ -35,30 +35,24 @@
 namespace hytopk {
 namespace pages {
 
-template <int D_, int N_>
+template <int D_>
 struct TCfg {
-  static constexpr int D = D_, N = N_;  // N: columns, of the heads
-  // Of few columns a warpgroup of the softmax has every other tile, with references and a
-  // result of its own, joined at an item's end; of many both have every tile, and half
-  // the columns each.
-  static constexpr bool TURNS = N == 16;
-  static constexpr int HG = TURNS ? N : N / 2;  // columns of a warpgroup
-  static constexpr int SW = TURNS ? 4 : 8;      // softmax warps of a tile
+  static constexpr int D = D_, N = 16;  // N: columns, of the heads
   static constexpr int RB = 2 * D;
   using Geo = tc::Geo<RB>;
   static constexpr int SLOT = 128 * RB;  // f16 V of a tile
   static constexpr int PB = 16384;       // P of a tile: [128 keys][64 heads], whole atoms
   static constexpr int QB = N * RB;
   static constexpr int UNIT = 128 * D;  // codes, K in even units and V in odd ones
-  static constexpr int UNITS = D == 128 ? (N == 64 ? 4 : 6) : 8;
+  static constexpr int UNITS = D == 128 ? 6 : 8;
   static constexpr int P_OFF = 2 * SLOT;
   static constexpr int Q_OFF = P_OFF + 2 * PB;
   static constexpr int STAGE_OFF = Q_OFF + 2 * QB;
   static constexpr int CONST_OFF = STAGE_OFF + UNITS * UNIT;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int QS_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);  // [2][N] queries' powers of two
-  // of a warpgroup: [2][HG] -m, factors; [4][HG] maxima, sums; [HG + 16] what the other is told
-  static constexpr int SOFT = (12 * HG + HG + 16) * 4;
+  // of a warpgroup: [2][N] -m, factors; [4][N] maxima, sums; [N + 16] what the other is told
+  static constexpr int SOFT = (12 * N + N + 16) * 4;
   static constexpr int SOFT_OFF = QS_OFF + 2 * N * 4;
   static constexpr int SHARE_OFF = SOFT_OFF + 2 * SOFT;
   static constexpr int BAR_OFF = SHARE_OFF + (int)sizeof(Share);
@@ -93,8 +87,7 @@ template <class C>
 __global__ void __launch_bounds__(kTThreads, 1)
     k_attend_tokens(const AttendArgs a, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map) {
-  constexpr int D = C::D, N = C::N, HG = C::HG, UNITS = C::UNITS;
-  constexpr bool TURNS = C::TURNS;
+  constexpr int D = C::D, N = C::N, UNITS = C::UNITS;
   using Geo = typename C::Geo;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem = tc::align1024(smem_dyn);
@@ -113,7 +106,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* pv_done = p_full + 2;   // [2] products with them
   uint64_t* o_full = pv_done + 2;   // a segment's
   uint64_t* o_empty = o_full + 1;
-  uint64_t* ml_full = o_empty + 1;  // the second warpgroup's sums (turns)
+  uint64_t* ml_full = o_empty + 1;  // the second warpgroup's sums
   uint64_t* ml_empty = ml_full + 1;
   uint64_t* q_full = ml_empty + 1;  // [2]
   uint64_t* q_empty = q_full + 2;   // [2]
@@ -124,7 +117,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* unit_empty = unit_full + UNITS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + UNITS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((24 + 2 * kSegs + kConsts + 2 * UNITS) * 8 + 8 <= 640, "barriers");
+  volatile int* several_s = abort_flag + 1;  // some sequence has several rows
+  static_assert((24 + 2 * kSegs + kConsts + 2 * UNITS) * 8 + 12 <= 640, "barriers");
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -134,14 +128,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
       tc::mbar_init(v_full + i, 4);
       tc::mbar_init(v_empty + i, 1);
       tc::mbar_init(s_full + i, 1);
-      tc::mbar_init(s_empty + i, C::SW);
-      tc::mbar_init(p_full + i, C::SW);
+      tc::mbar_init(s_empty + i, 4);
+      tc::mbar_init(p_full + i, 4);
       tc::mbar_init(pv_done + i, 1);
       tc::mbar_init(q_full + i, 4);
       tc::mbar_init(q_empty + i, 1 + 8);
     }
     tc::mbar_init(o_full, 1);
-    tc::mbar_init(o_empty, C::SW);
+    tc::mbar_init(o_empty, 4);
     tc::mbar_init(ml_full, 4);
     tc::mbar_init(ml_empty, 4);
     for (int i = 0; i < kSegs; ++i) {
@@ -154,6 +148,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       tc::mbar_init(unit_empty + i, 4);
     }
     *abort_flag = 0;
+    *several_s = 0;
     tc::fence_barrier_init();
   }
   if (warp == 0) {
@@ -166,7 +161,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   allow_next();
   wait_for_earlier();
-  find_share<kTThreads>(a, reinterpret_cast<int64_t*>(const_s), share);
+  if (find_share<kTThreads>(a, reinterpret_cast<int64_t*>(const_s), share)) *several_s = 1;
   __syncthreads();
 
   const uint32_t abort_at = tc::smem_u32(tmem_slot + 1);
@@ -225,6 +220,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsCtl));
     if (warp == 1) {
       // ---------------- segments ----------------
+      // (several rows of a sequence: no segment here, all of it is the next kernel's; a return here
+      // and now cost the roles' code 10 % of their speed)
+      const int several = *several_s;
+      if (a.several) {
+        if (blockIdx.x == 0 && lane == 0) *a.several = several;
+        if (lane == 0 && several) share->any = 0;
+        __syncwarp();
+      }
       int number = 0;
       segments<D>(a, *share, lane, [&](const Seg& s) {
         if (!wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1)) return false;
@@ -342,8 +345,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             tc::fence_after_sync();
             const uint32_t ad = (low(smem) + buf * (C::SLOT >> 4)) | LBO_MN;
             const uint32_t bd = (low(smem + C::P_OFF) + buf * (C::PB >> 4)) | LBO_MN;
-            const uint32_t o = tmem + C::O_COL + (TURNS ? buf * 64 : 0);
-            const uint32_t add = i < (TURNS ? 2 : 1) ? 0u : 1u;
+            const uint32_t o = tmem + C::O_COL + buf * 64, add = i < 2 ? 0u : 1u;
             if (elect_one()) {
               // (d = 64 has one atom of 64 columns; the second one that M = 128 takes is what
               // follows in shared memory, and fills lanes that are never read)
@@ -544,16 +546,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsSoft));
     // ---------------- softmax: TMEM lane = key ----------------
+    // A warpgroup has every other tile, with references and a result of its own, joined at an
+    // item's end.
     const int wg = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane;
-    const int bar = 1 + wg, c0 = TURNS ? 0 : wg * HG;  // first column of this warpgroup
+    const int bar = 1 + wg;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_base = tmem + lane_off + C::S_COL + c0;
-    const uint32_t o_addr = tmem + lane_off + C::O_COL + (TURNS ? wg * 64 : c0);
-    float* nm_s = reinterpret_cast<float*>(smem + C::SOFT_OFF + wg * C::SOFT);  // [2][HG] -m
-    float* f_s = nm_s + 2 * HG;                                                 // [2][HG]
-    float* quad_s = f_s + 2 * HG;                                               // [4][HG] maxima
-    float* sum_s = quad_s + 4 * HG;                                             // [4][HG]
-    float* told_s = sum_s + 4 * HG;  // [HG] -m, and the reference of v's scales
+    const uint32_t s_addr = tmem + lane_off + C::S_COL + wg * 64;
+    const uint32_t o_addr = tmem + lane_off + C::O_COL + wg * 64;
+    float* nm_s = reinterpret_cast<float*>(smem + C::SOFT_OFF + wg * C::SOFT);  // [2][N] -m
+    float* f_s = nm_s + 2 * N;                                                 // [2][N]
+    float* quad_s = f_s + 2 * N;                                               // [4][N] maxima
+    float* sum_s = quad_s + 4 * N;                                             // [4][N]
+    float* told_s = sum_s + 4 * N;  // [N] -m, and the reference of v's scales
     const int Hq = a.Hkv * a.G;
     int g0 = 0, cur = 0;  // tiles of the segments before; which nm_s counts
     Seg s;
@@ -565,34 +569,32 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const bool got = take(segs, s);
       if (some_of_us(!got) || (s.flags & kStop)) break;
       const int T = s.t1 - s.t0;
-      float l[HG];
+      float l[N];
 #pragma unroll
-      for (int r = 0; r < HG; ++r) l[r] = 0.0f;
+      for (int r = 0; r < N; ++r) l[r] = 0.0f;
       float ref = 1.0f;
       bool exact = false, started = false, ok = true;  // exact: some reference is far from 0
-      const float* qs = qs_s + (segs & 1) * N + c0;
-      int i = TURNS ? (g0 ^ wg) & 1 : 0;
+      const float* qs = qs_s + (segs & 1) * N;
 #pragma unroll 1
-      for (; i < T; i += TURNS ? 2 : 1) {
-        const int g = g0 + i, buf = g & 1;
+      for (int i = (g0 ^ wg) & 1; i < T; i += 2) {
+        const int g = g0 + i;
         const TileConst* tile = const_s + g % kConsts;
         ok = ok && wait(c_full + g % kConsts, (g / kConsts) & 1);
         const float2 k = reinterpret_cast<const float2*>(tile->group)[row >> 4];
         const bool seen = (s.t0 + i) * 128 + row < s.end && !(tile->absent >> (row >> 4) & 1);
-        ok = ok && wait(s_full + buf, g >> 1 & 1);
+        ok = ok && wait(s_full + wg, g >> 1 & 1);
         tc::fence_after_sync();
-        const uint32_t s_addr = s_base + buf * 64;
-        float v[HG];
+        float v[N];
         // s + b - m of all columns; the largest
         auto weights = [&]() -> float {
-          const float* nm = nm_s + cur * HG;
+          const float* nm = nm_s + cur * N;
 #pragma unroll
-          for (int j = 0; j < HG; j += 16) tc::tmem_ld16(s_addr + j, reinterpret_cast<float(&)[16]>(v[j]));
+          for (int j = 0; j < N; j += 16) tc::tmem_ld16(s_addr + j, reinterpret_cast<float(&)[16]>(v[j]));
 #pragma unroll
-          for (int j = 0; j < HG; j += 16) tc::tmem_wait_ld(reinterpret_cast<float(&)[16]>(v[j]));
+          for (int j = 0; j < N; j += 16) tc::tmem_wait_ld(reinterpret_cast<float(&)[16]>(v[j]));
           if (!exact) {
 #pragma unroll
-            for (int j = 0; j < HG; j += 4) {
+            for (int j = 0; j < N; j += 4) {
               float4 c = *reinterpret_cast<const float4*>(qs + j);
               float4 m = *reinterpret_cast<const float4*>(nm + j);
               att::mul2(c.x, c.y, k.x, k.x);
@@ -604,16 +606,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
           } else {  // far from 0: products rounded as the maximum was
 #pragma unroll
-            for (int j = 0; j < HG; ++j)
+            for (int j = 0; j < N; ++j)
               v[j] = __fadd_rn(__fadd_rn(__fmul_rn(v[j], k.x * qs[j]), k.y), nm[j]);
           }
           float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
 #pragma unroll
-          for (int j = 6; j + 3 < HG; j += 4) {
+          for (int j = 6; j + 3 < N; j += 4) {
             m0 = max3(m0, v[j], v[j + 1]);
             m1 = max3(m1, v[j + 2], v[j + 3]);
           }
-          return fmaxf(max3(m0, v[HG - 2], v[HG - 1]), m1);
+          return fmaxf(max3(m0, v[N - 2], v[N - 1]), m1);
         };
         bool raise = !started;
         if (started) raise = weights() > 11.0f && seen;
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           // the tile's maxima, a column at a time, and new references where they pass
 #pragma unroll 1
-          for (int j = 0; j < HG; j += 16) {
+          for (int j = 0; j < N; j += 16) {
             float x[16];
             tc::tmem_ld16(s_addr + j, x);
             tc::tmem_wait_ld(x);
@@ -635,23 +637,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
               x[e] = seen && x[e] > -INFINITY ? x[e] : -INFINITY;  // (NaN as well)
             }
             const float top = att::reduce_columns<16, true>(x, lane);
-            if (!(lane & 1)) quad_s[quad * HG + j + lane / 2] = top;
+            if (!(lane & 1)) quad_s[quad * N + j + lane / 2] = top;
           }
           some_of_us(false);
-          const float* nm0 = nm_s + cur * HG;
+          const float* nm0 = nm_s + cur * N;
           cur ^= 1;
           bool some = false, far = false;  // O to be scaled; a reference far from 0
-          if (lane < HG) {
+          if (lane < N) {
             const int r = lane;
-            const float top = fmaxf(fmaxf(quad_s[r], quad_s[HG + r]), fmaxf(quad_s[2 * HG + r], quad_s[3 * HG + r]));
+            const float top = fmaxf(fmaxf(quad_s[r], quad_s[N + r]), fmaxf(quad_s[2 * N + r], quad_s[3 * N + r]));
             const float was = started ? nm0[r] : -INFINITY;
             const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
             const bool none = was == -INFINITY, over = top > -INFINITY && (none || top + was > 11.0f);
             const float now = over ? to : was;
             const float f = over && !none ? ex2(to - was) : 1.0f;
             // (all four warps write the same)
-            nm_s[cur * HG + r] = now;
-            f_s[cur * HG + r] = f;
+            nm_s[cur * N + r] = now;
+            f_s[cur * N + r] = f;
             some = f != 1.0f;
             far = now > -INFINITY && fabsf(now) > 1048576.0f;
           }
@@ -659,16 +661,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
           some = __any_sync(0xffffffffu, some);
           exact = __any_sync(0xffffffffu, far);
           if (some) {
-            const float* f = f_s + cur * HG;
+            const float* f = f_s + cur * N;
 #pragma unroll
-            for (int r = 0; r < HG; ++r) l[r] *= f[r];
+            for (int r = 0; r < N; ++r) l[r] *= f[r];
             // the last products with this result
-            const int last = TURNS ? g - 2 : g - 1;
-            ok = wait(pv_done + (last & 1), last >> 1 & 1);
+            ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
             tc::fence_after_sync();
             if (ok) {
 #pragma unroll 1
-              for (int j = 0; j < HG; j += 8) {
+              for (int j = 0; j < N; j += 8) {
                 float o[8];
                 att::tmem_load(o_addr + j, o);
 #pragma unroll
@@ -683,14 +684,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         ref = tile->ref;
         tc::fence_before_sync();
-        arrive(s_empty + buf);
+        arrive(s_empty + wg);
         // the weights' place: of the products two tiles before (a wait that was given up is told
         // of in the next vote)
-        if (g >= 2 && ok) ok = wait(pv_done + buf, (g - 2) >> 1 & 1);
+        if (g >= 2 && ok) ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
         const float share_b = ex2(-k.y);  // (b goes out of the denominators)
-        const uint32_t p0 = tc::smem_u32(smem + C::P_OFF + buf * C::PB);
+        const uint32_t p0 = tc::smem_u32(smem + C::P_OFF + wg * C::PB);
 #pragma unroll
-        for (int j = 0; j < HG; j += 8) {
+        for (int j = 0; j < N; j += 8) {
           uint4 y = make_uint4(0, 0, 0, 0);
           if (seen) {
 #pragma unroll
@@ -705,59 +706,52 @@ __global__ void __launch_bounds__(kTThreads, 1)
             y = make_uint4(pack_f16(v[j], v[j + 1]), pack_f16(v[j + 2], v[j + 3]),
                            pack_f16(v[j + 4], v[j + 5]), pack_f16(v[j + 6], v[j + 7]));
           }
-          att::st_shared16(p0 + p_chunk(row, c0 + j), y);
+          att::st_shared16(p0 + p_chunk(row, j), y);
         }
-        arrive(p_full + buf);
+        arrive(p_full + wg);
       }
       if (some_of_us(!ok)) break;
       // ---- the result ----
       const bool part = s.part >= 0;
-      if (TURNS && wg == 1) ok = wait(ml_empty, (segs & 1) ^ 1);  // (the last ones are read)
+      if (wg == 1) ok = wait(ml_empty, (segs & 1) ^ 1);  // (the last ones are read)
 #pragma unroll
-      for (int j = 0; j < HG; j += 16) {
+      for (int j = 0; j < N; j += 16) {
         const float sum = att::reduce_columns<16, false>(reinterpret_cast<float(&)[16]>(l[j]), lane);
-        if (!(lane & 1)) sum_s[quad * HG + j + lane / 2] = sum;
+        if (!(lane & 1)) sum_s[quad * N + j + lane / 2] = sum;
       }
-      const int r = lane % HG;  // a lane a column
-      const float nm = started ? nm_s[cur * HG + r] : -INFINITY;
+      const int r = lane % N;  // a column
+      const float nm = started ? nm_s[cur * N + r] : -INFINITY;
       arrive(q_empty + (segs & 1));  // (their powers of two)
-      if (TURNS && wg == 1) {
+      if (wg == 1) {
         // the first warpgroup takes this one's sums, references and result along
-        if (quad == 0 && lane < HG) told_s[r] = nm;
-        if (quad == 0 && lane == 0) told_s[HG] = ref;
+        if (quad == 0 && lane < N) told_s[r] = nm;
+        if (quad == 0 && lane == 0) told_s[N] = ref;
         arrive(ml_full);
         if (some_of_us(!ok)) break;
         g0 += T;
         continue;
       }
-      if (TURNS) ok = wait(ml_full, segs & 1);
-      ok = ok && wait(o_full, segs & 1);
+      ok = wait(ml_full, segs & 1) && wait(o_full, segs & 1);
       if (some_of_us(!ok)) break;
       tc::fence_after_sync();
       // of this lane's column: factors of the results, so that the sum of weights is 1
-      auto sum_of = [&](const float* x) { return (x[r] + x[HG + r]) + (x[2 * HG + r] + x[3 * HG + r]); };
-      const bool mine = !TURNS || T > 1 || !(g0 & 1), other = TURNS && (T > 1 || (g0 & 1));
-      float f1 = 1.0f, f2 = 0.0f, sum = sum_of(sum_s), m = nm;
-      if (TURNS) {
-        const float* theirs = sum_s + C::SOFT / 4;  // the second warpgroup's
-        const float nm2 = theirs[4 * HG + r], l2 = sum_of(theirs);
-        if (!mine) ref = theirs[5 * HG];
-        // one reference for both; -inf: no key so far
-        const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
-        f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
-        f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
-        sum = sum * f1 + l2 * f2;
-        m = both == INFINITY ? -INFINITY : both;
-      }
+      auto sum_of = [&](const float* x) { return (x[r] + x[N + r]) + (x[2 * N + r] + x[3 * N + r]); };
+      const bool mine = T > 1 || !(g0 & 1), other = T > 1 || (g0 & 1);
+      const float* theirs = sum_s + C::SOFT / 4;  // the second warpgroup's
+      const float nm2 = theirs[4 * N + r];
+      if (!mine) ref = theirs[5 * N];
+      // one reference for both; -inf: no key so far
+      const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
+      float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm), f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
+      const float sum = sum_of(sum_s) * f1 + sum_of(theirs) * f2, m = both == INFINITY ? -INFINITY : both;
       const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
       f1 *= norm;
       f2 *= norm;
-      const int heads = min(a.G - c0, HG);
-      const size_t at = (size_t)s.row0 * Hq + (size_t)s.hk * a.G + c0;  // the first head of out
-      const size_t part_at = (size_t)max(s.part, 0) * a.rows + c0;
+      const size_t at = (size_t)s.row0 * Hq + (size_t)s.hk * a.G;  // the first head of out
+      const size_t part_at = (size_t)max(s.part, 0) * a.rows;
       if (quad * 32 < D) {
 #pragma unroll 1
-        for (int j = 0; j < heads; j += 8) {
+        for (int j = 0; j < a.G; j += 8) {
           float o[8], x[8];
           if (mine) att::tmem_load(o_addr + j, o);
           if (other) att::tmem_load(o_addr + 64 + j, x);
@@ -767,22 +761,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
             float y = 0.0f;
             if (mine) y = o[e] * a1;
             if (other) y += x[e] * a2;
-            if (j + e < heads) {
+            if (j + e < a.G) {
               if (part) a.part[(part_at + j + e) * D + row] = y;
               else a.out[(at + j + e) * D + row] = __float2bfloat16_rn(y);
             }
           }
         }
       }
-      if (quad == 0 && lane < heads) {
+      if (quad == 0 && lane < a.G) {
         if (part) a.ml[part_at + lane] = make_float2(sum, m);
         else if (a.lse) a.lse[at + lane] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
       }
       tc::fence_before_sync();
       arrive(o_empty);
-      if (TURNS) {
-        if (lane == 0) tc::mbar_arrive(ml_empty);
-      }
+      arrive(ml_empty);
       g0 += T;
     }
   }
@@ -795,8 +787,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 }
 
+// (the parts are joined after the general kernel, or by `join`)
 template <class C>
-cudaError_t launch_attend_tokens(const AttendArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_attend_tokens(const AttendArgs& a, int ctas, bool join, cudaStream_t st) {
   auto kernel = k_attend_tokens<C>;
   CUtensorMap k_map, v_map;
   const uint64_t rows = (uint64_t)a.s.N * a.s.P;
@@ -817,7 +810,7 @@ cudaError_t launch_attend_tokens(const AttendArgs& a, int ctas, cudaStream_t st)
       att::launch_opted_in(reinterpret_cast<const void*>(kernel), C::SMEM, &opted_in, [&] {
         return launch_early(kernel, (unsigned)ctas, kTThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !join) return e;
   return launch_early(k_join_parts<C::D>, (unsigned)(ctas * kJoinBlocks), kJoinThreads, 0, st, 1, a,
                       ctas);
 }
