@@ -5,7 +5,8 @@ namespace hytopk {
 namespace pages {
 
 cudaError_t launch_attend_pages_d128(const AttendArgs& a, int ctas, cudaStream_t st) {
-  return launch_attend_pages<PCfg<128>>(a, ctas, st);
+  return a.several ? launch_attend_pages<PCfg<128>, true>(a, ctas, st)
+                   : launch_attend_pages<PCfg<128>, false>(a, ctas, st);
 }
 
 }  // namespace pages

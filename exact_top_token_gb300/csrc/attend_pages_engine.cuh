@@ -438,7 +438,9 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
   return ok != 0;
 }
 
-template <class C>
+// SECOND: launched behind the kernel of single rows, for calls that this one found not to be its
+// own. An instance of its own, because the return at the top costs the others 1 to 2 %.
+template <class C, bool SECOND>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_pages(const AttendArgs a, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map) {
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Share* share = reinterpret_cast<Share*>(ml_s);           // (before anything else is there)
   int64_t* scan_s = reinterpret_cast<int64_t*>(const_s);
 
-  if (a.several) {
+  if (SECOND) {
     allow_next();
     wait_for_earlier();
     if (!ld_after(a.several)) return;
@@ -1446,9 +1448,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   }
 }
 
-template <class C>
+template <class C, bool SECOND>
 cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) {
-  auto kernel = k_attend_pages<C>;
+  auto kernel = k_attend_pages<C, SECOND>;
   // rows of one head of a pool [N P rows, Hkv d]
   CUtensorMap k_map, v_map;
   const uint64_t rows = (uint64_t)a.s.N * a.s.P;
