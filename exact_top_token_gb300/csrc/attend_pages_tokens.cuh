@@ -22,11 +22,11 @@
 // operands of 128 rows among them; here the keys' f16 form goes to tensor memory.
 //
 //   warp 0        products with V; tensor memory
-//   warp 1        this CTA's segments: (item, tiles) in order, through a ring
+//   warp 1        this CTA's segments: (item, tiles) in order, and the tiles' scales, through rings
 //   warp 2        codes of the tiles by TMA
 //   warp 3        products with K
 //   warps 4-11    softmax, two warpgroups; results
-//   warps 12-15   K's codes to f16, into tensor memory; queries; the tiles' scales, through a ring
+//   warps 12-15   K's codes to f16, into tensor memory; queries
 //   warps 16-19   V's codes to f16, into shared memory
 #pragma once
 
@@ -56,14 +56,10 @@ struct TCfg {
   static constexpr int SOFT_OFF = QS_OFF + 2 * N * 4;
   static constexpr int SHARE_OFF = SOFT_OFF + 2 * SOFT;
   static constexpr int BAR_OFF = SHARE_OFF + (int)sizeof(Share);
-  static constexpr int SMEM = BAR_OFF + 640 + 1024;
+  static constexpr int SMEM = BAR_OFF + 768 + 1024;
   static constexpr int K_COL = 0, S_COL = 128, O_COL = 256, COLS = 512;  // two each
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(SEG_OFF % 16 == 0 && SHARE_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
-  // The scales of a tile are written before its K is widened: K of the tile before has its place
-  // then, so the scores of the tile three before are done, and the softmax has read those
-  // of the one another two before.
-  static_assert(5 < kConsts, "scales");
 };
 constexpr int kTThreads = 640;
 // Registers: 96 a thread at launch; the widening warps keep them.
@@ -113,12 +109,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t* seg_full = q_empty + 2;        // [kSegs]
   uint64_t* seg_empty = seg_full + kSegs;  // [kSegs]
   uint64_t* c_full = seg_empty + kSegs;    // [kConsts] scales of a tile
-  uint64_t* unit_full = c_full + kConsts;  // [UNITS] codes
+  uint64_t* c_empty = c_full + kConsts;    // [kConsts]
+  uint64_t* unit_full = c_empty + kConsts;  // [UNITS] codes
   uint64_t* unit_empty = unit_full + UNITS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + UNITS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* several_s = abort_flag + 1;  // some sequence has several rows
-  static_assert((24 + 2 * kSegs + kConsts + 2 * UNITS) * 8 + 12 <= 640, "barriers");
+  static_assert((24 + 2 * kSegs + 2 * kConsts + 2 * UNITS) * 8 + 12 <= 768, "barriers");
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -142,7 +139,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       tc::mbar_init(seg_full + i, 1);
       tc::mbar_init(seg_empty + i, 3 + 16);
     }
-    for (int i = 0; i < kConsts; ++i) tc::mbar_init(c_full + i, 1);
+    for (int i = 0; i < kConsts; ++i) {
+      tc::mbar_init(c_full + i, 1);
+      tc::mbar_init(c_empty + i, 4);
+    }
     for (int i = 0; i < UNITS; ++i) {
       tc::mbar_init(unit_full + i, 1);
       tc::mbar_init(unit_empty + i, 4);
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   };
   // A role's walk over the tiles of the segments, in order.
   struct At {
-    int b, hk, row, end, t, t0, t1, number;
+    int hk, row, end, t, t0, t1, number;
     bool ok;
   };
   auto settle = [&](At& c) {  // to the next tile at or after c
@@ -188,7 +188,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
       Seg s;
       c.ok = take(c.number, s) && !(s.flags & kStop);
       ++c.number;
-      c.b = s.b;
       c.hk = s.hk;
       c.row = s.row0;
       c.end = s.end;
@@ -204,16 +203,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
     return c;
   };
   auto begin = [&]() {
-    At c{0, 0, 0, 0, 0, 0, 0, 0, true};
+    At c{0, 0, 0, 0, 0, 0, 0, true};
     settle(c);
     return c;
   };
 
-  // The page of the lane's group of 16 keys (eight lanes have one each); -1: none there.
-  auto page_of = [&](const At& c) -> int {
-    const int key = c.t * 128 + (lane & 7) * 16;
-    if (!c.ok || key >= c.end) return -1;
-    return ld_after(a.s.table + (size_t)c.b * a.s.columns + (key >> a.shift));
+  // Pages of four tiles from t on, a lane a group of 16 keys; -1: none there.
+  auto pages_of = [&](int b, int t, int end) -> int {
+    const int key = t * 128 + lane * 16;
+    return key < end ? ld_after(a.s.table + (size_t)b * a.s.columns + (key >> a.shift)) : -1;
   };
 
   if (warp < 4) {
@@ -228,7 +226,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (lane == 0 && several) share->any = 0;
         __syncwarp();
       }
-      int number = 0;
+      // The scales of a segment's tiles follow it, up to kConsts tiles ahead of the softmax.
+      const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
+      int number = 0, g = 0;
       segments<D>(a, *share, lane, [&](const Seg& s) {
         if (!wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1)) return false;
         if (lane == 0) {
@@ -236,19 +236,56 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
+        float ref = 1.0f;
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1; t += 4) {
+          const int page = pages_of(s.b, t, min(s.end, s.t1 * 128));
+          const bool in = page >= 0 && page < a.s.N, past = t * 128 + lane * 16 >= s.end;
+          float2 sc = make_float2(0.0f, 0.0f);
+          if (in) {
+            const size_t at = (size_t)page * a.Hkv + s.hk;
+            sc = make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
+          }
+          if (page != -1 && !in && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+          const bool k_ok = sc.x > 0.0f && sc.x <= att::kLargest;
+          const bool v_ok = sc.y > 0.0f && sc.y <= att::kLargest;
+          if (in && !(k_ok && v_ok) && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
+          if (t == s.t0) {  // the largest of a segment's first tile is the reference
+            float top = lane < 8 && in && v_ok ? sc.y : 0.0f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
+          }
+          const float nan = __int_as_float(0x7fc00000);
+          float2 group = make_float2(1.0f, 0.0f);  // (masked keys: any factor will do)
+          if (in) {
+            group.x = k_ok ? fmaxf(c_scale * sc.x, 1.17549435e-38f) : nan;
+            group.y = v_ok ? fminf(fmaxf(log2f(sc.y * (1.0f / ref)), -100.0f), 100.0f) : nan;
+          }
+          const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past);
+#pragma unroll 1
+          for (int k = 0; k < 4 && t + k < s.t1; ++k, ++g) {
+            const int slot = g % kConsts;
+            if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
+            TileConst* out = const_s + slot;
+            if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
+            if (lane == 0) {
+              out->ref = ref;
+              out->absent = absent >> (8 * k) & 0xFFu;
+            }
+            arrive(c_full + slot);
+          }
+        }
         return true;
       });
     } else if (warp == 2) {
       // ---------------- codes of the tiles ----------------
       // They come by TMA, as many rows at a time as a page and a tile share (a page that is not
-      // there lies past the pool's end, where rows of zeros are). The pages of the tile after
-      // next are loaded while this one's codes go out.
-      At c0 = begin();
-      At c1 = next(c0);
-      int page0 = page_of(c0), page1 = page_of(c1);
+      // there lies past the pool's end, where rows of zeros are).
       int unit = 0;
       uint32_t used = 0, phases = 0;  // bits of the units' places
-      auto copy = [&](const CUtensorMap* map, const At& c, int page) -> bool {
+      // tile t of a segment, whose pages eight lanes from `first` on have
+      auto copy = [&](const CUtensorMap* map, int hk, int t, int page, int first) -> bool {
         const uint32_t bit = 1u << unit;
         if (!wait(unit_empty + unit, (phases & bit) ? 0u : 1u)) return false;
         phases ^= bit;
@@ -258,11 +295,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         __syncwarp();
 #pragma unroll 1
         for (int r = 0; r < 128; r += a.box) {
-          const int pg = __shfl_sync(0xffffffffu, page, r >> 4);
+          const int pg = __shfl_sync(0xffffffffu, page, first + (r >> 4));
           const int row = (uint32_t)pg < (uint32_t)a.s.N
-                              ? (pg << a.shift) + ((c.t * 128 + r) & (a.s.P - 1))
+                              ? (pg << a.shift) + ((t * 128 + r) & (a.s.P - 1))
                               : a.s.N << a.shift;
-          if (elect_one()) tc::tma_load_2d(to + r * D, map, unit_full + unit, c.hk * D, row);
+          if (elect_one()) tc::tma_load_2d(to + r * D, map, unit_full + unit, hk * D, row);
           __syncwarp();
         }
         if (++unit == UNITS) unit = 0;
@@ -274,16 +311,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       // (what earlier kernels stored is read by the copies' own path)
       asm volatile("fence.proxy.async.global;" ::: "memory");
+      Seg s;
       bool ok = true;
 #pragma unroll 1
-      while (c0.ok) {
-        const At c2 = next(c1);
-        const int page2 = page_of(c2);
-        if (!(ok = copy(&k_map, c0, page0) && copy(&v_map, c0, page0))) break;
-        c0 = c1;
-        c1 = c2;
-        page0 = page1;
-        page1 = page2;
+      for (int segs = 0; ok && take(segs, s) && !(s.flags & kStop); ++segs) {
+        int page = pages_of(s.b, s.t0, s.end), next = -1;
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1; ++t) {
+          const int first = (t - s.t0) % 4 * 8;
+          if (first == 0) {  // (the four after these, as early)
+            if (t > s.t0) page = next;
+            if (t + 4 < s.t1) next = pages_of(s.b, t + 4, s.end);
+          }
+          if (!(ok = copy(&k_map, s.hk, t, page, first) && copy(&v_map, s.hk, t, page, first))) break;
+        }
       }
       if (!ok || *abort_flag) {
         // given up: copies in flight land before the CTA ends (a bounded wait)
@@ -453,61 +494,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (c == 0) qs_s[qb * N + r] = __int_as_float((ex + 127) << 23);
       }
     };
-    // The scales of a tile (the first warp's): loaded a tile ahead, their pages two.
-    auto scales_of = [&](const At& c, int page) -> float2 {
-      if (page < 0 || page >= a.s.N) return make_float2(0.0f, 0.0f);
-      const size_t at = (size_t)page * a.Hkv + c.hk;
-      return make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
-    };
-    const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
-    float ref = 1.0f, inv_ref = 1.0f;
-    auto scales = [&](int g, const At& c, int page, float2 sc) {
-      const bool in = page >= 0 && page < a.s.N;
-      if (page != -1 && !in && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-      const bool k_ok = sc.x > 0.0f && sc.x <= att::kLargest;
-      const bool v_ok = sc.y > 0.0f && sc.y <= att::kLargest;
-      if (in && !(k_ok && v_ok) && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
-      if (c.t == c.t0) {  // the largest of a segment's first tile is the reference
-        float top = in && v_ok ? sc.y : 0.0f;
-#pragma unroll
-        for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
-        inv_ref = 1.0f / ref;
-      }
-      const float nan = __int_as_float(0x7fc00000);
-      const bool past = c.t * 128 + (lane & 7) * 16 >= c.end;
-      float2 group = make_float2(1.0f, 0.0f);  // (masked keys: any factor will do)
-      if (in) {
-        group.x = k_ok ? fmaxf(c_scale * sc.x, 1.17549435e-38f) : nan;
-        group.y = v_ok ? fminf(fmaxf(log2f(sc.y * inv_ref), -100.0f), 100.0f) : nan;
-      }
-      const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past) & 0xFFu;
-      TileConst* out = const_s + g % kConsts;
-      if (lane < 8) reinterpret_cast<float2*>(out->group)[lane] = group;
-      if (lane == 0) {
-        out->ref = ref;
-        out->absent = absent;
-      }
-      arrive(c_full + g % kConsts);
-    };
     int unit = 0, g = 0, items = 0;
     uint32_t phase = 0;
-    At at = begin(), at1 = next(at), at2;
-    int page = -1, page1 = -1, page2 = -1;
-    float2 sc = make_float2(0.0f, 0.0f), sc1 = sc;
-    if (quad == 0) {
-      page = page_of(at);
-      page1 = page_of(at1);
-      sc = scales_of(at, page);
-    }
 #pragma unroll 1
-    for (; at.ok; at = at1, at1 = at2, page = page1, page1 = page2, sc = sc1, ++g) {
-      at2 = next(at1);
-      if (quad == 0) {
-        page2 = page_of(at2);
-        sc1 = scales_of(at1, page1);
-        scales(g, at, page, sc);
-      }
+    for (At at = begin(); at.ok; at = next(at), ++g) {
       if (at.t == at.t0) {
         const int qb = items & 1;
         if (!wait(q_empty + qb, ((items >> 1) & 1) ^ 1)) break;
@@ -685,6 +675,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ref = tile->ref;
         tc::fence_before_sync();
         arrive(s_empty + wg);
+        if (lane == 0) tc::mbar_arrive(c_empty + g % kConsts);
         // the weights' place: of the products two tiles before (a wait that was given up is told
         // of in the next vote)
         if (g >= 2 && ok) ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
