@@ -36,8 +36,8 @@
 // themselves, pieces of 128 bytes 1 KB apart come at 4.1 TB/s, whole rows at 5.4.
 //
 //   warp 0        tensor memory
-//   warp 1        this CTA's segments: (item, tiles) in order, through a ring
-//   warp 2        pages: codes of the tiles by TMA, their scales through a ring
+//   warp 1        this CTA's segments: (item, tiles) in order, and the tiles' scales, through rings
+//   warp 2        codes of the tiles by TMA
 //   warp 3        products
 //   warps 4-11    softmax, two warpgroups; queries; results
 //   warps 12-15   codes to f16, as they land, into the ring of operands
@@ -116,13 +116,10 @@ struct PCfg {
   static constexpr int QS_OFF = ML_OFF + 128 * 8;
   static constexpr int EPI_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;  // [8 warps][1 KB]
   static constexpr int BAR_OFF = EPI_OFF + 8 * 1024;
-  static constexpr int SMEM = BAR_OFF + 768 + 1024;
+  static constexpr int SMEM = BAR_OFF + 896 + 1024;
   static constexpr int S_COL = 0, O_COL = 256, COLS = 512;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NS % 2 == 0, "K in even slots, V in odd ones");
-  // The scales of a tile are written once its K has a place: the tile SMALL_UNITS / 2 before
-  // it is widened then, so the one NS / 2 before that is done with.
-  static_assert((SMALL_UNITS + 1) / 2 + NS / 2 + 1 < kConsts, "scales");
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -418,6 +415,51 @@ __device__ __forceinline__ void segments(const AttendArgs& a, const Share& share
   if (ok) push(s);
 }
 
+// Pages of four tiles from t on, a lane a group of 16 keys; -1: none there.
+__device__ __forceinline__ int pages_of(const AttendArgs& a, int lane, int b, int t, int end) {
+  const uint32_t key = (uint32_t)t * 128 + lane * 16;  // (may pass 2^31)
+  return key < (uint32_t)end ? ld_after(a.s.table + (size_t)b * a.s.columns + (key >> a.shift)) : -1;
+}
+
+// A segment's scales, four tiles at a time: put(k, group, ref, absent) for its tiles in order, of
+// which the lanes from 8 k on have the groups; put tells whether to go on. One warp.
+template <class Put>
+__device__ __forceinline__ bool segment_scales(const AttendArgs& a, const Seg& s, int lane, Put put) {
+  const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
+  float ref = 1.0f;
+#pragma unroll 1
+  for (int t = s.t0; t < s.t1; t += 4) {
+    const int page = pages_of(a, lane, s.b, t, s.end);
+    const bool in = page >= 0 && page < a.s.N, past = (uint32_t)t * 128 + lane * 16 >= (uint32_t)s.end;
+    float2 sc = make_float2(0.0f, 0.0f);
+    if (in) {
+      const size_t at = (size_t)page * a.Hkv + s.hk;
+      sc = make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
+    }
+    if (page != -1 && !in && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
+    const bool k_ok = sc.x > 0.0f && sc.x <= att::kLargest;
+    const bool v_ok = sc.y > 0.0f && sc.y <= att::kLargest;
+    if (in && !(k_ok && v_ok) && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
+    if (t == s.t0) {  // the largest of a segment's first tile is the reference
+      float top = lane < 8 && in && v_ok ? sc.y : 0.0f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
+    }
+    const float nan = __int_as_float(0x7fc00000);
+    float2 group = make_float2(1.0f, 0.0f);  // (masked keys: any factor will do)
+    if (in) {
+      group.x = k_ok ? fmaxf(c_scale * sc.x, 1.17549435e-38f) : nan;
+      group.y = v_ok ? fminf(fmaxf(log2f(sc.y * (1.0f / ref)), -100.0f), 100.0f) : nan;
+    }
+    const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past);
+#pragma unroll 1
+    for (int k = 0; k < 4 && t + k < s.t1; ++k)
+      if (!put(k, group, ref, absent >> (8 * k) & 0xFFu)) return false;
+  }
+  return true;
+}
+
 // ---- the kernel -------------------------------------------------------------------------
 
 // Wait for a phase of `bar`; gives up (false, abort flag) when another role has, or after
@@ -467,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* seg_full = ml_empty + 1;  // [kSegs]
   uint64_t* seg_empty = seg_full + kSegs;
   uint64_t* c_full = seg_empty + kSegs;       // [kConsts] scales of a tile
-  uint64_t* unit_full = c_full + kConsts;     // [SMALL_UNITS] codes
+  uint64_t* c_empty = c_full + kConsts;       // [kConsts]
+  uint64_t* unit_full = c_empty + kConsts;    // [SMALL_UNITS] codes
   uint64_t* unit_empty = unit_full + C::SMALL_UNITS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_empty + C::SMALL_UNITS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -502,7 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(seg_full + i, 1);
       tc::mbar_init(seg_empty + i, 1 + 1 + 8 + 4);
     }
-    for (int i = 0; i < kConsts; ++i) tc::mbar_init(c_full + i, 1);
+    for (int i = 0; i < kConsts; ++i) {
+      tc::mbar_init(c_full + i, 1);
+      tc::mbar_init(c_empty + i, 8);
+    }
     for (int i = 0; i < C::SMALL_UNITS; ++i) {
       tc::mbar_init(unit_full + i, 1);
       tc::mbar_init(unit_empty + i, 4);
@@ -547,71 +593,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
     if (warp == 1) {
       // ---------------- segments ----------------
-      int number = 0;
+      // The scales of a segment's tiles follow it, up to kConsts tiles ahead of the softmax.
+      int number = 0, g = 0;
       segments<D>(a, *share, lane, [&](const Seg& s) {
-        const bool ok = wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1);
-        if (!ok) return false;
+        if (!wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1)) return false;
         if (lane == 0) {
           seg_s[number % kSegs] = s;
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
-        return true;
+        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t absent) {
+          const int slot = g % kConsts;
+          if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
+          TileConst* out = const_s + slot;
+          if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
+          if (lane == 0) {
+            out->ref = ref;
+            out->absent = absent;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(c_full + slot);
+          ++g;
+          return true;
+        });
       });
     } else if (warp == 2) {
-      // ---------------- codes and scales of the tiles ----------------
-      // Lanes 0 .. 7 take a group each: its page and its scales. The codes come by TMA, as many
-      // rows at a time as a page and a tile share (a page that is not there lies past the
-      // pool's end, where rows of zeros are); eight copies for each tile, issued by a lane
-      // each, took 2500 cycles of it. The page of the tile after next and the scales of the
-      // next one are loaded while this one's go out.
-      struct At {
-        int b, hk, end, t, t1, flags, number;
-        bool ok;
-      };
-      auto settle = [&](At& c) {  // to the next tile at or after c
-        while (c.ok && c.t >= c.t1) {
-          Seg s;
-          c.ok = take(c.number, s) && !(s.flags & kStop);
-          ++c.number;
-          c.b = s.b;
-          c.hk = s.hk;
-          c.end = s.end;
-          c.t = s.t0;
-          c.t1 = s.t1;
-          c.flags = s.flags;
-        }
-      };
-      auto next = [&](At c) {
-        if (c.ok) {
-          ++c.t;
-          settle(c);
-        }
-        return c;
-      };
-      auto page_of = [&](const At& c) -> int {
-        const int key = c.t * 128 + (lane & 7) * 16;
-        if (!c.ok || key >= c.end) return -1;
-        return ld_after(a.s.table + (size_t)c.b * a.s.columns + (key >> a.shift));
-      };
-      auto scales_of = [&](const At& c, int page) -> float2 {
-        if (page < 0 || page >= a.s.N) return make_float2(0.0f, 0.0f);
-        const size_t at = (size_t)page * a.Hkv + c.hk;
-        return make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
-      };
-      const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
-      At c0{0, 0, 0, 0, 0, 0, 0, true};
-      settle(c0);
-      At c1 = next(c0);
-      int page0 = page_of(c0), page1 = page_of(c1);
-      float2 sc0 = scales_of(c0, page0);
-      int tile = 0, segs = 0;  // tiles and segments (with tiles) so far
-      float ref = 1.0f, inv_ref = 1.0f;
-      bool fresh = true;  // the segment's first tile, whose largest is the reference
+      // ---------------- codes of the tiles ----------------
+      // They come by TMA, as many rows at a time as a page and a tile share (a page that is not
+      // there lies past the pool's end, where rows of zeros are); eight copies for each tile,
+      // issued by a lane each, took 2500 cycles of it.
       bool was_large = false;
       int unit = 0;
       uint32_t used = 0, phases = 0;  // bits of the units' places
-      auto copy = [&](const CUtensorMap* map, const At& c, int page) -> bool {
+      // tile t of a segment, whose pages eight lanes from `first` on have
+      auto copy = [&](const CUtensorMap* map, const Seg& s, int t, int page, int first) -> bool {
         const uint32_t bit = 1u << unit;
         if (!wait(unit_empty + unit, (phases & bit) ? 0u : 1u)) return false;
         phases ^= bit;
@@ -621,14 +636,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
 #pragma unroll 1
         for (int r = 0; r < 128; r += a.box) {
-          const int pg = __shfl_sync(0xffffffffu, page, r >> 4);
-          const int row = (uint32_t)pg < (uint32_t)a.s.N
-                              ? (pg << a.shift) + ((c.t * 128 + r) & (a.s.P - 1))
-                              : a.s.N << a.shift;
-          if (elect_one()) tc::tma_load_2d(to + r * D, map, unit_full + unit, c.hk * D, row);
+          const int pg = __shfl_sync(0xffffffffu, page, first + (r >> 4));
+          const int row = (uint32_t)pg < (uint32_t)a.s.N ? (pg << a.shift) + ((t * 128 + r) & (a.s.P - 1))
+                                                         : a.s.N << a.shift;
+          if (elect_one()) tc::tma_load_2d(to + r * D, map, unit_full + unit, s.hk * D, row);
           __syncwarp();
         }
-        unit = unit + 1 < (c.flags & kSmall ? C::SMALL_UNITS : C::UNITS) ? unit + 1 : 0;
+        unit = unit + 1 < (s.flags & kSmall ? C::SMALL_UNITS : C::UNITS) ? unit + 1 : 0;
         return true;
       };
       if (lane == 0) {
@@ -637,61 +651,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // (what earlier kernels stored is read by the copies' own path)
       asm volatile("fence.proxy.async.global;" ::: "memory");
+      Seg s;
       bool ok = true;
 #pragma unroll 1
-      while (c0.ok) {
-        const At c2 = next(c1);
-        const int page2 = page_of(c2);
-        const float2 sc1 = scales_of(c1, page1);
-        if (fresh) {
-          const bool small = c0.flags & kSmall;
-          if (C::SHARED && small == was_large) unit = 0;
-          // (the last large item's queries lie in the place of a small one's codes)
-          if (C::SHARED && small && was_large && !(ok = wait(q_empty, (segs - 1) & 1))) break;
-          was_large = !small;
+      for (int segs = 0; ok && take(segs, s) && !(s.flags & kStop); ++segs) {
+        const bool small = s.flags & kSmall;
+        if (C::SHARED && small == was_large) unit = 0;
+        // (the last large item's queries lie in the place of a small one's codes)
+        if (C::SHARED && small && was_large && !(ok = wait(q_empty, (segs - 1) & 1))) break;
+        was_large = !small;
+        int page = pages_of(a, lane, s.b, s.t0, s.end), next = -1;
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1; ++t) {
+          const int first = (t - s.t0) % 4 * 8;
+          if (first == 0) {  // (the four after these, as early)
+            if (t > s.t0) page = next;
+            if (t + 4 < s.t1) next = pages_of(a, lane, s.b, t + 4, s.end);
+          }
+          if (!(ok = copy(&k_map, s, t, page, first) && copy(&v_map, s, t, page, first))) break;
         }
-        if (!(ok = copy(&k_map, c0, page0))) break;
-        const bool in = page0 >= 0 && page0 < a.s.N;
-        if (page0 != -1 && !in && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-        const bool k_ok = sc0.x > 0.0f && sc0.x <= att::kLargest;
-        const bool v_ok = sc0.y > 0.0f && sc0.y <= att::kLargest;
-        if (in && !(k_ok && v_ok) && lane < 8 && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
-        if (fresh) {
-          float top = in && v_ok ? sc0.y : 0.0f;
-#pragma unroll
-          for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
-          inv_ref = 1.0f / ref;
-          fresh = false;
-        }
-        const float nan = __int_as_float(0x7fc00000);
-        // (masked keys: any factor will do)
-        const bool past = c0.t * 128 + (lane & 7) * 16 >= c0.end;
-        float2 group = make_float2(1.0f, 0.0f);
-        if (in) {
-          group.x = k_ok ? fmaxf(c_scale * sc0.x, 1.17549435e-38f) : nan;
-          group.y = v_ok ? fminf(fmaxf(log2f(sc0.y * inv_ref), -100.0f), 100.0f) : nan;
-        }
-        const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past) & 0xFFu;
-        TileConst* out = const_s + tile % kConsts;
-        if (lane < 8) reinterpret_cast<float2*>(out->group)[lane] = group;
-        if (lane == 0) {
-          out->ref = ref;
-          out->absent = absent;
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(c_full + tile % kConsts);
-        if (!(ok = copy(&v_map, c0, page0))) break;
-        ++tile;
-        if (c1.number != c0.number) {
-          fresh = true;
-          ++segs;
-        }
-        c0 = c1;
-        c1 = c2;
-        page0 = page1;
-        page1 = page2;
-        sc0 = sc1;
       }
       if (!ok || *abort_flag) {
         // given up: copies in flight land before the CTA ends (a bounded wait)
@@ -1155,6 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(p_full + w);
+        if (lane < (small ? 2 : 1)) tc::mbar_arrive(c_empty + number_c % kConsts);
       }
       if (!ok) break;
       if (T > 0) {

@@ -208,12 +208,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
     return c;
   };
 
-  // Pages of four tiles from t on, a lane a group of 16 keys; -1: none there.
-  auto pages_of = [&](int b, int t, int end) -> int {
-    const int key = t * 128 + lane * 16;
-    return key < end ? ld_after(a.s.table + (size_t)b * a.s.columns + (key >> a.shift)) : -1;
-  };
-
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsCtl));
     if (warp == 1) {
@@ -227,7 +221,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         __syncwarp();
       }
       // The scales of a segment's tiles follow it, up to kConsts tiles ahead of the softmax.
-      const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
       int number = 0, g = 0;
       segments<D>(a, *share, lane, [&](const Seg& s) {
         if (!wait(seg_empty + number % kSegs, ((number / kSegs) & 1) ^ 1)) return false;
@@ -236,47 +229,20 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
-        float ref = 1.0f;
-#pragma unroll 1
-        for (int t = s.t0; t < s.t1; t += 4) {
-          const int page = pages_of(s.b, t, min(s.end, s.t1 * 128));
-          const bool in = page >= 0 && page < a.s.N, past = t * 128 + lane * 16 >= s.end;
-          float2 sc = make_float2(0.0f, 0.0f);
-          if (in) {
-            const size_t at = (size_t)page * a.Hkv + s.hk;
-            sc = make_float2(ld_after(a.k_scale + at), ld_after(a.v_scale + at));
+        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t absent) {
+          const int slot = g % kConsts;
+          if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
+          TileConst* out = const_s + slot;
+          if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
+          if (lane == 0) {
+            out->ref = ref;
+            out->absent = absent;
           }
-          if (page != -1 && !in && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_INDEX);
-          const bool k_ok = sc.x > 0.0f && sc.x <= att::kLargest;
-          const bool v_ok = sc.y > 0.0f && sc.y <= att::kLargest;
-          if (in && !(k_ok && v_ok) && a.status) atomicOr(a.status, HYTOPK_DEV_BAD_SCALE);
-          if (t == s.t0) {  // the largest of a segment's first tile is the reference
-            float top = lane < 8 && in && v_ok ? sc.y : 0.0f;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            ref = fmaxf(top > 0.0f ? top : 1.0f, 1.17549435e-38f);
-          }
-          const float nan = __int_as_float(0x7fc00000);
-          float2 group = make_float2(1.0f, 0.0f);  // (masked keys: any factor will do)
-          if (in) {
-            group.x = k_ok ? fmaxf(c_scale * sc.x, 1.17549435e-38f) : nan;
-            group.y = v_ok ? fminf(fmaxf(log2f(sc.y * (1.0f / ref)), -100.0f), 100.0f) : nan;
-          }
-          const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past);
-#pragma unroll 1
-          for (int k = 0; k < 4 && t + k < s.t1; ++k, ++g) {
-            const int slot = g % kConsts;
-            if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
-            TileConst* out = const_s + slot;
-            if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
-            if (lane == 0) {
-              out->ref = ref;
-              out->absent = absent >> (8 * k) & 0xFFu;
-            }
-            arrive(c_full + slot);
-          }
-        }
-        return true;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(c_full + slot);
+          ++g;
+          return true;
+        });
       });
     } else if (warp == 2) {
       // ---------------- codes of the tiles ----------------
@@ -315,13 +281,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int segs = 0; ok && take(segs, s) && !(s.flags & kStop); ++segs) {
-        int page = pages_of(s.b, s.t0, s.end), next = -1;
+        int page = pages_of(a, lane, s.b, s.t0, s.end), next = -1;
 #pragma unroll 1
         for (int t = s.t0; t < s.t1; ++t) {
           const int first = (t - s.t0) % 4 * 8;
           if (first == 0) {  // (the four after these, as early)
             if (t > s.t0) page = next;
-            if (t + 4 < s.t1) next = pages_of(s.b, t + 4, s.end);
+            if (t + 4 < s.t1) next = pages_of(a, lane, s.b, t + 4, s.end);
           }
           if (!(ok = copy(&k_map, s.hk, t, page, first) && copy(&v_map, s.hk, t, page, first))) break;
         }
