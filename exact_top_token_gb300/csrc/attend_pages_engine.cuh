@@ -1317,11 +1317,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 
 // Parts of an item: number 2c + 1 of the share c where it starts, then 2c' + 0 of the shares after
-// it, up to the one that ends it (shares between may hold none of it). kJoinBlocks blocks take
+// it, up to the one that ends it (shares between may hold none of it). a.join blocks take
 // the rows of the item that starts in a share, if one does that does not end there. Many parts: a
 // block a row, its warps sharing the parts; few: a warp a row.
-constexpr int kJoinBlocks = 32;
-
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a, int ctas) {
   allow_next();
@@ -1332,7 +1330,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   __shared__ float4 acc_s[WARPS][32];
   __shared__ float sum_s[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = blockIdx.x / kJoinBlocks, block = blockIdx.x % kJoinBlocks;
+  const int c = blockIdx.x / a.join, block = blockIdx.x % a.join;
   const int4 first = ld_after(a.record + 2 * c + 1);
   if (!(first.x & kStop)) return;
   if (tid == 0) last_s = ctas - 1;
@@ -1352,7 +1350,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   const bool small = first.x & kSmall, wide = count > 8;
   const int units = wide ? rows : (rows + WARPS - 1) / WARPS;
 #pragma unroll 1
-  for (int u = block; u < units; u += kJoinBlocks) {
+  for (int u = block; u < units; u += a.join) {
     const int x = wide ? u : u * WARPS + warp;  // row of the item
     const bool on = x < rows;
     const int token = x / a.G, head = x % a.G;
@@ -1451,7 +1449,7 @@ cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) 
         return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
   if (e != cudaSuccess) return e;
-  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * kJoinBlocks), kJoinThreads, 0, st, 1, a,
+  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * a.join), kJoinThreads, 0, st, 1, a,
                       ctas);
 }
 
