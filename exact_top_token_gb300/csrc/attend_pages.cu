@@ -94,9 +94,6 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
   a.record = reinterpret_cast<int4*>(ws + part_bytes(a.rows, d) + ml_bytes(a.rows));
   const int sms = num_sms(), ctas = sms < kMaxCtas ? sms : kMaxCtas;
   a.groups = std::gcd(Hkv, ctas);
-  // A block a row of an item that has many parts, up to 32; where an item is likely to have the
-  // rows of one token, as few as those: 4864 blocks that find nothing to join take 1 us more.
-  a.join = n > paged->B || a.G > 32 ? 32 : a.G < 4 ? 4 : a.G;
   cudaError_t e;
   const int64_t tiles = ((int64_t)paged->columns * paged->P + 127) / 128 * paged->B * Hkv;
   const bool tokens = n <= paged->B && a.G <= kTokenHeads && tiles >= (int64_t)kTokenTiles * ctas;

@@ -33,7 +33,6 @@ struct AttendArgs {
   // both kernels are launched: the first tells here whether some sequence has several rows, which
   // are the second's; NULL: one alone
   int* several;
-  int join;      // blocks that join the parts of an item
   int groups;    // of CTAs, by cache heads: divides Hkv and the number of CTAs
 };
 

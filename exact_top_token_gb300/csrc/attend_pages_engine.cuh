@@ -1317,40 +1317,83 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 
 // Parts of an item: number 2c + 1 of the share c where it starts, then 2c' + 0 of the shares after
-// it, up to the one that ends it (shares between may hold none of it). a.join blocks take
-// the rows of the item that starts in a share, if one does that does not end there. Many parts: a
-// block a row, its warps sharing the parts; few: a warp a row.
+// it, up to the one that ends it (shares between may hold none of it). Many parts: a block a row,
+// its warps sharing the parts; few: a warp a row. Every block finds out what there is to join,
+// from all shares' records, and takes every gridDim.x-th of it (blocks for the rows that each
+// share might start, 4864 of them, took 4 us more).
+constexpr int kJoinBlocks = 4;  // for each share
+
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a, int ctas) {
   allow_next();
   wait_for_earlier();
-  constexpr int WARPS = kJoinThreads / 32, V = D / 32;
-  __shared__ int last_s;
-  __shared__ uint32_t held[(kMaxCtas + 31) / 32];  // shares after c that hold a part
+  constexpr int WARPS = kJoinThreads / 32, V = D / 32, WORDS = kJoinThreads / 32;
+  static_assert(kMaxCtas <= kJoinThreads, "a thread a share");
+  __shared__ uint32_t held_s[WORDS], ends_s[WORDS];  // shares that hold a part begun before; ends
+  __shared__ int4 first_s[kMaxCtas];                 // what starts there and does not end
+  __shared__ int before_s[kJoinThreads + 1];         // blocks' worth of rows in the shares before
+  __shared__ int sums_s[WARPS];
   __shared__ float4 acc_s[WARPS][32];
   __shared__ float sum_s[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = blockIdx.x / a.join, block = blockIdx.x % a.join;
-  const int4 first = ld_after(a.record + 2 * c + 1);
-  if (!(first.x & kStop)) return;
-  if (tid == 0) last_s = ctas - 1;
+  int4 first0 = make_int4(0, 0, 0, 0);
+  int flags0 = 0;
+  if (tid < ctas) {
+    first0 = ld_after(a.record + 2 * tid + 1);
+    flags0 = ld_after(&a.record[2 * tid].x);
+    first_s[tid] = first0;
+  }
+  const uint32_t some = __ballot_sync(0xffffffffu, (flags0 & kStop) != 0);
+  const uint32_t end = __ballot_sync(0xffffffffu, (flags0 & kStop) && (flags0 & kEnds));
+  if (lane == 0) {
+    held_s[warp] = some;
+    ends_s[warp] = end;
+  }
   __syncthreads();
-  const int i0 = c + 1 + tid;  // (kMaxCtas <= kJoinThreads)
-  const int flags = i0 < ctas ? ld_after(&a.record[2 * i0].x) : 0;
-  if ((flags & kStop) && (flags & kEnds)) atomicMin(&last_s, i0);
-  const uint32_t some = __ballot_sync(0xffffffffu, (flags & kStop) != 0);
-  if (lane == 0 && warp < (int)(sizeof(held) / 4)) held[warp] = some;
-  __syncthreads();
-  const int count = last_s - c;  // shares after c, of which held tells
-  auto part_of = [&](int i) -> int {  // i-th share from c on; -1: no part
-    if (i == 0) return 2 * c + 1;
-    return held[(i - 1) / 32] >> ((i - 1) % 32) & 1 ? 2 * (c + i) : -1;
+  auto last_of = [&](int c) -> int {  // the share after c that ends what starts there
+    uint32_t word = ends_s[c / 32] & ~((2u << (c % 32)) - 1u);
+    int w = c / 32;
+    while (!word && ++w < WORDS) word = ends_s[w];
+    return word ? w * 32 + __ffs(word) - 1 : ctas - 1;
   };
-  const int Hq = a.Hkv * a.G, rows = first.z * a.G;
-  const bool small = first.x & kSmall, wide = count > 8;
-  const int units = wide ? rows : (rows + WARPS - 1) / WARPS;
+  auto units_of = [&](const int4& f, int count) {  // of a block each
+    const int rows = f.z * a.G;
+    return !(f.x & kStop) ? 0 : count > 8 ? rows : (rows + WARPS - 1) / WARPS;
+  };
+  {
+    int sum = tid < ctas ? units_of(first0, last_of(tid) - tid) : 0;
+    const int mine = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) sums_s[warp] = sum;
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+      if (w < warp) base += sums_s[w];
+    before_s[tid] = base + sum - mine;
+    if (tid == kJoinThreads - 1) before_s[kJoinThreads] = base + sum;
+    __syncthreads();
+  }
+  const int Hq = a.Hkv * a.G;
 #pragma unroll 1
-  for (int u = block; u < units; u += a.join) {
+  for (int at = blockIdx.x; at < before_s[kJoinThreads]; at += gridDim.x) {
+    int c = 0;  // the share that has it
+#pragma unroll
+    for (int step = kJoinThreads / 2; step; step >>= 1)
+      if (before_s[c + step] <= at) c += step;
+    const int u = at - before_s[c];
+    const int4 first = first_s[c];
+    const int count = last_of(c) - c;  // shares after c
+    auto part_of = [&](int i) -> int {  // i-th share from c on; -1: no part
+      if (i == 0) return 2 * c + 1;
+      return held_s[(c + i) / 32] >> ((c + i) % 32) & 1 ? 2 * (c + i) : -1;
+    };
+    const int rows = first.z * a.G;
+    const bool small = first.x & kSmall, wide = count > 8;
     const int x = wide ? u : u * WARPS + warp;  // row of the item
     const bool on = x < rows;
     const int token = x / a.G, head = x % a.G;
@@ -1414,14 +1457,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] *= norm;
-    const size_t at = (size_t)(first.y + token) * Hq + first.w * a.G + head;
+    const size_t to = (size_t)(first.y + token) * Hq + first.w * a.G + head;
     if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(a.out + at * D + lane * V) =
+      *reinterpret_cast<uint2*>(a.out + to * D + lane * V) =
           make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));
     else
-      *reinterpret_cast<uint32_t*>(a.out + at * D + lane * V) = att::pack_bf16(o[0], o[1]);
+      *reinterpret_cast<uint32_t*>(a.out + to * D + lane * V) = att::pack_bf16(o[0], o[1]);
     if (a.lse && lane == 0)
-      a.lse[at] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
+      a.lse[to] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
   }
 }
 
@@ -1449,7 +1492,7 @@ cudaError_t launch_attend_pages(const AttendArgs& a, int ctas, cudaStream_t st) 
         return launch_early(kernel, (unsigned)ctas, kThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
   if (e != cudaSuccess) return e;
-  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * a.join), kJoinThreads, 0, st, 1, a,
+  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * kJoinBlocks), kJoinThreads, 0, st, 1, a,
                       ctas);
 }
 

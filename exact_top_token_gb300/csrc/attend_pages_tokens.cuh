@@ -768,7 +768,7 @@ cudaError_t launch_attend_tokens(const AttendArgs& a, int ctas, bool join, cudaS
         return launch_early(kernel, (unsigned)ctas, kTThreads, C::SMEM, st, 1, a, k_map, v_map);
       });
   if (e != cudaSuccess || !join) return e;
-  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * a.join), kJoinThreads, 0, st, 1, a,
+  return launch_early(k_join_parts<C::D>, (unsigned)(ctas * kJoinBlocks), kJoinThreads, 0, st, 1, a,
                       ctas);
 }
 
