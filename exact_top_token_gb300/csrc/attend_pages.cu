@@ -16,11 +16,11 @@ cudaError_t launch_attend_tokens_d64(const AttendArgs& a, int ctas, bool join, c
 cudaError_t launch_attend_tokens_d128(const AttendArgs& a, int ctas, bool join, cudaStream_t st);
 
 constexpr int kTokenHeads = 16;
-// The kernel of single rows is taken where at most that many rows are given as there are
-// sequences, and contexts may be long enough: 64 rows over up to 16384 keys, 8 cache heads of 128
-// columns, take 208 us with it and 233 with the general one, but a cu_q may hold several rows
-// of a sequence all the same, so that both are launched and the second one mostly ends at once,
-// which takes 2 us: as much as 16 tiles of 128 keys a multiprocessor gain.
+// The kernel of single rows is taken where at most that many heads share a cache head, no more
+// rows are given than there are sequences, and contexts may be long enough: 64 rows over up to
+// 16384 keys, 8 cache heads of 128 columns, take 166 us with it and 229 with the general one. A
+// cu_q may hold several rows of a sequence all the same, so with one both are launched and the
+// second mostly ends at once, which takes 4 us: what 16 tiles of 128 keys a multiprocessor gain.
 constexpr int kTokenTiles = 16;
 
 namespace {

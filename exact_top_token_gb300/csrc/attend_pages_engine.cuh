@@ -42,14 +42,15 @@
 //   warps 4-11    softmax, two warpgroups; queries; results
 //   warps 12-15   codes to f16, as they land, into the ring of operands
 //
-// What bounds it: a prompt of 8192 tokens (32 heads of 128 on 8) takes 560 us, 980 TFLOP/s. A
-// tile of two blocks takes 4300 cycles: its products alone 2048, shared memory for them, the
+// What bounds it: a prompt of 8192 tokens (32 heads of 128 on 4) takes 540 us, 1020 TFLOP/s. A
+// tile of two blocks takes 4100 cycles: its products alone 2048, shared memory for them, the
 // codes and their f16 form 2560, the softmax 2300 on the same schedulers, and a warpgroup's
-// softmax waits for its own products. Weights handed over by halves of a tile, with scores by
-// halves (649 us) or whole (600), two more softmax warpgroups (593), twice the widening warps
-// (573) and a sum in place of the maximum (573) were slower. 64 sequences of one token over 128
-// to 32768 keys take 251 us, 3.8 TB/s: a tile takes 2500 cycles, 1750 of them shared memory's for
-// operands of 128 rows, most of which no head uses.
+// softmax waits for its own products. At 560 us, weights handed over by halves of a tile, with
+// scores by halves (649) or whole (600), two more softmax warpgroups (593), twice the widening
+// warps (573) and a sum in place of the maximum (573) were slower. One token of 64 heads on one
+// cache head over 2^20 keys takes 87 us, 3.1 TB/s: 2300 cycles a tile, 1750 of them shared
+// memory's for operands of 128 rows, half of which no head uses. Where a sequence has one token
+// and few heads share a cache head, attend_pages_tokens.cuh is faster.
 #pragma once
 
 #include "attend_engine.cuh"
@@ -1317,11 +1318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256;
 
 // Parts of an item: number 2c + 1 of the share c where it starts, then 2c' + 0 of the shares after
-// it, up to the one that ends it (shares between may hold none of it). Many parts: a block a row,
-// its warps sharing the parts; few: a warp a row. Every block finds out what there is to join,
-// from all shares' records, and takes every gridDim.x-th of it (blocks for the rows that each
-// share might start, 4864 of them, took 4 us more).
-constexpr int kJoinBlocks = 4;  // for each share
+// it, up to the one that ends it (shares between may hold none of it). Many parts or few rows: a block
+// a row, its warps sharing the parts; else eight lanes a row, 32 rows a block. Every block finds out
+// what there is to join, from all shares' records, and takes every gridDim.x-th of it. (A warp a
+// row took 37 sequences of up to 256 rows 129 us instead of 116; blocks for the rows that each
+// share might start, 4864 of them, one token 18.7 instead of 16.)
+constexpr int kJoinBlocks = 8;  // for each share
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a, int ctas) {
@@ -1356,9 +1358,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
     while (!word && ++w < WORDS) word = ends_s[w];
     return word ? w * 32 + __ffs(word) - 1 : ctas - 1;
   };
+  // a row is a block's
+  auto alone = [](int rows, int count) { return count > 8 || rows <= 16; };
   auto units_of = [&](const int4& f, int count) {  // of a block each
     const int rows = f.z * a.G;
-    return !(f.x & kStop) ? 0 : count > 8 ? rows : (rows + WARPS - 1) / WARPS;
+    return !(f.x & kStop) ? 0 : alone(rows, count) ? rows : (rows + 4 * WARPS - 1) / (4 * WARPS);
   };
   {
     int sum = tid < ctas ? units_of(first0, last_of(tid) - tid) : 0;
@@ -1393,78 +1397,117 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
       return held_s[(c + i) / 32] >> ((c + i) % 32) & 1 ? 2 * (c + i) : -1;
     };
     const int rows = first.z * a.G;
-    const bool small = first.x & kSmall, wide = count > 8;
-    const int x = wide ? u : u * WARPS + warp;  // row of the item
-    const bool on = x < rows;
+    const bool small = first.x & kSmall, wide = alone(rows, count);
+    const int x = wide ? u : (u * WARPS + warp) * 4 + lane / 8;  // row of the item
     const int token = x / a.G, head = x % a.G;
     const int half = small || token < a.tokens ? 0 : 1;
     const size_t r = half * 128 + (token - half * a.tokens) * a.G + head;
-    float top = INFINITY, sum = 0.0f, o[V];  // top: the least -m
+    const size_t to = (size_t)(first.y + token) * Hq + first.w * a.G + head;
+    float top = INFINITY, sum = 0.0f;  // top: the least -m
+    auto log_sum = [&]() { return sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2; };
+    if (!wide) {
+      const bool on = x < rows;
+      const size_t row = on ? r : 0;
+      const int l = lane & 7;  // columns 4 l + 32 c
+      float4 o[D / 32];
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.0f;
-    if (on) {
-      for (int i = lane; i <= count; i += 32) {
+      for (int e = 0; e < D / 32; ++e) o[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int i = l; i <= count; i += 8) {
         const int part = part_of(i);
         if (part < 0) continue;
-        const float m = ld_after(&a.ml[part * (size_t)a.rows + r].y);
+        const float m = ld_after(&a.ml[part * (size_t)a.rows + row].y);
         if (m > -INFINITY) top = fminf(top, m);
       }
 #pragma unroll
-      for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
-#pragma unroll 8
-      for (int i = wide ? warp : 0; i <= count; i += wide ? WARPS : 1) {
+      for (int i = 4; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+#pragma unroll 2
+      for (int i = 0; i <= count; ++i) {
         const int part = part_of(i);
         if (part < 0) continue;
-        const float2 m = ld_after(a.ml + part * (size_t)a.rows + r);
-        const float* y = a.part + (part * (size_t)a.rows + r) * D + lane * V;
-        float z[V];
-        if constexpr (V == 4) {
-          const float4 t = ld_after(reinterpret_cast<const float4*>(y));
-          z[0] = t.x, z[1] = t.y, z[2] = t.z, z[3] = t.w;
-        } else {
-          const float2 t = ld_after(reinterpret_cast<const float2*>(y));
-          z[0] = t.x, z[1] = t.y;
-        }
+        const float2 m = ld_after(a.ml + part * (size_t)a.rows + row);
+        const float4* y = reinterpret_cast<const float4*>(a.part + (part * (size_t)a.rows + row) * D) + l;
+        float4 z[D / 32];
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) z[e] = ld_after(y + 8 * e);
         // a part without rows counts nothing, but its NaN columns do
         const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
         sum += m.x * f;
+        auto add = [&](float& to, float from) { to += from == 0.0f ? 0.0f : from * f; };
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
-      }
-    }
-    if (wide) {
-      __syncthreads();
-      acc_s[warp][lane] = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
-      if (lane == 0) sum_s[warp] = sum;
-      __syncthreads();
-      if (warp) continue;
-      sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) {
-        const float4 t = acc_s[i][lane];
-        o[0] += t.x;
-        o[1] += t.y;
-        if constexpr (V > 2) {
-          o[2] += t.z;
-          o[3] += t.w;
+        for (int e = 0; e < D / 32; ++e) {
+          add(o[e].x, z[e].x);
+          add(o[e].y, z[e].y);
+          add(o[e].z, z[e].z);
+          add(o[e].w, z[e].w);
         }
-        sum += sum_s[i];
       }
+      if (!on) continue;
+      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        *reinterpret_cast<uint2*>(a.out + to * D + 32 * e + 4 * l) =
+            make_uint2(att::pack_bf16(o[e].x * norm, o[e].y * norm), att::pack_bf16(o[e].z * norm, o[e].w * norm));
+      if (a.lse && l == 0) a.lse[to] = log_sum();
+      continue;
     }
-    if (!on) continue;
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+    for (int i = lane; i <= count; i += 32) {
+      const int part = part_of(i);
+      if (part < 0) continue;
+      const float m = ld_after(&a.ml[part * (size_t)a.rows + r].y);
+      if (m > -INFINITY) top = fminf(top, m);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+#pragma unroll 8
+    for (int i = warp; i <= count; i += WARPS) {
+      const int part = part_of(i);
+      if (part < 0) continue;
+      const float2 m = ld_after(a.ml + part * (size_t)a.rows + r);
+      const float* y = a.part + (part * (size_t)a.rows + r) * D + lane * V;
+      float z[V];
+      if constexpr (V == 4) {
+        const float4 t = ld_after(reinterpret_cast<const float4*>(y));
+        z[0] = t.x, z[1] = t.y, z[2] = t.z, z[3] = t.w;
+      } else {
+        const float2 t = ld_after(reinterpret_cast<const float2*>(y));
+        z[0] = t.x, z[1] = t.y;
+      }
+      const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
+      sum += m.x * f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
+    }
+    __syncthreads();
+    acc_s[warp][lane] = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (warp) continue;
+    sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+      const float4 t = acc_s[i][lane];
+      o[0] += t.x;
+      o[1] += t.y;
+      if constexpr (V > 2) {
+        o[2] += t.z;
+        o[3] += t.w;
+      }
+      sum += sum_s[i];
+    }
     const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] *= norm;
-    const size_t to = (size_t)(first.y + token) * Hq + first.w * a.G + head;
     if constexpr (V == 4)
       *reinterpret_cast<uint2*>(a.out + to * D + lane * V) =
           make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));
     else
       *reinterpret_cast<uint32_t*>(a.out + to * D + lane * V) = att::pack_bf16(o[0], o[1]);
-    if (a.lse && lane == 0)
-      a.lse[to] = sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2;
+    if (a.lse && lane == 0) a.lse[to] = log_sum();
   }
 }
 
