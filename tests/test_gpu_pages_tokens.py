@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import exact_top_token_gb300 as hk
-from test_gpu_pages_attend import Case, cuda
+from test_gpu_pages_attend import Case as AnyCase
+from test_gpu_pages_attend import cuda
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +15,16 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def built():
     hk.build()
+
+
+class Case(AnyCase):
+    """With a table so wide that contexts may be long: calls of no more rows than sequences have a
+    kernel of their own then (of at most 16 heads on a cache head)."""
+
+    def __init__(self, seqs, Hkv=2, P=16, columns=None, **kw):
+        held = max([-(-s[0] // P) for s in seqs] + [1]) + 1
+        wide = 2600 * 128 // (len(seqs) * Hkv * P) + 1
+        super().__init__(seqs, Hkv=Hkv, P=P, columns=max(columns or 0, held, wide), **kw)
 
 
 def tokens(lengths, both=True, status=0, **kw):
@@ -42,7 +53,7 @@ def test_ragged_batches(d, P, G):
     tokens(lengths, Hq=2 * G, Hkv=2, d=d, P=P, seed=G)
 
 
-@pytest.mark.parametrize("length,G", [(40000, 8), (25000, 64)])
+@pytest.mark.parametrize("length,G", [(40000, 8), (30000, 16), (25000, 64)])
 def test_a_context_that_all_share(length, G):
     tokens([length], Hq=G, Hkv=1, d=128, P=64, seed=G)
 
@@ -71,18 +82,19 @@ def test_one_tile_each():
            P=16, seed=2)
 
 
-def test_weights_that_grow():
+@pytest.mark.parametrize("G", [13, 24])
+def test_weights_that_grow(G):
     """Scores that rise through a context, so that references are raised in later tiles, by rows
     of their own, and fall in others."""
     for d in (64, 128):
-        c = Case([(1500, 1), (900, 1)], Hq=24, Hkv=1, d=d, P=16, seed=4, single=True)
+        c = Case([(1500, 1), (900, 1)], Hq=G, Hkv=1, d=d, P=16, seed=4, single=True)
         c.k = (c.k & 0x87) | 0x38                              # 1 .. 1.875, of either sign
         c.q[:, 0] = torch.sign(c.q[:, 0].float()).bfloat16()
         for b in range(2):
             for j in range((c.lengths[b] + 15) // 16):
                 c.ks[c.table[b, j]] = 0.02 * (j + 1)
         c.k[..., 0] = 0x38 + 4                                  # one column for the trend
-        c.q[..., 0] = torch.linspace(-30, 30, 24).bfloat16()
+        c.q[..., 0] = torch.linspace(-30, 30, G).bfloat16()
         check(c)
 
 
@@ -93,7 +105,7 @@ def test_sizes_of_queries(size):
 
 @pytest.mark.parametrize("scale", [0.0, -0.125, 2.0, -3.0])
 def test_scale_of_either_sign(scale):
-    c = Case([(300, 1), (90, 1)], Hq=20, Hkv=1, seed=3, single=True)
+    c = Case([(300, 1), (90, 1)], Hq=15, Hkv=1, seed=3, single=True)
     c.scale = scale
     check(c)
 
@@ -149,9 +161,10 @@ def test_entries_and_scales_that_are_none():
 
 
 def test_lengths_out_of_range():
-    c = Case([(40, 1), (64, 1)], Hq=4, Hkv=2, d=64, P=16, seed=14, columns=4, single=True)
+    c = Case([(40, 1), (64, 1)], Hq=4, Hkv=2, d=64, P=16, seed=14, single=True)
+    c.lengths[1] = c.table.shape[1] * 16                   # (most of its entries are -1)
     a = c.device()
-    for given, rows in (([40, 10 ** 9], slice(None)), ([-3, 64], slice(1, None))):
+    for given, rows in (([40, 10 ** 9], slice(None)), ([-3, c.lengths[1]], slice(1, None))):
         a["lengths"] = cuda(given)
         word = torch.zeros(1, dtype=torch.int32, device="cuda")
         out, lse = hk.attend_pages(scale=c.scale, status=word, **a)
@@ -179,7 +192,7 @@ def test_strided_queries_given_results_and_same_bits():
 def test_two_streams_and_graphs():
     """Calls at once on two streams, and two captured ones, replayed with other lengths."""
     c = Case([(5000, 1), (700, 1), (64, 1)], Hq=8, Hkv=2, d=128, P=64, seed=19, single=True)
-    e = Case([(900, 1), (3000, 1)], Hq=40, Hkv=1, d=64, P=32, seed=20, single=True)
+    e = Case([(900, 1), (3000, 1)], Hq=16, Hkv=1, d=64, P=32, seed=20, single=True)
     a, b = c.device(), e.device()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -204,3 +217,40 @@ def test_two_streams_and_graphs():
     torch.cuda.synchronize()
     c.compare(*graphs[0][1])
     e.compare(*graphs[1][1])
+
+
+@pytest.mark.parametrize("new", [[3, 0, 1, 0, 0, 1], [0, 0, 0, 0, 0, 6], [1, 1, 1, 1, 2, 0], [1] * 6,
+                                 [0, 1, 0, 1, 0, 0], [0] * 6])
+@pytest.mark.parametrize("d", [64, 128])
+def test_no_more_rows_than_sequences(d, new):
+    """A cu_q of one row a sequence, or of several of some and none of others; rows of no sequence
+    behind them are left."""
+    lengths = [3000, 40, 700, 129, 1, 2600]
+    c = Case([(x, m) for x, m in zip(lengths, new)], Hq=12, Hkv=4, d=d, P=32, seed=d)
+    n = sum(new)
+    c.q = torch.cat([c.q, torch.full((6 - n, 12, d), float("nan")).bfloat16()])
+    out = torch.full((6, 12, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((6, 12), 7.0, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hk.attend_pages(scale=c.scale, out=out, lse=lse, status=word, **c.device())
+    assert word.item() == 0
+    if n:
+        c.compare(out, lse, slice(0, n))
+    assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+
+
+def test_a_graph_whose_rows_change():
+    """One captured call whose cu_q tells single rows, then several, then single ones again."""
+    c = Case([(900, 1), (3000, 1), (64, 1), (200, 1)], Hq=8, Hkv=2, d=128, P=64, seed=23, single=True)
+    a = c.device()
+    a["cu_q"] = cuda([0, 1, 2, 3, 4])
+    graph = torch.cuda.CUDAGraph()
+    hk.attend_pages(scale=c.scale, **a)
+    with torch.cuda.graph(graph):
+        out, lse = hk.attend_pages(scale=c.scale, **a)
+    for cu in ([0, 1, 2, 3, 4], [0, 0, 3, 3, 4], [0, 1, 2, 3, 4], [0, 1, 1, 1, 4]):
+        a["cu_q"].copy_(cuda(cu))
+        c.cu = cu
+        graph.replay()
+        torch.cuda.synchronize()
+        c.compare(out, lse)
