@@ -1,5 +1,6 @@
 // attend_pages.cu -- hytopk_attend_pages: host checks and dispatch; instances in
 // attend_pages_d*.cu.
+#include <cmath>
 #include <numeric>
 
 #include "attend_pages.h"
@@ -55,7 +56,7 @@ extern "C" hytopk_status hytopk_attend_pages(const void* q, int64_t q_row, const
                                              uint32_t* dev_status, cudaStream_t stream) {
   const hytopk_status s = check_paged(paged, n);
   if (s != HYTOPK_OK) return s;
-  if (Hkv < 1 || Hq < 1 || Hq % Hkv) return HYTOPK_INVALID_ARG;
+  if (Hkv < 1 || Hq < 1 || Hq % Hkv || !std::isfinite(scale)) return HYTOPK_INVALID_ARG;
   if (Hq / Hkv > 128 || (d != 64 && d != 128) || (int64_t)n * Hq >= (int64_t)1 << 31)
     return HYTOPK_UNSUPPORTED;
   // rows of a pool are numbered in 32 bits, one past the last included

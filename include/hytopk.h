@@ -587,8 +587,8 @@ typedef struct {
  * f16, which holds every e4m3 value, and queries to 2^-39 of their row's largest (a power
  * of two is taken out of each); weights are rounded to f16, 11 bits and at least 2^-28 of
  * the largest, where the result has 8.
- *   1 <= G <= 128, d in {64, 128}, n * Hq < 2^31, N * P < 2^31 - 16. Base pointers 16-byte
- *   aligned, q_row a multiple of 8.
+ *   1 <= G <= 128, d in {64, 128}, n * Hq < 2^31, N * P < 2^31 - 16, scale finite. Base
+ *   pointers 16-byte aligned, q_row a multiple of 8.
  *   workspace: hytopk_attend_pages_workspace_size bytes (parts of contexts that several
  *   multiprocessors share), 256-byte aligned; it holds nothing between calls. */
 HYTOPK_API size_t hytopk_attend_pages_workspace_size(int n, int Hq, int Hkv, int d);

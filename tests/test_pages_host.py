@@ -1,6 +1,7 @@
 """The cache in pages without a GPU: host-side argument checks of the C entry points, and of
 the Python module on tensors that only claim a device."""
 import ctypes
+import math
 import os
 import subprocess
 import sys
@@ -74,7 +75,8 @@ def test_sequences(lib, fields, status):
 
 def test_attend(lib):
     assert attend(lib, n=-1) == INVALID
-    for kw in (dict(Hkv=0), dict(Hq=0), dict(Hq=9), dict(Hq=1, Hkv=2)):
+    for kw in (dict(Hkv=0), dict(Hq=0), dict(Hq=9), dict(Hq=1, Hkv=2), dict(scale=math.nan),
+               dict(scale=-math.inf)):
         assert attend(lib, **kw) == INVALID, kw
     for kw in (dict(Hq=258), dict(d=96), dict(d=256), dict(n=1 << 28)):
         assert attend(lib, **kw) == UNSUPPORTED, kw
