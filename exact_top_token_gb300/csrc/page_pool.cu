@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kRowThreads) k_free(const Pool a, const int32_
 
 constexpr int kGrowThreads = 1024;
 
-// fresh: [N] workspace, the free pages that are given out, ascending. Between the phases
+// fresh: [2 N] workspace, the free pages that are given out, ascending. Between the phases
 // src_out holds a sequence's flags and need, dst_out its last page, then its first place in
 // `fresh`.
 __global__ void __launch_bounds__(kGrowThreads) k_grow(const Pool a, const int32_t* add,
@@ -162,10 +162,24 @@ __global__ void __launch_bounds__(kGrowThreads) k_grow(const Pool a, const int32
     }
     return r;
   };
-  // the partly filled pages that sequences of this call grow into
+  // the partly filled pages that sequences of this call grow into; of each, how many do (in
+  // `fresh`, for now) and the last of them (every sequence looking at all others took 10 us of
+  // 512)
+  int32_t* most = fresh + a.N;
   for (int b = tid; b < a.B; b += kGrowThreads) {
     const Row r = row_of(b);
     dst_out[b] = r.open ? r.last : -1;
+    if (r.open) {
+      fresh[r.last] = 0;
+      most[r.last] = -1;
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kGrowThreads) {
+    const int p = dst_out[b];
+    if (p < 0) continue;
+    atomicAdd(fresh + p, 1);
+    atomicMax(most + p, b);
   }
   __syncthreads();
   // who needs another page for it: all holders but the last, if all of them grow, else all
@@ -174,16 +188,7 @@ __global__ void __launch_bounds__(kGrowThreads) k_grow(const Pool a, const int32
     int away = 0;
     if (p >= 0) {
       const int holders = ld_after(a.refs + p);
-      if (holders > 1) {
-        int same = 0;
-#pragma unroll 8
-        for (int o = 0; o < a.B; ++o) {
-          const int q = dst_out[o];
-          same += q == p;
-          away |= q == p && o > b;
-        }
-        away |= same != holders;
-      }
+      away = holders > 1 && (__ldcg(most + p) > b || __ldcg(fresh + p) != holders);
     }
     src_out[b] = away;
   }
@@ -485,7 +490,7 @@ extern "C" hytopk_status hytopk_page_free(int32_t* table, int32_t* lengths, int3
 
 extern "C" size_t hytopk_page_workspace_size(int N) {
   if (N < 1) return 0;
-  return (((size_t)N + chunks_of(N) + 1) * sizeof(int32_t) + 255) / 256 * 256;
+  return (2 * (size_t)N + chunks_of(N) + 1) * sizeof(int32_t) / 256 * 256 + 256;
 }
 
 extern "C" hytopk_status hytopk_page_grow(int32_t* table, int32_t* lengths, int32_t* refs, int B,
