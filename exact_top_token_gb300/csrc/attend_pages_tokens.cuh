@@ -13,8 +13,8 @@
 // numbers that are raised when a weight would pass 2^11. Here a thread of the softmax owns a
 // key: k's scale, b, and whether the key is seen are its own, the denominators are summed per
 // thread and joined at an item's end, and m is agreed on by a vote of the four warps, a tile.
-// Keys past the context end have their v replaced by zeros as it is widened, all rows see the
-// same ones, so that their NaN codes reach nothing.
+// Keys past the context's end, the same for all heads, have v replaced by zeros as it is
+// widened, so that NaN codes there reach nothing.
 //
 // 64 sequences over up to 16384 keys, 32 heads of 128 on 8, take 166 us, 5.8 TB/s of the 6.7 that a
 // copy reaches (the general kernel 229). Memory bounds it, shared memory is just behind: of a tile
@@ -23,8 +23,8 @@
 // and here the keys' f16 form goes to tensor memory. A tile is a chain of short steps of
 // single warps, a few hundred cycles each however little they do, so what counts is that no
 // warp has too many of them: with both products in one warp, or the scales beside the copies
-// or the widening, one warp a tile took 2000 cycles (205 us); with pages of four tiles looked
-// up at once and the scales beside the segments, 1400. Items of 17 to 64 heads, with 64
+// or the widening, that warp took 2000 cycles a tile (205 us); with the pages of four tiles
+// looked up at once and the scales beside the segments a tile takes 1400. Items of 17 to 64 heads, with 64
 // columns, took 134 us where the general kernel takes 87 (one token over 2^20 keys, 64 heads).
 //
 //   warp 0        products with V; tensor memory

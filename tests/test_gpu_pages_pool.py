@@ -208,6 +208,26 @@ def test_compact_sizes(N):
     assert g is not None
 
 
+@pytest.mark.parametrize("N,columns", [(16383, 4000), (16384, 8192), (16384, 8193), (16385, 4000),
+                                       (5000, 9000), (70001, 20000)])
+def test_compact_around_one_block(N, columns):
+    """Pools of 16384 pages and tables of 16384 entries are the most that one block takes."""
+    t = Both(2, columns, N, 16, [3000 * 8, 2000 * 16 - 5], N)
+    t.compact()
+    t.free([0])
+    t.compact()
+
+
+def test_compact_refs_at_any_address():
+    """refs that start 4 bytes behind a 16-byte boundary."""
+    t = Both(2, 60, 300, 16, [900, 700], 4)
+    shifted = torch.zeros(301, dtype=torch.int32, device="cuda")[1:]
+    shifted.copy_(t.refs)
+    t.refs = shifted
+    t.compact()
+    t.grow([20, 300])
+
+
 def test_compact_full_and_front():
     t = Both(2, 8, 16, 16, [128, 128])
     t.compact()
