@@ -343,9 +343,11 @@ __device__ __forceinline__ void move_pages(const Pool& a, const Compact& c, int 
   if (wrong) flag(a.status, HYTOPK_DEV_BAD_INDEX);
 }
 
-// One launch instead of three: 6.3 us of the host instead of 12.3, and of the GPU 3.7 instead of
-// 7.9 for 512 pages, 8.7 instead of 10.3 for 8192; at twice those pages the gain is gone.
-constexpr int kOneThreads = 1024, kOnePages = kOneThreads * kPer, kOneEntries = 16 * kOneThreads;
+// One launch instead of three: 6.3 us of the host instead of 12.3, and of the GPU 4.3 instead of
+// 7.9 for 512 pages and 224 entries of the table, but 9.0 instead of 7.2 for 1000 and 16384, 12.2
+// instead of 9.9 for 8192 of both: taken up to 4096 of both.
+constexpr int kOneThreads = 1024, kOnePages = 4096, kOneEntries = 4096;
+static_assert(kOnePages <= kOneThreads * kPer, "a thread's pages");
 
 __global__ void __launch_bounds__(kOneThreads) k_compact_one(const Pool a, const Compact c) {
   allow_next();

@@ -208,11 +208,11 @@ def test_compact_sizes(N):
     assert g is not None
 
 
-@pytest.mark.parametrize("N,columns", [(16383, 4000), (16384, 8192), (16384, 8193), (16385, 4000),
-                                       (5000, 9000), (70001, 20000)])
+@pytest.mark.parametrize("N,columns", [(4095, 1500), (4096, 2048), (4096, 2049), (4097, 1500),
+                                       (3000, 9000), (16385, 4000), (70001, 20000)])
 def test_compact_around_one_block(N, columns):
-    """Pools of 16384 pages and tables of 16384 entries are the most that one block takes."""
-    t = Both(2, columns, N, 16, [3000 * 8, 2000 * 16 - 5], N)
+    """Pools of 4096 pages and tables of 4096 entries are the most that one block takes."""
+    t = Both(2, columns, N, 16, [1500 * 8, 1000 * 16 - 5], N)
     t.compact()
     t.free([0])
     t.compact()
