@@ -18,11 +18,12 @@ cudaError_t launch_attend_tokens_d128(const AttendArgs& a, int ctas, bool join, 
 
 constexpr int kTokenHeads = 16;
 // The kernel of single rows is taken where at most that many heads share a cache head, no more
-// rows are given than there are sequences, and contexts may be long enough: 64 rows over up to
-// 16384 keys, 8 cache heads of 128 columns, take 166 us with it and 229 with the general one. A
-// cu_q may hold several rows of a sequence all the same, so with one both are launched and the
-// second mostly ends at once, which takes 4 us: what 16 tiles of 128 keys a multiprocessor gain.
-constexpr int kTokenTiles = 16;
+// rows are given than there are sequences, and contexts may be as long as kTokenTiles tiles of
+// 128 keys a multiprocessor: 64 rows over up to 16384 keys, 8 cache heads of 128 columns, take
+// 167 us with it and 221 with the general one, over 256 keys each (7 tiles) 28 and 36. A cu_q
+// may hold several rows of a sequence all the same, so with one both are launched and the
+// second mostly ends at once, which takes 2 to 4 us; one row over 500 keys takes 15 us in all.
+constexpr int kTokenTiles = 4;
 
 namespace {
 

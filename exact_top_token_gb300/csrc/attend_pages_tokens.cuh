@@ -17,7 +17,7 @@
 // widened, so that NaN codes there reach nothing.
 //
 // 64 sequences over up to 16384 keys, 32 heads of 128 on 8, take 166 us, 5.8 TB/s of the 6.7 that a
-// copy reaches (the general kernel 229). Memory bounds it, shared memory is just behind: of a tile
+// copy reaches (the general kernel 221). Memory bounds it, shared memory is just behind: of a tile
 // 32 KB come as codes and 152 KB pass through shared memory, 1190 cycles where memory's share of an
 // SM takes 1400; the general kernel passes 224 KB, f16 keys and operands of 128 rows among them,
 // and here the keys' f16 form goes to tensor memory. A tile is a chain of short steps of
