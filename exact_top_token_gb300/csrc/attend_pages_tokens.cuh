@@ -535,7 +535,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
       float ref = 1.0f;
-      bool exact = false, started = false, ok = true;  // exact: some reference is far from 0
+      // exact: some reference is far from 0; unset: some head has none, because all scores so far
+      // are -inf or of rows that are not there
+      bool exact = false, started = false, unset = false, ok = true;
       const float* qs = qs_s + (segs & 1) * N;
 #pragma unroll 1
       for (int i = (g0 ^ wg) & 1; i < T; i += 2) {
@@ -579,9 +581,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           return fmaxf(max3(m0, v[N - 2], v[N - 1]), m1);
         };
-        bool raise = !started;
-        if (started) raise = weights() > 11.0f && seen;
-        else ok = ok && wait(q_full + (segs & 1), segs >> 1 & 1);  // (their powers of two)
+        if (!started) ok = ok && wait(q_full + (segs & 1), segs >> 1 & 1);  // (their powers of two)
+        bool raise = !started || unset;
+        if (!raise) raise = weights() > 11.0f && seen;
         if (some_of_us(raise || !ok)) {
           if (some_of_us(!ok)) {
             ok = false;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           some_of_us(false);
           const float* nm0 = nm_s + cur * N;
           cur ^= 1;
-          bool some = false, far = false;  // O to be scaled; a reference far from 0
+          bool some = false, far = false, none_yet = false;  // O to be scaled; a reference far from 0
           if (lane < N) {
             const int r = lane;
             const float top = fmaxf(fmaxf(quad_s[r], quad_s[N + r]), fmaxf(quad_s[2 * N + r], quad_s[3 * N + r]));
@@ -618,9 +620,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
             f_s[cur * N + r] = f;
             some = f != 1.0f;
             far = now > -INFINITY && fabsf(now) > 1048576.0f;
+            none_yet = r < a.G && now == -INFINITY;
           }
           __syncwarp();
           some = __any_sync(0xffffffffu, some);
+          unset = __any_sync(0xffffffffu, none_yet);
           exact = __any_sync(0xffffffffu, far);
           if (some) {
             const float* f = f_s + cur * N;
