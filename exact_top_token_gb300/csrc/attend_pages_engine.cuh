@@ -833,11 +833,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((*h & 0x7FFFu) <= 0x7C00u) continue;
           *h = 0;
           if (key >= end) continue;
-#pragma unroll 1
-          for (int i = 0; i < 2; ++i) {  // a softmax warpgroup's own, which it clears
-            atomicMin(first + i * D + e, key);
-            nan_any[nans * 2 + i] = 1;
-          }
+          // a softmax warpgroup's own, which it clears once all products with the item are
+          // done (of a small item the second one writes no result, and may not even wait for V)
+          atomicMin(first + e, key);
+          nan_any[nans * 2] = 1;
+          if (!large) continue;
+          atomicMin(first + D + e, key);
+          nan_any[nans * 2 + 1] = 1;
         }
       }
       __syncwarp();

@@ -51,3 +51,39 @@ def test_heads_whose_first_scores_are_minus_infinity(d):
     c.ks[c.table[:, :16]] = 2.0 ** 60
     out, lse = check(c)
     assert torch.isfinite(lse).all() and (out[:, ::2] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", [(100, 128), (257, 384)])
+def test_codes_of_nan_stay_in_their_sequences(lengths, d):
+    """Single tokens that see a NaN code of v, of an odd number of tiles, between pieces of
+    prompts of two blocks of rows, in no order, a dozen of both for each multiprocessor: NaN in
+    the column of those tokens, and nowhere else."""
+    g = np.random.default_rng(d)
+    G, P, B, N = 32, 128, 1800, 8
+    piece = g.random(B) < 0.4                          # (8 rows, twice those of a block)
+    new = np.where(piece, 8, 1)
+    length = np.where(piece, 300, g.integers(lengths[0], lengths[1] + 1, B))
+    tile = (length[:, None] + P - 1) // P > np.arange(3)
+    table = np.where(tile, g.integers(0, N, (B, 3)), -1)
+    # the last page of a token's context has a NaN code in one column, a page for each column
+    pages, last = N + d, (length - 1) // P
+    column = g.integers(0, d, B)
+    tokens = np.nonzero(~piece)[0]
+    table[tokens, last[tokens]] = N + column[tokens]
+    v = torch.full((pages, P, 1, d), 0x30, dtype=torch.uint8, device="cuda")
+    at = torch.arange(d, device="cuda")
+    v[N + at, 0, 0, at] = 0x7F
+    k = torch.full_like(v, 0x31)
+    q = torch.randn(int(new.sum()), G, d, device="cuda").bfloat16()
+    one = torch.ones(pages, 1, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(new)])
+    want = torch.zeros(int(new.sum()), G, d, dtype=torch.bool, device="cuda")
+    want[cuda(cu[:-1][tokens], torch.int64), :, cuda(column[tokens], torch.int64)] = True
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        out, lse = hk.attend_pages(q, k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), one, one,
+                                   cuda(table), cuda(length), cuda(cu), status=word)
+        assert word.item() == 0
+        assert torch.equal(torch.isnan(out), want)
+        assert torch.isfinite(lse).all()
