@@ -92,6 +92,10 @@ __device__ bool find_unit(const WriteArgs& a, int unit, Unit& u) {
     __syncthreads();
     if (unit < total) {
       u = found;
+      // (all sequences are reported on, those of no unit here too)
+      if (blockIdx.x == 0)
+        for (int i = b0 + kThreads + threadIdx.x; i < a.s.B; i += kThreads)
+          if (seq_of(a.s, a.n, i).bad) flag(a.status, HYTOPK_DEV_BAD_POSITION);
       return true;
     }
     base = total;
