@@ -14,6 +14,8 @@ namespace hytopk {
 namespace pages {
 namespace {
 
+constexpr int kMostPages = 1 << 30;  // of a pool: page numbers a few thousand past its end are ints
+
 struct Pool {
   int32_t* table;
   int32_t* lengths;
@@ -485,7 +487,8 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 hytopk_status check_pool(const void* table, const void* lengths, const void* refs, int B,
                          int columns, int N, int P) {
   if (B < 0 || columns < 1 || N < 1) return HYTOPK_INVALID_ARG;
-  if (!page_rows_ok(P) || (int64_t)columns * P >= (int64_t)1 << 31) return HYTOPK_UNSUPPORTED;
+  if (!page_rows_ok(P) || (int64_t)columns * P >= (int64_t)1 << 31 || N > kMostPages)
+    return HYTOPK_UNSUPPORTED;
   if (!refs || (B > 0 && (!table || !lengths))) return HYTOPK_INVALID_ARG;
   if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(refs, 4)) return HYTOPK_MISALIGNED;
   return HYTOPK_OK;
@@ -530,7 +533,7 @@ extern "C" hytopk_status hytopk_page_free(int32_t* table, int32_t* lengths, int3
 }
 
 extern "C" size_t hytopk_page_workspace_size(int N) {
-  if (N < 1) return 0;
+  if (N < 1 || N > kMostPages) return 0;
   return (2 * (size_t)N + chunks_of(N) + 1) * sizeof(int32_t) / 256 * 256 + 256;
 }
 

@@ -642,7 +642,8 @@ HYTOPK_API hytopk_status hytopk_page_write(const void* x, int64_t x_row, int64_t
  * hytopk_page_compact: with K pages in use, those numbered K and up, in ascending order, are
  *   to move to the free ones below K, in ascending order: src_out, dst_out [max(1, N / 2)]
  *   (-1 past the last move) for hytopk_page_copy, with table and refs changed already.
- *   B may be 0. workspace as above. */
+ *   B may be 0. workspace as above.
+ * N <= 2^30 for these four (HYTOPK_UNSUPPORTED above). */
 HYTOPK_API hytopk_status hytopk_page_fork(int32_t* table, int32_t* lengths, int32_t* refs, int B,
                                           int columns, int N, int P, const int32_t* src,
                                           const int32_t* dst, int count, uint32_t* dev_status,
