@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         phase ^= 1u;
       }
       const int key = at.t * 128 + ww * 32 + rl;
-      if (at.t * 128 + 128 > at.end) {  // no row sees what lies past the end
+      if (at.end - at.t * 128 < 128) {  // no row sees what lies past the end
 #pragma unroll
         for (int u = 0; u < PASSES; ++u)
           if (key + u * RPP >= at.end) x[u] = make_uint4(0, 0, 0, 0);

@@ -87,3 +87,31 @@ def test_codes_of_nan_stay_in_their_sequences(lengths, d):
         assert word.item() == 0
         assert torch.equal(torch.isnan(out), want)
         assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_a_context_of_almost_2_31_rows(rows):
+    """Of which only the last page is there; the row behind the context holds NaN codes."""
+    P, d, columns = 16, 64, (1 << 27) - 1
+    length = columns * P - 1
+    table = torch.full((1, columns), -1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randint(0x20, 0x40, (4, P, 1, d), dtype=torch.uint8, device="cuda", generator=g)
+    v = torch.randint(0x20, 0x40, (4, P, 1, d), dtype=torch.uint8, device="cuda", generator=g)
+    k[:, 15] = v[:, 15] = 0x7F
+    one = torch.ones(4, 1, device="cuda")
+    q = torch.randn(rows, 4, d, device="cuda", generator=g).bfloat16()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = None if rows == 1 else cuda([0, rows])
+    out, lse = hk.attend_pages(q, k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), one, one,
+                               table, cuda([length]), cu, status=word)
+    assert word.item() == 0
+    for i in range(rows):
+        there = 15 - (rows - 1 - i)
+        K, V = (t[2, :there, 0].view(torch.float8_e4m3fn).double() for t in (k, v))
+        s = q[i].double() @ K.T / 8
+        want = torch.softmax(s, -1) @ V
+        # the result's rounding, f16 weights, and fp32 scores below 2^6
+        assert ((out[i].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs()).all()
+        assert ((lse[i].double() - torch.logsumexp(s, -1)).abs() <= 2.0 ** -16).all()
