@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kGrowThreads) k_grow(const Pool a, const int32
     const long long at = base + block_scan<kGrowThreads>((long long)need, warps, total);
     if (b < a.B) {
       src_out[b] = r.ok ? need * 2 + away : -1;
-      dst_out[b] = (int)(at < a.N ? at : (long long)a.N);  // (N: past every free page)
+      dst_out[b] = (int)(at <= a.N ? at : (long long)a.N + 1);  // (N + 1: past every free page)
     }
     base += total;
   }
