@@ -26,8 +26,8 @@ struct AttendArgs {
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
-  float* part;   // [2 * ctas][rows][d] unnormalised results
-  float2* ml;    // [2 * ctas][rows] their sums and -m
+  float* part;   // [2 * ctas][rows][d] results, each divided by its own sum
+  float2* ml;    // [2 * ctas][rows] sums and -m of them
   int4* record;  // [2 * ctas][2]: what each is a part of
   int rows;      // of a part
   // both kernels are launched: the first tells here whether some sequence has several rows, which

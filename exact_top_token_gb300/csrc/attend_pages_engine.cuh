@@ -24,13 +24,19 @@
 // with v's scale, has an error of 2^-25, less than 2^-28 of it. m is a whole number, so that
 // s + (b - m) is rounded once. Queries are taken to f16 with a power of two out of each row.
 //
+// That is the quick form. Scales of v that lie 2^60 and more from the reference, or scores so far
+// from 0 that b is lost beside m, take a slow one from there to the segment's end: denominators
+// have a reference m' of their own, the largest s or so, and weights are 2^(((s - m') + b) + d).
+// Results of parts are kept divided by their denominators, so that no product of a scale and a
+// weight passes the range of fp32.
+//
 // A masked weight is 0 whatever the score is, but 0 times a NaN code of v is not: in the
 // tiles that hold keys some row does not see, NaN codes of v are replaced by 0 and, by column,
 // the first key that has one is kept; the rows that see it become NaN there at the end.
 //
 // The work of a call is only known on the device (contexts and their new rows). Every CTA
 // adds it up, in units of a tile's time, and takes an equal share of it in order, tile by
-// tile: an item that lies in several shares leaves unnormalised parts in the workspace,
+// tile: an item that lies in several shares leaves parts in the workspace, each with its sum,
 // and a second kernel joins them. The result does not depend on timing. A row of a page holds
 // all cache heads, so neighbouring CTAs take the same places of different heads: read by
 // themselves, pieces of 128 bytes 1 KB apart come at 4.1 TB/s, whole rows at 5.4.
@@ -71,6 +77,9 @@ constexpr int kSegs = 8;       // ring of segments
 constexpr int kConsts = 16;    // ring of the tiles' scales
 constexpr int kThreads = 512;
 constexpr int kBlock = 4;      // groups of 16 keys that the softmax takes at a time
+// The quick form of the softmax has one reference m for weights and denominators: |b| may be up to
+// kWide in it (of 2^60, 2^11 and 2^31 keys fp32 holds the product), and |m| up to kFar.
+constexpr float kWide = 60.0f, kFar = 1048576.0f;
 // Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 184 + 80) = 65536.
 constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 184, kRegsWide = 80;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");
@@ -87,7 +96,7 @@ enum : int { kStop = 1, kSmall = 2, kStarts = 4, kEnds = 8 };
 struct TileConst {
   float4 group[4];  // of two groups: factor of the scores, b
   float ref;        // reference of v's scales
-  uint32_t absent;  // groups of the contexts' rows that are not there
+  uint32_t odd;     // bits of the groups: 0 on: rows that are not there, 8 on: b past kWide
   uint32_t pad[2];
 };
 
@@ -114,7 +123,7 @@ struct PCfg {
   static constexpr int CONST_OFF = NAN_OFF + NANS * 2 * D * 4;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int ML_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);
-  static constexpr int QS_OFF = ML_OFF + 128 * 8;
+  static constexpr int QS_OFF = ML_OFF + 128 * 12;
   static constexpr int EPI_OFF = (QS_OFF + 2 * 128 * 4 + 15) / 16 * 16;  // [8 warps][1 KB]
   static constexpr int BAR_OFF = EPI_OFF + 8 * 1024;
   static constexpr int SMEM = BAR_OFF + 896 + 1024;
@@ -423,7 +432,7 @@ __device__ __forceinline__ int pages_of(const AttendArgs& a, int lane, int b, in
 }
 
 // A segment's scales, four tiles at a time: put(k, group, ref, absent) for its tiles in order, of
-// which the lanes from 8 k on have the groups; put tells whether to go on. One warp.
+// which the lanes from 8 k on have the groups (odd: their bits); put tells whether to go on. One warp.
 template <class Put>
 __device__ __forceinline__ bool segment_scales(const AttendArgs& a, const Seg& s, int lane, Put put) {
   const float c_scale = (a.scale == 0.0f ? 1.0f : fabsf(a.scale)) * att::kLog2e;
@@ -451,14 +460,46 @@ __device__ __forceinline__ bool segment_scales(const AttendArgs& a, const Seg& s
     float2 group = make_float2(1.0f, 0.0f);  // (masked keys: any factor will do)
     if (in) {
       group.x = k_ok ? fmaxf(c_scale * sc.x, 1.17549435e-38f) : nan;
-      group.y = v_ok ? fminf(fmaxf(log2f(sc.y * (1.0f / ref)), -100.0f), 100.0f) : nan;
+      const float ratio = sc.y * (1.0f / ref);  // (may pass the range of fp32)
+      group.y = !v_ok ? nan
+                : ratio > 1e-30f && ratio < 1e30f ? log2f(ratio) : log2f(sc.y) - log2f(ref);
     }
     const uint32_t absent = ~__ballot_sync(0xffffffffu, in || past);
+    const uint32_t wide = __ballot_sync(0xffffffffu, fabsf(group.y) > kWide);
 #pragma unroll 1
     for (int k = 0; k < 4 && t + k < s.t1; ++k)
-      if (!put(k, group, ref, absent >> (8 * k) & 0xFFu)) return false;
+      if (!put(k, group, ref, (absent >> (8 * k) & 0xFFu) | (wide >> (8 * k) & 0xFFu) << 8)) return false;
   }
   return true;
+}
+
+// Two sums with references of their own (-m' of the denominators l, d more of the weights; nm = -inf:
+// nothing so far) as one: sum, nm, and what the results with the weights are multiplied with
+// for softmax times v: f1, f2, or, where these could pass the range of fp32 somewhere in the warp
+// (`odd`), f1, f2 and the powers of two p1, p2 on top.
+struct Factors {
+  float sum, nm, f1, f2, p1, p2;
+  bool odd;
+};
+__device__ __forceinline__ Factors factors(float l, float nm, float d, float l2, float nm2, float d2,
+                                           float ref) {
+  Factors r;
+  const bool one = nm > -INFINITY, two = nm2 > -INFINITY;
+  const float both = fminf(one ? nm : INFINITY, two ? nm2 : INFINITY);
+  r.nm = one || two ? both : -INFINITY;
+  r.sum = l * (one ? ex2(both - nm) : 0.0f) + l2 * (two ? ex2(both - nm2) : 0.0f);
+  // powers of two of the weights, beside ref
+  const float a1 = one ? (both - nm) - d : -INFINITY, a2 = two ? (both - nm2) - d2 : -INFINITY;
+  const float most = one || two ? fmaxf(a1, a2) : 0.0f;
+  const int e = (int)(__float_as_uint(ref) >> 23) - 127;
+  r.odd = __any_sync(0xffffffffu, fabsf(most) > kWide || abs(e) > (int)kWide);
+  const float norm = (r.odd ? 1.0f : ref) / r.sum, shift = r.odd ? most : 0.0f;
+  r.f1 = r.sum == 0.0f ? 0.0f : one ? ex2(a1 - shift) * norm : 0.0f * norm;
+  r.f2 = r.sum == 0.0f ? 0.0f : two ? ex2(a2 - shift) * norm : 0.0f * norm;
+  const float all = e + most, half = floorf(0.5f * all);
+  r.p1 = ex2(half) * (ref * __uint_as_float((uint32_t)(127 - min(e, 126)) << 23)) * (e > 126 ? 0.5f : 1.0f);
+  r.p2 = ex2(all - half);
+  return r;
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -494,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* nan_s = reinterpret_cast<int*>(smem + C::NAN_OFF);  // [NANS][2][D] first key
   TileConst* const_s = reinterpret_cast<TileConst*>(smem + C::CONST_OFF);
   Seg* seg_s = reinterpret_cast<Seg*>(smem + C::SEG_OFF);
-  float2* ml_s = reinterpret_cast<float2*>(smem + C::ML_OFF);
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::ML_OFF);  // [128] of the second warpgroup: l, nm
+  float* d_s = reinterpret_cast<float*>(ml_s + 128);           // [128] its d
   float* qs_s = reinterpret_cast<float*>(smem + C::QS_OFF);  // [2][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* full = bars;              // [NS] operands of a tile
@@ -603,14 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
-        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t absent) {
+        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t odd) {
           const int slot = g % kConsts;
           if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
           TileConst* out = const_s + slot;
           if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
           if (lane == 0) {
             out->ref = ref;
-            out->absent = absent;
+            out->odd = odd;
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(c_full + slot);
@@ -961,8 +1003,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p = there ? s.p0 + token_of(s) : -1;  // the row's position
       const bool warp_there = __any_sync(0xffffffffu, there);
       const int p_first = s.p0 + (small ? 0 : w * a.tokens);  // the least position
-      float nm = -INFINITY, l = 0.0f, ref = 1.0f;
-      bool ok = true;
+      // nm: -m of the denominators, d: by how much -m of the weights is more (0 in the quick form)
+      float nm = -INFINITY, d = 0.0f, l = 0.0f, ref = 1.0f;
+      bool ok = true, slow = false;
       int mine = 0;  // tiles of this segment so far
 #pragma unroll 1
       for (int t = s.t0 + (small ? w : 0); t < s.t1; t += step, ++mine, ++cnt) {
@@ -971,7 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const TileConst* tile = const_s + number_c % kConsts;
         if (!(ok = wait(c_full + number_c % kConsts, (number_c / kConsts) & 1))) break;
         ref = tile->ref;
-        const uint32_t absent = tile->absent;
+        const uint32_t absent = tile->odd & 0xFFu;
+        slow |= tile->odd > 0xFFu;
         if (!(ok = wait(s_full + w, cnt & 1))) break;
         tc::fence_after_sync();
         if (warp_there) {
@@ -979,12 +1023,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (uniform in the warp) some key is not seen by some row, or not there
           const bool masked = t * 128 + 127 > p_first || absent != 0;
           auto upto = [&](int g) { return absent >> g & 1 ? -1 : seen - 16 * g; };
-          // m by `by` more (whole numbers), where that is not 0; the tile's weights so far are
-          // those of `done` blocks.
-          auto raise = [&](float by, int done) -> bool {
+          // O and the tile's weights so far, those of `done` blocks, times 2^-by
+          auto shrink = [&](float by, int done) -> bool {
             const float f = ex2(-by);
-            l *= f;
-            nm -= by;
             const uint32_t f2 = pack_f16(f, f);
             tc::tmem_wait_st();
 #pragma unroll 1
@@ -1010,36 +1051,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_wait_st();
             return true;
           };
-          bool exact = __any_sync(0xffffffffu, there && !(fabsf(nm) <= 1048576.0f));
-          if (exact) {
-            // Rows without a reference (the item's first tile), or far from 0: the maximum of
-            // the whole tile first.
+          // the largest of 16 scores as they are, masked
+          auto largest = [&](int g, float (&v)[16]) -> float {
+            tc::tmem_ld16(s_addr + 16 * g, v);
+            tc::tmem_wait_ld(v);
+            if (masked) {
+              const int last = upto(g);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = j <= last ? v[j] : -INFINITY;
+            }
+            float m0 = max3(v[0], v[1], v[2]);
+#pragma unroll
+            for (int j = 3; j < 15; j += 2) m0 = max3(m0, v[j], v[j + 1]);
+            return fmaxf(m0, v[15]);
+          };
+          if (!slow && __any_sync(0xffffffffu, there && !(fabsf(nm) <= kFar))) {
+            // rows without a reference (the item's first tile): the maximum of the whole tile first
             float top = -INFINITY;
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float v[16];
-              tc::tmem_ld16(s_addr + 16 * g, v);
-              tc::tmem_wait_ld(v);
               const float2 k = reinterpret_cast<const float2*>(tile->group)[g];
-              if (masked) {
-                const int last = upto(g);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = j <= last ? v[j] : -INFINITY;
-              }
-              float m0 = max3(v[0], v[1], v[2]);
-#pragma unroll
-              for (int j = 3; j < 15; j += 2) m0 = max3(m0, v[j], v[j + 1]);
-              top = fmaxf(top, __fadd_rn(__fmul_rn(fmaxf(m0, v[15]), k.x * qs), k.y));
+              top = fmaxf(top, __fadd_rn(__fmul_rn(largest(g, v), k.x * qs), k.y));
             }
-            const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
-            const bool none = nm == -INFINITY, over = there && top > -INFINITY && (none || top + nm > 11.0f);
-            if (__any_sync(0xffffffffu, over && !none)) {
-              if (!(ok = raise(over && !none ? nm - to : 0.0f, 0))) break;
-            }
-            if (over) nm = to;
-            exact = __any_sync(0xffffffffu, there && fabsf(nm) > 1048576.0f && nm > -INFINITY);
+            if (there && top > -INFINITY && nm == -INFINITY) nm = 4.0f - ceilf(fmaxf(top, -att::kLargest));
+            slow = __any_sync(0xffffffffu, there && fabsf(nm) > kFar && nm > -INFINITY);
           }
-          if (!exact) {
+          int from = 0;  // the group that the slow form begins with
+          if (!slow) {
 #pragma unroll 1
             for (int i = 0; i < 8; i += kBlock) {  // groups
               float v[kBlock / 2][32], c[kBlock], kb[kBlock];
@@ -1081,8 +1120,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int g = 0; g < kBlock; ++g) kb[g] = nm - kb[g];
               if (__any_sync(0xffffffffu, there && top > 11.0f)) {
-                const float by = there && top > 11.0f ? ceilf(top) - 4.0f : 0.0f;
-                if (!(ok = raise(by, i / 2))) break;
+                // m by `by` more (whole numbers); where that is so much that nothing so far counts,
+                // from here on as if nothing had been, and slowly
+                slow = __any_sync(0xffffffffu, there && top > kFar);
+                const float by = !there || !(top > (slow ? kFar : 11.0f)) ? 0.0f
+                                 : slow ? INFINITY : ceilf(top) - 4.0f;
+                l *= ex2(-by);
+                nm -= by;
+                if (!(ok = shrink(by, i / 2))) break;
+                if (slow) {
+                  from = i;
+                  break;
+                }
 #pragma unroll
                 for (int j = 0; j < 16 * kBlock; ++j) v[j / 32][j % 32] -= by;
               }
@@ -1108,26 +1157,58 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (!ok) break;
-          } else {
-            // far from 0: products rounded as the maximum was
+          }
+          if (slow) {
+            // The slow form, for all that is left of a segment: scores far from 0, where b would be
+            // rounded away beside m, or b so far apart that no m would do for weights and
+            // denominators both. x = s rounded as the maximum was; denominators sum 2^(x - m') with
+            // m' of their own, weights are 2^(((x - m') + b) + d).
+            const bool none = nm == -INFINITY;
+            float by = 0.0f;
 #pragma unroll 1
-            for (int g = 0; g < 8; ++g) {
+            for (int pass = 0; pass < 2; ++pass) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int g = from; g < 8; ++g) {
+                float v[16];
+                const float2 k = reinterpret_cast<const float2*>(tile->group)[g];
+                const float x = __fmul_rn(largest(g, v), k.x * qs);
+                top = fmaxf(top, pass ? __fadd_rn(__fadd_rn(x, nm), k.y) : x);
+              }
+              if (there && top > -INFINITY && (none || top + (pass ? d : nm) > (pass ? 11.0f : kWide))) {
+                const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
+                if (pass) {
+                  if (!none) by = d - to;
+                  d = to;
+                } else {
+                  if (!none) {
+                    l *= ex2(to - nm);
+                    d += nm - to;
+                  }
+                  nm = to;
+                }
+              }
+              __syncwarp();
+            }
+            if (__any_sync(0xffffffffu, by != 0.0f) && !(ok = shrink(by, from / 2))) break;
+#pragma unroll 1
+            for (int g = from; g < 8; ++g) {
               float v[16];
               tc::tmem_ld16(s_addr + 16 * g, v);
               tc::tmem_wait_ld(v);
               const float2 k = reinterpret_cast<const float2*>(tile->group)[g];
               const int last = masked ? upto(g) : 15;
-              const float cc = k.x * qs;
+              const float c = k.x * qs, nan = k.y - k.y;  // (NaN of a scale that is none, or 0)
               float sum = 0.0f;
               uint32_t y[8];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                v[j] = ex2(__fadd_rn(__fadd_rn(__fmul_rn(v[j], cc), k.y), nm));
-                v[j] = j <= last ? v[j] : 0.0f;
-                sum += v[j];
+                const float x = __fadd_rn(__fmul_rn(v[j], c), nm), u = ex2(x) + nan;
+                sum += j <= last ? u : 0.0f;
+                v[j] = j <= last ? ex2(__fadd_rn(__fadd_rn(x, k.y), d)) : 0.0f;
                 if (j & 1) y[j / 2] = pack_f16(v[j - 1], v[j]);
               }
-              if (sum != 0.0f) l += sum * ex2(-k.y);
+              l += sum;
               tmem_store8(s_addr + 8 * g, y);
             }
           }
@@ -1171,12 +1252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(pv_done + w, (cnt - 1) & 1))) break;
           tc::fence_after_sync();
         }
-        float l2 = 0.0f, nm2 = -INFINITY;  // the other warpgroup's
+        float l2 = 0.0f, nm2 = -INFINITY, d2 = 0.0f;  // the other warpgroup's
         const bool other = small && T > 1;
         if (small) {
           if (w == 1) {
             if (!(ok = wait(ml_empty, (smalls & 1) ^ 1))) break;
             ml_s[row] = make_float2(l, nm);
+            d_s[row] = d;
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ml_full);
@@ -1186,6 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 x = ml_s[row];
             l2 = x.x;
             nm2 = x.y;
+            d2 = d_s[row];
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ml_empty);
           }
@@ -1195,16 +1278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t* any = nan_any + segs % C::NANS * 2 + w;
         const bool nan_here = *reinterpret_cast<volatile uint32_t*>(any) != 0;
         if (warp_there && !(small && w == 1)) {
-          // one reference for both; -inf: no row so far
-          const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
-          float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm);
-          float f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
-          const float sum = l * f1 + l2 * f2;
+          const Factors x = factors(l, nm, d, l2, nm2, d2, ref);
+          const float f1 = x.f1, f2 = x.f2, sum = x.sum;
           const bool part = s.part >= 0;
           const int r = w * 128 + row;
-          const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
-          f1 *= norm;
-          f2 *= norm;
           float* to_part = a.part + ((size_t)max(s.part, 0) * a.rows + r) * D;
           const uint64_t to_out = there ? (q_at * Hq + head) * D : 0;
           uint8_t* stage = smem + C::EPI_OFF + (warp - 4) * 1024;
@@ -1216,15 +1293,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) att::mul2(o[e], o[e + 1], f1, f1);
             if (other) {
-              float x[32];
-              tc::tmem_ld32(o_addr + D + i, x);
-              tc::tmem_wait_ld(x);
+              float z[32];
+              tc::tmem_ld32(o_addr + D + i, z);
+              tc::tmem_wait_ld(z);
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                fma2(x[e], x[e + 1], f2, o[e], o[e + 1]);
-                o[e] = x[e];
-                o[e + 1] = x[e + 1];
+                fma2(z[e], z[e + 1], f2, o[e], o[e + 1]);
+                o[e] = z[e];
+                o[e + 1] = z[e + 1];
               }
+            }
+            if (x.odd) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = o[e] * x.p1 * x.p2;
             }
             if (part) {
               if (there) {
@@ -1273,9 +1354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (there) {
-            const float m = both == INFINITY ? -INFINITY : both;
-            if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, m);
-            else if (a.lse) a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
+            if (part) a.ml[(size_t)s.part * a.rows + r] = make_float2(sum, x.nm);
+            else if (a.lse) a.lse[q_at * Hq + head] = sum == 0.0f ? -INFINITY : (log2f(sum) - x.nm) * att::kLn2;
           }
         }
         if (nan_here) {
@@ -1338,7 +1418,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
   __shared__ int before_s[kJoinThreads + 1];         // blocks' worth of rows in the shares before
   __shared__ int sums_s[WARPS];
   __shared__ float4 acc_s[WARPS][32];
-  __shared__ float sum_s[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int4 first0 = make_int4(0, 0, 0, 0);
   int flags0 = 0;
@@ -1405,7 +1484,28 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
     const int half = small || token < a.tokens ? 0 : 1;
     const size_t r = half * 128 + (token - half * a.tokens) * a.G + head;
     const size_t to = (size_t)(first.y + token) * Hq + first.w * a.G + head;
-    float top = INFINITY, sum = 0.0f;  // top: the least -m
+    float top = INFINITY, sum = 0.0f;  // top: the least -m; sum: the denominator there
+    // (a part without rows counts nothing, but what is NaN in it does)
+    auto count_in = [&](float s, float nm) {
+      const float t = fminf(top, nm > -INFINITY ? nm : INFINITY);
+      sum = (top < INFINITY ? sum * ex2(t - top) : sum) + (nm > -INFINITY ? s * ex2(t - nm) : s);
+      top = t;
+    };
+    auto join_lanes = [&](int lanes) {
+      for (int i = lanes / 2; i; i >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, sum, i), t = __shfl_xor_sync(0xffffffffu, top, i);
+        count_in(s, t < INFINITY ? t : -INFINITY);
+      }
+    };
+    // What a part's result, which is softmax times v of its keys alone, counts, as two factors: little
+    // of a large v may be more than all of a small one.
+    auto weight_of = [&](float2 m) {
+      if (!(m.x > 0.0f)) return make_float2(m.x, 1.0f);  // (0 or NaN)
+      auto exponent = [](float x) { return (int)(__float_as_uint(x) >> 23); };
+      auto fraction = [](float x) { return __uint_as_float((__float_as_uint(x) & 0x7FFFFFu) | 0x3F800000u); };
+      const float all = top - m.y + (float)(exponent(m.x) - exponent(sum)), half = floorf(0.5f * all);
+      return make_float2(fraction(m.x) / fraction(sum) * ex2(half), ex2(all - half));
+    };
     auto log_sum = [&]() { return sum == 0.0f ? -INFINITY : (log2f(sum) - top) * att::kLn2; };
     if (!wide) {
       const bool on = x < rows;
@@ -1417,11 +1517,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
       for (int i = l; i <= count; i += 8) {
         const int part = part_of(i);
         if (part < 0) continue;
-        const float m = ld_after(&a.ml[part * (size_t)a.rows + row].y);
-        if (m > -INFINITY) top = fminf(top, m);
+        const float2 m = ld_after(a.ml + part * (size_t)a.rows + row);
+        count_in(m.x, m.y);
       }
-#pragma unroll
-      for (int i = 4; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      join_lanes(8);
 #pragma unroll 2
       for (int i = 0; i <= count; ++i) {
         const int part = part_of(i);
@@ -1431,10 +1530,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
         float4 z[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) z[e] = ld_after(y + 8 * e);
-        // a part without rows counts nothing, but its NaN columns do
-        const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
-        sum += m.x * f;
-        auto add = [&](float& to, float from) { to += from == 0.0f ? 0.0f : from * f; };
+        const float2 f = weight_of(m);
+        auto add = [&](float& to, float from) { to += from == 0.0f ? 0.0f : from * f.x * f.y; };
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
           add(o[e].x, z[e].x);
@@ -1444,11 +1541,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
         }
       }
       if (!on) continue;
-      const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e)
         *reinterpret_cast<uint2*>(a.out + to * D + 32 * e + 4 * l) =
-            make_uint2(att::pack_bf16(o[e].x * norm, o[e].y * norm), att::pack_bf16(o[e].z * norm, o[e].w * norm));
+            make_uint2(att::pack_bf16(o[e].x, o[e].y), att::pack_bf16(o[e].z, o[e].w));
       if (a.lse && l == 0) a.lse[to] = log_sum();
       continue;
     }
@@ -1458,11 +1554,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
     for (int i = lane; i <= count; i += 32) {
       const int part = part_of(i);
       if (part < 0) continue;
-      const float m = ld_after(&a.ml[part * (size_t)a.rows + r].y);
-      if (m > -INFINITY) top = fminf(top, m);
+      const float2 m = ld_after(a.ml + part * (size_t)a.rows + r);
+      count_in(m.x, m.y);
     }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    join_lanes(32);
 #pragma unroll 8
     for (int i = warp; i <= count; i += WARPS) {
       const int part = part_of(i);
@@ -1477,17 +1572,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
         const float2 t = ld_after(reinterpret_cast<const float2*>(y));
         z[0] = t.x, z[1] = t.y;
       }
-      const float f = m.y == -INFINITY ? 0.0f : ex2(top - m.y);
-      sum += m.x * f;
+      const float2 f = weight_of(m);
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f;
+      for (int e = 0; e < V; ++e) o[e] += z[e] == 0.0f ? 0.0f : z[e] * f.x * f.y;
     }
     __syncthreads();
     acc_s[warp][lane] = make_float4(o[0], o[1], V > 2 ? o[V - 2] : 0.0f, V > 2 ? o[V - 1] : 0.0f);
-    if (lane == 0) sum_s[warp] = sum;
     __syncthreads();
     if (warp) continue;
-    sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.0f;
 #pragma unroll
@@ -1499,11 +1591,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_parts(const AttendArgs a,
         o[2] += t.z;
         o[3] += t.w;
       }
-      sum += sum_s[i];
     }
-    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] *= norm;
     if constexpr (V == 4)
       *reinterpret_cast<uint2*>(a.out + to * D + lane * V) =
           make_uint2(att::pack_bf16(o[0], o[1]), att::pack_bf16(o[2], o[3]));

@@ -10,9 +10,10 @@
 //
 // The mathematics, the types and the shares of the work are those of the general kernel
 // (attend_pages_engine.cuh): f16 operands, weights 2^(s + b - m) with b of v's scale, m whole
-// numbers that are raised when a weight would pass 2^11. Here a thread of the softmax owns a
-// key: k's scale, b, and whether the key is seen are its own, the denominators are summed per
-// thread and joined at an item's end, and m is agreed on by a vote of the four warps, a tile.
+// numbers that are raised when a weight would pass 2^11, the slow form. Here a thread of the
+// softmax owns a key: k's scale, b, and whether the key is seen are its own, the denominators are
+// summed per thread and joined at an item's end, and m is agreed on by a vote of the four warps, a
+// tile.
 // Keys past the context's end, the same for all heads, have v replaced by zeros as it is
 // widened, so that NaN codes there reach nothing.
 //
@@ -57,8 +58,8 @@ struct TCfg {
   static constexpr int CONST_OFF = STAGE_OFF + UNITS * UNIT;
   static constexpr int SEG_OFF = CONST_OFF + kConsts * (int)sizeof(TileConst);
   static constexpr int QS_OFF = SEG_OFF + kSegs * (int)sizeof(Seg);  // [2][N] queries' powers of two
-  // of a warpgroup: [2][N] -m, factors; [4][N] maxima, sums; [N + 16] what the other is told
-  static constexpr int SOFT = (12 * N + N + 16) * 4;
+  // of a warpgroup: [2][N] -m, factors, d; [4][N] maxima, sums; [2 N + 16] what the other is told
+  static constexpr int SOFT = (14 * N + 2 * N + 16) * 4;
   static constexpr int SOFT_OFF = QS_OFF + 2 * N * 4;
   static constexpr int SHARE_OFF = SOFT_OFF + 2 * SOFT;
   static constexpr int BAR_OFF = SHARE_OFF + (int)sizeof(Share);
@@ -235,14 +236,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tc::mbar_arrive(seg_full + number % kSegs);
         }
         ++number;
-        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t absent) {
+        return segment_scales(a, s, lane, [&](int k, float2 group, float ref, uint32_t odd) {
           const int slot = g % kConsts;
           if (!wait(c_empty + slot, ((g / kConsts) & 1) ^ 1)) return false;
           TileConst* out = const_s + slot;
           if (lane >> 3 == k) reinterpret_cast<float2*>(out->group)[lane & 7] = group;
           if (lane == 0) {
             out->ref = ref;
-            out->absent = absent;
+            out->odd = odd;
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(c_full + slot);
@@ -517,9 +518,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t o_addr = tmem + lane_off + C::O_COL + wg * 64;
     float* nm_s = reinterpret_cast<float*>(smem + C::SOFT_OFF + wg * C::SOFT);  // [2][N] -m
     float* f_s = nm_s + 2 * N;                                                 // [2][N]
-    float* quad_s = f_s + 2 * N;                                               // [4][N] maxima
-    float* sum_s = quad_s + 4 * N;                                             // [4][N]
-    float* told_s = sum_s + 4 * N;  // [N] -m, and the reference of v's scales
+    float* d_s = f_s + 2 * N;       // [2][N] (see the general kernel's softmax)
+    float* quad_s = d_s + 2 * N;    // [4][N] maxima
+    float* sum_s = quad_s + 4 * N;  // [4][N]
+    float* told_s = sum_s + 4 * N;  // [N] -m, [N] d, and the reference of v's scales
     const int Hq = a.Hkv * a.G;
     int g0 = 0, cur = 0;  // tiles of the segments before; which nm_s counts
     Seg s;
@@ -535,9 +537,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
       float ref = 1.0f;
-      // exact: some reference is far from 0; unset: some head has none, because all scores so far
-      // are -inf or of rows that are not there
-      bool exact = false, started = false, unset = false, ok = true;
+      // slow: the slow form, for all that is left of a segment (see the general kernel); unset: some
+      // head has no reference, because all scores so far are -inf or of rows that are not there
+      bool slow = false, started = false, unset = false, ok = true;
       const float* qs = qs_s + (segs & 1) * N;
 #pragma unroll 1
       for (int i = (g0 ^ wg) & 1; i < T; i += 2) {
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const TileConst* tile = const_s + g % kConsts;
         ok = ok && wait(c_full + g % kConsts, (g / kConsts) & 1);
         const float2 k = reinterpret_cast<const float2*>(tile->group)[row >> 4];
-        const bool seen = (s.t0 + i) * 128 + row < s.end && !(tile->absent >> (row >> 4) & 1);
+        const bool seen = (s.t0 + i) * 128 + row < s.end && !(tile->odd >> (row >> 4) & 1);
+        slow |= tile->odd > 0xFFu;
         ok = ok && wait(s_full + wg, g >> 1 & 1);
         tc::fence_after_sync();
         float v[N];
@@ -556,22 +559,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int j = 0; j < N; j += 16) tc::tmem_ld16(s_addr + j, reinterpret_cast<float(&)[16]>(v[j]));
 #pragma unroll
           for (int j = 0; j < N; j += 16) tc::tmem_wait_ld(reinterpret_cast<float(&)[16]>(v[j]));
-          if (!exact) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-              float4 c = *reinterpret_cast<const float4*>(qs + j);
-              float4 m = *reinterpret_cast<const float4*>(nm + j);
-              att::mul2(c.x, c.y, k.x, k.x);
-              att::mul2(c.z, c.w, k.x, k.x);
-              add2(m.x, m.y, k.y, k.y);
-              add2(m.z, m.w, k.y, k.y);
-              madd2(v[j], v[j + 1], c.x, c.y, m.x, m.y);
-              madd2(v[j + 2], v[j + 3], c.z, c.w, m.z, m.w);
-            }
-          } else {  // far from 0: products rounded as the maximum was
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-              v[j] = __fadd_rn(__fadd_rn(__fmul_rn(v[j], k.x * qs[j]), k.y), nm[j]);
+          for (int j = 0; j < N; j += 4) {
+            float4 c = *reinterpret_cast<const float4*>(qs + j);
+            float4 m = *reinterpret_cast<const float4*>(nm + j);
+            att::mul2(c.x, c.y, k.x, k.x);
+            att::mul2(c.z, c.w, k.x, k.x);
+            add2(m.x, m.y, k.y, k.y);
+            add2(m.z, m.w, k.y, k.y);
+            madd2(v[j], v[j + 1], c.x, c.y, m.x, m.y);
+            madd2(v[j + 2], v[j + 3], c.z, c.w, m.z, m.w);
           }
           float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
 #pragma unroll
@@ -582,14 +579,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
           return fmaxf(max3(m0, v[N - 2], v[N - 1]), m1);
         };
         if (!started) ok = ok && wait(q_full + (segs & 1), segs >> 1 & 1);  // (their powers of two)
-        bool raise = !started || unset;
-        if (!raise) raise = weights() > 11.0f && seen;
-        if (some_of_us(raise || !ok)) {
-          if (some_of_us(!ok)) {
-            ok = false;
-            break;
-          }
-          // the tile's maxima, a column at a time, and new references where they pass
+        // Maxima over the tile of f(x, column) for all columns, x the score rounded; those of column
+        // `lane` % N come back.
+        auto tops = [&](auto&& f) -> float {
 #pragma unroll 1
           for (int j = 0; j < N; j += 16) {
             float x[16];
@@ -597,56 +589,112 @@ __global__ void __launch_bounds__(kTThreads, 1)
             tc::tmem_wait_ld(x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              x[e] = __fadd_rn(__fmul_rn(x[e], k.x * qs[j + e]), k.y);
+              x[e] = f(__fmul_rn(x[e], k.x * qs[j + e]), j + e);
               x[e] = seen && x[e] > -INFINITY ? x[e] : -INFINITY;  // (NaN as well)
             }
             const float top = att::reduce_columns<16, true>(x, lane);
             if (!(lane & 1)) quad_s[quad * N + j + lane / 2] = top;
           }
           some_of_us(false);
-          const float* nm0 = nm_s + cur * N;
-          cur ^= 1;
-          bool some = false, far = false, none_yet = false;  // O to be scaled; a reference far from 0
-          if (lane < N) {
-            const int r = lane;
-            const float top = fmaxf(fmaxf(quad_s[r], quad_s[N + r]), fmaxf(quad_s[2 * N + r], quad_s[3 * N + r]));
-            const float was = started ? nm0[r] : -INFINITY;
+          const int r = lane % N;
+          return fmaxf(fmaxf(quad_s[r], quad_s[N + r]), fmaxf(quad_s[2 * N + r], quad_s[3 * N + r]));
+        };
+        // the result so far times f_s
+        auto shrink = [&]() {
+          const float* f = f_s + cur * N;
+          // the last products with this result
+          ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
+          tc::fence_after_sync();
+          if (ok) {
+#pragma unroll 1
+            for (int j = 0; j < N; j += 8) {
+              float o[8];
+              att::tmem_load(o_addr + j, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= f[j + e];
+              att::tmem_store8(o_addr + j, o);
+            }
+            tc::tmem_wait_st();
+          }
+        };
+        bool raise = slow || !started || unset;
+        if (!raise) raise = weights() > 11.0f && seen;
+        if (some_of_us(raise || !ok)) {
+          if (some_of_us(!ok)) {
+            ok = false;
+            break;
+          }
+          // (all four warps write the same, a lane a column)
+          const int r = lane % N;
+          float was = started ? nm_s[cur * N + r] : -INFINITY, d = started ? d_s[cur * N + r] : 0.0f;
+          if (!slow) {
+            // new references where the tile's maxima pass
+            const float top = tops([&](float x, int) { return __fadd_rn(x, k.y); });
             const float to = 4.0f - ceilf(fmaxf(top, -att::kLargest));
             const bool none = was == -INFINITY, over = top > -INFINITY && (none || top + was > 11.0f);
-            const float now = over ? to : was;
-            const float f = over && !none ? ex2(to - was) : 1.0f;
-            // (all four warps write the same)
+            const float now = over ? to : was, f = over && !none ? ex2(to - was) : 1.0f;
+            cur ^= 1;
             nm_s[cur * N + r] = now;
             f_s[cur * N + r] = f;
-            some = f != 1.0f;
-            far = now > -INFINITY && fabsf(now) > 1048576.0f;
-            none_yet = r < a.G && now == -INFINITY;
+            d_s[cur * N + r] = 0.0f;
+            __syncwarp();
+            if (__any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll
+              for (int j = 0; j < N; ++j) l[j] *= f_s[cur * N + j];
+              shrink();
+            }
+            unset = __any_sync(0xffffffffu, r < a.G && now == -INFINITY);
+            slow = __any_sync(0xffffffffu, now > -INFINITY && fabsf(now) > kFar);
+            was = now;
+            if (!slow) weights();
           }
-          __syncwarp();
-          some = __any_sync(0xffffffffu, some);
-          unset = __any_sync(0xffffffffu, none_yet);
-          exact = __any_sync(0xffffffffu, far);
-          if (some) {
-            const float* f = f_s + cur * N;
-#pragma unroll
-            for (int r = 0; r < N; ++r) l[r] *= f[r];
-            // the last products with this result
-            ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
-            tc::fence_after_sync();
-            if (ok) {
-#pragma unroll 1
-              for (int j = 0; j < N; j += 8) {
-                float o[8];
-                att::tmem_load(o_addr + j, o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= f[j + e];
-                att::tmem_store8(o_addr + j, o);
+          if (slow) {
+            // the denominators' reference, then the weights'
+            some_of_us(false);  // (the last maxima are read)
+            float top = tops([&](float x, int) { return x; });
+            const bool none = was == -INFINITY;
+            float f = 1.0f, now = was;
+            if (top > -INFINITY && (none || top + was > kWide)) {
+              now = 4.0f - ceilf(fmaxf(top, -att::kLargest));
+              if (!none) {
+                f = ex2(now - was);
+                d += was - now;
               }
-              tc::tmem_wait_st();
+            }
+            cur ^= 1;
+            nm_s[cur * N + r] = now;
+            f_s[cur * N + r] = f;
+            __syncwarp();
+            const float* nm = nm_s + cur * N;
+#pragma unroll
+            for (int j = 0; j < N; ++j) l[j] *= f_s[cur * N + j];
+            some_of_us(false);
+            top = tops([&](float x, int j) { return __fadd_rn(__fadd_rn(x, nm[j]), k.y); });
+            f = 1.0f;
+            if (top > -INFINITY && (none || top + d > 11.0f)) {
+              const float to = 4.0f - ceilf(top);
+              if (!none) f = ex2(to - d);
+              d = to;
+            }
+            f_s[cur * N + r] = f;
+            d_s[cur * N + r] = d;
+            __syncwarp();
+            if (__any_sync(0xffffffffu, f != 1.0f)) shrink();
+            const float nan = k.y - k.y;  // (NaN of a scale that is none, or 0)
+#pragma unroll
+            for (int j = 0; j < N; j += 16) {
+              float x[16];
+              tc::tmem_ld16(s_addr + j, x);
+              tc::tmem_wait_ld(x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                x[e] = __fadd_rn(__fmul_rn(x[e], k.x * qs[j + e]), nm[j + e]);
+                l[j + e] += seen ? ex2(x[e]) + nan : 0.0f;
+                v[j + e] = __fadd_rn(__fadd_rn(x[e], k.y), d_s[cur * N + j + e]);
+              }
             }
           }
           started = true;
-          weights();
         }
         ref = tile->ref;
         tc::fence_before_sync();
@@ -655,7 +703,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // the weights' place: of the products two tiles before (a wait that was given up is told
         // of in the next vote)
         if (g >= 2 && ok) ok = wait(pv_done + wg, (g - 2) >> 1 & 1);
-        const float share_b = ex2(-k.y);  // (b goes out of the denominators)
+        const float share_b = slow ? 0.0f : ex2(-k.y);  // (b goes out of the denominators)
         const uint32_t p0 = tc::smem_u32(smem + C::P_OFF + wg * C::PB);
 #pragma unroll
         for (int j = 0; j < N; j += 8) {
@@ -687,12 +735,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!(lane & 1)) sum_s[quad * N + j + lane / 2] = sum;
       }
       const int r = lane % N;  // a column
-      const float nm = started ? nm_s[cur * N + r] : -INFINITY;
+      const float nm = started ? nm_s[cur * N + r] : -INFINITY, d = started ? d_s[cur * N + r] : 0.0f;
       arrive(q_empty + (segs & 1));  // (their powers of two)
       if (wg == 1) {
         // the first warpgroup takes this one's sums, references and result along
-        if (quad == 0 && lane < N) told_s[r] = nm;
-        if (quad == 0 && lane == 0) told_s[N] = ref;
+        if (quad == 0 && lane < N) told_s[r] = nm, told_s[N + r] = d;
+        if (quad == 0 && lane == 0) told_s[2 * N] = ref;
         arrive(ml_full);
         if (some_of_us(!ok)) break;
         g0 += T;
@@ -705,29 +753,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto sum_of = [&](const float* x) { return (x[r] + x[N + r]) + (x[2 * N + r] + x[3 * N + r]); };
       const bool mine = T > 1 || !(g0 & 1), other = T > 1 || (g0 & 1);
       const float* theirs = sum_s + C::SOFT / 4;  // the second warpgroup's
-      const float nm2 = theirs[4 * N + r];
-      if (!mine) ref = theirs[5 * N];
-      // one reference for both; -inf: no key so far
-      const float both = fminf(nm == -INFINITY ? INFINITY : nm, nm2 == -INFINITY ? INFINITY : nm2);
-      float f1 = nm == -INFINITY ? 0.0f : ex2(both - nm), f2 = nm2 == -INFINITY ? 0.0f : ex2(both - nm2);
-      const float sum = sum_of(sum_s) * f1 + sum_of(theirs) * f2, m = both == INFINITY ? -INFINITY : both;
-      const float norm = part ? ref : sum == 0.0f ? 0.0f : ref / sum;
-      f1 *= norm;
-      f2 *= norm;
+      if (!mine) ref = theirs[6 * N];
+      const Factors x = factors(sum_of(sum_s), nm, d, sum_of(theirs), theirs[4 * N + r], theirs[5 * N + r], ref);
       const size_t at = (size_t)s.row0 * Hq + (size_t)s.hk * a.G;  // the first head of out
       const size_t part_at = (size_t)max(s.part, 0) * a.rows;
       if (quad * 32 < D) {
 #pragma unroll 1
         for (int j = 0; j < a.G; j += 8) {
-          float o[8], x[8];
+          float o[8], z[8];
           if (mine) att::tmem_load(o_addr + j, o);
-          if (other) att::tmem_load(o_addr + 64 + j, x);
+          if (other) att::tmem_load(o_addr + 64 + j, z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float a1 = __shfl_sync(0xffffffffu, f1, j + e), a2 = __shfl_sync(0xffffffffu, f2, j + e);
+            const float a1 = __shfl_sync(0xffffffffu, x.f1, j + e), a2 = __shfl_sync(0xffffffffu, x.f2, j + e);
             float y = 0.0f;
             if (mine) y = o[e] * a1;
-            if (other) y += x[e] * a2;
+            if (other) y += z[e] * a2;
+            if (x.odd) y = y * __shfl_sync(0xffffffffu, x.p1, j + e) * __shfl_sync(0xffffffffu, x.p2, j + e);
             if (j + e < a.G) {
               if (part) a.part[(part_at + j + e) * D + row] = y;
               else a.out[(at + j + e) * D + row] = __float2bfloat16_rn(y);
@@ -736,8 +778,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
       }
       if (quad == 0 && lane < a.G) {
-        if (part) a.ml[part_at + lane] = make_float2(sum, m);
-        else if (a.lse) a.lse[at + lane] = sum == 0.0f ? -INFINITY : (log2f(sum) - m) * att::kLn2;
+        if (part) a.ml[part_at + lane] = make_float2(x.sum, x.nm);
+        else if (a.lse) a.lse[at + lane] = x.sum == 0.0f ? -INFINITY : (log2f(x.sum) - x.nm) * att::kLn2;
       }
       tc::fence_before_sync();
       arrive(o_empty);

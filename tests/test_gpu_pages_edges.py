@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import exact_top_token_gb300 as hk
+import pages_oracle as po
 from test_gpu_pages_attend import Case as AnyCase
 from test_gpu_pages_attend import cuda
 from test_gpu_pages_tokens import Case, check
@@ -115,3 +116,128 @@ def test_a_context_of_almost_2_31_rows(rows):
         # the result's rounding, f16 weights, and fp32 scores below 2^6
         assert ((out[i].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want.abs()).all()
         assert ((lse[i].double() - torch.logsumexp(s, -1)).abs() <= 2.0 ** -16).all()
+
+
+# ---- scales of v far apart, scores far from 0 -------------------------------------------------
+
+def tight(c, equal=False):
+    """out, lse and bounds as tests/pages_oracle.py has them, but for weights that f16 holds as
+    subnormal numbers: each is off by 2^-27 (twice rounded) of the largest weight times its scale of
+    v, whatever the other scales are. `equal`: scores that matter are the same number, so that
+    their rounding falls out of the weights."""
+    q, k, v = c.q.double().numpy(), c.k, c.v
+    n, Hq, d = q.shape
+    G = Hq // c.Hkv
+    out, lse = np.zeros((n, Hq, d)), np.full((n, Hq), -np.inf)
+    t_out, t_lse = np.zeros((n, Hq, d)), np.zeros((n, Hq))
+    for b, length in enumerate(c.lengths):
+        lo, hi = (b, b + 1) if c.cu is None else (c.cu[b], c.cu[b + 1])
+        K, sk, there = po.context(k, c.ks.astype(np.float64), c.table[b], length)
+        V, sv, _ = po.context(v, c.vs.astype(np.float64), c.table[b], length)
+        for t in range(lo, hi):
+            rows = np.nonzero(there[:length - (hi - lo) + t - lo + 1])[0]
+            for h in range(Hq):
+                hk = h // G
+                size = sk[rows, hk] * abs(c.scale)
+                s = (K[rows, hk] @ q[t, h]) * sk[rows, hk] * c.scale
+                top = s.max()
+                e = np.exp(s - top)
+                z = e.sum()
+                val = V[rows, hk] * sv[rows, hk][:, None]
+                o = e @ val / z
+                delta = (d / 16 + 16) * po.U32 * ((np.abs(K[rows, hk]) @ np.abs(q[t, h])) * size).max() + \
+                    2.0 ** -20 + 2.0 ** -21 * np.abs(s).max()
+                out[t, h], lse[t, h] = o, top + np.log(z)
+                share = 2.0 ** -20 if equal else 2 * delta
+                small = (e / z * sv[rows, hk]).max()
+                t_out[t, h] = (share + 2.0 ** -11 + (rows.size / 16 + 16) * po.U32) * (e / z @ np.abs(val)) + \
+                    2.0 ** -27 * small * np.abs(V[rows, hk]).sum(0) + 2.0 ** -8 * np.abs(o)
+                t_lse[t, h] = 2 * delta + 2.0 ** -21 * abs(lse[t, h])
+    return out, lse, t_out, t_lse
+
+
+def compare(c, equal=False, both=True):
+    o, l, to, tl = tight(c, equal)
+    a = c.device()
+    runs = [a] if c.cu is not None or not both else [a, {**a, "cu_q": cuda(list(range(len(c.lengths) + 1)))}]
+    for args in runs:
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = hk.attend_pages(scale=c.scale, status=word, **args)
+        assert word.item() == 0
+        po.check("lse", lse.double().cpu().numpy(), l, tl)
+        po.check("out", out.double().cpu().numpy(), o, to)
+
+
+# (more items than multiprocessors of several tiles each, or few that they share; pieces of prompts)
+BATCHES = {"tokens": (Case, [(x, 1) for x in range(300, 460)], True),
+           "token": (Case, [(9000, 1)], True),
+           "pieces": (AnyCase, [(300, 40), (128, 128), (700, 3), (200, 1)], False)}
+
+
+def make(batch, d, **kw):
+    kind, seqs, single = BATCHES[batch]
+    return kind(seqs, Hq=4, Hkv=2, d=d, single=single, seed=d, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("first,rest", [(-60, 60), (60, -60), (-115, 0), (0, -120), (-126, 118)])
+def test_scales_of_v_that_change_after_a_tile(batch, first, rest, d):
+    c = make(batch, d, P=128)
+    c.v = (c.v & 0x80) | (c.v & 0x7F) % 0x39                # up to 1
+    c.vs[:] = 2.0 ** rest
+    c.vs[c.table[:, 0]] = np.float32(2.0 ** first * 1.5)
+    compare(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("q_size,far", [(1.0, 60), (1.0, 120), (64.0, 60), (64.0, 120), (512.0, 120)])
+def test_scales_of_v_in_no_order(batch, q_size, far, d):
+    """Scores of large queries outweigh scales: rows of tiny values alone, and of huge ones."""
+    c = make(batch, d, P=16, q_size=q_size)
+    c.v = (c.v & 0x80) | (c.v & 0x7F) % 0x39
+    c.vs = (2.0 ** np.random.default_rng(1).uniform(-far, far, c.vs.shape)).astype(np.float32)
+    compare(c)
+
+
+def test_rows_that_see_tiny_values_alone():
+    """The first page of a prompt, beside pages of another size in the same tile."""
+    for d in (64, 128):
+        c = AnyCase([(200, 200), (40, 40)], Hq=4, Hkv=2, d=d, P=16, seed=5)
+        c.v = (c.v & 0x80) | (c.v & 0x7F) % 0x39
+        c.vs[:] = 1.0
+        c.vs[c.table[:, 0]] = 2.0 ** -115
+        compare(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("log2", [21, 25, 31, 60, -22, -40])
+def test_scores_far_from_0_keep_the_scales_of_v(batch, log2, d):
+    """All keys alike, so that every weight is the same, whatever the score is."""
+    c = make(batch, d, P=64)
+    c.k[:] = 0x38
+    c.v = c.v & 0x7F
+    c.v[c.v == 0x7F] = 0x38
+    c.ks[:] = 2.0 ** -6
+    c.q = (torch.sign(torch.tensor(float(log2))) * 2.0 ** (abs(log2) - np.log2(d) + 6) *
+           torch.ones(c.q.shape)).bfloat16()
+    c.scale = 0.7
+    compare(c, equal=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("page", [0, 3, 5, 11])
+def test_scores_that_jump(batch, page, d):
+    """Two neighbouring pages whose scores lie 2^24 above all others, or below for other heads."""
+    c = make(batch, d, P=16)
+    c.k[:] = 0x38
+    c.v = c.v & 0x7F
+    c.v[c.v == 0x7F] = 0x38
+    c.ks[:] = 2.0 ** -20
+    c.ks[c.table[:, page:page + 2]] = 2.0 ** 18
+    c.q[:] = 1.0
+    c.q[:, ::2] = -1.0
+    compare(c, equal=True)
