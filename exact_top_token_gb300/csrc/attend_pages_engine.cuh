@@ -1026,14 +1026,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // O and the tile's weights so far, those of `done` blocks, times 2^-by
           auto shrink = [&](float by, int done) -> bool {
             const float f = ex2(-by);
-            const uint32_t f2 = pack_f16(f, f);
+            // (f16 has no 2^-25, but weights that it leaves something of: in two steps)
+            const float f_once = ex2(-fminf(by, 14.0f)), f_more = ex2(fminf(by, 14.0f) - by);
+            const uint32_t f2 = pack_f16(f_once, f_once), f3 = pack_f16(f_more, f_more);
             tc::tmem_wait_st();
 #pragma unroll 1
             for (int i = 0; i < 16 * done; i += 8) {
               uint32_t y[8];
               tmem_load8(s_addr + i, y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = mul_f16(y[e], f2);
+              for (int e = 0; e < 8; ++e) y[e] = mul_f16(mul_f16(y[e], f2), f3);
               tmem_store8(s_addr + i, y);
             }
             if (mine > 0) {

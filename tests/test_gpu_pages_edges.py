@@ -241,3 +241,22 @@ def test_scores_that_jump(batch, page, d):
     c.q[:] = 1.0
     c.q[:, ::2] = -1.0
     compare(c, equal=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rise", [20, 32])
+def test_weights_of_a_tile_whose_reference_rises(rise, d):
+    """Keys 2^6.5 times an earlier tile's, then some 2^rise times as heavy in the same tile: what the
+    former add to a column that the latter lack. So many items that shares hold whole ones."""
+    B, P = 120, 64
+    c = AnyCase([(512, 5)] * B, Hq=32, Hkv=1, d=d, P=P, seed=d)
+    c.k[:] = 0x38
+    c.v[:] = 0
+    c.v[..., 1] = 0x38
+    c.ks[:] = 2.0 ** -10
+    c.vs[:] = 1.0
+    c.q[:] = 1.0
+    c.scale = float(np.log(2)) / d                 # scores in powers of two: the page's scale of k
+    c.ks[c.table[:, 4]], c.ks[c.table[:, 5]] = 6.5, rise
+    c.v[c.table[:, 4], :, :, 0] = 0x38
+    compare(c)
