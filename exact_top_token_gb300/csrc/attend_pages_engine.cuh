@@ -78,8 +78,9 @@ constexpr int kConsts = 16;    // ring of the tiles' scales
 constexpr int kThreads = 512;
 constexpr int kBlock = 4;      // groups of 16 keys that the softmax takes at a time
 // The quick form of the softmax has one reference m for weights and denominators: |b| may be up to
-// kWide in it (of 2^60, 2^11 and 2^31 keys fp32 holds the product), and |m| up to kFar.
-constexpr float kWide = 60.0f, kFar = 1048576.0f;
+// kWide in it (of 2^60, 2^11 and 2^31 keys fp32 holds the product), and |m| up to kFar, where
+// b - m is rounded by 2^-13 at most and v's scale by 8.5e-5 (bf16 results by 2e-3 and more).
+constexpr float kWide = 60.0f, kFar = 4096.0f;
 // Registers: 128 a thread at launch, then by role: 128 (64 + 2 * 184 + 80) = 65536.
 constexpr int kRegsLaunch = 128, kRegsCtl = 64, kRegsSoft = 184, kRegsWide = 80;
 static_assert(kRegsCtl + 2 * kRegsSoft + kRegsWide <= 4 * kRegsLaunch, "register split");

@@ -260,3 +260,24 @@ def test_weights_of_a_tile_whose_reference_rises(rise, d):
     c.ks[c.table[:, 4]], c.ks[c.table[:, 5]] = 6.5, rise
     c.v[c.table[:, 4], :, :, 0] = 0x38
     compare(c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("log2", [10, 12, 15, 18.3, 19.7, -18.5, -13])
+def test_scores_of_middling_size_keep_the_scales_of_v(batch, log2, d):
+    """As above: contexts of two pages, the second of whose scales, as a power of two, lies almost half
+    a step from any fp32 number of the scores' size."""
+    kind, seqs, single = BATCHES[batch]
+    seqs = [(128, min(m, 128)) for _, m in seqs]
+    c = kind(seqs, Hq=4, Hkv=2, d=d, P=64, seed=d, single=single)
+    c.k[:] = 0x38
+    c.v[:] = 0x38
+    c.ks[:] = 1.0
+    c.vs[:] = 1.0
+    step = 2.0 ** (np.floor(abs(log2)) - 23)       # of fp32 there
+    c.vs[c.table[:, 1]] = np.float32(2.0 ** (-8 + 0.47 * step))
+    c.v[c.table[:, 0]] = 0
+    c.q[:] = 1.0 if log2 > 0 else -1.0
+    c.scale = float(2.0 ** abs(log2) * np.log(2) / d)
+    compare(c, equal=True)
