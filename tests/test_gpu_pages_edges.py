@@ -281,3 +281,22 @@ def test_scores_of_middling_size_keep_the_scales_of_v(batch, log2, d):
     c.q[:] = 1.0 if log2 > 0 else -1.0
     c.scale = float(2.0 ** abs(log2) * np.log(2) / d)
     compare(c, equal=True)
+
+
+@pytest.mark.parametrize("batch", BATCHES)
+def test_queries_that_are_not_finite(batch):
+    """NaN for their heads, and nothing else for the others of the group."""
+    for value in (float("nan"), float("inf"), -float("inf")):
+        c = make(batch, 64, P=32)
+        o, l, to, tl = tight(c)
+        c.q[:, 1, 5] = value
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = hk.attend_pages(scale=c.scale, status=word, **c.device())
+        assert word.item() == 0
+        # (a score of +inf or NaN makes the row NaN; the first rows of a prompt may only have -inf)
+        hurt = torch.isnan(lse[:, 1])
+        assert hurt[-1] and hurt.float().mean() > 0.8 and torch.isnan(out[:, 1][hurt]).all()
+        assert (out[:, 1][~hurt] == 0).all() and (lse[:, 1][~hurt] == -float("inf")).all()
+        for h in (0, 2, 3):
+            po.check("lse", lse[:, h].double().cpu().numpy(), l[:, h], tl[:, h])
+            po.check("out", out[:, h].double().cpu().numpy(), o[:, h], to[:, h])

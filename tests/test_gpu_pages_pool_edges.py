@@ -23,3 +23,14 @@ def test_nothing_is_granted_behind_what_an_empty_pool_lacks(wanted):
     t.grow([16 * wanted, 1, 0, 1])
     assert t.word.item() == hk.DEV_NO_PAGE
     assert t.lengths.tolist() == ([160, 6, 0, 0] if wanted == 10 else [0, 5, 0, 0])
+
+
+@pytest.mark.parametrize("N", [1, 40, 5000])
+def test_a_pool_that_no_sequence_uses(N):
+    """A table without rows: pages are counted all the same."""
+    t = Both(0, 3, N, 16, [])
+    t.refs[N // 2] = t.o.refs[N // 2] = 1
+    t.compact()
+    t.grow([])
+    t.free([])
+    t.fork([], [])
