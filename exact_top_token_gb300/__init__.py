@@ -707,15 +707,15 @@ def attend_pages(q, k_pages, v_pages, k_scale, v_scale, table, lengths, cu_q=Non
                  out=None, lse=None, status=None, stream=None):
     """Causal attention of rows q ([n, Hq, d] bf16) over their whole contexts, up to each
     row's own position: ``(out [n, Hq, d] bf16, lse [n, Hq] fp32)``. ``scale`` defaults to
-    d ** -0.5. Rows past cu_q[B] (a padded batch) are left as they are in ``out`` and
-    ``lse``. For contexts that are attended whole; :func:`attend` takes selected rows."""
+    d ** -0.5. Rows past cu_q[B] (a padded batch) are left as they are in a given ``out`` and
+    ``lse``, and hold anything in fresh ones. For contexts that are attended whole; :func:`attend` takes selected rows."""
     return (_module or _operators()).attend_pages(q, k_pages, v_pages, k_scale, v_scale, table,
                                                   lengths, cu_q, scale, out, lse, status, stream)
 
 
 def page_fork(table, lengths, refs, src, dst, *, page, status=None, stream=None):
-    """Sequences ``dst`` [m] (empty, distinct) become holders of the pages of sequences
-    ``src`` [m] (-1: skipped). ``page``: rows of a page. Returns ``table``."""
+    """Sequences ``dst`` [m] (empty, distinct, none of them in ``src``) become holders of the
+    pages of sequences ``src`` [m] (-1: skipped). ``page``: rows of a page. Returns ``table``."""
     return (_module or _operators()).page_fork(table, lengths, refs, src, dst, page, status, stream)
 
 

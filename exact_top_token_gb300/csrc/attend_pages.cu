@@ -20,9 +20,12 @@ constexpr int kTokenHeads = 16;
 // The kernel of single rows is taken where at most that many heads share a cache head, no more
 // rows are given than there are sequences, and contexts may be as long as kTokenTiles tiles of
 // 128 keys a multiprocessor: 64 rows over up to 16384 keys, 8 cache heads of 128 columns, take
-// 167 us with it and 221 with the general one, over 256 keys each (7 tiles) 28 and 36. A cu_q
+// 167 us with it and 221 with the general one, over 256 keys each (7 tiles) 29 and 37. A cu_q
 // may hold several rows of a sequence all the same, so with one both are launched and the
-// second mostly ends at once, which takes 2 to 4 us; one row over 500 keys takes 15 us in all.
+// second mostly ends at once, which takes 2 to 3 us: 16 rows over 100 keys (0.8 tiles) 17 us
+// either way, 32 (1.7 tiles) 19 and 23, one row over 500 keys 17 and 16. Without a cu_q the
+// kernel of single rows is ahead at any size (that row 14 and 16, 64 over 100 keys, 3.4 tiles,
+// 24 and 36), so that the rule, one for both, is cautious.
 constexpr int kTokenTiles = 4;
 
 namespace {

@@ -28,7 +28,7 @@ struct AttendArgs {
   uint32_t* status;
   float* part;   // [2 * ctas][rows][d] results, each divided by its own sum
   float2* ml;    // [2 * ctas][rows] sums and -m of them
-  int4* record;  // [2 * ctas][2]: what each is a part of
+  int4* record;  // [ctas][2]: what each is a part of
   int rows;      // of a part
   // both kernels are launched: the first tells here whether some sequence has several rows, which
   // are the second's; NULL: one alone

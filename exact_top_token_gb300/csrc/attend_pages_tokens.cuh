@@ -17,7 +17,7 @@
 // Keys past the context's end, the same for all heads, have v replaced by zeros as it is
 // widened, so that NaN codes there reach nothing.
 //
-// 64 sequences over up to 16384 keys, 32 heads of 128 on 8, take 166 us, 5.8 TB/s of the 6.7 that a
+// 64 sequences over up to 16384 keys, 32 heads of 128 on 8, take 167 us, 5.8 TB/s of the 6.7 that a
 // copy reaches (the general kernel 221). Memory bounds it, shared memory is just behind: of a tile
 // 32 KB come as codes and 152 KB pass through shared memory, 1190 cycles where memory's share of an
 // SM takes 1400; the general kernel passes 224 KB, f16 keys and operands of 128 rows among them,
@@ -26,7 +26,9 @@
 // warp has too many of them: with both products in one warp, or the scales beside the copies
 // or the widening, that warp took 2000 cycles a tile (205 us); with the pages of four tiles
 // looked up at once and the scales beside the segments a tile takes 1400. Items of 17 to 64 heads, with 64
-// columns, took 134 us where the general kernel takes 87 (one token over 2^20 keys, 64 heads).
+// columns, took 134 us where the general kernel took 87 (one token over 2^20 keys, 64 heads). Heads
+// of 64 columns, otherwise as above: 146 us, 3.3 TB/s; half the bytes of each tile, so the chain
+// of its steps bounds it.
 //
 //   warp 0        products with V; tensor memory
 //   warp 1        this CTA's segments: (item, tiles) in order, and the tiles' scales, through rings

@@ -564,7 +564,7 @@ HYTOPK_API hytopk_status hytopk_attend_backward(const void* q, int64_t q_row, co
  * each sequence (then n = B). Rows past cu_q[B] belong to no sequence: what belongs to
  * them in the outputs is left as it is. lengths below 0 or past columns * P, and cu_q that
  * leave 0 .. n or decrease, are brought back into the range and set
- * HYTOPK_DEV_BAD_POSITION; a row at a negative position sees nothing and is not written. */
+ * HYTOPK_DEV_BAD_POSITION, whichever sequence has them; a row at a negative position sees nothing and is not written. */
 typedef struct {
   const int32_t* table;
   const int32_t* lengths;
@@ -585,8 +585,10 @@ typedef struct {
  * its page NaN and sets HYTOPK_DEV_BAD_SCALE.
  * Scores, softmax statistics and sums are fp32. The tensor cores take codes and queries as
  * f16, which holds every e4m3 value, and queries to 2^-39 of their row's largest (a power
- * of two is taken out of each); weights are rounded to f16, 11 bits and at least 2^-28 of
- * the largest, where the result has 8.
+ * of two is taken out of each); weights, v's scale among them, are rounded to f16: 11 bits,
+ * where the result has 8, and at least 2^-28 of the row's largest, so that any number of keys
+ * below that add nothing to out (to lse they do). Scales of v may lie anywhere in the range of
+ * fp32; scale * k_scale is taken to be 2^-126 at least.
  *   1 <= G <= 128, d in {64, 128}, n * Hq < 2^31, N * P < 2^31 - 16, scale finite. Base
  *   pointers 16-byte aligned, q_row a multiple of 8.
  *   workspace: hytopk_attend_pages_workspace_size bytes (parts of contexts that several
@@ -626,9 +628,9 @@ HYTOPK_API hytopk_status hytopk_page_write(const void* x, int64_t x_row, int64_t
  * context's pages are taken to be -1 and left so.
  *
  * hytopk_page_fork: sequence dst[i] becomes another holder of all pages of sequence
- *   src[i] (its length too). dst[i] must be empty (length 0), appear once in dst and not in
- *   src; otherwise that entry (of a repeated dst all but the first) is skipped with
- *   HYTOPK_DEV_BAD_INDEX.
+ *   src[i] (its length too). dst[i] must be empty (length 0) and appear once in dst, and
+ *   src[i] not in dst; otherwise that entry (of a repeated dst all but the first) is skipped
+ *   with HYTOPK_DEV_BAD_INDEX.
  * hytopk_page_free: the pages of each sequence lose a holder; its entries become -1, its
  *   length 0. A sequence given twice is freed once.
  * hytopk_page_grow: every sequence b grows by add[b] >= 0 rows: its table row gets the
